@@ -11,6 +11,10 @@ Stages (EntropyCache, gist.science zh summary §2.2):
   kv_scatter         (c) fresh K/V rows of the recompute set into the cache
   partial_attention  (d) bidirectional attention of the recompute rows over all L rows
   step               all of the above for one denoising step over n layers
+
+The same stages over other caches: kv_scatter_quant / kv_gather_quant write and read a QuantCache
+(8-bit rows), partial_attention_quant attends to it, prefix_attention attends to a prefix that
+the batch shares and to each sequence's own cache.
 """
 from __future__ import annotations
 
@@ -36,6 +40,13 @@ __all__ = [
     "kv_scatter",
     "partial_attention",
     "partial_attention_workspace_size",
+    "QuantCache",
+    "kv_scatter_quant",
+    "kv_gather_quant",
+    "partial_attention_quant",
+    "partial_attention_quant_workspace_size",
+    "prefix_attention",
+    "prefix_attention_workspace_size",
     "step",
     "step_workspace_size",
     "LayerWeights",
@@ -272,6 +283,201 @@ def dense_attention(p: Params, q, k_cache, v_cache, out, scale: float | None = N
                                   _stream(stream))
     C.check(st, "ec_dense_attention")
     return out
+
+
+# ---- 8-bit caches and shared prefixes ------------------------------------------------------------
+
+
+def _checked(t, name: str, dtype, shape: tuple, device):
+    """t, a contiguous CUDA tensor of that type, shape and device."""
+    if t.dtype is not dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device} (EntropyCache kernels take CUDA tensors of one device)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class _Cache:
+    """The C view of one layer's cache (ec_kv) and the tensors that it points to."""
+
+    __slots__ = ("c", "ref", "shape", "device", "keep")
+
+    def __init__(self, dtype, k, v, k_exp=None, v_exp=None):
+        tdt = torch.float8_e4m3fn if dtype == C.EC_E4M3 else torch.bfloat16
+        self.shape, self.device = tuple(k.shape), k.device
+        kp = _checked(k, "k", tdt, self.shape, k.device)
+        vp = _checked(v, "v", tdt, self.shape, k.device)
+        if len(self.shape) != 4:
+            raise ValueError(f"a cache is [B, L, Hkv, D], got {list(self.shape)}")
+        ep = [None, None]
+        if dtype == C.EC_E4M3:
+            B, L, H, _ = self.shape
+            ep = [_checked(e, n, torch.uint8, (B, H, -(-L // 16) * 16), k.device)
+                  for e, n in ((k_exp, "k_exp"), (v_exp, "v_exp"))]
+        self.c = C.EcKv(dtype, self.shape[1], kp, vp, *ep)
+        self.ref = ctypes.byref(self.c)
+        self.keep = (k, v, k_exp, v_exp)
+
+
+class QuantCache:
+    """One layer's K/V cache in 8 bits (ec_kv, EC_E4M3): k, v float8_e4m3fn [B, L, Hkv, D] and
+    k_exp, v_exp uint8 [B, Hkv, S], S = L rounded up to a multiple of 16. The row of position j
+    and head h stands for k[b, j, h] * 2^(k_exp[b, h, j] - 127)."""
+
+    __slots__ = ("k", "v", "k_exp", "v_exp", "_view")
+
+    def __init__(self, k, v, k_exp, v_exp):
+        self._view = _Cache(C.EC_E4M3, k, v, k_exp, v_exp)
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+
+    @classmethod
+    def empty(cls, B: int, L: int, Hkv: int, D: int, device="cuda") -> "QuantCache":
+        """A cache of zero rows."""
+        S = -(-L // 16) * 16
+        z = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=device)  # noqa: E731
+        codes = [z(B, L, Hkv, D).view(torch.float8_e4m3fn) for _ in range(2)]
+        return cls(*codes, *(z(B, Hkv, S).fill_(17) for _ in range(2)))
+
+
+def _cache_view(cache, ndim: int = 4) -> _Cache:
+    if isinstance(cache, QuantCache):
+        return cache._view
+    k, v = cache
+    if ndim == 3 and k.dim() == 3 and v.dim() == 3:  # a prefix: one sequence
+        k, v = k.unsqueeze(0), v.unsqueeze(0)
+    return _Cache(C.EC_BF16, k, v)
+
+
+class _on_device:
+    """Makes `device` and the caller's `stream` (None: the device's current one) current for a call,
+    where they are not already, so that what the call allocates belongs to the stream that it
+    launches on; gives that stream's handle."""
+
+    __slots__ = ("guard", "stream")
+
+    def __init__(self, device, stream):
+        self.guard = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self.guard = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+        self.stream = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _opt(t, name, dtype, shape, device):
+    return None if t is None else _checked(t, name, dtype, shape, device)
+
+
+def _expect(view: _Cache, shape: tuple, what: str):
+    if view.shape != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(view.shape)}")
+
+
+def kv_scatter_quant(p: Params, cache: QuantCache, k_new, v_new, idx, R, src_by_position: bool = False, dev_err=None,
+                     stream=None):
+    """(c) the refresh of an 8-bit cache: cache[b, idx[b, r]] = the row k_new[b, r or idx[b, r]],
+    quantised (same for v), for r < R[b]. k_new, v_new bf16 [B, L, Hkv, D]; idx [B, L] (strictly
+    ascending per sequence unless src_by_position) and R [B] int32. See ec_kv_scatter_quant."""
+    view, shape = cache._view, (p.B, p.L, p.Hkv, p.D)
+    dev = view.device
+    _expect(view, shape, "cache")
+    kp = _checked(k_new, "k_new", torch.bfloat16, shape, dev)
+    vp = _checked(v_new, "v_new", torch.bfloat16, shape, dev)
+    ip = _checked(idx, "idx", torch.int32, (p.B, p.L), dev)
+    rp = _checked(R, "R", torch.int32, (p.B,), dev)
+    ep = _opt(dev_err, "dev_err", torch.int32, (1,), dev)
+    with _on_device(dev, stream) as s:
+        st = lib().ec_kv_scatter_quant(ctypes.byref(p.c()), view.ref, kp, vp, int(bool(src_by_position)), ip, rp, ep, s)
+    C.check(st, "ec_kv_scatter_quant")
+
+
+def kv_gather_quant(p: Params, cache: QuantCache, idx, R, out: tuple | None = None, dev_err=None, stream=None):
+    """Rows of an 8-bit cache back as bf16: (k, v) with k[b, r] = cache row idx[b, r] for r < R[b]
+    (idx None: row r). out: two bf16 tensors [B, L, Hkv, D], by default new ones whose other rows
+    are zeros. See ec_kv_gather_quant."""
+    view, shape = cache._view, (p.B, p.L, p.Hkv, p.D)
+    dev = view.device
+    _expect(view, shape, "cache")
+    ip = _opt(idx, "idx", torch.int32, (p.B, p.L), dev)
+    rp = _checked(R, "R", torch.int32, (p.B,), dev)
+    ep = _opt(dev_err, "dev_err", torch.int32, (1,), dev)
+    with _on_device(dev, stream) as s:
+        if out is None:
+            out = (torch.zeros(shape, dtype=torch.bfloat16, device=dev), torch.zeros(shape, dtype=torch.bfloat16, device=dev))
+        kp = _checked(out[0], "out[0]", torch.bfloat16, shape, dev)
+        vp = _checked(out[1], "out[1]", torch.bfloat16, shape, dev)
+        st = lib().ec_kv_gather_quant(ctypes.byref(p.c()), view.ref, ip, rp, kp, vp, ep, s)
+    C.check(st, "ec_kv_gather_quant")
+    return out
+
+
+def partial_attention_quant_workspace_size(p: Params) -> int:
+    return int(lib().ec_partial_attention_quant_workspace_size(ctypes.byref(p.c())))
+
+
+def prefix_attention_workspace_size(p: Params) -> int:
+    return int(lib().ec_prefix_attention_workspace_size(ctypes.byref(p.c())))
+
+
+def _attend(p: Params, q, prefix: _Cache | None, cache: _Cache, R, out, kv_len, scale, ws, dev_err, stream):
+    dev, shape = q.device, (p.B, p.L, p.Hq, p.D)
+    _expect(cache, (p.B, p.L, p.Hkv, p.D), "cache")
+    qp = _checked(q, "q", torch.bfloat16, shape, dev)
+    op = _checked(out, "out", torch.bfloat16, shape, dev)
+    rp = _checked(R, "R", torch.int32, (p.B,), dev)
+    lp = _opt(kv_len, "kv_len", torch.int32, (p.B,), dev)
+    ep = _opt(dev_err, "dev_err", torch.int32, (1,), dev)
+    if cache.device != dev or (prefix is not None and prefix.device != dev):
+        raise ValueError(f"the caches must be on {dev}, as q is")
+    if ws is not None and (not ws.is_cuda or ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+    sc = (1.0 / math.sqrt(p.D)) if scale is None else float(scale)
+    pc = ctypes.byref(p.c())
+    with _on_device(dev, stream) as s:
+        if prefix is None:
+            if ws is None:
+                ws = torch.empty(max(256, partial_attention_quant_workspace_size(p)), dtype=torch.uint8, device=dev)
+            st = lib().ec_partial_attention_quant(pc, qp, cache.ref, rp, lp, sc, op, ws.data_ptr(),
+                                                  ws.numel() * ws.element_size(), ep, s)
+        else:
+            if ws is None:
+                ws = torch.empty(max(256, prefix_attention_workspace_size(p)), dtype=torch.uint8, device=dev)
+            st = lib().ec_prefix_attention(pc, qp, prefix.ref, cache.ref, rp, lp, sc, op, ws.data_ptr(),
+                                           ws.numel() * ws.element_size(), ep, s)
+    C.check(st, "ec_partial_attention_quant" if prefix is None else "ec_prefix_attention")
+    return out
+
+
+def partial_attention_quant(p: Params, q, cache: QuantCache, R, out, kv_len=None, scale: float | None = None,
+                            ws: torch.Tensor | None = None, dev_err=None, stream=None):
+    """(d) against an 8-bit cache: out[b, r, h] = softmax(scale q k^T) v over the first kv_len[b]
+    keys (None: the scope's), for r < R[b]; zeros without a key. q, out bf16 [B, L, Hq, D]; R,
+    kv_len int32 [B]; scale > 0. See ec_partial_attention_quant."""
+    return _attend(p, q, None, cache._view, R, out, kv_len, scale, ws, dev_err, stream)
+
+
+def prefix_attention(p: Params, q, prefix, cache, R, out, kv_len=None, scale: float | None = None,
+                     ws: torch.Tensor | None = None, dev_err=None, stream=None):
+    """(d) for a batch behind one prefix: attention over the prefix's keys, which every sequence
+    sees, and the first kv_len[b] keys of the sequence's own cache. prefix: (k, v) bf16
+    [Lp, Hkv, D], or a QuantCache of one sequence; cache: (k, v) bf16 [B, L, Hkv, D], or a
+    QuantCache. The rest as partial_attention_quant. See ec_prefix_attention."""
+    pv, cv = _cache_view(prefix, 3), _cache_view(cache)
+    _expect(pv, (1, pv.shape[1], p.Hkv, p.D), "prefix")
+    return _attend(p, q, pv, cv, R, out, kv_len, scale, ws, dev_err, stream)
 
 
 @dataclass

@@ -20,9 +20,11 @@ EC_DEVERR_BAD_CAND_POS = 0x1
 EC_DEVERR_BAD_IDX = 0x2
 EC_DEVERR_BAD_R = 0x4
 EC_DEVERR_TIMEOUT = 0x8
+EC_DEVERR_BAD_LEN = 0x10
 
 EC_F32 = 0
 EC_BF16 = 1
+EC_E4M3 = 2
 
 EC_CAND_BLOCK = 0
 EC_CAND_SLIDING = 1
@@ -58,6 +60,10 @@ class EcLayer(ctypes.Structure):
     ]
 
 
+class EcKv(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("len", _i32), ("k", _p), ("v", _p), ("k_exp", _p), ("v_exp", _p)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES: dict[str, tuple] = {
     "ec_status_string": (ctypes.c_char_p, [_i32]),
@@ -79,6 +85,12 @@ SIGNATURES: dict[str, tuple] = {
     "ec_partial_attention_workspace_size": (_sz, [ctypes.POINTER(EcParams)]),
     "ec_partial_attention": (_i32, [ctypes.POINTER(EcParams), _p, _p, _p, _p, _f32, _p, _p, _sz, _p, _p]),
     "ec_dense_attention": (_i32, [ctypes.POINTER(EcParams), _p, _p, _p, _f32, _p, _p, _p]),
+    "ec_kv_scatter_quant": (_i32, [_p, _p, _p, _p, _i32, _p, _p, _p, _p]),
+    "ec_kv_gather_quant": (_i32, [_p, _p, _p, _p, _p, _p, _p, _p]),
+    "ec_partial_attention_quant_workspace_size": (_sz, [_p]),
+    "ec_partial_attention_quant": (_i32, [_p, _p, _p, _p, _p, _f32, _p, _p, _sz, _p, _p]),
+    "ec_prefix_attention_workspace_size": (_sz, [_p]),
+    "ec_prefix_attention": (_i32, [_p, _p, _p, _p, _p, _p, _f32, _p, _p, _sz, _p, _p]),
     "ec_step_workspace_size": (_sz, [ctypes.POINTER(EcParams)]),
     "ec_step": (_i32, [ctypes.POINTER(EcParams), ctypes.POINTER(EcState), _p, _p, _p, _i32,
                        ctypes.POINTER(_p), ctypes.POINTER(_p), ctypes.POINTER(_p), ctypes.POINTER(_p),

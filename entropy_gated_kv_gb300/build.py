@@ -23,7 +23,7 @@ LIB_PATH = PKG / LIB_NAME
 
 SOURCES = ["entropy_decode.cu", "select_recompute.cu", "kv_scatter.cu", "attention.cu", "attention_dense.cu", "ec_api.cu",
            "entropy_decode_noalloc.cu", "lm_head_entropy.cu", "layer_forward.cu",
-           "read_floor.cu"]
+           "read_floor.cu", "kv_quant.cu", "attention_cached.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = [
     "-O3",

@@ -1,0 +1,898 @@
+// attention_cached.cu — attention of the recompute rows against caches that the other attention
+// kernels do not read: an 8-bit K/V cache (quant_common.cuh), a prefix shared by the whole batch,
+// and per-sequence key lengths; on the 5th-generation tensor cores.
+//
+// EntropyCache, gist.science zh summary §2.2 (the partial forward reads every row outside the
+// recompute set from the cache) and pt summary §1 (bidirectional attention, no causal mask). With
+// block-by-block decoding (pt §5, zh §5) a prompt's K/V do not depend on what follows it, so a batch
+// behind one prompt holds them once. The 8-bit cache has no counterpart in the pages.
+//   out[b, r, h] = sum_j softmax_j(scale <q[b, r, h], k_j>) v_j,  r < R[b], over the prefix's Lp
+//   keys and the sequence's own kv_len[b] keys, KV head h / g;  zeros when there is no key
+//
+// Structure (one CTA per SM; the work plan is attention_cached.cuh's):
+//   warp 0       TMA producer: K and V blocks of 128 keys.
+//   warp 1       allocates 512 TMEM columns and issues tcgen05.mma.
+//   warps 2, 3   the query tile, row by row with cp.async (a tile packs rows of any sequences, which
+//                no one tensor box covers), swizzled by hand.
+//   warps 4..7   softmax of the CTA's even key blocks, warps 8..11 of the odd ones: two independent
+//                streams with their own S buffer, running maximum and sum, and O accumulator, joined
+//                once per item. One stream's softmax runs while the tensor cores work on the
+//                other's products; with one warpgroup a block takes its softmax and its
+//                products in series, and at 128 rows that is longer than the block's bytes take from HBM.
+//                One TMEM lane (= one packed query row) per thread; online softmax in base 2 with a
+//                lazy rescale of O (only when the running maximum grows by more than 2^8); P in
+//                bf16 written back over the first half of the S buffer.
+//   warps 12..15 (8-bit cache) dequantise: the producer's TMA brings codes and exponent bytes into a
+//                raw ring, and these warps write the bf16 tiles that the products read. The
+//                dequantised values are exact in bf16, so the products are those of a bf16 cache
+//                with the same values.
+// Keys past a sequence's length may hold anything: their scores are replaced, and their V rows are
+// zeroed in shared memory (0 x NaN is NaN in a matrix product).
+// Partial items write fp32 rows, their maximum and their sum to the workspace; the merge kernel
+// joins them in a fixed order, so results do not depend on timing.
+#include <cuda.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "attention_cached.cuh"
+#include "ec_common.cuh"
+#include "ec_internal.h"
+#include "quant_common.cuh"
+
+namespace ec {
+namespace cached {
+namespace {
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 256;  // stream s: S at columns [128 s, 128 s + 128), O at [256 + 128 s, + D)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per pipeline wait
+constexpr int kMaxCtas = 160;                     // bound of the attention grid, for the workspace
+constexpr int kMaxUnits = 6;                      // K or V tiles in shared memory
+constexpr int kMaxRaw = 3;
+constexpr int kDequantWarps = 4;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 16;  // rows of a tile per merge CTA step
+constexpr uint32_t kDescHi = sdesc_hi(1024);
+constexpr int kAtomBytes = 128 * 128;  // 128 rows x 128 bytes (64 bf16), 128-byte swizzle
+__host__ __device__ constexpr uint32_t step_qk(int kk) { return (kk >> 2) * (kAtomBytes / 16) + (kk & 3) * 2; }
+constexpr uint32_t kStepPV = 16 * 128 / 16;
+
+struct Bars {
+  uint64_t q_full, q_empty;
+  uint64_t unit_full[kMaxUnits], unit_empty[kMaxUnits];
+  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t o_free;
+  uint32_t tmem_base;
+  int abort;
+  int give_up;  // set by a softmax warp before the join of an item
+};
+
+// Shared memory: the query tile, a ring of bf16 tiles (K and V of a block in turn), for the 8-bit
+// cache a ring of raw tiles (128 rows of codes, then 128 exponent bytes), the row statistics that
+// the two streams exchange, the barriers.
+template <int D, bool Q8>
+struct Layout {
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kTileBytes = kAtoms * kAtomBytes;
+  static constexpr int kUnits = Q8 ? 4 : 6;
+  static constexpr int kRaw = Q8 ? kMaxRaw : 0;
+  static constexpr int kRawBytes = 128 * D + 128;
+  static constexpr int kUnitOff = kTileBytes;
+  static constexpr int kRawOff = kUnitOff + kUnits * kTileBytes;
+  static constexpr int kStatOff = kRawOff + kRaw * kRawBytes;
+  static constexpr int kBarOff = kStatOff + 2 * kBlockM * static_cast<int>(sizeof(float2));
+  static constexpr int kBytes = kBarOff + static_cast<int>(sizeof(Bars));
+  static constexpr int kThreads = Q8 ? 512 : 384;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+struct Args {
+  CUtensorMap tk, tv, tpk, tpv;  // own and prefix caches
+  const uint8_t *ke, *ve, *pke, *pve;
+  Shape s;
+  int32_t Hq, Ls, Lps;
+  float scale_log2;
+  const uint16_t* q;
+  uint16_t* out;
+  float* part_o;      // [slots][128][D]
+  float2* part_stat;  // [slots][128]: running maximum and sum
+  int32_t* dev_err;
+};
+
+EC_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+EC_DEV void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+EC_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+EC_DEV void st_shared16(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+EC_DEV uint4 ld_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
+EC_DEV uint32_t ld_shared8(uint32_t src) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u8 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(src) : "memory");
+  return v;
+}
+
+// tcgen05.wait::ld that also names the loaded registers, so that no use of them moves before it
+// while other loads are in flight.
+#define EC_TMEM_WAIT32(r)                                                                                    \
+  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                              \
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),         \
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),     \
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),  \
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),  \
+                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory")
+
+#define EC_TMEM_ST16(taddr, r)                                                                              \
+  asm volatile(                                                                                             \
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" \
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), \
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])          \
+      : "memory")
+
+// Whole warp: where packed row x of KV head kvh of the item lies in q, as (b L + r) Hq + h.
+EC_DEV int64_t query_row(const Args& a, const Plan& pl, const Item& it, int64_t x) {
+  const Shape& s = a.s;
+  int b = it.b;
+  if (it.b < 0) {  // row x over all sequences: b is the number of sequences that end at or before it
+    const int lane = threadIdx.x & 31;
+    int64_t base = 0, before = 0;
+    b = 0;
+    for (int b0 = 0; b0 < s.B; b0 += 32) {
+      int32_t r, n;
+      seq_of(s, pl, b0 + lane, r, n);
+      const int64_t incl = warp_inclusive(static_cast<int64_t>(r) * s.g);
+      for (int i = 0; i < min(32, s.B - b0); ++i) {
+        const int64_t e = base + __shfl_sync(0xffffffffu, incl, i);
+        if (e <= x) {
+          b = b0 + i + 1;
+          before = e;
+        }
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    x -= before;
+  }
+  const int64_t r = div_fast(x, s.g);
+  return (static_cast<int64_t>(b) * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g);
+}
+
+// Keys of block j of the item that take part.
+EC_DEV int valid_keys(const Shape& s, const Item& it, int j) {
+  const int left = j < it.np ? s.Lp - j * kBlockN : it.len - (j - it.np) * kBlockN;
+  return max(0, min(kBlockN, left));
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_kernel(const __grid_constant__ Args a) {
+  using LY = Layout<D, Q8>;
+  constexpr int kUnits = LY::kUnits;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* bars = reinterpret_cast<Bars*>(smem + LY::kBarOff);
+  const Shape& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 64);
+    mbar_init(&bars->q_empty, 1);
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&bars->unit_full[i], Q8 ? kDequantWarps : 1);
+      mbar_init(&bars->unit_empty[i], 1);
+    }
+    for (int i = 0; i < LY::kRaw; ++i) {
+      mbar_init(&bars->raw_full[i], 1);
+      mbar_init(&bars->raw_empty[i], kDequantWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 4);
+      mbar_init(&bars->pv_done[i], 1);
+    }
+    mbar_init(&bars->o_free, 8);
+    // the swizzled tiles need the 1024-byte alignment that dynamic shared memory has here
+    bars->abort = (smem_u32(smem) & 1023u) != 0u;
+    bars->give_up = 0;
+    if (bars->abort) report_error(a.dev_err, EC_DEVERR_TIMEOUT);
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&a.tk);
+    prefetch_tmap(&a.tv);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort_flag = &bars->abort;
+
+  pdl_wait();  // everything above overlaps the previous kernel
+  const Plan pl = make_plan(s, a.dev_err, blockIdx.x == 0 && warp == 0);
+  pdl_launch_dependents();
+  const int cta = static_cast<int>(blockIdx.x);
+  const int64_t u0 = cta * pl.chunk, uend = *abort_flag ? u0 : min(pl.units, u0 + pl.chunk);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait_bounded(bar, parity, abort_flag, a.dev_err, kWaitLimitNs);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    uint32_t n = 0;  // tiles requested: K and V of each block in turn
+    int ok = 1;
+    for (int64_t u = u0; ok && u < uend;) {
+      const Item it = cta_item(s, pl, u, uend);
+      if (lane == 0) {
+        for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j) {
+          const bool pre = j < it.np;
+          const int key0 = (pre ? j : j - it.np) * kBlockN;
+          const int b = pre ? 0 : it.b;
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const CUtensorMap* map = kv == 0 ? (pre ? &a.tpk : &a.tk) : (pre ? &a.tpv : &a.tv);
+            if constexpr (Q8) {
+              const uint32_t slot = n % LY::kRaw;
+              if (!(ok = wait(&bars->raw_empty[slot], ((n / LY::kRaw) & 1u) ^ 1u))) break;
+              uint8_t* dst = smem + LY::kRawOff + slot * LY::kRawBytes;
+              // exponent rows are padded to 16 positions: the copy stays inside its row
+              const int ls = pre ? a.Lps : a.Ls;
+              const uint32_t ne = static_cast<uint32_t>(min(kBlockN, ls - key0));
+              const uint8_t* exps = (kv == 0 ? (pre ? a.pke : a.ke) : (pre ? a.pve : a.ve)) +
+                                    (static_cast<int64_t>(b) * s.Hkv + it.kvh) * ls + key0;
+              mbar_arrive_expect_tx(&bars->raw_full[slot], 128 * D + ne);
+              tma_load_4d(dst, map, &bars->raw_full[slot], 0, it.kvh, key0, b);
+              bulk_load(dst + 128 * D, exps, ne, &bars->raw_full[slot]);
+            } else {
+              const uint32_t slot = n % kUnits;
+              if (!(ok = wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u))) break;
+              uint8_t* dst = smem + LY::kUnitOff + slot * LY::kTileBytes;
+              mbar_arrive_expect_tx(&bars->unit_full[slot], LY::kTileBytes);
+#pragma unroll
+              for (int at = 0; at < LY::kAtoms; ++at)
+                tma_load_4d(dst + at * kAtomBytes, map, &bars->unit_full[slot], at * 64, it.kvh, key0, b);
+            }
+          }
+        }
+      }
+      u += it.nblk;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer (whole warp, lane 0 issues)
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlockN, 0);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
+    const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
+    uint32_t n0 = 0;              // tiles of the items before
+    uint32_t used[2] = {0, 0};    // products finished or under way per stream
+    int items = 0;
+    bool ok = true;
+    auto wait_w = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    for (int64_t u = u0; ok && u < uend; ++items) {
+      const Item it = cta_item(s, pl, u, uend);
+      u += it.nblk;
+      auto issue_qk = [&](int i) {  // S of block i into its stream's buffer
+        const int st = i & 1;
+        const uint32_t n = n0 + 2 * i, slot = n % kUnits;
+        // the buffer's last P has been read
+        ok = ok && (used[st] == 0 || wait_w(&bars->pv_done[st], (used[st] - 1) & 1u)) &&
+             wait_w(&bars->unit_full[slot], (n / kUnits) & 1u);
+        if (!ok) return;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t k_lo = sdesc_lo(smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes), 16);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(tmem + st * kBlockN, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+          umma_commit(&bars->s_full[st]);
+          umma_commit(&bars->unit_empty[slot]);
+          if (i == it.nblk - 1) umma_commit(&bars->q_empty);
+        }
+        __syncwarp();
+      };
+      ok = wait_w(&bars->q_full, items & 1);
+      issue_qk(0);
+      if (it.nblk > 1) issue_qk(1);
+      for (int i = 0; ok && i < it.nblk; ++i) {
+        const int st = i & 1;
+        const uint32_t n = n0 + 2 * i + 1, slot = n % kUnits;
+        if (i == 0 && items > 0) ok = wait_w(&bars->o_free, (items - 1) & 1);
+        ok = ok && wait_w(&bars->unit_full[slot], (n / kUnits) & 1u);
+        if (!ok) break;
+        uint8_t* v_tile = smem + LY::kUnitOff + slot * LY::kTileBytes;
+        if constexpr (!Q8) {
+          // own rows past the sequence's length (the map zero-fills only past the cache's end)
+          const int j = it.j0 + i, nv = valid_keys(s, it, j);
+          if (j >= it.np && nv < kBlockN) {
+            for (int e = nv * 8 + lane; e < kBlockN * 8; e += 32)
+#pragma unroll
+              for (int at = 0; at < LY::kAtoms; ++at)
+                st_shared16(smem_u32(v_tile) + at * kAtomBytes + e * 16, make_uint4(0, 0, 0, 0));
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        ok = wait_w(&bars->p_full[st], used[st] & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t v_lo = sdesc_lo(smem_u32(v_tile), kAtomBytes);
+          const uint32_t acc0 = i > 1 ? 1u : 0u;  // the stream's first block of the item starts O anew
+#pragma unroll
+          for (int kk = 0; kk < kBlockN / 16; ++kk)
+            umma_ts(tmem + kTmemO + st * 128, tmem + st * kBlockN + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv,
+                    kk > 0 ? 1u : acc0);
+          umma_commit(&bars->unit_empty[slot]);
+          umma_commit(&bars->pv_done[st]);
+        }
+        __syncwarp();
+        ++used[st];
+        if (i + 2 < it.nblk) issue_qk(i + 2);
+      }
+      n0 += 2 * it.nblk;
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ query loader
+    constexpr int kChunks = D / 8;       // 16-byte pieces of a row
+    constexpr int kRowsStep = 32 / kChunks;
+    const int w = warp - 2;              // rows [64 w, 64 w + 64)
+    const uint32_t dst0 = smem_u32(smem);
+    const int chunk = lane % kChunks;
+    int items = 0;
+    bool ok = true;
+    for (int64_t u = u0; ok && u < uend; ++items) {
+      const Item it = cta_item(s, pl, u, uend);
+      u += it.nblk;
+      const int64_t last = it.row0 + it.nrows - 1;  // rows past the last are loaded as zeros
+      int64_t at[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) at[i] = query_row(a, pl, it, min(last, it.row0 + 64 * w + 32 * i + lane));
+      if (items > 0) ok = __all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1));
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < 64 / kRowsStep; ++i) {
+        const int rl = i * kRowsStep + lane / kChunks;  // row within this warp's 64
+        const int64_t src = __shfl_sync(0xffffffffu, at[i * kRowsStep / 32], rl & 31);
+        const int row = 64 * w + rl;
+        const uint32_t dst = dst0 + (chunk >> 3) * kAtomBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+        if (row < it.nrows)
+          cp_async16(dst, a.q + src * D + chunk * 8);
+        else
+          st_shared16(dst, make_uint4(0, 0, 0, 0));
+      }
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      mbar_arrive(&bars->q_full);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------------ softmax + epilogue
+    const int st = (warp - 4) >> 2;            // stream
+    const int row = 32 * (warp & 3) + lane;    // TMEM lane = packed query row
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t s_addr = tmem + lane_off + st * kBlockN;
+    float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
+    uint32_t used = 0, used_other = 0;  // blocks of this stream and of the other one
+    bool ok = true;
+    for (int64_t u = u0; ok && u < uend;) {
+      const Item it = cta_item(s, pl, u, uend);
+      u += it.nblk;
+      const bool live = 32 * (warp & 3) < it.nrows;  // else the warp's rows are all padding
+      float m_used = -INFINITY, l_sum = 0.f;
+      for (int i = st; i < it.nblk; i += 2, ++used) {
+        ok = __all_sync(0xffffffffu, wait(&bars->s_full[st], used & 1u));
+        if (!ok) break;
+        if (live) {
+          tc_fence_after();
+          const int nv = valid_keys(s, it, it.j0 + i);
+          uint32_t buf[2][32];
+          // row maximum (scale > 0 commutes with it), a chunk's load behind the next one's
+          float mx = -INFINITY;
+          EC_TMEM_LD32(s_addr, buf[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            EC_TMEM_WAIT32(buf[c & 1]);
+            if (c < 3) EC_TMEM_LD32(s_addr + (c + 1) * 32, buf[(c + 1) & 1]);
+            uint32_t* x = buf[c & 1];
+            if (nv < kBlockN) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c * 32 + e >= nv) x[e] = __float_as_uint(-INFINITY);
+            }
+            float m4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(x[e]);
+#pragma unroll
+            for (int e = 4; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[e]));
+            mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+          }
+          EC_TMEM_LD32(s_addr, buf[0]);
+          mx *= a.scale_log2;
+          bool rescale = false;
+          float alpha = 1.f;
+          if (i == st) {
+            m_used = mx;
+          } else if (mx > m_used + kRescaleLog2) {
+            alpha = ex2_approx(m_used - mx);
+            m_used = mx;
+            l_sum *= alpha;
+            rescale = true;
+          }
+          // p = 2^(s scale log2(e) - m); without a finite score so far, nothing is subtracted and p = 0
+          const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+          float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            EC_TMEM_WAIT32(buf[c & 1]);
+            if (c < 3) EC_TMEM_LD32(s_addr + (c + 1) * 32, buf[(c + 1) & 1]);
+            uint32_t* x = buf[c & 1];
+            if (nv < kBlockN) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c * 32 + e >= nv) x[e] = __float_as_uint(-INFINITY);
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float p0 = ex2_approx(fmaf(__uint_as_float(x[e]), a.scale_log2, neg_m));
+              const float p1 = ex2_approx(fmaf(__uint_as_float(x[e + 1]), a.scale_log2, neg_m));
+              sum4[(e >> 1) & 3] += p0 + p1;
+              pk[e >> 1] = pack_bf16x2(p0, p1);
+            }
+            // P over columns of S that this loop has read: [16 c, 16 c + 16) lies below 32 (c + 1)
+            EC_TMEM_ST16(s_addr + c * 16, pk);
+          }
+          l_sum += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+          // the stream's earlier products are done (they were waited for before this S was made)
+          if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t* o = buf[0];
+              EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+              EC_TMEM_WAIT32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              EC_TMEM_ST32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[st]);
+      }
+      // join the two streams: each warpgroup takes half of the columns of both accumulators
+      const int n_mine = (it.nblk + 1 - st) >> 1, n_other = it.nblk - n_mine;
+      used_other += n_other;
+      stat[st * kBlockM + row] = make_float2(m_used, l_sum);
+      if (n_mine > 0) ok = ok && wait(&bars->pv_done[st], (used - 1) & 1u);
+      if (n_other > 0) ok = ok && wait(&bars->pv_done[st ^ 1], (used_other - 1) & 1u);
+      ok = __all_sync(0xffffffffu, ok);
+      // a warp whose wait gave up still meets the others at both barriers, and all eight leave together
+      if (!ok && lane == 0) bars->give_up = 1;
+      named_bar_sync(2, 256);
+      ok = !*static_cast<volatile int*>(&bars->give_up);
+      tc_fence_after();
+      if (ok && live) {
+        const float2 s0 = stat[row], s1 = stat[kBlockM + row];
+        const float M = fmaxf(s0.x, s1.x);
+        // a stream without weight (no block, or no finite score) contributes nothing
+        const bool has0 = s0.y != 0.f, has1 = it.nblk > 1 && s1.y != 0.f;
+        const float w0 = has0 ? ex2_approx(s0.x - M) : 0.f, w1 = has1 ? ex2_approx(s1.x - M) : 0.f;
+        const float L = (has0 ? w0 * s0.y : 0.f) + (has1 ? w1 * s1.y : 0.f);
+        const bool complete = item_complete(pl, it);
+        const float norm = complete ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        const float f0 = w0 * norm, f1 = w1 * norm;
+        const bool valid = row < it.nrows;
+        uint16_t* orow = nullptr;
+        float* prow = nullptr;
+        if (complete) {
+          const int64_t x = it.row0 + row, r = div_fast(x, s.g);
+          orow = a.out + ((static_cast<int64_t>(it.b) * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g)) * D + st * (D / 2);
+        } else {
+          const int64_t slot = item_slot(pl, it, cta);
+          prow = a.part_o + (slot * kBlockM + row) * D + st * (D / 2);
+          if (st == 0 && valid) a.part_stat[slot * kBlockM + row] = make_float2(M, L);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t o0[32], o1[32];
+          EC_TMEM_LD32(tmem + lane_off + kTmemO + st * (D / 2) + c * 32, o0);
+          EC_TMEM_LD32(tmem + lane_off + kTmemO + 128 + st * (D / 2) + c * 32, o1);
+          EC_TMEM_WAIT32(o0);
+          EC_TMEM_WAIT32(o1);
+          float y[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            y[e] = has0 ? __uint_as_float(o0[e]) * f0 : 0.f;
+            if (has1) y[e] = fmaf(__uint_as_float(o1[e]), f1, y[e]);
+          }
+          if (valid && complete) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(orow + c * 32 + 8 * e) =
+                  make_uint4(pack_bf16x2(y[8 * e], y[8 * e + 1]), pack_bf16x2(y[8 * e + 2], y[8 * e + 3]),
+                             pack_bf16x2(y[8 * e + 4], y[8 * e + 5]), pack_bf16x2(y[8 * e + 6], y[8 * e + 7]));
+          } else if (valid) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(prow + c * 32 + 4 * e) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+          }
+        }
+        tc_fence_before();
+      }
+      named_bar_sync(2, 256);  // the statistics may be overwritten
+      if (lane == 0) mbar_arrive(&bars->o_free);
+    }
+  } else if constexpr (Q8) {
+    // ------------------------------------------------------------------ dequantisation
+    // Eight lanes read 128 neighbouring bytes of codes; the 16-byte pieces of bf16 that they
+    // store fall into eight different bank groups: for D = 128 lanes 0..3 take the first half of
+    // row r and lanes 4..7 the second half of row r ^ 1, whose swizzle differs in the lowest bit.
+    const int t = threadIdx.x - 384;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int64_t u = u0; ok && u < uend;) {
+      const Item it = cta_item(s, pl, u, uend);
+      u += it.nblk;
+      for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j) {
+        const int nv = valid_keys(s, it, j);
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const uint32_t rs = n % LY::kRaw, slot = n % kUnits;
+          ok = __all_sync(0xffffffffu, wait(&bars->raw_full[rs], (n / LY::kRaw) & 1u) &&
+                                           wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u));
+          if (!ok) break;
+          const uint32_t raw = smem_u32(smem + LY::kRawOff + rs * LY::kRawBytes);
+          const uint32_t tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes);
+          constexpr int kPieces = D / 16;  // 16-code pieces of a row
+          constexpr int kRowsStep = 128 / kPieces;
+#pragma unroll 4
+          for (int i = 0; i < kPieces; ++i) {
+            const int piece = t % kPieces;
+            int row = i * kRowsStep + t / kPieces;
+            if (D == 128) row ^= piece >> 2;
+            const uint4 w = ld_shared16(raw + row * D + piece * 16);
+            const DequantScale sc = dequant_scale(static_cast<int>(ld_shared8(raw + 128 * D + row)));
+            uint4 lo, hi;
+            dequantise4(w.x, sc, lo.x, lo.y);
+            dequantise4(w.y, sc, lo.z, lo.w);
+            dequantise4(w.z, sc, hi.x, hi.y);
+            dequantise4(w.w, sc, hi.z, hi.w);
+            if (kv == 1 && row >= nv) lo = hi = make_uint4(0, 0, 0, 0);  // past the length: no NaN may stay
+            const uint32_t dst = tile + (piece >> 2) * kAtomBytes + row * 128;
+            const uint32_t c = (piece & 3) * 2;
+            st_shared16(dst + ((c ^ (row & 7)) << 4), lo);
+            st_shared16(dst + (((c + 1) ^ (row & 7)) << 4), hi);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars->raw_empty[rs]);
+            mbar_arrive(&bars->unit_full[slot]);
+          }
+        }
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------------- merge
+
+// A tile of one sequence by its index among those (whole warp): also its first unit and the packed
+// rows of the sequences before it.
+struct OwnTile {
+  Item it;
+  int64_t u0, before;
+};
+
+EC_DEV OwnTile own_tile(const Shape& s, const Plan& pl, int tile) {
+  const int lane = threadIdx.x & 31;
+  OwnTile o;
+  int64_t ubase = pl.own0, rbase = 0;
+  int32_t tbase = 0;
+  for (int b0 = 0; b0 < s.B; b0 += 32) {
+    int32_t r, n;
+    seq_of(s, pl, b0 + lane, r, n);
+    const int32_t t = s.Hkv * tiles_of(s, r), tu = tile_units(pl, n);
+    const int32_t tincl = warp_inclusive(t);
+    const int32_t ttotal = __shfl_sync(0xffffffffu, tincl, 31);
+    const int64_t uincl = warp_inclusive(static_cast<int64_t>(t) * tu);
+    const int64_t rincl = warp_inclusive(static_cast<int64_t>(r) * s.g);
+    if (tile < tbase + ttotal) {
+      const int src = __ffs(__ballot_sync(0xffffffffu, tbase + tincl > tile)) - 1;
+      const int32_t tl = tile - tbase - __shfl_sync(0xffffffffu, tincl - t, src);
+      const int32_t rsel = __shfl_sync(0xffffffffu, r, src), per_head = tiles_of(s, rsel);
+      o.it.len = __shfl_sync(0xffffffffu, n, src);
+      o.it.units = __shfl_sync(0xffffffffu, tu, src);
+      o.it.b = b0 + src;
+      o.it.kvh = tl / per_head;
+      o.it.row0 = static_cast<int64_t>(tl - o.it.kvh * per_head) * kBlockM;
+      o.it.nrows = static_cast<int32_t>(min(static_cast<int64_t>(kBlockM), static_cast<int64_t>(rsel) * s.g - o.it.row0));
+      o.it.tile = pl.ptiles + tile;
+      o.u0 = ubase + __shfl_sync(0xffffffffu, uincl - static_cast<int64_t>(t) * tu, src) + static_cast<int64_t>(tl) * o.it.units;
+      o.before = rbase + __shfl_sync(0xffffffffu, rincl - static_cast<int64_t>(r) * s.g, src);
+      return o;
+    }
+    tbase += ttotal;
+    ubase += __shfl_sync(0xffffffffu, uincl, 31);
+    rbase += __shfl_sync(0xffffffffu, rincl, 31);
+  }
+  o.it.nrows = 0;  // not reached: tile is below pl.otiles
+  o.it.b = o.it.kvh = o.it.units = o.it.tile = o.it.len = 0;
+  o.it.row0 = o.u0 = o.before = 0;
+  return o;
+}
+
+// The partials of one row: n1 slots from a1 on and n2 from a2 on in steps of `step`.
+struct Parts {
+  int64_t a1, a2;
+  int32_t n1, n2, step, lane1, lane2;
+  EC_DEV int64_t row(int i) const { return i < n1 ? (a1 + i) * kBlockM + lane1 : (a2 + static_cast<int64_t>(i - n1) * step) * kBlockM + lane2; }
+};
+
+// Joins the partial rows of split tiles by their log-sum-exp weights, in slot order. A step takes
+// 16 rows of one tile: one warp a row, or with many partials several warps a row, each every
+// W-th partial. Bound by the partials' bytes, which the attention kernel has just written (L2).
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __grid_constant__ Args a) {
+  constexpr int kWarps = kMergeThreads / 32, kCols = D / 32;
+  __shared__ float acc_s[kWarps][D];
+  const Shape& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Plan pl = make_plan(s, nullptr, false);
+  constexpr int kSteps = kBlockM / kMergeRows;
+  const int64_t tasks = static_cast<int64_t>(pl.shared ? pl.otiles : s.ctas - 1) * kSteps;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int which = static_cast<int>(task / kSteps), step = static_cast<int>(task % kSteps);
+    OwnTile o;
+    Parts ps;
+    if (pl.shared) {
+      o = own_tile(s, pl, which);
+      const int64_t c0 = div_fast(o.u0, pl.chunk);
+      ps.a2 = o.it.tile + c0;
+      ps.n2 = o.it.units > 0 ? static_cast<int>(div_fast(o.u0 + o.it.units - 1, pl.chunk) - c0) + 1 : 0;
+      ps.step = 1;
+    } else {
+      // the tile that the boundary between CTA `which` and the next one cuts, if it began in this CTA
+      const int64_t u = (which + 1) * pl.chunk;
+      if (u >= pl.units) continue;
+      o.it = item_at(s, pl, u);
+      o.u0 = u - o.it.j0;
+      const int64_t c0 = div_fast(o.u0, pl.chunk);
+      if (o.it.j0 == 0 || c0 != which) continue;
+      ps.n1 = 1;
+      ps.a1 = 2 * c0 + 1;
+      ps.a2 = 2 * (c0 + 1);
+      ps.n2 = static_cast<int>(div_fast(o.u0 + o.it.units - 1, pl.chunk) - c0);
+      ps.step = 2;
+    }
+    const int rows = min(kMergeRows, o.it.nrows - step * kMergeRows);
+    if (rows <= 0) continue;
+    // warps per row: the least power of two that leaves a warp four partials, as far as rows are few
+    const int most = pl.shared ? ps.n2 + static_cast<int>(div_fast(pl.nbp, pl.chunk)) + 2 : ps.n1 + ps.n2;
+    int W = 1;
+    while (W < kWarps && W * 4 < most) W *= 2;
+    const int sub = warp % W;
+    for (int r0 = 0; r0 < rows; r0 += kWarps / W) {
+      const int rl = r0 + warp / W;
+      const bool mine = rl < rows;
+      float acc[kCols] = {};
+      float M = -INFINITY, Lsum = 0.f;
+      const int tl = step * kMergeRows + min(rl, rows - 1);  // row of the tile
+      if (pl.shared) {
+        const int64_t gp = o.before + o.it.row0 + tl;
+        const int64_t pt = static_cast<int64_t>(o.it.kvh) * (pl.ptiles / s.Hkv) + (gp >> 7);
+        const int64_t pu = pt * pl.nbp, pc0 = div_fast(pu, pl.chunk);
+        ps.a1 = pt + pc0;
+        ps.n1 = static_cast<int>(div_fast(pu + pl.nbp - 1, pl.chunk) - pc0) + 1;
+        ps.lane1 = static_cast<int>(gp & 127);
+        ps.lane2 = tl;
+      } else {
+        ps.lane1 = ps.lane2 = tl;
+      }
+      const int n = ps.n1 + ps.n2;
+      if (mine) {
+        for (int i = lane; i < n; i += 32) {
+          const float2 st = __ldcg(a.part_stat + ps.row(i));
+          if (st.y != 0.f) M = fmaxf(M, st.x);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        for (int i0 = 0; i0 < n; i0 += 32) {
+          float w = 0.f, wl = 0.f;
+          if (i0 + lane < n) {
+            const float2 st = __ldcg(a.part_stat + ps.row(i0 + lane));
+            if (st.y != 0.f) {
+              w = ex2_approx(st.x - M);
+              wl = w * st.y;
+            }
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
+          Lsum += wl;
+          const int hi = min(32, n - i0);
+#pragma unroll 4
+          for (int i = sub; i < hi; i += W) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const float* src = a.part_o + ps.row(i0 + i) * D + lane * kCols;
+            float x[kCols];
+            if constexpr (kCols == 4) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+              x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+            } else {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+              x[0] = v.x, x[1] = v.y;
+            }
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) acc[e] = wi == 0.f ? acc[e] : fmaf(wi, x[e], acc[e]);
+          }
+        }
+      }
+      if (W > 1) {
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) acc_s[warp][lane * kCols + e] = acc[e];
+        __syncthreads();
+        if (sub == 0)
+          for (int k = 1; k < W; ++k)
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) acc[e] += acc_s[warp + k][lane * kCols + e];
+        __syncthreads();
+      }
+      if (mine && sub == 0) {
+        const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+        const int64_t x = o.it.row0 + tl, r = div_fast(x, s.g);
+        uint16_t* dst = a.out + ((static_cast<int64_t>(o.it.b) * s.L + r) * a.Hq + o.it.kvh * s.g + (x - r * s.g)) * D + lane * kCols;
+        if constexpr (kCols == 4)
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        else
+          *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------- host
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// A cache [B, L, Hkv, D] in boxes of 128 positions of one head: bf16 in swizzled 64-element halves,
+// codes whole and unswizzled. Rows past L read as zeros.
+bool cache_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, bool q8, int D, int Hkv, int L, int B) {
+  const cuuint64_t e = q8 ? 1 : 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(L),
+                              static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {e * D, e * D * Hkv, e * D * Hkv * L};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(q8 ? D : 64), 1, kBlockN, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t part_slots(const ec_params& p, bool prefix) {
+  const int64_t separate = 2 * kMaxCtas;
+  if (!prefix) return separate;
+  // shared tiles at R = L, or as many as a step bound by its bytes can have: past that bound
+  // (eight tiles per SM) tiles are full of rows and the prefix is not shared between tiles
+  const int64_t g = p.Hq / p.Hkv;
+  const int64_t tiles = p.Hkv * ((p.B * (static_cast<int64_t>(p.L) * g) + kBlockM - 1) / kBlockM) +
+                        static_cast<int64_t>(p.B) * p.Hkv * ((static_cast<int64_t>(p.L) * g + kBlockM - 1) / kBlockM);
+  return std::max(separate, std::min<int64_t>(tiles + kMaxCtas, 8 * kMaxCtas));
+}
+
+template <int D, bool Q8>
+cudaError_t launch_impl(const ec_params& p, Args& a, cudaStream_t s) {
+  using LY = Layout<D, Q8>;
+  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(cached_attention_kernel<D, Q8>), LY::kBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(cached_attention_kernel<D, Q8>, dim3(a.s.ctas), dim3(LY::kThreads), LY::kBytes, s, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(cached_merge_kernel<D>, dim3(8 * a.s.ctas), dim3(kMergeThreads), 0, s, a);
+}
+
+}  // namespace
+}  // namespace cached
+
+size_t cached_attention_workspace_bytes(const ec_params& p, bool prefix) {
+  return static_cast<size_t>(cached::part_slots(p, prefix)) * cached::kBlockM * (static_cast<size_t>(p.D) * 4 + sizeof(float2));
+}
+
+cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_kv* prefix, const ec_kv& cache,
+                                    const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,
+                                    int32_t* dev_err, cudaStream_t s, ec_status* status) {
+  using namespace cached;
+  *status = EC_OK;
+  EncodeTiledFn enc = get_encode_fn();
+  if (enc == nullptr) {
+    *status = EC_ERR_CUDA;
+    return cudaErrorNotSupported;
+  }
+  const bool q8 = cache.dtype == EC_E4M3;
+  const bool pre = prefix != nullptr && prefix->len > 0;
+  int sms = 0;
+  cudaError_t e = current_device_sms(&sms);
+  if (e != cudaSuccess) {
+    *status = EC_ERR_CUDA;
+    return e;
+  }
+  Args a;
+  const ec_kv& pc = pre ? *prefix : cache;  // without a prefix its maps are not used
+  const int pB = pre ? 1 : p.B;
+  if (!cache_map(enc, &a.tk, cache.k, q8, p.D, p.Hkv, p.L, p.B) || !cache_map(enc, &a.tv, cache.v, q8, p.D, p.Hkv, p.L, p.B) ||
+      !cache_map(enc, &a.tpk, pc.k, q8, p.D, p.Hkv, pc.len, pB) || !cache_map(enc, &a.tpv, pc.v, q8, p.D, p.Hkv, pc.len, pB)) {
+    *status = EC_ERR_INVALID_ARG;
+    return cudaErrorInvalidValue;
+  }
+  a.ke = cache.k_exp;
+  a.ve = cache.v_exp;
+  a.pke = pc.k_exp;
+  a.pve = pc.v_exp;
+  a.s.R = R;
+  a.s.kv_len = kv_len;
+  a.s.B = p.B;
+  a.s.L = p.L;
+  a.s.Lk = scope_hi(p);
+  a.s.Lp = pre ? prefix->len : 0;
+  a.s.Hkv = p.Hkv;
+  a.s.g = p.Hq / p.Hkv;
+  a.s.ctas = std::min(sms, kMaxCtas);
+  a.s.slots = static_cast<int32_t>(part_slots(p, pre));
+  a.Hq = p.Hq;
+  a.Ls = static_cast<int32_t>(quant_exp_stride(p.L));
+  a.Lps = static_cast<int32_t>(quant_exp_stride(pc.len));
+  a.scale_log2 = scale * kLog2e;
+  a.q = static_cast<const uint16_t*>(q);
+  a.out = static_cast<uint16_t*>(out);
+  a.part_o = static_cast<float*>(ws);
+  a.part_stat = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.s.slots) * kBlockM * p.D);
+  a.dev_err = dev_err;
+  if (p.D == 128)
+    e = q8 ? launch_impl<128, true>(p, a, s) : launch_impl<128, false>(p, a, s);
+  else
+    e = q8 ? launch_impl<64, true>(p, a, s) : launch_impl<64, false>(p, a, s);
+  if (e != cudaSuccess) *status = EC_ERR_CUDA;
+  return e;
+}
+
+}  // namespace ec

@@ -78,6 +78,23 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
+struct Extent {
+  const void* p;
+  size_t n;
+};
+
+// A buffer of `w` shares bytes with another one of `w` or with one of `r`.
+template <size_t W, size_t N>
+bool any_overlap(const Extent (&w)[W], const Extent (&r)[N]) {
+  for (size_t i = 0; i < W; ++i) {
+    for (size_t j = i + 1; j < W; ++j)
+      if (overlaps(w[i].p, w[i].n, w[j].p, w[j].n)) return true;
+    for (size_t j = 0; j < N; ++j)
+      if (r[j].p != nullptr && overlaps(w[i].p, w[i].n, r[j].p, r[j].n)) return true;
+  }
+  return false;
+}
+
 size_t q_bytes(const ec_params& p) { return static_cast<size_t>(p.B) * p.L * p.Hq * p.D * 2; }
 size_t kv_bytes(const ec_params& p) { return static_cast<size_t>(p.B) * p.L * p.Hkv * p.D * 2; }
 
@@ -325,6 +342,118 @@ ec_status ec_partial_attention(const ec_params* p, const void* q, const void* k_
   launch_partial_attention(*p, q, k_cache, v_cache, R, scale, out, ws, dev_err, false, static_cast<cudaStream_t>(stream),
                            &st);
   return st;
+}
+
+// ---- 8-bit cache, shared prefix ------------------------------------------------------------------
+namespace {
+
+size_t kv_extent(const ec_params& p, const ec_kv& c, int32_t B) {
+  return static_cast<size_t>(B) * c.len * p.Hkv * p.D * (c.dtype == EC_BF16 ? 2 : 1);
+}
+size_t exp_extent(const ec_params& p, const ec_kv& c, int32_t B) {
+  return c.dtype == EC_BF16 ? 0 : static_cast<size_t>(B) * p.Hkv * quant_exp_stride(c.len);
+}
+
+// The cache `c` of len positions has a type, pointers and alignment that the kernels take.
+ec_status check_kv(const ec_kv* c, int32_t len) {
+  if (c == nullptr || c->len != len) return EC_ERR_INVALID_ARG;
+  if (c->dtype != EC_BF16 && c->dtype != EC_E4M3) return EC_ERR_INVALID_ARG;
+  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return EC_ERR_INVALID_ARG;
+  if (c->dtype == EC_E4M3 && (!c->k_exp || !c->v_exp || !aligned16(c->k_exp) || !aligned16(c->v_exp)))
+    return EC_ERR_INVALID_ARG;
+  return EC_OK;
+}
+
+ec_status check_quant_rows(const ec_params* p, const ec_kv* c) {
+  if (p == nullptr) return EC_ERR_INVALID_ARG;
+  if (p->B < 1 || p->B > kMaxB || p->L < 1 || p->L > kMaxL || p->Hkv < 1 || p->Hkv > 65536) return EC_ERR_INVALID_ARG;
+  if (p->D != 64 && p->D != 128) return EC_ERR_UNSUPPORTED;
+  const ec_status r = check_kv(c, p->L);
+  if (r != EC_OK) return r;
+  return c->dtype == EC_E4M3 ? EC_OK : EC_ERR_UNSUPPORTED;
+}
+
+ec_status cached_attention(const ec_params* p, const void* q, const ec_kv* prefix, const ec_kv* cache,
+                           const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,
+                           size_t ws_bytes, size_t ws_need, int32_t* dev_err, ec_stream_t stream) {
+  ec_status r = check_kv(cache, p->L);
+  if (r != EC_OK) return r;
+  if (!q || !R || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws)) return EC_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || scale > 3e38f || ws_bytes < ws_need) return EC_ERR_INVALID_ARG;
+  static const ec_kv none{};
+  const ec_kv* pre = prefix != nullptr && prefix->len != 0 ? prefix : &none;
+  if (pre->len != 0) {
+    if (pre->len < 0 || pre->len > kMaxL) return EC_ERR_INVALID_ARG;
+    if ((r = check_kv(pre, pre->len)) != EC_OK) return r;
+    if (pre->dtype != cache->dtype) return EC_ERR_UNSUPPORTED;
+  }
+  const size_t n = kv_extent(*p, *cache, p->B), ne = exp_extent(*p, *cache, p->B);
+  const size_t np = kv_extent(*p, *pre, 1), npe = exp_extent(*p, *pre, 1);
+  const Extent written[] = {{out, q_bytes(*p)}, {ws, ws_need}};
+  const Extent read[] = {{q, q_bytes(*p)},    {cache->k, n},      {cache->v, n},      {ne ? cache->k_exp : nullptr, ne},
+                         {ne ? cache->v_exp : nullptr, ne},       {pre->k, np},       {pre->v, np},
+                         {npe ? pre->k_exp : nullptr, npe},       {npe ? pre->v_exp : nullptr, npe}};
+  if (any_overlap(written, read)) return EC_ERR_INVALID_ARG;
+  ec_status st = EC_OK;
+  launch_cached_attention(*p, q, pre->len != 0 ? pre : nullptr, *cache, R, kv_len, scale, out, ws, dev_err,
+                          static_cast<cudaStream_t>(stream), &st);
+  return st;
+}
+
+}  // namespace
+
+ec_status ec_kv_scatter_quant(const ec_params* p, const ec_kv* cache, const void* k_new, const void* v_new,
+                              int32_t src_by_position, const int32_t* idx, const int32_t* R, int32_t* dev_err,
+                              ec_stream_t stream) {
+  const ec_status r = check_quant_rows(p, cache);
+  if (r != EC_OK) return r;
+  if (src_by_position != 0 && src_by_position != 1) return EC_ERR_INVALID_ARG;
+  if (!k_new || !v_new || !idx || !R || !aligned16(k_new) || !aligned16(v_new)) return EC_ERR_INVALID_ARG;
+  const size_t n = kv_extent(*p, *cache, p->B), ne = exp_extent(*p, *cache, p->B);
+  const Extent written[] = {{cache->k, n}, {cache->v, n}, {cache->k_exp, ne}, {cache->v_exp, ne}};
+  const Extent read[] = {{k_new, kv_bytes(*p)}, {v_new, kv_bytes(*p)}};
+  if (any_overlap(written, read)) return EC_ERR_INVALID_ARG;
+  return cuda_status(launch_kv_scatter_quant(*p, *cache, k_new, v_new, src_by_position, idx, R, dev_err,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+ec_status ec_kv_gather_quant(const ec_params* p, const ec_kv* cache, const int32_t* idx, const int32_t* R,
+                             void* k_out, void* v_out, int32_t* dev_err, ec_stream_t stream) {
+  const ec_status r = check_quant_rows(p, cache);
+  if (r != EC_OK) return r;
+  if (!R || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return EC_ERR_INVALID_ARG;
+  const size_t n = kv_extent(*p, *cache, p->B), ne = exp_extent(*p, *cache, p->B);
+  const Extent written[] = {{k_out, kv_bytes(*p)}, {v_out, kv_bytes(*p)}};
+  const Extent read[] = {{cache->k, n}, {cache->v, n}, {cache->k_exp, ne}, {cache->v_exp, ne}};
+  if (any_overlap(written, read)) return EC_ERR_INVALID_ARG;
+  return cuda_status(launch_kv_gather_quant(*p, *cache, idx, R, k_out, v_out, dev_err, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ec_partial_attention_quant_workspace_size(const ec_params* p) {
+  return check_params(p, kCheckAttn) != EC_OK ? 0 : cached_attention_workspace_bytes(*p, false);
+}
+
+ec_status ec_partial_attention_quant(const ec_params* p, const void* q, const ec_kv* cache, const int32_t* R,
+                                     const int32_t* kv_len, float scale, void* out, void* ws, size_t ws_bytes,
+                                     int32_t* dev_err, ec_stream_t stream) {
+  const ec_status r = check_params(p, kCheckAttn);
+  if (r != EC_OK) return r;
+  if (cache != nullptr && cache->dtype == EC_BF16) return EC_ERR_UNSUPPORTED;
+  return cached_attention(p, q, nullptr, cache, R, kv_len, scale, out, ws, ws_bytes,
+                          cached_attention_workspace_bytes(*p, false), dev_err, stream);
+}
+
+size_t ec_prefix_attention_workspace_size(const ec_params* p) {
+  return check_params(p, kCheckAttn) != EC_OK ? 0 : cached_attention_workspace_bytes(*p, true);
+}
+
+ec_status ec_prefix_attention(const ec_params* p, const void* q, const ec_kv* prefix, const ec_kv* cache,
+                              const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,
+                              size_t ws_bytes, int32_t* dev_err, ec_stream_t stream) {
+  const ec_status r = check_params(p, kCheckAttn);
+  if (r != EC_OK) return r;
+  return cached_attention(p, q, prefix, cache, R, kv_len, scale, out, ws, ws_bytes,
+                          cached_attention_workspace_bytes(*p, true), dev_err, stream);
 }
 
 // ---- the partial forward of one layer --------------------------------------------------------------

@@ -75,6 +75,19 @@ cudaError_t launch_partial_attention(const ec_params& p, const void* q, const vo
                                      const void* v_cache, const int32_t* R, float scale, void* out, void* ws,
                                      int32_t* dev_err, bool plan_early, cudaStream_t s, ec_status* status);
 
+// ---- 8-bit cache (kv_quant.cu) and the attentions that read it or a shared prefix -------------
+inline size_t quant_exp_stride(int32_t L) { return (static_cast<size_t>(L) + 15) / 16 * 16; }  // bytes of an exponent row
+cudaError_t launch_kv_scatter_quant(const ec_params& p, const ec_kv& c, const void* k_new, const void* v_new,
+                                    int32_t src_by_position, const int32_t* idx, const int32_t* R, int32_t* dev_err,
+                                    cudaStream_t s);
+cudaError_t launch_kv_gather_quant(const ec_params& p, const ec_kv& c, const int32_t* idx, const int32_t* R,
+                                   void* k_out, void* v_out, int32_t* dev_err, cudaStream_t s);
+// prefix (may be null): shared by every sequence, of the cache's type.
+size_t cached_attention_workspace_bytes(const ec_params& p, bool prefix);
+cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_kv* prefix, const ec_kv& cache,
+                                    const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,
+                                    int32_t* dev_err, cudaStream_t s, ec_status* status);
+
 // ---- dense attention, two query tiles per CTA (attention_dense.cu): every position against
 // every key ---------------------------------------------------------------------------------
 cudaError_t launch_dense_attention_tiles(const ec_params& p, const void* q, const void* k_cache, const void* v_cache,

@@ -19,6 +19,10 @@
  *       (or, for a step known to be full, of every row: ec_dense_attention)
  *   ec_step runs (a)(b)(c) once and then (c-scatter)(d) for every layer.
  *
+ * A cache may be held in 8 bits: ec_kv_scatter_quant and ec_kv_gather_quant write and read it,
+ * ec_partial_attention_quant attends to it. ec_prefix_attention serves a batch whose sequences
+ * share a prefix.
+ *
  * Beyond the step: ec_layer_forward runs the partial (or full) forward of one transformer layer
  * for the recompute set; ec_lm_head_entropy computes (a) from the candidates' hidden states (the
  * output projection fused with the decode, so the logits are never stored); ec_candidates builds
@@ -67,10 +71,12 @@ typedef int32_t ec_status;
 #define EC_DEVERR_BAD_IDX 0x2       /* recompute index outside [0, L)                    */
 #define EC_DEVERR_BAD_R 0x4         /* recompute-set size outside [0, L]                 */
 #define EC_DEVERR_TIMEOUT 0x8       /* a bounded pipeline wait ran out                   */
+#define EC_DEVERR_BAD_LEN 0x10      /* key length outside [0, L]                         */
 
 /* ---- logits element types ------------------------------------------------------------ */
 #define EC_F32 0
 #define EC_BF16 1
+#define EC_E4M3 2 /* caches only: 8-bit rows with an exponent byte each (ec_kv) */
 
 typedef void* ec_stream_t; /* a cudaStream_t */
 
@@ -343,6 +349,84 @@ ec_status ec_partial_attention(const ec_params* p, const void* q, const void* k_
  * must not overlap q, k_cache or v_cache (EC_ERR_INVALID_ARG). */
 ec_status ec_dense_attention(const ec_params* p, const void* q, const void* k_cache, const void* v_cache,
                              float scale, void* out, int32_t* dev_err, ec_stream_t stream);
+
+/* ---- K/V caches by type ------------------------------------------------------------------
+ * One layer's K/V cache of `len` positions per sequence. The pages keep the cache in the
+ * model's precision; the 8-bit form has no counterpart there.
+ *   EC_BF16  k, v bf16 [B, len, Hkv, D]; k_exp, v_exp unused.
+ *   EC_E4M3  k, v e4m3 codes [B, len, Hkv, D], k_exp, v_exp uint8 [B, Hkv, S] with S = len
+ *            rounded up to a multiple of 16 (positions len .. S-1 are never used). The row of
+ *            position j and KV head h stands for code * 2^(exp[b, h, j] - 127). As written by
+ *            ec_kv_scatter_quant the exponent is the smallest integer e >= -110 with
+ *            max|x| <= 448 * 2^e, and code = x * 2^-e rounded once to the nearest e4m3 (ties to
+ *            even; at e = 120 codes stop at 240, so that every value is a bf16 number).
+ *            Exponent byte 255: the row held an infinity or a NaN and reads as NaN.
+ *            The readers take bytes 17 .. 247 and 255.
+ * Every pointer 16-byte aligned. */
+typedef struct ec_kv {
+  int32_t dtype;
+  int32_t len;
+  void *k, *v;
+  uint8_t *k_exp, *v_exp;
+} ec_kv;
+
+/* ---- (c) refresh of an 8-bit K/V cache ----------------------------------------------------
+ * ec_kv_scatter with the rows quantised as they are written. For r < R[b], every KV head:
+ *   cache[b, idx[b, r]] = quantise(k_new[b, src_row]) and the same for v,
+ * src_row as in ec_kv_scatter. cache: EC_E4M3, len = p->L. k_new, v_new bf16 [B, L, Hkv, D].
+ * With src_by_position == 0 the idx of a sequence ascend strictly, as ec_select_recompute
+ * writes them: an idx that is not below its successor sets EC_DEVERR_BAD_IDX and its row is
+ * skipped (a position given twice would be written by two rows at once; what a list that is
+ * reported as bad leaves at such a position is unspecified). An idx outside [0, L) sets
+ * EC_DEVERR_BAD_IDX and its row is skipped; R outside [0, L] sets EC_DEVERR_BAD_R and that
+ * sequence is skipped. The four arrays of the cache must not overlap each other or the fresh
+ * rows (EC_ERR_INVALID_ARG). Hkv <= 65536, D 64 or 128. */
+ec_status ec_kv_scatter_quant(const ec_params* p, const ec_kv* cache, const void* k_new, const void* v_new,
+                              int32_t src_by_position, const int32_t* idx, const int32_t* R, int32_t* dev_err,
+                              ec_stream_t stream);
+
+/* Rows of an 8-bit cache back as bf16 (exact): for r < R[b], k_out[b, r] = cache.k[b, idx[b, r]],
+ * the same for v. idx NULL: the positions 0 .. R[b]-1. k_out, v_out bf16 [B, L, Hkv, D]; rows at
+ * and past R[b] are not written. Checks as ec_kv_scatter_quant; idx in any order, repeats
+ * allowed. The outputs must not overlap the cache or each other. */
+ec_status ec_kv_gather_quant(const ec_params* p, const ec_kv* cache, const int32_t* idx, const int32_t* R,
+                             void* k_out, void* v_out, int32_t* dev_err, ec_stream_t stream);
+
+/* ---- (d) partial attention against an 8-bit cache -------------------------------------------
+ * ec_partial_attention with K and V read from an EC_E4M3 cache (len = p->L) and a key length
+ * per sequence: row r < R[b] attends to the keys j < n, n = kv_len[b], or with kv_len NULL all
+ * keys of the gate's scope ([0, L), or [0, scope_hi)); a kv_len past scope_hi is cut there. What
+ * lies in the cache past n is not used, NaN included. n = 0: the row is zeros, as it is when
+ * every score is -infinity. R[b] = 1 is the single-token form.
+ * kv_len int32 [B] on the device, or NULL. A length outside [0, L] sets EC_DEVERR_BAD_LEN, an R
+ * outside [0, L] EC_DEVERR_BAD_R; the sequence is skipped.
+ * scale must be above 0 and finite. ws: ec_partial_attention_quant_workspace_size(p) bytes,
+ * 16-byte aligned, no initial contents needed; calls that share it must not overlap in time. It
+ * must not overlap the other buffers, nor out the inputs (EC_ERR_INVALID_ARG).
+ * The dequantised values are exact in bf16; products, sums and rounding as
+ * ec_partial_attention. Two launches (attention, merge of split tiles), no atomics: the same
+ * inputs give the same bits. */
+size_t ec_partial_attention_quant_workspace_size(const ec_params* p);
+ec_status ec_partial_attention_quant(const ec_params* p, const void* q, const ec_kv* cache, const int32_t* R,
+                                     const int32_t* kv_len, float scale, void* out, void* ws, size_t ws_bytes,
+                                     int32_t* dev_err, ec_stream_t stream);
+
+/* ---- (d) attention for a batch that shares a prefix -------------------------------------------
+ * Block-by-block decoding computes a prompt's K/V before the blocks that follow it, so a batch
+ * of sequences behind one prompt holds them once (the scope of ec_params; pt summary §5, zh
+ * summary §5). For r < R[b]:
+ *   out[b, r, h, :] = softmax over the keys of `prefix` [len, Hkv, D], which every sequence
+ *   sees whole, followed by the sequence's own keys (cache, len = p->L, and kv_len, as in
+ *   ec_partial_attention_quant) of scale <q, k>, times the values.
+ * Positions (idx, scope) count within the own cache. prefix: an ec_kv of one sequence
+ * ([len, Hkv, D], 0 <= len <= 2^20; len 0 or NULL: no prefix), of the cache's dtype, EC_BF16 or
+ * EC_E4M3 (types that differ return EC_ERR_UNSUPPORTED).
+ * Where rows of different sequences fit into one 128-row tile, the prefix is multiplied once
+ * for all of them. Everything else as ec_partial_attention_quant. */
+size_t ec_prefix_attention_workspace_size(const ec_params* p);
+ec_status ec_prefix_attention(const ec_params* p, const void* q, const ec_kv* prefix, const ec_kv* cache,
+                              const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,
+                              size_t ws_bytes, int32_t* dev_err, ec_stream_t stream);
 
 /* ---- the partial forward of one transformer layer ------------------------------------------
  * The forward pass the step's flag selects (EntropyCache, gist.science zh summary §2.2,
