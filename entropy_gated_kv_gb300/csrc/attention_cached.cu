@@ -10,7 +10,8 @@
 //   keys and the sequence's own kv_len[b] keys, KV head h / g;  zeros when there is no key
 //
 // Structure (one CTA per SM; the work plan is attention_cached.cuh's):
-//   warp 0       TMA producer: K and V blocks of 128 keys.
+//   warp 0       makes the work plan, hands out the CTA's items, and is the TMA producer: K and V
+//                blocks of 128 keys.
 //   warp 1       allocates 512 TMEM columns and issues tcgen05.mma.
 //   warps 2, 3   the query tile, row by row with cp.async (a tile packs rows of any sequences, which
 //                no one tensor box covers), swizzled by hand.
@@ -55,6 +56,8 @@ constexpr int kMaxRaw = 3;
 constexpr int kDequantWarps = 4;
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 16;  // rows of a tile per merge CTA step
+constexpr int kItems = 8;       // items handed out and not yet finished, see the producer
+constexpr int kCum = 32;        // sequences whose row ends are kept in shared memory
 constexpr uint32_t kDescHi = sdesc_hi(1024);
 constexpr int kAtomBytes = 128 * 128;  // 128 rows x 128 bytes (64 bf16), 128-byte swizzle
 __host__ __device__ constexpr uint32_t step_qk(int kk) { return (kk >> 2) * (kAtomBytes / 16) + (kk & 3) * 2; }
@@ -65,15 +68,15 @@ struct Bars {
   uint64_t unit_full[kMaxUnits], unit_empty[kMaxUnits];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t o_free;
+  uint64_t join, o_free;
+  uint64_t item_full[kItems];
   uint32_t tmem_base;
   int abort;
-  int give_up;  // set by a softmax warp before the join of an item
 };
 
 // Shared memory: the query tile, a ring of bf16 tiles (K and V of a block in turn), for the 8-bit
 // cache a ring of raw tiles (128 rows of codes, then 128 exponent bytes), the row statistics that
-// the two streams exchange, the barriers.
+// the two streams exchange, the items, where each sequence's packed rows end, the barriers.
 template <int D, bool Q8>
 struct Layout {
   static constexpr int kAtoms = D / 64;
@@ -84,7 +87,9 @@ struct Layout {
   static constexpr int kUnitOff = kTileBytes;
   static constexpr int kRawOff = kUnitOff + kUnits * kTileBytes;
   static constexpr int kStatOff = kRawOff + kRaw * kRawBytes;
-  static constexpr int kBarOff = kStatOff + 2 * kBlockM * static_cast<int>(sizeof(float2));
+  static constexpr int kItemOff = kStatOff + 2 * kBlockM * static_cast<int>(sizeof(float2));
+  static constexpr int kCumOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
+  static constexpr int kBarOff = kCumOff + kCum * 4;
   static constexpr int kBytes = kBarOff + static_cast<int>(sizeof(Bars));
   static constexpr int kThreads = Q8 ? 512 : 384;
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -100,6 +105,8 @@ struct Args {
   uint16_t* out;
   float* part_o;      // [slots][128][D]
   float2* part_stat;  // [slots][128]: running maximum and sum
+  Header* header;
+  Record* records;    // [max(slots, ctas)]
   int32_t* dev_err;
 };
 
@@ -146,31 +153,45 @@ EC_DEV uint32_t ld_shared8(uint32_t src) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])          \
       : "memory")
 
-// Whole warp: where packed row x of KV head kvh of the item lies in q, as (b L + r) Hq + h.
-EC_DEV int64_t query_row(const Args& a, const Plan& pl, const Item& it, int64_t x) {
+// Whole warp: where packed row x of the item's KV head lies in q, as (b L + r) Hq + h.
+EC_DEV int query_row(const Args& a, const int32_t* cum, const Item& it, int x) {
   const Shape& s = a.s;
   int b = it.b;
   if (it.b < 0) {  // row x over all sequences: b is the number of sequences that end at or before it
-    const int lane = threadIdx.x & 31;
-    int64_t base = 0, before = 0;
+    int before = 0;
     b = 0;
-    for (int b0 = 0; b0 < s.B; b0 += 32) {
-      int32_t r, n;
-      seq_of(s, pl, b0 + lane, r, n);
-      const int64_t incl = warp_inclusive(static_cast<int64_t>(r) * s.g);
-      for (int i = 0; i < min(32, s.B - b0); ++i) {
-        const int64_t e = base + __shfl_sync(0xffffffffu, incl, i);
+    if (s.B <= kCum) {
+#pragma unroll 1
+      for (int i = 0; i < s.B; ++i) {
+        const int e = cum[i];
         if (e <= x) {
-          b = b0 + i + 1;
+          b = i + 1;
           before = e;
         }
       }
-      base += __shfl_sync(0xffffffffu, incl, 31);
+    } else {
+      const int lane = threadIdx.x & 31;
+      int base = 0;
+#pragma unroll 1
+      for (int b0 = 0; b0 < s.B; b0 += 32) {
+        int32_t r, n;
+        load_seq(s, b0 + lane, r, n, nullptr, false);
+        const int incl = base + warp_inclusive(r * s.g);
+#pragma unroll 1
+        for (int i = 0; i < min(32, s.B - b0); ++i) {
+          const int e = __shfl_sync(0xffffffffu, incl, i);
+          if (e <= x) {
+            b = b0 + i + 1;
+            before = e;
+          }
+        }
+        base = __shfl_sync(0xffffffffu, incl, 31);
+      }
     }
     x -= before;
   }
-  const int64_t r = div_fast(x, s.g);
-  return (static_cast<int64_t>(b) * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g);
+  const int r = div_down(x, s.g);
+  return (b * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g);
 }
 
 // Keys of block j of the item that take part.
@@ -204,10 +225,11 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       mbar_init(&bars->p_full[i], 4);
       mbar_init(&bars->pv_done[i], 1);
     }
+    mbar_init(&bars->join, 8);
     mbar_init(&bars->o_free, 8);
+    for (int i = 0; i < kItems; ++i) mbar_init(&bars->item_full[i], 1);
     // the swizzled tiles need the 1024-byte alignment that dynamic shared memory has here
     bars->abort = (smem_u32(smem) & 1023u) != 0u;
-    bars->give_up = 0;
     if (bars->abort) report_error(a.dev_err, EC_DEVERR_TIMEOUT);
     fence_mbar_init();
   }
@@ -225,21 +247,62 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort;
 
-  pdl_wait();  // everything above overlaps the previous kernel
-  const Plan pl = make_plan(s, a.dev_err, blockIdx.x == 0 && warp == 0);
-  pdl_launch_dependents();
-  const int cta = static_cast<int>(blockIdx.x);
-  const int64_t u0 = cta * pl.chunk, uend = *abort_flag ? u0 : min(pl.units, u0 + pl.chunk);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_wait_bounded(bar, parity, abort_flag, a.dev_err, kWaitLimitNs);
   };
+  // The n-th item of this CTA, once the producer has made it; nblk = 0 at the end and after a wait
+  // that gave up.
+  Item* const items_s = reinterpret_cast<Item*>(smem + LY::kItemOff);
+  auto next_item = [&](int n) {
+    Item it;
+    const bool ok = __all_sync(0xffffffffu, wait(&bars->item_full[n % kItems], (n / kItems) & 1));
+    const uint32_t src = smem_u32(items_s + n % kItems);
+    uint4* dst = reinterpret_cast<uint4*>(&it);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) dst[i] = ld_shared16(src + 16 * i);
+    if (!ok) it.nblk = 0;
+    return it;
+  };
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------------ plan, TMA producer
+    pdl_wait();  // everything above overlaps the previous kernel
+    const int cta = static_cast<int>(blockIdx.x);
+    const Plan pl = make_plan(s, a.dev_err, cta == 0);
+    pdl_launch_dependents();
+    const int u0 = min(pl.units, cta * pl.chunk), uend = *abort_flag ? u0 : min(pl.units, u0 + pl.chunk);
+    if (pl.shared && s.B <= kCum) {
+      const int incl = warp_inclusive(pl.rows_l * s.g);
+      if (lane < s.B) reinterpret_cast<int32_t*>(smem + LY::kCumOff)[lane] = incl;
+      __syncwarp();
+    }
     uint32_t n = 0;  // tiles requested: K and V of each block in turn
-    int ok = 1;
-    for (int64_t u = u0; ok && u < uend;) {
-      const Item it = cta_item(s, pl, u, uend);
+    int ok = 1, count = 0;
+    Record rec{};
+    for (int u = u0;; ++count) {
+      Item it;
+      it.nblk = 0;
+      if (ok && u < uend) it = cta_item(s, pl, u, uend, cta);
+      // Slot count % kItems is free: it held item count - 8, and with that one's epilogue still to come
+      // no V tile of the item after it can have been released, so that the producer would be
+      // waiting for room at the latest with the fifth item after it.
+      if (lane == 0) {
+        items_s[count % kItems] = it;
+        mbar_arrive(&bars->item_full[count % kItems]);
+      }
+      if (it.nblk == 0) break;
+      if (it.slot >= 0 && it.j0 == 0 && it.b >= 0) {
+        rec.b = it.b;
+        rec.kvh = it.kvh;
+        rec.row0 = it.row0;
+        rec.nrows = it.nrows;
+        rec.before = it.before;
+        const int last = div_down(u + it.units - 1, pl.chunk);  // the CTA that ends the tile
+        rec.a1 = it.slot;
+        rec.a2 = pl.shared ? it.slot : 2 * (cta + 1);
+        rec.n2 = last - cta + (pl.shared ? 1 : 0);
+        if (pl.shared && lane == 0) a.records[it.tile - pl.ptiles] = rec;
+      }
       if (lane == 0) {
         for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j) {
           const bool pre = j < it.np;
@@ -274,6 +337,18 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       u += it.nblk;
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
+    if (lane == 0) {
+      if (!pl.shared) a.records[cta] = rec;
+      if (cta == 0) {
+        Header h{};
+        h.records = pl.shared ? pl.otiles : s.ctas;
+        h.shared = pl.shared;
+        h.nbp = pl.nbp;
+        h.chunk = pl.chunk;
+        h.ptiles_head = div_down(pl.ptiles, s.Hkv);
+        *a.header = h;
+      }
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer (whole warp, lane 0 issues)
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlockN, 0);
@@ -281,12 +356,11 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
     uint32_t n0 = 0;              // tiles of the items before
     uint32_t used[2] = {0, 0};    // products finished or under way per stream
-    int items = 0;
     bool ok = true;
     auto wait_w = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-    for (int64_t u = u0; ok && u < uend; ++items) {
-      const Item it = cta_item(s, pl, u, uend);
-      u += it.nblk;
+    for (int items = 0; ok; ++items) {
+      const Item it = next_item(items);
+      if (it.nblk == 0) break;
       auto issue_qk = [&](int i) {  // S of block i into its stream's buffer
         const int st = i & 1;
         const uint32_t n = n0 + 2 * i, slot = n % kUnits;
@@ -349,32 +423,29 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------------ query loader
-    constexpr int kChunks = D / 8;       // 16-byte pieces of a row
+    constexpr int kChunks = D / 8;  // 16-byte pieces of a row
     constexpr int kRowsStep = 32 / kChunks;
-    const int w = warp - 2;              // rows [64 w, 64 w + 64)
-    const uint32_t dst0 = smem_u32(smem);
     const int chunk = lane % kChunks;
-    int items = 0;
-    bool ok = true;
-    for (int64_t u = u0; ok && u < uend; ++items) {
-      const Item it = cta_item(s, pl, u, uend);
-      u += it.nblk;
-      const int64_t last = it.row0 + it.nrows - 1;  // rows past the last are loaded as zeros
-      int64_t at[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) at[i] = query_row(a, pl, it, min(last, it.row0 + 64 * w + 32 * i + lane));
-      if (items > 0) ok = __all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1));
-      if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < 64 / kRowsStep; ++i) {
-        const int rl = i * kRowsStep + lane / kChunks;  // row within this warp's 64
-        const int64_t src = __shfl_sync(0xffffffffu, at[i * kRowsStep / 32], rl & 31);
-        const int row = 64 * w + rl;
-        const uint32_t dst = dst0 + (chunk >> 3) * kAtomBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-        if (row < it.nrows)
-          cp_async16(dst, a.q + src * D + chunk * 8);
-        else
-          st_shared16(dst, make_uint4(0, 0, 0, 0));
+    const int32_t* cum = reinterpret_cast<const int32_t*>(smem + LY::kCumOff);
+    for (int items = 0;; ++items) {
+      const Item it = next_item(items);
+      if (it.nblk == 0) break;
+      if (items > 0 && !__all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1))) break;
+#pragma unroll 1
+      for (int h = 0; h < 64; h += 32) {  // 32 rows at a time; each lane finds one of them
+        const int row0 = 64 * (warp - 2) + h;
+        // rows past the last are zeros
+        const int at = query_row(a, cum, it, it.row0 + min(row0 + lane, it.nrows - 1));
+#pragma unroll 4
+        for (int i = lane / kChunks; i < 32; i += kRowsStep) {
+          const int64_t src = __shfl_sync(0xffffffffu, at, i);
+          const int row = row0 + i;
+          const uint32_t dst = smem_u32(smem) + (chunk >> 3) * kAtomBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+          if (row < it.nrows)
+            cp_async16(dst, a.q + src * D + chunk * 8);
+          else
+            st_shared16(dst, make_uint4(0, 0, 0, 0));
+        }
       }
       cp_async_wait_all();
       fence_proxy_async_smem();
@@ -389,9 +460,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
     uint32_t used = 0, used_other = 0;  // blocks of this stream and of the other one
     bool ok = true;
-    for (int64_t u = u0; ok && u < uend;) {
-      const Item it = cta_item(s, pl, u, uend);
-      u += it.nblk;
+    for (int items = 0; ok; ++items) {
+      const Item it = next_item(items);
+      if (it.nblk == 0) break;
       const bool live = 32 * (warp & 3) < it.nrows;  // else the warp's rows are all padding
       float m_used = -INFINITY, l_sum = 0.f;
       for (int i = st; i < it.nblk; i += 2, ++used) {
@@ -479,37 +550,39 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       // join the two streams: each warpgroup takes half of the columns of both accumulators
       const int n_mine = (it.nblk + 1 - st) >> 1, n_other = it.nblk - n_mine;
       used_other += n_other;
+      if (ok && n_mine > 0) ok = wait(&bars->pv_done[st], (used - 1) & 1u);
+      if (ok && n_other > 0) ok = wait(&bars->pv_done[st ^ 1], (used_other - 1) & 1u);
+      // this item's products began after every warp was done with the item before (o_free), so its
+      // statistics may be overwritten
       stat[st * kBlockM + row] = make_float2(m_used, l_sum);
-      if (n_mine > 0) ok = ok && wait(&bars->pv_done[st], (used - 1) & 1u);
-      if (n_other > 0) ok = ok && wait(&bars->pv_done[st ^ 1], (used_other - 1) & 1u);
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&bars->join);
+      ok = ok && wait(&bars->join, items & 1);
       ok = __all_sync(0xffffffffu, ok);
-      // a warp whose wait gave up still meets the others at both barriers, and all eight leave together
-      if (!ok && lane == 0) bars->give_up = 1;
-      named_bar_sync(2, 256);
-      ok = !*static_cast<volatile int*>(&bars->give_up);
+      if (!ok) break;
       tc_fence_after();
-      if (ok && live) {
+      if (live) {
         const float2 s0 = stat[row], s1 = stat[kBlockM + row];
         const float M = fmaxf(s0.x, s1.x);
         // a stream without weight (no block, or no finite score) contributes nothing
         const bool has0 = s0.y != 0.f, has1 = it.nblk > 1 && s1.y != 0.f;
         const float w0 = has0 ? ex2_approx(s0.x - M) : 0.f, w1 = has1 ? ex2_approx(s1.x - M) : 0.f;
         const float L = (has0 ? w0 * s0.y : 0.f) + (has1 ? w1 * s1.y : 0.f);
-        const bool complete = item_complete(pl, it);
+        const bool complete = it.slot < 0;
         const float norm = complete ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
         const float f0 = w0 * norm, f1 = w1 * norm;
         const bool valid = row < it.nrows;
         uint16_t* orow = nullptr;
         float* prow = nullptr;
         if (complete) {
-          const int64_t x = it.row0 + row, r = div_fast(x, s.g);
-          orow = a.out + ((static_cast<int64_t>(it.b) * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g)) * D + st * (D / 2);
+          const int x = it.row0 + row, r = div_down(x, s.g);
+          orow = a.out + static_cast<int64_t>((it.b * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g)) * D + st * (D / 2);
         } else {
-          const int64_t slot = item_slot(pl, it, cta);
-          prow = a.part_o + (slot * kBlockM + row) * D + st * (D / 2);
-          if (st == 0 && valid) a.part_stat[slot * kBlockM + row] = make_float2(M, L);
+          const int at = it.slot * kBlockM + row;
+          prow = a.part_o + static_cast<int64_t>(at) * D + st * (D / 2);
+          if (st == 0 && valid) a.part_stat[at] = make_float2(M, L);
         }
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           uint32_t o0[32], o1[32];
           EC_TMEM_LD32(tmem + lane_off + kTmemO + st * (D / 2) + c * 32, o0);
@@ -536,7 +609,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         }
         tc_fence_before();
       }
-      named_bar_sync(2, 256);  // the statistics may be overwritten
+      __syncwarp();
       if (lane == 0) mbar_arrive(&bars->o_free);
     }
   } else if constexpr (Q8) {
@@ -547,9 +620,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     const int t = threadIdx.x - 384;
     uint32_t n = 0;
     bool ok = true;
-    for (int64_t u = u0; ok && u < uend;) {
-      const Item it = cta_item(s, pl, u, uend);
-      u += it.nblk;
+    for (int items = 0; ok; ++items) {
+      const Item it = next_item(items);
+      if (it.nblk == 0) break;
       for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j) {
         const int nv = valid_keys(s, it, j);
         for (int kv = 0; kv < 2; ++kv, ++n) {
@@ -601,137 +674,66 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
 
 // ---------------------------------------------------------------------------------- merge
 
-// A tile of one sequence by its index among those (whole warp): also its first unit and the packed
-// rows of the sequences before it.
-struct OwnTile {
-  Item it;
-  int64_t u0, before;
-};
-
-EC_DEV OwnTile own_tile(const Shape& s, const Plan& pl, int tile) {
-  const int lane = threadIdx.x & 31;
-  OwnTile o;
-  int64_t ubase = pl.own0, rbase = 0;
-  int32_t tbase = 0;
-  for (int b0 = 0; b0 < s.B; b0 += 32) {
-    int32_t r, n;
-    seq_of(s, pl, b0 + lane, r, n);
-    const int32_t t = s.Hkv * tiles_of(s, r), tu = tile_units(pl, n);
-    const int32_t tincl = warp_inclusive(t);
-    const int32_t ttotal = __shfl_sync(0xffffffffu, tincl, 31);
-    const int64_t uincl = warp_inclusive(static_cast<int64_t>(t) * tu);
-    const int64_t rincl = warp_inclusive(static_cast<int64_t>(r) * s.g);
-    if (tile < tbase + ttotal) {
-      const int src = __ffs(__ballot_sync(0xffffffffu, tbase + tincl > tile)) - 1;
-      const int32_t tl = tile - tbase - __shfl_sync(0xffffffffu, tincl - t, src);
-      const int32_t rsel = __shfl_sync(0xffffffffu, r, src), per_head = tiles_of(s, rsel);
-      o.it.len = __shfl_sync(0xffffffffu, n, src);
-      o.it.units = __shfl_sync(0xffffffffu, tu, src);
-      o.it.b = b0 + src;
-      o.it.kvh = tl / per_head;
-      o.it.row0 = static_cast<int64_t>(tl - o.it.kvh * per_head) * kBlockM;
-      o.it.nrows = static_cast<int32_t>(min(static_cast<int64_t>(kBlockM), static_cast<int64_t>(rsel) * s.g - o.it.row0));
-      o.it.tile = pl.ptiles + tile;
-      o.u0 = ubase + __shfl_sync(0xffffffffu, uincl - static_cast<int64_t>(t) * tu, src) + static_cast<int64_t>(tl) * o.it.units;
-      o.before = rbase + __shfl_sync(0xffffffffu, rincl - static_cast<int64_t>(r) * s.g, src);
-      return o;
-    }
-    tbase += ttotal;
-    ubase += __shfl_sync(0xffffffffu, uincl, 31);
-    rbase += __shfl_sync(0xffffffffu, rincl, 31);
-  }
-  o.it.nrows = 0;  // not reached: tile is below pl.otiles
-  o.it.b = o.it.kvh = o.it.units = o.it.tile = o.it.len = 0;
-  o.it.row0 = o.u0 = o.before = 0;
-  return o;
-}
-
-// The partials of one row: n1 slots from a1 on and n2 from a2 on in steps of `step`.
-struct Parts {
-  int64_t a1, a2;
-  int32_t n1, n2, step, lane1, lane2;
-  EC_DEV int64_t row(int i) const { return i < n1 ? (a1 + i) * kBlockM + lane1 : (a2 + static_cast<int64_t>(i - n1) * step) * kBlockM + lane2; }
-};
-
 // Joins the partial rows of split tiles by their log-sum-exp weights, in slot order. A step takes
 // 16 rows of one tile: one warp a row, or with many partials several warps a row, each every
 // W-th partial. Bound by the partials' bytes, which the attention kernel has just written (L2).
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __grid_constant__ Args a) {
-  constexpr int kWarps = kMergeThreads / 32, kCols = D / 32;
+  constexpr int kWarps = kMergeThreads / 32, kCols = D / 32, kSteps = kBlockM / kMergeRows;
   __shared__ float acc_s[kWarps][D];
   const Shape& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const Plan pl = make_plan(s, nullptr, false);
-  constexpr int kSteps = kBlockM / kMergeRows;
-  const int64_t tasks = static_cast<int64_t>(pl.shared ? pl.otiles : s.ctas - 1) * kSteps;
-  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int which = static_cast<int>(task / kSteps), step = static_cast<int>(task % kSteps);
-    OwnTile o;
-    Parts ps;
-    if (pl.shared) {
-      o = own_tile(s, pl, which);
-      const int64_t c0 = div_fast(o.u0, pl.chunk);
-      ps.a2 = o.it.tile + c0;
-      ps.n2 = o.it.units > 0 ? static_cast<int>(div_fast(o.u0 + o.it.units - 1, pl.chunk) - c0) + 1 : 0;
-      ps.step = 1;
-    } else {
-      // the tile that the boundary between CTA `which` and the next one cuts, if it began in this CTA
-      const int64_t u = (which + 1) * pl.chunk;
-      if (u >= pl.units) continue;
-      o.it = item_at(s, pl, u);
-      o.u0 = u - o.it.j0;
-      const int64_t c0 = div_fast(o.u0, pl.chunk);
-      if (o.it.j0 == 0 || c0 != which) continue;
-      ps.n1 = 1;
-      ps.a1 = 2 * c0 + 1;
-      ps.a2 = 2 * (c0 + 1);
-      ps.n2 = static_cast<int>(div_fast(o.u0 + o.it.units - 1, pl.chunk) - c0);
-      ps.step = 2;
-    }
-    const int rows = min(kMergeRows, o.it.nrows - step * kMergeRows);
+  const int4* hp = reinterpret_cast<const int4*>(a.header);
+  const int4 h = __ldcg(hp);  // records, shared, nbp, chunk
+  const int ptiles_head = __ldcg(&a.header->ptiles_head);
+  for (int task = blockIdx.x; task < h.x * kSteps; task += gridDim.x) {
+    // the first steps of all records come first: few rows leave the later ones empty
+    const int step = div_down(task, h.x);
+    const int4* rp = reinterpret_cast<const int4*>(a.records + (task - step * h.x));
+    const int4 t0 = __ldcg(rp), t1 = __ldcg(rp + 1);  // b, kvh, row0, nrows; a1, a2, n2, before
+    const int rows = min(kMergeRows, t0.w - step * kMergeRows);
     if (rows <= 0) continue;
-    // warps per row: the least power of two that leaves a warp four partials, as far as rows are few
-    const int most = pl.shared ? ps.n2 + static_cast<int>(div_fast(pl.nbp, pl.chunk)) + 2 : ps.n1 + ps.n2;
+    const bool shared = h.y != 0;
+    // warps per row: the least power of two that leaves a warp four partials
+    const int most = t1.z + (shared ? div_down(h.z, h.w) + 2 : 1);
     int W = 1;
     while (W < kWarps && W * 4 < most) W *= 2;
-    const int sub = warp % W;
+    const int sub = warp & (W - 1);
     for (int r0 = 0; r0 < rows; r0 += kWarps / W) {
       const int rl = r0 + warp / W;
       const bool mine = rl < rows;
       float acc[kCols] = {};
-      float M = -INFINITY, Lsum = 0.f;
-      const int tl = step * kMergeRows + min(rl, rows - 1);  // row of the tile
-      if (pl.shared) {
-        const int64_t gp = o.before + o.it.row0 + tl;
-        const int64_t pt = static_cast<int64_t>(o.it.kvh) * (pl.ptiles / s.Hkv) + (gp >> 7);
-        const int64_t pu = pt * pl.nbp, pc0 = div_fast(pu, pl.chunk);
-        ps.a1 = pt + pc0;
-        ps.n1 = static_cast<int>(div_fast(pu + pl.nbp - 1, pl.chunk) - pc0) + 1;
-        ps.lane1 = static_cast<int>(gp & 127);
-        ps.lane2 = tl;
-      } else {
-        ps.lane1 = ps.lane2 = tl;
+      float Lsum = 0.f;
+      const int row = step * kMergeRows + min(rl, rows - 1);  // row of the tile
+      int a1 = t1.x, n1 = 1, lane1 = row;
+      if (shared) {  // the row's prefix tile, and the CTAs that its blocks fell to
+        const int gp = t1.w + t0.z + row;
+        const int pt = t0.y * ptiles_head + (gp >> 7), pu = pt * h.z;
+        const int c0 = div_down(pu, h.w);
+        a1 = pt + c0;
+        n1 = div_down(pu + h.z - 1, h.w) - c0 + 1;
+        lane1 = gp & 127;
       }
-      const int n = ps.n1 + ps.n2;
+      const int n = n1 + t1.z, step2 = shared ? 1 : 2;
+      auto at = [&](int i) { return i < n1 ? (a1 + i) * kBlockM + lane1 : (t1.y + (i - n1) * step2) * kBlockM + row; };
       if (mine) {
-        for (int i = lane; i < n; i += 32) {
-          const float2 st = __ldcg(a.part_stat + ps.row(i));
-          if (st.y != 0.f) M = fmaxf(M, st.x);
+        // the largest maximum, 32 partials at a time; the first 32 stay in registers
+        float2 st = lane < n ? __ldcg(a.part_stat + at(lane)) : make_float2(-INFINITY, 0.f);
+        float M = st.y != 0.f ? st.x : -INFINITY;
+#pragma unroll 1
+        for (int i = lane + 32; i < n; i += 32) {
+          const float2 v = __ldcg(a.part_stat + at(i));
+          if (v.y != 0.f) M = fmaxf(M, v.x);
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += 32) {
-          float w = 0.f, wl = 0.f;
-          if (i0 + lane < n) {
-            const float2 st = __ldcg(a.part_stat + ps.row(i0 + lane));
-            if (st.y != 0.f) {
-              w = ex2_approx(st.x - M);
-              wl = w * st.y;
-            }
-          }
+          if (i0 > 0) st = i0 + lane < n ? __ldcg(a.part_stat + at(i0 + lane)) : make_float2(-INFINITY, 0.f);
+          const float w = st.y != 0.f ? ex2_approx(st.x - M) : 0.f;
+          float wl = st.y != 0.f ? w * st.y : 0.f;
 #pragma unroll
           for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
           Lsum += wl;
@@ -739,7 +741,7 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
 #pragma unroll 4
           for (int i = sub; i < hi; i += W) {
             const float wi = __shfl_sync(0xffffffffu, w, i);
-            const float* src = a.part_o + ps.row(i0 + i) * D + lane * kCols;
+            const float* src = a.part_o + static_cast<int64_t>(at(i0 + i)) * D + lane * kCols;
             float x[kCols];
             if constexpr (kCols == 4) {
               const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
@@ -765,8 +767,8 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
       }
       if (mine && sub == 0) {
         const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-        const int64_t x = o.it.row0 + tl, r = div_fast(x, s.g);
-        uint16_t* dst = a.out + ((static_cast<int64_t>(o.it.b) * s.L + r) * a.Hq + o.it.kvh * s.g + (x - r * s.g)) * D + lane * kCols;
+        const int x = t0.z + row, r = div_down(x, s.g);
+        uint16_t* dst = a.out + static_cast<int64_t>((t0.x * s.L + r) * a.Hq + t0.y * s.g + (x - r * s.g)) * D + lane * kCols;
         if constexpr (kCols == 4)
           *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
         else
@@ -828,14 +830,16 @@ cudaError_t launch_impl(const ec_params& p, Args& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(cached_attention_kernel<D, Q8>, dim3(a.s.ctas), dim3(LY::kThreads), LY::kBytes, s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(cached_merge_kernel<D>, dim3(8 * a.s.ctas), dim3(kMergeThreads), 0, s, a);
+  return launch_pdl(cached_merge_kernel<D>, dim3(2 * a.s.ctas), dim3(kMergeThreads), 0, s, a);
 }
 
 }  // namespace
 }  // namespace cached
 
 size_t cached_attention_workspace_bytes(const ec_params& p, bool prefix) {
-  return static_cast<size_t>(cached::part_slots(p, prefix)) * cached::kBlockM * (static_cast<size_t>(p.D) * 4 + sizeof(float2));
+  return static_cast<size_t>(cached::part_slots(p, prefix)) *
+             (cached::kBlockM * (static_cast<size_t>(p.D) * 4 + sizeof(float2)) + sizeof(cached::Record)) +
+         sizeof(cached::Header);
 }
 
 cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_kv* prefix, const ec_kv& cache,
@@ -886,6 +890,8 @@ cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_
   a.out = static_cast<uint16_t*>(out);
   a.part_o = static_cast<float*>(ws);
   a.part_stat = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.s.slots) * kBlockM * p.D);
+  a.records = reinterpret_cast<Record*>(a.part_stat + static_cast<int64_t>(a.s.slots) * kBlockM);
+  a.header = reinterpret_cast<Header*>(a.records + a.s.slots);  // slots >= ctas
   a.dev_err = dev_err;
   if (p.D == 128)
     e = q8 ? launch_impl<128, true>(p, a, s) : launch_impl<128, false>(p, a, s);

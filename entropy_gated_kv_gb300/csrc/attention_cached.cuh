@@ -1,5 +1,9 @@
 // attention_cached.cuh — work plan of the cached attentions (attention_cached.cu), made on the
-// device from the recompute-set sizes and key lengths, by the attention kernel and by its merge.
+// device from the recompute-set sizes and key lengths by one warp of every CTA of the attention
+// kernel. It hands the CTA's items to the other warps through shared memory, and leaves what the
+// merge kernel needs in the workspace. (Straight-line code that a CTA runs once costs about ten
+// cycles an instruction, its fetch from the cold instruction cache: with the plan made by every
+// warp, and again by the merge, a one-block call took 24.6 us, 12 of them before the first score.)
 //
 // A tile is 128 packed query rows (a row of a sequence and one of the g query heads of a KV head)
 // of one KV head; a unit is a tile times one block of 128 keys. All units stand in one line, tile
@@ -30,47 +34,59 @@ struct Shape {
   int32_t ctas, slots;           // CTAs of the attention grid, partial tiles that the workspace holds
 };
 
+// Units, packed rows of a KV head and rows of q are counted in 32 bits: the host checks that q has
+// fewer than 2^31 rows, and a call of 2^31 units or more (seconds of work on every SM) is not run.
 struct Plan {
-  int64_t units;    // all units
-  int64_t own0;     // shared: units of the prefix tiles, which come first
-  int64_t rows;     // packed rows of one KV head over all sequences
-  int64_t chunk;    // units per CTA
-  int32_t nbp;      // key blocks of the prefix
-  int32_t ptiles;   // shared: prefix tiles (KV head major), 0 otherwise
-  int32_t otiles;   // tiles of single sequences
+  int32_t units;   // all units
+  int32_t own0;    // shared: units of the prefix tiles, which come first
+  int32_t rows;    // packed rows of one KV head over all sequences
+  int32_t chunk;   // units per CTA
+  int32_t nbp;     // key blocks of the prefix
+  int32_t ptiles;  // shared: prefix tiles (KV head major), 0 otherwise
+  int32_t otiles;  // tiles of single sequences
   bool shared;
   int32_t rows_l, len_l;  // B <= 32: rows and keys of sequence `lane`
 };
 
 struct Item {
   int32_t b, kvh;    // b = -1: rows of several sequences (a shared prefix tile)
-  int64_t row0;      // first packed row: within the sequence, or over all of them (b = -1)
+  int32_t row0;      // first packed row: within the sequence, or over all of them (b = -1)
   int32_t nrows;     // valid rows, 1 .. 128
   int32_t np;        // the tile's blocks [0, np) are the prefix's, the rest the sequence's own
-  int32_t units;     // blocks of the whole tile
-  int32_t j0, nblk;  // this item's blocks [j0, j0 + nblk)
-  int32_t tile;      // index over all tiles
+  int32_t j0, nblk;  // this item's blocks [j0, j0 + nblk); nblk = 0 ends the CTA's work
   int32_t len;       // own keys of the sequence
+  int32_t slot;      // where its partial rows go, -1: the tile is complete
+  int32_t units;     // blocks of the whole tile
+  int32_t tile;      // index over all tiles
+  int32_t before;    // packed rows of the sequences before b
+};
+static_assert(sizeof(Item) == 48, "three 16-byte words");
+
+// What the merge reads: one record per tile of a single sequence (shared), or per CTA, for the tile
+// that begins in it and does not end there (separate; nrows = 0 where there is none). A row's
+// partials lie in n1 slots from a1 on and n2 slots from a2 on; shared, the first ones are those of
+// the row's prefix tile, which the merge works out from the header.
+struct Record {
+  int32_t b, kvh, row0, nrows;
+  int32_t a1, a2, n2, before;
+};
+struct Header {
+  int32_t records, shared, nbp, chunk;
+  int32_t ptiles_head, pad[3];
 };
 
-EC_DEV int64_t div_fast(int64_t a, int64_t b) {  // a >= 0, b > 0; the 32-bit form when both fit
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
+// Quotients of numbers below 2^31; the divisor's bits are few enough here that the hardware's own
+// 32-bit division is used.
+EC_DEV int div_up(int a, int b) { return static_cast<int>((static_cast<uint32_t>(a) + b - 1) / static_cast<uint32_t>(b)); }
+EC_DEV int div_down(int a, int b) { return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)); }
 
-template <typename T>
-EC_DEV T warp_total(T v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
+EC_DEV int warp_total(int v) { return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v))); }
 
-template <typename T>
-EC_DEV T warp_inclusive(T v) {
+EC_DEV int warp_inclusive(int v) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
+#pragma unroll 1
   for (int off = 1; off < 32; off <<= 1) {
-    const T u = __shfl_up_sync(0xffffffffu, v, off);
+    const int u = __shfl_up_sync(0xffffffffu, v, off);
     if (lane >= off) v += u;
   }
   return v;
@@ -100,25 +116,22 @@ EC_DEV void seq_of(const Shape& s, const Plan& pl, int b, int32_t& rows, int32_t
   }
 }
 
-EC_DEV int tiles_of(const Shape& s, int32_t rows) {
-  return static_cast<int>((static_cast<int64_t>(rows) * s.g + kBlockM - 1) / kBlockM);
-}
+EC_DEV int tiles_of(const Shape& s, int32_t rows) { return (rows * s.g + kBlockM - 1) / kBlockM; }
 EC_DEV int blocks_of(int32_t len) { return (len + kBlockN - 1) / kBlockN; }
 
-// Blocks of one tile of a sequence. A sequence without any key still has one, all of it masked,
-// so that its rows are written (as zeros).
-EC_DEV int tile_units(const Plan& pl, int32_t len) {
-  return pl.shared ? blocks_of(len) : max(1, pl.nbp + blocks_of(len));
-}
+// Blocks of one tile of a sequence. A tile without any key still has one block, all of it masked, so
+// that its rows are written (as zeros) or, shared, so that a CTA leaves its record.
+EC_DEV int tile_units(const Plan& pl, int32_t len) { return max(1, (pl.shared ? 0 : pl.nbp) + blocks_of(len)); }
 
-// Whole warp; every warp of both kernels computes the same plan.
+// Whole warp.
 EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
   const int lane = threadIdx.x & 31;
   Plan pl;
   pl.nbp = blocks_of(s.Lp);
   pl.rows_l = pl.len_l = 0;
-  int64_t rows = 0, apart = 0, own = 0;
-  int32_t tiles = 0;
+  int rows = 0, apart = 0, own = 0, tiles = 0;
+  float most = 0.f;  // units as a float: 2^31 and more are seen there
+#pragma unroll 1
   for (int b = lane; b < s.B; b += 32) {
     int32_t r, n;
     load_seq(s, b, r, n, dev_err, report);
@@ -126,93 +139,96 @@ EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
       pl.rows_l = r;
       pl.len_l = n;
     }
-    const int t = s.Hkv * tiles_of(s, r);
-    rows += static_cast<int64_t>(r) * s.g;
+    const int t = s.Hkv * tiles_of(s, r), nb = blocks_of(n);
+    rows += r * s.g;
     tiles += t;
-    apart += static_cast<int64_t>(t) * max(1, pl.nbp + blocks_of(n));
-    own += static_cast<int64_t>(t) * blocks_of(n);
+    apart += t * max(1, pl.nbp + nb);
+    own += t * max(1, nb);
+    most += static_cast<float>(t) * static_cast<float>(pl.nbp + nb + 1);
   }
   pl.rows = warp_total(rows);
   pl.otiles = warp_total(tiles);
   apart = warp_total(apart);
-  own = warp_total(own);
-  const int64_t ptiles = static_cast<int64_t>(s.Hkv) * ((pl.rows + kBlockM - 1) / kBlockM);
-  const int64_t together = ptiles * pl.nbp + own;
-  pl.shared = pl.nbp > 0 && ptiles + pl.otiles + s.ctas <= s.slots && 8 * together <= 7 * apart;
-  pl.ptiles = pl.shared ? static_cast<int32_t>(ptiles) : 0;
-  pl.own0 = pl.shared ? ptiles * pl.nbp : 0;
-  pl.units = pl.shared ? together : apart;
-  pl.chunk = max(int64_t(1), div_fast(pl.units + s.ctas - 1, s.ctas));
+#pragma unroll 1
+  for (int off = 16; off > 0; off >>= 1) most += __shfl_xor_sync(0xffffffffu, most, off);
+  if (most > 2.1e9f) {
+    if (report && lane == 0) report_error(dev_err, EC_DEVERR_BAD_R);
+    apart = 0;
+  }
+  pl.shared = false;
+  pl.ptiles = pl.own0 = 0;
+  pl.units = apart;
+  if (pl.nbp > 0 && s.B > 1) {
+    const int ptiles = s.Hkv * ((pl.rows + kBlockM - 1) / kBlockM);
+    const int together = ptiles * pl.nbp + warp_total(own);
+    pl.shared = apart > 0 && ptiles + pl.otiles + s.ctas <= s.slots && together <= apart - apart / 8;
+    if (pl.shared) {
+      pl.ptiles = ptiles;
+      pl.own0 = ptiles * pl.nbp;
+      pl.units = together;
+    }
+  }
+  pl.chunk = max(1, div_up(pl.units, s.ctas));
   return pl;
 }
 
-// Whole warp: the tile that holds unit u, from its block u on.
-EC_DEV Item item_at(const Shape& s, const Plan& pl, int64_t u) {
+// Whole warp: the item of CTA c that starts at unit u (u below `end`, its last one's successor).
+EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c) {
   const int lane = threadIdx.x & 31;
   Item it;
+  it.before = 0;
   if (u < pl.own0) {
-    const int t = static_cast<int>(div_fast(u, pl.nbp)), per_head = pl.ptiles / s.Hkv;
+    const int t = div_down(u, pl.nbp), per_head = div_down(pl.ptiles, s.Hkv);
     it.b = -1;
-    it.kvh = t / per_head;
-    it.row0 = static_cast<int64_t>(t - it.kvh * per_head) * kBlockM;
-    it.nrows = static_cast<int32_t>(min(static_cast<int64_t>(kBlockM), pl.rows - it.row0));
+    it.kvh = div_down(t, per_head);
+    it.row0 = (t - it.kvh * per_head) * kBlockM;
+    it.nrows = min(kBlockM, pl.rows - it.row0);
     it.np = it.units = pl.nbp;
-    it.j0 = static_cast<int32_t>(u - static_cast<int64_t>(t) * pl.nbp);
+    it.j0 = u - t * pl.nbp;
     it.tile = t;
     it.len = 0;
-    return it;
-  }
-  int64_t base = pl.own0;
-  int32_t tbase = pl.ptiles;
-  for (int b0 = 0; b0 < s.B; b0 += 32) {
-    int32_t r, n;
-    seq_of(s, pl, b0 + lane, r, n);
-    const int32_t t = s.Hkv * tiles_of(s, r), tu = tile_units(pl, n);
-    const int64_t incl = warp_inclusive(static_cast<int64_t>(t) * tu);
-    const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
-    if (u < base + total) {
-      const int src = __ffs(__ballot_sync(0xffffffffu, base + incl > u)) - 1;
-      const int64_t before = __shfl_sync(0xffffffffu, incl - static_cast<int64_t>(t) * tu, src);
-      const int32_t tincl = warp_inclusive(t);
-      const int32_t tbefore = __shfl_sync(0xffffffffu, tincl - t, src);
-      const int32_t rsel = __shfl_sync(0xffffffffu, r, src);
+  } else {
+    int base = pl.own0, tbase = pl.ptiles, rsel = 0;
+#pragma unroll 1
+    for (int b0 = 0;; b0 += 32) {
+      int32_t r, n;
+      seq_of(s, pl, b0 + lane, r, n);
+      const int t = s.Hkv * tiles_of(s, r), tu = tile_units(pl, n);
+      int incl = t * tu, src = 0;
+      if (s.B > 1) {
+        incl = warp_inclusive(incl);
+        const int total = __shfl_sync(0xffffffffu, incl, 31);
+        const int nt = warp_total(t), nr = warp_total(r * s.g);
+        if (u >= base + total && b0 + 32 < s.B) {
+          base += total;
+          tbase += nt;
+          it.before += nr;
+          continue;
+        }
+        src = __ffs(__ballot_sync(0xffffffffu, base + incl > u)) - 1;
+        base += __shfl_sync(0xffffffffu, incl - t * tu, src);
+        tbase += warp_total(lane < src ? t : 0);
+        it.before += warp_total(lane < src ? r * s.g : 0);
+      }
+      rsel = __shfl_sync(0xffffffffu, r, src);
       it.len = __shfl_sync(0xffffffffu, n, src);
-      it.units = __shfl_sync(0xffffffffu, tu, src);
       it.b = b0 + src;
-      const int64_t w = u - base - before;
-      const int32_t tl = static_cast<int32_t>(div_fast(w, it.units));
-      const int32_t per_head = tiles_of(s, rsel);
-      it.kvh = tl / per_head;
-      it.row0 = static_cast<int64_t>(tl - it.kvh * per_head) * kBlockM;
-      it.nrows = static_cast<int32_t>(min(static_cast<int64_t>(kBlockM), static_cast<int64_t>(rsel) * s.g - it.row0));
-      it.np = pl.shared ? 0 : pl.nbp;
-      it.j0 = static_cast<int32_t>(w - static_cast<int64_t>(tl) * it.units);
-      it.tile = tbase + tbefore + tl;
-      return it;
+      break;
     }
-    base += total;
-    tbase += warp_total(t);
+    it.units = tile_units(pl, it.len);
+    const int w = u - base, tl = div_down(w, it.units), per_head = tiles_of(s, rsel);
+    it.kvh = div_down(tl, per_head);
+    it.row0 = (tl - it.kvh * per_head) * kBlockM;
+    it.nrows = min(kBlockM, rsel * s.g - it.row0);
+    it.np = pl.shared ? 0 : pl.nbp;
+    it.j0 = w - tl * it.units;
+    it.tile = tbase + tl;
   }
-  it.nrows = it.units = it.nblk = 0;  // not reached: u is below pl.units
-  it.b = it.kvh = it.j0 = it.np = it.len = it.tile = 0;
-  it.row0 = 0;
+  it.nblk = min(it.units - it.j0, end - u);
+  // Partial rows. Shared: tile + c grows from item to item, so no two share a slot. Separate: a CTA
+  // has at most two incomplete items, one that began before it and one that ends after it.
+  it.slot = pl.shared ? it.tile + c : it.nblk == it.units ? -1 : 2 * c + (it.j0 == 0 ? 1 : 0);
   return it;
-}
-
-// The item of CTA c that starts at unit u (u below its end).
-EC_DEV Item cta_item(const Shape& s, const Plan& pl, int64_t u, int64_t end) {
-  Item it = item_at(s, pl, u);
-  it.nblk = static_cast<int32_t>(min(static_cast<int64_t>(it.units - it.j0), end - u));
-  return it;
-}
-
-EC_DEV bool item_complete(const Plan& pl, const Item& it) { return !pl.shared && it.nblk == it.units; }
-
-// Where an incomplete item of CTA c leaves its partial rows. Shared: tile + c grows from item to
-// item, so no two share a slot. Separate: a CTA has at most two incomplete items, one that began
-// before it and one that ends after it.
-EC_DEV int64_t item_slot(const Plan& pl, const Item& it, int c) {
-  return pl.shared ? static_cast<int64_t>(it.tile) + c : 2 * static_cast<int64_t>(c) + (it.j0 == 0 ? 1 : 0);
 }
 
 }  // namespace cached

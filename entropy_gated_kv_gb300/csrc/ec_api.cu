@@ -378,6 +378,8 @@ ec_status cached_attention(const ec_params* p, const void* q, const ec_kv* prefi
                            size_t ws_bytes, size_t ws_need, int32_t* dev_err, ec_stream_t stream) {
   ec_status r = check_kv(cache, p->L);
   if (r != EC_OK) return r;
+  // rows of q are counted in 32 bits (more would not fit the device beside their output)
+  if (static_cast<int64_t>(p->B) * p->L * p->Hq > INT32_MAX) return EC_ERR_UNSUPPORTED;
   if (!q || !R || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws)) return EC_ERR_INVALID_ARG;
   if (!(scale > 0.f) || scale > 3e38f || ws_bytes < ws_need) return EC_ERR_INVALID_ARG;
   static const ec_kv none{};

@@ -399,7 +399,9 @@ ec_status ec_kv_gather_quant(const ec_params* p, const ec_kv* cache, const int32
  * lies in the cache past n is not used, NaN included. n = 0: the row is zeros, as it is when
  * every score is -infinity. R[b] = 1 is the single-token form.
  * kv_len int32 [B] on the device, or NULL. A length outside [0, L] sets EC_DEVERR_BAD_LEN, an R
- * outside [0, L] EC_DEVERR_BAD_R; the sequence is skipped.
+ * outside [0, L] EC_DEVERR_BAD_R; the sequence is skipped. EC_ERR_UNSUPPORTED for B * L * Hq of
+ * 2^31 or more. A call of 2.1e9 or more steps of 128 rows by 128 keys is not run either: it sets
+ * EC_DEVERR_BAD_R.
  * scale must be above 0 and finite. ws: ec_partial_attention_quant_workspace_size(p) bytes,
  * 16-byte aligned, no initial contents needed; calls that share it must not overlap in time. It
  * must not overlap the other buffers, nor out the inputs (EC_ERR_INVALID_ARG).

@@ -120,7 +120,7 @@ def test_workspace_sizes(capi):
         assert f(ctypes.byref(params(C, D=96))) == 0 and f(None) == 0
         assert f(ctypes.byref(params(C))) > f(ctypes.byref(params(C, D=64))) > 0
         # bounded by the SM count, whatever the batch and the length
-        assert f(ctypes.byref(params(C, B=64, L=1 << 17, Hq=4, Hkv=4))) <= 8 * 160 * 128 * (128 * 4 + 8)
+        assert f(ctypes.byref(params(C, B=64, L=1 << 17, Hq=4, Hkv=4))) <= 8 * 160 * (128 * (128 * 4 + 8) + 32) + 32
 
 
 def test_binding_refuses_cpu_tensors_types_and_shapes(capi):
