@@ -13,8 +13,8 @@
 //   warp 0       makes the work plan, hands out the CTA's items, and is the TMA producer: K and V
 //                blocks of 128 keys.
 //   warp 1       allocates 512 TMEM columns and issues tcgen05.mma.
-//   warps 2, 3   the query tile, row by row with cp.async (a tile packs rows of any sequences, which
-//                no one tensor box covers), swizzled by hand.
+//   warp 2       the query tile, four rows a TMA gather (a tile packs rows of any sequences, which no
+//                one tensor box covers). Warp 3 has no work: registers are granted by four warps.
 //   warps 4..7   softmax of the CTA's even key blocks, warps 8..11 of the odd ones: two independent
 //                streams with their own S buffer, running maximum and sum, and O accumulator, joined
 //                once per item. One stream's softmax runs while the tensor cores work on the
@@ -23,7 +23,7 @@
 //                One TMEM lane (= one packed query row) per thread; online softmax in base 2 with a
 //                lazy rescale of O (only when the running maximum grows by more than 2^8); P in
 //                bf16 written back over the first half of the S buffer.
-//   warps 12..15 (8-bit cache) dequantise: the producer's TMA brings codes and exponent bytes into a
+//   warps 12..19 (8-bit cache) dequantise, four the K tiles and four the V tiles: the producer's TMA brings codes and exponent bytes into a
 //                raw ring, and these warps write the bf16 tiles that the products read. The
 //                dequantised values are exact in bf16, so the products are those of a bf16 cache
 //                with the same values.
@@ -53,9 +53,10 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per pipeline wait
 constexpr int kMaxCtas = 160;                     // bound of the attention grid, for the workspace
 constexpr int kMaxUnits = 6;                      // K or V tiles in shared memory
 constexpr int kMaxRaw = 3;
-constexpr int kDequantWarps = 4;
+constexpr int kDequantWarps = 4;                  // per tile: four warps take the K tiles, four the V tiles
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = 16;  // rows of a tile per merge CTA step
+constexpr int kMergeRows = 32;  // rows of a tile per merge CTA
+constexpr int kMergeSteps = kBlockM / kMergeRows;
 constexpr int kItems = 8;       // items handed out and not yet finished, see the producer
 constexpr int kCum = 32;        // sequences whose row ends are kept in shared memory
 constexpr uint32_t kDescHi = sdesc_hi(1024);
@@ -91,11 +92,12 @@ struct Layout {
   static constexpr int kCumOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
   static constexpr int kBarOff = kCumOff + kCum * 4;
   static constexpr int kBytes = kBarOff + static_cast<int>(sizeof(Bars));
-  static constexpr int kThreads = Q8 ? 512 : 384;
+  static constexpr int kThreads = Q8 ? 640 : 384;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 struct Args {
+  CUtensorMap tq;                // rows of q
   CUtensorMap tk, tv, tpk, tpv;  // own and prefix caches
   const uint8_t *ke, *ve, *pke, *pve;
   Shape s;
@@ -117,10 +119,14 @@ EC_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
                : "memory");
 }
 
-EC_DEV void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Four rows of a matrix, 64 elements from column x on, below one another.
+EC_DEV void tma_gather4(void* dst, const void* tmap, uint64_t* bar, int x, int r0, int r1, int r2, int r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+      : "memory");
 }
-EC_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 EC_DEV void st_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -146,12 +152,46 @@ EC_DEV uint32_t ld_shared8(uint32_t src) {
                  "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),  \
                  "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory")
 
-#define EC_TMEM_ST16(taddr, r)                                                                              \
-  asm volatile(                                                                                             \
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" \
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), \
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])          \
-      : "memory")
+#define EC_TMEM_LD16(taddr, r)                                                                             \
+  asm volatile(                                                                                            \
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];" \
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),    \
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) \
+      : "r"(taddr))
+
+#define EC_TMEM_WAIT16(r)                                                                                  \
+  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                            \
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),       \
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),   \
+                 "+r"(r[14]), "+r"(r[15])::"memory")
+
+#define EC_TMEM_ST8(taddr, r)                                                                              \
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),      \
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])      \
+               : "memory")
+
+// Two fp32 lanes in one instruction.
+EC_DEV uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+EC_DEV void unpack_f32x2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+EC_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+EC_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+EC_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // Whole warp: where packed row x of the item's KV head lies in q, as (b L + r) Hq + h.
 EC_DEV int query_row(const Args& a, const int32_t* cum, const Item& it, int x) {
@@ -190,7 +230,7 @@ EC_DEV int query_row(const Args& a, const int32_t* cum, const Item& it, int x) {
     }
     x -= before;
   }
-  const int r = div_down(x, s.g);
+  const int r = s.div_g(x);
   return (b * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g);
 }
 
@@ -210,7 +250,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 64);
+    mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&bars->unit_full[i], Q8 ? kDequantWarps : 1);
@@ -345,7 +385,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         h.shared = pl.shared;
         h.nbp = pl.nbp;
         h.chunk = pl.chunk;
-        h.ptiles_head = div_down(pl.ptiles, s.Hkv);
+        h.ptiles_head = s.div_h(pl.ptiles);
         *a.header = h;
       }
     }
@@ -423,33 +463,26 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------------ query loader
-    constexpr int kChunks = D / 8;  // 16-byte pieces of a row
-    constexpr int kRowsStep = 32 / kChunks;
-    const int chunk = lane % kChunks;
+    // Each lane fetches four rows, wherever they lie; padding repeats the item's last row.
     const int32_t* cum = reinterpret_cast<const int32_t*>(smem + LY::kCumOff);
-    for (int items = 0;; ++items) {
+    for (int items = 0; warp == 2; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
-      if (items > 0 && !__all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1))) break;
+      int at[4];
 #pragma unroll 1
-      for (int h = 0; h < 64; h += 32) {  // 32 rows at a time; each lane finds one of them
-        const int row0 = 64 * (warp - 2) + h;
-        // rows past the last are zeros
-        const int at = query_row(a, cum, it, it.row0 + min(row0 + lane, it.nrows - 1));
-#pragma unroll 4
-        for (int i = lane / kChunks; i < 32; i += kRowsStep) {
-          const int64_t src = __shfl_sync(0xffffffffu, at, i);
-          const int row = row0 + i;
-          const uint32_t dst = smem_u32(smem) + (chunk >> 3) * kAtomBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-          if (row < it.nrows)
-            cp_async16(dst, a.q + src * D + chunk * 8);
-          else
-            st_shared16(dst, make_uint4(0, 0, 0, 0));
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int x = query_row(a, cum, it, it.row0 + min(4 * lane + i, it.nrows - 1));
+        at[0] = i == 0 ? x : at[0];
+        at[1] = i == 1 ? x : at[1];
+        at[2] = i == 2 ? x : at[2];
+        at[3] = x;
       }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      mbar_arrive(&bars->q_full);
+      if (items > 0 && !__all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1))) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars->q_full, LY::kTileBytes);
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < LY::kAtoms; ++c)
+        tma_gather4(smem + c * kAtomBytes + lane * 512, &a.tq, &bars->q_full, c * 64, at[0], at[1], at[2], at[3]);
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ softmax + epilogue
@@ -471,9 +504,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         if (live) {
           tc_fence_after();
           const int nv = valid_keys(s, it, it.j0 + i);
-          uint32_t buf[2][32];
           // row maximum (scale > 0 commutes with it), a chunk's load behind the next one's
-          float mx = -INFINITY;
+          uint32_t buf[2][32];
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           EC_TMEM_LD32(s_addr, buf[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -485,15 +518,13 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
               for (int e = 0; e < 32; ++e)
                 if (c * 32 + e >= nv) x[e] = __float_as_uint(-INFINITY);
             }
-            float m4[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(x[e]);
-#pragma unroll
-            for (int e = 4; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(x[e]));
-            mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+            for (int e = 0; e < 32; e += 2)
+              m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
           }
-          EC_TMEM_LD32(s_addr, buf[0]);
-          mx *= a.scale_log2;
+          uint32_t s16[2][16];
+          EC_TMEM_LD16(s_addr, s16[0]);
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
           bool rescale = false;
           float alpha = 1.f;
           if (i == st) {
@@ -506,32 +537,37 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           }
           // p = 2^(s scale log2(e) - m); without a finite score so far, nothing is subtracted and p = 0
           const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-          float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
+          uint64_t sum2[2] = {0, 0};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            EC_TMEM_WAIT32(buf[c & 1]);
-            if (c < 3) EC_TMEM_LD32(s_addr + (c + 1) * 32, buf[(c + 1) & 1]);
-            uint32_t* x = buf[c & 1];
+          for (int c = 0; c < 8; ++c) {
+            EC_TMEM_WAIT16(s16[c & 1]);
+            if (c < 7) EC_TMEM_LD16(s_addr + (c + 1) * 16, s16[(c + 1) & 1]);
+            uint32_t* x = s16[c & 1];
             if (nv < kBlockN) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c * 32 + e >= nv) x[e] = __float_as_uint(-INFINITY);
+              for (int e = 0; e < 16; ++e)
+                if (c * 16 + e >= nv) x[e] = __float_as_uint(-INFINITY);
             }
-            uint32_t pk[16];
+            uint32_t pk[8];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float p0 = ex2_approx(fmaf(__uint_as_float(x[e]), a.scale_log2, neg_m));
-              const float p1 = ex2_approx(fmaf(__uint_as_float(x[e + 1]), a.scale_log2, neg_m));
-              sum4[(e >> 1) & 3] += p0 + p1;
+            for (int e = 0; e < 16; e += 2) {
+              float p0, p1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
               pk[e >> 1] = pack_bf16x2(p0, p1);
             }
-            // P over columns of S that this loop has read: [16 c, 16 c + 16) lies below 32 (c + 1)
-            EC_TMEM_ST16(s_addr + c * 16, pk);
+            // P over columns of S that this loop has read: [8 c, 8 c + 8) lies below 16 (c + 1)
+            EC_TMEM_ST8(s_addr + c * 8, pk);
           }
-          l_sum += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+          float sum_lo, sum_hi;
+          unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
+          l_sum += sum_lo + sum_hi;
           // the stream's earlier products are done (they were waited for before this S was made)
           if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t* o = buf[0];
               EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
@@ -575,7 +611,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         uint16_t* orow = nullptr;
         float* prow = nullptr;
         if (complete) {
-          const int x = it.row0 + row, r = div_down(x, s.g);
+          const int x = it.row0 + row, r = s.div_g(x);
           orow = a.out + static_cast<int64_t>((it.b * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g)) * D + st * (D / 2);
         } else {
           const int at = it.slot * kBlockM + row;
@@ -617,47 +653,57 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     // Eight lanes read 128 neighbouring bytes of codes; the 16-byte pieces of bf16 that they
     // store fall into eight different bank groups: for D = 128 lanes 0..3 take the first half of
     // row r and lanes 4..7 the second half of row r ^ 1, whose swizzle differs in the lowest bit.
-    const int t = threadIdx.x - 384;
-    uint32_t n = 0;
+    // A thread's rows differ by multiples of 8, so its places in the swizzle are the same in all.
+    constexpr int kPieces = D / 16;  // 16-code pieces of a row
+    constexpr int kRowsStep = 128 / kPieces;
+    const int kv = warp >= 16;
+    const int t = threadIdx.x & 127, piece = t % kPieces;
+    const int row0 = D == 128 ? (t / kPieces) ^ (piece >> 2) : t / kPieces;
+    const uint32_t src_off = row0 * D + piece * 16, exp_off = 128 * D + row0;
+    const uint32_t dst_off = (piece >> 2) * kAtomBytes + row0 * 128 + ((((piece & 3) * 2) ^ (row0 & 7)) << 4);
+    uint32_t n = kv;
     bool ok = true;
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
-      for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j) {
-        const int nv = valid_keys(s, it, j);
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const uint32_t rs = n % LY::kRaw, slot = n % kUnits;
-          ok = __all_sync(0xffffffffu, wait(&bars->raw_full[rs], (n / LY::kRaw) & 1u) &&
-                                           wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u));
-          if (!ok) break;
-          const uint32_t raw = smem_u32(smem + LY::kRawOff + rs * LY::kRawBytes);
-          const uint32_t tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes);
-          constexpr int kPieces = D / 16;  // 16-code pieces of a row
-          constexpr int kRowsStep = 128 / kPieces;
+      for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j, n += 2) {
+        const int nv = kv ? valid_keys(s, it, j) : kBlockN;
+        const uint32_t rs = n % LY::kRaw, slot = n % kUnits;
+        ok = __all_sync(0xffffffffu, wait(&bars->raw_full[rs], (n / LY::kRaw) & 1u) &&
+                                         wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u));
+        if (!ok) break;
+        const uint32_t raw = smem_u32(smem + LY::kRawOff + rs * LY::kRawBytes);
+        const uint32_t tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes) + dst_off;
 #pragma unroll 4
-          for (int i = 0; i < kPieces; ++i) {
-            const int piece = t % kPieces;
-            int row = i * kRowsStep + t / kPieces;
-            if (D == 128) row ^= piece >> 2;
-            const uint4 w = ld_shared16(raw + row * D + piece * 16);
-            const DequantScale sc = dequant_scale(static_cast<int>(ld_shared8(raw + 128 * D + row)));
-            uint4 lo, hi;
+        for (int i = 0; i < kPieces; ++i) {
+          uint4 w = ld_shared16(raw + src_off + i * kRowsStep * D);
+          int byte = static_cast<int>(ld_shared8(raw + exp_off + i * kRowsStep));
+          if (row0 + i * kRowsStep >= nv) {  // V rows past the length: zeros, whatever lies there
+            w = make_uint4(0, 0, 0, 0);
+            byte = kExpZeroByte;
+          }
+          uint4 lo, hi;
+          if (byte <= kExpOneFactor) {
+            const uint32_t f = dequant_factor(byte);
+            dequantise4(w.x, f, lo.x, lo.y);
+            dequantise4(w.y, f, lo.z, lo.w);
+            dequantise4(w.z, f, hi.x, hi.y);
+            dequantise4(w.w, f, hi.z, hi.w);
+          } else {
+            const DequantScale sc = dequant_scale(byte);
             dequantise4(w.x, sc, lo.x, lo.y);
             dequantise4(w.y, sc, lo.z, lo.w);
             dequantise4(w.z, sc, hi.x, hi.y);
             dequantise4(w.w, sc, hi.z, hi.w);
-            if (kv == 1 && row >= nv) lo = hi = make_uint4(0, 0, 0, 0);  // past the length: no NaN may stay
-            const uint32_t dst = tile + (piece >> 2) * kAtomBytes + row * 128;
-            const uint32_t c = (piece & 3) * 2;
-            st_shared16(dst + ((c ^ (row & 7)) << 4), lo);
-            st_shared16(dst + (((c + 1) ^ (row & 7)) << 4), hi);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars->raw_empty[rs]);
-            mbar_arrive(&bars->unit_full[slot]);
-          }
+          st_shared16(tile + i * kRowsStep * 128, lo);
+          st_shared16((tile + i * kRowsStep * 128) ^ 16u, hi);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->raw_empty[rs]);
+          mbar_arrive(&bars->unit_full[slot]);
         }
       }
     }
@@ -674,105 +720,147 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
 
 // ---------------------------------------------------------------------------------- merge
 
-// Joins the partial rows of split tiles by their log-sum-exp weights, in slot order. A step takes
-// 16 rows of one tile: one warp a row, or with many partials several warps a row, each every
-// W-th partial. Bound by the partials' bytes, which the attention kernel has just written (L2).
+// Adds up the weighted partial rows i0, i0 + step, ... of one row (whole warp, D / 32 columns a
+// lane), kBatch loads in flight, and the sum of the weights; `M`: the largest maximum.
+template <int D, typename At>
+EC_DEV void merge_rows(const Args& a, const At& at, int n, int i0, int step, float (&acc)[D / 32], float& Lsum) {
+  constexpr int kCols = D / 32, kBatch = 8;
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY;
+  float2 st = make_float2(-INFINITY, 0.f);
+  if (lane < n) st = __ldcg(a.part_stat + at(lane));
+  for (int k0 = 0; k0 < n; k0 += 32) {  // weights of 32 partials at a time
+    if (k0 > 0) {
+      st = make_float2(-INFINITY, 0.f);
+      if (k0 + lane < n) st = __ldcg(a.part_stat + at(k0 + lane));
+    }
+    // the first batch of rows is on its way while the weights are worked out
+    float x[kBatch][kCols];
+    auto load = [&](int i) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = i + u * step;
+        if (k < min(n, k0 + 32)) {
+          const float* src = a.part_o + static_cast<int64_t>(at(k)) * D + lane * kCols;
+          if constexpr (kCols == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            x[u][0] = v.x, x[u][1] = v.y;
+          }
+        }
+      }
+    };
+    int i = k0 + i0;
+    load(i);
+    float mx = st.y != 0.f ? st.x : -INFINITY;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    if (mx > M) {  // the whole warp
+      const float f = M == -INFINITY ? 0.f : ex2_approx(M - mx);
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) acc[e] *= f;
+      Lsum *= f;
+      M = mx;
+    }
+    // a partial without weight (no finite score) contributes nothing, whatever its row holds
+    const float w = st.y != 0.f ? ex2_approx(st.x - M) : 0.f;
+    float wl = st.y != 0.f ? w * st.y : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
+    Lsum += wl;
+    for (;;) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = i + u * step;
+        const float wk = __shfl_sync(0xffffffffu, w, (k - k0) & 31);
+        if (k < min(n, k0 + 32) && wk != 0.f) {
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) acc[e] = fmaf(wk, x[u][e], acc[e]);
+        }
+      }
+      i += kBatch * step;
+      if (i >= min(n, k0 + 32)) break;
+      load(i);
+    }
+  }
+}
+
+// Joins the partial rows of split tiles by their log-sum-exp weights, in a fixed order. A CTA takes
+// 32 rows of one tile: one warp a row, or with more than 16 partials all eight warps a row, each
+// every eighth partial. Two chains of loads (the record; the statistics and the rows together) and
+// the partials' bytes, which the attention kernel has just written (L2), are its whole cost.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __grid_constant__ Args a) {
-  constexpr int kWarps = kMergeThreads / 32, kCols = D / 32, kSteps = kBlockM / kMergeRows;
+  constexpr int kWarps = kMergeThreads / 32, kCols = D / 32;
   __shared__ float acc_s[kWarps][D];
   const Shape& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const int4* hp = reinterpret_cast<const int4*>(a.header);
-  const int4 h = __ldcg(hp);  // records, shared, nbp, chunk
-  const int ptiles_head = __ldcg(&a.header->ptiles_head);
-  for (int task = blockIdx.x; task < h.x * kSteps; task += gridDim.x) {
-    // the first steps of all records come first: few rows leave the later ones empty
-    const int step = div_down(task, h.x);
-    const int4* rp = reinterpret_cast<const int4*>(a.records + (task - step * h.x));
+  const int4 h = __ldcg(reinterpret_cast<const int4*>(a.header));            // records, shared, nbp, chunk
+  const int4 g = __ldcg(reinterpret_cast<const int4*>(a.header) + 1);        // ptiles_head
+  const int row_base = (blockIdx.x & (kMergeSteps - 1)) * kMergeRows;
+  for (int which = blockIdx.x / kMergeSteps; which < h.x; which += gridDim.x / kMergeSteps) {
+    const int4* rp = reinterpret_cast<const int4*>(a.records + which);
     const int4 t0 = __ldcg(rp), t1 = __ldcg(rp + 1);  // b, kvh, row0, nrows; a1, a2, n2, before
-    const int rows = min(kMergeRows, t0.w - step * kMergeRows);
-    if (rows <= 0) continue;
+    const int end = min(row_base + kMergeRows, t0.w);
     const bool shared = h.y != 0;
-    // warps per row: the least power of two that leaves a warp four partials
-    const int most = t1.z + (shared ? div_down(h.z, h.w) + 2 : 1);
-    int W = 1;
-    while (W < kWarps && W * 4 < most) W *= 2;
-    const int sub = warp & (W - 1);
-    for (int r0 = 0; r0 < rows; r0 += kWarps / W) {
-      const int rl = r0 + warp / W;
-      const bool mine = rl < rows;
-      float acc[kCols] = {};
-      float Lsum = 0.f;
-      const int row = step * kMergeRows + min(rl, rows - 1);  // row of the tile
-      int a1 = t1.x, n1 = 1, lane1 = row;
+    // the partials of a row: n1 slots from a1 on at `lane1`, then every `step2`-th from a2 on
+    auto row_parts = [&](int row, int& a1, int& n1, int& lane1) {
+      a1 = t1.x, n1 = 1, lane1 = row;
       if (shared) {  // the row's prefix tile, and the CTAs that its blocks fell to
-        const int gp = t1.w + t0.z + row;
-        const int pt = t0.y * ptiles_head + (gp >> 7), pu = pt * h.z;
-        const int c0 = div_down(pu, h.w);
+        const int gp = t1.w + t0.z + row, pt = t0.y * g.x + (gp >> 7), pu = pt * h.z;
+        const float inv = __fdividef(1.f, static_cast<float>(h.w));
+        const int c0 = div_near(pu, h.w, inv);
         a1 = pt + c0;
-        n1 = div_down(pu + h.z - 1, h.w) - c0 + 1;
+        n1 = div_near(pu + h.z - 1, h.w, inv) - c0 + 1;
         lane1 = gp & 127;
       }
-      const int n = n1 + t1.z, step2 = shared ? 1 : 2;
-      auto at = [&](int i) { return i < n1 ? (a1 + i) * kBlockM + lane1 : (t1.y + (i - n1) * step2) * kBlockM + row; };
-      if (mine) {
-        // the largest maximum, 32 partials at a time; the first 32 stay in registers
-        float2 st = lane < n ? __ldcg(a.part_stat + at(lane)) : make_float2(-INFINITY, 0.f);
-        float M = st.y != 0.f ? st.x : -INFINITY;
+    };
+    auto write = [&](int row, const float (&acc)[kCols], float Lsum) {
+      const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+      const int x = t0.z + row, r = s.div_g(x);
+      uint16_t* dst = a.out + static_cast<int64_t>((t0.x * s.L + r) * a.Hq + t0.y * s.g + (x - r * s.g)) * D + lane * kCols;
+      if constexpr (kCols == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    };
+    const int step2 = shared ? 1 : 2;
+    // every row of the tile has about as many partials
+    int a1, n1, lane1;
+    row_parts(min(row_base, 127), a1, n1, lane1);
+    if (n1 + t1.z <= 16) {
 #pragma unroll 1
-        for (int i = lane + 32; i < n; i += 32) {
-          const float2 v = __ldcg(a.part_stat + at(i));
-          if (v.y != 0.f) M = fmaxf(M, v.x);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-#pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += 32) {
-          if (i0 > 0) st = i0 + lane < n ? __ldcg(a.part_stat + at(i0 + lane)) : make_float2(-INFINITY, 0.f);
-          const float w = st.y != 0.f ? ex2_approx(st.x - M) : 0.f;
-          float wl = st.y != 0.f ? w * st.y : 0.f;
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
-          Lsum += wl;
-          const int hi = min(32, n - i0);
-#pragma unroll 4
-          for (int i = sub; i < hi; i += W) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            const float* src = a.part_o + static_cast<int64_t>(at(i0 + i)) * D + lane * kCols;
-            float x[kCols];
-            if constexpr (kCols == 4) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-              x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-            } else {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-              x[0] = v.x, x[1] = v.y;
-            }
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) acc[e] = wi == 0.f ? acc[e] : fmaf(wi, x[e], acc[e]);
-          }
-        }
+      for (int row = row_base + warp; row < end; row += kWarps) {
+        row_parts(row, a1, n1, lane1);
+        float acc[kCols] = {};
+        float Lsum = 0.f;
+        merge_rows<D>(a, [&](int i) { return i < n1 ? (a1 + i) * kBlockM + lane1 : (t1.y + (i - n1) * step2) * kBlockM + row; },
+                      n1 + t1.z, 0, 1, acc, Lsum);
+        write(row, acc, Lsum);
       }
-      if (W > 1) {
+    } else {
+#pragma unroll 1
+      for (int row = row_base; row < end; ++row) {
+        row_parts(row, a1, n1, lane1);
+        float acc[kCols] = {};
+        float Lsum = 0.f;
+        merge_rows<D>(a, [&](int i) { return i < n1 ? (a1 + i) * kBlockM + lane1 : (t1.y + (i - n1) * step2) * kBlockM + row; },
+                      n1 + t1.z, warp, kWarps, acc, Lsum);
 #pragma unroll
         for (int e = 0; e < kCols; ++e) acc_s[warp][lane * kCols + e] = acc[e];
         __syncthreads();
-        if (sub == 0)
-          for (int k = 1; k < W; ++k)
+        if (warp == 0) {
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) acc[e] += acc_s[warp + k][lane * kCols + e];
+          for (int k = 1; k < kWarps; ++k)
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) acc[e] += acc_s[k][lane * kCols + e];
+          write(row, acc, Lsum);
+        }
         __syncthreads();
-      }
-      if (mine && sub == 0) {
-        const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
-        const int x = t0.z + row, r = div_down(x, s.g);
-        uint16_t* dst = a.out + static_cast<int64_t>((t0.x * s.L + r) * a.Hq + t0.y * s.g + (x - r * s.g)) * D + lane * kCols;
-        if constexpr (kCols == 4)
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-        else
-          *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
       }
     }
   }
@@ -812,6 +900,17 @@ bool cache_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, bool q8, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q as [B L Hq, D] in boxes of one row's 64-element half (gathered four at a time), swizzled.
+bool query_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int D, int64_t rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * D)};
+  const cuuint32_t box[2] = {64, 1};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int64_t part_slots(const ec_params& p, bool prefix) {
   const int64_t separate = 2 * kMaxCtas;
   if (!prefix) return separate;
@@ -830,7 +929,7 @@ cudaError_t launch_impl(const ec_params& p, Args& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(cached_attention_kernel<D, Q8>, dim3(a.s.ctas), dim3(LY::kThreads), LY::kBytes, s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(cached_merge_kernel<D>, dim3(2 * a.s.ctas), dim3(kMergeThreads), 0, s, a);
+  return launch_pdl(cached_merge_kernel<D>, dim3(kMergeSteps * a.s.ctas), dim3(kMergeThreads), 0, s, a);
 }
 
 }  // namespace
@@ -863,7 +962,8 @@ cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_
   Args a;
   const ec_kv& pc = pre ? *prefix : cache;  // without a prefix its maps are not used
   const int pB = pre ? 1 : p.B;
-  if (!cache_map(enc, &a.tk, cache.k, q8, p.D, p.Hkv, p.L, p.B) || !cache_map(enc, &a.tv, cache.v, q8, p.D, p.Hkv, p.L, p.B) ||
+  if (!query_map(enc, &a.tq, q, p.D, static_cast<int64_t>(p.B) * p.L * p.Hq) ||
+      !cache_map(enc, &a.tk, cache.k, q8, p.D, p.Hkv, p.L, p.B) || !cache_map(enc, &a.tv, cache.v, q8, p.D, p.Hkv, p.L, p.B) ||
       !cache_map(enc, &a.tpk, pc.k, q8, p.D, p.Hkv, pc.len, pB) || !cache_map(enc, &a.tpv, pc.v, q8, p.D, p.Hkv, pc.len, pB)) {
     *status = EC_ERR_INVALID_ARG;
     return cudaErrorInvalidValue;
@@ -880,6 +980,8 @@ cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_
   a.s.Lp = pre ? prefix->len : 0;
   a.s.Hkv = p.Hkv;
   a.s.g = p.Hq / p.Hkv;
+  a.s.div_g.set(a.s.g);
+  a.s.div_h.set(p.Hkv);
   a.s.ctas = std::min(sms, kMaxCtas);
   a.s.slots = static_cast<int32_t>(part_slots(p, pre));
   a.Hq = p.Hq;

@@ -28,10 +28,39 @@ namespace cached {
 constexpr int kBlockM = 128;  // packed query rows per tile (TMEM lanes)
 constexpr int kBlockN = 128;  // keys per block
 
+// Division of 0 <= x < 2^31 by a number that the host knows: a shift for a power of two, else
+// (x m) >> (31 + l) with l = ceil(log2 d), m = ceil(2^(31 + l) / d): m d - 2^(31 + l) < d <= 2^l, so
+// the quotient's error is below x / (d 2^31) < 1 / d, and its floor is exact.
+struct FastDiv {
+  uint32_t m;
+  int32_t shift;
+  void set(int32_t d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    const bool pow2 = (1ll << l) == d;
+    m = pow2 ? 0u : static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
+    shift = pow2 ? l : l - 1;
+  }
+  EC_DEV int operator()(int x) const {
+    return static_cast<int>((m != 0u ? __umulhi(static_cast<uint32_t>(x), m) : static_cast<uint32_t>(x)) >> shift);
+  }
+};
+
+// Floor of x / d, 0 <= x < 2^31, quotients up to a few thousand: `inv` is 1 / d rounded, so the
+// product's floor is at most one off.
+EC_DEV int div_near(int x, int d, float inv) {
+  int q = static_cast<int>(static_cast<float>(x) * inv);
+  const int r = x - q * d;
+  if (r < 0) --q;
+  if (r >= d) ++q;
+  return q;
+}
+
 struct Shape {
   const int32_t *R, *kv_len;
   int32_t B, L, Lk, Lp, Hkv, g;  // own keys [0, Lk) without kv_len; Lp prefix positions
   int32_t ctas, slots;           // CTAs of the attention grid, partial tiles that the workspace holds
+  FastDiv div_g, div_h;          // by g and by Hkv
 };
 
 // Units, packed rows of a KV head and rows of q are counted in 32 bits: the host checks that q has
@@ -178,7 +207,7 @@ EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c) {
   Item it;
   it.before = 0;
   if (u < pl.own0) {
-    const int t = div_down(u, pl.nbp), per_head = div_down(pl.ptiles, s.Hkv);
+    const int t = div_down(u, pl.nbp), per_head = s.div_h(pl.ptiles);
     it.b = -1;
     it.kvh = div_down(t, per_head);
     it.row0 = (t - it.kvh * per_head) * kBlockM;

@@ -70,17 +70,22 @@ EC_DEV DequantScale dequant_scale(int byte) {
   return s;
 }
 
+// The one factor of bytes up to kExpOneFactor.
+constexpr int kExpOneFactor = 134;
+EC_DEV uint32_t dequant_factor(int byte) { return static_cast<uint32_t>(byte + 120) * 0x00800080u; }
+
 // Four codes -> two words of two bf16.
-EC_DEV void dequantise4(uint32_t w, const DequantScale& s, uint32_t& lo, uint32_t& hi) {
+EC_DEV void dequantise4(uint32_t w, uint32_t f, uint32_t& lo, uint32_t& hi) {
   // each byte sign-extended to 16 bits, shifted left by 4, then the copies of the sign over the
   // exponent's upper bits cleared
   uint32_t a, b;
   asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));
   asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(w));
-  a = (a << 4) & 0x87F087F0u;
-  b = (b << 4) & 0x87F087F0u;
-  lo = mul_bf16x2(a, s.f1);
-  hi = mul_bf16x2(b, s.f1);
+  lo = mul_bf16x2((a << 4) & 0x87F087F0u, f);
+  hi = mul_bf16x2((b << 4) & 0x87F087F0u, f);
+}
+EC_DEV void dequantise4(uint32_t w, const DequantScale& s, uint32_t& lo, uint32_t& hi) {
+  dequantise4(w, s.f1, lo, hi);
   if (s.two) {
     lo = mul_bf16x2(lo, s.f2);
     hi = mul_bf16x2(hi, s.f2);
