@@ -12,9 +12,11 @@
 // Structure (one CTA per SM; the work plan is attention_cached.cuh's):
 //   warp 0       makes the work plan, hands out the CTA's items, and is the TMA producer: K and V
 //                blocks of 128 keys.
-//   warp 1       allocates 512 TMEM columns and issues tcgen05.mma.
+//   warps 1, 3   issue tcgen05.mma, each for one of two streams (below); warp 1 allocates 512 TMEM
+//                columns. One issuer for both has a block's four waits and two products in
+//                series (3150 cycles a bf16 block).
 //   warp 2       the query tile, four rows a TMA gather (a tile packs rows of any sequences, which no
-//                one tensor box covers). Warp 3 has no work: registers are granted by four warps.
+//                one tensor box covers).
 //   warps 4..7   softmax of the CTA's even key blocks, warps 8..11 of the odd ones: two independent
 //                streams with their own S buffer, running maximum and sum, and O accumulator, joined
 //                once per item. One stream's softmax runs while the tensor cores work on the
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_empty, 2);
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&bars->unit_full[i], Q8 ? kDequantWarps : 1);
       mbar_init(&bars->unit_empty[i], 1);
@@ -389,83 +391,62 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         *a.header = h;
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer (whole warp, lane 0 issues)
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------------ MMA issuer of one stream
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlockN, 0);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
+    const int st = warp >> 1;
     const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
-    uint32_t n0 = 0;              // tiles of the items before
-    uint32_t used[2] = {0, 0};    // products finished or under way per stream
-    bool ok = true;
-    auto wait_w = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    const uint32_t s_col = tmem + st * kBlockN, o_col = tmem + kTmemO + st * 128;
+    uint32_t n0 = 0, used = 0;  // tiles of the items before; products finished or under way in this stream
+    int ok = 1;
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
-      auto issue_qk = [&](int i) {  // S of block i into its stream's buffer
-        const int st = i & 1;
-        const uint32_t n = n0 + 2 * i, slot = n % kUnits;
-        // the buffer's last P has been read
-        ok = ok && (used[st] == 0 || wait_w(&bars->pv_done[st], (used[st] - 1) & 1u)) &&
-             wait_w(&bars->unit_full[slot], (n / kUnits) & 1u);
-        if (!ok) return;
-        tc_fence_after();
-        if (lane == 0) {
+      if (lane == 0) {
+        auto issue_qk = [&](int i) {  // S of block i
+          const uint32_t n = n0 + 2 * i, slot = n % kUnits;
+          // the buffer's last P has been read
+          if (!wait(&bars->unit_full[slot], (n / kUnits) & 1u) || (used != 0 && !wait(&bars->pv_done[st], (used - 1) & 1u)))
+            return 0;
+          tc_fence_after();
           const uint32_t k_lo = sdesc_lo(smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes), 16);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(tmem + st * kBlockN, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+            umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
           umma_commit(&bars->s_full[st]);
           umma_commit(&bars->unit_empty[slot]);
-          if (i == it.nblk - 1) umma_commit(&bars->q_empty);
-        }
-        __syncwarp();
-      };
-      ok = wait_w(&bars->q_full, items & 1);
-      issue_qk(0);
-      if (it.nblk > 1) issue_qk(1);
-      for (int i = 0; ok && i < it.nblk; ++i) {
-        const int st = i & 1;
-        const uint32_t n = n0 + 2 * i + 1, slot = n % kUnits;
-        if (i == 0 && items > 0) ok = wait_w(&bars->o_free, (items - 1) & 1);
-        ok = ok && wait_w(&bars->unit_full[slot], (n / kUnits) & 1u);
-        if (!ok) break;
-        uint8_t* v_tile = smem + LY::kUnitOff + slot * LY::kTileBytes;
-        if constexpr (!Q8) {
-          // own rows past the sequence's length (the map zero-fills only past the cache's end)
-          const int j = it.j0 + i, nv = valid_keys(s, it, j);
-          if (j >= it.np && nv < kBlockN) {
-            for (int e = nv * 8 + lane; e < kBlockN * 8; e += 32)
-#pragma unroll
-              for (int at = 0; at < LY::kAtoms; ++at)
-                st_shared16(smem_u32(v_tile) + at * kAtomBytes + e * 16, make_uint4(0, 0, 0, 0));
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-        }
-        ok = wait_w(&bars->p_full[st], used[st] & 1u);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t v_lo = sdesc_lo(smem_u32(v_tile), kAtomBytes);
+          return 1;
+        };
+        ok = wait(&bars->q_full, items & 1);
+        if (ok && st < it.nblk) ok = issue_qk(st);
+        for (int i = st; ok && i < it.nblk; i += 2) {
+          if (i + 2 >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last S of the item is under way
+          const uint32_t n = n0 + 2 * i + 1, slot = n % kUnits;
+          if (i == st && items > 0) ok = wait(&bars->o_free, (items - 1) & 1);
+          ok = ok && wait(&bars->unit_full[slot], (n / kUnits) & 1u) && wait(&bars->p_full[st], used & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v_lo = sdesc_lo(smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes), kAtomBytes);
           const uint32_t acc0 = i > 1 ? 1u : 0u;  // the stream's first block of the item starts O anew
 #pragma unroll
           for (int kk = 0; kk < kBlockN / 16; ++kk)
-            umma_ts(tmem + kTmemO + st * 128, tmem + st * kBlockN + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv,
-                    kk > 0 ? 1u : acc0);
-          umma_commit(&bars->unit_empty[slot]);
+            umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
           umma_commit(&bars->pv_done[st]);
+          umma_commit(&bars->unit_empty[slot]);
+          ++used;
+          if (i + 2 < it.nblk) ok = issue_qk(i + 2);
         }
-        __syncwarp();
-        ++used[st];
-        if (i + 2 < it.nblk) issue_qk(i + 2);
+        if (ok && st >= it.nblk) mbar_arrive(&bars->q_empty);  // nothing of this item falls to stream 1
       }
       n0 += 2 * it.nblk;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
-  } else if (warp < 4) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------------ query loader
     // Each lane fetches four rows, wherever they lie; padding repeats the item's last row.
     const int32_t* cum = reinterpret_cast<const int32_t*>(smem + LY::kCumOff);
-    for (int items = 0; warp == 2; ++items) {
+    for (int items = 0;; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
       int at[4];
@@ -491,6 +472,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_addr = tmem + lane_off + st * kBlockN;
     float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
+    uint32_t n0 = 0;                    // tiles of the items before
     uint32_t used = 0, used_other = 0;  // blocks of this stream and of the other one
     bool ok = true;
     for (int items = 0; ok; ++items) {
@@ -501,9 +483,22 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       for (int i = st; i < it.nblk; i += 2, ++used) {
         ok = __all_sync(0xffffffffu, wait(&bars->s_full[st], used & 1u));
         if (!ok) break;
+        const int nv = valid_keys(s, it, it.j0 + i);
+        if constexpr (!Q8) {
+          // V rows past the sequence's length (the map zero-fills only past the cache's end)
+          if (nv < kBlockN && it.j0 + i >= it.np) {
+            const uint32_t n = n0 + 2 * i + 1, slot = n % kUnits;
+            ok = __all_sync(0xffffffffu, wait(&bars->unit_full[slot], (n / kUnits) & 1u));
+            if (!ok) break;
+            const uint32_t v_tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes);
+            for (int e = nv * 8 + row; e < kBlockN * 8; e += 128)
+#pragma unroll
+              for (int at = 0; at < LY::kAtoms; ++at) st_shared16(v_tile + at * kAtomBytes + e * 16, make_uint4(0, 0, 0, 0));
+            fence_proxy_async_smem();
+          }
+        }
         if (live) {
           tc_fence_after();
-          const int nv = valid_keys(s, it, it.j0 + i);
           // row maximum (scale > 0 commutes with it), a chunk's load behind the next one's
           uint32_t buf[2][32];
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -586,6 +581,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       // join the two streams: each warpgroup takes half of the columns of both accumulators
       const int n_mine = (it.nblk + 1 - st) >> 1, n_other = it.nblk - n_mine;
       used_other += n_other;
+      n0 += 2 * it.nblk;
       if (ok && n_mine > 0) ok = wait(&bars->pv_done[st], (used - 1) & 1u);
       if (ok && n_other > 0) ok = wait(&bars->pv_done[st ^ 1], (used_other - 1) & 1u);
       // this item's products began after every warp was done with the item before (o_free), so its
