@@ -130,6 +130,15 @@ EC_DEV void tma_gather4(void* dst, const void* tmap, uint64_t* bar, int x, int r
       : "memory");
 }
 
+template <int N>
+EC_DEV void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+EC_DEV void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 EC_DEV void st_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -171,6 +180,10 @@ EC_DEV uint32_t ld_shared8(uint32_t src) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),      \
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])      \
                : "memory")
+
+#define EC_TMEM_LDC EC_TMEM_LD32
+#define EC_TMEM_WAITC EC_TMEM_WAIT32
+constexpr int kChunk = 32;  // columns of S per load
 
 // Two fp32 lanes in one instruction.
 EC_DEV uint64_t pack_f32x2(float lo, float hi) {
@@ -306,167 +319,173 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     return it;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ plan, TMA producer
-    pdl_wait();  // everything above overlaps the previous kernel
-    const int cta = static_cast<int>(blockIdx.x);
-    const Plan pl = make_plan(s, a.dev_err, cta == 0);
-    pdl_launch_dependents();
-    const int u0 = min(pl.units, cta * pl.chunk), uend = *abort_flag ? u0 : min(pl.units, u0 + pl.chunk);
-    if (pl.shared && s.B <= kCum) {
-      const int incl = warp_inclusive(pl.rows_l * s.g);
-      if (lane < s.B) reinterpret_cast<int32_t*>(smem + LY::kCumOff)[lane] = incl;
-      __syncwarp();
-    }
-    uint32_t n = 0;  // tiles requested: K and V of each block in turn
-    int ok = 1, count = 0;
-    Record rec{};
-    for (int u = u0;; ++count) {
-      Item it;
-      it.nblk = 0;
-      if (ok && u < uend) it = cta_item(s, pl, u, uend, cta);
-      // Slot count % kItems is free: it held item count - 8, and with that one's epilogue still to come
-      // no V tile of the item after it can have been released, so that the producer would be
-      // waiting for room at the latest with the fifth item after it.
-      if (lane == 0) {
-        items_s[count % kItems] = it;
-        mbar_arrive(&bars->item_full[count % kItems]);
+  // With 20 warps a thread is launched with 96 registers; the softmax warps hold a row of P and take
+  // 144, the others go down to 64: 128 x 64 + 256 x 144 + 256 x 64 = 640 x 96.
+  if (warp < 4) {
+    if constexpr (Q8) setmaxnreg_dec<64>();
+    if (warp == 0) {
+      // ------------------------------------------------------------------ plan, TMA producer
+      pdl_wait();  // everything above overlaps the previous kernel
+      const int cta = static_cast<int>(blockIdx.x);
+      const Plan pl = make_plan(s, a.dev_err, cta == 0);
+      pdl_launch_dependents();
+      const int u0 = min(pl.units, cta * pl.chunk), uend = *abort_flag ? u0 : min(pl.units, u0 + pl.chunk);
+      if (pl.shared && s.B <= kCum) {
+        const int incl = warp_inclusive(pl.rows_l * s.g);
+        if (lane < s.B) reinterpret_cast<int32_t*>(smem + LY::kCumOff)[lane] = incl;
+        __syncwarp();
       }
-      if (it.nblk == 0) break;
-      if (it.slot >= 0 && it.j0 == 0 && it.b >= 0) {
-        rec.b = it.b;
-        rec.kvh = it.kvh;
-        rec.row0 = it.row0;
-        rec.nrows = it.nrows;
-        rec.before = it.before;
-        const int last = div_down(u + it.units - 1, pl.chunk);  // the CTA that ends the tile
-        rec.a1 = it.slot;
-        rec.a2 = pl.shared ? it.slot : 2 * (cta + 1);
-        rec.n2 = last - cta + (pl.shared ? 1 : 0);
-        if (pl.shared && lane == 0) a.records[it.tile - pl.ptiles] = rec;
-      }
-      if (lane == 0) {
-        for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j) {
-          const bool pre = j < it.np;
-          const int key0 = (pre ? j : j - it.np) * kBlockN;
-          const int b = pre ? 0 : it.b;
-          for (int kv = 0; kv < 2; ++kv, ++n) {
-            const CUtensorMap* map = kv == 0 ? (pre ? &a.tpk : &a.tk) : (pre ? &a.tpv : &a.tv);
-            if constexpr (Q8) {
-              const uint32_t slot = n % LY::kRaw;
-              if (!(ok = wait(&bars->raw_empty[slot], ((n / LY::kRaw) & 1u) ^ 1u))) break;
-              uint8_t* dst = smem + LY::kRawOff + slot * LY::kRawBytes;
-              // exponent rows are padded to 16 positions: the copy stays inside its row
-              const int ls = pre ? a.Lps : a.Ls;
-              const uint32_t ne = static_cast<uint32_t>(min(kBlockN, ls - key0));
-              const uint8_t* exps = (kv == 0 ? (pre ? a.pke : a.ke) : (pre ? a.pve : a.ve)) +
-                                    (static_cast<int64_t>(b) * s.Hkv + it.kvh) * ls + key0;
-              mbar_arrive_expect_tx(&bars->raw_full[slot], 128 * D + ne);
-              tma_load_4d(dst, map, &bars->raw_full[slot], 0, it.kvh, key0, b);
-              bulk_load(dst + 128 * D, exps, ne, &bars->raw_full[slot]);
-            } else {
-              const uint32_t slot = n % kUnits;
-              if (!(ok = wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u))) break;
-              uint8_t* dst = smem + LY::kUnitOff + slot * LY::kTileBytes;
-              mbar_arrive_expect_tx(&bars->unit_full[slot], LY::kTileBytes);
+      uint32_t n = 0;  // tiles requested: K and V of each block in turn
+      int ok = 1, count = 0;
+      Record rec{};
+      for (int u = u0;; ++count) {
+        Item it;
+        it.nblk = 0;
+        if (ok && u < uend) it = cta_item(s, pl, u, uend, cta);
+        // Slot count % kItems is free: it held item count - 8, and with that one's epilogue still to come
+        // no V tile of the item after it can have been released, so that the producer would be
+        // waiting for room at the latest with the fifth item after it.
+        if (lane == 0) {
+          items_s[count % kItems] = it;
+          mbar_arrive(&bars->item_full[count % kItems]);
+        }
+        if (it.nblk == 0) break;
+        if (it.slot >= 0 && it.j0 == 0 && it.b >= 0) {
+          rec.b = it.b;
+          rec.kvh = it.kvh;
+          rec.row0 = it.row0;
+          rec.nrows = it.nrows;
+          rec.before = it.before;
+          const int last = div_down(u + it.units - 1, pl.chunk);  // the CTA that ends the tile
+          rec.a1 = it.slot;
+          rec.a2 = pl.shared ? it.slot : 2 * (cta + 1);
+          rec.n2 = last - cta + (pl.shared ? 1 : 0);
+          if (pl.shared && lane == 0) a.records[it.tile - pl.ptiles] = rec;
+        }
+        if (lane == 0) {
+          for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j) {
+            const bool pre = j < it.np;
+            const int key0 = (pre ? j : j - it.np) * kBlockN;
+            const int b = pre ? 0 : it.b;
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+              const CUtensorMap* map = kv == 0 ? (pre ? &a.tpk : &a.tk) : (pre ? &a.tpv : &a.tv);
+              if constexpr (Q8) {
+                const uint32_t slot = n % LY::kRaw;
+                if (!(ok = wait(&bars->raw_empty[slot], ((n / LY::kRaw) & 1u) ^ 1u))) break;
+                uint8_t* dst = smem + LY::kRawOff + slot * LY::kRawBytes;
+                // exponent rows are padded to 16 positions: the copy stays inside its row
+                const int ls = pre ? a.Lps : a.Ls;
+                const uint32_t ne = static_cast<uint32_t>(min(kBlockN, ls - key0));
+                const uint8_t* exps = (kv == 0 ? (pre ? a.pke : a.ke) : (pre ? a.pve : a.ve)) +
+                                      (static_cast<int64_t>(b) * s.Hkv + it.kvh) * ls + key0;
+                mbar_arrive_expect_tx(&bars->raw_full[slot], 128 * D + ne);
+                tma_load_4d(dst, map, &bars->raw_full[slot], 0, it.kvh, key0, b);
+                bulk_load(dst + 128 * D, exps, ne, &bars->raw_full[slot]);
+              } else {
+                const uint32_t slot = n % kUnits;
+                if (!(ok = wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u))) break;
+                uint8_t* dst = smem + LY::kUnitOff + slot * LY::kTileBytes;
+                mbar_arrive_expect_tx(&bars->unit_full[slot], LY::kTileBytes);
 #pragma unroll
-              for (int at = 0; at < LY::kAtoms; ++at)
-                tma_load_4d(dst + at * kAtomBytes, map, &bars->unit_full[slot], at * 64, it.kvh, key0, b);
+                for (int at = 0; at < LY::kAtoms; ++at)
+                  tma_load_4d(dst + at * kAtomBytes, map, &bars->unit_full[slot], at * 64, it.kvh, key0, b);
+              }
             }
           }
         }
+        u += it.nblk;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      u += it.nblk;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
-    if (lane == 0) {
-      if (!pl.shared) a.records[cta] = rec;
-      if (cta == 0) {
-        Header h{};
-        h.records = pl.shared ? pl.otiles : s.ctas;
-        h.shared = pl.shared;
-        h.nbp = pl.nbp;
-        h.chunk = pl.chunk;
-        h.ptiles_head = s.div_h(pl.ptiles);
-        *a.header = h;
-      }
-    }
-  } else if (warp == 1 || warp == 3) {
-    // ------------------------------------------------------------------ MMA issuer of one stream
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlockN, 0);
-    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
-    const int st = warp >> 1;
-    const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
-    const uint32_t s_col = tmem + st * kBlockN, o_col = tmem + kTmemO + st * 128;
-    uint32_t n0 = 0, used = 0;  // tiles of the items before; products finished or under way in this stream
-    int ok = 1;
-    for (int items = 0; ok; ++items) {
-      const Item it = next_item(items);
-      if (it.nblk == 0) break;
       if (lane == 0) {
-        auto issue_qk = [&](int i) {  // S of block i
-          const uint32_t n = n0 + 2 * i, slot = n % kUnits;
-          // the buffer's last P has been read
-          if (!wait(&bars->unit_full[slot], (n / kUnits) & 1u) || (used != 0 && !wait(&bars->pv_done[st], (used - 1) & 1u)))
-            return 0;
-          tc_fence_after();
-          const uint32_t k_lo = sdesc_lo(smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes), 16);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
-          umma_commit(&bars->s_full[st]);
-          umma_commit(&bars->unit_empty[slot]);
-          return 1;
-        };
-        ok = wait(&bars->q_full, items & 1);
-        if (ok && st < it.nblk) ok = issue_qk(st);
-        for (int i = st; ok && i < it.nblk; i += 2) {
-          if (i + 2 >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last S of the item is under way
-          const uint32_t n = n0 + 2 * i + 1, slot = n % kUnits;
-          if (i == st && items > 0) ok = wait(&bars->o_free, (items - 1) & 1);
-          ok = ok && wait(&bars->unit_full[slot], (n / kUnits) & 1u) && wait(&bars->p_full[st], used & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t v_lo = sdesc_lo(smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes), kAtomBytes);
-          const uint32_t acc0 = i > 1 ? 1u : 0u;  // the stream's first block of the item starts O anew
-#pragma unroll
-          for (int kk = 0; kk < kBlockN / 16; ++kk)
-            umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
-          umma_commit(&bars->pv_done[st]);
-          umma_commit(&bars->unit_empty[slot]);
-          ++used;
-          if (i + 2 < it.nblk) ok = issue_qk(i + 2);
+        if (!pl.shared) a.records[cta] = rec;
+        if (cta == 0) {
+          Header h{};
+          h.records = pl.shared ? pl.otiles : s.ctas;
+          h.shared = pl.shared;
+          h.nbp = pl.nbp;
+          h.chunk = pl.chunk;
+          h.ptiles_head = s.div_h(pl.ptiles);
+          *a.header = h;
         }
-        if (ok && st >= it.nblk) mbar_arrive(&bars->q_empty);  // nothing of this item falls to stream 1
       }
-      n0 += 2 * it.nblk;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------------ query loader
-    // Each lane fetches four rows, wherever they lie; padding repeats the item's last row.
-    const int32_t* cum = reinterpret_cast<const int32_t*>(smem + LY::kCumOff);
-    for (int items = 0;; ++items) {
-      const Item it = next_item(items);
-      if (it.nblk == 0) break;
-      int at[4];
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int x = query_row(a, cum, it, it.row0 + min(4 * lane + i, it.nrows - 1));
-        at[0] = i == 0 ? x : at[0];
-        at[1] = i == 1 ? x : at[1];
-        at[2] = i == 2 ? x : at[2];
-        at[3] = x;
-      }
-      if (items > 0 && !__all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1))) break;
-      if (lane == 0) mbar_arrive_expect_tx(&bars->q_full, LY::kTileBytes);
-      __syncwarp();
+    } else if (warp == 1 || warp == 3) {
+      // ------------------------------------------------------------------ MMA issuer of one stream
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlockN, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
+      const int st = warp >> 1;
+      const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
+      const uint32_t s_col = tmem + st * kBlockN, o_col = tmem + kTmemO + st * 128;
+      uint32_t n0 = 0, used = 0;  // tiles of the items before; products finished or under way in this stream
+      int ok = 1;
+      for (int items = 0; ok; ++items) {
+        const Item it = next_item(items);
+        if (it.nblk == 0) break;
+        if (lane == 0) {
+          auto issue_qk = [&](int i) {  // S of block i
+            const uint32_t n = n0 + 2 * i, slot = n % kUnits;
+            // the buffer's last P has been read
+            if (!wait(&bars->unit_full[slot], (n / kUnits) & 1u) || (used != 0 && !wait(&bars->pv_done[st], (used - 1) & 1u)))
+              return 0;
+            tc_fence_after();
+            const uint32_t k_lo = sdesc_lo(smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes), 16);
 #pragma unroll
-      for (int c = 0; c < LY::kAtoms; ++c)
-        tma_gather4(smem + c * kAtomBytes + lane * 512, &a.tq, &bars->q_full, c * 64, at[0], at[1], at[2], at[3]);
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+            umma_commit(&bars->s_full[st]);
+            umma_commit(&bars->unit_empty[slot]);
+            return 1;
+          };
+          ok = wait(&bars->q_full, items & 1);
+          if (ok && st < it.nblk) ok = issue_qk(st);
+          for (int i = st; ok && i < it.nblk; i += 2) {
+            if (i + 2 >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last S of the item is under way
+            const uint32_t n = n0 + 2 * i + 1, slot = n % kUnits;
+            if (i == st && items > 0) ok = wait(&bars->o_free, (items - 1) & 1);
+            ok = ok && wait(&bars->unit_full[slot], (n / kUnits) & 1u) && wait(&bars->p_full[st], used & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v_lo = sdesc_lo(smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes), kAtomBytes);
+            const uint32_t acc0 = i > 1 ? 1u : 0u;  // the stream's first block of the item starts O anew
+#pragma unroll
+            for (int kk = 0; kk < kBlockN / 16; ++kk)
+              umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
+            umma_commit(&bars->pv_done[st]);
+            umma_commit(&bars->unit_empty[slot]);
+            ++used;
+            if (i + 2 < it.nblk) ok = issue_qk(i + 2);
+          }
+          if (ok && st >= it.nblk) mbar_arrive(&bars->q_empty);  // nothing of this item falls to stream 1
+        }
+        n0 += 2 * it.nblk;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------------------ query loader
+      // Each lane fetches four rows, wherever they lie; padding repeats the item's last row.
+      const int32_t* cum = reinterpret_cast<const int32_t*>(smem + LY::kCumOff);
+      for (int items = 0;; ++items) {
+        const Item it = next_item(items);
+        if (it.nblk == 0) break;
+        int at[4];
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int x = query_row(a, cum, it, it.row0 + min(4 * lane + i, it.nrows - 1));
+          at[0] = i == 0 ? x : at[0];
+          at[1] = i == 1 ? x : at[1];
+          at[2] = i == 2 ? x : at[2];
+          at[3] = x;
+        }
+        if (items > 0 && !__all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->q_full, LY::kTileBytes);
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < LY::kAtoms; ++c)
+          tma_gather4(smem + c * kAtomBytes + lane * 512, &a.tq, &bars->q_full, c * 64, at[0], at[1], at[2], at[3]);
+      }
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ softmax + epilogue
+    if constexpr (Q8) setmaxnreg_inc<144>();
     const int st = (warp - 4) >> 2;            // stream
     const int row = 32 * (warp & 3) + lane;    // TMEM lane = packed query row
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -499,72 +518,66 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         }
         if (live) {
           tc_fence_after();
-          // row maximum (scale > 0 commutes with it), a chunk's load behind the next one's
-          uint32_t buf[2][32];
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          EC_TMEM_LD32(s_addr, buf[0]);
+          // p = 2^(s scale log2(e) - m) for the row, m the running maximum so far (0 while no score
+          // was finite): one pass over S, P kept in registers, so that a row whose new maximum is
+          // above m by more than the threshold, or that has no m yet, can take S again
+          const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2);
+          uint32_t pk[kBlockN / 2];
+          float sum = 0.f;
+          auto exponentials = [&](float neg_m) {  // fills pk and sum; returns the largest exponent
+            const uint64_t neg_m2 = pack_f32x2(neg_m, neg_m);
+            uint64_t sum2[2] = {0, 0};
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t buf[2][kChunk];
+            EC_TMEM_LDC(s_addr, buf[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            EC_TMEM_WAIT32(buf[c & 1]);
-            if (c < 3) EC_TMEM_LD32(s_addr + (c + 1) * 32, buf[(c + 1) & 1]);
-            uint32_t* x = buf[c & 1];
-            if (nv < kBlockN) {
+            for (int c = 0; c < kBlockN / kChunk; ++c) {
+              EC_TMEM_WAITC(buf[c & 1]);
+              if (c + 1 < kBlockN / kChunk) EC_TMEM_LDC(s_addr + (c + 1) * kChunk, buf[(c + 1) & 1]);
+              uint32_t* x = buf[c & 1];
+              if (nv < kBlockN) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c * 32 + e >= nv) x[e] = __float_as_uint(-INFINITY);
+                for (int e = 0; e < kChunk; ++e)
+                  if (c * kChunk + e >= nv) x[e] = __float_as_uint(-INFINITY);
+              }
+#pragma unroll
+              for (int e = 0; e < kChunk; e += 2) {
+                float p0, p1;
+                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
+                m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], p0, p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
+                pk[(c * kChunk + e) >> 1] = pack_bf16x2(p0, p1);
+              }
             }
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-          }
-          uint32_t s16[2][16];
-          EC_TMEM_LD16(s_addr, s16[0]);
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+            float lo, hi;
+            unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
+            sum = lo + hi;
+            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          };
+          float up = exponentials(m_used == -INFINITY ? 0.f : -m_used);
           bool rescale = false;
           float alpha = 1.f;
-          if (i == st) {
-            m_used = mx;
-          } else if (mx > m_used + kRescaleLog2) {
-            alpha = ex2_approx(m_used - mx);
-            m_used = mx;
-            l_sum *= alpha;
-            rescale = true;
-          }
-          // p = 2^(s scale log2(e) - m); without a finite score so far, nothing is subtracted and p = 0
-          const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-          const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
-          uint64_t sum2[2] = {0, 0};
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            EC_TMEM_WAIT16(s16[c & 1]);
-            if (c < 7) EC_TMEM_LD16(s_addr + (c + 1) * 16, s16[(c + 1) & 1]);
-            uint32_t* x = s16[c & 1];
-            if (nv < kBlockN) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (c * 16 + e >= nv) x[e] = __float_as_uint(-INFINITY);
+          // no m yet: the first finite score of the row's blocks sets it
+          if (__any_sync(0xffffffffu, up > kRescaleLog2 || (m_used == -INFINITY && up > -INFINITY))) {
+            const float base = m_used == -INFINITY ? 0.f : m_used;
+            if (up > kRescaleLog2 || (m_used == -INFINITY && up > -INFINITY)) {
+              alpha = m_used == -INFINITY ? 0.f : ex2_approx(-up);
+              m_used = base + up;
+              l_sum *= alpha;
+              rescale = i != st;
             }
-            uint32_t pk[8];
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float p0, p1;
-              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
-              pk[e >> 1] = pack_bf16x2(p0, p1);
-            }
-            // P over columns of S that this loop has read: [8 c, 8 c + 8) lies below 16 (c + 1)
-            EC_TMEM_ST8(s_addr + c * 8, pk);
+            exponentials(m_used == -INFINITY ? 0.f : -m_used);
           }
-          float sum_lo, sum_hi;
-          unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
-          l_sum += sum_lo + sum_hi;
+          l_sum += sum;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) EC_TMEM_ST32(s_addr + c * 32, (pk + 32 * c));
           // the stream's earlier products are done (they were waited for before this S was made)
           if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-              uint32_t* o = buf[0];
+              uint32_t o[32];
               EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
               EC_TMEM_WAIT32(o);
 #pragma unroll
@@ -646,6 +659,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     }
   } else if constexpr (Q8) {
     // ------------------------------------------------------------------ dequantisation
+    setmaxnreg_dec<64>();
     // Eight lanes read 128 neighbouring bytes of codes; the 16-byte pieces of bf16 that they
     // store fall into eight different bank groups: for D = 128 lanes 0..3 take the first half of
     // row r and lanes 4..7 the second half of row r ^ 1, whose swizzle differs in the lowest bit.
