@@ -107,7 +107,7 @@ struct Args {
   float scale_log2;
   const uint16_t* q;
   uint16_t* out;
-  float* part_o;      // [slots][128][D]
+  float4* part_o;     // [slots][D / 4][128]: four columns of a row, neighbouring rows side by side
   float2* part_stat;  // [slots][128]: running maximum and sum
   Header* header;
   Record* records;    // [max(slots, ctas)]
@@ -341,7 +341,11 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       for (int u = u0;; ++count) {
         Item it;
         it.nblk = 0;
-        if (ok && u < uend) it = cta_item(s, pl, u, uend, cta);
+        while (ok && it.nblk == 0 && u < uend) {
+          int span;
+          it = cta_item(s, pl, u, uend, cta, span);
+          u += span;
+        }
         // Slot count % kItems is free: it held item count - 8, and with that one's epilogue still to come
         // no V tile of the item after it can have been released, so that the producer would be
         // waiting for room at the latest with the fifth item after it.
@@ -356,7 +360,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           rec.row0 = it.row0;
           rec.nrows = it.nrows;
           rec.before = it.before;
-          const int last = div_down(u + it.units - 1, pl.chunk);  // the CTA that ends the tile
+          // the CTA that ends the tile: u is past this item and, if that is in here, the tile's cost
+          const int last = it.nblk == it.blocks ? cta : div_down(u + it.blocks - it.nblk - 1, pl.chunk);
           rec.a1 = it.slot;
           rec.a2 = pl.shared ? it.slot : 2 * (cta + 1);
           rec.n2 = last - cta + (pl.shared ? 1 : 0);
@@ -393,7 +398,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
             }
           }
         }
-        u += it.nblk;
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
       if (lane == 0) {
@@ -402,6 +406,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           Header h{};
           h.records = pl.shared ? pl.otiles : s.ctas;
           h.shared = pl.shared;
+          h.prefix_units = pl.nbp + kTileCost;
           h.nbp = pl.nbp;
           h.chunk = pl.chunk;
           h.ptiles_head = s.div_h(pl.ptiles);
@@ -618,13 +623,13 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         const float f0 = w0 * norm, f1 = w1 * norm;
         const bool valid = row < it.nrows;
         uint16_t* orow = nullptr;
-        float* prow = nullptr;
+        float4* prow = nullptr;
         if (complete) {
           const int x = it.row0 + row, r = s.div_g(x);
           orow = a.out + static_cast<int64_t>((it.b * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g)) * D + st * (D / 2);
         } else {
           const int at = it.slot * kBlockM + row;
-          prow = a.part_o + static_cast<int64_t>(at) * D + st * (D / 2);
+          prow = a.part_o + static_cast<int64_t>(it.slot * (D / 4) + st * (D / 8)) * kBlockM + row;
           if (st == 0 && valid) a.part_stat[at] = make_float2(M, L);
         }
 #pragma unroll 1
@@ -649,7 +654,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           } else if (valid) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4*>(prow + c * 32 + 4 * e) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+              prow[(c * 8 + e) * kBlockM] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           }
         }
         tc_fence_before();
@@ -730,147 +735,159 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
 
 // ---------------------------------------------------------------------------------- merge
 
-// Adds up the weighted partial rows i0, i0 + step, ... of one row (whole warp, D / 32 columns a
-// lane), kBatch loads in flight, and the sum of the weights; `M`: the largest maximum.
-template <int D, typename At>
-EC_DEV void merge_rows(const Args& a, const At& at, int n, int i0, int step, float (&acc)[D / 32], float& Lsum) {
-  constexpr int kCols = D / 32, kBatch = 8;
-  const int lane = threadIdx.x & 31;
-  float M = -INFINITY;
-  float2 st = make_float2(-INFINITY, 0.f);
-  if (lane < n) st = __ldcg(a.part_stat + at(lane));
-  for (int k0 = 0; k0 < n; k0 += 32) {  // weights of 32 partials at a time
-    if (k0 > 0) {
-      st = make_float2(-INFINITY, 0.f);
-      if (k0 + lane < n) st = __ldcg(a.part_stat + at(k0 + lane));
-    }
-    // the first batch of rows is on its way while the weights are worked out
-    float x[kBatch][kCols];
-    auto load = [&](int i) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int k = i + u * step;
-        if (k < min(n, k0 + 32)) {
-          const float* src = a.part_o + static_cast<int64_t>(at(k)) * D + lane * kCols;
-          if constexpr (kCols == 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-            x[u][0] = v.x, x[u][1] = v.y, x[u][2] = v.z, x[u][3] = v.w;
-          } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-            x[u][0] = v.x, x[u][1] = v.y;
-          }
-        }
-      }
-    };
-    int i = k0 + i0;
-    load(i);
-    float mx = st.y != 0.f ? st.x : -INFINITY;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    if (mx > M) {  // the whole warp
-      const float f = M == -INFINITY ? 0.f : ex2_approx(M - mx);
-#pragma unroll
-      for (int e = 0; e < kCols; ++e) acc[e] *= f;
-      Lsum *= f;
-      M = mx;
-    }
-    // a partial without weight (no finite score) contributes nothing, whatever its row holds
-    const float w = st.y != 0.f ? ex2_approx(st.x - M) : 0.f;
-    float wl = st.y != 0.f ? w * st.y : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, off);
-    Lsum += wl;
-    for (;;) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int k = i + u * step;
-        const float wk = __shfl_sync(0xffffffffu, w, (k - k0) & 31);
-        if (k < min(n, k0 + 32) && wk != 0.f) {
-#pragma unroll
-          for (int e = 0; e < kCols; ++e) acc[e] = fmaf(wk, x[u][e], acc[e]);
-        }
-      }
-      i += kBatch * step;
-      if (i >= min(n, k0 + 32)) break;
-      load(i);
-    }
-  }
-}
-
-// Joins the partial rows of split tiles by their log-sum-exp weights, in a fixed order. A CTA takes
-// 32 rows of one tile: one warp a row, or with more than 16 partials all eight warps a row, each
-// every eighth partial. Two chains of loads (the record; the statistics and the rows together) and
-// the partials' bytes, which the attention kernel has just written (L2), are its whole cost.
+// Joins the partial rows of split tiles by their log-sum-exp weights, in a fixed order. A CTA takes 32
+// rows of one tile. Up to 8 partials: a lane a row and a warp D / 8 columns of it, as the partials
+// lie, four partials in flight. More (few rows over a long cache): a warp takes one row's whole
+// width, eight partials in flight; above 32, all eight warps take it, each every eighth partial.
+// (A lane a row with 16 partials of 7 rows took 10 us longer, its loads one after another.) Two
+// chains of loads (the record; statistics and rows) and the partials' bytes, which the attention
+// kernel has just written (L2), are the whole cost.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __grid_constant__ Args a) {
-  constexpr int kWarps = kMergeThreads / 32, kCols = D / 32;
-  __shared__ float acc_s[kWarps][D];
+  constexpr int kWarps = kMergeThreads / 32, kQuads = D / 4, kMine = kQuads / kWarps;  // float4 columns; a warp's
+  __shared__ float red[kWarps][kQuads][4];
+  __shared__ float2 red_stat[kWarps];
   const Shape& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const int4 h = __ldcg(reinterpret_cast<const int4*>(a.header));            // records, shared, nbp, chunk
-  const int4 g = __ldcg(reinterpret_cast<const int4*>(a.header) + 1);        // ptiles_head
-  const int row_base = (blockIdx.x & (kMergeSteps - 1)) * kMergeRows;
+  const int4 h = __ldcg(reinterpret_cast<const int4*>(a.header));            // records, shared, prefix units, chunk
+  const int4 h2 = __ldcg(reinterpret_cast<const int4*>(a.header) + 1);       // ptiles_head, nbp
+  const bool shared = h.y != 0;
+  const int row0 = (blockIdx.x & (kMergeSteps - 1)) * kMergeRows;
   for (int which = blockIdx.x / kMergeSteps; which < h.x; which += gridDim.x / kMergeSteps) {
     const int4* rp = reinterpret_cast<const int4*>(a.records + which);
     const int4 t0 = __ldcg(rp), t1 = __ldcg(rp + 1);  // b, kvh, row0, nrows; a1, a2, n2, before
-    const int end = min(row_base + kMergeRows, t0.w);
-    const bool shared = h.y != 0;
+    const int rows = min(kMergeRows, t0.w - row0);
+    if (rows <= 0) continue;
     // the partials of a row: n1 slots from a1 on at `lane1`, then every `step2`-th from a2 on
+    const int step2 = shared ? 1 : 2;
     auto row_parts = [&](int row, int& a1, int& n1, int& lane1) {
       a1 = t1.x, n1 = 1, lane1 = row;
       if (shared) {  // the row's prefix tile, and the CTAs that its blocks fell to
-        const int gp = t1.w + t0.z + row, pt = t0.y * g.x + (gp >> 7), pu = pt * h.z;
+        const int gp = t1.w + t0.z + row, pt = t0.y * h2.x + (gp >> 7), pu = pt * h.z;
         const float inv = __fdividef(1.f, static_cast<float>(h.w));
         const int c0 = div_near(pu, h.w, inv);
         a1 = pt + c0;
-        n1 = div_near(pu + h.z - 1, h.w, inv) - c0 + 1;
+        n1 = div_near(pu + h2.y - 1, h.w, inv) - c0 + 1;
         lane1 = gp & 127;
       }
     };
-    auto write = [&](int row, const float (&acc)[kCols], float Lsum) {
-      const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+    auto out_row = [&](int row) {
       const int x = t0.z + row, r = s.div_g(x);
-      uint16_t* dst = a.out + static_cast<int64_t>((t0.x * s.L + r) * a.Hq + t0.y * s.g + (x - r * s.g)) * D + lane * kCols;
-      if constexpr (kCols == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-      else
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+      return a.out + static_cast<int64_t>((t0.x * s.L + r) * a.Hq + t0.y * s.g + (x - r * s.g)) * D;
     };
-    const int step2 = shared ? 1 : 2;
-    // every row of the tile has about as many partials
     int a1, n1, lane1;
-    row_parts(min(row_base, 127), a1, n1, lane1);
-    if (n1 + t1.z <= 16) {
+    row_parts(row0, a1, n1, lane1);
+    const int most = n1 + t1.z;
+    if (most <= 8) {
+      const int row = row0 + min(lane, rows - 1);
+      row_parts(row, a1, n1, lane1);
+      const int n = n1 + t1.z;
+      auto at = [&](int i, int& slot, int& ln) {
+        slot = i < n1 ? a1 + i : t1.y + (i - n1) * step2;
+        ln = i < n1 ? lane1 : row;
+      };
+      float M = -INFINITY, Lsum = 0.f;
+      float acc[4 * kMine] = {};
 #pragma unroll 1
-      for (int row = row_base + warp; row < end; row += kWarps) {
-        row_parts(row, a1, n1, lane1);
-        float acc[kCols] = {};
-        float Lsum = 0.f;
-        merge_rows<D>(a, [&](int i) { return i < n1 ? (a1 + i) * kBlockM + lane1 : (t1.y + (i - n1) * step2) * kBlockM + row; },
-                      n1 + t1.z, 0, 1, acc, Lsum);
-        write(row, acc, Lsum);
+      for (int i0 = 0; i0 < n; i0 += 4) {
+        float2 st[4];
+        float4 x[4][kMine];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          int slot, ln;
+          at(min(i0 + u, n - 1), slot, ln);
+          st[u] = __ldcg(a.part_stat + slot * kBlockM + ln);
+          const float4* src = a.part_o + static_cast<int64_t>(slot * kQuads + warp * kMine) * kBlockM + ln;
+#pragma unroll
+          for (int q = 0; q < kMine; ++q) x[u][q] = __ldcg(src + q * kBlockM);
+          if (i0 + u >= n) st[u].y = 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          // a partial without weight (no finite score) contributes nothing, whatever its row holds
+          if (st[u].y == 0.f) continue;
+          const float m = fmaxf(M, st[u].x), f = M == -INFINITY ? 0.f : ex2_approx(M - m), w = ex2_approx(st[u].x - m);
+          M = m;
+          Lsum = fmaf(w, st[u].y, Lsum * f);
+#pragma unroll
+          for (int q = 0; q < kMine; ++q) {
+            acc[4 * q] = fmaf(w, x[u][q].x, acc[4 * q] * f);
+            acc[4 * q + 1] = fmaf(w, x[u][q].y, acc[4 * q + 1] * f);
+            acc[4 * q + 2] = fmaf(w, x[u][q].z, acc[4 * q + 2] * f);
+            acc[4 * q + 3] = fmaf(w, x[u][q].w, acc[4 * q + 3] * f);
+          }
+        }
+      }
+      if (lane < rows) {
+        const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+        uint2* dst = reinterpret_cast<uint2*>(out_row(row) + warp * kMine * 4);
+#pragma unroll
+        for (int q = 0; q < kMine; ++q)
+          dst[q] = make_uint2(pack_bf16x2(acc[4 * q] * inv, acc[4 * q + 1] * inv), pack_bf16x2(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv));
       }
     } else {
+      // lane q holds a row's columns [4 q, 4 q + 4) (D = 64: lanes past 15 repeat)
+      const int quad = lane % kQuads;
+      const bool together = most > 32;  // all warps on one row
 #pragma unroll 1
-      for (int row = row_base; row < end; ++row) {
+      for (int row = row0 + (together ? 0 : warp); row < row0 + rows; row += together ? 1 : kWarps) {
         row_parts(row, a1, n1, lane1);
-        float acc[kCols] = {};
-        float Lsum = 0.f;
-        merge_rows<D>(a, [&](int i) { return i < n1 ? (a1 + i) * kBlockM + lane1 : (t1.y + (i - n1) * step2) * kBlockM + row; },
-                      n1 + t1.z, warp, kWarps, acc, Lsum);
+        const int n = n1 + t1.z, step = together ? kWarps : 1;
+        auto place = [&](int i, int& slot, int& ln) {
+          slot = i < n1 ? a1 + i : t1.y + (i - n1) * step2;
+          ln = i < n1 ? lane1 : row;
+        };
+        float acc[4] = {}, M = -INFINITY, Lsum = 0.f;
+#pragma unroll 1
+        for (int i0 = together ? warp : 0; i0 < n; i0 += 8 * step) {
+          float2 st[8];
+          float4 x[8];
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) acc_s[warp][lane * kCols + e] = acc[e];
-        __syncthreads();
-        if (warp == 0) {
+          for (int u = 0; u < 8; ++u) {
+            int slot, ln;
+            place(min(i0 + u * step, n - 1), slot, ln);
+            st[u] = __ldcg(a.part_stat + slot * kBlockM + ln);
+            x[u] = __ldcg(a.part_o + static_cast<int64_t>(slot * kQuads + quad) * kBlockM + ln);
+            if (i0 + u * step >= n) st[u].y = 0.f;
+          }
 #pragma unroll
-          for (int k = 1; k < kWarps; ++k)
-#pragma unroll
-            for (int e = 0; e < kCols; ++e) acc[e] += acc_s[k][lane * kCols + e];
-          write(row, acc, Lsum);
+          for (int u = 0; u < 8; ++u) {
+            if (st[u].y == 0.f) continue;
+            const float m = fmaxf(M, st[u].x), f = M == -INFINITY ? 0.f : ex2_approx(M - m), w = ex2_approx(st[u].x - m);
+            M = m;
+            Lsum = fmaf(w, st[u].y, Lsum * f);
+            acc[0] = fmaf(w, x[u].x, acc[0] * f);
+            acc[1] = fmaf(w, x[u].y, acc[1] * f);
+            acc[2] = fmaf(w, x[u].z, acc[2] * f);
+            acc[3] = fmaf(w, x[u].w, acc[3] * f);
+          }
         }
-        __syncthreads();
+        if (together) {
+          if (lane < kQuads) *reinterpret_cast<float4*>(red[warp][quad]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          if (lane == 0) red_stat[warp] = make_float2(M, Lsum);
+          __syncthreads();
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k)
+            if (red_stat[k].y != 0.f) top = fmaxf(top, red_stat[k].x);
+          Lsum = acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) {
+            if (red_stat[k].y == 0.f) continue;
+            const float w = ex2_approx(red_stat[k].x - top);
+            Lsum = fmaf(w, red_stat[k].y, Lsum);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = fmaf(w, red[k][quad][e], acc[e]);
+          }
+          __syncthreads();
+        }
+        if (lane < kQuads && (!together || warp == 0)) {
+          const float inv = Lsum == 0.f ? 0.f : 1.f / Lsum;
+          reinterpret_cast<uint2*>(out_row(row))[quad] =
+              make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        }
       }
     }
   }
@@ -1000,8 +1017,8 @@ cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_
   a.scale_log2 = scale * kLog2e;
   a.q = static_cast<const uint16_t*>(q);
   a.out = static_cast<uint16_t*>(out);
-  a.part_o = static_cast<float*>(ws);
-  a.part_stat = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.s.slots) * kBlockM * p.D);
+  a.part_o = static_cast<float4*>(ws);
+  a.part_stat = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.s.slots) * kBlockM * (p.D / 4));
   a.records = reinterpret_cast<Record*>(a.part_stat + static_cast<int64_t>(a.s.slots) * kBlockM);
   a.header = reinterpret_cast<Header*>(a.records + a.s.slots);  // slots >= ctas
   a.dev_err = dev_err;

@@ -6,11 +6,14 @@
 // warp, and again by the merge, a one-block call took 24.6 us, 12 of them before the first score.)
 //
 // A tile is 128 packed query rows (a row of a sequence and one of the g query heads of a KV head)
-// of one KV head; a unit is a tile times one block of 128 keys. All units stand in one line, tile
-// after tile, and CTA c takes the units [c chunk, (c + 1) chunk): every SM gets the same number
-// of key blocks whatever the batch, heads and lengths are. The part of a tile that falls to one CTA
-// is an item; a tile with one item is finished by it, one with several leaves partial rows in the
-// workspace for the merge.
+// of one KV head; a unit is a tile times one block of 128 keys. Each tile is followed by kTileCost
+// units without a block, for the time between one tile and the next (its queries, the join, the
+// rows' way out). All units stand in one line, tile after tile, and CTA c takes the units
+// [c chunk, (c + 1) chunk): every SM gets about the same time whatever the batch, heads and lengths
+// are. (Without the cost, a batch with a long shared prefix gave the last CTAs tens of two-block
+// tiles for the others' 140 blocks: 602 us, of which half was waiting for them.) The part of a tile
+// that falls to one CTA is an item; a tile with one item is finished by it, one with several leaves
+// partial rows in the workspace for the merge.
 //   separate  a tile holds rows of one sequence and runs over the prefix's blocks, then the sequence's own
 //   shared    rows of all sequences are packed into tiles for the prefix's blocks, each sequence's
 //             rows into tiles for its own blocks, and every row is merged. Taken when it saves
@@ -27,6 +30,7 @@ namespace cached {
 
 constexpr int kBlockM = 128;  // packed query rows per tile (TMEM lanes)
 constexpr int kBlockN = 128;  // keys per block
+constexpr int kTileCost = 3;  // blocks whose time a tile takes beside its own
 
 // Division of 0 <= x < 2^31 by a number that the host knows: a shift for a power of two, else
 // (x m) >> (31 + l) with l = ceil(log2 d), m = ceil(2^(31 + l) / d): m d - 2^(31 + l) < d <= 2^l, so
@@ -85,7 +89,7 @@ struct Item {
   int32_t j0, nblk;  // this item's blocks [j0, j0 + nblk); nblk = 0 ends the CTA's work
   int32_t len;       // own keys of the sequence
   int32_t slot;      // where its partial rows go, -1: the tile is complete
-  int32_t units;     // blocks of the whole tile
+  int32_t blocks;    // of the whole tile
   int32_t tile;      // index over all tiles
   int32_t before;    // packed rows of the sequences before b
 };
@@ -100,8 +104,8 @@ struct Record {
   int32_t a1, a2, n2, before;
 };
 struct Header {
-  int32_t records, shared, nbp, chunk;
-  int32_t ptiles_head, pad[3];
+  int32_t records, shared, prefix_units, chunk;  // units of a prefix tile, units of a CTA
+  int32_t ptiles_head, nbp, pad[2];              // prefix tiles of a KV head, blocks of each
 };
 
 // Quotients of numbers below 2^31; the divisor's bits are few enough here that the hardware's own
@@ -150,7 +154,7 @@ EC_DEV int blocks_of(int32_t len) { return (len + kBlockN - 1) / kBlockN; }
 
 // Blocks of one tile of a sequence. A tile without any key still has one block, all of it masked, so
 // that its rows are written (as zeros) or, shared, so that a CTA leaves its record.
-EC_DEV int tile_units(const Plan& pl, int32_t len) { return max(1, (pl.shared ? 0 : pl.nbp) + blocks_of(len)); }
+EC_DEV int tile_blocks(const Plan& pl, int32_t len) { return max(1, (pl.shared ? 0 : pl.nbp) + blocks_of(len)); }
 
 // Whole warp.
 EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
@@ -171,9 +175,9 @@ EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
     const int t = s.Hkv * tiles_of(s, r), nb = blocks_of(n);
     rows += r * s.g;
     tiles += t;
-    apart += t * max(1, pl.nbp + nb);
-    own += t * max(1, nb);
-    most += static_cast<float>(t) * static_cast<float>(pl.nbp + nb + 1);
+    apart += t * (max(1, pl.nbp + nb) + kTileCost);
+    own += t * (max(1, nb) + kTileCost);
+    most += static_cast<float>(t) * static_cast<float>(pl.nbp + nb + 1 + 2 * kTileCost);
   }
   pl.rows = warp_total(rows);
   pl.otiles = warp_total(tiles);
@@ -189,11 +193,11 @@ EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
   pl.units = apart;
   if (pl.nbp > 0 && s.B > 1) {
     const int ptiles = s.Hkv * ((pl.rows + kBlockM - 1) / kBlockM);
-    const int together = ptiles * pl.nbp + warp_total(own);
+    const int together = ptiles * (pl.nbp + kTileCost) + warp_total(own);
     pl.shared = apart > 0 && ptiles + pl.otiles + s.ctas <= s.slots && together <= apart - apart / 8;
     if (pl.shared) {
       pl.ptiles = ptiles;
-      pl.own0 = ptiles * pl.nbp;
+      pl.own0 = ptiles * (pl.nbp + kTileCost);
       pl.units = together;
     }
   }
@@ -201,19 +205,20 @@ EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
   return pl;
 }
 
-// Whole warp: the item of CTA c that starts at unit u (u below `end`, its last one's successor).
-EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c) {
+// Whole warp: the item of CTA c that starts at unit u (u below `end`, its last one's successor), and
+// the units `span` that it takes; nblk = 0 when those are a tile's cost only.
+EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c, int& span) {
   const int lane = threadIdx.x & 31;
   Item it;
   it.before = 0;
   if (u < pl.own0) {
-    const int t = div_down(u, pl.nbp), per_head = s.div_h(pl.ptiles);
+    const int t = div_down(u, pl.nbp + kTileCost), per_head = s.div_h(pl.ptiles);
     it.b = -1;
     it.kvh = div_down(t, per_head);
     it.row0 = (t - it.kvh * per_head) * kBlockM;
     it.nrows = min(kBlockM, pl.rows - it.row0);
-    it.np = it.units = pl.nbp;
-    it.j0 = u - t * pl.nbp;
+    it.np = it.blocks = pl.nbp;
+    it.j0 = u - t * (pl.nbp + kTileCost);
     it.tile = t;
     it.len = 0;
   } else {
@@ -222,7 +227,7 @@ EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c) {
     for (int b0 = 0;; b0 += 32) {
       int32_t r, n;
       seq_of(s, pl, b0 + lane, r, n);
-      const int t = s.Hkv * tiles_of(s, r), tu = tile_units(pl, n);
+      const int t = s.Hkv * tiles_of(s, r), tu = tile_blocks(pl, n) + kTileCost;
       int incl = t * tu, src = 0;
       if (s.B > 1) {
         incl = warp_inclusive(incl);
@@ -244,19 +249,20 @@ EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c) {
       it.b = b0 + src;
       break;
     }
-    it.units = tile_units(pl, it.len);
-    const int w = u - base, tl = div_down(w, it.units), per_head = tiles_of(s, rsel);
+    it.blocks = tile_blocks(pl, it.len);
+    const int w = u - base, tl = div_down(w, it.blocks + kTileCost), per_head = tiles_of(s, rsel);
     it.kvh = div_down(tl, per_head);
     it.row0 = (tl - it.kvh * per_head) * kBlockM;
     it.nrows = min(kBlockM, rsel * s.g - it.row0);
     it.np = pl.shared ? 0 : pl.nbp;
-    it.j0 = w - tl * it.units;
+    it.j0 = w - tl * (it.blocks + kTileCost);
     it.tile = tbase + tl;
   }
-  it.nblk = min(it.units - it.j0, end - u);
+  span = min(it.blocks + kTileCost - it.j0, end - u);
+  it.nblk = max(0, min(it.blocks - it.j0, span));
   // Partial rows. Shared: tile + c grows from item to item, so no two share a slot. Separate: a CTA
   // has at most two incomplete items, one that began before it and one that ends after it.
-  it.slot = pl.shared ? it.tile + c : it.nblk == it.units ? -1 : 2 * c + (it.j0 == 0 ? 1 : 0);
+  it.slot = pl.shared ? it.tile + c : it.nblk == it.blocks ? -1 : 2 * c + (it.j0 == 0 ? 1 : 0);
   return it;
 }
 
