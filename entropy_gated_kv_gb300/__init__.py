@@ -107,6 +107,17 @@ class Params:
                           float(self.tau), _dtype_code(self.logits_dtype), float(self.conf_threshold),
                           int(self.scope_lo), int(self.scope_hi))
 
+    def ref(self):
+        """byref(c()), made once and again after a field has changed."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = self.__dict__["_ref"] = ctypes.byref(self.c())
+        return r
+
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_ref", None)
+        self.__dict__[name] = value
+
 
 class DecodeState:
     """Per-sequence decode state (ec_state) as CUDA tensors."""
@@ -288,37 +299,45 @@ def dense_attention(p: Params, q, k_cache, v_cache, out, scale: float | None = N
 # ---- 8-bit caches and shared prefixes ------------------------------------------------------------
 
 
-def _checked(t, name: str, dtype, shape: tuple, device):
-    """t, a contiguous CUDA tensor of that type, shape and device."""
-    if t.dtype is not dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on {device} (EntropyCache kernels take CUDA tensors of one device)")
-    if not t.is_contiguous():
+def _checked(t, name: str, dtype, shape: tuple, index: int) -> int:
+    """Address of t, a contiguous tensor of that type and shape on CUDA device `index`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}: EntropyCache kernels take CUDA tensors, all of one device")
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _cuda_index(t, name: str) -> int:
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} is on {t.device}: EntropyCache kernels take CUDA tensors (there is no CPU path)")
+    return i
 
 
 class _Cache:
     """The C view of one layer's cache (ec_kv) and the tensors that it points to."""
 
-    __slots__ = ("c", "ref", "shape", "device", "keep")
+    __slots__ = ("c", "ref", "shape", "index")
 
     def __init__(self, dtype, k, v, k_exp=None, v_exp=None):
         tdt = torch.float8_e4m3fn if dtype == C.EC_E4M3 else torch.bfloat16
-        self.shape, self.device = tuple(k.shape), k.device
-        kp = _checked(k, "k", tdt, self.shape, k.device)
-        vp = _checked(v, "v", tdt, self.shape, k.device)
+        self.shape, self.index = tuple(k.shape), _cuda_index(k, "k")
         if len(self.shape) != 4:
             raise ValueError(f"a cache is [B, L, Hkv, D], got {list(self.shape)}")
+        kp = _checked(k, "k", tdt, self.shape, self.index)
+        vp = _checked(v, "v", tdt, self.shape, self.index)
         ep = [None, None]
         if dtype == C.EC_E4M3:
+            if k_exp is None or v_exp is None:
+                raise ValueError("an 8-bit cache has exponent bytes k_exp and v_exp")
             B, L, H, _ = self.shape
-            ep = [_checked(e, n, torch.uint8, (B, H, -(-L // 16) * 16), k.device)
+            ep = [_checked(e, n, torch.uint8, (B, H, -(-L // 16) * 16), self.index)
                   for e, n in ((k_exp, "k_exp"), (v_exp, "v_exp"))]
         self.c = C.EcKv(dtype, self.shape[1], kp, vp, *ep)
         self.ref = ctypes.byref(self.c)
-        self.keep = (k, v, k_exp, v_exp)
 
 
 class QuantCache:
@@ -326,11 +345,20 @@ class QuantCache:
     k_exp, v_exp uint8 [B, Hkv, S], S = L rounded up to a multiple of 16. The row of position j
     and head h stands for k[b, j, h] * 2^(k_exp[b, h, j] - 127)."""
 
-    __slots__ = ("k", "v", "k_exp", "v_exp", "_view")
+    __slots__ = ("k", "v", "k_exp", "v_exp", "_c", "_at")
 
     def __init__(self, k, v, k_exp, v_exp):
-        self._view = _Cache(C.EC_E4M3, k, v, k_exp, v_exp)
+        self._c = _Cache(C.EC_E4M3, k, v, k_exp, v_exp)
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self._at = (k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr())
+
+    def view(self) -> _Cache:
+        """The checked C view; made again when a tensor has been exchanged or has moved."""
+        at = (self.k.data_ptr(), self.v.data_ptr(), self.k_exp.data_ptr(), self.v_exp.data_ptr())
+        if at != self._at:
+            self._c = _Cache(C.EC_E4M3, self.k, self.v, self.k_exp, self.v_exp)
+            self._at = at
+        return self._c
 
     @classmethod
     def empty(cls, B: int, L: int, Hkv: int, D: int, device="cuda") -> "QuantCache":
@@ -343,42 +371,29 @@ class QuantCache:
 
 def _cache_view(cache, ndim: int = 4) -> _Cache:
     if isinstance(cache, QuantCache):
-        return cache._view
+        return cache.view()
     k, v = cache
     if ndim == 3 and k.dim() == 3 and v.dim() == 3:  # a prefix: one sequence
         k, v = k.unsqueeze(0), v.unsqueeze(0)
     return _Cache(C.EC_BF16, k, v)
 
 
-class _on_device:
-    """Makes `device` and the caller's `stream` (None: the device's current one) current for a call,
-    where they are not already, so that what the call allocates belongs to the stream that it
-    launches on; gives that stream's handle."""
-
-    __slots__ = ("guard", "stream")
-
-    def __init__(self, device, stream):
-        self.guard = None
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            self.guard = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-        self.stream = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(index: int, stream, call):
+    """call(stream handle) with CUDA device `index` and the caller's `stream` (None: the device's
+    current one) current, so that what the call allocates belongs to the stream it launches on."""
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() == index:
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return call(torch._C._cuda_getCurrentRawStream(index))
 
 
-def _opt(t, name, dtype, shape, device):
-    return None if t is None else _checked(t, name, dtype, shape, device)
+def _opt(t, name, dtype, shape, index):
+    return None if t is None else _checked(t, name, dtype, shape, index)
 
 
 def _expect(view: _Cache, shape: tuple, what: str):
@@ -391,16 +406,17 @@ def kv_scatter_quant(p: Params, cache: QuantCache, k_new, v_new, idx, R, src_by_
     """(c) the refresh of an 8-bit cache: cache[b, idx[b, r]] = the row k_new[b, r or idx[b, r]],
     quantised (same for v), for r < R[b]. k_new, v_new bf16 [B, L, Hkv, D]; idx [B, L] (strictly
     ascending per sequence unless src_by_position) and R [B] int32. See ec_kv_scatter_quant."""
-    view, shape = cache._view, (p.B, p.L, p.Hkv, p.D)
-    dev = view.device
+    view, shape = cache.view(), (p.B, p.L, p.Hkv, p.D)
+    i = view.index
     _expect(view, shape, "cache")
-    kp = _checked(k_new, "k_new", torch.bfloat16, shape, dev)
-    vp = _checked(v_new, "v_new", torch.bfloat16, shape, dev)
-    ip = _checked(idx, "idx", torch.int32, (p.B, p.L), dev)
-    rp = _checked(R, "R", torch.int32, (p.B,), dev)
-    ep = _opt(dev_err, "dev_err", torch.int32, (1,), dev)
-    with _on_device(dev, stream) as s:
-        st = lib().ec_kv_scatter_quant(ctypes.byref(p.c()), view.ref, kp, vp, int(bool(src_by_position)), ip, rp, ep, s)
+    kp = _checked(k_new, "k_new", torch.bfloat16, shape, i)
+    vp = _checked(v_new, "v_new", torch.bfloat16, shape, i)
+    ip = _checked(idx, "idx", torch.int32, shape[:2], i)
+    rp = _checked(R, "R", torch.int32, shape[:1], i)
+    ep = _opt(dev_err, "dev_err", torch.int32, (1,), i)
+    by_pos = 1 if src_by_position else 0
+    f = lib().ec_kv_scatter_quant
+    st = _launch(i, stream, lambda s: f(p.ref(), view.ref, kp, vp, by_pos, ip, rp, ep, s))
     C.check(st, "ec_kv_scatter_quant")
 
 
@@ -408,56 +424,56 @@ def kv_gather_quant(p: Params, cache: QuantCache, idx, R, out: tuple | None = No
     """Rows of an 8-bit cache back as bf16: (k, v) with k[b, r] = cache row idx[b, r] for r < R[b]
     (idx None: row r). out: two bf16 tensors [B, L, Hkv, D], by default new ones whose other rows
     are zeros. See ec_kv_gather_quant."""
-    view, shape = cache._view, (p.B, p.L, p.Hkv, p.D)
-    dev = view.device
+    view, shape = cache.view(), (p.B, p.L, p.Hkv, p.D)
+    i = view.index
     _expect(view, shape, "cache")
-    ip = _opt(idx, "idx", torch.int32, (p.B, p.L), dev)
-    rp = _checked(R, "R", torch.int32, (p.B,), dev)
-    ep = _opt(dev_err, "dev_err", torch.int32, (1,), dev)
-    with _on_device(dev, stream) as s:
-        if out is None:
-            out = (torch.zeros(shape, dtype=torch.bfloat16, device=dev), torch.zeros(shape, dtype=torch.bfloat16, device=dev))
-        kp = _checked(out[0], "out[0]", torch.bfloat16, shape, dev)
-        vp = _checked(out[1], "out[1]", torch.bfloat16, shape, dev)
-        st = lib().ec_kv_gather_quant(ctypes.byref(p.c()), view.ref, ip, rp, kp, vp, ep, s)
-    C.check(st, "ec_kv_gather_quant")
-    return out
+    ip = _opt(idx, "idx", torch.int32, shape[:2], i)
+    rp = _checked(R, "R", torch.int32, shape[:1], i)
+    ep = _opt(dev_err, "dev_err", torch.int32, (1,), i)
+
+    def call(s):
+        k, v = out if out is not None else (torch.zeros(shape, dtype=torch.bfloat16, device=R.device) for _ in range(2))
+        kp = _checked(k, "out[0]", torch.bfloat16, shape, i)
+        vp = _checked(v, "out[1]", torch.bfloat16, shape, i)
+        C.check(lib().ec_kv_gather_quant(p.ref(), view.ref, ip, rp, kp, vp, ep, s), "ec_kv_gather_quant")
+        return k, v
+
+    return _launch(i, stream, call)
 
 
 def partial_attention_quant_workspace_size(p: Params) -> int:
-    return int(lib().ec_partial_attention_quant_workspace_size(ctypes.byref(p.c())))
+    return int(lib().ec_partial_attention_quant_workspace_size(p.ref()))
 
 
 def prefix_attention_workspace_size(p: Params) -> int:
-    return int(lib().ec_prefix_attention_workspace_size(ctypes.byref(p.c())))
+    return int(lib().ec_prefix_attention_workspace_size(p.ref()))
 
 
 def _attend(p: Params, q, prefix: _Cache | None, cache: _Cache, R, out, kv_len, scale, ws, dev_err, stream):
-    dev, shape = q.device, (p.B, p.L, p.Hq, p.D)
+    i, shape = _cuda_index(q, "q"), (p.B, p.L, p.Hq, p.D)
     _expect(cache, (p.B, p.L, p.Hkv, p.D), "cache")
-    qp = _checked(q, "q", torch.bfloat16, shape, dev)
-    op = _checked(out, "out", torch.bfloat16, shape, dev)
-    rp = _checked(R, "R", torch.int32, (p.B,), dev)
-    lp = _opt(kv_len, "kv_len", torch.int32, (p.B,), dev)
-    ep = _opt(dev_err, "dev_err", torch.int32, (1,), dev)
-    if cache.device != dev or (prefix is not None and prefix.device != dev):
-        raise ValueError(f"the caches must be on {dev}, as q is")
-    if ws is not None and (not ws.is_cuda or ws.device != dev or not ws.is_contiguous()):
-        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+    qp = _checked(q, "q", torch.bfloat16, shape, i)
+    op = _checked(out, "out", torch.bfloat16, shape, i)
+    rp = _checked(R, "R", torch.int32, shape[:1], i)
+    lp = _opt(kv_len, "kv_len", torch.int32, shape[:1], i)
+    ep = _opt(dev_err, "dev_err", torch.int32, (1,), i)
+    if cache.index != i or (prefix is not None and prefix.index != i):
+        raise ValueError(f"the caches must be on {q.device}, as q is")
+    if ws is not None and (ws.get_device() != i or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {q.device}")
     sc = (1.0 / math.sqrt(p.D)) if scale is None else float(scale)
-    pc = ctypes.byref(p.c())
-    with _on_device(dev, stream) as s:
+
+    def call(s):
+        w = ws
+        if w is None:
+            size = partial_attention_quant_workspace_size if prefix is None else prefix_attention_workspace_size
+            w = torch.empty(max(256, size(p)), dtype=torch.uint8, device=q.device)
+        nw = w.numel() * w.element_size()
         if prefix is None:
-            if ws is None:
-                ws = torch.empty(max(256, partial_attention_quant_workspace_size(p)), dtype=torch.uint8, device=dev)
-            st = lib().ec_partial_attention_quant(pc, qp, cache.ref, rp, lp, sc, op, ws.data_ptr(),
-                                                  ws.numel() * ws.element_size(), ep, s)
-        else:
-            if ws is None:
-                ws = torch.empty(max(256, prefix_attention_workspace_size(p)), dtype=torch.uint8, device=dev)
-            st = lib().ec_prefix_attention(pc, qp, prefix.ref, cache.ref, rp, lp, sc, op, ws.data_ptr(),
-                                           ws.numel() * ws.element_size(), ep, s)
-    C.check(st, "ec_partial_attention_quant" if prefix is None else "ec_prefix_attention")
+            return lib().ec_partial_attention_quant(p.ref(), qp, cache.ref, rp, lp, sc, op, w.data_ptr(), nw, ep, s)
+        return lib().ec_prefix_attention(p.ref(), qp, prefix.ref, cache.ref, rp, lp, sc, op, w.data_ptr(), nw, ep, s)
+
+    C.check(_launch(i, stream, call), "ec_partial_attention_quant" if prefix is None else "ec_prefix_attention")
     return out
 
 
@@ -466,7 +482,7 @@ def partial_attention_quant(p: Params, q, cache: QuantCache, R, out, kv_len=None
     """(d) against an 8-bit cache: out[b, r, h] = softmax(scale q k^T) v over the first kv_len[b]
     keys (None: the scope's), for r < R[b]; zeros without a key. q, out bf16 [B, L, Hq, D]; R,
     kv_len int32 [B]; scale > 0. See ec_partial_attention_quant."""
-    return _attend(p, q, None, cache._view, R, out, kv_len, scale, ws, dev_err, stream)
+    return _attend(p, q, None, cache.view(), R, out, kv_len, scale, ws, dev_err, stream)
 
 
 def prefix_attention(p: Params, q, prefix, cache, R, out, kv_len=None, scale: float | None = None,

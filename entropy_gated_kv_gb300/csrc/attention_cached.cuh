@@ -32,24 +32,6 @@ constexpr int kBlockM = 128;  // packed query rows per tile (TMEM lanes)
 constexpr int kBlockN = 128;  // keys per block
 constexpr int kTileCost = 3;  // blocks whose time a tile takes beside its own
 
-// Division of 0 <= x < 2^31 by a number that the host knows: a shift for a power of two, else
-// (x m) >> (31 + l) with l = ceil(log2 d), m = ceil(2^(31 + l) / d): m d - 2^(31 + l) < d <= 2^l, so
-// the quotient's error is below x / (d 2^31) < 1 / d, and its floor is exact.
-struct FastDiv {
-  uint32_t m;
-  int32_t shift;
-  void set(int32_t d) {
-    int l = 0;
-    while ((1ll << l) < d) ++l;
-    const bool pow2 = (1ll << l) == d;
-    m = pow2 ? 0u : static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
-    shift = pow2 ? l : l - 1;
-  }
-  EC_DEV int operator()(int x) const {
-    return static_cast<int>((m != 0u ? __umulhi(static_cast<uint32_t>(x), m) : static_cast<uint32_t>(x)) >> shift);
-  }
-};
-
 // Floor of x / d, 0 <= x < 2^31, quotients up to a few thousand: `inv` is 1 / d rounded, so the
 // product's floor is at most one off.
 EC_DEV int div_near(int x, int d, float inv) {

@@ -368,6 +368,8 @@ ec_status check_quant_rows(const ec_params* p, const ec_kv* c) {
   if (p == nullptr) return EC_ERR_INVALID_ARG;
   if (p->B < 1 || p->B > kMaxB || p->L < 1 || p->L > kMaxL || p->Hkv < 1 || p->Hkv > 65536) return EC_ERR_INVALID_ARG;
   if (p->D != 64 && p->D != 128) return EC_ERR_UNSUPPORTED;
+  // a sequence's rows are counted in 32 bits (more would not fit the device)
+  if (2ll * p->L * p->Hkv > INT32_MAX) return EC_ERR_UNSUPPORTED;
   const ec_status r = check_kv(c, p->L);
   if (r != EC_OK) return r;
   return c->dtype == EC_E4M3 ? EC_OK : EC_ERR_UNSUPPORTED;

@@ -302,3 +302,25 @@ EC_DEV void bulk_copy_s2cluster(uint32_t dst_cluster_addr, const void* src, uint
 }
 
 }  // namespace ec
+
+namespace ec {
+
+// Division of 0 <= x < 2^31 by a number that the host knows: a shift for a power of two, else
+// (x m) >> (31 + l) with l = ceil(log2 d), m = ceil(2^(31 + l) / d): m d - 2^(31 + l) < d <= 2^l, so
+// the quotient's error is below x / (d 2^31) < 1 / d, and its floor is exact.
+struct FastDiv {
+  uint32_t m;
+  int32_t shift;
+  void set(int32_t d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    const bool pow2 = (1ll << l) == d;
+    m = pow2 ? 0u : static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d);
+    shift = pow2 ? l : l - 1;
+  }
+  EC_DEV int operator()(int x) const {
+    return static_cast<int>((m != 0u ? __umulhi(static_cast<uint32_t>(x), m) : static_cast<uint32_t>(x)) >> shift);
+  }
+};
+
+}  // namespace ec

@@ -380,7 +380,7 @@ typedef struct ec_kv {
  * reported as bad leaves at such a position is unspecified). An idx outside [0, L) sets
  * EC_DEVERR_BAD_IDX and its row is skipped; R outside [0, L] sets EC_DEVERR_BAD_R and that
  * sequence is skipped. The four arrays of the cache must not overlap each other or the fresh
- * rows (EC_ERR_INVALID_ARG). Hkv <= 65536, D 64 or 128. */
+ * rows (EC_ERR_INVALID_ARG). Hkv <= 65536, D 64 or 128, 2 L Hkv < 2^31. */
 ec_status ec_kv_scatter_quant(const ec_params* p, const ec_kv* cache, const void* k_new, const void* v_new,
                               int32_t src_by_position, const int32_t* idx, const int32_t* R, int32_t* dev_err,
                               ec_stream_t stream);
