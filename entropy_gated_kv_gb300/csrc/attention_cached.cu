@@ -58,6 +58,7 @@ constexpr int kMaxRaw = 3;
 constexpr int kDequantWarps = 4;                  // per tile: four warps take the K tiles, four the V tiles
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 32;  // rows of a tile per merge CTA
+constexpr int kNarrow = 16;
 constexpr int kMergeSteps = kBlockM / kMergeRows;
 constexpr int kItems = 8;       // items handed out and not yet finished, see the producer
 constexpr int kCum = 32;        // sequences whose row ends are kept in shared memory
@@ -107,7 +108,8 @@ struct Args {
   float scale_log2;
   const uint16_t* q;
   uint16_t* out;
-  float4* part_o;     // [slots][D / 4][128]: four columns of a row, neighbouring rows side by side
+  float4* part_o;     // [slots][D / 4][128]: four columns of a row, neighbouring rows side by side, or
+                      // (a tile of kNarrow rows or fewer) [slots][128][D / 4], row by row
   float2* part_stat;  // [slots][128]: running maximum and sum
   Header* header;
   Record* records;    // [max(slots, ctas)]
@@ -163,28 +165,6 @@ EC_DEV uint32_t ld_shared8(uint32_t src) {
                  "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),  \
                  "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory")
 
-#define EC_TMEM_LD16(taddr, r)                                                                             \
-  asm volatile(                                                                                            \
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];" \
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),    \
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) \
-      : "r"(taddr))
-
-#define EC_TMEM_WAIT16(r)                                                                                  \
-  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                            \
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),       \
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),   \
-                 "+r"(r[14]), "+r"(r[15])::"memory")
-
-#define EC_TMEM_ST8(taddr, r)                                                                              \
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),      \
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])      \
-               : "memory")
-
-#define EC_TMEM_LDC EC_TMEM_LD32
-#define EC_TMEM_WAITC EC_TMEM_WAIT32
-constexpr int kChunk = 32;  // columns of S per load
-
 // Two fp32 lanes in one instruction.
 EC_DEV uint64_t pack_f32x2(float lo, float hi) {
   uint64_t r;
@@ -208,45 +188,40 @@ EC_DEV float max3(float a, float b, float c) {
   return r;
 }
 
-// Whole warp: where packed row x of the item's KV head lies in q, as (b L + r) Hq + h.
-EC_DEV int query_row(const Args& a, const int32_t* cum, const Item& it, int x) {
-  const Shape& s = a.s;
-  int b = it.b;
-  if (it.b < 0) {  // row x over all sequences: b is the number of sequences that end at or before it
-    int before = 0;
-    b = 0;
-    if (s.B <= kCum) {
+// Whole warp: the sequence that packed row x over all sequences belongs to; x becomes the row within
+// it. The sequence's number is that of the sequences that end at or before x.
+EC_DEV int owner_of(const Shape& s, const int32_t* cum, int& x) {
+  int b = 0, before = 0;
+  if (s.B <= kCum) {
 #pragma unroll 1
-      for (int i = 0; i < s.B; ++i) {
-        const int e = cum[i];
+    for (int i = 0; i < s.B; ++i) {
+      const int e = cum[i];
+      if (e <= x) {
+        b = i + 1;
+        before = e;
+      }
+    }
+  } else {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < s.B; b0 += 32) {
+      int32_t r, n;
+      load_seq(s, b0 + lane, r, n, nullptr, false);
+      const int incl = base + warp_inclusive(r * s.g);
+#pragma unroll 1
+      for (int i = 0; i < min(32, s.B - b0); ++i) {
+        const int e = __shfl_sync(0xffffffffu, incl, i);
         if (e <= x) {
-          b = i + 1;
+          b = b0 + i + 1;
           before = e;
         }
       }
-    } else {
-      const int lane = threadIdx.x & 31;
-      int base = 0;
-#pragma unroll 1
-      for (int b0 = 0; b0 < s.B; b0 += 32) {
-        int32_t r, n;
-        load_seq(s, b0 + lane, r, n, nullptr, false);
-        const int incl = base + warp_inclusive(r * s.g);
-#pragma unroll 1
-        for (int i = 0; i < min(32, s.B - b0); ++i) {
-          const int e = __shfl_sync(0xffffffffu, incl, i);
-          if (e <= x) {
-            b = b0 + i + 1;
-            before = e;
-          }
-        }
-        base = __shfl_sync(0xffffffffu, incl, 31);
-      }
+      base = __shfl_sync(0xffffffffu, incl, 31);
     }
-    x -= before;
   }
-  const int r = s.div_g(x);
-  return (b * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g);
+  x -= before;
+  return b;
 }
 
 // Keys of block j of the item that take part.
@@ -289,6 +264,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
+    prefetch_tmap(&a.tq);
     prefetch_tmap(&a.tk);
     prefetch_tmap(&a.tv);
   }
@@ -408,6 +384,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           h.shared = pl.shared;
           h.prefix_units = pl.nbp + kTileCost;
           h.nbp = pl.nbp;
+          h.rows = pl.rows;
           h.chunk = pl.chunk;
           h.ptiles_head = s.div_h(pl.ptiles);
           *a.header = h;
@@ -471,14 +448,29 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       for (int items = 0;; ++items) {
         const Item it = next_item(items);
         if (it.nblk == 0) break;
-        int at[4];
-#pragma unroll 1
+        // row x of KV head kvh lies in q at (b L + x / g) Hq + kvh g + x % g
+        int at[4], seq[4];
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int x = query_row(a, cum, it, it.row0 + min(4 * lane + i, it.nrows - 1));
-          at[0] = i == 0 ? x : at[0];
-          at[1] = i == 1 ? x : at[1];
-          at[2] = i == 2 ? x : at[2];
-          at[3] = x;
+          at[i] = it.row0 + min(4 * lane + i, it.nrows - 1);
+          seq[i] = it.b;
+        }
+        if (it.b < 0) {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            int x = i == 0 ? at[0] : i == 1 ? at[1] : i == 2 ? at[2] : at[3];
+            const int b = owner_of(s, cum, x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              at[k] = k == i ? x : at[k];
+              seq[k] = k == i ? b : seq[k];
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = s.div_g(at[i]);
+          at[i] += (seq[i] * s.L + r) * a.Hq + it.kvh * s.g - r * s.g;
         }
         if (items > 0 && !__all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1))) break;
         if (lane == 0) mbar_arrive_expect_tx(&bars->q_full, LY::kTileBytes);
@@ -523,58 +515,75 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         }
         if (live) {
           tc_fence_after();
-          // p = 2^(s scale log2(e) - m) for the row, m the running maximum so far (0 while no score
-          // was finite): one pass over S, P kept in registers, so that a row whose new maximum is
-          // above m by more than the threshold, or that has no m yet, can take S again
+          // The stream's first block of the item: its maximum is the first m (scale > 0 commutes
+          // with the maximum).
+          if (i == st) {
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int c = 0; c < kBlockN; c += 32) {
+              uint32_t x[32];
+              EC_TMEM_LD32(s_addr + c, x);
+              EC_TMEM_WAIT32(x);
+              if (c + 32 > nv) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (c + e >= nv) x[e] = __float_as_uint(-INFINITY);
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            }
+            m_used = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+          }
+          // p = 2^(s scale log2(e) - m), m the running maximum so far (0 while no score was finite),
+          // in one pass over S. P stays in registers: where a row's new maximum is above m by more
+          // than the threshold, or the first one, m is put right and S taken again.
           const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2);
           uint32_t pk[kBlockN / 2];
-          float sum = 0.f;
-          auto exponentials = [&](float neg_m) {  // fills pk and sum; returns the largest exponent
+          float sum, alpha = 1.f;
+          bool rescale = false;
+#pragma unroll 1
+          for (;;) {
+            const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
             const uint64_t neg_m2 = pack_f32x2(neg_m, neg_m);
             uint64_t sum2[2] = {0, 0};
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            uint32_t buf[2][kChunk];
-            EC_TMEM_LDC(s_addr, buf[0]);
+            uint32_t buf[2][32];
+            EC_TMEM_LD32(s_addr, buf[0]);
 #pragma unroll
-            for (int c = 0; c < kBlockN / kChunk; ++c) {
-              EC_TMEM_WAITC(buf[c & 1]);
-              if (c + 1 < kBlockN / kChunk) EC_TMEM_LDC(s_addr + (c + 1) * kChunk, buf[(c + 1) & 1]);
+            for (int c = 0; c < kBlockN / 32; ++c) {
+              EC_TMEM_WAIT32(buf[c & 1]);
+              if (c + 1 < kBlockN / 32) EC_TMEM_LD32(s_addr + (c + 1) * 32, buf[(c + 1) & 1]);
               uint32_t* x = buf[c & 1];
-              if (nv < kBlockN) {
+              if (c * 32 + 32 > nv) {
 #pragma unroll
-                for (int e = 0; e < kChunk; ++e)
-                  if (c * kChunk + e >= nv) x[e] = __float_as_uint(-INFINITY);
+                for (int e = 0; e < 32; ++e)
+                  if (c * 32 + e >= nv) x[e] = __float_as_uint(-INFINITY);
               }
 #pragma unroll
-              for (int e = 0; e < kChunk; e += 2) {
+              for (int e = 0; e < 32; e += 2) {
                 float p0, p1;
                 unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
                 m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], p0, p1);
                 p0 = ex2_approx(p0);
                 p1 = ex2_approx(p1);
                 sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
-                pk[(c * kChunk + e) >> 1] = pack_bf16x2(p0, p1);
+                pk[(c * 32 + e) >> 1] = pack_bf16x2(p0, p1);
               }
             }
             float lo, hi;
             unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
             sum = lo + hi;
-            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          };
-          float up = exponentials(m_used == -INFINITY ? 0.f : -m_used);
-          bool rescale = false;
-          float alpha = 1.f;
-          // no m yet: the first finite score of the row's blocks sets it
-          if (__any_sync(0xffffffffu, up > kRescaleLog2 || (m_used == -INFINITY && up > -INFINITY))) {
-            const float base = m_used == -INFINITY ? 0.f : m_used;
-            if (up > kRescaleLog2 || (m_used == -INFINITY && up > -INFINITY)) {
-              alpha = m_used == -INFINITY ? 0.f : ex2_approx(-up);
-              m_used = base + up;
-              l_sum *= alpha;
+            const float up = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));  // the new maximum less m
+            const bool above = up > (m_used == -INFINITY ? -INFINITY : kRescaleLog2);
+            if (!__any_sync(0xffffffffu, above)) break;
+            if (above) {
+              alpha *= m_used == -INFINITY ? 0.f : ex2_approx(-up);
+              m_used = m_used == -INFINITY ? up : m_used + up;
               rescale = i != st;
             }
-            exponentials(m_used == -INFINITY ? 0.f : -m_used);
           }
+          l_sum *= alpha;
           l_sum += sum;
 #pragma unroll
           for (int c = 0; c < 2; ++c) EC_TMEM_ST32(s_addr + c * 32, (pk + 32 * c));
@@ -624,12 +633,15 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         const bool valid = row < it.nrows;
         uint16_t* orow = nullptr;
         float4* prow = nullptr;
+        int pstep = 0;
         if (complete) {
           const int x = it.row0 + row, r = s.div_g(x);
           orow = a.out + static_cast<int64_t>((it.b * s.L + r) * a.Hq + it.kvh * s.g + (x - r * s.g)) * D + st * (D / 2);
         } else {
           const int at = it.slot * kBlockM + row;
-          prow = a.part_o + static_cast<int64_t>(it.slot * (D / 4) + st * (D / 8)) * kBlockM + row;
+          pstep = it.nrows <= kNarrow ? 1 : kBlockM;
+          prow = a.part_o + static_cast<int64_t>(it.slot) * (kBlockM * (D / 4)) + st * (D / 8) * pstep +
+                 row * (it.nrows <= kNarrow ? D / 4 : 1);
           if (st == 0 && valid) a.part_stat[at] = make_float2(M, L);
         }
 #pragma unroll 1
@@ -654,7 +666,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           } else if (valid) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              prow[(c * 8 + e) * kBlockM] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+              prow[(c * 8 + e) * pstep] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
           }
         }
         tc_fence_before();
@@ -752,7 +764,7 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
   pdl_wait();
   pdl_launch_dependents();
   const int4 h = __ldcg(reinterpret_cast<const int4*>(a.header));            // records, shared, prefix units, chunk
-  const int4 h2 = __ldcg(reinterpret_cast<const int4*>(a.header) + 1);       // ptiles_head, nbp
+  const int4 h2 = __ldcg(reinterpret_cast<const int4*>(a.header) + 1);       // ptiles_head, nbp, rows
   const bool shared = h.y != 0;
   const int row0 = (blockIdx.x & (kMergeSteps - 1)) * kMergeRows;
   for (int which = blockIdx.x / kMergeSteps; which < h.x; which += gridDim.x / kMergeSteps) {
@@ -762,8 +774,9 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
     if (rows <= 0) continue;
     // the partials of a row: n1 slots from a1 on at `lane1`, then every `step2`-th from a2 on
     const int step2 = shared ? 1 : 2;
-    auto row_parts = [&](int row, int& a1, int& n1, int& lane1) {
-      a1 = t1.x, n1 = 1, lane1 = row;
+    const bool narrow2 = t0.w <= kNarrow;
+    auto row_parts = [&](int row, int& a1, int& n1, int& lane1, bool& narrow1) {
+      a1 = t1.x, n1 = 1, lane1 = row, narrow1 = narrow2;
       if (shared) {  // the row's prefix tile, and the CTAs that its blocks fell to
         const int gp = t1.w + t0.z + row, pt = t0.y * h2.x + (gp >> 7), pu = pt * h.z;
         const float inv = __fdividef(1.f, static_cast<float>(h.w));
@@ -771,6 +784,7 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
         a1 = pt + c0;
         n1 = div_near(pu + h2.y - 1, h.w, inv) - c0 + 1;
         lane1 = gp & 127;
+        narrow1 = h2.z - (gp & ~127) <= kNarrow;
       }
     };
     auto out_row = [&](int row) {
@@ -778,11 +792,12 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
       return a.out + static_cast<int64_t>((t0.x * s.L + r) * a.Hq + t0.y * s.g + (x - r * s.g)) * D;
     };
     int a1, n1, lane1;
-    row_parts(row0, a1, n1, lane1);
+    bool narrow1;
+    row_parts(row0, a1, n1, lane1, narrow1);
     const int most = n1 + t1.z;
-    if (most <= 8) {
+    if (most <= 8 && rows > 8) {
       const int row = row0 + min(lane, rows - 1);
-      row_parts(row, a1, n1, lane1);
+      row_parts(row, a1, n1, lane1, narrow1);
       const int n = n1 + t1.z;
       auto at = [&](int i, int& slot, int& ln) {
         slot = i < n1 ? a1 + i : t1.y + (i - n1) * step2;
@@ -799,9 +814,11 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
           int slot, ln;
           at(min(i0 + u, n - 1), slot, ln);
           st[u] = __ldcg(a.part_stat + slot * kBlockM + ln);
-          const float4* src = a.part_o + static_cast<int64_t>(slot * kQuads + warp * kMine) * kBlockM + ln;
+          const bool nw = min(i0 + u, n - 1) < n1 ? narrow1 : narrow2;
+          const int qs = nw ? 1 : kBlockM;
+          const float4* src = a.part_o + static_cast<int64_t>(slot) * (kBlockM * kQuads) + warp * kMine * qs + ln * (nw ? kQuads : 1);
 #pragma unroll
-          for (int q = 0; q < kMine; ++q) x[u][q] = __ldcg(src + q * kBlockM);
+          for (int q = 0; q < kMine; ++q) x[u][q] = __ldcg(src + q * qs);
           if (i0 + u >= n) st[u].y = 0.f;
         }
 #pragma unroll
@@ -833,7 +850,7 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
       const bool together = most > 32;  // all warps on one row
 #pragma unroll 1
       for (int row = row0 + (together ? 0 : warp); row < row0 + rows; row += together ? 1 : kWarps) {
-        row_parts(row, a1, n1, lane1);
+        row_parts(row, a1, n1, lane1, narrow1);
         const int n = n1 + t1.z, step = together ? kWarps : 1;
         auto place = [&](int i, int& slot, int& ln) {
           slot = i < n1 ? a1 + i : t1.y + (i - n1) * step2;
@@ -849,7 +866,9 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
             int slot, ln;
             place(min(i0 + u * step, n - 1), slot, ln);
             st[u] = __ldcg(a.part_stat + slot * kBlockM + ln);
-            x[u] = __ldcg(a.part_o + static_cast<int64_t>(slot * kQuads + quad) * kBlockM + ln);
+            const bool nw = min(i0 + u * step, n - 1) < n1 ? narrow1 : narrow2;
+            x[u] = __ldcg(a.part_o + static_cast<int64_t>(slot) * (kBlockM * kQuads) +
+                          (nw ? ln * kQuads + quad : quad * kBlockM + ln));
             if (i0 + u * step >= n) st[u].y = 0.f;
           }
 #pragma unroll

@@ -87,7 +87,7 @@ struct Record {
 };
 struct Header {
   int32_t records, shared, prefix_units, chunk;  // units of a prefix tile, units of a CTA
-  int32_t ptiles_head, nbp, pad[2];              // prefix tiles of a KV head, blocks of each
+  int32_t ptiles_head, nbp, rows, pad;           // of a KV head: prefix tiles, blocks of each, packed rows
 };
 
 // Quotients of numbers below 2^31; the divisor's bits are few enough here that the hardware's own
