@@ -12,11 +12,12 @@
 // Structure (one CTA per SM; the work plan is attention_cached.cuh's):
 //   warp 0       makes the work plan, hands out the CTA's items, and is the TMA producer: K and V
 //                blocks of 128 keys.
-//   warps 1, 3   issue tcgen05.mma, each for one of two streams (below); warp 1 allocates 512 TMEM
-//                columns. One issuer for both has a block's four waits and two products in
-//                series (3150 cycles a bf16 block).
-//   warp 2       the query tile, four rows a TMA gather (a tile packs rows of any sequences, which no
-//                one tensor box covers).
+//   warp 1       allocates 512 TMEM columns and issues tcgen05.mma for two streams (below),
+//                whichever has its operands; no product of one lies between those of the other.
+//   warp 2       the query tiles of later items, four rows a TMA gather (a tile packs rows of any
+//                sequences, which no one tensor box covers). The gathers take 6000 cycles a tile, behind the
+//                products of the item before; the first item's tile, which nothing hides, is
+//                fetched by the softmax warps. Warp 3 has no work.
 //   warps 4..7   softmax of the CTA's even key blocks, warps 8..11 of the odd ones: two independent
 //                streams with their own S buffer, running maximum and sum, and O accumulator, joined
 //                once per item. One stream's softmax runs while the tensor cores work on the
@@ -25,10 +26,14 @@
 //                One TMEM lane (= one packed query row) per thread; online softmax in base 2 with a
 //                lazy rescale of O (only when the running maximum grows by more than 2^8); P in
 //                bf16 written back over the first half of the S buffer.
-//   warps 12..19 (8-bit cache) dequantise, four the K tiles and four the V tiles: the producer's TMA brings codes and exponent bytes into a
-//                raw ring, and these warps write the bf16 tiles that the products read. The
-//                dequantised values are exact in bf16, so the products are those of a bf16 cache
-//                with the same values.
+//   warps 12..19 (8-bit cache) dequantise, four the K tiles and four the V tiles: the producer's TMA
+//                brings the codes into a raw ring, and these warps write the bf16 tiles that the
+//                products read, each with the next tile's codes already in its registers. The dequantised values are exact in bf16, so the products are those of
+//                a bf16 cache with the same values. (Codes loaded from global memory into
+//                registers, without the ring: 180 us for 120 on the long case. The shared memory
+//                that the kernel takes leaves L1 little room for loads in flight.)
+// A waiter on an mbarrier sees a phase's parity only, so each follows every phase of what it waits for:
+// in both rings K and V have slots of their own.
 // Keys past a sequence's length may hold anything: their scores are replaced, and their V rows are
 // zeroed in shared memory (0 x NaN is NaN in a matrix product).
 // Partial items write fp32 rows, their maximum and their sum to the workspace; the merge kernel
@@ -54,13 +59,13 @@ constexpr float kRescaleLog2 = 8.f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per pipeline wait
 constexpr int kMaxCtas = 160;                     // bound of the attention grid, for the workspace
 constexpr int kMaxUnits = 6;                      // K or V tiles in shared memory
-constexpr int kMaxRaw = 3;
+constexpr int kMaxRaw = 4;
 constexpr int kDequantWarps = 4;                  // per tile: four warps take the K tiles, four the V tiles
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 32;  // rows of a tile per merge CTA
 constexpr int kNarrow = 16;
 constexpr int kMergeSteps = kBlockM / kMergeRows;
-constexpr int kItems = 8;       // items handed out and not yet finished, see the producer
+constexpr int kItems = 4;       // items handed out and not yet finished, see the producer
 constexpr int kCum = 32;        // sequences whose row ends are kept in shared memory
 constexpr uint32_t kDescHi = sdesc_hi(1024);
 constexpr int kAtomBytes = 128 * 128;  // 128 rows x 128 bytes (64 bf16), 128-byte swizzle
@@ -68,26 +73,26 @@ __host__ __device__ constexpr uint32_t step_qk(int kk) { return (kk >> 2) * (kAt
 constexpr uint32_t kStepPV = 16 * 128 / 16;
 
 struct Bars {
-  uint64_t q_full, q_empty;
+  uint64_t q_first, q_full, q_empty;  // q_first: the first item's queries
   uint64_t unit_full[kMaxUnits], unit_empty[kMaxUnits];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t join, o_free;
-  uint64_t item_full[kItems];
+  uint64_t join, o_free, v_here[2];  // v_here: a stream's V tile with rows to be zeroed has come
+  uint64_t item_full[kItems], item_empty[kItems];
   uint32_t tmem_base;
   int abort;
 };
 
 // Shared memory: the query tile, a ring of bf16 tiles (K and V of a block in turn), for the 8-bit
-// cache a ring of raw tiles (128 rows of codes, then 128 exponent bytes), the row statistics that
-// the two streams exchange, the items, where each sequence's packed rows end, the barriers.
+// cache a ring of raw tiles (128 rows of codes), the row statistics that the two streams exchange,
+// the items, where each sequence's packed rows end, the barriers.
 template <int D, bool Q8>
 struct Layout {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;
   static constexpr int kUnits = Q8 ? 4 : 6;
   static constexpr int kRaw = Q8 ? kMaxRaw : 0;
-  static constexpr int kRawBytes = 128 * D + 128;
+  static constexpr int kRawBytes = 128 * D;
   static constexpr int kUnitOff = kTileBytes;
   static constexpr int kRawOff = kUnitOff + kUnits * kTileBytes;
   static constexpr int kStatOff = kRawOff + kRaw * kRawBytes;
@@ -102,7 +107,7 @@ struct Layout {
 struct Args {
   CUtensorMap tq;                // rows of q
   CUtensorMap tk, tv, tpk, tpv;  // own and prefix caches
-  const uint8_t *ke, *ve, *pke, *pve;
+  const uint8_t *exps[2], *pexps[2];  // 8-bit: exponents of K and V, own and prefix
   Shape s;
   int32_t Hq, Ls, Lps;
   float scale_log2;
@@ -116,11 +121,22 @@ struct Args {
   int32_t* dev_err;
 };
 
-EC_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+EC_DEV void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+EC_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Whether the phase of the given parity is complete; returns at once.
+EC_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Four rows of a matrix, 64 elements from column x on, below one another.
@@ -149,12 +165,6 @@ EC_DEV uint4 ld_shared16(uint32_t src) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
   return v;
 }
-EC_DEV uint32_t ld_shared8(uint32_t src) {
-  uint32_t v;
-  asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u8 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(v) : "r"(src) : "memory");
-  return v;
-}
-
 // tcgen05.wait::ld that also names the loaded registers, so that no use of them moves before it
 // while other loads are in flight.
 #define EC_TMEM_WAIT32(r)                                                                                    \
@@ -240,8 +250,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    mbar_init(&bars->q_first, 256);
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 2);
+    mbar_init(&bars->q_empty, 1);
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&bars->unit_full[i], Q8 ? kDequantWarps : 1);
       mbar_init(&bars->unit_empty[i], 1);
@@ -257,7 +268,12 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     }
     mbar_init(&bars->join, 8);
     mbar_init(&bars->o_free, 8);
-    for (int i = 0; i < kItems; ++i) mbar_init(&bars->item_full[i], 1);
+    mbar_init(&bars->v_here[0], 1);
+    mbar_init(&bars->v_here[1], 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], 8);
+    }
     // the swizzled tiles need the 1024-byte alignment that dynamic shared memory has here
     bars->abort = (smem_u32(smem) & 1023u) != 0u;
     if (bars->abort) report_error(a.dev_err, EC_DEVERR_TIMEOUT);
@@ -295,6 +311,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     return it;
   };
 
+  // Block j of the item has rows past the sequence's length (a map zero-fills only past the cache's end).
+  auto ragged = [&](const Item& it, int j) { return j >= it.np && valid_keys(s, it, j) < kBlockN; };
+
   // With 20 warps a thread is launched with 96 registers; the softmax warps hold a row of P and take
   // 144, the others go down to 64: 128 x 64 + 256 x 144 + 256 x 64 = 640 x 96.
   if (warp < 4) {
@@ -322,13 +341,12 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           it = cta_item(s, pl, u, uend, cta, span);
           u += span;
         }
-        // Slot count % kItems is free: it held item count - 8, and with that one's epilogue still to come
-        // no V tile of the item after it can have been released, so that the producer would be
-        // waiting for room at the latest with the fifth item after it.
         if (lane == 0) {
+          if (!wait(&bars->item_empty[count % kItems], ((count / kItems) & 1) ^ 1)) it.nblk = 0;
           items_s[count % kItems] = it;
           mbar_arrive(&bars->item_full[count % kItems]);
         }
+        it.nblk = __shfl_sync(0xffffffffu, it.nblk, 0);
         if (it.nblk == 0) break;
         if (it.slot >= 0 && it.j0 == 0 && it.b >= 0) {
           rec.b = it.b;
@@ -354,14 +372,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
                 const uint32_t slot = n % LY::kRaw;
                 if (!(ok = wait(&bars->raw_empty[slot], ((n / LY::kRaw) & 1u) ^ 1u))) break;
                 uint8_t* dst = smem + LY::kRawOff + slot * LY::kRawBytes;
-                // exponent rows are padded to 16 positions: the copy stays inside its row
-                const int ls = pre ? a.Lps : a.Ls;
-                const uint32_t ne = static_cast<uint32_t>(min(kBlockN, ls - key0));
-                const uint8_t* exps = (kv == 0 ? (pre ? a.pke : a.ke) : (pre ? a.pve : a.ve)) +
-                                      (static_cast<int64_t>(b) * s.Hkv + it.kvh) * ls + key0;
-                mbar_arrive_expect_tx(&bars->raw_full[slot], 128 * D + ne);
+                mbar_arrive_expect_tx(&bars->raw_full[slot], LY::kRawBytes);
                 tma_load_4d(dst, map, &bars->raw_full[slot], 0, it.kvh, key0, b);
-                bulk_load(dst + 128 * D, exps, ne, &bars->raw_full[slot]);
               } else {
                 const uint32_t slot = n % kUnits;
                 if (!(ok = wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u))) break;
@@ -390,53 +402,79 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           *a.header = h;
         }
       }
-    } else if (warp == 1 || warp == 3) {
-      // ------------------------------------------------------------------ MMA issuer of one stream
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ MMA issuer
       constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlockN, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
-      const int st = warp >> 1;
-      const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16);
-      const uint32_t s_col = tmem + st * kBlockN, o_col = tmem + kTmemO + st * 128;
-      uint32_t n0 = 0, used = 0;  // tiles of the items before; products finished or under way in this stream
+      const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16), unit0 = smem_u32(smem + LY::kUnitOff);
+      uint32_t n0 = 0;            // tiles of the items before
+      uint32_t used[2] = {0, 0};  // P V products under way or done, per stream
       int ok = 1;
       for (int items = 0; ok; ++items) {
         const Item it = next_item(items);
         if (it.nblk == 0) break;
         if (lane == 0) {
-          auto issue_qk = [&](int i) {  // S of block i
-            const uint32_t n = n0 + 2 * i, slot = n % kUnits;
-            // the buffer's last P has been read
-            if (!wait(&bars->unit_full[slot], (n / kUnits) & 1u) || (used != 0 && !wait(&bars->pv_done[st], (used - 1) & 1u)))
-              return 0;
-            tc_fence_after();
-            const uint32_t k_lo = sdesc_lo(smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes), 16);
+          ok = items == 0 ? wait(&bars->q_first, 0) : wait(&bars->q_full, (items - 1) & 1);
+          // Per stream, in turn: S of its next block (the buffer's last P has been read, and K is here), then
+          // O += P V (P and V are here; the item's first one once O has been read out).
+          int blk[2] = {0, 1}, s_left = it.nblk, pv_left = it.nblk;
+          bool want_pv[2] = {false, false}, told[2] = {false, false};
+          uint64_t t0 = 0;
+          for (uint32_t idle = 0; ok && pv_left > 0;) {
+            bool issued = false;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
-            umma_commit(&bars->s_full[st]);
-            umma_commit(&bars->unit_empty[slot]);
-            return 1;
-          };
-          ok = wait(&bars->q_full, items & 1);
-          if (ok && st < it.nblk) ok = issue_qk(st);
-          for (int i = st; ok && i < it.nblk; i += 2) {
-            if (i + 2 >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last S of the item is under way
-            const uint32_t n = n0 + 2 * i + 1, slot = n % kUnits;
-            if (i == st && items > 0) ok = wait(&bars->o_free, (items - 1) & 1);
-            ok = ok && wait(&bars->unit_full[slot], (n / kUnits) & 1u) && wait(&bars->p_full[st], used & 1u);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v_lo = sdesc_lo(smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes), kAtomBytes);
-            const uint32_t acc0 = i > 1 ? 1u : 0u;  // the stream's first block of the item starts O anew
+            for (int st = 0; st < 2; ++st) {
+              if (blk[st] >= it.nblk) continue;
+              const uint32_t n = n0 + 2 * blk[st] + (want_pv[st] ? 1 : 0), slot = n % kUnits;
+              const uint32_t s_col = tmem + st * kBlockN, o_col = tmem + kTmemO + st * 128;
+              if (!mbar_test(&bars->unit_full[slot], (n / kUnits) & 1u)) continue;
+              if (!want_pv[st]) {
+                if (used[st] != 0 && !mbar_test(&bars->pv_done[st], (used[st] - 1) & 1u)) continue;
+                tc_fence_after();
+                const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, 16);
 #pragma unroll
-            for (int kk = 0; kk < kBlockN / 16; ++kk)
-              umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
-            umma_commit(&bars->pv_done[st]);
-            umma_commit(&bars->unit_empty[slot]);
-            ++used;
-            if (i + 2 < it.nblk) ok = issue_qk(i + 2);
+                for (int kk = 0; kk < D / 16; ++kk)
+                  umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+                umma_commit(&bars->s_full[st]);
+                umma_commit(&bars->unit_empty[slot]);
+                if (--s_left == 0) umma_commit(&bars->q_empty);
+                want_pv[st] = true;
+              } else {
+                if constexpr (!Q8) {
+                  if (!told[st] && ragged(it, it.j0 + blk[st])) mbar_arrive(&bars->v_here[st]);
+                  told[st] = true;
+                }
+                if (!mbar_test(&bars->p_full[st], used[st] & 1u)) continue;
+                if (blk[st] == st && items > 0 && !mbar_test(&bars->o_free, (items - 1) & 1)) continue;
+                tc_fence_after();
+                const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, kAtomBytes);
+                const uint32_t acc0 = blk[st] > 1 ? 1u : 0u;  // the stream's first block of the item starts O anew
+#pragma unroll
+                for (int kk = 0; kk < kBlockN / 16; ++kk)
+                  umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
+                umma_commit(&bars->pv_done[st]);
+                umma_commit(&bars->unit_empty[slot]);
+                ++used[st];
+                --pv_left;
+                blk[st] += 2;
+                want_pv[st] = told[st] = false;
+              }
+              issued = true;
+            }
+            // as mbar_wait_bounded, over all that is waited for here
+            if (issued) {
+              idle = 0;
+            } else if ((++idle & 255u) == 0u) {
+              const uint64_t now = global_timer_ns();
+              if (idle == 256u) t0 = now;
+              if (*abort_flag) ok = 0;
+              if (now - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                report_error(a.dev_err, EC_DEVERR_TIMEOUT);
+                ok = 0;
+              }
+            }
           }
-          if (ok && st >= it.nblk) mbar_arrive(&bars->q_empty);  // nothing of this item falls to stream 1
         }
         n0 += 2 * it.nblk;
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -448,6 +486,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       for (int items = 0;; ++items) {
         const Item it = next_item(items);
         if (it.nblk == 0) break;
+        if (items == 0) continue;
         // row x of KV head kvh lies in q at (b L + x / g) Hq + kvh g + x % g
         int at[4], seq[4];
 #pragma unroll
@@ -472,7 +511,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           const int r = s.div_g(at[i]);
           at[i] += (seq[i] * s.L + r) * a.Hq + it.kvh * s.g - r * s.g;
         }
-        if (items > 0 && !__all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1))) break;
+        if (!__all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1))) break;
         if (lane == 0) mbar_arrive_expect_tx(&bars->q_full, LY::kTileBytes);
         __syncwarp();
 #pragma unroll
@@ -489,22 +528,40 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     const uint32_t s_addr = tmem + lane_off + st * kBlockN;
     float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
     uint32_t n0 = 0;                    // tiles of the items before
-    uint32_t used = 0, used_other = 0;  // blocks of this stream and of the other one
+    uint32_t used = 0, n_ragged = 0;    // blocks of this stream, and those with rows past a length
     bool ok = true;
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
       const bool live = 32 * (warp & 3) < it.nrows;  // else the warp's rows are all padding
+      if (items == 0) {
+        // the first query tile, 16 rows a warp: each lane finds one row, 16-byte pieces by all
+        constexpr int kPieces = D / 8, kStep = 32 / kPieces;
+        const int base = 16 * (warp - 4), piece = lane % kPieces;
+        int x = it.row0 + min(base + (lane & 15), it.nrows - 1), b = it.b;
+        if (b < 0) b = owner_of(s, reinterpret_cast<const int32_t*>(smem + LY::kCumOff), x);
+        const int r = s.div_g(x);
+        const int at = x + (b * s.L + r) * a.Hq + it.kvh * s.g - r * s.g;
+#pragma unroll 4
+        for (int i = lane / kPieces; i < 16; i += kStep) {
+          const int64_t src = __shfl_sync(0xffffffffu, at, i);
+          const int q_row = base + i;
+          cp_async16(smem_u32(smem) + (piece >> 3) * kAtomBytes + q_row * 128 + (((piece & 7) ^ (q_row & 7)) << 4),
+                     a.q + src * D + piece * 8);
+        }
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->q_first);
+      }
       float m_used = -INFINITY, l_sum = 0.f;
       for (int i = st; i < it.nblk; i += 2, ++used) {
         ok = __all_sync(0xffffffffu, wait(&bars->s_full[st], used & 1u));
         if (!ok) break;
         const int nv = valid_keys(s, it, it.j0 + i);
         if constexpr (!Q8) {
-          // V rows past the sequence's length (the map zero-fills only past the cache's end)
-          if (nv < kBlockN && it.j0 + i >= it.np) {
-            const uint32_t n = n0 + 2 * i + 1, slot = n % kUnits;
-            ok = __all_sync(0xffffffffu, wait(&bars->unit_full[slot], (n / kUnits) & 1u));
+          if (ragged(it, it.j0 + i)) {  // their V rows become zeros
+            const uint32_t slot = (n0 + 2 * i + 1) % kUnits;
+            ok = __all_sync(0xffffffffu, wait(&bars->v_here[st], n_ragged++ & 1u));
             if (!ok) break;
             const uint32_t v_tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes);
             for (int e = nv * 8 + row; e < kBlockN * 8; e += 128)
@@ -606,13 +663,10 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         if (lane == 0) mbar_arrive(&bars->p_full[st]);
       }
       // join the two streams: each warpgroup takes half of the columns of both accumulators
-      const int n_mine = (it.nblk + 1 - st) >> 1, n_other = it.nblk - n_mine;
-      used_other += n_other;
       n0 += 2 * it.nblk;
-      if (ok && n_mine > 0) ok = wait(&bars->pv_done[st], (used - 1) & 1u);
-      if (ok && n_other > 0) ok = wait(&bars->pv_done[st ^ 1], (used_other - 1) & 1u);
-      // this item's products began after every warp was done with the item before (o_free), so its
-      // statistics may be overwritten
+      if (ok && st < it.nblk) ok = wait(&bars->pv_done[st], (used - 1) & 1u);
+      // every warp is done with the item before, so its statistics may be overwritten
+      if (ok && items > 0) ok = wait(&bars->o_free, (items - 1) & 1);
       stat[st * kBlockM + row] = make_float2(m_used, l_sum);
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&bars->join);
@@ -672,66 +726,94 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->o_free);
+      if (lane == 0) {
+        mbar_arrive(&bars->o_free);
+        mbar_arrive(&bars->item_empty[items % kItems]);
+      }
     }
   } else if constexpr (Q8) {
     // ------------------------------------------------------------------ dequantisation
     setmaxnreg_dec<64>();
-    // Eight lanes read 128 neighbouring bytes of codes; the 16-byte pieces of bf16 that they
-    // store fall into eight different bank groups: for D = 128 lanes 0..3 take the first half of
-    // row r and lanes 4..7 the second half of row r ^ 1, whose swizzle differs in the lowest bit.
-    // A thread's rows differ by multiples of 8, so its places in the swizzle are the same in all.
-    constexpr int kPieces = D / 16;  // 16-code pieces of a row
-    constexpr int kRowsStep = 128 / kPieces;
-    const int kv = warp >= 16;
-    const int t = threadIdx.x & 127, piece = t % kPieces;
-    const int row0 = D == 128 ? (t / kPieces) ^ (piece >> 2) : t / kPieces;
-    const uint32_t src_off = row0 * D + piece * 16, exp_off = 128 * D + row0;
+    // A thread takes a 16-code piece of kPieces rows: eight lanes read 128 neighbouring bytes, and the
+    // 16-byte pieces of bf16 that they store fall into eight different bank groups: for D = 128
+    // lanes 0..3 take the first half of row r and lanes 4..7 the second half of row r ^ 1, whose
+    // swizzle differs in the lowest bit. A thread's rows differ by multiples of 8, so its places in
+    // the swizzle are the same in all. Each lane loads the exponent byte of one of its warp's 32 rows.
+    constexpr int kPieces = D / 16;            // 16-code pieces of a row = steps over the tile's rows
+    constexpr int kRowsStep = 128 / kPieces;   // rows of a step
+    constexpr int kRowsWarp = 32 / kPieces;    // of a warp
+    const int kv = warp >= 16, w4 = warp & 3, piece = lane % kPieces;
+    const int sub = D == 128 ? (lane / kPieces) ^ (piece >> 2) : lane / kPieces;  // row of the warp's
+    const int row0 = w4 * kRowsWarp + sub;
+    const int exp_row = (lane / kRowsWarp) * kRowsStep + w4 * kRowsWarp + lane % kRowsWarp;
+    const uint32_t src_off = row0 * D + piece * 16;
     const uint32_t dst_off = (piece >> 2) * kAtomBytes + row0 * 128 + ((((piece & 3) * 2) ^ (row0 & 7)) << 4);
     uint32_t n = kv;
     bool ok = true;
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
+      uint4 w[kPieces];
+      int e_next = 0;
+      auto raw_wait = [&](uint32_t m) {  // tile m of the CTA is in the raw ring
+        return __all_sync(0xffffffffu, wait(&bars->raw_full[m % LY::kRaw], (m / LY::kRaw) & 1u)) != 0;
+      };
+      auto raw_at = [&](uint32_t m) { return smem_u32(smem + LY::kRawOff + (m % LY::kRaw) * LY::kRawBytes); };
+      auto raw_done = [&](uint32_t m) {  // it has been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->raw_empty[m % LY::kRaw]);
+      };
+      auto exponent = [&](int j) {  // of this lane's row of block j (past the cache's end: any)
+        const bool pre = j < it.np;
+        const int key = (pre ? j : j - it.np) * kBlockN + exp_row, b = pre ? 0 : it.b;
+        return key < (pre ? s.Lp : s.L) ? static_cast<int>(__ldg((pre ? a.pexps : a.exps)[kv] +
+                                                                 (static_cast<int64_t>(b) * s.Hkv + it.kvh) * (pre ? a.Lps : a.Ls) + key))
+                                        : kExpZeroByte;
+      };
+      e_next = exponent(it.j0);
+      ok = raw_wait(n);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) w[i] = ld_shared16(raw_at(n) + src_off + i * kRowsStep * D);
+      raw_done(n);
       for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j, n += 2) {
         const int nv = kv ? valid_keys(s, it, j) : kBlockN;
-        const uint32_t rs = n % LY::kRaw, slot = n % kUnits;
-        ok = __all_sync(0xffffffffu, wait(&bars->raw_full[rs], (n / LY::kRaw) & 1u) &&
-                                         wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u));
+        const int e_here = e_next;
+        const bool more = j + 1 < it.j0 + it.nblk;
+        if (more) e_next = exponent(j + 1);
+        const uint32_t slot = n % kUnits;
+        ok = __all_sync(0xffffffffu, wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u));
+        if (ok && more) ok = raw_wait(n + 2);
         if (!ok) break;
-        const uint32_t raw = smem_u32(smem + LY::kRawOff + rs * LY::kRawBytes);
         const uint32_t tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes) + dst_off;
-#pragma unroll 4
+        const uint32_t raw = raw_at(n + 2);
+#pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          uint4 w = ld_shared16(raw + src_off + i * kRowsStep * D);
-          int byte = static_cast<int>(ld_shared8(raw + exp_off + i * kRowsStep));
-          if (row0 + i * kRowsStep >= nv) {  // V rows past the length: zeros, whatever lies there
-            w = make_uint4(0, 0, 0, 0);
-            byte = kExpZeroByte;
-          }
+          const int byte = __shfl_sync(0xffffffffu, e_here, i * kRowsWarp + sub);
           uint4 lo, hi;
           if (byte <= kExpOneFactor) {
             const uint32_t f = dequant_factor(byte);
-            dequantise4(w.x, f, lo.x, lo.y);
-            dequantise4(w.y, f, lo.z, lo.w);
-            dequantise4(w.z, f, hi.x, hi.y);
-            dequantise4(w.w, f, hi.z, hi.w);
+            dequantise4(w[i].x, f, lo.x, lo.y);
+            dequantise4(w[i].y, f, lo.z, lo.w);
+            dequantise4(w[i].z, f, hi.x, hi.y);
+            dequantise4(w[i].w, f, hi.z, hi.w);
           } else {
             const DequantScale sc = dequant_scale(byte);
-            dequantise4(w.x, sc, lo.x, lo.y);
-            dequantise4(w.y, sc, lo.z, lo.w);
-            dequantise4(w.z, sc, hi.x, hi.y);
-            dequantise4(w.w, sc, hi.z, hi.w);
+            dequantise4(w[i].x, sc, lo.x, lo.y);
+            dequantise4(w[i].y, sc, lo.z, lo.w);
+            dequantise4(w[i].z, sc, hi.x, hi.y);
+            dequantise4(w[i].w, sc, hi.z, hi.w);
           }
+          // V rows past the length: zeros, whatever lies there
+          if (row0 + i * kRowsStep >= nv) lo = hi = make_uint4(0, 0, 0, 0);
           st_shared16(tile + i * kRowsStep * 128, lo);
           st_shared16((tile + i * kRowsStep * 128) ^ 16u, hi);
+          if (more) w[i] = ld_shared16(raw + src_off + i * kRowsStep * D);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->raw_empty[rs]);
-          mbar_arrive(&bars->unit_full[slot]);
-        }
+        if (lane == 0) mbar_arrive(&bars->unit_full[slot]);
+        if (more) raw_done(n + 2);
       }
     }
   }
@@ -1014,10 +1096,10 @@ cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_
     *status = EC_ERR_INVALID_ARG;
     return cudaErrorInvalidValue;
   }
-  a.ke = cache.k_exp;
-  a.ve = cache.v_exp;
-  a.pke = pc.k_exp;
-  a.pve = pc.v_exp;
+  a.exps[0] = cache.k_exp;
+  a.exps[1] = cache.v_exp;
+  a.pexps[0] = pc.k_exp;
+  a.pexps[1] = pc.v_exp;
   a.s.R = R;
   a.s.kv_len = kv_len;
   a.s.B = p.B;
