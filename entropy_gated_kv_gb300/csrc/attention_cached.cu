@@ -28,7 +28,7 @@
 //                bf16 written back over the first half of the S buffer.
 //   warps 12..19 (8-bit cache) dequantise, four the K tiles and four the V tiles: the producer's TMA
 //                brings the codes into a raw ring, and these warps write the bf16 tiles that the
-//                products read, each with the next tile's codes already in its registers. The dequantised values are exact in bf16, so the products are those of
+//                products read. The dequantised values are exact in bf16, so the products are those of
 //                a bf16 cache with the same values. (Codes loaded from global memory into
 //                registers, without the ring: 180 us for 120 on the long case. The shared memory
 //                that the kernel takes leaves L1 little room for loads in flight.)
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
       const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16), unit0 = smem_u32(smem + LY::kUnitOff);
       uint32_t n0 = 0;            // tiles of the items before
-      uint32_t used[2] = {0, 0};  // P V products under way or done, per stream
+      uint32_t used0 = 0, used1 = 0;  // P V products under way or done, per stream
       int ok = 1;
       for (int items = 0; ok; ++items) {
         const Item it = next_item(items);
@@ -417,56 +417,59 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           ok = items == 0 ? wait(&bars->q_first, 0) : wait(&bars->q_full, (items - 1) & 1);
           // Per stream, in turn: S of its next block (the buffer's last P has been read, and K is here), then
           // O += P V (P and V are here; the item's first one once O has been read out).
-          int blk[2] = {0, 1}, s_left = it.nblk, pv_left = it.nblk;
-          bool want_pv[2] = {false, false}, told[2] = {false, false};
+          // One copy of the code serves both: the streams change places after every look.
+          struct Stream {
+            int st, blk;    // stream, its block of the item
+            bool pv, told;  // what is next is P V; its V tile's coming has been told
+          } x = {0, 0, false, false}, y = {1, 1, false, false};
+          int s_left = it.nblk, pv_left = it.nblk;
           uint64_t t0 = 0;
-          for (uint32_t idle = 0; ok && pv_left > 0;) {
-            bool issued = false;
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-              if (blk[st] >= it.nblk) continue;
-              const uint32_t n = n0 + 2 * blk[st] + (want_pv[st] ? 1 : 0), slot = n % kUnits;
-              const uint32_t s_col = tmem + st * kBlockN, o_col = tmem + kTmemO + st * 128;
-              if (!mbar_test(&bars->unit_full[slot], (n / kUnits) & 1u)) continue;
-              if (!want_pv[st]) {
-                if (used[st] != 0 && !mbar_test(&bars->pv_done[st], (used[st] - 1) & 1u)) continue;
-                tc_fence_after();
-                const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, 16);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                  umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
-                umma_commit(&bars->s_full[st]);
-                umma_commit(&bars->unit_empty[slot]);
-                if (--s_left == 0) umma_commit(&bars->q_empty);
-                want_pv[st] = true;
-              } else {
-                if constexpr (!Q8) {
-                  if (!told[st] && ragged(it, it.j0 + blk[st])) mbar_arrive(&bars->v_here[st]);
-                  told[st] = true;
+#pragma unroll 1
+          for (uint32_t idle = 1; ok && pv_left > 0; ++idle) {
+            const uint32_t st = x.st, done = st ? used1 : used0;
+            const uint32_t n = n0 + 2 * x.blk + (x.pv ? 1 : 0), slot = n % kUnits;
+            const uint32_t tile = sdesc_lo(unit0 + slot * LY::kTileBytes, x.pv ? kAtomBytes : 16);
+            const uint32_t s_col = tmem + st * kBlockN, o_col = tmem + kTmemO + st * 128;
+            if (x.blk < it.nblk && mbar_test(&bars->unit_full[slot], (n / kUnits) & 1u)) {
+              if (!x.pv) {
+                if (done == 0 || mbar_test(&bars->pv_done[st], (done - 1) & 1u)) {
+                  tc_fence_after();
+#pragma unroll 2
+                  for (int kk = 0; kk < D / 16; ++kk)
+                    umma_ss(s_col, q_lo + step_qk(kk), tile + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+                  umma_commit(&bars->s_full[st]);
+                  umma_commit(&bars->unit_empty[slot]);
+                  if (--s_left == 0) umma_commit(&bars->q_empty);
+                  x.pv = true;
+                  idle = 0;
                 }
-                if (!mbar_test(&bars->p_full[st], used[st] & 1u)) continue;
-                if (blk[st] == st && items > 0 && !mbar_test(&bars->o_free, (items - 1) & 1)) continue;
-                tc_fence_after();
-                const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, kAtomBytes);
-                const uint32_t acc0 = blk[st] > 1 ? 1u : 0u;  // the stream's first block of the item starts O anew
-#pragma unroll
-                for (int kk = 0; kk < kBlockN / 16; ++kk)
-                  umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
-                umma_commit(&bars->pv_done[st]);
-                umma_commit(&bars->unit_empty[slot]);
-                ++used[st];
-                --pv_left;
-                blk[st] += 2;
-                want_pv[st] = told[st] = false;
+              } else {
+                if (!Q8 && !x.told && ragged(it, it.j0 + x.blk)) mbar_arrive(&bars->v_here[st]);
+                x.told = true;
+                if (mbar_test(&bars->p_full[st], done & 1u) &&
+                    (x.blk > 1 || items == 0 || mbar_test(&bars->o_free, (items - 1) & 1))) {
+                  tc_fence_after();
+                  // the stream's first block of the item starts O anew
+#pragma unroll 2
+                  for (int kk = 0; kk < kBlockN / 16; ++kk)
+                    umma_ts(o_col, s_col + kk * 8, tile + kk * kStepPV, kDescHi, idesc_pv, kk > 0 || x.blk > 1 ? 1u : 0u);
+                  umma_commit(&bars->pv_done[st]);
+                  umma_commit(&bars->unit_empty[slot]);
+                  used0 += st ^ 1;
+                  used1 += st;
+                  --pv_left;
+                  x.blk += 2;
+                  x.pv = x.told = false;
+                  idle = 0;
+                }
               }
-              issued = true;
             }
-            // as mbar_wait_bounded, over all that is waited for here
-            if (issued) {
-              idle = 0;
-            } else if ((++idle & 255u) == 0u) {
+            const Stream other = y;
+            y = x;
+            x = other;
+            if ((idle & 255u) == 255u) {  // as mbar_wait_bounded, over all that is waited for here
               const uint64_t now = global_timer_ns();
-              if (idle == 256u) t0 = now;
+              if (idle == 255u) t0 = now;
               if (*abort_flag) ok = 0;
               if (now - t0 > kWaitLimitNs) {
                 *abort_flag = 1;
@@ -572,6 +575,19 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         }
         if (live) {
           tc_fence_after();
+          if (nv < kBlockN) {  // keys that take no part: -infinity in S itself
+#pragma unroll 1
+            for (int c = nv & ~31; c < kBlockN; c += 32) {
+              uint32_t x[32];
+              EC_TMEM_LD32(s_addr + c, x);
+              EC_TMEM_WAIT32(x);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c + e >= nv) x[e] = __float_as_uint(-INFINITY);
+              EC_TMEM_ST32(s_addr + c, x);
+            }
+            tmem_wait_st();
+          }
           // The stream's first block of the item: its maximum is the first m (scale > 0 commutes
           // with the maximum).
           if (i == st) {
@@ -581,11 +597,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
               uint32_t x[32];
               EC_TMEM_LD32(s_addr + c, x);
               EC_TMEM_WAIT32(x);
-              if (c + 32 > nv) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (c + e >= nv) x[e] = __float_as_uint(-INFINITY);
-              }
 #pragma unroll
               for (int e = 0; e < 32; e += 2)
                 m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
@@ -612,11 +623,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
               EC_TMEM_WAIT32(buf[c & 1]);
               if (c + 1 < kBlockN / 32) EC_TMEM_LD32(s_addr + (c + 1) * 32, buf[(c + 1) & 1]);
               uint32_t* x = buf[c & 1];
-              if (c * 32 + 32 > nv) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (c * 32 + e >= nv) x[e] = __float_as_uint(-INFINITY);
-              }
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 float p0, p1;
@@ -753,16 +759,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
-      uint4 w[kPieces];
-      int e_next = 0;
-      auto raw_wait = [&](uint32_t m) {  // tile m of the CTA is in the raw ring
-        return __all_sync(0xffffffffu, wait(&bars->raw_full[m % LY::kRaw], (m / LY::kRaw) & 1u)) != 0;
-      };
-      auto raw_at = [&](uint32_t m) { return smem_u32(smem + LY::kRawOff + (m % LY::kRaw) * LY::kRawBytes); };
-      auto raw_done = [&](uint32_t m) {  // it has been read
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->raw_empty[m % LY::kRaw]);
-      };
       auto exponent = [&](int j) {  // of this lane's row of block j (past the cache's end: any)
         const bool pre = j < it.np;
         const int key = (pre ? j : j - it.np) * kBlockN + exp_row, b = pre ? 0 : it.b;
@@ -770,50 +766,57 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
                                                                  (static_cast<int64_t>(b) * s.Hkv + it.kvh) * (pre ? a.Lps : a.Ls) + key))
                                         : kExpZeroByte;
       };
-      e_next = exponent(it.j0);
-      ok = raw_wait(n);
-      if (!ok) break;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) w[i] = ld_shared16(raw_at(n) + src_off + i * kRowsStep * D);
-      raw_done(n);
+      int e_next = exponent(it.j0);
       for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j, n += 2) {
         const int nv = kv ? valid_keys(s, it, j) : kBlockN;
         const int e_here = e_next;
-        const bool more = j + 1 < it.j0 + it.nblk;
-        if (more) e_next = exponent(j + 1);
-        const uint32_t slot = n % kUnits;
-        ok = __all_sync(0xffffffffu, wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u));
-        if (ok && more) ok = raw_wait(n + 2);
+        if (j + 1 < it.j0 + it.nblk) e_next = exponent(j + 1);
+        const uint32_t rs = n % LY::kRaw, slot = n % kUnits;
+        ok = __all_sync(0xffffffffu, wait(&bars->raw_full[rs], (n / LY::kRaw) & 1u) &&
+                                         wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u));
         if (!ok) break;
-        const uint32_t tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes) + dst_off;
-        const uint32_t raw = raw_at(n + 2);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int byte = __shfl_sync(0xffffffffu, e_here, i * kRowsWarp + sub);
-          uint4 lo, hi;
-          if (byte <= kExpOneFactor) {
-            const uint32_t f = dequant_factor(byte);
-            dequantise4(w[i].x, f, lo.x, lo.y);
-            dequantise4(w[i].y, f, lo.z, lo.w);
-            dequantise4(w[i].z, f, hi.x, hi.y);
-            dequantise4(w[i].w, f, hi.z, hi.w);
-          } else {
-            const DequantScale sc = dequant_scale(byte);
-            dequantise4(w[i].x, sc, lo.x, lo.y);
-            dequantise4(w[i].y, sc, lo.z, lo.w);
-            dequantise4(w[i].z, sc, hi.x, hi.y);
-            dequantise4(w[i].w, sc, hi.z, hi.w);
+        uint32_t src = smem_u32(smem + LY::kRawOff + rs * LY::kRawBytes) + src_off;
+        uint32_t dst = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes) + dst_off;
+        if (nv == kBlockN && __all_sync(0xffffffffu, e_here <= kExpOneFactor)) {
+          uint4 w = ld_shared16(src);
+#pragma unroll 2
+          for (int i = 0; i < kPieces; ++i) {
+            const uint4 here = w;
+            src += kRowsStep * D;
+            if (i + 1 < kPieces) w = ld_shared16(src);
+            const uint32_t f = dequant_factor(__shfl_sync(0xffffffffu, e_here, i * kRowsWarp + sub));
+            uint4 lo, hi;
+            dequantise4(here.x, f, lo.x, lo.y);
+            dequantise4(here.y, f, lo.z, lo.w);
+            dequantise4(here.z, f, hi.x, hi.y);
+            dequantise4(here.w, f, hi.z, hi.w);
+            st_shared16(dst, lo);
+            st_shared16(dst ^ 16u, hi);
+            dst += kRowsStep * 128;
           }
-          // V rows past the length: zeros, whatever lies there
-          if (row0 + i * kRowsStep >= nv) lo = hi = make_uint4(0, 0, 0, 0);
-          st_shared16(tile + i * kRowsStep * 128, lo);
-          st_shared16((tile + i * kRowsStep * 128) ^ 16u, hi);
-          if (more) w[i] = ld_shared16(raw + src_off + i * kRowsStep * D);
+        } else {  // large exponents, NaN rows, V rows past the length (zeros, whatever lies there)
+#pragma unroll 1
+          for (int i = 0; i < kPieces; ++i) {
+            const uint4 here = ld_shared16(src);
+            const DequantScale sc = dequant_scale(__shfl_sync(0xffffffffu, e_here, i * kRowsWarp + sub));
+            uint4 lo, hi;
+            dequantise4(here.x, sc, lo.x, lo.y);
+            dequantise4(here.y, sc, lo.z, lo.w);
+            dequantise4(here.z, sc, hi.x, hi.y);
+            dequantise4(here.w, sc, hi.z, hi.w);
+            if (row0 + i * kRowsStep >= nv) lo = hi = make_uint4(0, 0, 0, 0);
+            st_shared16(dst, lo);
+            st_shared16(dst ^ 16u, hi);
+            src += kRowsStep * D;
+            dst += kRowsStep * 128;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->unit_full[slot]);
-        if (more) raw_done(n + 2);
+        if (lane == 0) {
+          mbar_arrive(&bars->raw_empty[rs]);
+          mbar_arrive(&bars->unit_full[slot]);
+        }
       }
     }
   }
