@@ -175,6 +175,13 @@ EC_DEV uint4 ld_shared16(uint32_t src) {
                  "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),  \
                  "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory")
 
+#define EC_TMEM_ST16(taddr, r)                                                                              \
+  asm volatile(                                                                                             \
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" \
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), \
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])          \
+      : "memory")
+
 // Two fp32 lanes in one instruction.
 EC_DEV uint64_t pack_f32x2(float lo, float hi) {
   uint64_t r;
@@ -588,68 +595,67 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
             }
             tmem_wait_st();
           }
-          // The stream's first block of the item: its maximum is the first m (scale > 0 commutes
-          // with the maximum).
-          if (i == st) {
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-            for (int c = 0; c < kBlockN; c += 32) {
-              uint32_t x[32];
-              EC_TMEM_LD32(s_addr + c, x);
-              EC_TMEM_WAIT32(x);
+          // Two passes over S in chunks of 32 columns, the next chunk's load behind the work on this
+          // one: the maximum (scale > 0 commutes with it), then p = 2^(s scale log2(e) - m). The loops
+          // are rolled to two chunks, and P leaves with each chunk: the passes' code, fetched again
+          // for every block beside the other warps', costs more than reading S twice.
+          uint32_t b0[32], b1[32];
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto top = [&](const uint32_t (&x)[32]) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            }
-            m_used = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+            for (int e = 0; e < 32; e += 2)
+              m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          };
+          EC_TMEM_LD32(s_addr, b0);
+#pragma unroll 1
+          for (int c = 0; c < kBlockN; c += 64) {
+            EC_TMEM_WAIT32(b0);
+            EC_TMEM_LD32(s_addr + c + 32, b1);
+            top(b0);
+            EC_TMEM_WAIT32(b1);
+            EC_TMEM_LD32(s_addr + ((c + 64) & 127), b0);  // after the last chunk: the first one again
+            top(b1);
           }
-          // p = 2^(s scale log2(e) - m), m the running maximum so far (0 while no score was finite),
-          // in one pass over S. P stays in registers: where a row's new maximum is above m by more
-          // than the threshold, or the first one, m is put right and S taken again.
-          const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2);
-          uint32_t pk[kBlockN / 2];
-          float sum, alpha = 1.f;
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
           bool rescale = false;
-#pragma unroll 1
-          for (;;) {
-            const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-            const uint64_t neg_m2 = pack_f32x2(neg_m, neg_m);
-            uint64_t sum2[2] = {0, 0};
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            uint32_t buf[2][32];
-            EC_TMEM_LD32(s_addr, buf[0]);
-#pragma unroll
-            for (int c = 0; c < kBlockN / 32; ++c) {
-              EC_TMEM_WAIT32(buf[c & 1]);
-              if (c + 1 < kBlockN / 32) EC_TMEM_LD32(s_addr + (c + 1) * 32, buf[(c + 1) & 1]);
-              uint32_t* x = buf[c & 1];
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float p0, p1;
-                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
-                m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], p0, p1);
-                p0 = ex2_approx(p0);
-                p1 = ex2_approx(p1);
-                sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
-                pk[(c * 32 + e) >> 1] = pack_bf16x2(p0, p1);
-              }
-            }
-            float lo, hi;
-            unpack_f32x2(add_f32x2(sum2[0], sum2[1]), lo, hi);
-            sum = lo + hi;
-            const float up = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));  // the new maximum less m
-            const bool above = up > (m_used == -INFINITY ? -INFINITY : kRescaleLog2);
-            if (!__any_sync(0xffffffffu, above)) break;
-            if (above) {
-              alpha *= m_used == -INFINITY ? 0.f : ex2_approx(-up);
-              m_used = m_used == -INFINITY ? up : m_used + up;
-              rescale = i != st;
-            }
+          float alpha = 1.f;
+          if (i == st) {
+            m_used = mx;
+          } else if (mx > m_used + kRescaleLog2) {
+            alpha = ex2_approx(m_used - mx);
+            m_used = mx;
+            l_sum *= alpha;
+            rescale = true;
           }
-          l_sum *= alpha;
-          l_sum += sum;
+          // without a finite score so far, nothing is subtracted and p = 0
+          const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+          const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
+          uint64_t sum2[2] = {0, 0};
+          auto weights = [&](const uint32_t (&x)[32], int c) {  // P over columns of S that have been read
+            uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) EC_TMEM_ST32(s_addr + c * 32, (pk + 32 * c));
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
+              pk[e >> 1] = pack_bf16x2(p0, p1);
+            }
+            EC_TMEM_ST16(s_addr + (c >> 1), pk);
+          };
+#pragma unroll 1
+          for (int c = 0; c < kBlockN; c += 64) {
+            EC_TMEM_WAIT32(b0);
+            EC_TMEM_LD32(s_addr + c + 32, b1);
+            weights(b0, c);
+            EC_TMEM_WAIT32(b1);
+            if (c == 0) EC_TMEM_LD32(s_addr + 64, b0);
+            weights(b1, c + 32);
+          }
+          float sum_lo, sum_hi;
+          unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
+          l_sum += sum_lo + sum_hi;
           // the stream's earlier products are done (they were waited for before this S was made)
           if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
