@@ -431,83 +431,103 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
       uint32_t n0 = 0;            // tiles of the items before
       uint32_t used0 = 0, used1 = 0;  // P V products under way or done, per stream
+      uint32_t last = 1;              // the stream served last
       int ok = 1;
       for (int items = 0; ok; ++items) {
         const Item it = next_item(items);
         if (it.nblk == 0) break;
-        // the whole warp goes this way, and one thread of it issues
-        auto test = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
         ok = __all_sync(0xffffffffu, items == 0 ? wait(&bars->q_first, 0) : wait(&bars->q_full, (items - 1) & 1));
         // Per stream, in turn: S of its next block (the buffer's last P has been read, and K is here), then
-        // O += P V (P and V are here; the item's first one once O has been read out).
-        // One copy of the code serves both: the streams change places after every look.
-        struct Stream {
-          int st, blk;    // stream, its block of the item
-          bool pv, told;  // what is next is P V; its V tile's coming has been told
-        } x = {0, 0, false, false}, y = {1, 1, false, false};
+        // O += P V (P and V are here; the item's first one once O has been read out). The whole warp
+        // looks, three lanes a stream, each at one barrier; one thread issues.
+        uint32_t blk = 0x10000u;  // the block of stream 0 in the low half, of stream 1 in the high one: 0 and 1
+        uint32_t pv = 0, told = 0;  // bit st: what is next is P V; its V tile's coming has been told
         int s_left = it.nblk, pv_left = it.nblk;
-        uint64_t t0 = 0;
-#pragma unroll 1
-        for (uint32_t idle = 1; ok && pv_left > 0; ++idle) {
-          const uint32_t st = __shfl_sync(0xffffffffu, x.st, 0), done = st ? used1 : used0;
-          const uint32_t n = n0 + 2 * x.blk + (x.pv ? 1 : 0), slot = __shfl_sync(0xffffffffu, n % kUnits, 0);
+        while (ok && pv_left > 0) {
+          // what this lane looks at
+          const uint32_t my = lane >= 3 ? 1u : 0u, my_blk = my ? blk >> 16 : blk & 0xFFFFu, my_pv = (pv >> my) & 1u;
+          const uint32_t my_n = n0 + 2 * my_blk + my_pv, my_done = my ? used1 : used0;
+          uint64_t* bar = &bars->unit_full[my_n % kUnits];
+          uint32_t parity = (my_n / kUnits) & 1u;
+          bool need = lane < 6;
+          if (lane == 1 || lane == 4) {
+            bar = my_pv ? &bars->p_full[my] : &bars->pv_done[my];
+            parity = (my_pv ? my_done : my_done - 1) & 1u;
+            need = my_pv != 0 || my_done != 0;
+          }
+          if (lane == 2 || lane == 5) {
+            bar = &bars->o_free;
+            parity = (items - 1) & 1;
+            need = my_pv != 0 && my_blk < 2 && items > 0;
+          }
+          const bool over = my_blk >= static_cast<uint32_t>(it.nblk);  // the stream has no block left
+          uint32_t ready = 0;
+          uint64_t t0 = 0;
+          for (uint32_t idle = 1;; ++idle) {
+            const uint32_t here = __ballot_sync(0xffffffffu, !over && (!need || mbar_test(bar, parity)));
+            if constexpr (!Q8) {  // a V tile with rows to be zeroed: tell the stream's warps, once
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int j = it.j0 + static_cast<int>(k ? blk >> 16 : blk & 0xFFFFu);
+                if ((here >> (3 * k) & 1u) && (pv >> k & 1u) && !(told >> k & 1u)) {
+                  told |= 1u << k;
+                  if (ragged(it, j) && lane == 0) mbar_arrive(&bars->v_here[k]);
+                }
+              }
+            }
+            ready = ((here & 7u) == 7u ? 1u : 0u) | ((here & 0x38u) == 0x38u ? 2u : 0u);
+            if (ready != 0) break;
+            if ((idle & 255u) == 0u) {  // as mbar_wait_bounded, over all that is waited for here
+              const uint64_t now = global_timer_ns();
+              if (idle == 256u) t0 = now;
+              if (*abort_flag) ok = 0;
+              if (now - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                report_error(a.dev_err, EC_DEVERR_TIMEOUT);
+                ok = 0;
+              }
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+            }
+          }
+          if (!ok) break;
+          // with both ready, the one whose turn it was not
+          const uint32_t st = __shfl_sync(0xffffffffu, ready == 3u ? last ^ 1u : ready >> 1, 0);
+          last = st;
+          const uint32_t b = st ? blk >> 16 : blk & 0xFFFFu, is_pv = (pv >> st) & 1u;
+          const uint32_t slot = __shfl_sync(0xffffffffu, (n0 + 2 * b + is_pv) % kUnits, 0);
           const uint32_t s_col = tmem_u + st * kBlockN, o_col = tmem_u + kTmemO + st * 128;
-          if (x.blk < it.nblk && test(&bars->unit_full[slot], (n / kUnits) & 1u)) {
-            if (!x.pv) {
-              if (done == 0 || test(&bars->pv_done[st], (done - 1) & 1u)) {
-                tc_fence_after();
-                const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, 16);
-                if (elect_one()) {
+          tc_fence_after();
+          if (!is_pv) {
+            const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, 16);
+            if (elect_one()) {
 #pragma unroll
-                  for (int kk = 0; kk < D / 16; ++kk)
-                    umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
-                  umma_commit(&bars->s_full[st]);
-                  umma_commit(&bars->unit_empty[slot]);
-                  if (s_left == 1) umma_commit(&bars->q_empty);
-                }
-                __syncwarp();
-                --s_left;
-                x.pv = true;
-                idle = 0;
-              }
-            } else {
-              if (!Q8 && !x.told && ragged(it, it.j0 + x.blk) && lane == 0) mbar_arrive(&bars->v_here[st]);
-              x.told = true;
-              if (test(&bars->p_full[st], done & 1u) && (x.blk > 1 || items == 0 || test(&bars->o_free, (items - 1) & 1))) {
-                tc_fence_after();
-                const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, kAtomBytes);
-                const uint32_t acc0 = __shfl_sync(0xffffffffu, x.blk > 1 ? 1u : 0u, 0);  // the item's first block starts O anew
-                if (elect_one()) {
+              for (int kk = 0; kk < D / 16; ++kk)
+                umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+              umma_commit(&bars->s_full[st]);
+              umma_commit(&bars->unit_empty[slot]);
+              if (s_left == 1) umma_commit(&bars->q_empty);
+            }
+            __syncwarp();
+            --s_left;
+          } else {
+            const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, kAtomBytes);
+            const uint32_t acc0 = __shfl_sync(0xffffffffu, b > 1 ? 1u : 0u, 0);  // the stream's first block of the item starts O anew
+            if (elect_one()) {
 #pragma unroll
-                  for (int kk = 0; kk < kBlockN / 16; ++kk)
-                    umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
-                  umma_commit(&bars->pv_done[st]);
-                  umma_commit(&bars->unit_empty[slot]);
-                }
-                __syncwarp();
-                used0 += st ^ 1;
-                used1 += st;
-                --pv_left;
-                x.blk += 2;
-                x.pv = x.told = false;
-                idle = 0;
-              }
+              for (int kk = 0; kk < kBlockN / 16; ++kk)
+                umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
+              umma_commit(&bars->pv_done[st]);
+              umma_commit(&bars->unit_empty[slot]);
             }
+            __syncwarp();
+            used0 += st ^ 1u;
+            used1 += st;
+            --pv_left;
+            blk += st ? 0x20000u : 2u;
+            told &= ~(1u << st);
           }
-          const Stream other = y;
-          y = x;
-          x = other;
-          if ((idle & 255u) == 255u) {  // as mbar_wait_bounded, over all that is waited for here
-            const uint64_t now = global_timer_ns();
-            if (idle == 255u) t0 = now;
-            if (*abort_flag) ok = 0;
-            if (now - t0 > kWaitLimitNs) {
-              *abort_flag = 1;
-              report_error(a.dev_err, EC_DEVERR_TIMEOUT);
-              ok = 0;
-            }
-            ok = __all_sync(0xffffffffu, ok);
-          }
+          pv ^= 1u << st;
         }
         n0 += 2 * it.nblk;
       }
@@ -787,12 +807,20 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
-      auto exponent = [&](int j) {  // of this lane's row of block j (past the cache's end: any)
-        const bool pre = j < it.np;
-        const int key = (pre ? j : j - it.np) * kBlockN + exp_row, b = pre ? 0 : it.b;
-        return key < (pre ? s.Lp : s.L) ? static_cast<int>(__ldg((pre ? a.pexps : a.exps)[kv] +
-                                                                 (static_cast<int64_t>(b) * s.Hkv + it.kvh) * (pre ? a.Lps : a.Ls) + key))
-                                        : kExpZeroByte;
+      // the exponent of this lane's row, a block ahead (past the cache's end: any)
+      const uint8_t* ep = nullptr;
+      int left = 0;  // positions from the lane's row to the cache's end
+      auto exponent = [&](int j) {
+        if (j == it.j0 || j == it.np) {
+          const bool pre = j < it.np;
+          const int key = (pre ? j : j - it.np) * kBlockN + exp_row, b = pre ? 0 : it.b;
+          left = (pre ? s.Lp : s.L) - key;
+          ep = (pre ? a.pexps : a.exps)[kv] + (static_cast<int64_t>(b) * s.Hkv + it.kvh) * (pre ? a.Lps : a.Ls) + key;
+        } else {
+          left -= kBlockN;
+          ep += kBlockN;
+        }
+        return left > 0 ? static_cast<int>(__ldg(ep)) : kExpZeroByte;
       };
       int e_next = exponent(it.j0);
       for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j, n += 2) {
