@@ -12,12 +12,13 @@
 // Structure (one CTA per SM; the work plan is attention_cached.cuh's):
 //   warp 0       makes the work plan, hands out the CTA's items, and is the TMA producer: K and V
 //                blocks of 128 keys.
-//   warp 1       allocates 512 TMEM columns and issues tcgen05.mma for two streams (below),
-//                whichever has its operands; no product of one lies between those of the other.
+//   warps 1, 3   issue tcgen05.mma, each for one of two streams (below); warp 1 allocates 512 TMEM
+//                columns. (One issuer for both: 102 us for 85 on the long 8-bit case, every wait
+//                and every product of a stream in the other's way.)
 //   warp 2       the query tiles of later items, four rows a TMA gather (a tile packs rows of any
 //                sequences, which no one tensor box covers). The gathers take 6000 cycles a tile, behind the
 //                products of the item before; the first item's tile, which nothing hides, is
-//                fetched by the softmax warps. Warp 3 has no work.
+//                fetched by the softmax warps.
 //   warps 4..7   softmax of the CTA's even key blocks, warps 8..11 of the odd ones: two independent
 //                streams with their own S buffer, running maximum and sum, and O accumulator, joined
 //                once per item. One stream's softmax runs while the tensor cores work on the
@@ -32,8 +33,9 @@
 //                a bf16 cache with the same values. (Codes loaded from global memory into
 //                registers, without the ring: 180 us for 120 on the long case. The shared memory
 //                that the kernel takes leaves L1 little room for loads in flight.)
-// A waiter on an mbarrier sees a phase's parity only, so each follows every phase of what it waits for:
-// in both rings K and V have slots of their own.
+// A waiter on an mbarrier sees a phase's parity only: it cannot tell a phase that is complete from one
+// whose predecessor is still open. So whoever waits on a barrier follows every one of its phases: a slot of
+// the K/V ring belongs to one stream, a slot of the raw ring to K or to V.
 // Keys past a sequence's length may hold anything: their scores are replaced, and their V rows are
 // zeroed in shared memory (0 x NaN is NaN in a matrix product).
 // Partial items write fp32 rows, their maximum and their sum to the workspace; the merge kernel
@@ -83,14 +85,14 @@ struct Bars {
   int abort;
 };
 
-// Shared memory: the query tile, a ring of bf16 tiles (K and V of a block in turn), for the 8-bit
+// Shared memory: the query tile, for each stream a ring of bf16 tiles (its blocks' K and V in turn), for the 8-bit
 // cache a ring of raw tiles (128 rows of codes), the row statistics that the two streams exchange,
 // the items, where each sequence's packed rows end, the barriers.
 template <int D, bool Q8>
 struct Layout {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;
-  static constexpr int kUnits = Q8 ? 4 : 6;
+  static constexpr int kUnits = Q8 ? 4 : 6, kPer = kUnits / 2;  // bf16 tiles; of one stream
   static constexpr int kRaw = Q8 ? kMaxRaw : 0;
   static constexpr int kRawBytes = 128 * D;
   static constexpr int kUnitOff = kTileBytes;
@@ -138,19 +140,6 @@ EC_DEV bool elect_one() {
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(p));
   return p != 0;
-}
-
-// Whether the phase of the given parity is complete; returns at once.
-EC_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // Four rows of a matrix, 64 elements from column x on, below one another.
@@ -261,10 +250,21 @@ EC_DEV int valid_keys(const Shape& s, const Item& it, int j) {
   return max(0, min(kBlockN, left));
 }
 
+// K/V tiles of the two streams in the items before: block i of an item goes to stream i % 2, its K and V
+// to two successive places of that stream's ring.
+struct TileCount {
+  uint32_t of[2] = {0, 0};
+  EC_DEV uint32_t tile(int i, int kv) const { return (i & 1 ? of[1] : of[0]) + (i & ~1) + kv; }
+  EC_DEV void add(int nblk) {
+    of[0] += (nblk + 1) & ~1;
+    of[1] += nblk & ~1;
+  }
+};
+
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_kernel(const __grid_constant__ Args a) {
   using LY = Layout<D, Q8>;
-  constexpr int kUnits = LY::kUnits;
+  constexpr int kPer = LY::kPer;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + LY::kBarOff);
   const Shape& s = a.s;
@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_first, 256);
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
-    for (int i = 0; i < kUnits; ++i) {
+    mbar_init(&bars->q_empty, 2);
+    for (int i = 0; i < LY::kUnits; ++i) {
       mbar_init(&bars->unit_full[i], Q8 ? kDequantWarps : 1);
       mbar_init(&bars->unit_empty[i], 1);
     }
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     mbar_init(&bars->v_here[1], 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
-      mbar_init(&bars->item_empty[i], 8);
+      mbar_init(&bars->item_empty[i], 10);
     }
     // the swizzled tiles need the 1024-byte alignment that dynamic shared memory has here
     bars->abort = (smem_u32(smem) & 1023u) != 0u;
@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         if (lane < s.B) reinterpret_cast<int32_t*>(smem + LY::kCumOff)[lane] = incl;
         __syncwarp();
       }
+      TileCount tiles;
       uint32_t n = 0;  // tiles requested: K and V of each block in turn
       int ok = 1, count = 0;
       Record rec{};
@@ -396,8 +397,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
                 mbar_arrive_expect_tx(&bars->raw_full[slot], LY::kRawBytes);
                 tma_load_4d(dst, map, &bars->raw_full[slot], 0, it.kvh, key0, b);
               } else {
-                const uint32_t slot = n % kUnits;
-                if (!(ok = wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u))) break;
+                const uint32_t m = tiles.tile(j - it.j0, kv), slot = ((j - it.j0) & 1) * kPer + m % kPer;
+                if (!(ok = wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u))) break;
                 uint8_t* dst = smem + LY::kUnitOff + slot * LY::kTileBytes;
                 mbar_arrive_expect_tx(&bars->unit_full[slot], LY::kTileBytes);
 #pragma unroll
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
             }
           }
         }
+        tiles.add(it.nblk);
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
       if (lane == 0) {
@@ -423,113 +425,70 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           *a.header = h;
         }
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------------ MMA issuer
+    } else if (warp == 1 || warp == 3) {
+      // ------------------------------------------------------------------ MMA issuer of one stream
+      // The whole warp waits, one thread issues.
       constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlockN, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
+      const uint32_t st = __shfl_sync(0xffffffffu, warp >> 1, 0);
       const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16), unit0 = smem_u32(smem + LY::kUnitOff);
       const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
-      uint32_t n0 = 0;            // tiles of the items before
-      uint32_t used0 = 0, used1 = 0;  // P V products under way or done, per stream
-      uint32_t last = 1;              // the stream served last
-      int ok = 1;
+      const uint32_t s_col = tmem_u + st * kBlockN, o_col = tmem_u + kTmemO + st * 128;
+      uint32_t m0 = 0, used = 0;  // this stream's tiles in the items before; products P V under way or done
+      bool ok = true;
+      auto wait_w = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       for (int items = 0; ok; ++items) {
         const Item it = next_item(items);
         if (it.nblk == 0) break;
-        ok = __all_sync(0xffffffffu, items == 0 ? wait(&bars->q_first, 0) : wait(&bars->q_full, (items - 1) & 1));
-        // Per stream, in turn: S of its next block (the buffer's last P has been read, and K is here), then
-        // O += P V (P and V are here; the item's first one once O has been read out). The whole warp
-        // looks, three lanes a stream, each at one barrier; one thread issues.
-        uint32_t blk = 0x10000u;  // the block of stream 0 in the low half, of stream 1 in the high one: 0 and 1
-        uint32_t pv = 0, told = 0;  // bit st: what is next is P V; its V tile's coming has been told
-        int s_left = it.nblk, pv_left = it.nblk;
-        while (ok && pv_left > 0) {
-          // what this lane looks at
-          const uint32_t my = lane >= 3 ? 1u : 0u, my_blk = my ? blk >> 16 : blk & 0xFFFFu, my_pv = (pv >> my) & 1u;
-          const uint32_t my_n = n0 + 2 * my_blk + my_pv, my_done = my ? used1 : used0;
-          uint64_t* bar = &bars->unit_full[my_n % kUnits];
-          uint32_t parity = (my_n / kUnits) & 1u;
-          bool need = lane < 6;
-          if (lane == 1 || lane == 4) {
-            bar = my_pv ? &bars->p_full[my] : &bars->pv_done[my];
-            parity = (my_pv ? my_done : my_done - 1) & 1u;
-            need = my_pv != 0 || my_done != 0;
-          }
-          if (lane == 2 || lane == 5) {
-            bar = &bars->o_free;
-            parity = (items - 1) & 1;
-            need = my_pv != 0 && my_blk < 2 && items > 0;
-          }
-          const bool over = my_blk >= static_cast<uint32_t>(it.nblk);  // the stream has no block left
-          uint32_t ready = 0;
-          uint64_t t0 = 0;
-          for (uint32_t idle = 1;; ++idle) {
-            const uint32_t here = __ballot_sync(0xffffffffu, !over && (!need || mbar_test(bar, parity)));
-            if constexpr (!Q8) {  // a V tile with rows to be zeroed: tell the stream's warps, once
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int j = it.j0 + static_cast<int>(k ? blk >> 16 : blk & 0xFFFFu);
-                if ((here >> (3 * k) & 1u) && (pv >> k & 1u) && !(told >> k & 1u)) {
-                  told |= 1u << k;
-                  if (ragged(it, j) && lane == 0) mbar_arrive(&bars->v_here[k]);
-                }
-              }
-            }
-            ready = ((here & 7u) == 7u ? 1u : 0u) | ((here & 0x38u) == 0x38u ? 2u : 0u);
-            if (ready != 0) break;
-            if ((idle & 255u) == 0u) {  // as mbar_wait_bounded, over all that is waited for here
-              const uint64_t now = global_timer_ns();
-              if (idle == 256u) t0 = now;
-              if (*abort_flag) ok = 0;
-              if (now - t0 > kWaitLimitNs) {
-                *abort_flag = 1;
-                report_error(a.dev_err, EC_DEVERR_TIMEOUT);
-                ok = 0;
-              }
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-            }
-          }
-          if (!ok) break;
-          // with both ready, the one whose turn it was not
-          const uint32_t st = __shfl_sync(0xffffffffu, ready == 3u ? last ^ 1u : ready >> 1, 0);
-          last = st;
-          const uint32_t b = st ? blk >> 16 : blk & 0xFFFFu, is_pv = (pv >> st) & 1u;
-          const uint32_t slot = __shfl_sync(0xffffffffu, (n0 + 2 * b + is_pv) % kUnits, 0);
-          const uint32_t s_col = tmem_u + st * kBlockN, o_col = tmem_u + kTmemO + st * 128;
+        auto issue_qk = [&](int i) {  // S of block i
+          const uint32_t m = m0 + (i & ~1), slot = __shfl_sync(0xffffffffu, st * kPer + m % kPer, 0);
+          // K is here, and the buffer's last P has been read
+          ok = ok && wait_w(&bars->unit_full[slot], (m / kPer) & 1u) &&
+               (used == 0 || wait_w(&bars->pv_done[st], (used - 1) & 1u));
+          if (!ok) return;
           tc_fence_after();
-          if (!is_pv) {
-            const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, 16);
-            if (elect_one()) {
+          const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, 16);
+          if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
-              umma_commit(&bars->s_full[st]);
-              umma_commit(&bars->unit_empty[slot]);
-              if (s_left == 1) umma_commit(&bars->q_empty);
-            }
-            __syncwarp();
-            --s_left;
-          } else {
-            const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, kAtomBytes);
-            const uint32_t acc0 = __shfl_sync(0xffffffffu, b > 1 ? 1u : 0u, 0);  // the stream's first block of the item starts O anew
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < kBlockN / 16; ++kk)
-                umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
-              umma_commit(&bars->pv_done[st]);
-              umma_commit(&bars->unit_empty[slot]);
-            }
-            __syncwarp();
-            used0 += st ^ 1u;
-            used1 += st;
-            --pv_left;
-            blk += st ? 0x20000u : 2u;
-            told &= ~(1u << st);
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+            umma_commit(&bars->s_full[st]);
+            umma_commit(&bars->unit_empty[slot]);
+            if (i + 2 >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last S of the item
           }
-          pv ^= 1u << st;
+          __syncwarp();
+        };
+        ok = items == 0 ? wait_w(&bars->q_first, 0) : wait_w(&bars->q_full, (items - 1) & 1);
+        if (static_cast<int>(st) < it.nblk) {
+          issue_qk(st);
+        } else {  // nothing of this item falls to stream 1
+          if (ok && lane == 0) mbar_arrive(&bars->q_empty);
+          if (items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);
         }
-        n0 += 2 * it.nblk;
+#pragma unroll 1
+        for (int i = st; ok && i < it.nblk; i += 2) {
+          const uint32_t m = m0 + (i & ~1) + 1, slot = __shfl_sync(0xffffffffu, st * kPer + m % kPer, 0);
+          ok = wait_w(&bars->unit_full[slot], (m / kPer) & 1u);
+          if (!Q8 && ok && ragged(it, it.j0 + i) && lane == 0) mbar_arrive(&bars->v_here[st]);
+          if (i < 2 && items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);
+          ok = ok && wait_w(&bars->p_full[st], used & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, kAtomBytes);
+          const uint32_t acc0 = __shfl_sync(0xffffffffu, i > 1 ? 1u : 0u, 0);  // the stream's first block of the item starts O anew
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kBlockN / 16; ++kk)
+              umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
+            umma_commit(&bars->pv_done[st]);
+            umma_commit(&bars->unit_empty[slot]);
+          }
+          __syncwarp();
+          ++used;
+          if (i + 2 < it.nblk) issue_qk(i + 2);
+        }
+        m0 += (it.nblk + 1 - st) & ~1u;
+        if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------------ query loader
@@ -579,7 +538,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t s_addr = tmem + lane_off + st * kBlockN;
     float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
-    uint32_t n0 = 0;                    // tiles of the items before
+    TileCount tiles;
     uint32_t used = 0, n_ragged = 0;    // blocks of this stream, and those with rows past a length
     bool ok = true;
     for (int items = 0; ok; ++items) {
@@ -612,7 +571,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         const int nv = valid_keys(s, it, it.j0 + i);
         if constexpr (!Q8) {
           if (ragged(it, it.j0 + i)) {  // their V rows become zeros
-            const uint32_t slot = (n0 + 2 * i + 1) % kUnits;
+            const uint32_t slot = st * kPer + tiles.tile(i, 1) % kPer;
             ok = __all_sync(0xffffffffu, wait(&bars->v_here[st], n_ragged++ & 1u));
             if (!ok) break;
             const uint32_t v_tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes);
@@ -717,7 +676,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         if (lane == 0) mbar_arrive(&bars->p_full[st]);
       }
       // join the two streams: each warpgroup takes half of the columns of both accumulators
-      n0 += 2 * it.nblk;
+      tiles.add(it.nblk);
       if (ok && st < it.nblk) ok = wait(&bars->pv_done[st], (used - 1) & 1u);
       // every warp is done with the item before, so its statistics may be overwritten
       if (ok && items > 0) ok = wait(&bars->o_free, (items - 1) & 1);
@@ -802,6 +761,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     const int exp_row = (lane / kRowsWarp) * kRowsStep + w4 * kRowsWarp + lane % kRowsWarp;
     const uint32_t src_off = row0 * D + piece * 16;
     const uint32_t dst_off = (piece >> 2) * kAtomBytes + row0 * 128 + ((((piece & 3) * 2) ^ (row0 & 7)) << 4);
+    TileCount tiles;
     uint32_t n = kv;
     bool ok = true;
     for (int items = 0; ok; ++items) {
@@ -827,9 +787,10 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         const int nv = kv ? valid_keys(s, it, j) : kBlockN;
         const int e_here = e_next;
         if (j + 1 < it.j0 + it.nblk) e_next = exponent(j + 1);
-        const uint32_t rs = n % LY::kRaw, slot = n % kUnits;
+        const int i0 = j - it.j0;
+        const uint32_t m = tiles.tile(i0, kv), rs = n % LY::kRaw, slot = (i0 & 1) * kPer + m % kPer;
         ok = __all_sync(0xffffffffu, wait(&bars->raw_full[rs], (n / LY::kRaw) & 1u) &&
-                                         wait(&bars->unit_empty[slot], ((n / kUnits) & 1u) ^ 1u));
+                                         wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u));
         if (!ok) break;
         uint32_t src = smem_u32(smem + LY::kRawOff + rs * LY::kRawBytes) + src_off;
         uint32_t dst = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes) + dst_off;
@@ -874,10 +835,16 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           mbar_arrive(&bars->unit_full[slot]);
         }
       }
+      tiles.add(it.nblk);
     }
   }
 
   // ---------------------------------------------------------------------- teardown
+  if (*abort_flag) {  // copies and products may still be under way: they take microseconds
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 200000u) {
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
