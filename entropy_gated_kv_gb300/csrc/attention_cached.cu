@@ -15,10 +15,7 @@
 //   warps 1, 3   issue tcgen05.mma, each for one of two streams (below); warp 1 allocates 512 TMEM
 //                columns. (One issuer for both: 102 us for 85 on the long 8-bit case, every wait
 //                and every product of a stream in the other's way.)
-//   warp 2       the query tiles of later items, four rows a TMA gather (a tile packs rows of any
-//                sequences, which no one tensor box covers). The gathers take 6000 cycles a tile, behind the
-//                products of the item before; the first item's tile, which nothing hides, is
-//                fetched by the softmax warps.
+//                Warp 2 has no work.
 //   warps 4..7   softmax of the CTA's even key blocks, warps 8..11 of the odd ones: two independent
 //                streams with their own S buffer, running maximum and sum, and O accumulator, joined
 //                once per item. One stream's softmax runs while the tensor cores work on the
@@ -26,7 +23,9 @@
 //                products in series, and at 128 rows that is longer than the block's bytes take from HBM.
 //                One TMEM lane (= one packed query row) per thread; online softmax in base 2 with a
 //                lazy rescale of O (only when the running maximum grows by more than 2^8); P in
-//                bf16 written back over the first half of the S buffer.
+//                bf16 written back over the first half of the S buffer. Between an item's last softmax and
+//                its join they fetch the next item's query tile, row by row (a tile packs rows of any
+//                sequences, which no one tensor box covers; TMA gathers of four rows took 6000 cycles a tile).
 //   warps 12..19 (8-bit cache) dequantise, four the K tiles and four the V tiles: the producer's TMA
 //                brings the codes into a raw ring, and these warps write the bf16 tiles that the
 //                products read. The dequantised values are exact in bf16, so the products are those of
@@ -75,7 +74,7 @@ __host__ __device__ constexpr uint32_t step_qk(int kk) { return (kk >> 2) * (kAt
 constexpr uint32_t kStepPV = 16 * 128 / 16;
 
 struct Bars {
-  uint64_t q_first, q_full, q_empty;  // q_first: the first item's queries
+  uint64_t q_full, q_empty;
   uint64_t unit_full[kMaxUnits], unit_empty[kMaxUnits];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t s_full[2], p_full[2], pv_done[2];
@@ -107,7 +106,6 @@ struct Layout {
 };
 
 struct Args {
-  CUtensorMap tq;                // rows of q
   CUtensorMap tk, tv, tpk, tpv;  // own and prefix caches
   const uint8_t *exps[2], *pexps[2];  // 8-bit: exponents of K and V, own and prefix
   Shape s;
@@ -140,15 +138,6 @@ EC_DEV bool elect_one() {
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(p));
   return p != 0;
-}
-
-// Four rows of a matrix, 64 elements from column x on, below one another.
-EC_DEV void tma_gather4(void* dst, const void* tmap, uint64_t* bar, int x, int r0, int r1, int r2, int r3) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-      : "memory");
 }
 
 template <int N>
@@ -271,8 +260,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_first, 256);
-    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_full, 256);
     mbar_init(&bars->q_empty, 2);
     for (int i = 0; i < LY::kUnits; ++i) {
       mbar_init(&bars->unit_full[i], Q8 ? kDequantWarps : 1);
@@ -301,7 +289,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tmap(&a.tq);
     prefetch_tmap(&a.tk);
     prefetch_tmap(&a.tv);
   }
@@ -458,7 +445,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           }
           __syncwarp();
         };
-        ok = items == 0 ? wait_w(&bars->q_first, 0) : wait_w(&bars->q_full, (items - 1) & 1);
+        ok = wait_w(&bars->q_full, items & 1);
         if (static_cast<int>(st) < it.nblk) {
           issue_qk(st);
         } else {  // nothing of this item falls to stream 1
@@ -490,45 +477,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         m0 += (it.nblk + 1 - st) & ~1u;
         if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
       }
-    } else if (warp == 2) {
-      // ------------------------------------------------------------------ query loader
-      // Each lane fetches four rows, wherever they lie; padding repeats the item's last row.
-      const int32_t* cum = reinterpret_cast<const int32_t*>(smem + LY::kCumOff);
-      for (int items = 0;; ++items) {
-        const Item it = next_item(items);
-        if (it.nblk == 0) break;
-        if (items == 0) continue;
-        // row x of KV head kvh lies in q at (b L + x / g) Hq + kvh g + x % g
-        int at[4], seq[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          at[i] = it.row0 + min(4 * lane + i, it.nrows - 1);
-          seq[i] = it.b;
-        }
-        if (it.b < 0) {
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            int x = i == 0 ? at[0] : i == 1 ? at[1] : i == 2 ? at[2] : at[3];
-            const int b = owner_of(s, cum, x);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              at[k] = k == i ? x : at[k];
-              seq[k] = k == i ? b : seq[k];
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = s.div_g(at[i]);
-          at[i] += (seq[i] * s.L + r) * a.Hq + it.kvh * s.g - r * s.g;
-        }
-        if (!__all_sync(0xffffffffu, wait(&bars->q_empty, (items - 1) & 1))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->q_full, LY::kTileBytes);
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < LY::kAtoms; ++c)
-          tma_gather4(smem + c * kAtomBytes + lane * 512, &a.tq, &bars->q_full, c * 64, at[0], at[1], at[2], at[3]);
-      }
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ softmax + epilogue
@@ -541,29 +489,35 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     TileCount tiles;
     uint32_t used = 0, n_ragged = 0;    // blocks of this stream, and those with rows past a length
     bool ok = true;
-    for (int items = 0; ok; ++items) {
-      const Item it = next_item(items);
-      if (it.nblk == 0) break;
-      const bool live = 32 * (warp & 3) < it.nrows;  // else the warp's rows are all padding
-      if (items == 0) {
-        // the first query tile, 16 rows a warp: each lane finds one row, 16-byte pieces by all
-        constexpr int kPieces = D / 8, kStep = 32 / kPieces;
-        const int base = 16 * (warp - 4), piece = lane % kPieces;
-        int x = it.row0 + min(base + (lane & 15), it.nrows - 1), b = it.b;
-        if (b < 0) b = owner_of(s, reinterpret_cast<const int32_t*>(smem + LY::kCumOff), x);
-        const int r = s.div_g(x);
-        const int at = x + (b * s.L + r) * a.Hq + it.kvh * s.g - r * s.g;
+    // An item's query tile, 16 rows a warp: each lane finds one row, and all fetch 16-byte pieces.
+    auto fetch_q = [&](const Item& q) {
+      constexpr int kPieces = D / 8, kStep = 32 / kPieces;
+      const int base = 16 * (warp - 4), piece = lane % kPieces;
+      int x = q.row0 + min(base + (lane & 15), q.nrows - 1), b = q.b;  // padding repeats the last row
+      if (b < 0) b = owner_of(s, reinterpret_cast<const int32_t*>(smem + LY::kCumOff), x);
+      const int r = s.div_g(x);
+      const int at = x + (b * s.L + r) * a.Hq + q.kvh * s.g - r * s.g;
 #pragma unroll 4
-        for (int i = lane / kPieces; i < 16; i += kStep) {
-          const int64_t src = __shfl_sync(0xffffffffu, at, i);
-          const int q_row = base + i;
-          cp_async16(smem_u32(smem) + (piece >> 3) * kAtomBytes + q_row * 128 + (((piece & 7) ^ (q_row & 7)) << 4),
-                     a.q + src * D + piece * 8);
-        }
-        cp_async_wait_all();
-        fence_proxy_async_smem();
-        mbar_arrive(&bars->q_first);
+      for (int i = lane / kPieces; i < 16; i += kStep) {
+        const int64_t src = __shfl_sync(0xffffffffu, at, i);
+        const int q_row = base + i;
+        cp_async16(smem_u32(smem) + (piece >> 3) * kAtomBytes + q_row * 128 + (((piece & 7) ^ (q_row & 7)) << 4),
+                   a.q + src * D + piece * 8);
       }
+    };
+    auto q_here = [&]() {
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      mbar_arrive(&bars->q_full);
+    };
+    Item it = next_item(0);
+    if (it.nblk > 0) {
+      fetch_q(it);
+      q_here();
+    }
+#pragma unroll 1
+    for (int items = 0; it.nblk > 0; ++items) {
+      const bool live = 32 * (warp & 3) < it.nrows;  // else the warp's rows are all padding
       float m_used = -INFINITY, l_sum = 0.f;
       for (int i = st; i < it.nblk; i += 2, ++used) {
         ok = __all_sync(0xffffffffu, wait(&bars->s_full[st], used & 1u));
@@ -677,6 +631,11 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       }
       // join the two streams: each warpgroup takes half of the columns of both accumulators
       tiles.add(it.nblk);
+      const Item next = next_item(items + 1);
+      if (next.nblk > 0) {
+        ok = __all_sync(0xffffffffu, ok && wait(&bars->q_empty, items & 1));
+        if (ok) fetch_q(next);
+      }
       if (ok && st < it.nblk) ok = wait(&bars->pv_done[st], (used - 1) & 1u);
       // every warp is done with the item before, so its statistics may be overwritten
       if (ok && items > 0) ok = wait(&bars->o_free, (items - 1) & 1);
@@ -684,6 +643,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&bars->join);
       ok = ok && wait(&bars->join, items & 1);
+      if (next.nblk > 0) q_here();
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -743,6 +703,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         mbar_arrive(&bars->o_free);
         mbar_arrive(&bars->item_empty[items % kItems]);
       }
+      it = next;
     }
   } else if constexpr (Q8) {
     // ------------------------------------------------------------------ dequantisation
@@ -1054,17 +1015,6 @@ bool cache_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, bool q8, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// q as [B L Hq, D] in boxes of one row's 64-element half (gathered four at a time), swizzled.
-bool query_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int D, int64_t rows) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * D)};
-  const cuuint32_t box[2] = {64, 1};
-  const cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int64_t part_slots(const ec_params& p, bool prefix) {
   const int64_t separate = 2 * kMaxCtas;
   if (!prefix) return separate;
@@ -1116,8 +1066,7 @@ cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_
   Args a;
   const ec_kv& pc = pre ? *prefix : cache;  // without a prefix its maps are not used
   const int pB = pre ? 1 : p.B;
-  if (!query_map(enc, &a.tq, q, p.D, static_cast<int64_t>(p.B) * p.L * p.Hq) ||
-      !cache_map(enc, &a.tk, cache.k, q8, p.D, p.Hkv, p.L, p.B) || !cache_map(enc, &a.tv, cache.v, q8, p.D, p.Hkv, p.L, p.B) ||
+  if (!cache_map(enc, &a.tk, cache.k, q8, p.D, p.Hkv, p.L, p.B) || !cache_map(enc, &a.tv, cache.v, q8, p.D, p.Hkv, p.L, p.B) ||
       !cache_map(enc, &a.tpk, pc.k, q8, p.D, p.Hkv, pc.len, pB) || !cache_map(enc, &a.tpv, pc.v, q8, p.D, p.Hkv, pc.len, pB)) {
     *status = EC_ERR_INVALID_ARG;
     return cudaErrorInvalidValue;
