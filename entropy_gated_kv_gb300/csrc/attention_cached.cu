@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         if (!pl.shared) a.records[cta] = rec;
         if (cta == 0) {
           Header h{};
-          h.records = pl.shared ? pl.otiles : s.ctas;
+          h.records = pl.shared ? pl.otiles : pl.whole != 0 ? 0 : s.ctas;
           h.shared = pl.shared;
           h.prefix_units = pl.nbp + kTileCost;
           h.nbp = pl.nbp;

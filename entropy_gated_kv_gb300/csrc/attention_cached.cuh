@@ -19,6 +19,10 @@
 //             rows into tiles for its own blocks, and every row is merged. Taken when it saves
 //             more than an eighth of the units (tiles that were mostly padding), which pays for
 //             the merge of every row.
+//   whole     as separate, with a tile to a CTA: taken when there are CTAs enough and the longest
+//             tile is not kWholeExtra units above an equal share, as the partial rows and their merge
+//             cost more than that (a ragged batch of 148 tiles of 9 to 16 blocks: 38 us cut into
+//             equal shares, 9 of them the merge).
 #pragma once
 
 #include <cstdint>
@@ -31,6 +35,7 @@ namespace cached {
 constexpr int kBlockM = 128;  // packed query rows per tile (TMEM lanes)
 constexpr int kBlockN = 128;  // keys per block
 constexpr int kTileCost = 3;  // blocks whose time a tile takes beside its own
+constexpr int kWholeExtra = 5;  // units that a merge of all tiles costs
 
 // Floor of x / d, 0 <= x < 2^31, quotients up to a few thousand: `inv` is 1 / d rounded, so the
 // product's floor is at most one off.
@@ -59,6 +64,7 @@ struct Plan {
   int32_t nbp;     // key blocks of the prefix
   int32_t ptiles;  // shared: prefix tiles (KV head major), 0 otherwise
   int32_t otiles;  // tiles of single sequences
+  int32_t whole;   // whole tiles: units of every tile's place in the line, 0 otherwise
   bool shared;
   int32_t rows_l, len_l;  // B <= 32: rows and keys of sequence `lane`
 };
@@ -137,6 +143,8 @@ EC_DEV int blocks_of(int32_t len) { return (len + kBlockN - 1) / kBlockN; }
 // Blocks of one tile of a sequence. A tile without any key still has one block, all of it masked, so
 // that its rows are written (as zeros) or, shared, so that a CTA leaves its record.
 EC_DEV int tile_blocks(const Plan& pl, int32_t len) { return max(1, (pl.shared ? 0 : pl.nbp) + blocks_of(len)); }
+// The units of its place in the line.
+EC_DEV int tile_units(const Plan& pl, int blocks) { return pl.whole != 0 ? pl.whole : blocks + kTileCost; }
 
 // Whole warp.
 EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
@@ -144,7 +152,7 @@ EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
   Plan pl;
   pl.nbp = blocks_of(s.Lp);
   pl.rows_l = pl.len_l = 0;
-  int rows = 0, apart = 0, own = 0, tiles = 0;
+  int rows = 0, apart = 0, own = 0, tiles = 0, longest = 0;
   float most = 0.f;  // units as a float: 2^31 and more are seen there
 #pragma unroll 1
   for (int b = lane; b < s.B; b += 32) {
@@ -159,6 +167,7 @@ EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
     tiles += t;
     apart += t * (max(1, pl.nbp + nb) + kTileCost);
     own += t * (max(1, nb) + kTileCost);
+    if (t > 0) longest = max(longest, max(1, pl.nbp + nb) + kTileCost);
     most += static_cast<float>(t) * static_cast<float>(pl.nbp + nb + 1 + 2 * kTileCost);
   }
   pl.rows = warp_total(rows);
@@ -173,6 +182,7 @@ EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
   pl.shared = false;
   pl.ptiles = pl.own0 = 0;
   pl.units = apart;
+  pl.whole = 0;
   if (pl.nbp > 0 && s.B > 1) {
     const int ptiles = s.Hkv * ((pl.rows + kBlockM - 1) / kBlockM);
     const int together = ptiles * (pl.nbp + kTileCost) + warp_total(own);
@@ -184,6 +194,11 @@ EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
     }
   }
   pl.chunk = max(1, div_up(pl.units, s.ctas));
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (!pl.shared && pl.otiles <= s.ctas && longest <= pl.chunk + kWholeExtra) {
+    pl.whole = pl.chunk = max(1, longest);
+    pl.units = pl.otiles * longest;
+  }
   return pl;
 }
 
@@ -209,7 +224,7 @@ EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c, int&
     for (int b0 = 0;; b0 += 32) {
       int32_t r, n;
       seq_of(s, pl, b0 + lane, r, n);
-      const int t = s.Hkv * tiles_of(s, r), tu = tile_blocks(pl, n) + kTileCost;
+      const int t = s.Hkv * tiles_of(s, r), tu = tile_units(pl, tile_blocks(pl, n));
       int incl = t * tu, src = 0;
       if (s.B > 1) {
         incl = warp_inclusive(incl);
@@ -232,15 +247,16 @@ EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c, int&
       break;
     }
     it.blocks = tile_blocks(pl, it.len);
-    const int w = u - base, tl = div_down(w, it.blocks + kTileCost), per_head = tiles_of(s, rsel);
+    const int units = tile_units(pl, it.blocks);
+    const int w = u - base, tl = div_down(w, units), per_head = tiles_of(s, rsel);
     it.kvh = div_down(tl, per_head);
     it.row0 = (tl - it.kvh * per_head) * kBlockM;
     it.nrows = min(kBlockM, rsel * s.g - it.row0);
     it.np = pl.shared ? 0 : pl.nbp;
-    it.j0 = w - tl * (it.blocks + kTileCost);
+    it.j0 = w - tl * units;
     it.tile = tbase + tl;
   }
-  span = min(it.blocks + kTileCost - it.j0, end - u);
+  span = min(tile_units(pl, it.blocks) - it.j0, end - u);
   it.nblk = max(0, min(it.blocks - it.j0, span));
   // Partial rows. Shared: tile + c grows from item to item, so no two share a slot. Separate: a CTA
   // has at most two incomplete items, one that began before it and one that ends after it.
