@@ -17,10 +17,11 @@
 //                and every product of a stream in the other's way.)
 //                Warp 2 has no work.
 //   warps 4..7   softmax of the CTA's even key blocks, warps 8..11 of the odd ones: two independent
-//                streams with their own S buffer, running maximum and sum, and O accumulator, joined
-//                once per item. One stream's softmax runs while the tensor cores work on the
-//                other's products; with one warpgroup a block takes its softmax and its
-//                products in series, and at 128 rows that is longer than the block's bytes take from HBM.
+//                streams with their own running maximum and sum and O accumulator, joined once per
+//                item. A stream takes a block in two halves of 64 keys with an S buffer each: while one
+//                half's softmax runs, the tensor cores do the other half's P V and the next block's
+//                scores. (With one S buffer of 128 keys a stream's softmax, P V and next scores
+//                follow one another: 4130 cycles a bf16 block, 2100 of them the softmax.)
 //                One TMEM lane (= one packed query row) per thread; online softmax in base 2 with a
 //                lazy rescale of O (only when the running maximum grows by more than 2^8); P in
 //                bf16 written back over the first half of the S buffer. Between an item's last softmax and
@@ -54,7 +55,8 @@ namespace cached {
 namespace {
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 256;  // stream s: S at columns [128 s, 128 s + 128), O at [256 + 128 s, + D)
+constexpr int kHalf = 64;         // keys of an S buffer
+constexpr uint32_t kTmemO = 256;  // stream s: S of half h at columns [128 s + 64 h, + 64), O at [256 + 128 s, + D)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per pipeline wait
@@ -77,7 +79,7 @@ struct Bars {
   uint64_t q_full, q_empty;
   uint64_t unit_full[kMaxUnits], unit_empty[kMaxUnits];
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a stream's halves
   uint64_t join, o_free, v_here[2];  // v_here: a stream's V tile with rows to be zeroed has come
   uint64_t item_full[kItems], item_empty[kItems];
   uint32_t tmem_base;
@@ -166,13 +168,6 @@ EC_DEV uint4 ld_shared16(uint32_t src) {
                  "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),  \
                  "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),  \
                  "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory")
-
-#define EC_TMEM_ST16(taddr, r)                                                                              \
-  asm volatile(                                                                                             \
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" \
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), \
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])          \
-      : "memory")
 
 // Two fp32 lanes in one instruction.
 EC_DEV uint64_t pack_f32x2(float lo, float hi) {
@@ -270,10 +265,10 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       mbar_init(&bars->raw_full[i], 1);
       mbar_init(&bars->raw_empty[i], kDequantWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 4);
-      mbar_init(&bars->pv_done[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bars->s_full[i >> 1][i & 1], 1);
+      mbar_init(&bars->p_full[i >> 1][i & 1], 4);
+      mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
     }
     mbar_init(&bars->join, 8);
     mbar_init(&bars->o_free, 8);
@@ -415,39 +410,42 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     } else if (warp == 1 || warp == 3) {
       // ------------------------------------------------------------------ MMA issuer of one stream
       // The whole warp waits, one thread issues.
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlockN, 0);
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kHalf, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
       const uint32_t st = __shfl_sync(0xffffffffu, warp >> 1, 0);
       const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16), unit0 = smem_u32(smem + LY::kUnitOff);
       const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t s_col = tmem_u + st * kBlockN, o_col = tmem_u + kTmemO + st * 128;
-      uint32_t m0 = 0, used = 0;  // this stream's tiles in the items before; products P V under way or done
+      uint32_t m0 = 0, used = 0;  // this stream's tiles in the items before; blocks whose P V is under way or done
       bool ok = true;
       auto wait_w = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       for (int items = 0; ok; ++items) {
         const Item it = next_item(items);
         if (it.nblk == 0) break;
-        auto issue_qk = [&](int i) {  // S of block i
+        // S of half h of block i; `used` counts the halves' earlier blocks
+        auto issue_qk = [&](int i, int h) {
           const uint32_t m = m0 + (i & ~1), slot = __shfl_sync(0xffffffffu, st * kPer + m % kPer, 0);
           // K is here, and the buffer's last P has been read
-          ok = ok && wait_w(&bars->unit_full[slot], (m / kPer) & 1u) &&
-               (used == 0 || wait_w(&bars->pv_done[st], (used - 1) & 1u));
+          if (h == 0) ok = ok && wait_w(&bars->unit_full[slot], (m / kPer) & 1u);
+          if (used != 0) ok = ok && wait_w(&bars->pv_done[st][h], (used - 1) & 1u);
           if (!ok) return;
           tc_fence_after();
-          const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, 16);
+          const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, 16) + h * (kHalf * 128 / 16);
+          const uint32_t col = s_col + h * kHalf;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(s_col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
-            umma_commit(&bars->s_full[st]);
-            umma_commit(&bars->unit_empty[slot]);
-            if (i + 2 >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last S of the item
+              umma_ss(col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+            umma_commit(&bars->s_full[st][h]);
+            if (h == 1) umma_commit(&bars->unit_empty[slot]);
+            if (h == 1 && i + 2 >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last S of the item
           }
           __syncwarp();
         };
         ok = wait_w(&bars->q_full, items & 1);
         if (static_cast<int>(st) < it.nblk) {
-          issue_qk(st);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) issue_qk(st, h);
         } else {  // nothing of this item falls to stream 1
           if (ok && lane == 0) mbar_arrive(&bars->q_empty);
           if (items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);
@@ -458,21 +456,26 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           ok = wait_w(&bars->unit_full[slot], (m / kPer) & 1u);
           if (!Q8 && ok && ragged(it, it.j0 + i) && lane == 0) mbar_arrive(&bars->v_here[st]);
           if (i < 2 && items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);
-          ok = ok && wait_w(&bars->p_full[st], used & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, kAtomBytes);
-          const uint32_t acc0 = __shfl_sync(0xffffffffu, i > 1 ? 1u : 0u, 0);  // the stream's first block of the item starts O anew
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < kBlockN / 16; ++kk)
-              umma_ts(o_col, s_col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
-            umma_commit(&bars->pv_done[st]);
-            umma_commit(&bars->unit_empty[slot]);
-          }
-          __syncwarp();
           ++used;
-          if (i + 2 < it.nblk) issue_qk(i + 2);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait_w(&bars->p_full[st][h], (used - 1) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, kAtomBytes) + h * (kHalf / 16) * kStepPV;
+            const uint32_t col = s_col + h * kHalf;
+            // the stream's first half of the item starts O anew
+            const uint32_t acc0 = __shfl_sync(0xffffffffu, i > 1 || h > 0 ? 1u : 0u, 0);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kHalf / 16; ++kk)
+                umma_ts(o_col, col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
+              umma_commit(&bars->pv_done[st][h]);
+              if (h == 1) umma_commit(&bars->unit_empty[slot]);
+            }
+            __syncwarp();
+            if (i + 2 < it.nblk) issue_qk(i + 2, h);
+          }
         }
         m0 += (it.nblk + 1 - st) & ~1u;
         if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
@@ -484,7 +487,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     const int st = (warp - 4) >> 2;            // stream
     const int row = 32 * (warp & 3) + lane;    // TMEM lane = packed query row
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t s_addr = tmem + lane_off + st * kBlockN;
     float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
     TileCount tiles;
     uint32_t used = 0, n_ragged = 0;    // blocks of this stream, and those with rows past a length
@@ -519,17 +521,21 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     for (int items = 0; it.nblk > 0; ++items) {
       const bool live = 32 * (warp & 3) < it.nrows;  // else the warp's rows are all padding
       float m_used = -INFINITY, l_sum = 0.f;
-      for (int i = st; i < it.nblk; i += 2, ++used) {
-        ok = __all_sync(0xffffffffu, wait(&bars->s_full[st], used & 1u));
+#pragma unroll 1
+      for (int sub = 2 * st; sub < 2 * it.nblk; sub += (sub & 1) ? 3 : 1) {
+        const int i = sub >> 1, h = sub & 1;
+        const uint32_t s_addr = tmem + lane_off + st * kBlockN + h * kHalf;
+        ok = __all_sync(0xffffffffu, wait(&bars->s_full[st][h], used & 1u));
         if (!ok) break;
-        const int nv = valid_keys(s, it, it.j0 + i);
+        const int nv = valid_keys(s, it, it.j0 + i) - h * kHalf;  // keys of the half that take part: none if 0 or less
         if constexpr (!Q8) {
-          if (ragged(it, it.j0 + i)) {  // their V rows become zeros
+          if (h == 0 && ragged(it, it.j0 + i)) {  // their V rows become zeros
             const uint32_t slot = st * kPer + tiles.tile(i, 1) % kPer;
             ok = __all_sync(0xffffffffu, wait(&bars->v_here[st], n_ragged++ & 1u));
             if (!ok) break;
+            const int n_keys = valid_keys(s, it, it.j0 + i);
             const uint32_t v_tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes);
-            for (int e = nv * 8 + row; e < kBlockN * 8; e += 128)
+            for (int e = n_keys * 8 + row; e < kBlockN * 8; e += 128)
 #pragma unroll
               for (int at = 0; at < LY::kAtoms; ++at) st_shared16(v_tile + at * kAtomBytes + e * 16, make_uint4(0, 0, 0, 0));
             fence_proxy_async_smem();
@@ -537,44 +543,29 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         }
         if (live) {
           tc_fence_after();
-          if (nv < kBlockN) {  // keys that take no part: -infinity in S itself
-#pragma unroll 1
-            for (int c = nv & ~31; c < kBlockN; c += 32) {
-              uint32_t x[32];
-              EC_TMEM_LD32(s_addr + c, x);
-              EC_TMEM_WAIT32(x);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c + e >= nv) x[e] = __float_as_uint(-INFINITY);
-              EC_TMEM_ST32(s_addr + c, x);
-            }
-            tmem_wait_st();
-          }
-          // Two passes over S in chunks of 32 columns, the next chunk's load behind the work on this
-          // one: the maximum (scale > 0 commutes with it), then p = 2^(s scale log2(e) - m). The loops
-          // are rolled to two chunks, and P leaves with each chunk: the passes' code, fetched again
-          // for every block beside the other warps', costs more than reading S twice.
+          // maximum (scale > 0 commutes with it), then p = 2^(s scale log2(e) - m)
           uint32_t b0[32], b1[32];
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto top = [&](const uint32_t (&x)[32]) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-          };
           EC_TMEM_LD32(s_addr, b0);
-#pragma unroll 1
-          for (int c = 0; c < kBlockN; c += 64) {
-            EC_TMEM_WAIT32(b0);
-            EC_TMEM_LD32(s_addr + c + 32, b1);
-            top(b0);
-            EC_TMEM_WAIT32(b1);
-            EC_TMEM_LD32(s_addr + ((c + 64) & 127), b0);  // after the last chunk: the first one again
-            top(b1);
+          EC_TMEM_LD32(s_addr + 32, b1);
+          EC_TMEM_WAIT32(b0);
+          EC_TMEM_WAIT32(b1);
+          if (nv < kHalf) {  // keys that take no part
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (e >= nv) b0[e] = __float_as_uint(-INFINITY);
+              if (32 + e >= nv) b1[e] = __float_as_uint(-INFINITY);
+            }
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            m4[e & 2] = max3(m4[e & 2], __uint_as_float(b0[e]), __uint_as_float(b0[e + 1]));
+            m4[(e & 2) + 1] = max3(m4[(e & 2) + 1], __uint_as_float(b1[e]), __uint_as_float(b1[e + 1]));
           }
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
           bool rescale = false;
           float alpha = 1.f;
-          if (i == st) {
+          if (sub == 2 * st) {
             m_used = mx;
           } else if (mx > m_used + kRescaleLog2) {
             alpha = ex2_approx(m_used - mx);
@@ -586,8 +577,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
           const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
           uint64_t sum2[2] = {0, 0};
-          auto weights = [&](const uint32_t (&x)[32], int c) {  // P over columns of S that have been read
-            uint32_t pk[16];
+          uint32_t pk[32];
+          auto weights = [&](const uint32_t (&x)[32], int c) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               float p0, p1;
@@ -595,24 +586,20 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
               sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
-              pk[e >> 1] = pack_bf16x2(p0, p1);
+              pk[c + (e >> 1)] = pack_bf16x2(p0, p1);
             }
-            EC_TMEM_ST16(s_addr + (c >> 1), pk);
           };
-#pragma unroll 1
-          for (int c = 0; c < kBlockN; c += 64) {
-            EC_TMEM_WAIT32(b0);
-            EC_TMEM_LD32(s_addr + c + 32, b1);
-            weights(b0, c);
-            EC_TMEM_WAIT32(b1);
-            if (c == 0) EC_TMEM_LD32(s_addr + 64, b0);
-            weights(b1, c + 32);
-          }
+          weights(b0, 0);
+          weights(b1, 16);
+          EC_TMEM_ST32(s_addr, pk);  // P over the buffer's first 32 columns
           float sum_lo, sum_hi;
           unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
           l_sum += sum_lo + sum_hi;
-          // the stream's earlier products are done (they were waited for before this S was made)
           if (__any_sync(0xffffffffu, rescale)) {
+            // the half before this one may still be under way into O
+            ok = __all_sync(0xffffffffu, wait(&bars->pv_done[st][h ^ 1], (h ? used : used - 1) & 1u));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -627,7 +614,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           tc_fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[st]);
+        if (lane == 0) mbar_arrive(&bars->p_full[st][h]);
+        used += h;
       }
       // join the two streams: each warpgroup takes half of the columns of both accumulators
       tiles.add(it.nblk);
@@ -636,7 +624,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         ok = __all_sync(0xffffffffu, ok && wait(&bars->q_empty, items & 1));
         if (ok) fetch_q(next);
       }
-      if (ok && st < it.nblk) ok = wait(&bars->pv_done[st], (used - 1) & 1u);
+      if (ok && st < it.nblk) ok = wait(&bars->pv_done[st][1], (used - 1) & 1u);
       // every warp is done with the item before, so its statistics may be overwritten
       if (ok && items > 0) ok = wait(&bars->o_free, (items - 1) & 1);
       stat[st * kBlockM + row] = make_float2(m_used, l_sum);
