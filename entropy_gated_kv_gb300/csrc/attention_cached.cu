@@ -27,15 +27,16 @@
 //                bf16 written back over the first half of the S buffer. Between an item's last softmax and
 //                its join they fetch the next item's query tile, row by row (a tile packs rows of any
 //                sequences, which no one tensor box covers; TMA gathers of four rows took 6000 cycles a tile).
-//   warps 12..19 (8-bit cache) dequantise, four the K tiles and four the V tiles: the producer's TMA
-//                brings the codes into a raw ring, and these warps write the bf16 tiles that the
-//                products read. The dequantised values are exact in bf16, so the products are those of
-//                a bf16 cache with the same values. (Codes loaded from global memory into
-//                registers, without the ring: 180 us for 120 on the long case. The shared memory
-//                that the kernel takes leaves L1 little room for loads in flight.)
+//   warps 12..27 (8-bit cache) dequantise, four warps the K and four the V tiles of each stream: the
+//                producer's TMA brings the codes into a raw ring, and these warps write the bf16
+//                halves that the products read. The dequantised values are exact in bf16, so the
+//                products are those of a bf16 cache with the same values. (Codes loaded from global
+//                memory into registers, without the ring: 180 us for 120 on the long case, as
+//                the shared memory that the kernel takes leaves L1 little room for loads in
+//                flight.)
 // A waiter on an mbarrier sees a phase's parity only: it cannot tell a phase that is complete from one
 // whose predecessor is still open. So whoever waits on a barrier follows every one of its phases: a slot of
-// the K/V ring belongs to one stream, a slot of the raw ring to K or to V.
+// the K/V ring belongs to one stream, a raw tile to K or V of one stream.
 // Keys past a sequence's length may hold anything: their scores are replaced, and their V rows are
 // zeroed in shared memory (0 x NaN is NaN in a matrix product).
 // Partial items write fp32 rows, their maximum and their sum to the workspace; the merge kernel
@@ -61,9 +62,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per pipeline wait
 constexpr int kMaxCtas = 160;                     // bound of the attention grid, for the workspace
-constexpr int kMaxUnits = 6;                      // K or V tiles in shared memory
-constexpr int kMaxRaw = 4;
-constexpr int kDequantWarps = 4;                  // per tile: four warps take the K tiles, four the V tiles
+constexpr int kMaxUnits = 12;                     // halves of K or V tiles in shared memory
+constexpr int kMaxRaw = 4;                        // raw tiles: K and V of each stream
+constexpr int kDequantWarps = 4;                  // for each of them
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 32;  // rows of a tile per merge CTA
 constexpr int kNarrow = 16;
@@ -71,8 +72,9 @@ constexpr int kMergeSteps = kBlockM / kMergeRows;
 constexpr int kItems = 4;       // items handed out and not yet finished, see the producer
 constexpr int kCum = 32;        // sequences whose row ends are kept in shared memory
 constexpr uint32_t kDescHi = sdesc_hi(1024);
-constexpr int kAtomBytes = 128 * 128;  // 128 rows x 128 bytes (64 bf16), 128-byte swizzle
-__host__ __device__ constexpr uint32_t step_qk(int kk) { return (kk >> 2) * (kAtomBytes / 16) + (kk & 3) * 2; }
+constexpr int kAtomBytes = 128 * 128;  // 128 rows x 128 bytes (64 bf16), 128-byte swizzle: the query tile
+constexpr int kHalfAtom = kHalf * 128;  // 64 rows x 128 bytes: K and V
+__host__ __device__ constexpr uint32_t step_k(int kk, int atom) { return (kk >> 2) * (atom / 16) + (kk & 3) * 2; }
 constexpr uint32_t kStepPV = 16 * 128 / 16;
 
 struct Bars {
@@ -86,24 +88,25 @@ struct Bars {
   int abort;
 };
 
-// Shared memory: the query tile, for each stream a ring of bf16 tiles (its blocks' K and V in turn), for the 8-bit
-// cache a ring of raw tiles (128 rows of codes), the row statistics that the two streams exchange,
+// Shared memory: the query tile, for each stream a ring of bf16 half tiles (its blocks' K and V in turn), for
+// the 8-bit cache their raw tiles (128 rows of codes), the row statistics that the two streams exchange,
 // the items, where each sequence's packed rows end, the barriers.
 template <int D, bool Q8>
 struct Layout {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;
-  static constexpr int kUnits = Q8 ? 4 : 6, kPer = kUnits / 2;  // bf16 tiles; of one stream
+  static constexpr int kHalfBytes = kAtoms * kHalfAtom;
+  static constexpr int kUnits = Q8 ? 8 : 12, kPer = kUnits / 2;  // bf16 half tiles; of one stream
   static constexpr int kRaw = Q8 ? kMaxRaw : 0;
   static constexpr int kRawBytes = 128 * D;
   static constexpr int kUnitOff = kTileBytes;
-  static constexpr int kRawOff = kUnitOff + kUnits * kTileBytes;
+  static constexpr int kRawOff = kUnitOff + kUnits * kHalfBytes;
   static constexpr int kStatOff = kRawOff + kRaw * kRawBytes;
   static constexpr int kItemOff = kStatOff + 2 * kBlockM * static_cast<int>(sizeof(float2));
   static constexpr int kCumOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
   static constexpr int kBarOff = kCumOff + kCum * 4;
   static constexpr int kBytes = kBarOff + static_cast<int>(sizeof(Bars));
-  static constexpr int kThreads = Q8 ? 640 : 384;
+  static constexpr int kThreads = Q8 ? 896 : 384;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -168,6 +171,13 @@ EC_DEV uint4 ld_shared16(uint32_t src) {
                  "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),  \
                  "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),  \
                  "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory")
+
+#define EC_TMEM_ST16(taddr, r)                                                                              \
+  asm volatile(                                                                                             \
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" \
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), \
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])          \
+      : "memory")
 
 // Two fp32 lanes in one instruction.
 EC_DEV uint64_t pack_f32x2(float lo, float hi) {
@@ -234,14 +244,14 @@ EC_DEV int valid_keys(const Shape& s, const Item& it, int j) {
   return max(0, min(kBlockN, left));
 }
 
-// K/V tiles of the two streams in the items before: block i of an item goes to stream i % 2, its K and V
-// to two successive places of that stream's ring.
-struct TileCount {
+// Blocks of the two streams in the items before: block i of an item goes to stream i % 2, and its half
+// tiles (K's two, then V's two) to four successive places of that stream's ring.
+struct Streams {
   uint32_t of[2] = {0, 0};
-  EC_DEV uint32_t tile(int i, int kv) const { return (i & 1 ? of[1] : of[0]) + (i & ~1) + kv; }
+  EC_DEV uint32_t block(int i) const { return (i & 1 ? of[1] : of[0]) + (i >> 1); }
   EC_DEV void add(int nblk) {
-    of[0] += (nblk + 1) & ~1;
-    of[1] += nblk & ~1;
+    of[0] += (nblk + 1) >> 1;
+    of[1] += nblk >> 1;
   }
 };
 
@@ -317,10 +327,10 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   // Block j of the item has rows past the sequence's length (a map zero-fills only past the cache's end).
   auto ragged = [&](const Item& it, int j) { return j >= it.np && valid_keys(s, it, j) < kBlockN; };
 
-  // With 20 warps a thread is launched with 96 registers; the softmax warps hold a row of P and take
-  // 144, the others go down to 64: 128 x 64 + 256 x 144 + 256 x 64 = 640 x 96.
+  // With 28 warps a thread is launched with 72 registers; the softmax warps take 112, the others go
+  // down: 128 x 48 + 256 x 112 + 512 x 56 is below 896 x 72.
   if (warp < 4) {
-    if constexpr (Q8) setmaxnreg_dec<64>();
+    if constexpr (Q8) setmaxnreg_dec<48>();
     if (warp == 0) {
       // ------------------------------------------------------------------ plan, TMA producer
       pdl_wait();  // everything above overlaps the previous kernel
@@ -333,8 +343,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         if (lane < s.B) reinterpret_cast<int32_t*>(smem + LY::kCumOff)[lane] = incl;
         __syncwarp();
       }
-      TileCount tiles;
-      uint32_t n = 0;  // tiles requested: K and V of each block in turn
+      Streams streams;
       int ok = 1, count = 0;
       Record rec{};
       for (int u = u0;; ++count) {
@@ -370,27 +379,30 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
             const bool pre = j < it.np;
             const int key0 = (pre ? j : j - it.np) * kBlockN;
             const int b = pre ? 0 : it.b;
-            for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int i = j - it.j0, sto = (i & 1);
+            const uint32_t c = streams.block(i);
+            for (int kv = 0; ok && kv < 2; ++kv) {
               const CUtensorMap* map = kv == 0 ? (pre ? &a.tpk : &a.tk) : (pre ? &a.tpv : &a.tv);
               if constexpr (Q8) {
-                const uint32_t slot = n % LY::kRaw;
-                if (!(ok = wait(&bars->raw_empty[slot], ((n / LY::kRaw) & 1u) ^ 1u))) break;
-                uint8_t* dst = smem + LY::kRawOff + slot * LY::kRawBytes;
-                mbar_arrive_expect_tx(&bars->raw_full[slot], LY::kRawBytes);
-                tma_load_4d(dst, map, &bars->raw_full[slot], 0, it.kvh, key0, b);
+                const int raw = 2 * sto + kv;
+                if (!(ok = wait(&bars->raw_empty[raw], (c & 1u) ^ 1u))) break;
+                mbar_arrive_expect_tx(&bars->raw_full[raw], LY::kRawBytes);
+                tma_load_4d(smem + LY::kRawOff + raw * LY::kRawBytes, map, &bars->raw_full[raw], 0, it.kvh, key0, b);
               } else {
-                const uint32_t m = tiles.tile(j - it.j0, kv), slot = ((j - it.j0) & 1) * kPer + m % kPer;
-                if (!(ok = wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u))) break;
-                uint8_t* dst = smem + LY::kUnitOff + slot * LY::kTileBytes;
-                mbar_arrive_expect_tx(&bars->unit_full[slot], LY::kTileBytes);
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t m = 4 * c + 2 * kv + h, slot = sto * kPer + m % kPer;
+                  if (!(ok = wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u))) break;
+                  uint8_t* dst = smem + LY::kUnitOff + slot * LY::kHalfBytes;
+                  mbar_arrive_expect_tx(&bars->unit_full[slot], LY::kHalfBytes);
 #pragma unroll
-                for (int at = 0; at < LY::kAtoms; ++at)
-                  tma_load_4d(dst + at * kAtomBytes, map, &bars->unit_full[slot], at * 64, it.kvh, key0, b);
+                  for (int at = 0; at < LY::kAtoms; ++at)
+                    tma_load_4d(dst + at * kHalfAtom, map, &bars->unit_full[slot], at * 64, it.kvh, key0 + h * kHalf, b);
+                }
               }
             }
           }
         }
-        tiles.add(it.nblk);
+        streams.add(it.nblk);
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
       if (lane == 0) {
@@ -416,28 +428,28 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       const uint32_t q_lo = sdesc_lo(smem_u32(smem), 16), unit0 = smem_u32(smem + LY::kUnitOff);
       const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t s_col = tmem_u + st * kBlockN, o_col = tmem_u + kTmemO + st * 128;
-      uint32_t m0 = 0, used = 0;  // this stream's tiles in the items before; blocks whose P V is under way or done
+      uint32_t used = 0;  // blocks of this stream whose P V is under way or done
       bool ok = true;
       auto wait_w = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       for (int items = 0; ok; ++items) {
         const Item it = next_item(items);
         if (it.nblk == 0) break;
-        // S of half h of block i; `used` counts the halves' earlier blocks
-        auto issue_qk = [&](int i, int h) {
-          const uint32_t m = m0 + (i & ~1), slot = __shfl_sync(0xffffffffu, st * kPer + m % kPer, 0);
+        // S of half h of the stream's block c (block i of the item)
+        auto issue_qk = [&](int i, uint32_t c, int h) {
+          const uint32_t m = 4 * c + h, slot = __shfl_sync(0xffffffffu, st * kPer + m % kPer, 0);
           // K is here, and the buffer's last P has been read
-          if (h == 0) ok = ok && wait_w(&bars->unit_full[slot], (m / kPer) & 1u);
-          if (used != 0) ok = ok && wait_w(&bars->pv_done[st][h], (used - 1) & 1u);
+          ok = ok && wait_w(&bars->unit_full[slot], (m / kPer) & 1u);
+          if (c != 0) ok = ok && wait_w(&bars->pv_done[st][h], (c - 1) & 1u);
           if (!ok) return;
           tc_fence_after();
-          const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, 16) + h * (kHalf * 128 / 16);
+          const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kHalfBytes, 16);
           const uint32_t col = s_col + h * kHalf;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(col, q_lo + step_qk(kk), k_lo + step_qk(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+              umma_ss(col, q_lo + step_k(kk, kAtomBytes), k_lo + step_k(kk, kHalfAtom), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
             umma_commit(&bars->s_full[st][h]);
-            if (h == 1) umma_commit(&bars->unit_empty[slot]);
+            umma_commit(&bars->unit_empty[slot]);
             if (h == 1 && i + 2 >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last S of the item
           }
           __syncwarp();
@@ -445,24 +457,24 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         ok = wait_w(&bars->q_full, items & 1);
         if (static_cast<int>(st) < it.nblk) {
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) issue_qk(st, h);
+          for (int h = 0; h < 2; ++h) issue_qk(st, used, h);
         } else {  // nothing of this item falls to stream 1
           if (ok && lane == 0) mbar_arrive(&bars->q_empty);
           if (items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);
         }
 #pragma unroll 1
         for (int i = st; ok && i < it.nblk; i += 2) {
-          const uint32_t m = m0 + (i & ~1) + 1, slot = __shfl_sync(0xffffffffu, st * kPer + m % kPer, 0);
-          ok = wait_w(&bars->unit_full[slot], (m / kPer) & 1u);
-          if (!Q8 && ok && ragged(it, it.j0 + i) && lane == 0) mbar_arrive(&bars->v_here[st]);
-          if (i < 2 && items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);
-          ++used;
+          if (i < 2 && items > 0) ok = wait_w(&bars->o_free, (items - 1) & 1);
+          const uint32_t c = used++;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            ok = ok && wait_w(&bars->p_full[st][h], (used - 1) & 1u);
+            const uint32_t m = 4 * c + 2 + h, slot = __shfl_sync(0xffffffffu, st * kPer + m % kPer, 0);
+            ok = ok && wait_w(&bars->unit_full[slot], (m / kPer) & 1u);
+            if (!Q8 && ok && ragged(it, it.j0 + i) && lane == 0) mbar_arrive(&bars->v_here[st]);
+            ok = ok && wait_w(&bars->p_full[st][h], c & 1u);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kTileBytes, kAtomBytes) + h * (kHalf / 16) * kStepPV;
+            const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kHalfBytes, kHalfAtom);
             const uint32_t col = s_col + h * kHalf;
             // the stream's first half of the item starts O anew
             const uint32_t acc0 = __shfl_sync(0xffffffffu, i > 1 || h > 0 ? 1u : 0u, 0);
@@ -471,24 +483,23 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
               for (int kk = 0; kk < kHalf / 16; ++kk)
                 umma_ts(o_col, col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
               umma_commit(&bars->pv_done[st][h]);
-              if (h == 1) umma_commit(&bars->unit_empty[slot]);
+              umma_commit(&bars->unit_empty[slot]);
             }
             __syncwarp();
-            if (i + 2 < it.nblk) issue_qk(i + 2, h);
+            if (i + 2 < it.nblk) issue_qk(i + 2, c + 1, h);
           }
         }
-        m0 += (it.nblk + 1 - st) & ~1u;
         if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
       }
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ softmax + epilogue
-    if constexpr (Q8) setmaxnreg_inc<144>();
+    if constexpr (Q8) setmaxnreg_inc<112>();
     const int st = (warp - 4) >> 2;            // stream
     const int row = 32 * (warp & 3) + lane;    // TMEM lane = packed query row
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
-    TileCount tiles;
+    Streams streams;
     uint32_t used = 0, n_ragged = 0;    // blocks of this stream, and those with rows past a length
     bool ok = true;
     // An item's query tile, 16 rows a warp: each lane finds one row, and all fetch 16-byte pieces.
@@ -529,15 +540,14 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         if (!ok) break;
         const int nv = valid_keys(s, it, it.j0 + i) - h * kHalf;  // keys of the half that take part: none if 0 or less
         if constexpr (!Q8) {
-          if (h == 0 && ragged(it, it.j0 + i)) {  // their V rows become zeros
-            const uint32_t slot = st * kPer + tiles.tile(i, 1) % kPer;
+          if (ragged(it, it.j0 + i)) {  // their V rows become zeros
+            const uint32_t m = 4 * streams.block(i) + 2 + h, slot = st * kPer + m % kPer;
             ok = __all_sync(0xffffffffu, wait(&bars->v_here[st], n_ragged++ & 1u));
             if (!ok) break;
-            const int n_keys = valid_keys(s, it, it.j0 + i);
-            const uint32_t v_tile = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes);
-            for (int e = n_keys * 8 + row; e < kBlockN * 8; e += 128)
+            const uint32_t v_half = smem_u32(smem + LY::kUnitOff + slot * LY::kHalfBytes);
+            for (int e = max(nv, 0) * 8 + row; e < kHalf * 8; e += 128)
 #pragma unroll
-              for (int at = 0; at < LY::kAtoms; ++at) st_shared16(v_tile + at * kAtomBytes + e * 16, make_uint4(0, 0, 0, 0));
+              for (int at = 0; at < LY::kAtoms; ++at) st_shared16(v_half + at * kHalfAtom + e * 16, make_uint4(0, 0, 0, 0));
             fence_proxy_async_smem();
           }
         }
@@ -577,8 +587,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
           const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
           uint64_t sum2[2] = {0, 0};
-          uint32_t pk[32];
-          auto weights = [&](const uint32_t (&x)[32], int c) {
+          auto weights = [&](const uint32_t (&x)[32], int c) {  // P over the buffer's first 32 columns
+            uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               float p0, p1;
@@ -586,12 +596,12 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
               sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
-              pk[c + (e >> 1)] = pack_bf16x2(p0, p1);
+              pk[e >> 1] = pack_bf16x2(p0, p1);
             }
+            EC_TMEM_ST16(s_addr + c, pk);
           };
           weights(b0, 0);
           weights(b1, 16);
-          EC_TMEM_ST32(s_addr, pk);  // P over the buffer's first 32 columns
           float sum_lo, sum_hi;
           unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
           l_sum += sum_lo + sum_hi;
@@ -618,7 +628,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         used += h;
       }
       // join the two streams: each warpgroup takes half of the columns of both accumulators
-      tiles.add(it.nblk);
+      streams.add(it.nblk);
       const Item next = next_item(items + 1);
       if (next.nblk > 0) {
         ok = __all_sync(0xffffffffu, ok && wait(&bars->q_empty, items & 1));
@@ -695,8 +705,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     }
   } else if constexpr (Q8) {
     // ------------------------------------------------------------------ dequantisation
-    setmaxnreg_dec<64>();
-    // A thread takes a 16-code piece of kPieces rows: eight lanes read 128 neighbouring bytes, and the
+    setmaxnreg_dec<56>();
+    // A thread takes a 16-code piece of a row per step: eight lanes read 128 neighbouring bytes, and the
     // 16-byte pieces of bf16 that they store fall into eight different bank groups: for D = 128
     // lanes 0..3 take the first half of row r and lanes 4..7 the second half of row r ^ 1, whose
     // swizzle differs in the lowest bit. A thread's rows differ by multiples of 8, so its places in
@@ -704,87 +714,90 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     constexpr int kPieces = D / 16;            // 16-code pieces of a row = steps over the tile's rows
     constexpr int kRowsStep = 128 / kPieces;   // rows of a step
     constexpr int kRowsWarp = 32 / kPieces;    // of a warp
-    const int kv = warp >= 16, w4 = warp & 3, piece = lane % kPieces;
+    const int kv = ((warp >> 2) & 1) ^ 1, st = warp >= 20, raw = 2 * st + kv, w4 = warp & 3, piece = lane % kPieces;
     const int sub = D == 128 ? (lane / kPieces) ^ (piece >> 2) : lane / kPieces;  // row of the warp's
     const int row0 = w4 * kRowsWarp + sub;
     const int exp_row = (lane / kRowsWarp) * kRowsStep + w4 * kRowsWarp + lane % kRowsWarp;
-    const uint32_t src_off = row0 * D + piece * 16;
-    const uint32_t dst_off = (piece >> 2) * kAtomBytes + row0 * 128 + ((((piece & 3) * 2) ^ (row0 & 7)) << 4);
-    TileCount tiles;
-    uint32_t n = kv;
+    const uint32_t src0 = smem_u32(smem + LY::kRawOff + raw * LY::kRawBytes) + row0 * D + piece * 16;
+    const uint32_t dst_off = (piece >> 2) * kHalfAtom + row0 * 128 + ((((piece & 3) * 2) ^ (row0 & 7)) << 4);
+    uint32_t c = 0;  // the stream's blocks
     bool ok = true;
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
-      // the exponent of this lane's row, a block ahead (past the cache's end: any)
+      // the exponent of this lane's row, one of the stream's blocks ahead (past the cache's end: any)
       const uint8_t* ep = nullptr;
       int left = 0;  // positions from the lane's row to the cache's end
       auto exponent = [&](int j) {
-        if (j == it.j0 || j == it.np) {
+        if (j < it.j0 + 2 || (j >= it.np && j < it.np + 2)) {
           const bool pre = j < it.np;
           const int key = (pre ? j : j - it.np) * kBlockN + exp_row, b = pre ? 0 : it.b;
           left = (pre ? s.Lp : s.L) - key;
           ep = (pre ? a.pexps : a.exps)[kv] + (static_cast<int64_t>(b) * s.Hkv + it.kvh) * (pre ? a.Lps : a.Ls) + key;
         } else {
-          left -= kBlockN;
-          ep += kBlockN;
+          left -= 2 * kBlockN;
+          ep += 2 * kBlockN;
         }
         return left > 0 ? static_cast<int>(__ldg(ep)) : kExpZeroByte;
       };
-      int e_next = exponent(it.j0);
-      for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j, n += 2) {
-        const int nv = kv ? valid_keys(s, it, j) : kBlockN;
-        const int e_here = e_next;
-        if (j + 1 < it.j0 + it.nblk) e_next = exponent(j + 1);
-        const int i0 = j - it.j0;
-        const uint32_t m = tiles.tile(i0, kv), rs = n % LY::kRaw, slot = (i0 & 1) * kPer + m % kPer;
-        ok = __all_sync(0xffffffffu, wait(&bars->raw_full[rs], (n / LY::kRaw) & 1u) &&
-                                         wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u));
-        if (!ok) break;
-        uint32_t src = smem_u32(smem + LY::kRawOff + rs * LY::kRawBytes) + src_off;
-        uint32_t dst = smem_u32(smem + LY::kUnitOff + slot * LY::kTileBytes) + dst_off;
-        if (nv == kBlockN && __all_sync(0xffffffffu, e_here <= kExpOneFactor)) {
-          uint4 w = ld_shared16(src);
-#pragma unroll 2
-          for (int i = 0; i < kPieces; ++i) {
-            const uint4 here = w;
-            src += kRowsStep * D;
-            if (i + 1 < kPieces) w = ld_shared16(src);
-            const uint32_t f = dequant_factor(__shfl_sync(0xffffffffu, e_here, i * kRowsWarp + sub));
-            uint4 lo, hi;
-            dequantise4(here.x, f, lo.x, lo.y);
-            dequantise4(here.y, f, lo.z, lo.w);
-            dequantise4(here.z, f, hi.x, hi.y);
-            dequantise4(here.w, f, hi.z, hi.w);
-            st_shared16(dst, lo);
-            st_shared16(dst ^ 16u, hi);
-            dst += kRowsStep * 128;
-          }
-        } else {  // large exponents, NaN rows, V rows past the length (zeros, whatever lies there)
+      int e_next = st < it.nblk ? exponent(it.j0 + st) : 0;
 #pragma unroll 1
-          for (int i = 0; i < kPieces; ++i) {
-            const uint4 here = ld_shared16(src);
-            const DequantScale sc = dequant_scale(__shfl_sync(0xffffffffu, e_here, i * kRowsWarp + sub));
-            uint4 lo, hi;
-            dequantise4(here.x, sc, lo.x, lo.y);
-            dequantise4(here.y, sc, lo.z, lo.w);
-            dequantise4(here.z, sc, hi.x, hi.y);
-            dequantise4(here.w, sc, hi.z, hi.w);
-            if (row0 + i * kRowsStep >= nv) lo = hi = make_uint4(0, 0, 0, 0);
-            st_shared16(dst, lo);
-            st_shared16(dst ^ 16u, hi);
-            src += kRowsStep * D;
-            dst += kRowsStep * 128;
+      for (int i = st; ok && i < it.nblk; i += 2, ++c) {
+        const int nv = kv ? valid_keys(s, it, it.j0 + i) : kBlockN;
+        const int e_here = e_next;
+        if (i + 2 < it.nblk) e_next = exponent(it.j0 + i + 2);
+        ok = __all_sync(0xffffffffu, wait(&bars->raw_full[raw], c & 1u));
+        const bool plain = nv == kBlockN && __all_sync(0xffffffffu, e_here <= kExpOneFactor);
+#pragma unroll 1
+        for (int h = 0; ok && h < 2; ++h) {
+          const uint32_t m = 4 * c + 2 * kv + h, slot = st * kPer + m % kPer;
+          ok = __all_sync(0xffffffffu, wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u));
+          if (!ok) break;
+          uint32_t src = src0 + h * kHalf * D;
+          uint32_t dst = smem_u32(smem + LY::kUnitOff + slot * LY::kHalfBytes) + dst_off;
+          const int q0 = h * (kPieces / 2);
+          if (plain) {
+            uint4 w = ld_shared16(src);
+#pragma unroll 2
+            for (int q = 0; q < kPieces / 2; ++q) {
+              const uint4 here = w;
+              src += kRowsStep * D;
+              if (q + 1 < kPieces / 2) w = ld_shared16(src);
+              const uint32_t f = dequant_factor(__shfl_sync(0xffffffffu, e_here, (q0 + q) * kRowsWarp + sub));
+              uint4 lo, hi;
+              dequantise4(here.x, f, lo.x, lo.y);
+              dequantise4(here.y, f, lo.z, lo.w);
+              dequantise4(here.z, f, hi.x, hi.y);
+              dequantise4(here.w, f, hi.z, hi.w);
+              st_shared16(dst, lo);
+              st_shared16(dst ^ 16u, hi);
+              dst += kRowsStep * 128;
+            }
+          } else {  // large exponents, NaN rows, V rows past the length (zeros, whatever lies there)
+#pragma unroll 1
+            for (int q = 0; q < kPieces / 2; ++q) {
+              const uint4 here = ld_shared16(src);
+              const DequantScale sc = dequant_scale(__shfl_sync(0xffffffffu, e_here, (q0 + q) * kRowsWarp + sub));
+              uint4 lo, hi;
+              dequantise4(here.x, sc, lo.x, lo.y);
+              dequantise4(here.y, sc, lo.z, lo.w);
+              dequantise4(here.z, sc, hi.x, hi.y);
+              dequantise4(here.w, sc, hi.z, hi.w);
+              if (row0 + (q0 + q) * kRowsStep >= nv) lo = hi = make_uint4(0, 0, 0, 0);
+              st_shared16(dst, lo);
+              st_shared16(dst ^ 16u, hi);
+              src += kRowsStep * D;
+              dst += kRowsStep * 128;
+            }
           }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->raw_empty[rs]);
-          mbar_arrive(&bars->unit_full[slot]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (h == 1) mbar_arrive(&bars->raw_empty[raw]);
+            mbar_arrive(&bars->unit_full[slot]);
+          }
         }
       }
-      tiles.add(it.nblk);
     }
   }
 
@@ -988,14 +1001,14 @@ EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-// A cache [B, L, Hkv, D] in boxes of 128 positions of one head: bf16 in swizzled 64-element halves,
-// codes whole and unswizzled. Rows past L read as zeros.
+// A cache [B, L, Hkv, D] in boxes of one head: bf16 in 64 positions by 64 swizzled elements, codes in 128
+// whole unswizzled positions. Rows past L read as zeros.
 bool cache_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, bool q8, int D, int Hkv, int L, int B) {
   const cuuint64_t e = q8 ? 1 : 2;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(L),
                               static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {e * D, e * D * Hkv, e * D * Hkv * L};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(q8 ? D : 64), 1, kBlockN, 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(q8 ? D : 64), 1, static_cast<cuuint32_t>(q8 ? kBlockN : kHalf), 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
