@@ -10,12 +10,11 @@
 //   keys and the sequence's own kv_len[b] keys, KV head h / g;  zeros when there is no key
 //
 // Structure (one CTA per SM; the work plan is attention_cached.cuh's):
-//   warp 0       makes the work plan, hands out the CTA's items, and is the TMA producer: K and V
-//                blocks of 128 keys.
-//   warps 1, 3   issue tcgen05.mma, each for one of two streams (below); warp 1 allocates 512 TMEM
+//   warps 0, 2   make the work plan and are the TMA producers, each for one of two streams (below): halves of
+//                64 keys; warp 0 hands out the CTA's items to the others.
+//   warps 1, 3   issue tcgen05.mma, each for one stream; warp 1 allocates 512 TMEM
 //                columns. (One issuer for both: 102 us for 85 on the long 8-bit case, every wait
 //                and every product of a stream in the other's way.)
-//                Warp 2 has no work.
 //   warps 4..7   softmax of the CTA's even key blocks, warps 8..11 of the odd ones: two independent
 //                streams with their own running maximum and sum and O accumulator, joined once per
 //                item. A stream takes a block in two halves of 64 keys with an S buffer each: while one
@@ -28,15 +27,17 @@
 //                its join they fetch the next item's query tile, row by row (a tile packs rows of any
 //                sequences, which no one tensor box covers; TMA gathers of four rows took 6000 cycles a tile).
 //   warps 12..27 (8-bit cache) dequantise, four warps the K and four the V tiles of each stream: the
-//                producer's TMA brings the codes into a raw ring, and these warps write the bf16
+//                producers' TMA brings the codes into raw halves, and these warps write the bf16
 //                halves that the products read. The dequantised values are exact in bf16, so the
-//                products are those of a bf16 cache with the same values. (Codes loaded from global
+//                products are those of a bf16 cache with the same values. (Raw tiles of 128 keys and
+//                one producer: 93 us for 84 on the long 8-bit case, a tile's refill not under way before all of it
+//                was read. Codes loaded from global
 //                memory into registers, without the ring: 180 us for 120 on the long case, as
 //                the shared memory that the kernel takes leaves L1 little room for loads in
 //                flight.)
 // A waiter on an mbarrier sees a phase's parity only: it cannot tell a phase that is complete from one
 // whose predecessor is still open. So whoever waits on a barrier follows every one of its phases: a slot of
-// the K/V ring belongs to one stream, a raw tile to K or V of one stream.
+// the K/V ring belongs to one stream, a raw half to K or V of one stream.
 // Keys past a sequence's length may hold anything: their scores are replaced, and their V rows are
 // zeroed in shared memory (0 x NaN is NaN in a matrix product).
 // Partial items write fp32 rows, their maximum and their sum to the workspace; the merge kernel
@@ -63,8 +64,8 @@ constexpr float kRescaleLog2 = 8.f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per pipeline wait
 constexpr int kMaxCtas = 160;                     // bound of the attention grid, for the workspace
 constexpr int kMaxUnits = 12;                     // halves of K or V tiles in shared memory
-constexpr int kMaxRaw = 4;                        // raw tiles: K and V of each stream
-constexpr int kDequantWarps = 4;                  // for each of them
+constexpr int kMaxRaw = 8;                        // halves of raw tiles: K and V of each stream
+constexpr int kDequantWarps = 4;                  // for K and for V of each stream
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 32;  // rows of a tile per merge CTA
 constexpr int kNarrow = 16;
@@ -89,7 +90,7 @@ struct Bars {
 };
 
 // Shared memory: the query tile, for each stream a ring of bf16 half tiles (its blocks' K and V in turn), for
-// the 8-bit cache their raw tiles (128 rows of codes), the row statistics that the two streams exchange,
+// the 8-bit cache their raw halves (64 rows of codes), the row statistics that the two streams exchange,
 // the items, where each sequence's packed rows end, the barriers.
 template <int D, bool Q8>
 struct Layout {
@@ -98,7 +99,7 @@ struct Layout {
   static constexpr int kHalfBytes = kAtoms * kHalfAtom;
   static constexpr int kUnits = Q8 ? 8 : 12, kPer = kUnits / 2;  // bf16 half tiles; of one stream
   static constexpr int kRaw = Q8 ? kMaxRaw : 0;
-  static constexpr int kRawBytes = 128 * D;
+  static constexpr int kRawBytes = kHalf * D;
   static constexpr int kUnitOff = kTileBytes;
   static constexpr int kRawOff = kUnitOff + kUnits * kHalfBytes;
   static constexpr int kStatOff = kRawOff + kRaw * kRawBytes;
@@ -331,14 +332,16 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   // down: 128 x 48 + 256 x 112 + 512 x 56 is below 896 x 72.
   if (warp < 4) {
     if constexpr (Q8) setmaxnreg_dec<48>();
-    if (warp == 0) {
-      // ------------------------------------------------------------------ plan, TMA producer
+    if (warp == 0 || warp == 2) {
+      // ------------------------------------------------------------------ plan, TMA producer of one stream
+      // Both warps make the plan and walk the items; warp 0 hands them out.
+      const int st = warp >> 1;
       pdl_wait();  // everything above overlaps the previous kernel
       const int cta = static_cast<int>(blockIdx.x);
-      const Plan pl = make_plan(s, a.dev_err, cta == 0);
+      const Plan pl = make_plan(s, a.dev_err, cta == 0 && warp == 0);
       pdl_launch_dependents();
       const int u0 = min(pl.units, cta * pl.chunk), uend = *abort_flag ? u0 : min(pl.units, u0 + pl.chunk);
-      if (pl.shared && s.B <= kCum) {
+      if (warp == 0 && pl.shared && s.B <= kCum) {
         const int incl = warp_inclusive(pl.rows_l * s.g);
         if (lane < s.B) reinterpret_cast<int32_t*>(smem + LY::kCumOff)[lane] = incl;
         __syncwarp();
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           it = cta_item(s, pl, u, uend, cta, span);
           u += span;
         }
-        if (lane == 0) {
+        if (warp == 0 && lane == 0) {
           if (!wait(&bars->item_empty[count % kItems], ((count / kItems) & 1) ^ 1)) it.nblk = 0;
           items_s[count % kItems] = it;
           mbar_arrive(&bars->item_full[count % kItems]);
@@ -372,32 +375,36 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           rec.a1 = it.slot;
           rec.a2 = pl.shared ? it.slot : 2 * (cta + 1);
           rec.n2 = last - cta + (pl.shared ? 1 : 0);
-          if (pl.shared && lane == 0) a.records[it.tile - pl.ptiles] = rec;
+          if (pl.shared && threadIdx.x == 0) a.records[it.tile - pl.ptiles] = rec;
         }
         if (lane == 0) {
-          for (int j = it.j0; ok && j < it.j0 + it.nblk; ++j) {
+#pragma unroll 1
+          for (int i = st; ok && i < it.nblk; i += 2) {
+            const int j = it.j0 + i;
             const bool pre = j < it.np;
             const int key0 = (pre ? j : j - it.np) * kBlockN;
             const int b = pre ? 0 : it.b;
-            const int i = j - it.j0, sto = (i & 1);
             const uint32_t c = streams.block(i);
-            for (int kv = 0; ok && kv < 2; ++kv) {
+#pragma unroll 1
+            for (int n = 0; n < 4; ++n) {
+              // bf16: K's halves, then V's, as the products want them; 8-bit: the halves of both by turns,
+              // as their warps dequantise them
+              const int kv = Q8 ? n & 1 : n >> 1, h = Q8 ? n >> 1 : n & 1;
               const CUtensorMap* map = kv == 0 ? (pre ? &a.tpk : &a.tk) : (pre ? &a.tpv : &a.tv);
               if constexpr (Q8) {
-                const int raw = 2 * sto + kv;
+                const int raw = 4 * st + 2 * kv + h;
                 if (!(ok = wait(&bars->raw_empty[raw], (c & 1u) ^ 1u))) break;
                 mbar_arrive_expect_tx(&bars->raw_full[raw], LY::kRawBytes);
-                tma_load_4d(smem + LY::kRawOff + raw * LY::kRawBytes, map, &bars->raw_full[raw], 0, it.kvh, key0, b);
+                tma_load_4d(smem + LY::kRawOff + raw * LY::kRawBytes, map, &bars->raw_full[raw], 0, it.kvh,
+                            key0 + h * kHalf, b);
               } else {
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t m = 4 * c + 2 * kv + h, slot = sto * kPer + m % kPer;
-                  if (!(ok = wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u))) break;
-                  uint8_t* dst = smem + LY::kUnitOff + slot * LY::kHalfBytes;
-                  mbar_arrive_expect_tx(&bars->unit_full[slot], LY::kHalfBytes);
+                const uint32_t m = 4 * c + n, slot = st * kPer + m % kPer;
+                if (!(ok = wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u))) break;
+                uint8_t* dst = smem + LY::kUnitOff + slot * LY::kHalfBytes;
+                mbar_arrive_expect_tx(&bars->unit_full[slot], LY::kHalfBytes);
 #pragma unroll
-                  for (int at = 0; at < LY::kAtoms; ++at)
-                    tma_load_4d(dst + at * kHalfAtom, map, &bars->unit_full[slot], at * 64, it.kvh, key0 + h * kHalf, b);
-                }
+                for (int at = 0; at < LY::kAtoms; ++at)
+                  tma_load_4d(dst + at * kHalfAtom, map, &bars->unit_full[slot], at * 64, it.kvh, key0 + h * kHalf, b);
               }
             }
           }
@@ -405,7 +412,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         streams.add(it.nblk);
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      if (lane == 0) {
+      if (threadIdx.x == 0) {
         if (!pl.shared) a.records[cta] = rec;
         if (cta == 0) {
           Header h{};
@@ -714,7 +721,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     constexpr int kPieces = D / 16;            // 16-code pieces of a row = steps over the tile's rows
     constexpr int kRowsStep = 128 / kPieces;   // rows of a step
     constexpr int kRowsWarp = 32 / kPieces;    // of a warp
-    const int kv = ((warp >> 2) & 1) ^ 1, st = warp >= 20, raw = 2 * st + kv, w4 = warp & 3, piece = lane % kPieces;
+    const int kv = ((warp >> 2) & 1) ^ 1, st = warp >= 20, raw = 4 * st + 2 * kv, w4 = warp & 3, piece = lane % kPieces;
     const int sub = D == 128 ? (lane / kPieces) ^ (piece >> 2) : lane / kPieces;  // row of the warp's
     const int row0 = w4 * kRowsWarp + sub;
     const int exp_row = (lane / kRowsWarp) * kRowsStep + w4 * kRowsWarp + lane % kRowsWarp;
@@ -746,12 +753,11 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         const int nv = kv ? valid_keys(s, it, it.j0 + i) : kBlockN;
         const int e_here = e_next;
         if (i + 2 < it.nblk) e_next = exponent(it.j0 + i + 2);
-        ok = __all_sync(0xffffffffu, wait(&bars->raw_full[raw], c & 1u));
         const bool plain = nv == kBlockN && __all_sync(0xffffffffu, e_here <= kExpOneFactor);
 #pragma unroll 1
         for (int h = 0; ok && h < 2; ++h) {
           const uint32_t m = 4 * c + 2 * kv + h, slot = st * kPer + m % kPer;
-          ok = __all_sync(0xffffffffu, wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u));
+          ok = __all_sync(0xffffffffu, wait(&bars->raw_full[raw + h], c & 1u) && wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u));
           if (!ok) break;
           uint32_t src = src0 + h * kHalf * D;
           uint32_t dst = smem_u32(smem + LY::kUnitOff + slot * LY::kHalfBytes) + dst_off;
@@ -793,7 +799,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (h == 1) mbar_arrive(&bars->raw_empty[raw]);
+            mbar_arrive(&bars->raw_empty[raw + h]);
             mbar_arrive(&bars->unit_full[slot]);
           }
         }
@@ -1001,14 +1007,14 @@ EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-// A cache [B, L, Hkv, D] in boxes of one head: bf16 in 64 positions by 64 swizzled elements, codes in 128
+// A cache [B, L, Hkv, D] in boxes of one head: bf16 in 64 positions by 64 swizzled elements, codes in 64
 // whole unswizzled positions. Rows past L read as zeros.
 bool cache_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, bool q8, int D, int Hkv, int L, int B) {
   const cuuint64_t e = q8 ? 1 : 2;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(L),
                               static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {e * D, e * D * Hkv, e * D * Hkv * L};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(q8 ? D : 64), 1, static_cast<cuuint32_t>(q8 ? kBlockN : kHalf), 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(q8 ? D : 64), 1, static_cast<cuuint32_t>(kHalf), 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
