@@ -753,6 +753,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         const int nv = kv ? valid_keys(s, it, it.j0 + i) : kBlockN;
         const int e_here = e_next;
         if (i + 2 < it.nblk) e_next = exponent(it.j0 + i + 2);
+        const uint32_t f_here = dequant_factor(e_here);
         const bool plain = nv == kBlockN && __all_sync(0xffffffffu, e_here <= kExpOneFactor);
 #pragma unroll 1
         for (int h = 0; ok && h < 2; ++h) {
@@ -764,20 +765,18 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           const int q0 = h * (kPieces / 2);
           if (plain) {
             uint4 w = ld_shared16(src);
-#pragma unroll 2
+#pragma unroll
             for (int q = 0; q < kPieces / 2; ++q) {
               const uint4 here = w;
-              src += kRowsStep * D;
-              if (q + 1 < kPieces / 2) w = ld_shared16(src);
-              const uint32_t f = dequant_factor(__shfl_sync(0xffffffffu, e_here, (q0 + q) * kRowsWarp + sub));
+              if (q + 1 < kPieces / 2) w = ld_shared16(src + (q + 1) * kRowsStep * D);
+              const uint32_t f = __shfl_sync(0xffffffffu, f_here, q0 * kRowsWarp + sub + q * kRowsWarp);
               uint4 lo, hi;
               dequantise4(here.x, f, lo.x, lo.y);
               dequantise4(here.y, f, lo.z, lo.w);
               dequantise4(here.z, f, hi.x, hi.y);
               dequantise4(here.w, f, hi.z, hi.w);
-              st_shared16(dst, lo);
-              st_shared16(dst ^ 16u, hi);
-              dst += kRowsStep * 128;
+              st_shared16(dst + q * kRowsStep * 128, lo);
+              st_shared16((dst ^ 16u) + q * kRowsStep * 128, hi);
             }
           } else {  // large exponents, NaN rows, V rows past the length (zeros, whatever lies there)
 #pragma unroll 1
