@@ -118,6 +118,9 @@ class Params:
         self.__dict__.pop("_ref", None)
         self.__dict__[name] = value
 
+    def __getstate__(self):  # copies and pickles hold the fields only
+        return {n: v for n, v in self.__dict__.items() if n != "_ref"}
+
 
 class DecodeState:
     """Per-sequence decode state (ec_state) as CUDA tensors."""
@@ -348,16 +351,21 @@ class QuantCache:
     __slots__ = ("k", "v", "k_exp", "v_exp", "_c", "_at")
 
     def __init__(self, k, v, k_exp, v_exp):
-        self._c = _Cache(C.EC_E4M3, k, v, k_exp, v_exp)
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
-        self._at = (k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr())
+        self.view()
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, "_c", None)
+        object.__setattr__(self, name, value)
+
+    def _places(self):
+        return self.k.data_ptr(), self.v.data_ptr(), self.k_exp.data_ptr(), self.v_exp.data_ptr()
 
     def view(self) -> _Cache:
         """The checked C view; made again when a tensor has been exchanged or has moved."""
-        at = (self.k.data_ptr(), self.v.data_ptr(), self.k_exp.data_ptr(), self.v_exp.data_ptr())
-        if at != self._at:
-            self._c = _Cache(C.EC_E4M3, self.k, self.v, self.k_exp, self.v_exp)
-            self._at = at
+        if self._c is None or self._at != self._places():
+            object.__setattr__(self, "_c", _Cache(C.EC_E4M3, self.k, self.v, self.k_exp, self.v_exp))
+            object.__setattr__(self, "_at", self._places())
         return self._c
 
     @classmethod

@@ -347,6 +347,7 @@ ec_status ec_partial_attention(const ec_params* p, const void* q, const void* k_
 // ---- 8-bit cache, shared prefix ------------------------------------------------------------------
 namespace {
 
+size_t int_bytes(size_t n) { return n * sizeof(int32_t); }
 size_t kv_extent(const ec_params& p, const ec_kv& c, int32_t B) {
   return static_cast<size_t>(B) * c.len * p.Hkv * p.D * (c.dtype == EC_BF16 ? 2 : 1);
 }
@@ -383,7 +384,7 @@ ec_status cached_attention(const ec_params* p, const void* q, const ec_kv* prefi
   // rows of q are counted in 32 bits (more would not fit the device beside their output)
   if (static_cast<int64_t>(p->B) * p->L * p->Hq > INT32_MAX) return EC_ERR_UNSUPPORTED;
   if (!q || !R || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws)) return EC_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || scale > 3e38f || ws_bytes < ws_need) return EC_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || scale > 2e38f || ws_bytes < ws_need) return EC_ERR_INVALID_ARG;
   static const ec_kv none{};
   const ec_kv* pre = prefix != nullptr && prefix->len != 0 ? prefix : &none;
   if (pre->len != 0) {
@@ -396,7 +397,8 @@ ec_status cached_attention(const ec_params* p, const void* q, const ec_kv* prefi
   const Extent written[] = {{out, q_bytes(*p)}, {ws, ws_need}};
   const Extent read[] = {{q, q_bytes(*p)},    {cache->k, n},      {cache->v, n},      {ne ? cache->k_exp : nullptr, ne},
                          {ne ? cache->v_exp : nullptr, ne},       {pre->k, np},       {pre->v, np},
-                         {npe ? pre->k_exp : nullptr, npe},       {npe ? pre->v_exp : nullptr, npe}};
+                         {npe ? pre->k_exp : nullptr, npe},       {npe ? pre->v_exp : nullptr, npe},
+                         {R, int_bytes(p->B)}, {kv_len, int_bytes(p->B)}};
   if (any_overlap(written, read)) return EC_ERR_INVALID_ARG;
   ec_status st = EC_OK;
   launch_cached_attention(*p, q, pre->len != 0 ? pre : nullptr, *cache, R, kv_len, scale, out, ws, dev_err,
@@ -415,7 +417,8 @@ ec_status ec_kv_scatter_quant(const ec_params* p, const ec_kv* cache, const void
   if (!k_new || !v_new || !idx || !R || !aligned16(k_new) || !aligned16(v_new)) return EC_ERR_INVALID_ARG;
   const size_t n = kv_extent(*p, *cache, p->B), ne = exp_extent(*p, *cache, p->B);
   const Extent written[] = {{cache->k, n}, {cache->v, n}, {cache->k_exp, ne}, {cache->v_exp, ne}};
-  const Extent read[] = {{k_new, kv_bytes(*p)}, {v_new, kv_bytes(*p)}};
+  const Extent read[] = {{k_new, kv_bytes(*p)}, {v_new, kv_bytes(*p)}, {R, int_bytes(p->B)},
+                         {idx, int_bytes(static_cast<size_t>(p->B) * p->L)}};
   if (any_overlap(written, read)) return EC_ERR_INVALID_ARG;
   return cuda_status(launch_kv_scatter_quant(*p, *cache, k_new, v_new, src_by_position, idx, R, dev_err,
                                              static_cast<cudaStream_t>(stream)));
@@ -428,7 +431,8 @@ ec_status ec_kv_gather_quant(const ec_params* p, const ec_kv* cache, const int32
   if (!R || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return EC_ERR_INVALID_ARG;
   const size_t n = kv_extent(*p, *cache, p->B), ne = exp_extent(*p, *cache, p->B);
   const Extent written[] = {{k_out, kv_bytes(*p)}, {v_out, kv_bytes(*p)}};
-  const Extent read[] = {{cache->k, n}, {cache->v, n}, {cache->k_exp, ne}, {cache->v_exp, ne}};
+  const Extent read[] = {{cache->k, n}, {cache->v, n}, {cache->k_exp, ne}, {cache->v_exp, ne}, {R, int_bytes(p->B)},
+                         {idx, int_bytes(static_cast<size_t>(p->B) * p->L)}};
   if (any_overlap(written, read)) return EC_ERR_INVALID_ARG;
   return cuda_status(launch_kv_gather_quant(*p, *cache, idx, R, k_out, v_out, dev_err, static_cast<cudaStream_t>(stream)));
 }

@@ -379,8 +379,8 @@ typedef struct ec_kv {
  * skipped (a position given twice would be written by two rows at once; what a list that is
  * reported as bad leaves at such a position is unspecified). An idx outside [0, L) sets
  * EC_DEVERR_BAD_IDX and its row is skipped; R outside [0, L] sets EC_DEVERR_BAD_R and that
- * sequence is skipped. The four arrays of the cache must not overlap each other or the fresh
- * rows (EC_ERR_INVALID_ARG). Hkv <= 65536, D 64 or 128, 2 L Hkv < 2^31. */
+ * sequence is skipped. The four arrays of the cache must not overlap each other or the other
+ * buffers (EC_ERR_INVALID_ARG). Hkv <= 65536, D 64 or 128, 2 L Hkv < 2^31. */
 ec_status ec_kv_scatter_quant(const ec_params* p, const ec_kv* cache, const void* k_new, const void* v_new,
                               int32_t src_by_position, const int32_t* idx, const int32_t* R, int32_t* dev_err,
                               ec_stream_t stream);
@@ -388,7 +388,7 @@ ec_status ec_kv_scatter_quant(const ec_params* p, const ec_kv* cache, const void
 /* Rows of an 8-bit cache back as bf16 (exact): for r < R[b], k_out[b, r] = cache.k[b, idx[b, r]],
  * the same for v. idx NULL: the positions 0 .. R[b]-1. k_out, v_out bf16 [B, L, Hkv, D]; rows at
  * and past R[b] are not written. Checks as ec_kv_scatter_quant; idx in any order, repeats
- * allowed. The outputs must not overlap the cache or each other. */
+ * allowed. The outputs must not overlap the other buffers or each other. */
 ec_status ec_kv_gather_quant(const ec_params* p, const ec_kv* cache, const int32_t* idx, const int32_t* R,
                              void* k_out, void* v_out, int32_t* dev_err, ec_stream_t stream);
 
@@ -402,7 +402,7 @@ ec_status ec_kv_gather_quant(const ec_params* p, const ec_kv* cache, const int32
  * outside [0, L] EC_DEVERR_BAD_R; the sequence is skipped. EC_ERR_UNSUPPORTED for B * L * Hq of
  * 2^31 or more. A call of 2.1e9 or more steps of 128 rows by 128 keys is not run either: it sets
  * EC_DEVERR_BAD_R.
- * scale must be above 0 and finite. ws: ec_partial_attention_quant_workspace_size(p) bytes,
+ * scale must be above 0 and at most 2e38. ws: ec_partial_attention_quant_workspace_size(p) bytes,
  * 16-byte aligned, no initial contents needed; calls that share it must not overlap in time. It
  * must not overlap the other buffers, nor out the inputs (EC_ERR_INVALID_ARG).
  * The dequantised values are exact in bf16; products, sums and rounding as

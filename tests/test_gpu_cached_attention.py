@@ -351,3 +351,59 @@ def test_binding_refusals(E):
         E.prefix_attention(**{**ok, "cache": E.QuantCache.empty(2, 48, 2, 64)})
     with pytest.raises(ValueError):
         E.partial_attention_quant(p, q, E.QuantCache.empty(2, 40, 2, 64), R, out)
+
+
+WHOLE = [
+    # B, L, Hq, Hkv, D, rows, lengths, Lp: about as many tiles as SMs, of about one length (a tile to a CTA)
+    (8, 200, 16, 16, 128, [100, 128, 5, 90, 128, 1, 77, 128], [200, 130, 128, 199, 1, 200, 0, 200], None),
+    (6, 1100, 40, 20, 64, [64, 3, 60, 11, 64, 40], [1100, 800, 700, 901, 640, 1099], None),
+    (5, 60, 28, 28, 128, [60, 60, 33, 1, 60], [60, 0, 59, 2, 60], 700),
+]
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("B,L,Hq,Hkv,D,Rs,lens,Lp", WHOLE)
+def test_a_tile_to_a_cta(E, B, L, Hq, Hkv, D, Rs, lens, Lp, quant):
+    if not quant and Lp is None:
+        Lp = 0
+    Case(B, L, Hq, Hkv, D, Rs, lens, Lp=Lp, quant=quant, seed=L + B).run(E)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_queries_and_outputs_at_odd_multiples_of_16_bytes(E, quant):
+    c = Case(2, 150, 6, 2, 64, [150, 31], [150, 70], Lp=100, quant=quant, seed=23)
+    d = c.inputs(E)
+    for n in ("q", "out"):
+        t = torch.empty(d[n].numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(d[n].shape)
+        d[n] = t.copy_(d[n])
+        assert t.data_ptr() % 32 == 16
+    c.call(E, d)
+    c.check(d["out"])
+
+
+REPEATS = [
+    # shapes with several items to a CTA, both streams, ragged ends, the merge; run often, with the same bits
+    (7, 500, 24, 8, 128, [90, 128, 1, 0, 300, 500, 17], [500, 1, 500, 400, 0, 333, 499], 1000),
+    (4, 900, 16, 16, 64, [900, 1, 450, 130], [900, 899, 64, 65], 130),
+    (16, 64, 32, 4, 128, [1] * 16, list(range(0, 64, 4)), 3000),
+]
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("B,L,Hq,Hkv,D,Rs,lens,Lp", REPEATS)
+def test_the_same_bits_every_time(E, B, L, Hq, Hkv, D, Rs, lens, Lp, quant):
+    c = Case(B, L, Hq, Hkv, D, Rs, lens, Lp=Lp, quant=quant, seed=B)
+    d = c.inputs(E)
+    ws = E.workspace(E.prefix_attention_workspace_size(d["p"]))
+    c.call(E, d, ws=ws)
+    c.check(d["out"])
+    first = d["out"].clone()
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for n in range(60):
+        if n % 3 == 0:
+            flush.fill_(n)  # the caches from memory, not from L2
+        ws.fill_(255)
+        d["out"].fill_(SENTINEL)
+        c.call(E, d, ws=ws)
+        assert torch.equal(d["out"].view(torch.int16), first.view(torch.int16)), n
+    assert int(d["dev_err"].item()) == 0

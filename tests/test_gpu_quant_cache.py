@@ -202,3 +202,51 @@ def test_graph_and_another_stream(E):
     k2, _ = E.kv_gather_quant(p, cache, idx, R, stream=s2)
     s2.synchronize()
     np.testing.assert_array_equal(Q.f64(k2)[0], want[0])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_buffers_at_odd_multiples_of_16_bytes(E, D):
+    # the alignment that the interface asks for, and no more
+    B, L, Hkv = 2, 77, 3
+    rng = np.random.default_rng(D)
+    p = params(E, B, L, Hkv, D)
+
+    def shifted(shape, dtype):  # a tensor that starts 16 bytes into its buffer
+        n = int(np.prod(shape)) * (2 if dtype == torch.bfloat16 else 1)
+        return torch.full((n + 16,), 0x5A, dtype=torch.uint8, device="cuda")[16:].view(dtype).view(shape)
+
+    cache = E.QuantCache(*(shifted((B, L, Hkv, D), torch.uint8).view(torch.float8_e4m3fn) for _ in range(2)),
+                         *(shifted((B, Hkv, 80), torch.uint8) for _ in range(2)))
+    x = [rows_of(rng, B, L, Hkv, D) for _ in range(2)]
+    new, out = [shifted((B, L, Hkv, D), torch.bfloat16) for _ in range(2)], [shifted((B, L, Hkv, D), torch.bfloat16) for _ in range(2)]
+    for a, b in zip(new, x):
+        a.copy_(b)
+    assert all(t.data_ptr() % 32 == 16 for t in (*new, *out, cache.k, cache.v_exp))
+    Rs = [77, 40]
+    idx = torch.from_numpy(np.stack([np.pad(positions(rng, L, r), (0, L - r)) for r in Rs])).cuda()
+    R = torch.tensor(Rs, dtype=torch.int32, device="cuda")
+    E.kv_scatter_quant(p, cache, *new, idx, R)
+    E.kv_gather_quant(p, cache, idx, R, out=tuple(out))
+    for a, b in zip(out, x):
+        c, e = Q.quantise(Q.f64(b))
+        want = c * 2.0 ** (e.astype(float) - 127)[..., None]
+        for i, r in enumerate(Rs):
+            np.testing.assert_array_equal(Q.f64(a)[i, :r], want[i, :r])
+
+
+def test_a_cache_whose_tensors_are_exchanged(E):
+    p, cache = params(E, 1, 32, 2, 64), E.QuantCache.empty(1, 32, 2, 64)
+    x = Q.bf16(np.random.default_rng(0).standard_normal((1, 32, 2, 64))).cuda()
+    idx, R = torch.arange(32, dtype=torch.int32, device="cuda")[None].contiguous(), torch.tensor([32], dtype=torch.int32, device="cuda")
+    E.kv_scatter_quant(p, cache, x, x, idx, R)
+    old, other = cache.k, E.QuantCache.empty(1, 32, 2, 64)
+    cache.k, cache.k_exp = other.k, other.k_exp
+    k, v = E.kv_gather_quant(p, cache, idx, R)
+    assert not k.any() and v.any()
+    cache.k = old[:, :, :1]  # the same address, another shape
+    with pytest.raises(ValueError):
+        E.kv_gather_quant(p, cache, idx, R)
+    with pytest.raises(ValueError):  # and stays refused
+        E.kv_gather_quant(p, cache, idx, R)
+    cache.k = other.k
+    E.kv_gather_quant(p, cache, idx, R)

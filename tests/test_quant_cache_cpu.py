@@ -156,3 +156,47 @@ def test_plain_row_format():
         row[0, 5] = bad
         c, e = Q.quantise(row)
         assert e[0] == 255 and np.isnan(c).all()
+
+
+def test_sizes_that_leave_32_bits_are_refused(capi):
+    lib, C = capi.load(), capi
+    # 2 L Hkv and B L Hq at 2^31 and just below, where the next check (a null pointer) answers
+    for L, Hkv, want in [(1 << 16, 1 << 14, C.EC_ERR_UNSUPPORTED), ((1 << 16) - 1, 1 << 14, C.EC_ERR_INVALID_ARG)]:
+        p, c = params(C, L=L, Hq=Hkv, Hkv=Hkv), kv(C, len=L)
+        assert lib.ec_kv_scatter_quant(ctypes.byref(p), ctypes.byref(c), None, at(9), 0, at(10), at(11), None, None) == want
+        assert lib.ec_kv_gather_quant(ctypes.byref(p), ctypes.byref(c), at(10), at(11), None, at(9), None, None) == want
+    for B, L, want in [(128, 1 << 17, C.EC_ERR_UNSUPPORTED), (128, (1 << 17) - 1, C.EC_ERR_INVALID_ARG)]:
+        p, c = params(C, B=B, L=L, Hq=128, Hkv=128, D=64), kv(C, len=L)
+        assert lib.ec_partial_attention_quant(ctypes.byref(p), None, ctypes.byref(c), at(21), None, 0.1, at(23), at(24), 1 << 31,
+                                              None, None) == want
+
+
+def test_outputs_over_sizes_and_indices_are_refused(capi):
+    lib, C = capi.load(), capi
+    p, c = params(C), kv(C)
+    P, INV = ctypes.byref, C.EC_ERR_INVALID_ARG
+    assert lib.ec_partial_attention_quant(P(p), at(20), P(c), at(23, 64), None, 0.1, at(23), at(24), 1 << 31, None, None) == INV
+    assert lib.ec_partial_attention_quant(P(p), at(20), P(c), at(21), at(24, 64), 0.1, at(23), at(24), 1 << 31, None, None) == INV
+    assert lib.ec_partial_attention_quant(P(p), at(20), P(c), at(21), None, 3e38, at(23), at(24), 1 << 31, None, None) == INV
+    assert lib.ec_kv_scatter_quant(P(p), P(c), at(8), at(9), 0, at(0, 64), at(11), None, None) == INV
+    assert lib.ec_kv_scatter_quant(P(p), P(c), at(8), at(9), 0, at(10), at(3, 64), None, None) == INV
+    assert lib.ec_kv_gather_quant(P(p), P(c), at(8, 64), at(11), at(8), at(9), None, None) == INV
+    assert lib.ec_kv_gather_quant(P(p), P(c), at(10), at(9, 64), at(8), at(9), None, None) == INV
+
+
+def test_params_are_copied_and_pickled_after_use(capi):
+    import copy
+    import pickle
+
+    import entropy_gated_kv_gb300 as E
+
+    p = E.Params(B=2, L=32, Hq=4, Hkv=2, D=64, V=8, C_max=1, k=1)
+    one = E.partial_attention_quant_workspace_size(p)
+    assert one > E.partial_attention_quant_workspace_size(E.Params(B=2, L=32, Hq=4, Hkv=2, D=128, V=8, C_max=1, k=1)) // 4
+    for q in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
+        assert q == p
+        q.D = 128  # a copy's change reaches the C view, and the copy's only
+        assert E.partial_attention_quant_workspace_size(q) > one
+        assert E.partial_attention_quant_workspace_size(p) == one
+    p.D = 96
+    assert E.partial_attention_quant_workspace_size(p) == 0
