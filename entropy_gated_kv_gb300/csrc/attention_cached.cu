@@ -265,30 +265,32 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   const Shape& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (warp == 0) {  // the lanes share the barriers
+    if (lane < LY::kUnits) {
+      mbar_init(&bars->unit_full[lane], Q8 ? kDequantWarps : 1);
+      mbar_init(&bars->unit_empty[lane], 1);
+    }
+    if (lane < LY::kRaw) {
+      mbar_init(&bars->raw_full[lane], 1);
+      mbar_init(&bars->raw_empty[lane], kDequantWarps);
+    }
+    if (lane < 4) {
+      mbar_init(&bars->s_full[lane >> 1][lane & 1], 1);
+      mbar_init(&bars->p_full[lane >> 1][lane & 1], 4);
+      mbar_init(&bars->pv_done[lane >> 1][lane & 1], 1);
+    }
+    if (lane < kItems) {
+      mbar_init(&bars->item_full[lane], 1);
+      mbar_init(&bars->item_empty[lane], 10);
+    }
+    if (lane < 2) mbar_init(&bars->v_here[lane], 1);
+    fence_mbar_init();
+  }
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 256);
     mbar_init(&bars->q_empty, 2);
-    for (int i = 0; i < LY::kUnits; ++i) {
-      mbar_init(&bars->unit_full[i], Q8 ? kDequantWarps : 1);
-      mbar_init(&bars->unit_empty[i], 1);
-    }
-    for (int i = 0; i < LY::kRaw; ++i) {
-      mbar_init(&bars->raw_full[i], 1);
-      mbar_init(&bars->raw_empty[i], kDequantWarps);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&bars->s_full[i >> 1][i & 1], 1);
-      mbar_init(&bars->p_full[i >> 1][i & 1], 4);
-      mbar_init(&bars->pv_done[i >> 1][i & 1], 1);
-    }
     mbar_init(&bars->join, 8);
     mbar_init(&bars->o_free, 8);
-    mbar_init(&bars->v_here[0], 1);
-    mbar_init(&bars->v_here[1], 1);
-    for (int i = 0; i < kItems; ++i) {
-      mbar_init(&bars->item_full[i], 1);
-      mbar_init(&bars->item_empty[i], 10);
-    }
     // the swizzled tiles need the 1024-byte alignment that dynamic shared memory has here
     bars->abort = (smem_u32(smem) & 1023u) != 0u;
     if (bars->abort) report_error(a.dev_err, EC_DEVERR_TIMEOUT);
@@ -328,10 +330,10 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   // Block j of the item has rows past the sequence's length (a map zero-fills only past the cache's end).
   auto ragged = [&](const Item& it, int j) { return j >= it.np && valid_keys(s, it, j) < kBlockN; };
 
-  // With 28 warps a thread is launched with 72 registers; the softmax warps take 112, the others go
-  // down: 128 x 48 + 256 x 112 + 512 x 56 is below 896 x 72.
+  // With 28 warps a thread is launched with 72 registers; the softmax warps take 104, the others go
+  // down: 128 x 64 + 256 x 104 + 512 x 56 is below 896 x 72. (With 48 the producers spill.)
   if (warp < 4) {
-    if constexpr (Q8) setmaxnreg_dec<48>();
+    if constexpr (Q8) setmaxnreg_dec<64>();
     if (warp == 0 || warp == 2) {
       // ------------------------------------------------------------------ plan, TMA producer of one stream
       // Both warps make the plan and walk the items; warp 0 hands them out.
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------------ softmax + epilogue
-    if constexpr (Q8) setmaxnreg_inc<112>();
+    if constexpr (Q8) setmaxnreg_inc<104>();
     const int st = (warp - 4) >> 2;            // stream
     const int row = 32 * (warp & 3) + lane;    // TMEM lane = packed query row
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -509,11 +511,14 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     Streams streams;
     uint32_t used = 0, n_ragged = 0;    // blocks of this stream, and those with rows past a length
     bool ok = true;
-    // An item's query tile, 16 rows a warp: each lane finds one row, and all fetch 16-byte pieces.
+    // An item's query tile, 16 rows a warp: each lane finds one row, and all fetch 16-byte pieces. The rows
+    // behind the last one keep what lies there: a row's scores, weights and sums are its own, and no one
+    // reads theirs. (With all 128 rows fetched, a one-row
+    // tile's from one address: 12.9 us for 12.1 on a single-token call.)
     auto fetch_q = [&](const Item& q) {
       constexpr int kPieces = D / 8, kStep = 32 / kPieces;
       const int base = 16 * (warp - 4), piece = lane % kPieces;
-      int x = q.row0 + min(base + (lane & 15), q.nrows - 1), b = q.b;  // padding repeats the last row
+      int x = q.row0 + min(base + (lane & 15), q.nrows - 1), b = q.b;
       if (b < 0) b = owner_of(s, reinterpret_cast<const int32_t*>(smem + LY::kCumOff), x);
       const int r = s.div_g(x);
       const int at = x + (b * s.L + r) * a.Hq + q.kvh * s.g - r * s.g;
@@ -521,8 +526,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       for (int i = lane / kPieces; i < 16; i += kStep) {
         const int64_t src = __shfl_sync(0xffffffffu, at, i);
         const int q_row = base + i;
-        cp_async16(smem_u32(smem) + (piece >> 3) * kAtomBytes + q_row * 128 + (((piece & 7) ^ (q_row & 7)) << 4),
-                   a.q + src * D + piece * 8);
+        if (q_row < q.nrows)
+          cp_async16(smem_u32(smem) + (piece >> 3) * kAtomBytes + q_row * 128 + (((piece & 7) ^ (q_row & 7)) << 4),
+                     a.q + src * D + piece * 8);
       }
     };
     auto q_here = [&]() {
@@ -1091,6 +1097,7 @@ cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_
   a.s.g = p.Hq / p.Hkv;
   a.s.div_g.set(a.s.g);
   a.s.div_h.set(p.Hkv);
+  a.s.div_ctas.set(std::min(sms, kMaxCtas));
   a.s.ctas = std::min(sms, kMaxCtas);
   a.s.slots = static_cast<int32_t>(part_slots(p, pre));
   a.Hq = p.Hq;

@@ -51,7 +51,7 @@ struct Shape {
   const int32_t *R, *kv_len;
   int32_t B, L, Lk, Lp, Hkv, g;  // own keys [0, Lk) without kv_len; Lp prefix positions
   int32_t ctas, slots;           // CTAs of the attention grid, partial tiles that the workspace holds
-  FastDiv div_g, div_h;          // by g and by Hkv
+  FastDiv div_g, div_h, div_ctas;  // by g, by Hkv and by ctas
 };
 
 // Units, packed rows of a KV head and rows of q are counted in 32 bits: the host checks that q has
@@ -98,7 +98,6 @@ struct Header {
 
 // Quotients of numbers below 2^31; the divisor's bits are few enough here that the hardware's own
 // 32-bit division is used.
-EC_DEV int div_up(int a, int b) { return static_cast<int>((static_cast<uint32_t>(a) + b - 1) / static_cast<uint32_t>(b)); }
 EC_DEV int div_down(int a, int b) { return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)); }
 
 EC_DEV int warp_total(int v) { return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v))); }
@@ -193,7 +192,7 @@ EC_DEV Plan make_plan(const Shape& s, int32_t* dev_err, bool report) {
       pl.units = together;
     }
   }
-  pl.chunk = max(1, div_up(pl.units, s.ctas));
+  pl.chunk = s.div_ctas(max(1, pl.units) - 1) + 1;
   longest = __reduce_max_sync(0xffffffffu, longest);
   if (!pl.shared && pl.otiles <= s.ctas && longest <= pl.chunk + kWholeExtra) {
     pl.whole = pl.chunk = max(1, longest);
@@ -249,7 +248,7 @@ EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c, int&
     it.blocks = tile_blocks(pl, it.len);
     const int units = tile_units(pl, it.blocks);
     const int w = u - base, tl = div_down(w, units), per_head = tiles_of(s, rsel);
-    it.kvh = div_down(tl, per_head);
+    it.kvh = per_head == 1 ? tl : div_down(tl, per_head);
     it.row0 = (tl - it.kvh * per_head) * kBlockM;
     it.nrows = min(kBlockM, rsel * s.g - it.row0);
     it.np = pl.shared ? 0 : pl.nbp;
