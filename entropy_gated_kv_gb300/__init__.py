@@ -321,25 +321,20 @@ def _cuda_index(t, name: str) -> int:
 
 
 class _Cache:
-    """The C view of one layer's cache (ec_kv) and the tensors that it points to."""
+    """The checked C view (ec_kv) of an 8-bit cache."""
 
     __slots__ = ("c", "ref", "shape", "index")
 
-    def __init__(self, dtype, k, v, k_exp=None, v_exp=None):
-        tdt = torch.float8_e4m3fn if dtype == C.EC_E4M3 else torch.bfloat16
+    def __init__(self, k, v, k_exp, v_exp):
         self.shape, self.index = tuple(k.shape), _cuda_index(k, "k")
         if len(self.shape) != 4:
             raise ValueError(f"a cache is [B, L, Hkv, D], got {list(self.shape)}")
-        kp = _checked(k, "k", tdt, self.shape, self.index)
-        vp = _checked(v, "v", tdt, self.shape, self.index)
-        ep = [None, None]
-        if dtype == C.EC_E4M3:
-            if k_exp is None or v_exp is None:
-                raise ValueError("an 8-bit cache has exponent bytes k_exp and v_exp")
-            B, L, H, _ = self.shape
-            ep = [_checked(e, n, torch.uint8, (B, H, -(-L // 16) * 16), self.index)
-                  for e, n in ((k_exp, "k_exp"), (v_exp, "v_exp"))]
-        self.c = C.EcKv(dtype, self.shape[1], kp, vp, *ep)
+        kv = [_checked(t, n, torch.float8_e4m3fn, self.shape, self.index) for t, n in ((k, "k"), (v, "v"))]
+        if k_exp is None or v_exp is None:
+            raise ValueError("an 8-bit cache has exponent bytes k_exp and v_exp")
+        B, L, H, _ = self.shape
+        ep = [_checked(e, n, torch.uint8, (B, H, -(-L // 16) * 16), self.index) for e, n in ((k_exp, "k_exp"), (v_exp, "v_exp"))]
+        self.c = C.EcKv(C.EC_E4M3, L, *kv, *ep)
         self.ref = ctypes.byref(self.c)
 
 
@@ -364,7 +359,7 @@ class QuantCache:
     def view(self) -> _Cache:
         """The checked C view; made again when a tensor has been exchanged or has moved."""
         if self._c is None or self._at != self._places():
-            object.__setattr__(self, "_c", _Cache(C.EC_E4M3, self.k, self.v, self.k_exp, self.v_exp))
+            object.__setattr__(self, "_c", _Cache(self.k, self.v, self.k_exp, self.v_exp))
             object.__setattr__(self, "_at", self._places())
         return self._c
 
@@ -377,13 +372,27 @@ class QuantCache:
         return cls(*codes, *(z(B, Hkv, S).fill_(17) for _ in range(2)))
 
 
-def _cache_view(cache, ndim: int = 4) -> _Cache:
+def _kv(cache, shape: tuple, index: int, what: str):
+    """byref of the ec_kv of `cache`, a QuantCache or a pair of bf16 tensors, of that shape ([.., L, Hkv, D])."""
     if isinstance(cache, QuantCache):
-        return cache.view()
+        view = cache.view()
+        _expect(view, shape, what)
+        if view.index != index:
+            raise ValueError(f"{what} is on cuda:{view.index}, the other tensors on cuda:{index}")
+        return view.ref
     k, v = cache
-    if ndim == 3 and k.dim() == 3 and v.dim() == 3:  # a prefix: one sequence
-        k, v = k.unsqueeze(0), v.unsqueeze(0)
-    return _Cache(C.EC_BF16, k, v)
+    kp = _checked(k, what, torch.bfloat16, shape, index)
+    return ctypes.byref(C.EcKv(C.EC_BF16, shape[-3], kp, _checked(v, what, torch.bfloat16, shape, index), None, None))
+
+
+def _prefix_shape(prefix, p: Params) -> tuple:
+    if isinstance(prefix, QuantCache):
+        return (1, prefix.k.shape[1], p.Hkv, p.D)
+    k = prefix[0]  # [Lp, Hkv, D], or one sequence of a batch's layout
+    n = k.dim()
+    if n != 3 and n != 4:
+        raise ValueError(f"a prefix is [Lp, Hkv, D], got {list(k.shape)}")
+    return (k.shape[0], p.Hkv, p.D) if n == 3 else (1, k.shape[1], p.Hkv, p.D)
 
 
 def _launch(index: int, stream, call):
@@ -394,7 +403,7 @@ def _launch(index: int, stream, call):
             raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         return call(torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(index):
         return call(torch._C._cuda_getCurrentRawStream(index))
@@ -457,16 +466,19 @@ def prefix_attention_workspace_size(p: Params) -> int:
     return int(lib().ec_prefix_attention_workspace_size(p.ref()))
 
 
-def _attend(p: Params, q, prefix: _Cache | None, cache: _Cache, R, out, kv_len, scale, ws, dev_err, stream):
-    i, shape = _cuda_index(q, "q"), (p.B, p.L, p.Hq, p.D)
-    _expect(cache, (p.B, p.L, p.Hkv, p.D), "cache")
+def _attend(p: Params, q, prefix, cache, R, out, kv_len, scale, ws, dev_err, stream):
+    i, shape, own = q.get_device(), (p.B, p.L, p.Hq, p.D), (p.B, p.L, p.Hkv, p.D)
+    if i < 0:
+        _cuda_index(q, "q")
+    what = "ec_partial_attention_quant" if prefix is None else "ec_prefix_attention"
+    kv = [_kv(cache, own, i, "cache")]
+    if prefix is not None:
+        kv.insert(0, _kv(prefix, _prefix_shape(prefix, p), i, "prefix"))
     qp = _checked(q, "q", torch.bfloat16, shape, i)
     op = _checked(out, "out", torch.bfloat16, shape, i)
     rp = _checked(R, "R", torch.int32, shape[:1], i)
     lp = _opt(kv_len, "kv_len", torch.int32, shape[:1], i)
     ep = _opt(dev_err, "dev_err", torch.int32, (1,), i)
-    if cache.index != i or (prefix is not None and prefix.index != i):
-        raise ValueError(f"the caches must be on {q.device}, as q is")
     if ws is not None and (ws.get_device() != i or not ws.is_contiguous()):
         raise ValueError(f"ws must be a contiguous tensor on {q.device}")
     sc = (1.0 / math.sqrt(p.D)) if scale is None else float(scale)
@@ -474,14 +486,10 @@ def _attend(p: Params, q, prefix: _Cache | None, cache: _Cache, R, out, kv_len, 
     def call(s):
         w = ws
         if w is None:
-            size = partial_attention_quant_workspace_size if prefix is None else prefix_attention_workspace_size
-            w = torch.empty(max(256, size(p)), dtype=torch.uint8, device=q.device)
-        nw = w.numel() * w.element_size()
-        if prefix is None:
-            return lib().ec_partial_attention_quant(p.ref(), qp, cache.ref, rp, lp, sc, op, w.data_ptr(), nw, ep, s)
-        return lib().ec_prefix_attention(p.ref(), qp, prefix.ref, cache.ref, rp, lp, sc, op, w.data_ptr(), nw, ep, s)
+            w = torch.empty(max(256, int(getattr(lib(), what + "_workspace_size")(p.ref()))), dtype=torch.uint8, device=q.device)
+        return getattr(lib(), what)(p.ref(), qp, *kv, rp, lp, sc, op, w.data_ptr(), w.nbytes, ep, s)
 
-    C.check(_launch(i, stream, call), "ec_partial_attention_quant" if prefix is None else "ec_prefix_attention")
+    C.check(_launch(i, stream, call), what)
     return out
 
 
@@ -490,7 +498,9 @@ def partial_attention_quant(p: Params, q, cache: QuantCache, R, out, kv_len=None
     """(d) against an 8-bit cache: out[b, r, h] = softmax(scale q k^T) v over the first kv_len[b]
     keys (None: the scope's), for r < R[b]; zeros without a key. q, out bf16 [B, L, Hq, D]; R,
     kv_len int32 [B]; scale > 0. See ec_partial_attention_quant."""
-    return _attend(p, q, None, cache.view(), R, out, kv_len, scale, ws, dev_err, stream)
+    if not isinstance(cache, QuantCache):
+        raise ValueError("cache must be a QuantCache")
+    return _attend(p, q, None, cache, R, out, kv_len, scale, ws, dev_err, stream)
 
 
 def prefix_attention(p: Params, q, prefix, cache, R, out, kv_len=None, scale: float | None = None,
@@ -499,9 +509,7 @@ def prefix_attention(p: Params, q, prefix, cache, R, out, kv_len=None, scale: fl
     sees, and the first kv_len[b] keys of the sequence's own cache. prefix: (k, v) bf16
     [Lp, Hkv, D], or a QuantCache of one sequence; cache: (k, v) bf16 [B, L, Hkv, D], or a
     QuantCache. The rest as partial_attention_quant. See ec_prefix_attention."""
-    pv, cv = _cache_view(prefix, 3), _cache_view(cache)
-    _expect(pv, (1, pv.shape[1], p.Hkv, p.D), "prefix")
-    return _attend(p, q, pv, cv, R, out, kv_len, scale, ws, dev_err, stream)
+    return _attend(p, q, prefix, cache, R, out, kv_len, scale, ws, dev_err, stream)
 
 
 @dataclass

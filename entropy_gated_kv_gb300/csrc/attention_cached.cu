@@ -1076,13 +1076,17 @@ cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_
     return e;
   }
   Args a;
-  const ec_kv& pc = pre ? *prefix : cache;  // without a prefix its maps are not used
-  const int pB = pre ? 1 : p.B;
   if (!cache_map(enc, &a.tk, cache.k, q8, p.D, p.Hkv, p.L, p.B) || !cache_map(enc, &a.tv, cache.v, q8, p.D, p.Hkv, p.L, p.B) ||
-      !cache_map(enc, &a.tpk, pc.k, q8, p.D, p.Hkv, pc.len, pB) || !cache_map(enc, &a.tpv, pc.v, q8, p.D, p.Hkv, pc.len, pB)) {
+      (pre && (!cache_map(enc, &a.tpk, prefix->k, q8, p.D, p.Hkv, prefix->len, 1) ||
+               !cache_map(enc, &a.tpv, prefix->v, q8, p.D, p.Hkv, prefix->len, 1)))) {
     *status = EC_ERR_INVALID_ARG;
     return cudaErrorInvalidValue;
   }
+  if (!pre) {  // not used
+    a.tpk = a.tk;
+    a.tpv = a.tv;
+  }
+  const ec_kv& pc = pre ? *prefix : cache;
   a.exps[0] = cache.k_exp;
   a.exps[1] = cache.v_exp;
   a.pexps[0] = pc.k_exp;
