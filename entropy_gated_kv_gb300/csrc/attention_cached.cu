@@ -36,8 +36,9 @@
 //                the shared memory that the kernel takes leaves L1 little room for loads in
 //                flight.)
 // A waiter on an mbarrier sees a phase's parity only: it cannot tell a phase that is complete from one
-// whose predecessor is still open. So whoever waits on a barrier follows every one of its phases: a slot of
-// the K/V ring belongs to one stream, a raw half to K or V of one stream.
+// whose predecessor is still open. So whoever waits on a barrier follows every one of its phases, or has seen
+// that the one before is complete: a place in shared memory belongs to one half of K or V of one stream.
+// Such a place is free again when the product that read it is done (s_full, pv_done).
 // Keys past a sequence's length may hold anything: their scores are replaced, and their V rows are
 // zeroed in shared memory (0 x NaN is NaN in a matrix product).
 // Partial items write fp32 rows, their maximum and their sum to the workspace; the merge kernel
@@ -63,7 +64,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per pipeline wait
 constexpr int kMaxCtas = 160;                     // bound of the attention grid, for the workspace
-constexpr int kMaxUnits = 12;                     // halves of K or V tiles in shared memory
+constexpr int kMaxUnits = 8;                      // halves of K or V tiles in shared memory
 constexpr int kMaxRaw = 8;                        // halves of raw tiles: K and V of each stream
 constexpr int kDequantWarps = 4;                  // for K and for V of each stream
 constexpr int kMergeThreads = 256;
@@ -80,7 +81,7 @@ constexpr uint32_t kStepPV = 16 * 128 / 16;
 
 struct Bars {
   uint64_t q_full, q_empty;
-  uint64_t unit_full[kMaxUnits], unit_empty[kMaxUnits];
+  uint64_t unit_full[kMaxUnits];  // a half is free when the product that reads it is done: s_full, pv_done
   uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // of a stream's halves
   uint64_t join, o_free, v_here[2];  // v_here: a stream's V tile with rows to be zeroed has come
@@ -89,7 +90,7 @@ struct Bars {
   int abort;
 };
 
-// Shared memory: the query tile, for each stream a ring of bf16 half tiles (its blocks' K and V in turn), for
+// Shared memory: the query tile, for each stream the bf16 halves of one block's K and V, for
 // the 8-bit cache their raw halves (64 rows of codes), the row statistics that the two streams exchange,
 // the items, where each sequence's packed rows end, the barriers.
 template <int D, bool Q8>
@@ -97,7 +98,7 @@ struct Layout {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;
   static constexpr int kHalfBytes = kAtoms * kHalfAtom;
-  static constexpr int kUnits = Q8 ? 8 : 12, kPer = kUnits / 2;  // bf16 half tiles; of one stream
+  static constexpr int kUnits = 8, kPer = 4;  // bf16 half tiles: K's two and V's two of each stream
   static constexpr int kRaw = Q8 ? kMaxRaw : 0;
   static constexpr int kRawBytes = kHalf * D;
   static constexpr int kUnitOff = kTileBytes;
@@ -245,17 +246,6 @@ EC_DEV int valid_keys(const Shape& s, const Item& it, int j) {
   return max(0, min(kBlockN, left));
 }
 
-// Blocks of the two streams in the items before: block i of an item goes to stream i % 2, and its half
-// tiles (K's two, then V's two) to four successive places of that stream's ring.
-struct Streams {
-  uint32_t of[2] = {0, 0};
-  EC_DEV uint32_t block(int i) const { return (i & 1 ? of[1] : of[0]) + (i >> 1); }
-  EC_DEV void add(int nblk) {
-    of[0] += (nblk + 1) >> 1;
-    of[1] += nblk >> 1;
-  }
-};
-
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_kernel(const __grid_constant__ Args a) {
   using LY = Layout<D, Q8>;
@@ -266,10 +256,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0) {  // the lanes share the barriers
-    if (lane < LY::kUnits) {
-      mbar_init(&bars->unit_full[lane], Q8 ? kDequantWarps : 1);
-      mbar_init(&bars->unit_empty[lane], 1);
-    }
+    if (lane < LY::kUnits) mbar_init(&bars->unit_full[lane], Q8 ? kDequantWarps : 1);
     if (lane < LY::kRaw) {
       mbar_init(&bars->raw_full[lane], 1);
       mbar_init(&bars->raw_empty[lane], kDequantWarps);
@@ -348,7 +335,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         if (lane < s.B) reinterpret_cast<int32_t*>(smem + LY::kCumOff)[lane] = incl;
         __syncwarp();
       }
-      Streams streams;
+      uint32_t c = 0;  // the stream's blocks
       int ok = 1, count = 0;
       Record rec{};
       for (int u = u0;; ++count) {
@@ -381,12 +368,11 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         }
         if (lane == 0) {
 #pragma unroll 1
-          for (int i = st; ok && i < it.nblk; i += 2) {
+          for (int i = st; ok && i < it.nblk; i += 2, ++c) {
             const int j = it.j0 + i;
             const bool pre = j < it.np;
             const int key0 = (pre ? j : j - it.np) * kBlockN;
             const int b = pre ? 0 : it.b;
-            const uint32_t c = streams.block(i);
 #pragma unroll 1
             for (int n = 0; n < 4; ++n) {
               // bf16: K's halves, then V's, as the products want them; 8-bit: the halves of both by turns,
@@ -400,8 +386,8 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
                 tma_load_4d(smem + LY::kRawOff + raw * LY::kRawBytes, map, &bars->raw_full[raw], 0, it.kvh,
                             key0 + h * kHalf, b);
               } else {
-                const uint32_t m = 4 * c + n, slot = st * kPer + m % kPer;
-                if (!(ok = wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u))) break;
+                const int slot = st * kPer + n;
+                if (c != 0 && !(ok = wait(kv ? &bars->pv_done[st][h] : &bars->s_full[st][h], (c - 1) & 1u))) break;
                 uint8_t* dst = smem + LY::kUnitOff + slot * LY::kHalfBytes;
                 mbar_arrive_expect_tx(&bars->unit_full[slot], LY::kHalfBytes);
 #pragma unroll
@@ -411,7 +397,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
             }
           }
         }
-        streams.add(it.nblk);
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
       if (threadIdx.x == 0) {
@@ -440,62 +425,59 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       uint32_t used = 0;  // blocks of this stream whose P V is under way or done
       bool ok = true;
       auto wait_w = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+      uint64_t* const full = bars->unit_full + st * kPer;
       for (int items = 0; ok; ++items) {
         const Item it = next_item(items);
         if (it.nblk == 0) break;
+        const int last = it.nblk - 2;  // block i is the stream's last one if i >= last
         // S of half h of the stream's block c (block i of the item)
         auto issue_qk = [&](int i, uint32_t c, int h) {
-          const uint32_t m = 4 * c + h, slot = __shfl_sync(0xffffffffu, st * kPer + m % kPer, 0);
           // K is here, and the buffer's last P has been read
-          ok = ok && wait_w(&bars->unit_full[slot], (m / kPer) & 1u);
-          if (c != 0) ok = ok && wait_w(&bars->pv_done[st][h], (c - 1) & 1u);
-          if (!ok) return;
+          if (!wait_w(full + h, c & 1u) || (c != 0 && !wait_w(&bars->pv_done[st][h], (c - 1) & 1u))) return false;
           tc_fence_after();
-          const uint32_t k_lo = sdesc_lo(unit0 + slot * LY::kHalfBytes, 16);
+          const uint32_t k_lo = sdesc_lo(unit0 + (st * kPer + h) * LY::kHalfBytes, 16);
           const uint32_t col = s_col + h * kHalf;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               umma_ss(col, q_lo + step_k(kk, kAtomBytes), k_lo + step_k(kk, kHalfAtom), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
             umma_commit(&bars->s_full[st][h]);
-            umma_commit(&bars->unit_empty[slot]);
-            if (h == 1 && i + 2 >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last S of the item
+            if (h == 1 && i >= last) umma_commit(&bars->q_empty);  // the stream's last S of the item
           }
           __syncwarp();
+          return true;
+        };
+        auto issue_pv = [&](int i, uint32_t c, int h) {
+          if (!wait_w(full + 2 + h, c & 1u)) return false;
+          if (!Q8 && i >= last && ragged(it, it.j0 + i) && lane == 0) mbar_arrive(&bars->v_here[st]);
+          if (!wait_w(&bars->p_full[st][h], c & 1u)) return false;
+          tc_fence_after();
+          const uint32_t v_lo = sdesc_lo(unit0 + (st * kPer + 2 + h) * LY::kHalfBytes, kHalfAtom);
+          const uint32_t col = s_col + h * kHalf;
+          // the stream's first half of the item starts O anew
+          const uint32_t acc0 = h > 0 ? 1u : __shfl_sync(0xffffffffu, i > 1 ? 1u : 0u, 0);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kHalf / 16; ++kk)
+              umma_ts(o_col, col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
+            umma_commit(&bars->pv_done[st][h]);
+          }
+          __syncwarp();
+          return true;
         };
         ok = wait_w(&bars->q_full, items & 1);
         if (static_cast<int>(st) < it.nblk) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) issue_qk(st, used, h);
+          ok = ok && issue_qk(st, used, 0) && issue_qk(st, used, 1);
         } else {  // nothing of this item falls to stream 1
           if (ok && lane == 0) mbar_arrive(&bars->q_empty);
-          if (items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);
         }
+        if (items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);
 #pragma unroll 1
-        for (int i = st; ok && i < it.nblk; i += 2) {
-          if (i < 2 && items > 0) ok = wait_w(&bars->o_free, (items - 1) & 1);
-          const uint32_t c = used++;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t m = 4 * c + 2 + h, slot = __shfl_sync(0xffffffffu, st * kPer + m % kPer, 0);
-            ok = ok && wait_w(&bars->unit_full[slot], (m / kPer) & 1u);
-            if (!Q8 && ok && ragged(it, it.j0 + i) && lane == 0) mbar_arrive(&bars->v_here[st]);
-            ok = ok && wait_w(&bars->p_full[st][h], c & 1u);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t v_lo = sdesc_lo(unit0 + slot * LY::kHalfBytes, kHalfAtom);
-            const uint32_t col = s_col + h * kHalf;
-            // the stream's first half of the item starts O anew
-            const uint32_t acc0 = __shfl_sync(0xffffffffu, i > 1 || h > 0 ? 1u : 0u, 0);
-            if (elect_one()) {
+        for (int i = st; ok && i < it.nblk; i += 2, ++used) {
 #pragma unroll
-              for (int kk = 0; kk < kHalf / 16; ++kk)
-                umma_ts(o_col, col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
-              umma_commit(&bars->pv_done[st][h]);
-              umma_commit(&bars->unit_empty[slot]);
-            }
-            __syncwarp();
-            if (i + 2 < it.nblk) issue_qk(i + 2, c + 1, h);
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && issue_pv(i, used, h);
+            if (i < last) ok = ok && issue_qk(i + 2, used + 1, h);
           }
         }
         if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
@@ -508,7 +490,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     const int row = 32 * (warp & 3) + lane;    // TMEM lane = packed query row
     const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
-    Streams streams;
     uint32_t used = 0, n_ragged = 0;    // blocks of this stream, and those with rows past a length
     bool ok = true;
     // An item's query tile, 16 rows a warp: each lane finds one row, and all fetch 16-byte pieces. The rows
@@ -554,10 +535,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         const int nv = valid_keys(s, it, it.j0 + i) - h * kHalf;  // keys of the half that take part: none if 0 or less
         if constexpr (!Q8) {
           if (ragged(it, it.j0 + i)) {  // their V rows become zeros
-            const uint32_t m = 4 * streams.block(i) + 2 + h, slot = st * kPer + m % kPer;
             ok = __all_sync(0xffffffffu, wait(&bars->v_here[st], n_ragged++ & 1u));
             if (!ok) break;
-            const uint32_t v_half = smem_u32(smem + LY::kUnitOff + slot * LY::kHalfBytes);
+            const uint32_t v_half = smem_u32(smem + LY::kUnitOff + (st * kPer + 2 + h) * LY::kHalfBytes);
             for (int e = max(nv, 0) * 8 + row; e < kHalf * 8; e += 128)
 #pragma unroll
               for (int at = 0; at < LY::kAtoms; ++at) st_shared16(v_half + at * kHalfAtom + e * 16, make_uint4(0, 0, 0, 0));
@@ -641,7 +621,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         used += h;
       }
       // join the two streams: each warpgroup takes half of the columns of both accumulators
-      streams.add(it.nblk);
       const Item next = next_item(items + 1);
       if (next.nblk > 0) {
         ok = __all_sync(0xffffffffu, ok && wait(&bars->q_empty, items & 1));
@@ -763,8 +742,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         const bool plain = nv == kBlockN && __all_sync(0xffffffffu, e_here <= kExpOneFactor);
 #pragma unroll 1
         for (int h = 0; ok && h < 2; ++h) {
-          const uint32_t m = 4 * c + 2 * kv + h, slot = st * kPer + m % kPer;
-          ok = __all_sync(0xffffffffu, wait(&bars->raw_full[raw + h], c & 1u) && wait(&bars->unit_empty[slot], ((m / kPer) & 1u) ^ 1u));
+          const int slot = st * kPer + 2 * kv + h;
+          ok = __all_sync(0xffffffffu, wait(&bars->raw_full[raw + h], c & 1u) &&
+                                             (c == 0 || wait(kv ? &bars->pv_done[st][h] : &bars->s_full[st][h], (c - 1) & 1u)));
           if (!ok) break;
           uint32_t src = src0 + h * kHalf * D;
           uint32_t dst = smem_u32(smem + LY::kUnitOff + slot * LY::kHalfBytes) + dst_off;
