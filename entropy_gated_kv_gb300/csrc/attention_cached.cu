@@ -527,98 +527,102 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
       const bool live = 32 * (warp & 3) < it.nrows;  // else the warp's rows are all padding
       float m_used = -INFINITY, l_sum = 0.f;
 #pragma unroll 1
-      for (int sub = 2 * st; sub < 2 * it.nblk; sub += (sub & 1) ? 3 : 1) {
-        const int i = sub >> 1, h = sub & 1;
-        const uint32_t s_addr = tmem + lane_off + st * kBlockN + h * kHalf;
-        ok = __all_sync(0xffffffffu, wait(&bars->s_full[st][h], used & 1u));
-        if (!ok) break;
-        const int nv = valid_keys(s, it, it.j0 + i) - h * kHalf;  // keys of the half that take part: none if 0 or less
-        if constexpr (!Q8) {
-          if (ragged(it, it.j0 + i)) {  // their V rows become zeros
-            ok = __all_sync(0xffffffffu, wait(&bars->v_here[st], n_ragged++ & 1u));
-            if (!ok) break;
-            const uint32_t v_half = smem_u32(smem + LY::kUnitOff + (st * kPer + 2 + h) * LY::kHalfBytes);
-            for (int e = max(nv, 0) * 8 + row; e < kHalf * 8; e += 128)
+      for (int i = st; ok && i < it.nblk; i += 2, ++used) {
+        const int j = it.j0 + i;
+        // only the prefix's last block and the tile's are cut by a length
+        const int keys = j + 1 == it.np || j + 1 == it.blocks ? valid_keys(s, it, j) : kBlockN;
+        uint32_t s_addr = tmem + lane_off + st * kBlockN;
+        int nv = keys;  // keys of the half that take part: none if 0 or less
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h, s_addr += kHalf, nv -= kHalf) {
+          ok = __all_sync(0xffffffffu, wait(&bars->s_full[st][h], used & 1u));
+          if (!ok) break;
+          if constexpr (!Q8) {
+            if (keys < kBlockN && j >= it.np) {  // their V rows become zeros
+              ok = __all_sync(0xffffffffu, wait(&bars->v_here[st], n_ragged++ & 1u));
+              if (!ok) break;
+              const uint32_t v_half = smem_u32(smem + LY::kUnitOff + (st * kPer + 2 + h) * LY::kHalfBytes);
+              for (int e = max(nv, 0) * 8 + row; e < kHalf * 8; e += 128)
 #pragma unroll
-              for (int at = 0; at < LY::kAtoms; ++at) st_shared16(v_half + at * kHalfAtom + e * 16, make_uint4(0, 0, 0, 0));
-            fence_proxy_async_smem();
-          }
-        }
-        if (live) {
-          tc_fence_after();
-          // maximum (scale > 0 commutes with it), then p = 2^(s scale log2(e) - m)
-          uint32_t b0[32], b1[32];
-          EC_TMEM_LD32(s_addr, b0);
-          EC_TMEM_LD32(s_addr + 32, b1);
-          EC_TMEM_WAIT32(b0);
-          EC_TMEM_WAIT32(b1);
-          if (nv < kHalf) {  // keys that take no part
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (e >= nv) b0[e] = __float_as_uint(-INFINITY);
-              if (32 + e >= nv) b1[e] = __float_as_uint(-INFINITY);
+                for (int at = 0; at < LY::kAtoms; ++at) st_shared16(v_half + at * kHalfAtom + e * 16, make_uint4(0, 0, 0, 0));
+              fence_proxy_async_smem();
             }
           }
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (live) {
+            tc_fence_after();
+            // maximum (scale > 0 commutes with it), then p = 2^(s scale log2(e) - m)
+            uint32_t b0[32], b1[32];
+            EC_TMEM_LD32(s_addr, b0);
+            EC_TMEM_LD32(s_addr + 32, b1);
+            EC_TMEM_WAIT32(b0);
+            EC_TMEM_WAIT32(b1);
+            if (nv < kHalf) {  // keys that take no part
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            m4[e & 2] = max3(m4[e & 2], __uint_as_float(b0[e]), __uint_as_float(b0[e + 1]));
-            m4[(e & 2) + 1] = max3(m4[(e & 2) + 1], __uint_as_float(b1[e]), __uint_as_float(b1[e + 1]));
-          }
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
-          bool rescale = false;
-          float alpha = 1.f;
-          if (sub == 2 * st) {
-            m_used = mx;
-          } else if (mx > m_used + kRescaleLog2) {
-            alpha = ex2_approx(m_used - mx);
-            m_used = mx;
-            l_sum *= alpha;
-            rescale = true;
-          }
-          // without a finite score so far, nothing is subtracted and p = 0
-          const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-          const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
-          uint64_t sum2[2] = {0, 0};
-          auto weights = [&](const uint32_t (&x)[32], int c) {  // P over the buffer's first 32 columns
-            uint32_t pk[16];
+              for (int e = 0; e < 32; ++e) {
+                if (e >= nv) b0[e] = __float_as_uint(-INFINITY);
+                if (32 + e >= nv) b1[e] = __float_as_uint(-INFINITY);
+              }
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              float p0, p1;
-              unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
-              pk[e >> 1] = pack_bf16x2(p0, p1);
+              m4[e & 2] = max3(m4[e & 2], __uint_as_float(b0[e]), __uint_as_float(b0[e + 1]));
+              m4[(e & 2) + 1] = max3(m4[(e & 2) + 1], __uint_as_float(b1[e]), __uint_as_float(b1[e + 1]));
             }
-            EC_TMEM_ST16(s_addr + c, pk);
-          };
-          weights(b0, 0);
-          weights(b1, 16);
-          float sum_lo, sum_hi;
-          unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
-          l_sum += sum_lo + sum_hi;
-          if (__any_sync(0xffffffffu, rescale)) {
-            // the half before this one may still be under way into O
-            ok = __all_sync(0xffffffffu, wait(&bars->pv_done[st][h ^ 1], (h ? used : used - 1) & 1u));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
-              EC_TMEM_WAIT32(o);
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+            bool rescale = false;
+            float alpha = 1.f;
+            if (i < 2 && h == 0) {
+              m_used = mx;
+            } else if (mx > m_used + kRescaleLog2) {
+              alpha = ex2_approx(m_used - mx);
+              m_used = mx;
+              l_sum *= alpha;
+              rescale = true;
+            }
+            // without a finite score so far, nothing is subtracted and p = 0
+            const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+            const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
+            uint64_t sum2[2] = {0, 0};
+            auto weights = [&](const uint32_t (&x)[32], int c) {  // P over the buffer's first 32 columns
+              uint32_t pk[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              EC_TMEM_ST32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+              for (int e = 0; e < 32; e += 2) {
+                float p0, p1;
+                unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
+                pk[e >> 1] = pack_bf16x2(p0, p1);
+              }
+              EC_TMEM_ST16(s_addr + c, pk);
+            };
+            weights(b0, 0);
+            weights(b1, 16);
+            float sum_lo, sum_hi;
+            unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
+            l_sum += sum_lo + sum_hi;
+            if (__any_sync(0xffffffffu, rescale)) {
+              // the half before this one may still be under way into O
+              ok = __all_sync(0xffffffffu, wait(&bars->pv_done[st][h ^ 1], (h ? used : used - 1) & 1u));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+                EC_TMEM_WAIT32(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                EC_TMEM_ST32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+              }
             }
+            tmem_wait_st();
+            tc_fence_before();
           }
-          tmem_wait_st();
-          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[st][h]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[st][h]);
-        used += h;
       }
       // join the two streams: each warpgroup takes half of the columns of both accumulators
       const Item next = next_item(items + 1);
