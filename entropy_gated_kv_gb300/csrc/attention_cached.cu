@@ -12,15 +12,17 @@
 // Structure (one CTA per SM; the work plan is attention_cached.cuh's):
 //   warps 0, 2   make the work plan and are the TMA producers, each for one of two streams (below): halves of
 //                64 keys; warp 0 hands out the CTA's items to the others.
-//   warps 1, 3   issue tcgen05.mma, each for one stream; warp 1 allocates 512 TMEM
-//                columns. (One issuer for both: 102 us for 85 on the long 8-bit case, every wait
-//                and every product of a stream in the other's way.)
-//   warps 4..7   softmax of the CTA's even key blocks, warps 8..11 of the odd ones: two independent
+//   warps 1, 3   issue tcgen05.mma, each for one stream; warp 1 allocates 512 TMEM columns. (One
+//                issuer for both: 102 us for 85 on the long 8-bit case, every wait and every product
+//                of a stream in the other's way. Places in a ring worked out between the products:
+//                205 us for 189 on the long shared prefix, so every half has a fixed place.)
+//   warps 4..7   softmax of an item's even key blocks, warps 8..11 of the odd ones: two independent
 //                streams with their own running maximum and sum and O accumulator, joined once per
 //                item. A stream takes a block in two halves of 64 keys with an S buffer each: while one
 //                half's softmax runs, the tensor cores do the other half's P V and the next block's
-//                scores. (With one S buffer of 128 keys a stream's softmax, P V and next scores
-//                follow one another: 4130 cycles a bf16 block, 2100 of them the softmax.)
+//                scores. (One S buffer of 128 keys: 4130 cycles a bf16 block, 2100 of them the
+//                softmax, one thing after another. Scores of 128 keys in one product with the softmax in halves:
+//                227 us for 184 on the long shared prefix.)
 //                One TMEM lane (= one packed query row) per thread; online softmax in base 2 with a
 //                lazy rescale of O (only when the running maximum grows by more than 2^8); P in
 //                bf16 written back over the first half of the S buffer. Between an item's last softmax and
@@ -30,11 +32,17 @@
 //                producers' TMA brings the codes into raw halves, and these warps write the bf16
 //                halves that the products read. The dequantised values are exact in bf16, so the
 //                products are those of a bf16 cache with the same values. (Raw tiles of 128 keys and
-//                one producer: 93 us for 84 on the long 8-bit case, a tile's refill not under way before all of it
-//                was read. Codes loaded from global
-//                memory into registers, without the ring: 180 us for 120 on the long case, as
-//                the shared memory that the kernel takes leaves L1 little room for loads in
-//                flight.)
+//                one producer: 93 us for 84 on the long 8-bit case, a tile's refill not under way before all
+//                of it was read. Codes loaded from global memory into registers: 180 us for 120, as
+//                the shared memory that the kernel takes leaves L1 little room for loads in flight.)
+// What bounds it, past the smallest calls: shared memory's 128 bytes a cycle. A block of 128 keys in 8 bits
+// moves 256 KB there (D = 128): the scores' operands 96 (a product of 64 keys reads all of Q), P V 32, the codes 32
+// in and 32 out, the bf16 halves 64. Counters on the long shared prefix: 50% of those cycles loads and stores,
+// 45% products' operands; 184 us, 1.0 PFLOP/s. The long 8-bit case: 79 us, 3.4 TB/s. (Q in tensor
+// memory takes 64 KB off, but leaves room for one S buffer a stream beside it: 220 and 85 us.)
+// A bf16 cache is bound by its bytes from L2, a call of a few blocks a CTA by the chain plan, first
+// loads, first scores, join, merge: straight-line code from a cold instruction cache.
+//
 // A waiter on an mbarrier sees a phase's parity only: it cannot tell a phase that is complete from one
 // whose predecessor is still open. So whoever waits on a barrier follows every one of its phases, or has seen
 // that the one before is complete: a place in shared memory belongs to one half of K or V of one stream.
@@ -74,7 +82,7 @@ constexpr int kMergeSteps = kBlockM / kMergeRows;
 constexpr int kItems = 4;       // items handed out and not yet finished, see the producer
 constexpr int kCum = 32;        // sequences whose row ends are kept in shared memory
 constexpr uint32_t kDescHi = sdesc_hi(1024);
-constexpr int kAtomBytes = 128 * 128;  // 128 rows x 128 bytes (64 bf16), 128-byte swizzle: the query tile
+constexpr int kAtomBytes = 128 * 128;   // 128 rows x 128 bytes (64 bf16), 128-byte swizzle: the query tile
 constexpr int kHalfAtom = kHalf * 128;  // 64 rows x 128 bytes: K and V
 __host__ __device__ constexpr uint32_t step_k(int kk, int atom) { return (kk >> 2) * (atom / 16) + (kk & 3) * 2; }
 constexpr uint32_t kStepPV = 16 * 128 / 16;
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
     }
     if (lane < kItems) {
       mbar_init(&bars->item_full[lane], 1);
-      mbar_init(&bars->item_empty[lane], 10);
+      mbar_init(&bars->item_empty[lane], Q8 ? 10 + 4 * kDequantWarps : 10);  // all that read the items
     }
     if (lane < 2) mbar_init(&bars->v_here[lane], 1);
     fence_mbar_init();
@@ -793,6 +801,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           }
         }
       }
+      if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
     }
   }
 
