@@ -348,6 +348,8 @@ ec_status ec_partial_attention(const ec_params* p, const void* q, const void* k_
 namespace {
 
 size_t int_bytes(size_t n) { return n * sizeof(int32_t); }
+// Sizes and indices are read, and the error word is written, as whole 32-bit words.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 size_t kv_extent(const ec_params& p, const ec_kv& c, int32_t B) {
   return static_cast<size_t>(B) * c.len * p.Hkv * p.D * (c.dtype == EC_BF16 ? 2 : 1);
 }
@@ -385,6 +387,7 @@ ec_status cached_attention(const ec_params* p, const void* q, const ec_kv* prefi
   if (static_cast<int64_t>(p->B) * p->L * p->Hq > INT32_MAX) return EC_ERR_UNSUPPORTED;
   if (!q || !R || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws)) return EC_ERR_INVALID_ARG;
   if (!(scale > 0.f) || scale > 2e38f || ws_bytes < ws_need) return EC_ERR_INVALID_ARG;
+  if (!aligned4(R) || !aligned4(kv_len) || !aligned4(dev_err)) return EC_ERR_INVALID_ARG;
   static const ec_kv none{};
   const ec_kv* pre = prefix != nullptr && prefix->len != 0 ? prefix : &none;
   if (pre->len != 0) {
@@ -415,6 +418,7 @@ ec_status ec_kv_scatter_quant(const ec_params* p, const ec_kv* cache, const void
   if (r != EC_OK) return r;
   if (src_by_position != 0 && src_by_position != 1) return EC_ERR_INVALID_ARG;
   if (!k_new || !v_new || !idx || !R || !aligned16(k_new) || !aligned16(v_new)) return EC_ERR_INVALID_ARG;
+  if (!aligned4(idx) || !aligned4(R) || !aligned4(dev_err)) return EC_ERR_INVALID_ARG;
   const size_t n = kv_extent(*p, *cache, p->B), ne = exp_extent(*p, *cache, p->B);
   const Extent written[] = {{cache->k, n}, {cache->v, n}, {cache->k_exp, ne}, {cache->v_exp, ne}};
   const Extent read[] = {{k_new, kv_bytes(*p)}, {v_new, kv_bytes(*p)}, {R, int_bytes(p->B)},
@@ -429,6 +433,7 @@ ec_status ec_kv_gather_quant(const ec_params* p, const ec_kv* cache, const int32
   const ec_status r = check_quant_rows(p, cache);
   if (r != EC_OK) return r;
   if (!R || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return EC_ERR_INVALID_ARG;
+  if (!aligned4(idx) || !aligned4(R) || !aligned4(dev_err)) return EC_ERR_INVALID_ARG;
   const size_t n = kv_extent(*p, *cache, p->B), ne = exp_extent(*p, *cache, p->B);
   const Extent written[] = {{k_out, kv_bytes(*p)}, {v_out, kv_bytes(*p)}};
   const Extent read[] = {{cache->k, n}, {cache->v, n}, {cache->k_exp, ne}, {cache->v_exp, ne}, {R, int_bytes(p->B)},

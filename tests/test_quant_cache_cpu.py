@@ -200,3 +200,14 @@ def test_params_are_copied_and_pickled_after_use(capi):
         assert E.partial_attention_quant_workspace_size(p) == one
     p.D = 96
     assert E.partial_attention_quant_workspace_size(p) == 0
+
+
+def test_unaligned_words_are_refused(capi):
+    lib, C = capi.load(), capi
+    p, c = params(C), kv(C)
+    P, INV = ctypes.byref, C.EC_ERR_INVALID_ARG
+    for R, n, err in [(at(21, 2), None, None), (at(21), at(22, 1), None), (at(21), None, at(25, 2))]:
+        assert lib.ec_partial_attention_quant(P(p), at(20), P(c), R, n, 0.1, at(23), at(24), 1 << 31, err, None) == INV
+    for idx, R, err in [(at(10, 2), at(11), None), (at(10), at(11, 1), None), (at(10), at(11), at(12, 3))]:
+        assert lib.ec_kv_scatter_quant(P(p), P(c), at(8), at(9), 0, idx, R, err, None) == INV
+        assert lib.ec_kv_gather_quant(P(p), P(c), idx, R, at(8), at(9), err, None) == INV
