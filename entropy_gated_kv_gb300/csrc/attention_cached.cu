@@ -837,14 +837,20 @@ __global__ void __launch_bounds__(kMergeThreads) cached_merge_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const int4 h = __ldcg(reinterpret_cast<const int4*>(a.header));            // records, shared, prefix units, chunk
-  const int4 h2 = __ldcg(reinterpret_cast<const int4*>(a.header) + 1);       // ptiles_head, nbp, rows
-  const bool shared = h.y != 0;
   // the first rows of all tiles first: a tile of few rows has no work for the others, and two CTAs fit an SM
-  const int per = gridDim.x / kMergeSteps, row0 = blockIdx.x / per * kMergeRows;
-  for (int which = blockIdx.x % per; which < h.x; which += per) {
-    const int4* rp = reinterpret_cast<const int4*>(a.records + which);
-    const int4 t0 = __ldcg(rp), t1 = __ldcg(rp + 1);  // b, kvh, row0, nrows; a1, a2, n2, before
+  const int per = gridDim.x / kMergeSteps, row0 = blockIdx.x / per * kMergeRows;  // per <= slots
+  int which = blockIdx.x % per;
+  const int4* rp = reinterpret_cast<const int4*>(a.records + which);
+  int4 t0 = __ldcg(rp), t1 = __ldcg(rp + 1);  // b, kvh, row0, nrows; a1, a2, n2, before (if there is such a record)
+  const int4 h = __ldcg(reinterpret_cast<const int4*>(a.header));       // records, shared, prefix units, chunk
+  const int4 h2 = __ldcg(reinterpret_cast<const int4*>(a.header) + 1);  // ptiles_head, nbp, rows
+  const bool shared = h.y != 0;
+  for (bool first = true; which < h.x; which += per, first = false) {
+    if (!first) {
+      rp = reinterpret_cast<const int4*>(a.records + which);
+      t0 = __ldcg(rp);
+      t1 = __ldcg(rp + 1);
+    }
     const int rows = min(kMergeRows, t0.w - row0);
     if (rows <= 0) continue;
     // the partials of a row: n1 slots from a1 on at `lane1`, then every `step2`-th from a2 on
