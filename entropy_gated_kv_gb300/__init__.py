@@ -323,7 +323,7 @@ def _cuda_index(t, name: str) -> int:
 class _Cache:
     """The checked C view (ec_kv) of an 8-bit cache."""
 
-    __slots__ = ("c", "ref", "shape", "index")
+    __slots__ = ("c", "ref", "shape", "index", "at")
 
     def __init__(self, k, v, k_exp, v_exp):
         self.shape, self.index = tuple(k.shape), _cuda_index(k, "k")
@@ -334,7 +334,8 @@ class _Cache:
             raise ValueError("an 8-bit cache has exponent bytes k_exp and v_exp")
         B, L, H, _ = self.shape
         ep = [_checked(e, n, torch.uint8, (B, H, -(-L // 16) * 16), self.index) for e, n in ((k_exp, "k_exp"), (v_exp, "v_exp"))]
-        self.c = C.EcKv(C.EC_E4M3, L, *kv, *ep)
+        self.at = (*kv, *ep)
+        self.c = C.EcKv(C.EC_E4M3, L, *self.at)
         self.ref = ctypes.byref(self.c)
 
 
@@ -343,7 +344,7 @@ class QuantCache:
     k_exp, v_exp uint8 [B, Hkv, S], S = L rounded up to a multiple of 16. The row of position j
     and head h stands for k[b, j, h] * 2^(k_exp[b, h, j] - 127)."""
 
-    __slots__ = ("k", "v", "k_exp", "v_exp", "_c", "_at")
+    __slots__ = ("k", "v", "k_exp", "v_exp", "_c")
 
     def __init__(self, k, v, k_exp, v_exp):
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
@@ -353,15 +354,13 @@ class QuantCache:
         object.__setattr__(self, "_c", None)
         object.__setattr__(self, name, value)
 
-    def _places(self):
-        return self.k.data_ptr(), self.v.data_ptr(), self.k_exp.data_ptr(), self.v_exp.data_ptr()
-
     def view(self) -> _Cache:
         """The checked C view; made again when a tensor has been exchanged or has moved."""
-        if self._c is None or self._at != self._places():
-            object.__setattr__(self, "_c", _Cache(self.k, self.v, self.k_exp, self.v_exp))
-            object.__setattr__(self, "_at", self._places())
-        return self._c
+        c, k, v, ke, ve = self._c, self.k, self.v, self.k_exp, self.v_exp
+        if c is None or c.at != (k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr()):
+            c = _Cache(k, v, ke, ve)
+            object.__setattr__(self, "_c", c)
+        return c
 
     @classmethod
     def empty(cls, B: int, L: int, Hkv: int, D: int, device="cuda") -> "QuantCache":
@@ -433,7 +432,10 @@ def kv_scatter_quant(p: Params, cache: QuantCache, k_new, v_new, idx, R, src_by_
     ep = _opt(dev_err, "dev_err", torch.int32, (1,), i)
     by_pos = 1 if src_by_position else 0
     f = lib().ec_kv_scatter_quant
-    st = _launch(i, stream, lambda s: f(p.ref(), view.ref, kp, vp, by_pos, ip, rp, ep, s))
+    if stream is None and torch._C._cuda_getDevice() == i:
+        st = f(p.ref(), view.ref, kp, vp, by_pos, ip, rp, ep, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        st = _launch(i, stream, lambda s: f(p.ref(), view.ref, kp, vp, by_pos, ip, rp, ep, s))
     C.check(st, "ec_kv_scatter_quant")
 
 
@@ -471,9 +473,8 @@ def _attend(p: Params, q, prefix, cache, R, out, kv_len, scale, ws, dev_err, str
     if i < 0:
         _cuda_index(q, "q")
     what = "ec_partial_attention_quant" if prefix is None else "ec_prefix_attention"
-    kv = [_kv(cache, own, i, "cache")]
-    if prefix is not None:
-        kv.insert(0, _kv(prefix, _prefix_shape(prefix, p), i, "prefix"))
+    own_kv = _kv(cache, own, i, "cache")
+    kv = (own_kv,) if prefix is None else (_kv(prefix, _prefix_shape(prefix, p), i, "prefix"), own_kv)
     qp = _checked(q, "q", torch.bfloat16, shape, i)
     op = _checked(out, "out", torch.bfloat16, shape, i)
     rp = _checked(R, "R", torch.int32, shape[:1], i)
@@ -483,13 +484,19 @@ def _attend(p: Params, q, prefix, cache, R, out, kv_len, scale, ws, dev_err, str
         raise ValueError(f"ws must be a contiguous tensor on {q.device}")
     sc = (1.0 / math.sqrt(p.D)) if scale is None else float(scale)
 
-    def call(s):
-        w = ws
-        if w is None:
-            w = torch.empty(max(256, int(getattr(lib(), what + "_workspace_size")(p.ref()))), dtype=torch.uint8, device=q.device)
-        return getattr(lib(), what)(p.ref(), qp, *kv, rp, lp, sc, op, w.data_ptr(), w.nbytes, ep, s)
+    f = getattr(lib(), what)
+    if ws is not None and stream is None and torch._C._cuda_getDevice() == i:
+        st = f(p.ref(), qp, *kv, rp, lp, sc, op, ws.data_ptr(), ws.nbytes, ep, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        def call(s):
+            w = ws
+            if w is None:
+                size = int(getattr(lib(), what + "_workspace_size")(p.ref()))
+                w = torch.empty(max(256, size), dtype=torch.uint8, device=q.device)
+            return f(p.ref(), qp, *kv, rp, lp, sc, op, w.data_ptr(), w.nbytes, ep, s)
 
-    C.check(_launch(i, stream, call), what)
+        st = _launch(i, stream, call)
+    C.check(st, what)
     return out
 
 
