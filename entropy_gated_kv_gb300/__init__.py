@@ -342,7 +342,8 @@ class _Cache:
 class QuantCache:
     """One layer's K/V cache in 8 bits (ec_kv, EC_E4M3): k, v float8_e4m3fn [B, L, Hkv, D] and
     k_exp, v_exp uint8 [B, Hkv, S], S = L rounded up to a multiple of 16. The row of position j
-    and head h stands for k[b, j, h] * 2^(k_exp[b, h, j] - 127)."""
+    and head h stands for k[b, j, h] * 2^(k_exp[b, h, j] - 127). A tensor may be exchanged for another one;
+    resizing or restriding one in place is not noticed."""
 
     __slots__ = ("k", "v", "k_exp", "v_exp", "_c")
 
