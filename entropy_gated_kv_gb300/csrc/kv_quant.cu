@@ -95,17 +95,17 @@ __global__ void __launch_bounds__(kThreads) kv_scatter_quant_kernel(const __grid
   const int Rb = checked_rows(a, b);
   const int64_t rowL = static_cast<int64_t>(b) * a.L;
   const int n = Rb * 2 * a.Hkv;  // below 2^31
-  for (int base = blockIdx.x * (kStep * kRows); base < n; base += gridDim.x * (kStep * kRows)) {
+  for (Pieces line(n, kStep * kRows, blockIdx.x, gridDim.x); line.more(); line.next()) {
     Oct x[kRows];
     int pos[kRows], head[kRows];  // head: of 2 Hkv, the K heads first
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int i = base + u * kStep + sub;
+      const uint32_t i = line.at + u * kStep + sub;
       pos[u] = -1;
       head[u] = 0;
-      if (i >= n) continue;
-      const int r = a.div_2h(i);
-      head[u] = i - r * 2 * a.Hkv;
+      if (i >= line.n) continue;
+      const int r = a.div_2h(static_cast<int>(i));
+      head[u] = static_cast<int>(i) - r * 2 * a.Hkv;
       const int p = __ldg(a.idx + rowL + r);
       // rows in recompute order ascend: a position that is not below its successor is a bad
       // (possibly repeated) one, whose codes and exponent two rows could write at once
@@ -172,17 +172,17 @@ __global__ void __launch_bounds__(kThreads) kv_gather_quant_kernel(const __grid_
   const int Rb = checked_rows(a, b);
   const int64_t rowL = static_cast<int64_t>(b) * a.L;
   const int n = Rb * 2 * a.Hkv;
-  for (int base = blockIdx.x * (kStep * kRows); base < n; base += gridDim.x * (kStep * kRows)) {
+  for (Pieces line(n, kStep * kRows, blockIdx.x, gridDim.x); line.more(); line.next()) {
     uint4 code[kRows];
     int byte[kRows];
     int64_t to[kRows];  // the output row, complemented for V; kNone: none
     constexpr int64_t kNone = INT64_MIN;
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int i = base + u * kStep + sub;
+      const uint32_t i = line.at + u * kStep + sub;
       to[u] = kNone;
-      if (i >= n) continue;
-      const int r = a.div_2h(i), head = i - r * 2 * a.Hkv;
+      if (i >= line.n) continue;
+      const int r = a.div_2h(static_cast<int>(i)), head = static_cast<int>(i) - r * 2 * a.Hkv;
       const int p = a.idx != nullptr ? __ldg(a.idx + rowL + r) : r;
       if (p < 0 || p >= a.L) {
         if (head == 0) report_error(a.dev_err, EC_DEVERR_BAD_IDX);

@@ -45,6 +45,18 @@ EC_DEV uint32_t quantise4(uint32_t lo, uint32_t hi, float f) {
 // Codes of a row of exponent 120: magnitudes above 240 (0x77) become 240.
 EC_DEV uint32_t cap_top_codes(uint32_t w) { return __vminu4(w & 0x7F7F7F7Fu, 0x77777777u) | (w & 0x80808080u); }
 
+// The rows [0, n) of a sequence's line in pieces of `piece`, dealt to the CTAs in turn. Counted without
+// a sign: n is below 2^31 and a step (piece times CTAs) below 2^22, so the sum that ends the loop, and
+// a row of the last piece past n, stay below 2^32. (With a sign the last step of a line close to 2^31
+// rows wraps, and the loop goes on at negative rows.)
+struct Pieces {
+  uint32_t at, n, step;
+  EC_DEV Pieces(int32_t rows, uint32_t piece, uint32_t cta, uint32_t ctas)
+      : at(cta * piece), n(static_cast<uint32_t>(rows)), step(ctas * piece) {}
+  EC_DEV bool more() const { return at < n; }
+  EC_DEV void next() { at += step; }
+};
+
 EC_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
