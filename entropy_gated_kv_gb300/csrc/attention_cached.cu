@@ -476,10 +476,13 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         ok = wait_w(&bars->q_full, items & 1);
         if (static_cast<int>(st) < it.nblk) {
           ok = ok && issue_qk(st, used, 0) && issue_qk(st, used, 1);
-        } else {  // nothing of this item falls to stream 1
+          if (items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);  // O is about to start anew
+        } else {
+          // Nothing of this item falls to stream 1. It leaves o_free alone: the item ends without this warp, so a
+          // wait here could find the barrier a phase ahead. Its next one follows all the same: q_full of an
+          // item comes after the join of the one before, and that after o_free of the second last.
           if (ok && lane == 0) mbar_arrive(&bars->q_empty);
         }
-        if (items > 0) ok = ok && wait_w(&bars->o_free, (items - 1) & 1);
 #pragma unroll 1
         for (int i = st; ok && i < it.nblk; i += 2, ++used) {
 #pragma unroll
