@@ -361,19 +361,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         }
         it.nblk = __shfl_sync(0xffffffffu, it.nblk, 0);
         if (it.nblk == 0) break;
-        if (it.slot >= 0 && it.j0 == 0 && it.b >= 0) {
-          rec.b = it.b;
-          rec.kvh = it.kvh;
-          rec.row0 = it.row0;
-          rec.nrows = it.nrows;
-          rec.before = it.before;
-          // the CTA that ends the tile: u is past this item and, if that is in here, the tile's cost
-          const int last = it.nblk == it.blocks ? cta : div_down(u + it.blocks - it.nblk - 1, pl.chunk);
-          rec.a1 = it.slot;
-          rec.a2 = pl.shared ? it.slot : 2 * (cta + 1);
-          rec.n2 = last - cta + (pl.shared ? 1 : 0);
-          if (pl.shared && threadIdx.x == 0) a.records[it.tile - pl.ptiles] = rec;
-        }
+        if (tile_record(pl, it, u, cta, rec) && pl.shared && threadIdx.x == 0) a.records[it.tile - pl.ptiles] = rec;
         if (lane == 0) {
 #pragma unroll 1
           for (int i = st; ok && i < it.nblk; i += 2, ++c) {
@@ -407,6 +395,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
+      if (warp == 0 && pl.shared && __any_sync(0xffffffffu, *abort_flag != 0)) write_records(s, pl, cta, a.records);
       if (threadIdx.x == 0) {
         if (!pl.shared) a.records[cta] = rec;
         if (cta == 0) {

@@ -263,5 +263,36 @@ EC_DEV Item cta_item(const Shape& s, const Plan& pl, int u, int end, int c, int&
   return it;
 }
 
+// The record of an item of CTA c that begins a cut tile of one sequence; u is the unit past the item.
+// False for any other item.
+EC_DEV bool tile_record(const Plan& pl, const Item& it, int u, int c, Record& rec) {
+  if (it.slot < 0 || it.j0 != 0 || it.b < 0) return false;
+  rec.b = it.b;
+  rec.kvh = it.kvh;
+  rec.row0 = it.row0;
+  rec.nrows = it.nrows;
+  rec.before = it.before;
+  // the CTA that ends the tile: u is past this item and, if that is in here, the tile's cost
+  const int last = it.nblk == it.blocks ? c : div_down(u + it.blocks - it.nblk - 1, pl.chunk);
+  rec.a1 = it.slot;
+  rec.a2 = pl.shared ? it.slot : 2 * (c + 1);
+  rec.n2 = last - c + (pl.shared ? 1 : 0);
+  return true;
+}
+
+// Whole warp, shared: the records of all tiles that begin in CTA c. For a CTA that gave up before it
+// came to them: the merge reads the record of every tile, and one that no one wrote in this call would send
+// it to rows and slots of whatever the workspace held before.
+EC_DEV void write_records(const Shape& s, const Plan& pl, int c, Record* records) {
+  const int end = min(pl.units, (c + 1) * pl.chunk);
+#pragma unroll 1
+  for (int u = min(pl.units, c * pl.chunk), span; u < end;) {
+    const Item it = cta_item(s, pl, u, end, c, span);
+    u += span;
+    Record rec;
+    if (it.nblk > 0 && tile_record(pl, it, u, c, rec) && (threadIdx.x & 31) == 0) records[it.tile - pl.ptiles] = rec;
+  }
+}
+
 }  // namespace cached
 }  // namespace ec

@@ -51,3 +51,46 @@ def test_a_signed_counter_would_leave_the_line(program):
     assert run(program("pieces"), 1000, 128, 3, "signed") == (0, "ok\n")
     code, out = run(program("pieces"), MAX_ROWS, 256, 1216, "signed")
     assert code == 1 and "row -" in out
+
+
+def plan(exe, B, L, Hq, Hkv, Rs, lens=None, Lp=0, scope=0, ctas=152, slots=1280, *args):
+    """Runs the plan of a call with these sizes and checks it; (mode, prefix tiles, own tiles, units)."""
+    text = f"{B} {L} {scope or L} {Lp} {Hkv} {Hq // Hkv} {ctas} {slots} {int(lens is not None)}\n"
+    text += " ".join(map(str, Rs)) + "\n" + " ".join(map(str, lens or [])) + "\n"
+    r = subprocess.run([str(exe), *args], input=text, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
+    mode, *n = r.stdout.split()
+    return (mode, *map(int, n))
+
+
+PLANS = [
+    # B, L, Hq, Hkv, rows, lengths, Lp, mode
+    (1, 1, 1, 1, [1], [0], 0, "whole"),
+    (1, 1024, 32, 32, [95], None, 0, "separate"),
+    (1, 32768, 32, 32, [95], None, 0, "separate"),
+    (8, 2048, 28, 4, [95, 89, 83, 78, 72, 66, 60, 54], [2048 - 128 * b for b in range(8)], 0, "whole"),
+    (3, 300, 6, 2, [5, 0, 300], [300, 17, 129], 0, "whole"),
+    (40, 70, 2, 1, [(7 * b) % 5 for b in range(40)], [(11 * b) % 71 for b in range(40)], 0, "whole"),
+    (4, 640, 16, 16, [640] * 4, [640, 5, 333, 640], 0, "separate"),
+    (4, 50, 4, 2, [5, 51, 7, -1], [50, 50, 51, 3], 200, "whole"),
+    (32, 256, 28, 4, [1] * 32, None, 1792, "shared"),
+    (8, 256, 32, 32, [32 - 2 * b for b in range(8)], [256 - 16 * b for b in range(8)], 3840, "shared"),
+    (16, 256, 28, 4, [31 - b for b in range(16)], [256 - 8 * b for b in range(16)], 32512, "shared"),
+    (37, 9, 14, 2, [b % 4 for b in range(37)], [(5 * b) % 10 for b in range(37)], 700, "shared"),
+    (5, 40, 6, 3, [3, 0, 40, 17, 1], [40, 3, 0, 17, 39], 640, "shared"),
+    (2, 384, 4, 4, [384, 256], None, 512, "separate"),  # 20 tiles of 10 units: a share is 2
+    (16, 64, 32, 4, [1] * 16, list(range(0, 64, 4)), 3000, "shared"),
+    (7, 500, 24, 8, [90, 128, 1, 0, 300, 500, 17], [500, 1, 500, 400, 0, 333, 499], 1000, None),
+]
+
+
+@pytest.mark.parametrize("B,L,Hq,Hkv,Rs,lens,Lp,mode", PLANS)
+@pytest.mark.parametrize("ctas", [152, 148, 7])
+def test_a_plan_covers_every_block_once_and_leaves_every_record(program, B, L, Hq, Hkv, Rs, lens, Lp, mode, ctas):
+    got = plan(program("plan"), B, L, Hq, Hkv, Rs, lens, Lp, ctas=ctas)
+    assert mode is None or ctas != 152 or got[0] == mode, got
+
+
+def test_a_tile_without_a_record_is_noticed(program):
+    with pytest.raises(AssertionError, match="no record after giving up"):
+        plan(program("plan"), 32, 256, 28, 4, [1] * 32, None, 1792, 0, 152, 1280, "lost")
