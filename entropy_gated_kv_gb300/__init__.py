@@ -323,7 +323,7 @@ def _cuda_index(t, name: str) -> int:
 class _Cache:
     """The checked C view (ec_kv) of an 8-bit cache."""
 
-    __slots__ = ("c", "ref", "shape", "index", "at")
+    __slots__ = ("c", "ref", "shape", "exp_shape", "index", "at")
 
     def __init__(self, k, v, k_exp, v_exp):
         self.shape, self.index = tuple(k.shape), _cuda_index(k, "k")
@@ -333,17 +333,27 @@ class _Cache:
         if k_exp is None or v_exp is None:
             raise ValueError("an 8-bit cache has exponent bytes k_exp and v_exp")
         B, L, H, _ = self.shape
-        ep = [_checked(e, n, torch.uint8, (B, H, -(-L // 16) * 16), self.index) for e, n in ((k_exp, "k_exp"), (v_exp, "v_exp"))]
+        self.exp_shape = (B, H, -(-L // 16) * 16)
+        ep = [_checked(e, n, torch.uint8, self.exp_shape, self.index) for e, n in ((k_exp, "k_exp"), (v_exp, "v_exp"))]
         self.at = (*kv, *ep)
         self.c = C.EcKv(C.EC_E4M3, L, *self.at)
         self.ref = ctypes.byref(self.c)
+
+    def holds(self, k, v, k_exp, v_exp) -> bool:
+        """Whether the view is still that of these tensors. Addresses alone do not tell: one that was
+        resized, restrided or given other data in place may lie where it lay."""
+        return (self.at == (k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr())
+                and k.shape == self.shape and v.shape == self.shape
+                and k_exp.shape == self.exp_shape and v_exp.shape == self.exp_shape
+                and k.is_contiguous() and v.is_contiguous() and k_exp.is_contiguous() and v_exp.is_contiguous()
+                and k.dtype is v.dtype is torch.float8_e4m3fn and k_exp.dtype is v_exp.dtype is torch.uint8)
 
 
 class QuantCache:
     """One layer's K/V cache in 8 bits (ec_kv, EC_E4M3): k, v float8_e4m3fn [B, L, Hkv, D] and
     k_exp, v_exp uint8 [B, Hkv, S], S = L rounded up to a multiple of 16. The row of position j
-    and head h stands for k[b, j, h] * 2^(k_exp[b, h, j] - 127). A tensor may be exchanged for another one;
-    resizing or restriding one in place is not noticed."""
+    and head h stands for k[b, j, h] * 2^(k_exp[b, h, j] - 127). A tensor may be exchanged for another one or
+    changed in place; every call checks what the cache holds then."""
 
     __slots__ = ("k", "v", "k_exp", "v_exp", "_c")
 
@@ -356,9 +366,9 @@ class QuantCache:
         object.__setattr__(self, name, value)
 
     def view(self) -> _Cache:
-        """The checked C view; made again when a tensor has been exchanged or has moved."""
+        """The checked C view; made and checked again when a tensor is not what it was."""
         c, k, v, ke, ve = self._c, self.k, self.v, self.k_exp, self.v_exp
-        if c is None or c.at != (k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr()):
+        if c is None or not c.holds(k, v, ke, ve):
             c = _Cache(k, v, ke, ve)
             object.__setattr__(self, "_c", c)
         return c

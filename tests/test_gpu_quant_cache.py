@@ -250,3 +250,19 @@ def test_a_cache_whose_tensors_are_exchanged(E):
         E.kv_gather_quant(p, cache, idx, R)
     cache.k = other.k
     E.kv_gather_quant(p, cache, idx, R)
+
+
+def test_a_cache_whose_tensors_change_in_place(E):
+    p, cache = params(E, 1, 32, 2, 64), E.QuantCache.empty(1, 32, 2, 64)
+    idx, R = torch.arange(32, dtype=torch.int32, device="cuda")[None].contiguous(), torch.tensor([32], dtype=torch.int32, device="cuda")
+    E.kv_gather_quant(p, cache, idx, R)
+    at = cache.k.data_ptr()
+    cache.k.resize_(1, 16, 2, 64)
+    assert cache.k.data_ptr() == at
+    with pytest.raises(ValueError):
+        E.kv_gather_quant(p, cache, idx, R)
+    cache.k.resize_(1, 32, 2, 64)
+    E.kv_gather_quant(p, cache, idx, R)
+    cache.v.as_strided_((1, 32, 2, 64), (4096, 64, 2048, 1))
+    with pytest.raises(ValueError):
+        E.kv_gather_quant(p, cache, idx, R)

@@ -211,3 +211,49 @@ def test_unaligned_words_are_refused(capi):
     for idx, R, err in [(at(10, 2), at(11), None), (at(10), at(11, 1), None), (at(10), at(11), at(12, 3))]:
         assert lib.ec_kv_scatter_quant(P(p), P(c), at(8), at(9), 0, idx, R, err, None) == INV
         assert lib.ec_kv_gather_quant(P(p), P(c), idx, R, at(8), at(9), err, None) == INV
+
+
+class _Tensor:
+    """What the binding asks of a CUDA tensor."""
+
+    def __init__(self, shape, dtype, ptr):
+        self.shape, self.dtype, self.ptr, self.contiguous, self.device, self.index = shape, dtype, ptr, True, "cuda:0", 0
+
+    def data_ptr(self):
+        return self.ptr
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return self.contiguous
+
+
+def test_a_cache_tensor_changed_in_place_is_checked_again(capi):
+    import entropy_gated_kv_gb300 as E
+
+    def fresh():
+        k, v = (_Tensor((2, 40, 3, 64), torch.float8_e4m3fn, at(i)) for i in (0, 1))
+        ke, ve = (_Tensor((2, 3, 48), torch.uint8, at(i)) for i in (2, 3))
+        return E.QuantCache(k, v, ke, ve)
+
+    c = fresh()
+    view = c.view()
+    assert c.view() is view  # nothing has changed
+    for name in ("k", "v", "k_exp", "v_exp"):
+        for attribute, value in (("shape", (2, 20, 3, 64)), ("dtype", torch.int8), ("contiguous", False)):
+            c = fresh()
+            c.view()
+            setattr(getattr(c, name), attribute, value)  # the address stays
+            for _ in range(2):
+                with pytest.raises(ValueError):
+                    c.view()
+    # all of them to another length: a new view, and calls for the old length are refused
+    c = fresh()
+    for t in (c.k, c.v):
+        t.shape = (2, 20, 3, 64)
+    for t in (c.k_exp, c.v_exp):
+        t.shape = (2, 3, 32)
+    assert c.view().shape == (2, 20, 3, 64) and c.view().c.len == 20
+    with pytest.raises(ValueError, match="cache must be"):
+        E.kv_scatter_quant(E.Params(B=2, L=40, Hq=3, Hkv=3, D=64, V=8, C_max=1, k=1), c, None, None, None, None)
