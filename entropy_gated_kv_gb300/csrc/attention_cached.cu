@@ -753,7 +753,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
           uint32_t src = src0 + h * kHalf * D;
           uint32_t dst = smem_u32(smem + LY::kUnitOff + slot * LY::kHalfBytes) + dst_off;
           const int q0 = h * (kPieces / 2);
+          bool done = false;
           if (plain) {
+            uint32_t marks = 0;
             uint4 w = ld_shared16(src);
 #pragma unroll
             for (int q = 0; q < kPieces / 2; ++q) {
@@ -767,8 +769,11 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
               dequantise4(here.w, f, hi.z, hi.w);
               st_shared16(dst + q * kRowsStep * 128, lo);
               st_shared16((dst ^ 16u) + q * kRowsStep * 128, hi);
+              marks |= nan_marks(here.x) | nan_marks(here.y) | nan_marks(here.z) | nan_marks(here.w);
             }
-          } else {  // large exponents, NaN rows, V rows past the length (zeros, whatever lies there)
+            done = !__any_sync(0xffffffffu, (marks & kNaNMarks) != 0);
+          }
+          if (!done) {  // large exponents, NaN, V rows past the length (zeros, whatever lies there)
 #pragma unroll 1
             for (int q = 0; q < kPieces / 2; ++q) {
               const uint4 here = ld_shared16(src);

@@ -204,6 +204,9 @@ __global__ void __launch_bounds__(kThreads) kv_gather_quant_kernel(const __grid_
         const uint32_t f = dequant_factor(byte[u]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) dequantise4(c[q], f, y.w[2 * q], y.w[2 * q + 1]);
+        if ((nan_marks(c[0]) | nan_marks(c[1]) | nan_marks(c[2]) | nan_marks(c[3])) & kNaNMarks)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) keep_nan(c[q], y.w[2 * q], y.w[2 * q + 1]);
       } else {
         const DequantScale s = dequant_scale(byte[u]);
 #pragma unroll

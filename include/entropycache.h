@@ -361,7 +361,8 @@ ec_status ec_dense_attention(const ec_params* p, const void* q, const void* k_ca
  *            max|x| <= 448 * 2^e, and code = x * 2^-e rounded once to the nearest e4m3 (ties to
  *            even; at e = 120 codes stop at 240, so that every value is a bf16 number).
  *            Exponent byte 255: the row held an infinity or a NaN and reads as NaN.
- *            The readers take bytes 17 .. 247 and 255.
+ *            The readers take bytes 17 .. 247 and 255, and every code; e4m3's NaN codes (0x7F,
+ *            0xFF), which are written in rows of byte 255 only, read as NaN in any row.
  * Every pointer 16-byte aligned. */
 typedef struct ec_kv {
   int32_t dtype;

@@ -407,3 +407,47 @@ def test_the_same_bits_every_time(E, B, L, Hq, Hkv, D, Rs, lens, Lp, quant):
         c.call(E, d, ws=ws)
         assert torch.equal(d["out"].view(torch.int16), first.view(torch.int16)), n
     assert int(d["dev_err"].item()) == 0
+
+
+@pytest.mark.parametrize("up", [0, 20])  # exponent bytes around 120, and above 134 (two factors)
+@pytest.mark.parametrize("B,L,Hq,Hkv,D,Rs,lens,Lp", [
+    (2, 256, 6, 3, 128, [9, 140], [256, 200], None),           # one block a tile or two
+    (1, 4000, 4, 2, 64, [3], [3999], None),                    # a tile over many CTAs, merged
+    (4, 200, 8, 4, 128, [1, 5, 0, 2], [200, 64, 10, 0], 900),  # a shared prefix, every row merged
+])
+def test_nan_in_an_8_bit_cache(E, B, L, Hq, Hkv, D, Rs, lens, Lp, up):
+    """NaN codes in rows of ordinary exponents and rows of byte 255, among the keys that take part: a NaN key
+    makes its head's rows NaN, a NaN value its column of them; every other value is as it was."""
+    c = Case(B, L, Hq, Hkv, D, Rs, lens, Lp=Lp, seed=41 + up, q_scale=2.0**-up)
+    for t in (c.own, c.pre):
+        if t is not None and up:
+            t[2].copy_((t[2].int() + up).to(torch.uint8))
+            t[3].copy_((t[3].int() + up).to(torch.uint8))
+    g = Hq // Hkv
+    where = [("own", 0, 0), ("own", 0, lens[0] - 1), ("own", 0, 63), ("own", 0, lens[0] // 2)]
+    if Lp is not None:
+        where += [("pre", 0, Lp - 1), ("pre", 0, 128)]
+    for kv in (0, 1):
+        for name, b, pos in where:
+            for byte in (None, 255):
+                d = c.inputs(E)
+                cache = d["cache"] if name == "own" else d["prefix"]
+                code = (cache.k, cache.v)[kv].view(torch.uint8)
+                h, col = 1, D - 3
+                if byte is None:
+                    code[b, pos, h, col] = 0x7F if pos % 2 else 0xFF
+                else:
+                    code[b, pos, h] = 0x7F
+                    (cache.k_exp, cache.v_exp)[kv][b, h, pos] = byte
+                clean = c.inputs(E)
+                c.call(E, clean)
+                c.call(E, d)
+                assert int(d["dev_err"].item()) == 0
+                c.check(clean["out"])
+                nan = np.zeros((B, L, Hq, D), bool)
+                for i, r in enumerate(Rs):
+                    if name == "pre" or i == b:
+                        nan[i, :r, h * g : (h + 1) * g, slice(None) if kv == 0 or byte else col] = True
+                got, was = Q.f64(d["out"]), Q.f64(clean["out"])
+                np.testing.assert_array_equal(np.isnan(got), nan)
+                np.testing.assert_array_equal(got[~nan], was[~nan])

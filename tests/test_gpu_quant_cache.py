@@ -266,3 +266,29 @@ def test_a_cache_whose_tensors_change_in_place(E):
     cache.v.as_strided_((1, 32, 2, 64), (4096, 64, 2048, 1))
     with pytest.raises(ValueError):
         E.kv_gather_quant(p, cache, idx, R)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_codes_read_as_nan_in_any_row(E, D):
+    # all 256 codes under every exponent, e4m3's NaN codes among them: at each place of a 16-byte piece and
+    # beside 0x7E, 0x00 and each other (a carry from one byte to the next)
+    L, H = 247 - 17 + 1, 512 // D + 2
+    rng = np.random.default_rng(D)
+    codes = np.zeros((H, D), np.uint8)
+    codes[: 256 // D] = np.arange(256, dtype=np.uint8).reshape(-1, D)
+    codes[256 // D : 512 // D] = rng.permutation(256).astype(np.uint8).reshape(-1, D)
+    codes[-2] = np.resize(np.array([0xFF, 0x7E, 0x7F, 0x00, 0xFF, 0xFF, 0xFE, 0x7F], np.uint8), D)
+    codes[-1] = 0xFE
+    codes[-1, D // 2 + 3] = 0x7F
+    cache = cache_of(E, 1, L, H, D)
+    for t, e in ((cache.k, cache.k_exp), (cache.v, cache.v_exp)):
+        t.view(torch.uint8).copy_(torch.from_numpy(codes).cuda()[None, None].expand(1, L, H, D))
+        e[:, :, :L] = torch.arange(17, 248, dtype=torch.uint8, device="cuda")
+    k, v = E.kv_gather_quant(params(E, 1, L, H, D), cache, None, torch.tensor([L], dtype=torch.int32, device="cuda"))
+    want = Q.widen(cache.k, cache.k_exp)
+    nan = (codes & 0x7F) == 0x7F
+    assert (np.isnan(want[0]) == nan).all()
+    fits = np.abs(want) < 3.39e38  # not NaN, and not past bf16's largest value
+    for got in (Q.f64(k), Q.f64(v)):
+        np.testing.assert_array_equal(np.isnan(got[0]), np.broadcast_to(nan, (L, H, D)))
+        np.testing.assert_array_equal(got[fits], want[fits])
