@@ -83,8 +83,14 @@ def _dtype_code(d) -> int:
     raise ValueError(f"unsupported logits dtype {d!r}")
 
 
+class _Kept:
+    """Room for what Params keeps beside its fields: __dict__ holds the fields, and nothing else."""
+
+    __slots__ = ("_kept",)
+
+
 @dataclass
-class Params:
+class Params(_Kept):
     """Step shape and knobs (ec_params)."""
 
     B: int
@@ -109,17 +115,13 @@ class Params:
 
     def ref(self):
         """byref(c()), made once and again after a field has changed."""
-        r = self.__dict__.get("_ref")
-        if r is None:
-            r = self.__dict__["_ref"] = ctypes.byref(self.c())
-        return r
-
-    def __setattr__(self, name, value):
-        self.__dict__.pop("_ref", None)
-        self.__dict__[name] = value
+        fields, kept = tuple(self.__dict__.values()), getattr(self, "_kept", None)
+        if kept is None or kept[0] != fields:
+            kept = self._kept = (fields, ctypes.byref(self.c()))
+        return kept[1]
 
     def __getstate__(self):  # copies and pickles hold the fields only
-        return {n: v for n, v in self.__dict__.items() if n != "_ref"}
+        return dict(self.__dict__)
 
 
 class DecodeState:

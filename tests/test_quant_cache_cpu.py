@@ -257,3 +257,27 @@ def test_a_cache_tensor_changed_in_place_is_checked_again(capi):
     assert c.view().shape == (2, 20, 3, 64) and c.view().c.len == 20
     with pytest.raises(ValueError, match="cache must be"):
         E.kv_scatter_quant(E.Params(B=2, L=40, Hq=3, Hkv=3, D=64, V=8, C_max=1, k=1), c, None, None, None, None)
+
+
+def test_params_hold_their_fields_and_nothing_else(capi):
+    import dataclasses
+
+    import entropy_gated_kv_gb300 as E
+
+    p = E.Params(B=2, L=32, Hq=4, Hkv=2, D=64, V=8, C_max=1, k=1)
+    names = [f.name for f in dataclasses.fields(E.Params)]
+    for _ in range(2):
+        assert list(p.__dict__) == names == list(vars(p))
+        assert E.Params(**p.__dict__) == p and E.Params(**{**vars(p), "D": 128}).D == 128
+        assert dataclasses.asdict(p) == p.__dict__
+        one = E.prefix_attention_workspace_size(p)  # the C view is made, and used again
+    # a change reaches the C view however it is made
+    other = E.prefix_attention_workspace_size(E.Params(B=2, L=32, Hq=4, Hkv=2, D=128, V=8, C_max=1, k=1))
+    assert other != one
+    p.__dict__["D"] = 128
+    assert E.prefix_attention_workspace_size(p) == other
+    vars(p).update(D=64)
+    assert E.prefix_attention_workspace_size(p) == one
+    p.D = 128
+    assert E.prefix_attention_workspace_size(p) == other
+    assert E.prefix_attention_workspace_size(dataclasses.replace(p, D=64)) == one
