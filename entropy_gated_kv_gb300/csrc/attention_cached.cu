@@ -1029,8 +1029,10 @@ bool cache_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, bool q8, int
 int64_t part_slots(const ec_params& p, bool prefix) {
   const int64_t separate = 2 * kMaxCtas;
   if (!prefix) return separate;
-  // shared tiles at R = L, or as many as a step bound by its bytes can have: past that bound
-  // (eight tiles per SM) tiles are full of rows and the prefix is not shared between tiles
+  // A place of 128 rows for every tile at R = L, but for eight tiles per SM at most (85 MB at D = 128): a
+  // workspace does not grow with the batch. With more tiles than places the prefix is not shared, and a
+  // large batch of short tiles (36 sequences of 32 KV heads, one row each) pays for it: its tiles run over
+  // the prefix one by one.
   const int64_t g = p.Hq / p.Hkv;
   const int64_t tiles = p.Hkv * ((p.B * (static_cast<int64_t>(p.L) * g) + kBlockM - 1) / kBlockM) +
                         static_cast<int64_t>(p.B) * p.Hkv * ((static_cast<int64_t>(p.L) * g + kBlockM - 1) / kBlockM);

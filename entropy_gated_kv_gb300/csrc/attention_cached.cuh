@@ -18,7 +18,7 @@
 //   shared    rows of all sequences are packed into tiles for the prefix's blocks, each sequence's
 //             rows into tiles for its own blocks, and every row is merged. Taken when it saves
 //             more than an eighth of the units (tiles that were mostly padding), which pays for
-//             the merge of every row.
+//             the merge of every row, and the workspace has a place for every tile's partial rows.
 //   whole     as separate, with a tile to a CTA: taken when there are CTAs enough and the longest
 //             tile is not kWholeExtra units above an equal share, as the partial rows and their merge
 //             cost more than that (a ragged batch of 148 tiles of 9 to 16 blocks: 38 us cut into

@@ -424,8 +424,14 @@ ec_status ec_partial_attention_quant(const ec_params* p, const void* q, const ec
  * Positions (idx, scope) count within the own cache. prefix: an ec_kv of one sequence
  * ([len, Hkv, D], 0 <= len <= 2^20; len 0 or NULL: no prefix), of the cache's dtype, EC_BF16 or
  * EC_E4M3 (types that differ return EC_ERR_UNSUPPORTED).
- * Where rows of different sequences fit into one 128-row tile, the prefix is multiplied once
- * for all of them. Everything else as ec_partial_attention_quant. */
+ * Where rows of different sequences fit into one 128-row tile and that saves an eighth of the
+ * work, the prefix is multiplied once for all of them, as long as the workspace has a place for
+ * every tile's partial rows: with n_b = R[b] Hq / Hkv and n their sum,
+ *   Hkv (ceil(n / 128) + sum_b ceil(n_b / 128)) + SMs <= 1280
+ * (with one row per sequence and head on 152 SMs: 34 sequences of 32 KV heads, 139 of 8, 279 of
+ * 4). Past that every sequence's rows run over the prefix by themselves: the same results at the
+ * cost of a batch that shares nothing. A larger batch is better cut into calls that fit.
+ * Everything else as ec_partial_attention_quant. */
 size_t ec_prefix_attention_workspace_size(const ec_params* p);
 ec_status ec_prefix_attention(const ec_params* p, const void* q, const ec_kv* prefix, const ec_kv* cache,
                               const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,

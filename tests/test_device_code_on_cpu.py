@@ -94,3 +94,28 @@ def test_a_plan_covers_every_block_once_and_leaves_every_record(program, B, L, H
 def test_a_tile_without_a_record_is_noticed(program):
     with pytest.raises(AssertionError, match="no record after giving up"):
         plan(program("plan"), 32, 256, 28, 4, [1] * 32, None, 1792, 0, 152, 1280, "lost")
+
+
+def slots(B, L, Hq, Hkv):
+    """Tiles whose partial rows the workspace of ec_prefix_attention holds."""
+    g = Hq // Hkv
+    return max(320, min(Hkv * -(-B * L * g // 128) + B * Hkv * -(-L * g // 128) + 160, 1280))
+
+
+@pytest.mark.parametrize("Hkv,last", [(32, 34), (8, 139), (4, 279)])
+def test_where_the_prefix_stops_being_shared(program, Hkv, last):
+    # the interface's own figures: one row per sequence and head, as many sequences as the workspace has places for
+    for B, mode in ((last, "shared"), (last + 1, "separate")):
+        got = plan(program("plan"), B, 8, Hkv, Hkv, [1] * B, None, 700, slots=slots(B, 8, Hkv, Hkv))
+        assert got[0] == mode, (B, got)
+
+
+@pytest.mark.parametrize("B,L,Hq,Hkv,Rs,lens,Lp,mode", [
+    # the sizes of the GPU tests that are meant for one mode of the plan
+    (34, 8, 32, 32, [1 + b % 2 for b in range(34)], [b % 9 for b in range(34)], 700, "shared"),
+    (36, 8, 32, 32, [1 + b % 2 for b in range(36)], [b % 9 for b in range(36)], 700, "separate"),
+    (5, 130, 28, 28, [128, 120, 128, 101, 128], [130, 0, 59, 2, 128], 700, "whole"),
+    (3, 260, 80, 40, [64, 50, 33], [260, 129, 7], 1000, "whole"),
+])
+def test_the_mode_that_a_gpu_test_is_meant_for(program, B, L, Hq, Hkv, Rs, lens, Lp, mode):
+    assert plan(program("plan"), B, L, Hq, Hkv, Rs, lens, Lp, slots=slots(B, L, Hq, Hkv))[0] == mode

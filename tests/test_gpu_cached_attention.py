@@ -451,3 +451,18 @@ def test_nan_in_an_8_bit_cache(E, B, L, Hq, Hkv, D, Rs, lens, Lp, up):
                 got, was = Q.f64(d["out"]), Q.f64(clean["out"])
                 np.testing.assert_array_equal(np.isnan(got), nan)
                 np.testing.assert_array_equal(got[~nan], was[~nan])
+
+
+# the modes of the plan that these sizes have (on 152 SMs) are checked in test_device_code_on_cpu.py
+BORDERS = [
+    (34, 8, 32, 32, 64, [1 + b % 2 for b in range(34)], [b % 9 for b in range(34)], 700),   # shared, as many tiles as there are places
+    (36, 8, 32, 32, 64, [1 + b % 2 for b in range(36)], [b % 9 for b in range(36)], 700),   # more: each tile by itself
+    (5, 130, 28, 28, 128, [128, 120, 128, 101, 128], [130, 0, 59, 2, 128], 700),            # a tile to a CTA, prefix and own blocks
+    (3, 260, 80, 40, 64, [64, 50, 33], [260, 129, 7], 1000),                                # the same, grouped heads
+]
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("B,L,Hq,Hkv,D,Rs,lens,Lp", BORDERS)
+def test_each_mode_of_the_plan_behind_a_prefix(E, B, L, Hq, Hkv, D, Rs, lens, Lp, quant):
+    Case(B, L, Hq, Hkv, D, Rs, lens, Lp=Lp, quant=quant, seed=L + B).run(E)
