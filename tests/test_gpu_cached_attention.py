@@ -466,3 +466,59 @@ BORDERS = [
 @pytest.mark.parametrize("B,L,Hq,Hkv,D,Rs,lens,Lp", BORDERS)
 def test_each_mode_of_the_plan_behind_a_prefix(E, B, L, Hq, Hkv, D, Rs, lens, Lp, quant):
     Case(B, L, Hq, Hkv, D, Rs, lens, Lp=Lp, quant=quant, seed=L + B).run(E)
+
+
+@pytest.mark.parametrize("by_pos", [False, True])
+def test_a_step_on_8_bit_caches_from_the_selection(E, by_pos):
+    """Selection, quantised refresh and attention in one row on the device: idx and R are those that
+    select_recompute leaves, with partial and full steps in one batch; everything against 64 bits."""
+    B, L, Hq, Hkv, D, Lp, k, C_max, n_dec = 4, 120, 8, 2, 128, 300, 12, 16, 2
+    rng = np.random.default_rng(51 + by_pos)
+    p = E.Params(B=B, L=L, Hq=Hq, Hkv=Hkv, D=D, V=1000, C_max=C_max, k=k, n_dec=n_dec, tau=1.0)
+    masked = np.stack([np.sort(rng.permutation(L)[:40]) for _ in range(B)])
+    mask = np.zeros((B, L), np.uint8)
+    np.put_along_axis(mask, masked, 1, 1)
+    st = E.DecodeState.from_arrays(p, tokens=rng.integers(0, 1000, (B, L)), mask=mask)
+    own = Q.random_cache(rng, B, L, Hkv, D)
+    cache = E.QuantCache(*(t.cuda() for t in own))
+    pre = Q.random_cache(rng, 1, Lp, Hkv, D)
+    prompt = E.QuantCache(*(t.cuda() for t in pre))
+    k64, v64 = Q.widen(own[0], own[2]), Q.widen(own[1], own[3])
+    pk64, pv64 = Q.widen(pre[0], pre[2])[0], Q.widen(pre[1], pre[3])[0]
+    ws = [E.workspace(f(p)) for f in (E.partial_attention_quant_workspace_size, E.prefix_attention_workspace_size)]
+    seen = set()
+    for step in range(3):
+        left = st.mask.cpu().numpy()
+        cand = np.stack([np.resize(rng.permutation(np.flatnonzero(left[b])), C_max) for b in range(B)]).astype(np.int32)
+        entropy = rng.random((B, C_max)).astype(np.float32)
+        entropy[step % B] += 2.0  # above tau: this sequence's step is full
+        conf = -rng.random((B, C_max)).astype(np.float32)
+        fresh = [Q.bf16(rng.standard_normal((B, L, Hkv, D))) for _ in range(2)]  # by position
+        q = Q.bf16(rng.standard_normal((B, L, Hq, D)))
+        E.select_recompute(p, st, torch.from_numpy(cand).cuda(), torch.full((B,), C_max, dtype=torch.int32, device="cuda"),
+                           torch.zeros(B * C_max, dtype=torch.int32, device="cuda"), torch.from_numpy(entropy.ravel()).cuda(),
+                           torch.from_numpy(conf.ravel()).cuda())
+        at = st.idx.long().clamp(0, L - 1)[..., None, None]
+        rows = [x.cuda() if by_pos else x.cuda().take_along_dim(at, 1) for x in fresh]
+        E.kv_scatter_quant(p, cache, *rows, st.idx, st.R, src_by_position=by_pos, dev_err=st.dev_err)
+        qr = q.cuda().take_along_dim(at, 1)
+        outs = [torch.full_like(qr, SENTINEL) for _ in range(2)]
+        E.partial_attention_quant(p, qr, cache, st.R, outs[0], ws=ws[0], dev_err=st.dev_err)
+        E.prefix_attention(p, qr, prompt, cache, st.R, outs[1], ws=ws[1], dev_err=st.dev_err)
+        assert E.read_device_error(st.dev_err) == (0, 0)
+        R, idx = st.R.cpu().numpy(), st.idx.cpu().numpy()
+        for b in range(B):
+            r, pos = R[b], idx[b, : R[b]]
+            seen.add(r == L)
+            assert 0 < r <= L and (np.diff(pos) > 0).all()
+            for x64, x in ((k64, fresh[0]), (v64, fresh[1])):
+                c, e = Q.quantise(Q.f64(x[b, pos]))
+                x64[b, pos] = c * 2.0 ** (e.astype(float) - 127)[..., None]
+        for out, kk, vv in ((outs[0], k64, v64), (outs[1], [np.concatenate([pk64, x]) for x in k64],
+                                                  [np.concatenate([pv64, x]) for x in v64])):
+            for b in range(B):
+                want, tol = Q.attention(Q.f64(q[b, idx[b, : R[b]]]), kk[b], vv[b], Q.default_scale(D))
+                got = Q.f64(out[b])
+                assert (np.abs(got[: R[b]] - want) <= tol).all(), (step, b)
+                assert (got[R[b] :] == SENTINEL).all()
+    assert seen == {True, False}  # partial and full steps
