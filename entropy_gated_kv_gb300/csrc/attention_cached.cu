@@ -35,13 +35,15 @@
 //                one producer: 93 us for 84 on the long 8-bit case, a tile's refill not under way before all
 //                of it was read. Codes loaded from global memory into registers: 180 us for 120, as
 //                the shared memory that the kernel takes leaves L1 little room for loads in flight.)
-// What bounds it, past the smallest calls: shared memory's 128 bytes a cycle. A block of 128 keys in 8 bits
+// What bounds an 8-bit call, past the smallest ones: shared memory's 128 bytes a cycle. A block of 128 keys
 // moves 256 KB there (D = 128): the scores' operands 96 (a product of 64 keys reads all of Q), P V 32, the codes 32
 // in and 32 out, the bf16 halves 64. Counters on the long shared prefix: 50% of those cycles loads and stores,
-// 45% products' operands; 184 us, 1.0 PFLOP/s. The long 8-bit case: 79 us, 3.4 TB/s. (Q in tensor
-// memory takes 64 KB off, but leaves room for one S buffer a stream beside it: 220 and 85 us.)
-// A bf16 cache is bound by its bytes from L2, a call of a few blocks a CTA by the chain plan, first
-// loads, first scores, join, merge: straight-line code from a cold instruction cache.
+// 43% products' operands; 196 us, 0.94 PFLOP/s. The long 8-bit case: 82 us, 3.3 TB/s. (Q in tensor
+// memory takes 64 KB off, but leaves room for one S buffer a stream beside it: 220 us for 184, 85 for 79.)
+// A bf16 cache leaves every unit below half (8 x 32 rows of 32 heads behind 3840 keys: tensor pipe 23%, HBM 40%, L2
+// 26%, issue slots 26%; an SM is active for 73% of the launch): the chain scores, softmax, P V of each block, and a
+// call of a few blocks a CTA the chain plan, first loads, first scores, join, merge, straight-line code from a cold
+// instruction cache.
 //
 // A waiter on an mbarrier sees a phase's parity only: it cannot tell a phase that is complete from one
 // whose predecessor is still open. So whoever waits on a barrier follows every one of its phases, or has seen
@@ -584,7 +586,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) cached_attention_k
             const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
             const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
             uint64_t sum2[2] = {0, 0};
-            auto weights = [&](const uint32_t (&x)[32], int c) {  // P over the buffer's first 32 columns
+            // P over the buffer's first 32 columns, in bf16 as the products take it: each weight is off by 2^-8 of
+            // itself at most, as in the attention over a bf16 cache. Their sum is that of the fp32 weights.
+            auto weights = [&](const uint32_t (&x)[32], int c) {
               uint32_t pk[16];
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {

@@ -96,8 +96,8 @@ struct Header {
   int32_t ptiles_head, nbp, rows, pad;           // of a KV head: prefix tiles, blocks of each, packed rows
 };
 
-// Quotients of numbers below 2^31; the divisor's bits are few enough here that the hardware's own
-// 32-bit division is used.
+// Quotients of numbers below 2^31 by a divisor that is known on the device only: the compiler's unsigned
+// 32-bit division.
 EC_DEV int div_down(int a, int b) { return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)); }
 
 EC_DEV int warp_total(int v) { return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v))); }

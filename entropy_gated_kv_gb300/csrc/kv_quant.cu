@@ -13,7 +13,7 @@
 // the buffers are aligned to it) and 16 of codes each; a thread loads its part of kRows rows before
 // it works on any. The maxima of two rows share a register's halves, so a reduction step is one
 // shuffle for both. (With 16 bytes a lane the write was bound by its instructions, most of them
-// addresses: 190 us for 807 MB; with 32, 132 us, 6.1 TB/s. The read of 332 MB takes 58 us, 5.7 TB/s; a call
+// addresses: 190 us for 807 MB; with 32, 133 us, 6.1 TB/s. The read of 332 MB takes 59 us, 5.6 TB/s; a call
 // of a few hundred rows 3.7 us.)
 #include <algorithm>
 
