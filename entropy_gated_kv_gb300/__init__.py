@@ -14,7 +14,8 @@ Stages (EntropyCache, gist.science zh summary §2.2):
 
 The same stages over other caches: kv_scatter_quant / kv_gather_quant write and read a QuantCache
 (8-bit rows), partial_attention_quant attends to it, prefix_attention attends to a prefix that
-the batch shares and to each sequence's own cache.
+the batch shares and to each sequence's own cache. A PagedCache lies in pages of a pool:
+kv_append_paged rotates and writes rows, paged_attention and paged_window_attention attend to them.
 """
 from __future__ import annotations
 
@@ -47,6 +48,11 @@ __all__ = [
     "partial_attention_quant_workspace_size",
     "prefix_attention",
     "prefix_attention_workspace_size",
+    "PagedCache",
+    "kv_append_paged",
+    "paged_attention",
+    "paged_window_attention",
+    "paged_attention_workspace_size",
     "step",
     "step_workspace_size",
     "LayerWeights",
@@ -530,6 +536,204 @@ def prefix_attention(p: Params, q, prefix, cache, R, out, kv_len=None, scale: fl
     [Lp, Hkv, D], or a QuantCache of one sequence; cache: (k, v) bf16 [B, L, Hkv, D], or a
     QuantCache. The rest as partial_attention_quant. See ec_prefix_attention."""
     return _attend(p, q, prefix, cache, R, out, kv_len, scale, ws, dev_err, stream)
+
+
+# ---- caches in pages of a pool ---------------------------------------------------------------------
+
+
+class _Pages:
+    """The checked C view (ec_paged_kv) of a paged cache."""
+
+    __slots__ = ("c", "ref", "index", "heads", "B", "positions", "at")
+
+    def __init__(self, k, v, table):
+        self.index = _cuda_index(k, "k")
+        self.at = self.key(k, v, table)
+        if k.dim() != 4 or 0 in k.shape:
+            raise ValueError(f"a pool is [n_pages, page_size, Hkv, D], got {list(k.shape)}")
+        n, ps, H, D = k.shape
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dtype is not torch.bfloat16 or t.shape != k.shape or t.get_device() != self.index:
+                raise ValueError(f"{name} must be a bf16 tensor {list(k.shape)} on {k.device}, got {t.dtype} {list(t.shape)} on {t.device}")
+            if n > 0 and not t[0].is_contiguous():
+                raise ValueError(f"the pages of {name} must be contiguous")
+        if n > 1 and k.stride(0) != v.stride(0):
+            raise ValueError(f"k and v have page strides {k.stride(0)} and {v.stride(0)}")
+        if table.dtype is not torch.int32 or table.dim() != 2 or table.get_device() != self.index:
+            raise ValueError(f"table must be int32 [B, pages of a sequence] on {k.device}, got {table.dtype} {list(table.shape)} on {table.device}")
+        self.B, w = table.shape
+        if w > 1 and table.stride(1) != 1:
+            raise ValueError("a sequence's page numbers must be contiguous")
+        row = w if self.B <= 1 else table.stride(0)
+        if row < w:
+            raise ValueError("the table's sequences must not share entries")
+        self.heads, self.positions = (H, D), w * ps
+        stride = k.stride(0) if n > 1 else ps * H * D
+        self.c = C.EcPagedKv(ps, n, stride, k.data_ptr(), v.data_ptr(), table.data_ptr(), row)
+        self.ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def key(k, v, t):
+        """What the view was made of: addresses alone do not tell a tensor that was changed in place."""
+        return (k.data_ptr(), v.data_ptr(), t.data_ptr(), k.shape, v.shape, t.shape, k.stride(), v.stride(), t.stride(), k.dtype, v.dtype,
+                t.dtype)
+
+
+class PagedCache:
+    """One layer's K/V cache in pages (ec_paged_kv): k, v bf16 [n_pages, page_size, Hkv, D] (contiguous
+    pages; the two may be views of one pool), table int32 [B, pages of a sequence]. Position j of
+    sequence b is row j % page_size of page table[b, j // page_size]; entries of positions that no call
+    touches may hold anything. A tensor may be exchanged for another one or changed in place; every
+    call checks what the cache holds then."""
+
+    __slots__ = ("k", "v", "table", "_c")
+
+    def __init__(self, k, v, table):
+        self.k, self.v, self.table = k, v, table
+        self.view()
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, "_c", None)
+        object.__setattr__(self, name, value)
+
+    def view(self) -> _Pages:
+        """The checked C view; made and checked again when a tensor is not what it was."""
+        c, k, v, t = self._c, self.k, self.v, self.table
+        if c is None or c.at != _Pages.key(k, v, t):
+            c = _Pages(k, v, t)
+            object.__setattr__(self, "_c", c)
+        return c
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, Hkv: int, D: int, table, device="cuda") -> "PagedCache":
+        """A cache over a new pool of zero rows."""
+        z = lambda: torch.zeros(n_pages, page_size, Hkv, D, dtype=torch.bfloat16, device=device)  # noqa: E731
+        return cls(z(), z(), table)
+
+
+def _pages_of(p: Params, cache: PagedCache) -> _Pages:
+    if not isinstance(cache, PagedCache):
+        raise ValueError("cache must be a PagedCache")
+    c = cache.view()
+    if c.heads != (p.Hkv, p.D) or c.B != p.B or c.positions < p.L:
+        raise ValueError(f"the cache has {c.heads[0]} heads of {c.heads[1]} and a table of {c.B} sequences of {c.positions} positions, "
+                         f"the call {p.Hkv} heads of {p.D}, {p.B} sequences of {p.L}")
+    return c
+
+
+def _row_view(t, name: str, heads: int, p: Params, rows: int, index: int):
+    """byref of the ec_rows of t, bf16 [B, rows, heads, D] with adjacent heads."""
+    if t.dtype is not torch.bfloat16 or t.shape != (p.B, rows, heads, p.D):
+        raise ValueError(f"{name} must be bf16 {[p.B, rows, heads, p.D]}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}: EntropyCache kernels take CUDA tensors, all of one device")
+    sb, sr, sh, sd = t.stride()
+    if (sd != 1 and p.D > 1) or (sh != p.D and heads > 1):
+        raise ValueError(f"the heads of a row of {name} must be adjacent")
+    return ctypes.byref(C.EcRows(t.data_ptr(), sb if p.B > 1 else 0, sr if rows > 1 else heads * p.D))
+
+
+def _places(p: Params, idx, start, rows: int, index: int):
+    """(address of idx, its row stride, address of start): where the rows of a call stand."""
+    if idx is None:
+        return None, 0, _opt(start, "start", torch.int32, (p.B,), index)
+    if start is not None:
+        raise ValueError("idx and start exclude each other")
+    if idx.dtype is not torch.int32 or idx.dim() != 2 or idx.shape[0] != p.B or idx.shape[1] < rows or idx.get_device() != index:
+        raise ValueError(f"idx must be int32 [{p.B}, {rows} or more] on cuda:{index}, got {idx.dtype} {list(idx.shape)} on {idx.device}")
+    if idx.shape[1] > 1 and idx.stride(1) != 1:
+        raise ValueError("a sequence's idx must be contiguous")
+    return idx.data_ptr(), (idx.stride(0) if p.B > 1 else idx.shape[1]), None
+
+
+def kv_append_paged(p: Params, cache: PagedCache, k_new, v_new, R, idx=None, start=None, rope=None, q_new=None, q_out=None,
+                    dev_err=None, stream=None):
+    """(c) rows into a paged cache: for r < R[b], at position pos = idx[b, r] (strictly ascending), or
+    start[b] + r, or r: the K row of pos is k_new[b, r] turned by pos's angles, its V row v_new[b, r], and
+    q_out[b, r] is q_new[b, r] turned. k_new, v_new bf16 [B, rows, Hkv, D], q_new [B, rows, Hq, D]: views with
+    adjacent heads are taken (a fused projection's output); q_out contiguous. rope: (cos, sin) of rope_table
+    [L, D / 2], None: rows are copied. Returns q_out, a new tensor of zeros by default. See
+    ec_kv_append_paged."""
+    c = _pages_of(p, cache)
+    i, rows = c.index, k_new.shape[1]
+    kr, vr = _row_view(k_new, "k_new", p.Hkv, p, rows, i), _row_view(v_new, "v_new", p.Hkv, p, rows, i)
+    if q_new is None and q_out is not None:
+        raise ValueError("q_out without q_new")
+    qr = None if q_new is None else _row_view(q_new, "q_new", p.Hq, p, rows, i)
+    rp = _checked(R, "R", torch.int32, (p.B,), i)
+    ip, si, sp = _places(p, idx, start, rows, i)
+    cs = sn = None
+    if rope is not None:
+        cs, sn = (_checked(t, n, torch.float32, (p.L, p.D // 2), i) for t, n in zip(rope, ("cos", "sin")))
+    ep = _opt(dev_err, "dev_err", torch.int32, (1,), i)
+    op = None if q_out is None else _checked(q_out, "q_out", torch.bfloat16, (p.B, rows, p.Hq, p.D), i)
+    f = lib().ec_kv_append_paged
+    if stream is None and (op is not None or qr is None) and torch._C._cuda_getDevice() == i:
+        st = f(p.ref(), c.ref, rows, kr, vr, qr, op, cs, sn, ip, si, sp, rp, ep, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        def call(s):
+            nonlocal q_out
+            if q_new is not None and q_out is None:
+                q_out = torch.zeros(p.B, rows, p.Hq, p.D, dtype=torch.bfloat16, device=q_new.device)
+            o = None if q_out is None else q_out.data_ptr()
+            return f(p.ref(), c.ref, rows, kr, vr, qr, o, cs, sn, ip, si, sp, rp, ep, s)
+
+        st = _launch(i, stream, call)
+    C.check(st, "ec_kv_append_paged")
+    return q_out
+
+
+def paged_attention_workspace_size(p: Params, rows: int) -> int:
+    """Scratch bytes of paged_attention and paged_window_attention for q of [B, rows, Hq, D]."""
+    return int(lib().ec_paged_attention_workspace_size(p.ref(), rows))
+
+
+def _attend_paged(p: Params, q, cache, R, out, places, window, kv_len, scale, ws, dev_err, stream):
+    c = _pages_of(p, cache)
+    i = c.index
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, rows, Hq, D], got {list(q.shape)}")
+    rows = q.shape[1]
+    shape = (p.B, rows, p.Hq, p.D)
+    qp = _checked(q, "q", torch.bfloat16, shape, i)
+    op = _checked(out, "out", torch.bfloat16, shape, i)
+    rp = _checked(R, "R", torch.int32, (p.B,), i)
+    lp = _opt(kv_len, "kv_len", torch.int32, (p.B,), i)
+    ep = _opt(dev_err, "dev_err", torch.int32, (1,), i)
+    if ws is not None and (ws.get_device() != i or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {q.device}")
+    sc = (1.0 / math.sqrt(p.D)) if scale is None else float(scale)
+    if window is None:
+        what, where = "ec_paged_attention", ()
+    else:
+        what, where = "ec_paged_window_attention", _places(p, *places, rows, i)
+    f = getattr(lib(), what)
+
+    def call(s):
+        w = ws
+        if w is None:
+            w = torch.empty(max(256, paged_attention_workspace_size(p, rows)), dtype=torch.uint8, device=q.device)
+        if window is None:
+            return f(p.ref(), rows, qp, c.ref, rp, lp, sc, op, w.data_ptr(), w.nbytes, ep, s)
+        return f(p.ref(), rows, qp, c.ref, *where, rp, lp, *window, sc, op, w.data_ptr(), w.nbytes, ep, s)
+
+    C.check(_launch(i, stream, call), what)
+    return out
+
+
+def paged_attention(p: Params, q, cache: PagedCache, R, out, kv_len=None, scale: float | None = None,
+                    ws: torch.Tensor | None = None, dev_err=None, stream=None):
+    """(d) over a paged cache: out[b, r, h] = softmax(scale q k^T) v over the first kv_len[b] keys (None: the
+    scope's), for r < R[b]; zeros without a key. q, out bf16 [B, rows, Hq, D] (rows: the most that a sequence
+    has; 1 is the single-token form); R, kv_len int32 [B]; scale > 0. See ec_paged_attention."""
+    return _attend_paged(p, q, cache, R, out, None, None, kv_len, scale, ws, dev_err, stream)
+
+
+def paged_window_attention(p: Params, q, cache: PagedCache, R, out, left: int, right: int, sinks: int = 0, idx=None, start=None,
+                           kv_len=None, scale: float | None = None, ws: torch.Tensor | None = None, dev_err=None, stream=None):
+    """paged_attention where the row at position pos (idx[b, r], or start[b] + r, or r) sees the keys pos - left ..
+    pos + right (-1: no bound on that side) and the first `sinks` ones. See ec_paged_window_attention."""
+    return _attend_paged(p, q, cache, R, out, (idx, start), (int(left), int(right), int(sinks)), kv_len, scale, ws, dev_err, stream)
 
 
 @dataclass

@@ -21,6 +21,7 @@ EC_DEVERR_BAD_IDX = 0x2
 EC_DEVERR_BAD_R = 0x4
 EC_DEVERR_TIMEOUT = 0x8
 EC_DEVERR_BAD_LEN = 0x10
+EC_DEVERR_BAD_PAGE = 0x20
 
 EC_F32 = 0
 EC_BF16 = 1
@@ -64,6 +65,15 @@ class EcKv(ctypes.Structure):
     _fields_ = [("dtype", _i32), ("len", _i32), ("k", _p), ("v", _p), ("k_exp", _p), ("v_exp", _p)]
 
 
+class EcPagedKv(ctypes.Structure):
+    _fields_ = [("page_size", _i32), ("n_pages", _i32), ("page_stride", _i64), ("k", _p), ("v", _p), ("table", _p),
+                ("table_stride", _i64)]
+
+
+class EcRows(ctypes.Structure):
+    _fields_ = [("x", _p), ("batch_stride", _i64), ("row_stride", _i64)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES: dict[str, tuple] = {
     "ec_status_string": (ctypes.c_char_p, [_i32]),
@@ -91,6 +101,11 @@ SIGNATURES: dict[str, tuple] = {
     "ec_partial_attention_quant": (_i32, [_p, _p, _p, _p, _p, _f32, _p, _p, _sz, _p, _p]),
     "ec_prefix_attention_workspace_size": (_sz, [_p]),
     "ec_prefix_attention": (_i32, [_p, _p, _p, _p, _p, _p, _f32, _p, _p, _sz, _p, _p]),
+    "ec_kv_append_paged": (_i32, [_p, _p, _i32, _p, _p, _p, _p, _p, _p, _p, _i64, _p, _p, _p, _p]),
+    "ec_paged_attention_workspace_size": (_sz, [_p, _i32]),
+    "ec_paged_attention": (_i32, [_p, _i32, _p, _p, _p, _p, _f32, _p, _p, _sz, _p, _p]),
+    "ec_paged_window_attention": (_i32, [_p, _i32, _p, _p, _p, _i64, _p, _p, _p, _i32, _i32, _i32, _f32, _p, _p, _sz, _p,
+                                         _p]),
     "ec_step_workspace_size": (_sz, [ctypes.POINTER(EcParams)]),
     "ec_step": (_i32, [ctypes.POINTER(EcParams), ctypes.POINTER(EcState), _p, _p, _p, _i32,
                        ctypes.POINTER(_p), ctypes.POINTER(_p), ctypes.POINTER(_p), ctypes.POINTER(_p),

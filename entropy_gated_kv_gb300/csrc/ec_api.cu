@@ -469,6 +469,132 @@ ec_status ec_prefix_attention(const ec_params* p, const void* q, const ec_kv* pr
                           cached_attention_workspace_bytes(*p, true), dev_err, stream);
 }
 
+// ---- caches in pages -------------------------------------------------------------------------------
+namespace {
+
+size_t page_bytes(const ec_params& p, const ec_paged_kv& c) { return static_cast<size_t>(c.page_size) * p.Hkv * p.D * 2; }
+size_t pool_extent(const ec_params& p, const ec_paged_kv& c) {
+  return static_cast<size_t>(c.n_pages - 1) * c.page_stride * 2 + page_bytes(p, c);
+}
+size_t table_extent(const ec_params& p, const ec_paged_kv& c) {
+  const size_t row = (static_cast<size_t>(p.L) + c.page_size - 1) / c.page_size;
+  return (static_cast<size_t>(p.B - 1) * c.table_stride + row) * sizeof(int32_t);
+}
+// The pages of K and of V share no byte: apart, or page by page in one pool.
+bool pools_apart(const ec_params& p, const ec_paged_kv& c) {
+  const size_t n = pool_extent(p, c);
+  if (!overlaps(c.k, n, c.v, n)) return true;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(c.k), b = reinterpret_cast<uintptr_t>(c.v);
+  const size_t off = (a < b ? b - a : a - b) % (static_cast<size_t>(c.page_stride) * 2), page = page_bytes(p, c);
+  return off >= page && off + page <= static_cast<size_t>(c.page_stride) * 2;
+}
+
+ec_status check_pages(const ec_params& p, const ec_paged_kv* c, int32_t rows_max) {
+  if (c == nullptr || rows_max < 1 || rows_max > p.L) return EC_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0) return EC_ERR_UNSUPPORTED;
+  if (c->n_pages < 1 || !c->k || !c->v || !c->table) return EC_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->table)) return EC_ERR_INVALID_ARG;
+  if (c->page_stride % 8 != 0 || c->page_stride < static_cast<int64_t>(c->page_size) * p.Hkv * p.D) return EC_ERR_INVALID_ARG;
+  // bytes to any page in 40 bits, as tensor maps count them
+  if (c->page_stride >= (1ll << 36) || c->page_stride * 2 > (1ll << 40) / c->n_pages) return EC_ERR_UNSUPPORTED;
+  if (c->table_stride < 1 || c->table_stride > (1ll << 31) || c->table_stride * c->page_size < p.L) return EC_ERR_INVALID_ARG;
+  return pools_apart(p, *c) ? EC_OK : EC_ERR_INVALID_ARG;
+}
+
+// Strides of rows of `width` elements, and the bytes that they span.
+bool check_rows(const ec_params& p, const ec_rows& x, int32_t rows_max, int64_t width, size_t* bytes) {
+  if (!x.x || !aligned16(x.x) || x.batch_stride < 0 || x.row_stride < 0) return false;
+  if (x.batch_stride % 8 != 0 || x.row_stride % 8 != 0 || x.batch_stride > (1ll << 40) || x.row_stride > (1ll << 36)) return false;
+  if (rows_max > 1 && x.row_stride < width) return false;
+  *bytes = (static_cast<size_t>(p.B - 1) * x.batch_stride + static_cast<size_t>(rows_max - 1) * x.row_stride + width) * 2;
+  return true;
+}
+
+size_t idx_extent(const ec_params& p, int64_t stride, int32_t rows_max) {
+  return (static_cast<size_t>(p.B - 1) * stride + rows_max) * sizeof(int32_t);
+}
+bool check_places(const ec_params& p, const int32_t* idx, int64_t stride, const int32_t* start, int32_t rows_max) {
+  if (idx != nullptr && (start != nullptr || stride < rows_max || stride > (1ll << 31))) return false;
+  return aligned4(idx) && aligned4(start);
+}
+
+ec_status paged_attention(const ec_params* p, int32_t rows_max, const void* q, const ec_paged_kv* c, const RowPlaces& at,
+                          const Window* window, const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,
+                          size_t ws_bytes, int32_t* dev_err, ec_stream_t stream) {
+  ec_status r = check_params(p, kCheckAttn);
+  if (r != EC_OK) return r;
+  if ((r = check_pages(*p, c, rows_max)) != EC_OK) return r;
+  const int64_t heads = static_cast<int64_t>(p->B) * rows_max * p->Hq;  // rows of q, counted in 32 bits
+  if (heads > INT32_MAX) return EC_ERR_UNSUPPORTED;
+  if (!q || !R || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws)) return EC_ERR_INVALID_ARG;
+  const size_t ws_need = paged_attention_workspace_bytes(*p, rows_max);
+  if (!(scale > 0.f) || scale > 2e38f || ws_bytes < ws_need) return EC_ERR_INVALID_ARG;
+  if (!aligned4(R) || !aligned4(kv_len) || !aligned4(dev_err)) return EC_ERR_INVALID_ARG;
+  if (!check_places(*p, at.idx, at.stride, at.start, rows_max)) return EC_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(heads) * p->D * 2, pool = pool_extent(*p, *c);
+  const Extent written[] = {{out, n}, {ws, ws_need}};
+  const Extent read[] = {{q, n},          {c->k, pool},
+                         {c->v, pool},    {c->table, table_extent(*p, *c)},
+                         {R, int_bytes(p->B)}, {kv_len, int_bytes(p->B)},
+                         {at.idx, at.idx ? idx_extent(*p, at.stride, rows_max) : 0}, {at.start, int_bytes(p->B)}};
+  if (any_overlap(written, read)) return EC_ERR_INVALID_ARG;
+  ec_status st = EC_OK;
+  launch_paged_attention(*p, rows_max, q, *c, at, window, R, kv_len, scale, out, ws, dev_err,
+                         static_cast<cudaStream_t>(stream), &st);
+  return st;
+}
+
+}  // namespace
+
+ec_status ec_kv_append_paged(const ec_params* p, const ec_paged_kv* cache, int32_t rows_max, const ec_rows* k_new,
+                             const ec_rows* v_new, const ec_rows* q_new, void* q_out, const float* rope_cos,
+                             const float* rope_sin, const int32_t* idx, int64_t idx_stride, const int32_t* start,
+                             const int32_t* R, int32_t* dev_err, ec_stream_t stream) {
+  ec_status r = check_params(p, kCheckAttn);
+  if (r != EC_OK) return r;
+  if ((r = check_pages(*p, cache, rows_max)) != EC_OK) return r;
+  if (!k_new || !v_new || !R || (q_new != nullptr) != (q_out != nullptr) || (rope_cos != nullptr) != (rope_sin != nullptr))
+    return EC_ERR_INVALID_ARG;
+  const int64_t kv_width = static_cast<int64_t>(p->Hkv) * p->D, q_width = static_cast<int64_t>(p->Hq) * p->D;
+  if (kv_width > (1 << 26) || q_width > (1 << 26)) return EC_ERR_UNSUPPORTED;  // a row's pieces are counted in 32 bits
+  size_t nk = 0, nv = 0, nq = 0;
+  if (!check_rows(*p, *k_new, rows_max, kv_width, &nk) || !check_rows(*p, *v_new, rows_max, kv_width, &nv)) return EC_ERR_INVALID_ARG;
+  if (q_new && (!check_rows(*p, *q_new, rows_max, q_width, &nq) || !aligned16(q_out))) return EC_ERR_INVALID_ARG;
+  if (!aligned16(rope_cos) || !aligned16(rope_sin) || !aligned4(R) || !aligned4(dev_err)) return EC_ERR_INVALID_ARG;
+  if (!check_places(*p, idx, idx_stride, start, rows_max)) return EC_ERR_INVALID_ARG;
+  const size_t pool = pool_extent(*p, *cache), table = static_cast<size_t>(p->L) * p->D / 2 * sizeof(float);
+  const size_t no = q_out ? static_cast<size_t>(p->B) * rows_max * q_width * 2 : 0;
+  const Extent read[] = {{k_new->x, nk},  {v_new->x, nv}, {q_new ? q_new->x : nullptr, nq}, {rope_cos, table}, {rope_sin, table},
+                         {idx, idx ? idx_extent(*p, idx_stride, rows_max) : 0}, {start, int_bytes(p->B)}, {R, int_bytes(p->B)},
+                         {cache->table, table_extent(*p, *cache)}};
+  const Extent pools[] = {{cache->k, pool}}, pools_v[] = {{cache->v, pool}}, rotated[] = {{q_out, no}};
+  const Extent caches[] = {{cache->k, pool}, {cache->v, pool}};
+  if (any_overlap(pools, read) || any_overlap(pools_v, read)) return EC_ERR_INVALID_ARG;
+  if (no != 0 && (any_overlap(rotated, read) || any_overlap(rotated, caches))) return EC_ERR_INVALID_ARG;
+  return cuda_status(launch_kv_append_paged(*p, *cache, rows_max, *k_new, *v_new, q_new ? *q_new : ec_rows{}, q_out, rope_cos,
+                                            rope_sin, {idx, idx_stride, start}, R, dev_err, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ec_paged_attention_workspace_size(const ec_params* p, int32_t rows_max) {
+  if (check_params(p, kCheckAttn) != EC_OK || rows_max < 1 || rows_max > p->L) return 0;
+  return paged_attention_workspace_bytes(*p, rows_max);
+}
+
+ec_status ec_paged_attention(const ec_params* p, int32_t rows_max, const void* q, const ec_paged_kv* cache, const int32_t* R,
+                             const int32_t* kv_len, float scale, void* out, void* ws, size_t ws_bytes, int32_t* dev_err,
+                             ec_stream_t stream) {
+  return paged_attention(p, rows_max, q, cache, {}, nullptr, R, kv_len, scale, out, ws, ws_bytes, dev_err, stream);
+}
+
+ec_status ec_paged_window_attention(const ec_params* p, int32_t rows_max, const void* q, const ec_paged_kv* cache,
+                                    const int32_t* idx, int64_t idx_stride, const int32_t* start, const int32_t* R,
+                                    const int32_t* kv_len, int32_t left, int32_t right, int32_t sinks, float scale, void* out,
+                                    void* ws, size_t ws_bytes, int32_t* dev_err, ec_stream_t stream) {
+  if (left < -1 || right < -1 || sinks < 0) return EC_ERR_INVALID_ARG;
+  const Window w{left < 0 ? kMaxL : std::min(left, kMaxL), right < 0 ? kMaxL : std::min(right, kMaxL), std::min(sinks, kMaxL)};
+  return paged_attention(p, rows_max, q, cache, {idx, idx_stride, start}, &w, R, kv_len, scale, out, ws, ws_bytes, dev_err, stream);
+}
+
 // ---- the partial forward of one layer --------------------------------------------------------------
 namespace {
 ec_status check_layer(const ec_params* p, const ec_layer* w) {

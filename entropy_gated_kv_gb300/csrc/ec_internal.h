@@ -88,6 +88,27 @@ cudaError_t launch_cached_attention(const ec_params& p, const void* q, const ec_
                                     const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,
                                     int32_t* dev_err, cudaStream_t s, ec_status* status);
 
+// ---- cache in pages (kv_paged.cu, attention_paged.cu) -----------------------------------------
+// Where a call's rows stand: idx[b * stride + r], or start[b] + r, or r.
+struct RowPlaces {
+  const int32_t* idx;
+  int64_t stride;
+  const int32_t* start;
+};
+// The keys j that the row at pos sees: j < sinks, or pos - left <= j <= pos + right. No bound: the
+// largest position (left, right <= 2^20).
+struct Window {
+  int32_t left, right, sinks;
+};
+cudaError_t launch_kv_append_paged(const ec_params& p, const ec_paged_kv& c, int32_t rows_max, const ec_rows& k,
+                                   const ec_rows& v, const ec_rows& q, void* q_out, const float* cs, const float* sn,
+                                   const RowPlaces& at, const int32_t* R, int32_t* dev_err, cudaStream_t s);
+size_t paged_attention_workspace_bytes(const ec_params& p, int32_t rows_max);
+// window null: every key.
+cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const void* q, const ec_paged_kv& c,
+                                   const RowPlaces& at, const Window* window, const int32_t* R, const int32_t* kv_len,
+                                   float scale, void* out, void* ws, int32_t* dev_err, cudaStream_t s, ec_status* status);
+
 // ---- dense attention, two query tiles per CTA (attention_dense.cu): every position against
 // every key ---------------------------------------------------------------------------------
 cudaError_t launch_dense_attention_tiles(const ec_params& p, const void* q, const void* k_cache, const void* v_cache,

@@ -21,7 +21,8 @@
  *
  * A cache may be held in 8 bits: ec_kv_scatter_quant and ec_kv_gather_quant write and read it,
  * ec_partial_attention_quant attends to it. ec_prefix_attention serves a batch whose sequences
- * share a prefix.
+ * share a prefix. A cache may lie in pages of a pool: ec_kv_append_paged rotates and writes rows,
+ * ec_paged_attention and ec_paged_window_attention attend to them.
  *
  * Beyond the step: ec_layer_forward runs the partial (or full) forward of one transformer layer
  * for the recompute set; ec_lm_head_entropy computes (a) from the candidates' hidden states (the
@@ -72,6 +73,7 @@ typedef int32_t ec_status;
 #define EC_DEVERR_BAD_R 0x4         /* recompute-set size outside [0, L]                 */
 #define EC_DEVERR_TIMEOUT 0x8       /* a bounded pipeline wait ran out                   */
 #define EC_DEVERR_BAD_LEN 0x10      /* key length outside [0, L]                         */
+#define EC_DEVERR_BAD_PAGE 0x20     /* page number outside [0, n_pages)                  */
 
 /* ---- logits element types ------------------------------------------------------------ */
 #define EC_F32 0
@@ -436,6 +438,93 @@ size_t ec_prefix_attention_workspace_size(const ec_params* p);
 ec_status ec_prefix_attention(const ec_params* p, const void* q, const ec_kv* prefix, const ec_kv* cache,
                               const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,
                               size_t ws_bytes, int32_t* dev_err, ec_stream_t stream);
+
+/* ---- K/V caches in pages -------------------------------------------------------------------
+ * One layer's K/V cache of a batch whose sequences grow and end at different times: positions lie
+ * in pages of a pool, and a table names the pages of each sequence in order. The pages (gist.science)
+ * keep one dense cache per generation and have no counterpart.
+ *   k, v         bf16 [n_pages, page_size, Hkv, D]; page_stride elements from a page to the next (at
+ *                least page_size Hkv D, a multiple of 8; the two arrays may lie in one pool page by
+ *                page, but share no byte).
+ *   page_size    positions per page: a power of two, 16 .. 1024.
+ *   table        int32 [B, table_stride], table_stride page_size >= p->L: position j of sequence b is
+ *                row j % page_size of page table[b, j / page_size]. Entries of positions that no
+ *                call touches may hold anything. Two sequences may read the same page.
+ * A page number outside [0, n_pages) sets EC_DEVERR_BAD_PAGE; its rows are not written, and are read
+ * as zeros. */
+typedef struct ec_paged_kv {
+  int32_t page_size, n_pages;
+  int64_t page_stride;
+  void *k, *v;
+  const int32_t* table;
+  int64_t table_stride;
+} ec_paged_kv;
+
+/* Rows [B, rows_max, heads, D], bf16: the heads of a row are adjacent (D elements each); batch_stride
+ * and row_stride in elements, not negative, multiples of 8 (a view of a fused projection's output). x
+ * 16-byte aligned. row_stride >= heads D where rows_max > 1; a batch_stride of 0 repeats the rows. */
+typedef struct ec_rows {
+  const void* x;
+  int64_t batch_stride, row_stride;
+} ec_rows;
+
+/* ---- (c) rotated rows into a paged cache -----------------------------------------------------
+ * For r < R[b], at position pos = idx[b * idx_stride + r], or with idx NULL start[b] + r (start NULL:
+ * r; rows that are appended at a sequence's end):
+ *   K row of pos = rotate(k_new[b, r], pos), V row of pos = v_new[b, r],
+ *   q_out[b, r] = rotate(q_new[b, r], pos)               (q_new and q_out both NULL: no queries)
+ * rotate turns features i and i + D/2 of each head by the angle whose cosine and sine stand in
+ * rope_cos, rope_sin [L, D / 2] at row pos (ec_rope_table), in fp32, rounded once to bf16; both NULL: rows
+ * are copied as they are.
+ * k_new, v_new: ec_rows of Hkv heads, q_new of Hq; q_out bf16 [B, rows_max, Hq, D], rows at and past R[b]
+ * are not written. idx int32 on the device, strictly ascending per sequence, as ec_select_recompute
+ * writes them (idx_stride >= rows_max: st->idx with idx_stride = L may be given); an idx that is not
+ * below its successor sets EC_DEVERR_BAD_IDX and its row is skipped. start int32 [B] on the device.
+ * A position outside [0, L) sets EC_DEVERR_BAD_IDX, an R outside [0, rows_max] EC_DEVERR_BAD_R; the row,
+ * the sequence is skipped (a row whose page is bad still writes q_out). Pages that the call writes belong to
+ * one sequence and stand once in its table. 1 <= rows_max <= L; D 64 or 128. The caches and q_out must not
+ * overlap each other or the other buffers (EC_ERR_INVALID_ARG). */
+ec_status ec_kv_append_paged(const ec_params* p, const ec_paged_kv* cache, int32_t rows_max, const ec_rows* k_new,
+                             const ec_rows* v_new, const ec_rows* q_new, void* q_out, const float* rope_cos,
+                             const float* rope_sin, const int32_t* idx, int64_t idx_stride, const int32_t* start,
+                             const int32_t* R, int32_t* dev_err, ec_stream_t stream);
+
+/* ---- (d) attention over a paged cache --------------------------------------------------------
+ * ec_partial_attention with K and V in pages, rows in arrays of rows_max per sequence and a key length
+ * per sequence. For r < R[b], query head h:
+ *   out[b, r, h, :] = softmax over the keys j < n of scale <q[b, r, h], k_j>, times the values,
+ * n = kv_len[b], or with kv_len NULL all keys of the gate's scope ([0, L), or [0, scope_hi)); a kv_len past
+ * scope_hi is cut there. rows_max = 1 is the single-token form.
+ * q, out bf16 [B, rows_max, Hq, D], 1 <= rows_max <= L; rows at and past R[b] are not written. Without a
+ * key, or when every score is -infinity, a row is zeros. What lies in the pages past n is not used,
+ * NaN included, nor the table's entries there.
+ * kv_len int32 [B] on the device, or NULL. A length outside [0, L] sets EC_DEVERR_BAD_LEN, an R outside
+ * [0, rows_max] EC_DEVERR_BAD_R; the sequence is skipped. EC_ERR_UNSUPPORTED for B * rows_max * Hq of
+ * 2^31 or more. scale must be above 0 and at most 2e38.
+ * ws: ec_paged_attention_workspace_size(p, rows_max) bytes, 16-byte aligned, no initial contents needed;
+ * calls that share it must not overlap in time. It must not overlap the other buffers, nor out the inputs
+ * (EC_ERR_INVALID_ARG). Products, sums and rounding as ec_partial_attention; no atomics: the same inputs
+ * give the same bits. */
+size_t ec_paged_attention_workspace_size(const ec_params* p, int32_t rows_max);
+ec_status ec_paged_attention(const ec_params* p, int32_t rows_max, const void* q, const ec_paged_kv* cache,
+                             const int32_t* R, const int32_t* kv_len, float scale, void* out, void* ws,
+                             size_t ws_bytes, int32_t* dev_err, ec_stream_t stream);
+
+/* ---- (d) attention over a paged cache with a window and first tokens that stay visible -------
+ * ec_paged_attention where the row at position pos (idx, idx_stride and start as in
+ * ec_kv_append_paged) sees the keys j < n with
+ *   j < sinks, or pos - left <= j <= pos + right;
+ * left, right, sinks >= 0, and left or right -1: no bound on that side (left -1, right 0 is the causal
+ * form). A row that sees no key is zeros. A row at a position outside [0, L) sets EC_DEVERR_BAD_IDX and is
+ * not written. idx ascend per sequence (repeats allowed); where they do not, a row is either right, or not
+ * written and EC_DEVERR_BAD_IDX is set.
+ * Only the pages between the first and the last key that a sequence's rows see, and the sinks', are
+ * read; the values they hold there must be finite (a weight of zero times NaN is NaN). What lies outside
+ * is not used, NaN included. Same workspace as ec_paged_attention. */
+ec_status ec_paged_window_attention(const ec_params* p, int32_t rows_max, const void* q, const ec_paged_kv* cache,
+                                    const int32_t* idx, int64_t idx_stride, const int32_t* start, const int32_t* R,
+                                    const int32_t* kv_len, int32_t left, int32_t right, int32_t sinks, float scale,
+                                    void* out, void* ws, size_t ws_bytes, int32_t* dev_err, ec_stream_t stream);
 
 /* ---- the partial forward of one transformer layer ------------------------------------------
  * The forward pass the step's flag selects (EntropyCache, gist.science zh summary §2.2,
