@@ -1,0 +1,456 @@
+// attention_paged_rows.cu — attention over a paged K/V cache for few rows: single tokens and short blocks, at most 32
+// packed rows (a sequence's positions times the g query heads of a KV head).
+//
+//   out[x] = sum_j p_xj v_j / sum_j p_xj, p_xj = 2^(s_xj - m_x), s_xj = scale log2(e) <q_x, k_j>, m_x a running maximum
+// A cache byte is used for two products a row, so HBM bounds the call, and for short caches the chain of
+// sizes, page numbers, first keys, join. Hence:
+//   - Warps work by themselves: a chunk of 16 keys (inside one page, as pages are multiples of 16) is one TMA
+//     box for K and one for V in the warp's own ring; scores, softmax and P V of it stay in the warp's
+//     registers (mma.sync m16n8k16: with 16 rows a tensor-memory tile would be an eighth full and every block would
+//     pass through other warps). No barrier of the CTA until an item ends.
+//   - The chunks of all items (sequence, KV head) stand in one line, eight to a unit, and the CTAs, one an SM,
+//     take equal shares of it: long and short sequences load the SMs alike. An item cut between CTAs leaves
+//     fp32 partial rows, which a second launch joins.
+//   - A window leaves the chunks of its keys and of the sinks in the line, nothing else is read.
+#include <algorithm>
+
+#include "paged_common.cuh"
+
+namespace ec {
+namespace paged {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kChunk = 16;  // keys of a warp's step
+constexpr int kChunkShift = 4;
+
+// A CTA's place in the line: unit u of item (b, kvh), `left` units of the share from there on.
+struct Place {
+  int b, kvh, u, left;
+};
+
+struct Misc {
+  int scan[kWarps];
+  Place begin;
+  int share, abort;
+};
+
+template <int D, int MT>
+struct Layout {
+  static constexpr int kKBytes = kChunk * D * 2;  // a K or V chunk: [D / 64][16][64], 128-byte swizzle
+  static constexpr int kStage = 2 * kKBytes;
+  static constexpr int kStages = D == 64 ? 5 : MT == 1 ? 3 : 2;  // chunks in flight a warp
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kPitch = D + 4;  // floats of a row in the join's buffers: two rows in 8 share a bank
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kJoinOff = kRing;
+  static constexpr int kStatOff = kJoinOff + kWarps / 2 * kRows * kPitch * 4;
+  static constexpr int kBarOff = kStatOff + kWarps * kRows * 8;
+  static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
+  static constexpr int kBytes = kMiscOff + static_cast<int>(sizeof(Misc));
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+// A sequence in the line: its chunks, and what its rows see.
+struct Seq {
+  int rows, n, chunks, units;
+  Hull h;
+  Blocks k;
+};
+
+EC_DEV Seq load_seq(const Shape& s, int b, bool tell) {
+  Seq q;
+  sizes_of(s, b, tell, q.rows, q.n);
+  q.h = q.rows > 0 ? hull_of(s, b, 0, q.rows, q.n) : Hull{0, 0, 0};
+  q.k = blocks_of(q.h, kChunkShift);
+  q.chunks = q.k.count;
+  q.units = q.rows > 0 ? max(1, (q.chunks + kWarps - 1) / kWarps) : 0;  // rows without a key are written too
+  return q;
+}
+
+EC_DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+EC_DEV void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+EC_DEV void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_constant__ Args a) {
+  using LY = Layout<D, MT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc& misc = *reinterpret_cast<Misc*>(smem + LY::kMiscOff);
+  const Shape& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + LY::kBarOff) + warp * LY::kStages;
+  const uint32_t ring = smem_u32(smem) + warp * LY::kStages * LY::kStage;
+  if (lane < LY::kStages) {
+    mbar_init(&full[lane], 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    misc.abort = (smem_u32(smem) & 1023u) != 0u;  // the swizzled chunks need the alignment that dynamic shared memory has here
+    if (misc.abort) report_error(s.dev_err, EC_DEVERR_TIMEOUT);
+    misc.begin = {0, 0, 0, 0};
+    prefetch_tmap(&a.tk);
+    prefetch_tmap(&a.tv);
+  }
+  pdl_wait();  // everything may come from the previous kernels in the stream
+  pdl_launch_dependents();
+
+  // The line: each thread adds up the units of its sequences, the CTA their sum, and the thread whose sequences hold the
+  // first unit of this CTA's share finds it.
+  const int per = (s.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
+  int mine = 0;
+  for (int b = b0; b < min(b0 + per, s.B); ++b) mine += load_seq(s, b, blockIdx.x == 0).units * s.Hkv;
+  int incl = warp_inclusive(mine);
+  if (lane == 31) misc.scan[warp] = incl;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) incl += misc.scan[w];
+    total += misc.scan[w];
+  }
+  const int share = (total + gridDim.x - 1) / gridDim.x;
+  const int begin = blockIdx.x * share;
+  if (begin < total && begin >= incl - mine && begin < incl) {
+    int off = begin - (incl - mine);
+    for (int b = b0;; ++b) {
+      const int units = load_seq(s, b, false).units;
+      if (off < units * s.Hkv) {
+        misc.begin = {b, off / units, off % units, min(share, total - begin)};
+        break;
+      }
+      off -= units * s.Hkv;
+    }
+  }
+  if (threadIdx.x == 0) misc.share = share;
+  __syncthreads();
+  if (threadIdx.x == 0) a.records[blockIdx.x].parts = 0;
+  Place at = misc.begin;
+  if (at.left == 0 || misc.abort) return;
+
+  // ---- loads: the warp's chunks in the line's order, kStages of them ahead
+  Place la = at;
+  Seq ls = load_seq(s, la.b, false);
+  int l_u1 = min(ls.units, la.u + la.left);  // end of this item's units in the share
+  int l_base = -1, l_page = 0;               // lane i: the page of the warp's chunk of unit l_base + i
+  int issued = 0;
+  auto issue = [&]() {
+    for (;;) {
+      if (la.left == 0) return;
+      const int v = la.u * kWarps + warp;
+      if (la.u < l_u1 && v < ls.chunks) break;
+      if (la.u < l_u1) {  // the last unit of an item has no chunk for this warp
+        ++la.u;
+        --la.left;
+        continue;
+      }
+      la.u = 0;
+      if (++la.kvh == s.Hkv) {
+        la.kvh = 0;
+        do ls = load_seq(s, ++la.b, false);
+        while (ls.units == 0);
+      }
+      l_u1 = min(ls.units, la.left);
+      l_base = -1;
+    }
+    if (l_base < 0 || la.u >= l_base + 32) {
+      l_base = la.u;
+      const int v = (l_base + lane) * kWarps + warp;
+      l_page = l_base + lane < l_u1 && v < ls.chunks ? page_of(s, la.b, ls.k.block(v) << kChunkShift) : s.n_pages;
+    }
+    const int page = __shfl_sync(0xffffffffu, l_page, la.u - l_base);
+    if (lane == 0) {
+      const int st = issued % LY::kStages;
+      const int slot = (ls.k.block(la.u * kWarps + warp) << kChunkShift) & ((1 << s.page_shift) - 1);
+      uint8_t* dst = smem + (warp * LY::kStages + st) * LY::kStage;
+      mbar_arrive_expect_tx(&full[st], LY::kStage);
+      tma_load_5d(dst, &a.tk, &full[st], 0, slot, 0, la.kvh, page);
+      tma_load_5d(dst + LY::kKBytes, &a.tv, &full[st], 0, slot, 0, la.kvh, page);
+    }
+    ++issued;
+    ++la.u;
+    --la.left;
+  };
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < LY::kStages; ++i) issue();
+
+  // ---- items of the share
+  const int gid = lane >> 2, tid = lane & 3;  // a fragment's row and column pair
+  const uint32_t k_lane = ((lane >> 4) * 8 + (lane & 7)) * 128, k_c = (lane >> 3) & 1;
+  const uint32_t v_lane = (((lane >> 3) & 1) * 8 + (lane & 7)) * 128, v_c = lane >> 4;
+  const uint32_t swz = lane & 7;
+  int used = 0;
+  bool ok = true;
+  Seq cs = load_seq(s, at.b, false);
+  for (;;) {
+    const int u1 = min(cs.units, at.u + at.left);
+    const int packed = cs.rows * s.g;
+    // the rows of this thread's fragments: their queries, and the keys that they see
+    uint32_t qf[MT][D / 16][4];
+    int r_lo[MT][2], r_hi[MT][2];
+    bool even = true;  // this thread's rows see the same keys as the hull
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int x = 16 * t + gid + 8 * e;
+        const bool live = x < packed;
+        const int r = live ? s.by_g(x) : 0;
+        const uint16_t* src = a.q + ((static_cast<int64_t>(at.b) * s.rows_max + r) * s.Hq + at.kvh * s.g + (x - r * s.g)) * D + 2 * tid;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qf[t][kk][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk)) : 0u;
+          qf[t][kk][e + 2] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8)) : 0u;
+        }
+        r_lo[t][e] = cs.h.lo, r_hi[t][e] = cs.h.hi;
+        if (s.windowed && live) {
+          const int64_t pos = raw_position(s.at, at.b, r);
+          const int p = inside(pos, s.L) ? static_cast<int>(pos) : 0;
+          r_lo[t][e] = max(p - s.w.left, 0);
+          r_hi[t][e] = min(p + s.w.right + 1, cs.n);
+          even = even && r_lo[t][e] <= cs.h.lo && r_hi[t][e] >= cs.h.hi;
+        }
+      }
+    even = __all_sync(0xffffffffu, even);
+
+    float o[MT][D / 8][4] = {};
+    float m[MT][2], l[MT][2];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[t][e] = -INFINITY, l[t][e] = 0.f;
+
+#pragma unroll 1
+    for (int u = at.u; u < u1; ++u) {
+      const int v = u * kWarps + warp;
+      if (v >= cs.chunks) break;
+      const int st = used % LY::kStages;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&full[st], (used / LY::kStages) & 1, &misc.abort, s.dev_err, kWaitLimitNs));
+      if (!ok) break;
+      const int j0 = cs.k.block(v) << kChunkShift;
+      const uint32_t kb = ring + st * LY::kStage, vb = kb + LY::kKBytes;
+      const bool whole = j0 + kChunk <= cs.h.near || (j0 >= cs.h.lo && j0 + kChunk <= cs.h.hi);
+      if (!whole) {  // rows of V outside the hull may hold anything, and a weight of zero times NaN is NaN
+        const int j = j0 + (lane >> 1);
+        if (!(j < cs.h.near || (j >= cs.h.lo && j < cs.h.hi)))
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const int c = (lane & 1) * (D / 16) + i;
+            st_shared16(vb + (c >> 3) * (kChunk * 128) + (lane >> 1) * 128 + (c & 7) * 16, make_uint4(0, 0, 0, 0));
+          }
+        fence_proxy_async_smem();  // before the TMA writes there again
+        __syncwarp();
+      }
+      // scores of 16 keys: two fragments of 8
+      float sc[MT][2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t kf[4];
+        ldsm4(kf, kb + (kk >> 2) * (kChunk * 128) + k_lane + ((((kk & 3) * 2 + k_c) ^ swz) << 4));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          mma16816(sc[t][0], qf[t][kk], kf[0], kf[1]);
+          mma16816(sc[t][1], qf[t][kk], kf[2], kf[3]);
+        }
+      }
+      if (!(whole && even)) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int j = j0 + 8 * i + 2 * tid + (c & 1);
+              if (!(j < cs.h.near || (j >= r_lo[t][c >> 1] && j < r_hi[t][c >> 1]))) sc[t][i][c] = -INFINITY;
+            }
+      }
+      uint32_t pf[MT][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        float mx[2];
+        bool grow = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(fmaxf(sc[t][0][2 * e], sc[t][0][2 * e + 1]), fmaxf(sc[t][1][2 * e], sc[t][1][2 * e + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          mx[e] = x * s.scale_log2;
+          grow = grow || mx[e] > m[t][e] + kRescaleLog2;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+          float al[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool up = mx[e] > m[t][e] + kRescaleLog2;
+            al[e] = up ? ex2_approx(m[t][e] - mx[e]) : 1.f;
+            if (up) m[t][e] = mx[e];
+            l[t][e] *= al[e];
+          }
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[t][d][c] *= al[c >> 1];
+        }
+        float p[2][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float nm = m[t][e] == -INFINITY ? 0.f : -m[t][e];  // no key seen yet: every score is -infinity
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) p[i][2 * e + c] = ex2_approx(fmaf(sc[t][i][2 * e + c], s.scale_log2, nm));
+          l[t][e] += (p[0][2 * e] + p[0][2 * e + 1]) + (p[1][2 * e] + p[1][2 * e + 1]);
+        }
+        // the weights are rounded to bf16 for the product (2^-8 of each), the sum is of the unrounded ones
+        pf[t][0] = pack_bf16x2(p[0][0], p[0][1]);
+        pf[t][1] = pack_bf16x2(p[0][2], p[0][3]);
+        pf[t][2] = pack_bf16x2(p[1][0], p[1][1]);
+        pf[t][3] = pack_bf16x2(p[1][2], p[1][3]);
+      }
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        uint32_t vf[4];
+        ldsm4t(vf, vb + (d >> 2) * (kChunk * 128) + v_lane + ((((d & 3) * 2 + v_c) ^ swz) << 4));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          mma16816(o[t][2 * d], pf[t], vf[0], vf[1]);
+          mma16816(o[t][2 * d + 1], pf[t], vf[2], vf[3]);
+        }
+      }
+      ++used;
+      __syncwarp();
+      issue();
+    }
+
+    // ---- join of the eight warps
+    float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
+    float* join = reinterpret_cast<float*>(smem + LY::kJoinOff);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 1);
+        l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 2);
+        if (tid == 0) stat[warp * LY::kRows + 16 * t + gid + 8 * e] = make_float2(m[t][e], l[t][e]);
+      }
+    __syncthreads();
+    auto put = [&](int w, bool add) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int x = 16 * t + gid + 8 * e;
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) top = fmaxf(top, stat[i * LY::kRows + x].x);
+          const float f = m[t][e] == -INFINITY ? 0.f : ex2_approx(m[t][e] - top);
+          float2* row = reinterpret_cast<float2*>(join + (w * LY::kRows + x) * LY::kPitch) + tid;
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            float2 y = make_float2(o[t][d][2 * e] * f, o[t][d][2 * e + 1] * f);
+            if (add) y.x += row[4 * d].x, y.y += row[4 * d].y;
+            row[4 * d] = y;
+          }
+        }
+    };
+    if (warp >= kWarps / 2) put(warp - kWarps / 2, false);
+    __syncthreads();
+    if (warp < kWarps / 2) put(warp, true);
+    __syncthreads();
+    const bool cut_here = u1 < cs.units;
+    const bool part = at.u > 0 || cut_here;
+    const int slot = blockIdx.x * kFewSlots + (at.u == 0 ? 1 : 0);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < packed * (D / 8); i += kThreads) {
+      const int x = i / (D / 8), c = i % (D / 8) * 8;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * LY::kRows + x].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 st = stat[w * LY::kRows + x];
+        sum += st.x == -INFINITY ? 0.f * st.y : ex2_approx(st.x - top) * st.y;  // a NaN sum stays one
+      }
+      float4 y[2] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps / 2; ++w)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 z = *reinterpret_cast<const float4*>(join + (w * LY::kRows + x) * LY::kPitch + c + 4 * h);
+          y[h].x += z.x, y[h].y += z.y, y[h].z += z.z, y[h].w += z.w;
+        }
+      if (part) {
+        float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * kFewRows + x) * D + c);
+        dst[0] = y[0], dst[1] = y[1];
+        if (c == 0) a.part_stat[slot * kFewRows + x] = make_float2(top, sum);
+      } else {
+        const int r = s.by_g(x);
+        if (s.windowed && !inside(raw_position(s.at, at.b, r), s.L)) {
+          report_error(s.dev_err, EC_DEVERR_BAD_IDX);
+          continue;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint4 z;
+        z.x = pack_bf16x2(y[0].x * inv, y[0].y * inv);
+        z.y = pack_bf16x2(y[0].z * inv, y[0].w * inv);
+        z.z = pack_bf16x2(y[1].x * inv, y[1].y * inv);
+        z.w = pack_bf16x2(y[1].z * inv, y[1].w * inv);
+        *reinterpret_cast<uint4*>(a.out + ((static_cast<int64_t>(at.b) * s.rows_max + r) * s.Hq + at.kvh * s.g + (x - r * s.g)) * D + c) = z;
+      }
+    }
+    at.left -= u1 - at.u;
+    if (!ok)  // a wait gave up: the copies in flight land before the CTA ends, as far as they do
+      for (; used < issued; ++used)
+        for (int i = 0; i < (1 << 16) && !mbar_try_wait(&full[used % LY::kStages], (used / LY::kStages) & 1); ++i) {
+        }
+    if (at.left == 0) {
+      if (threadIdx.x == 0 && cut_here && at.u == 0) {  // the item begins here and goes on in the next CTAs
+        const int rest = cs.units - u1;
+        a.records[blockIdx.x] = {1 + (rest + misc.share - 1) / misc.share, at.b, at.kvh, 0, packed, {0, 0, 0}};
+      }
+      break;
+    }
+    __syncthreads();  // the join's buffers are free
+    at.u = 0;
+    if (++at.kvh == s.Hkv) {
+      at.kvh = 0;
+      do cs = load_seq(s, ++at.b, false);
+      while (cs.units == 0);
+    }
+  }
+}
+
+template <int D, int MT>
+cudaError_t launch(const Args& a, int ctas, cudaStream_t s) {
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(few_rows_kernel<D, MT>), Layout<D, MT>::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(few_rows_kernel<D, MT>, dim3(ctas), dim3(kThreads), Layout<D, MT>::kBytes, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_few_rows(const Args& a, int D, int ctas, cudaStream_t s) {
+  const bool one = a.s.rows_max * a.s.g <= 16;
+  if (D == 64) return one ? launch<64, 1>(a, ctas, s) : launch<64, 2>(a, ctas, s);
+  return one ? launch<128, 1>(a, ctas, s) : launch<128, 2>(a, ctas, s);
+}
+
+}  // namespace paged
+}  // namespace ec

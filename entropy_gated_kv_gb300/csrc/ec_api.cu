@@ -526,6 +526,8 @@ ec_status paged_attention(const ec_params* p, int32_t rows_max, const void* q, c
   if ((r = check_pages(*p, c, rows_max)) != EC_OK) return r;
   const int64_t heads = static_cast<int64_t>(p->B) * rows_max * p->Hq;  // rows of q, counted in 32 bits
   if (heads > INT32_MAX) return EC_ERR_UNSUPPORTED;
+  const int64_t tiles = (static_cast<int64_t>(rows_max) * (p->Hq / p->Hkv) + 127) / 128, blocks = p->L / 128 + 2;
+  if (p->B * static_cast<int64_t>(p->Hkv) * tiles > (1ll << 30) / blocks) return EC_ERR_UNSUPPORTED;  // steps, in 32 bits
   if (!q || !R || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws)) return EC_ERR_INVALID_ARG;
   const size_t ws_need = paged_attention_workspace_bytes(*p, rows_max);
   if (!(scale > 0.f) || scale > 2e38f || ws_bytes < ws_need) return EC_ERR_INVALID_ARG;

@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       const int u = base + i * kThreads;
       if (u >= n) break;
       const int rl = a.per_row(u), w = u - rl * a.pieces, h = w / T, t = w % T, r = r0 + rl;
-      const int pos = position(a.at, b, r, a.L);
+      const int64_t raw = raw_position(a.at, b, r);
+      const int pos = inside(raw, a.L) ? static_cast<int>(raw) : -1;
       // a position given twice would be written by two rows at once
       const bool twice = a.at.idx != nullptr && r + 1 < Rb && pos >= __ldg(a.at.idx + b * a.at.stride + r + 1);
       if (pos < 0 || twice) {

@@ -1,6 +1,8 @@
-// paged_common.cuh — what the kernels over a paged K/V cache share: where a call's rows stand and
-// which keys they see.
+// paged_common.cuh — what the kernels over a paged K/V cache share: where a call's rows stand, which
+// keys they see, the line of work that the CTAs cut into shares, and the partial rows that a cut leaves.
 #pragma once
+
+#include <cuda.h>
 
 #include "ec_common.cuh"
 #include "ec_internal.h"
@@ -8,20 +10,124 @@
 namespace ec {
 namespace paged {
 
-// Position of row r of sequence b; -1 when it lies outside [0, L).
-EC_DEV int position(const RowPlaces& at, int b, int r, int L) {
-  int64_t p = r;
-  if (at.idx != nullptr) p = __ldg(at.idx + b * at.stride + r);
-  else if (at.start != nullptr) p += __ldg(at.start + b);
-  return p >= 0 && p < L ? static_cast<int>(p) : -1;
+constexpr int kMaxCtas = 160;  // bound of the attention grids, for the workspace
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.f;  // the running maximum is moved when it grows by more than 2^8
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per pipeline wait
+
+// An item that is cut between CTAs, as the CTA that begins it leaves it for the merge: parts 0 (nothing to merge) or
+// the number of CTAs from this one on that hold partial rows of it.
+struct Record {
+  int32_t parts, b, kvh, row0, rows;  // packed rows row0 .. row0 + rows - 1 of (b, kvh)
+  int32_t pad[3];
+};
+
+struct Shape {
+  int32_t B, L, Hq, Hkv, g, rows_max, scope_hi, windowed, page_shift, n_pages;
+  int64_t table_stride;
+  float scale_log2;
+  FastDiv by_g;
+  Window w;
+  RowPlaces at;
+  const int32_t *R, *kv_len, *table;
+  int32_t* dev_err;
+};
+
+struct Args {
+  CUtensorMap tk, tv, tq;
+  Shape s;
+  const uint16_t* q;
+  uint16_t* out;
+  float* part_o;      // [slots][rows of a slot][D]
+  float2* part_stat;  // [slots][rows of a slot]: running maximum (base 2, scaled) and sum
+  Record* records;    // [CTAs]
+};
+
+// Position of row r of sequence b; it may lie outside [0, L).
+EC_DEV int64_t raw_position(const RowPlaces& at, int b, int r) {
+  if (at.idx != nullptr) return __ldg(at.idx + b * at.stride + r);
+  return at.start != nullptr ? static_cast<int64_t>(__ldg(at.start + b)) + r : r;
+}
+EC_DEV bool inside(int64_t pos, int L) { return pos >= 0 && pos < L; }
+
+// Rows and keys of sequence b; rows 0 where a size is bad (`tell`: reported).
+EC_DEV void sizes_of(const Shape& s, int b, bool tell, int& rows, int& keys) {
+  rows = __ldg(s.R + b);
+  keys = s.kv_len == nullptr ? s.scope_hi : __ldg(s.kv_len + b);
+  if (rows < 0 || rows > s.rows_max) {
+    if (tell) report_error(s.dev_err, EC_DEVERR_BAD_R);
+    rows = 0;
+  }
+  if (keys < 0 || keys > s.L) {
+    if (tell) report_error(s.dev_err, EC_DEVERR_BAD_LEN);
+    rows = keys = 0;
+  }
+  keys = min(keys, s.scope_hi);
 }
 
-// Keys of sequence b: kv_len, cut at the scope's end; -1 for a length outside [0, L].
-EC_DEV int key_count(const int32_t* kv_len, int b, int L, int scope_hi) {
-  if (kv_len == nullptr) return scope_hi;
-  const int n = __ldg(kv_len + b);
-  return n < 0 || n > L ? -1 : min(n, scope_hi);
+// The keys that rows r0 .. r1 - 1 of a sequence of n keys see between them: j < near, or lo <= j < hi.
+struct Hull {
+  int near, lo, hi;
+};
+EC_DEV Hull hull_of(const Shape& s, int b, int r0, int r1, int n) {
+  if (!s.windowed) return {0, 0, n};
+  int64_t p0 = raw_position(s.at, b, r0), p1 = raw_position(s.at, b, r1 - 1);
+  while (!inside(p0, s.L) && r0 + 1 < r1) p0 = raw_position(s.at, b, ++r0);  // rows at bad positions are not written
+  while (!inside(p1, s.L) && r0 + 1 < r1) p1 = raw_position(s.at, b, --r1 - 1);
+  if (!inside(p0, s.L) || !inside(p1, s.L)) return {0, 0, 0};
+  Hull h;
+  h.near = min(s.w.sinks, n);
+  h.lo = min(max(static_cast<int>(p0) - s.w.left, 0), n);
+  h.hi = max(min(static_cast<int>(p1) + s.w.right + 1, n), h.lo);
+  return h;
 }
+
+// The hull's blocks of 2^shift keys in order: first those of the keys below near, then the others.
+struct Blocks {
+  int near, first, count;
+  EC_DEV int block(int v) const { return v < near ? v : v - near + first; }
+};
+EC_DEV Blocks blocks_of(const Hull& h, int shift) {
+  const int up = (1 << shift) - 1;
+  Blocks k;
+  k.near = (h.near + up) >> shift;
+  k.first = max(h.lo >> shift, k.near);
+  const int end = h.hi > h.lo ? (h.hi + up) >> shift : 0;
+  k.count = k.near + max(0, end - k.first);
+  return k;
+}
+
+// The page of position j of sequence b; a bad number is reported and reads as n_pages, past the
+// tensor map's end, where a load fills in zeros.
+EC_DEV int page_of(const Shape& s, int b, int j) {
+  const int page = __ldg(s.table + b * s.table_stride + (j >> s.page_shift));
+  if (page >= 0 && page < s.n_pages) return page;
+  report_error(s.dev_err, EC_DEVERR_BAD_PAGE);
+  return s.n_pages;
+}
+
+EC_DEV int warp_inclusive(int x) {
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, i);
+    if ((threadIdx.x & 31) >= i) x += y;
+  }
+  return x;
+}
+
+EC_DEV uint4 ld_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
+EC_DEV void st_shared16(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// attention_paged_rows.cu: at most kFewRows packed rows (positions times the heads of a KV head) a sequence.
+constexpr int kFewRows = 32;
+cudaError_t launch_few_rows(const Args& a, int D, int ctas, cudaStream_t s);
+constexpr int kFewSlots = 2;  // partial tiles that a CTA leaves at most, of kFewRows rows
 
 }  // namespace paged
 }  // namespace ec
