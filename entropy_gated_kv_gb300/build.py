@@ -24,7 +24,8 @@ LIB_PATH = PKG / LIB_NAME
 SOURCES = ["entropy_decode.cu", "select_recompute.cu", "kv_scatter.cu", "attention.cu", "attention_dense.cu", "ec_api.cu",
            "entropy_decode_noalloc.cu", "lm_head_entropy.cu", "layer_forward.cu",
            "read_floor.cu", "kv_quant.cu", "attention_cached.cu",
-           "kv_paged.cu", "attention_paged.cu", "attention_paged_rows.cu"]
+           "kv_paged.cu", "attention_paged.cu", "attention_paged_rows.cu",
+           "attention_paged_tiles.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = [
     "-O3",

@@ -18,7 +18,7 @@ namespace {
 constexpr int kMergeWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_constant__ Args a, int slot_rows, int slots) {
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(const __grid_constant__ Args a) {
   constexpr int E = D / 32;
   __shared__ float acc[kMergeWarps][D];
   const Shape& s = a.s;
@@ -27,15 +27,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_co
   pdl_launch_dependents();
   const Record rec = a.records[blockIdx.x];
   if (rec.parts == 0 || x >= rec.rows) return;
-  auto slot = [&](int i) { return i == 0 ? blockIdx.x * slots + 1 : (blockIdx.x + i) * slots; };
   float top = -INFINITY;
+  bool lost = false;
   float2 st[(kMaxCtas + 31) / 32];
 #pragma unroll
   for (int k = 0; k < (kMaxCtas + 31) / 32; ++k) {
     const int i = lane + 32 * k;
-    st[k] = i < rec.parts ? a.part_stat[static_cast<int64_t>(slot(i)) * slot_rows + x] : make_float2(-INFINITY, 0.f);
+    st[k] = i < rec.parts ? a.part_stat[part_slot(blockIdx.x, i, 1, 0) * kFewRows + x] : make_float2(-INFINITY, 0.f);
     top = fmaxf(top, st[k].x);
+    lost = lost || st[k].x != st[k].x;
   }
+  if (__any_sync(0xffffffffu, lost)) return;  // a row that is not written, in every warp
   for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
   float sum = 0.f;
 #pragma unroll
@@ -53,7 +55,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_co
       const int i = 32 * k + i0 + warp;
       const float f = __shfl_sync(0xffffffffu, st[k].x, i0 + warp);
       if (i < rec.parts) {
-        const float* src = a.part_o + (static_cast<int64_t>(slot(i)) * slot_rows + x) * D + lane * E;
+        const float* src = a.part_o + (part_slot(blockIdx.x, i, 1, 0) * kFewRows + x) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
           const float2 y = *reinterpret_cast<const float2*>(src + e);
@@ -67,10 +69,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_co
   __syncthreads();
   if (threadIdx.x >= D / 2) return;
   const int xr = rec.row0 + x, r = s.by_g(xr);
-  if (s.windowed && !inside(raw_position(s.at, rec.b, r), s.L)) {
-    report_error(s.dev_err, EC_DEVERR_BAD_IDX);
-    return;
-  }
   float2 y = make_float2(0.f, 0.f);
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) {
@@ -83,80 +81,70 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_co
   dst[threadIdx.x] = pack_bf16x2(y.x * inv, y.y * inv);
 }
 
-constexpr int kWarps = 4;
+// The same for tiles: a thread takes a row and four columns, four parts in flight. The CTAs share out the pieces of all
+// records, 32 rows by 16 columns each.
+constexpr int kTileMergeThreads = 128;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) paged_rows_kernel(const __grid_constant__ Args args, const uint16_t* kpool, const uint16_t* vpool, int64_t page_stride, int64_t rows) {
-  const Shape& a = args.s;
-  __shared__ __align__(16) float qs[kWarps][D];
+__global__ void __launch_bounds__(kTileMergeThreads) merge_tiles_kernel(const __grid_constant__ Args a, int tiles, int records) {
+  constexpr int kPieces = 4 * (D / 16);
+  __shared__ int list[2 * kMaxCtas];
+  __shared__ int count;
+  const Shape& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  if (row >= rows) return;
-  const int h = static_cast<int>(row % a.Hq), r = static_cast<int>(row / a.Hq % a.rows_max),
-            b = static_cast<int>(row / a.Hq / a.rows_max), kvh = h / a.g;
-  int Rb, n;
-  sizes_of(a, b, lane == 0, Rb, n);
-  if (r >= Rb) return;
-  int near = 0, first = 0, end = n;
-  if (a.windowed) {
-    const int64_t rp = raw_position(a.at, b, r);
-    const int pos = static_cast<int>(rp);
-    if (!inside(rp, a.L)) {
-      if (lane == 0) report_error(a.dev_err, EC_DEVERR_BAD_IDX);
-      return;
+  if (warp == 0) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < 2 * kMaxCtas / 32; ++k) {
+      const int i = 32 * k + lane;
+      const uint32_t have = __ballot_sync(0xffffffffu, i < records && a.records[i].parts > 0);
+      if ((have >> lane) & 1u) list[n + __popc(have & ((1u << lane) - 1u))] = i;
+      n += __popc(have);
     }
-    near = min(a.w.sinks, n);
-    first = max(0, pos - a.w.left);
-    end = min(n, pos + a.w.right + 1);
+    if (lane == 0) count = n;
   }
-  for (int d = lane; d < D; d += 32) qs[warp][d] = bf16lo_to_f32(args.q[row * D + d]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[D / 32] = {};
-  for (int j0 = near > 0 ? 0 : first / 32 * 32; j0 < max(near, end); j0 += 32) {
-    const int j = j0 + lane;
-    const bool see = j < near || (j >= first && j < end);
-    if (!__any_sync(0xffffffffu, see)) continue;
-    int64_t at = 0;
-    int page = 0;
-    float sc = -INFINITY;
-    if (see) {
-      page = __ldg(a.table + b * a.table_stride + (j >> a.page_shift));
-      if (page < 0 || page >= a.n_pages) {
-        report_error(a.dev_err, EC_DEVERR_BAD_PAGE);
-        page = -1;
+  __syncthreads();
+  for (int piece = blockIdx.x; piece < count * kPieces; piece += gridDim.x) {
+    const int which = list[piece / kPieces], sub = piece % kPieces;
+    const Record rec = a.records[which];
+    const int row = (sub & 3) * 32 + lane, quad = (sub >> 2) * 4 + warp;
+    if (row >= rec.rows) continue;
+    const int cta = which / tiles, tile = which - cta * tiles;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool lost = false;
+    for (int i0 = 0; i0 < rec.parts; i0 += 4) {
+      float2 st[4];
+      float4 y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        st[k] = make_float2(-INFINITY, 0.f);
+        y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + k < rec.parts) {
+          const int64_t slot = part_slot(cta, i0 + k, tiles, tile);
+          st[k] = __ldcg(a.part_stat + slot * kTileRows + row);
+          y[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * (D / 4) + quad) * kTileRows + row);
+        }
       }
-      at = page * page_stride + (static_cast<int64_t>(j & ((1 << a.page_shift) - 1)) * a.Hkv + kvh) * D;
-      float dot = 0.f;
-      if (page >= 0)
-        for (int d = 0; d < D; ++d) dot += qs[warp][d] * bf16lo_to_f32(kpool[at + d]);
-      sc = dot * a.scale_log2;
-    }
-    float mx = sc;
-    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-    const float mn = fmaxf(m, mx);
-    if (mn == -INFINITY) continue;
-    const float alpha = exp2f(m - mn), pr = exp2f(sc - mn);
-    m = mn;
-    l *= alpha;
+      const float top = fmaxf(fmaxf(fmaxf(st[0].x, st[1].x), fmaxf(st[2].x, st[3].x)), m);
+      const float f0 = m == -INFINITY ? 1.f : ex2_approx(m - top);
+      m = top;
+      l *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] *= alpha;
-    for (int i = 0; i < 32; ++i) {
-      const float p = __shfl_sync(0xffffffffu, pr, i);
-      const int64_t ai = __shfl_sync(0xffffffffu, at, i);
-      const bool si = __shfl_sync(0xffffffffu, see, i), pi = __shfl_sync(0xffffffffu, page, i) >= 0;
-      if (!si) continue;
-      l += p;
-      if (pi)
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e) o[e] += p * bf16lo_to_f32(vpool[ai + lane + 32 * e]);
+      for (int k = 0; k < 4; ++k) {
+        lost = lost || st[k].x != st[k].x;
+        const float f = st[k].x == -INFINITY ? 1.f : ex2_approx(st[k].x - top);  // no finite score: zeros, or NaN
+        l += f * st[k].y, o.x += f * y[k].x, o.y += f * y[k].y, o.z += f * y[k].z, o.w += f * y[k].w;
+      }
     }
+    if (lost) continue;
+    const int xr = rec.row0 + row, r = s.by_g(xr);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint2* dst = reinterpret_cast<uint2*>(a.out + ((static_cast<int64_t>(rec.b) * s.rows_max + r) * s.Hq + rec.kvh * s.g + (xr - r * s.g)) * D);
+    dst[quad] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   }
-  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e)
-    args.out[row * D + lane + 32 * e] = static_cast<uint16_t>(pack_bf16x2(l == 0.f ? 0.f : o[e] * inv, 0.f));
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -190,19 +178,36 @@ bool encode_pool(EncodeTiledFn enc, CUtensorMap* m, const void* base, const ec_p
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries as [sequence][row][KV head][head of it][D]: a box is nr rows of the g heads of a KV head, 64 features.
+bool encode_queries(EncodeTiledFn enc, CUtensorMap* m, const void* q, const ec_params& p, int rows_max, int nr) {
+  const cuuint64_t D = p.D, g = p.Hq / p.Hkv, H = p.Hkv, n = rows_max;
+  const cuuint64_t dims[5] = {D, g, H, n, static_cast<cuuint64_t>(p.B)};
+  const cuuint64_t strides[4] = {D * 2, g * D * 2, H * g * D * 2, n * H * g * D * 2};
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(g), 1, static_cast<cuuint32_t>(nr), 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool few_rows(const ec_params& p, int32_t rows_max) { return static_cast<int64_t>(rows_max) * (p.Hq / p.Hkv) <= kFewRows; }
+
+// Positions of a tile.
+int tile_positions(const ec_params& p, int32_t rows_max) { return std::min(kTileRows / (p.Hq / p.Hkv), rows_max); }
+
 struct WsLayout {
   size_t stat, records, total;
 };
 WsLayout ws_layout(const ec_params& p, int32_t rows_max) {
-  const size_t rows = static_cast<size_t>(kMaxCtas) * kFewSlots * kFewRows;
+  const int nr = tile_positions(p, rows_max);
+  const bool few = few_rows(p, rows_max);
+  const size_t tiles = few || rows_max <= nr ? 1 : 2;
+  const size_t rows = kMaxCtas * 2 * tiles * (few ? kFewRows : kTileRows);
   WsLayout w{};
   w.stat = rows * p.D * sizeof(float);
   w.records = w.stat + rows * sizeof(float2);
-  w.total = w.records + kMaxCtas * sizeof(Record);
+  w.total = w.records + kMaxCtas * tiles * sizeof(Record);
   return w;
 }
-
-bool few_rows(const ec_params& p, int32_t rows_max) { return static_cast<int64_t>(rows_max) * (p.Hq / p.Hkv) <= kFewRows; }
 
 }  // namespace
 
@@ -236,20 +241,25 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
   a.part_stat = reinterpret_cast<float2*>(w + lay.stat);
   a.records = reinterpret_cast<Record*>(w + lay.records);
   const int ctas = std::min(sms, kMaxCtas);
-  if (few_rows(p, rows_max)) {
-    if (!encode_pool(enc, &a.tk, c.k, p, c, 16, p.D / 64) || !encode_pool(enc, &a.tv, c.v, p, c, 16, p.D / 64)) {
-      *status = EC_ERR_INVALID_ARG;
-      return cudaErrorInvalidValue;
-    }
+  const bool few = few_rows(p, rows_max);
+  // a chunk of 16 keys, or a half block of 64 as far as a page holds it
+  const int box = few ? 16 : std::min(64, c.page_size), atoms = few || box == 64 ? p.D / 64 : 1;
+  const int nr = tile_positions(p, rows_max);
+  if (!encode_pool(enc, &a.tk, c.k, p, c, box, atoms) || !encode_pool(enc, &a.tv, c.v, p, c, box, atoms) ||
+      (!few && !encode_queries(enc, &a.tq, q, p, rows_max, nr))) {
+    *status = EC_ERR_INVALID_ARG;
+    return cudaErrorInvalidValue;
+  }
+  if (few) {
     e = launch_few_rows(a, p.D, ctas, s);
     if (e == cudaSuccess)
-      e = launch_pdl(p.D == 64 ? merge_kernel<64> : merge_kernel<128>, dim3(ctas, rows_max * sh.g), dim3(32 * kMergeWarps), 0, s, a,
-                     kFewRows, kFewSlots);
+      e = launch_pdl(p.D == 64 ? merge_rows_kernel<64> : merge_rows_kernel<128>, dim3(ctas, rows_max * sh.g), dim3(32 * kMergeWarps), 0, s, a);
   } else {
-    const int64_t rows = static_cast<int64_t>(p.B) * rows_max * p.Hq;
-    const unsigned grid = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
-    e = launch_pdl(p.D == 64 ? paged_rows_kernel<64> : paged_rows_kernel<128>, dim3(grid), dim3(32 * kWarps), 0, s, a,
-                   static_cast<const uint16_t*>(c.k), static_cast<const uint16_t*>(c.v), c.page_stride, rows);
+    const int tiles = rows_max <= nr ? 1 : 2;
+    e = launch_tiles(a, p.D, nr, ctas, s);
+    if (e == cudaSuccess)
+      e = launch_pdl(p.D == 64 ? merge_tiles_kernel<64> : merge_tiles_kernel<128>, dim3(2 * ctas), dim3(kTileMergeThreads), 0, s, a, tiles,
+                     ctas * tiles);
   }
   if (e == cudaSuccess) *status = EC_OK;
   return e;

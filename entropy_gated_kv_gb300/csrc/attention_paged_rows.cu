@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
     __syncthreads();
     const bool cut_here = u1 < cs.units;
     const bool part = at.u > 0 || cut_here;
-    const int slot = blockIdx.x * kFewSlots + (at.u == 0 ? 1 : 0);
+    const int slot = blockIdx.x * 2 + (at.u == 0 ? 1 : 0);
 #pragma unroll 1
     for (int i = threadIdx.x; i < packed * (D / 8); i += kThreads) {
       const int x = i / (D / 8), c = i % (D / 8) * 8;
@@ -387,6 +387,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
       for (int w = 0; w < kWarps; ++w) {
         const float2 st = stat[w * LY::kRows + x];
         sum += st.x == -INFINITY ? 0.f * st.y : ex2_approx(st.x - top) * st.y;  // a NaN sum stays one
+      }
+      const int r = s.by_g(x);
+      bool good = true;  // right, or not written: the row's keys are between those of the first and the last row
+      if (s.windowed) {
+        const int64_t pos = raw_position(s.at, at.b, r);
+        const int p = inside(pos, s.L) ? static_cast<int>(pos) : 0;
+        good = inside(pos, s.L) && min(max(p - s.w.left, 0), cs.n) >= cs.h.lo && min(p + s.w.right + 1, cs.n) <= cs.h.hi;
+        if (!good && c == 0) report_error(s.dev_err, EC_DEVERR_BAD_IDX);
       }
       float4 y[2] = {};
 #pragma unroll
@@ -399,13 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
       if (part) {
         float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * kFewRows + x) * D + c);
         dst[0] = y[0], dst[1] = y[1];
-        if (c == 0) a.part_stat[slot * kFewRows + x] = make_float2(top, sum);
-      } else {
-        const int r = s.by_g(x);
-        if (s.windowed && !inside(raw_position(s.at, at.b, r), s.L)) {
-          report_error(s.dev_err, EC_DEVERR_BAD_IDX);
-          continue;
-        }
+        if (c == 0) a.part_stat[slot * kFewRows + x] = make_float2(good ? top : kNotWritten(), sum);
+      } else if (good) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         uint4 z;
         z.x = pack_bf16x2(y[0].x * inv, y[0].y * inv);

@@ -1,0 +1,721 @@
+// attention_paged_tiles.cu — attention over a paged K/V cache for more rows than a few: tiles of 128 packed query rows (a
+// sequence's positions times the g query heads of a KV head) on the 5th-generation tensor cores.
+//
+//   out[x] = sum_j p_xj v_j / sum_j p_xj, p_xj = 2^(s_xj - m_x), s_xj = scale log2(e) <q_x, k_j>, m_x a running maximum
+// Two streams run through a CTA, each with its issuer, its softmax warps, two score buffers of 64 keys and an O
+// accumulator in tensor memory: while one half's softmax runs, the tensor cores do the other half's P V and the next
+// scores. Two forms:
+//   - pair (a sequence may have more rows than a tile): a stream a tile, two tiles side by side on the same K/V, so that
+//     a byte brought to shared memory feeds 256 rows;
+//   - split (every sequence has one tile): the streams take the even and the odd key blocks of the tile and are
+//     joined at the item's end.
+// Blocks are 128 keys, brought in by TMA in halves of 64: one box of 64 rows, or of a smaller page, from the page
+// that the table names. The blocks of all items (sequence, group of tiles, KV head) stand in one line of
+// which the CTAs, one an SM, take equal shares; an item cut between CTAs leaves fp32 partial rows, which a second
+// launch joins in a fixed order. A window leaves only the blocks that a group's rows see between them in the line.
+// Roles (12 warps):
+//   warp 0      plan, items, TMA producer        warps 4..7    softmax and epilogue of stream 0
+//   warps 1, 2  issuers of the two streams       warps 8..11   of stream 1
+//   warp 3      zeroes V rows that no row of the group may see (a page's rest may hold NaN, and 0 x NaN is NaN)
+// A waiter on an mbarrier sees a phase's parity only, so whoever waits on a barrier follows every one of its
+// phases or has seen by another way that the one before is complete.
+#include <algorithm>
+
+#include "paged_common.cuh"
+
+namespace ec {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kBlockM = 128;
+constexpr int kBlockN = 128;
+constexpr int kHalf = 64;  // keys of a score buffer, of a unit in shared memory
+constexpr int kItems = 4;  // items handed out and not yet finished
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 256;  // stream t: scores of half h at columns [128 t + 64 h, + 64), O at [256 + 128 t, + D)
+constexpr uint32_t kDescHi = sdesc_hi(1024);
+constexpr int kAtomBytes = 128 * 128;   // 128 rows x 128 bytes (64 bf16): the query tile
+constexpr int kHalfAtom = kHalf * 128;  // 64 rows x 128 bytes: K and V
+__host__ __device__ constexpr uint32_t step_k(int kk, int atom) { return (kk >> 2) * (atom / 16) + (kk & 3) * 2; }
+constexpr uint32_t kStepPV = 16 * 128 / 16;
+
+// Work of a CTA on one (sequence, group of tiles, KV head): blocks v0 .. v0 + nblk - 1 of the group's; nblk 0: the end.
+// part -1: the whole item; else the CTA's partial rows stand in its slots of an item that goes on here (0) or
+// begins here (1).
+struct __align__(16) Item {
+  int b, kvh, nblk, v0, near_blocks, first, near, lo, hi, n, r0, rows0, rows1, part, pad[2];
+};
+static_assert(sizeof(Item) == 64, "four 16-byte pieces");
+
+// A block's place in shared memory: in the pair form blocks alternate between the two, in the split form each stream has
+// its own, as a waiter that does not follow every use of a place could take one use for another.
+constexpr int NB = 2;
+
+struct Bars {
+  uint64_t q_full, q_empty;
+  uint64_t unit_full[NB * 4], unit_empty[NB * 4];  // a block's K halves, then its V halves
+  uint64_t v_ok[NB * 2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][half]
+  uint64_t join, o_free;
+  uint64_t item_full[kItems], item_empty[kItems];
+  uint32_t tmem_base;
+  int abort;
+  int scan[kThreads / 32];
+  int begin[4], share;  // b, group, KV head, block of the CTA's first item
+};
+
+template <int D, bool PAIR>
+struct Layout {
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kTileBytes = kAtoms * kAtomBytes;
+  static constexpr int kUnit = kAtoms * kHalfAtom;
+  static constexpr int kUnitOff = (PAIR ? 2 : 1) * kTileBytes;
+  static constexpr int kStatOff = kUnitOff + NB * 4 * kUnit;
+  static constexpr int kItemOff = kStatOff + 2 * kBlockM * 8;
+  static constexpr int kBarOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
+  static constexpr int kBytes = kBarOff + static_cast<int>(sizeof(Bars));
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+EC_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// tcgen05.wait::ld that names the loaded registers, so that no use of them moves before it.
+#define EC_TMEM_WAIT32(r)                                                                                    \
+  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                              \
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),         \
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),     \
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),  \
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),  \
+                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory")
+
+#define EC_TMEM_ST16(taddr, r)                                                                              \
+  asm volatile(                                                                                             \
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" \
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), \
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])          \
+      : "memory")
+
+EC_DEV uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+EC_DEV void unpack_f32x2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+EC_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+EC_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+EC_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// A group of tiles of a sequence: its positions (at most `step`), what they see, its blocks.
+struct Group {
+  int rows, n, blocks;
+  Hull h;
+  Blocks k;
+};
+EC_DEV Group load_group(const Shape& s, int b, int grp, int step, bool tell) {
+  Group q;
+  sizes_of(s, b, tell, q.rows, q.n);
+  const int r0 = grp * step;
+  q.rows = min(step, q.rows - r0);
+  q.h = q.rows > 0 ? hull_of(s, b, r0, r0 + q.rows, q.n) : Hull{0, 0, 0};
+  q.k = blocks_of(q.h, 7);
+  q.blocks = q.rows > 0 ? max(1, q.k.count) : 0;  // rows without a key are written too
+  return q;
+}
+
+// Keys j0 .. j0 + count - 1 are all of the hull, or some of them.
+EC_DEV bool all_in(int near, int lo, int hi, int j0, int count) { return j0 + count <= near || (j0 >= lo && j0 + count <= hi); }
+EC_DEV bool some_in(int near, int lo, int hi, int j0, int count) { return j0 < near || (j0 < hi && j0 + count > lo); }
+
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Args a, int nr, int groups) {
+  using LY = Layout<D, PAIR>;
+  constexpr int kTiles = PAIR ? 2 : 1;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* bars = reinterpret_cast<Bars*>(smem + LY::kBarOff);
+  const Shape& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int step = nr * kTiles;  // positions of a group
+
+  if (warp == 0) {  // the lanes share the barriers
+    if (lane < NB * 4) {
+      mbar_init(&bars->unit_full[lane], 1);
+      // released by the issuers that read it, a V half by warp 3 too
+      mbar_init(&bars->unit_empty[lane], kTiles + ((lane & 3) >= 2 ? 1 : 0));
+    }
+    if (lane < NB * 2) mbar_init(&bars->v_ok[lane], 1);
+    if (lane < 4) {
+      mbar_init(&bars->s_full[lane >> 1][lane & 1], 1);
+      mbar_init(&bars->p_full[lane >> 1][lane & 1], 4);
+      mbar_init(&bars->pv_done[lane >> 1][lane & 1], 1);
+    }
+    if (lane < kItems) {
+      mbar_init(&bars->item_full[lane], 1);
+      mbar_init(&bars->item_empty[lane], 11);  // all that read the items
+    }
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 2);
+    mbar_init(&bars->join, 8);
+    mbar_init(&bars->o_free, 8);
+    bars->abort = (smem_u32(smem) & 1023u) != 0u;  // the swizzled tiles need the alignment that dynamic shared memory has here
+    if (bars->abort) report_error(s.dev_err, EC_DEVERR_TIMEOUT);
+    bars->begin[3] = -1;
+    fence_mbar_init();
+    prefetch_tmap(&a.tq);
+    prefetch_tmap(&a.tk);
+    prefetch_tmap(&a.tv);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();  // everything above overlaps the previous kernel
+  pdl_launch_dependents();
+
+  // The line: each thread adds up the blocks of its (sequence, group) pairs, the CTA their sum, and the thread whose pairs
+  // hold the first block of this CTA's share finds it.
+  const int pairs = s.B * groups, per = (pairs + kThreads - 1) / kThreads, p0 = threadIdx.x * per;
+  int mine = 0;
+#pragma unroll 2
+  for (int i = p0; i < min(p0 + per, pairs); ++i) {
+    const int b = i / groups;
+    mine += load_group(s, b, i - b * groups, step, blockIdx.x == 0).blocks * s.Hkv;
+  }
+  int incl = warp_inclusive(mine);
+  if (lane == 31) bars->scan[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) incl += bars->scan[w];
+    total += bars->scan[w];
+  }
+  const int share = (total + gridDim.x - 1) / gridDim.x;
+  const int begin = blockIdx.x * share;
+  if (begin < total && begin >= incl - mine && begin < incl) {
+    int off = begin - (incl - mine);
+    for (int i = p0;; ++i) {
+      const int b = i / groups, blocks = load_group(s, b, i - b * groups, step, false).blocks;
+      if (off < blocks * s.Hkv) {
+        bars->begin[0] = b, bars->begin[1] = i - b * groups, bars->begin[2] = off / blocks, bars->begin[3] = off % blocks;
+        break;
+      }
+      off -= blocks * s.Hkv;
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort_flag = &bars->abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait_bounded(bar, parity, abort_flag, s.dev_err, kWaitLimitNs);
+  };
+  auto wait_w = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+  // The n-th item of this CTA, once the producer has made it; nblk = 0 at the end and after a wait that gave up.
+  Item* const items_s = reinterpret_cast<Item*>(smem + LY::kItemOff);
+  auto next_item = [&](int n) {
+    Item it;
+    const bool ok = wait_w(&bars->item_full[n % kItems], (n / kItems) & 1);
+    const uint32_t src = smem_u32(items_s + n % kItems);
+    uint4* dst = reinterpret_cast<uint4*>(&it);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = ld_shared16(src + 16 * i);
+    if (!ok) it.nblk = 0;
+    return it;
+  };
+  // Place and use of the blocks of an item in order, for the roles that see all of them.
+  struct Places {
+    uint32_t blocks = 0, used[2] = {0, 0};
+    EC_DEV void at(int i, uint32_t& place, uint32_t& use) {
+      if constexpr (PAIR) {
+        place = blocks & 1u, use = blocks >> 1;
+        ++blocks;
+      } else {
+        place = i & 1u, use = used[place];
+        used[0] += place ^ 1u, used[1] += place;
+      }
+    }
+  };
+  auto block_of = [](const Item& it, int i) {
+    const int v = it.v0 + i;
+    return v < it.near_blocks ? v : v - it.near_blocks + it.first;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ items and loads
+    const int box = min(kHalf, 1 << s.page_shift);       // rows of a TMA box
+    const int boxes = kHalf / box;                       // boxes of a half's rows: 1, 2 or 4
+    const int atoms = box < kHalf ? LY::kAtoms : 1;      // boxes beside each other
+    if (lane < kTiles) a.records[blockIdx.x * kTiles + lane].parts = 0;
+    int left = bars->begin[3] >= 0 && !*abort_flag ? min(share, total - begin) : 0;
+    int b = bars->begin[0], grp = bars->begin[1], kvh = bars->begin[2], u = bars->begin[3];
+    Group g{};
+    if (left > 0) g = load_group(s, b, grp, step, false);
+    Places places;
+    bool ok = true;
+#pragma unroll 1
+    for (int count = 0;; ++count) {
+      Item it;
+      it.nblk = ok && left > 0 ? min(g.blocks - u, left) : 0;
+      if (it.nblk > 0) {
+        it.b = b, it.kvh = kvh, it.v0 = u;
+        it.near_blocks = g.k.near, it.first = g.k.first;
+        it.near = g.h.near, it.lo = g.h.lo, it.hi = g.h.hi, it.n = g.n;
+        it.r0 = grp * step, it.rows0 = min(nr, g.rows), it.rows1 = g.rows - it.rows0;
+        it.part = it.nblk == g.blocks ? -1 : u == 0 ? 1 : 0;
+      }
+      ok = wait_w(&bars->item_empty[count % kItems], ((count / kItems) & 1) ^ 1);
+      if (!ok) it.nblk = 0;
+      if (lane == 0) {
+        items_s[count % kItems] = it;
+        mbar_arrive(&bars->item_full[count % kItems]);
+      }
+      if (it.nblk == 0) break;
+      if (it.part == 1 && lane < kTiles) {  // the item begins here and goes on in the next CTAs
+        const int rest = g.blocks - it.nblk;
+        Record r{};
+        r.rows = (lane == 0 ? it.rows0 : it.rows1) * s.g;
+        r.parts = r.rows > 0 ? 1 + (rest + share - 1) / share : 0;
+        r.b = b, r.kvh = kvh, r.row0 = (it.r0 + lane * nr) * s.g;
+        a.records[blockIdx.x * kTiles + lane] = r;
+      }
+      // the queries, when the products of the item before have read theirs
+      if (count > 0) ok = wait_w(&bars->q_empty, (count - 1) & 1);
+      if (ok && lane == 0) {
+        const int tiles = PAIR && it.rows1 > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(&bars->q_full, tiles * LY::kAtoms * nr * s.g * 128);
+        for (int t = 0; t < tiles; ++t)
+          for (int at = 0; at < LY::kAtoms; ++at)
+            tma_load_5d(smem + t * LY::kTileBytes + at * kAtomBytes, &a.tq, &bars->q_full, at * 64, 0, kvh, it.r0 + t * nr, b);
+      }
+      // lane i: the page of the i-th box of a block's rows, one block ahead
+      auto look = [&](int i) {
+        const int j = block_of(it, i) * kBlockN + lane * box;
+        return lane < 2 * boxes && some_in(it.near, it.lo, it.hi, j, box) ? page_of(s, b, j) : -1;
+      };
+      int next = look(0);
+#pragma unroll 1
+      for (int i = 0; ok && i < it.nblk; ++i) {
+        const int page = next, j0 = block_of(it, i) * kBlockN;
+        if (i + 1 < it.nblk) next = look(i + 1);
+        const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+        uint32_t place, use;
+        places.at(i, place, use);
+#pragma unroll 1
+        for (int n = 0; ok && n < 4; ++n) {
+          const int h = n & 1, unit = place * 4 + n;
+          ok = wait_w(&bars->unit_empty[unit], (use & 1u) ^ 1u);
+          if (!ok) break;
+          const uint32_t mask = (have >> (h * boxes)) & ((1u << boxes) - 1u);
+          if (lane == 0) mbar_arrive_expect_tx(&bars->unit_full[unit], __popc(mask) * box * D * 2);
+          __syncwarp();
+          const int r = lane % boxes, at = lane / boxes;
+          const int pg = __shfl_sync(0xffffffffu, page, h * boxes + r);
+          if (at < atoms && ((mask >> r) & 1u))
+            tma_load_5d(smem + LY::kUnitOff + unit * LY::kUnit + at * kHalfAtom + r * box * 128, n < 2 ? &a.tk : &a.tv,
+                        &bars->unit_full[unit], 0, (j0 + h * kHalf + r * box) & ((1 << s.page_shift) - 1), at, kvh, pg);
+        }
+      }
+      left -= it.nblk;
+      u = 0;
+      if (left > 0 && ++kvh == s.Hkv) {
+        kvh = 0;
+        do {
+          if (++grp == groups) grp = 0, ++b;
+          g = load_group(s, b, grp, step, false);
+        } while (g.blocks == 0);
+      }
+    }
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------------ issuer of one stream
+    // The whole warp waits, one thread issues: the products' descriptors live in uniform registers.
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kHalf, 0);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
+    const uint32_t st = __shfl_sync(0xffffffffu, warp - 1, 0);
+    const uint32_t q_lo = sdesc_lo(smem_u32(smem) + (PAIR ? st * LY::kTileBytes : 0), 16), unit0 = smem_u32(smem + LY::kUnitOff);
+    const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t s_col = tmem_u + st * 128, o_col = tmem_u + kTmemO + st * 128;
+    constexpr int kBy = PAIR ? 1 : 2;  // a stream takes every kBy-th block
+    uint32_t used = 0;    // blocks of this stream whose P V is under way or done
+    uint32_t blocks = 0;  // all blocks, in the pair form
+    bool ok = true;
+    for (int items = 0; ok; ++items) {
+      const Item it = next_item(items);
+      if (it.nblk == 0) break;
+      const bool live = PAIR ? (st == 0 || it.rows1 > 0) : static_cast<int>(st) < it.nblk;
+      const int i0 = PAIR ? 0 : st;
+      uint32_t kb = blocks;  // the block whose scores are issued next, and the one whose P V is, in the pair form
+      uint32_t vb = blocks;
+      auto issue_qk = [&](int i, uint32_t n, int h) {
+        const uint32_t unit = (PAIR ? kb & 1u : st) * 4 + h, use = PAIR ? kb >> 1 : n;
+        // K is here, and the buffer's last P has been read
+        if (!wait_w(&bars->unit_full[unit], use & 1u) || (n != 0 && !wait_w(&bars->pv_done[st][h], (n - 1) & 1u))) return false;
+        tc_fence_after();
+        const uint32_t k_lo = sdesc_lo(unit0 + unit * LY::kUnit, 16);
+        const uint32_t col = s_col + h * kHalf;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(col, q_lo + step_k(kk, kAtomBytes), k_lo + step_k(kk, kHalfAtom), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+          umma_commit(&bars->s_full[st][h]);
+          umma_commit(&bars->unit_empty[unit]);
+          if (h == 1 && i + kBy >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last scores of the item
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_pv = [&](int i, uint32_t n, int h) {
+        const uint32_t place = PAIR ? vb & 1u : st, use = PAIR ? vb >> 1 : n, unit = place * 4 + 2 + h;
+        if (!wait_w(&bars->unit_full[unit], use & 1u)) return false;
+        const int j0 = block_of(it, i) * kBlockN + h * kHalf;
+        if (!all_in(it.near, it.lo, it.hi, j0, kHalf) && !wait_w(&bars->v_ok[place * 2 + h], use & 1u)) return false;
+        if (!wait_w(&bars->p_full[st][h], n & 1u)) return false;
+        // the item's first product starts O anew: the warps of both streams have read it
+        if (!PAIR && items > 0 && i == i0 && h == 0 && !wait_w(&bars->o_free, (items - 1) & 1)) return false;
+        tc_fence_after();
+        const uint32_t v_lo = sdesc_lo(unit0 + unit * LY::kUnit, kHalfAtom);
+        const uint32_t col = s_col + h * kHalf;
+        const uint32_t acc0 = h > 0 ? 1u : __shfl_sync(0xffffffffu, i > i0 ? 1u : 0u, 0);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kHalf / 16; ++kk)
+            umma_ts(o_col, col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
+          umma_commit(&bars->pv_done[st][h]);
+          umma_commit(&bars->unit_empty[unit]);
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = wait_w(&bars->q_full, items & 1);
+      if (live) {
+        ok = ok && issue_qk(i0, used, 0) && issue_qk(i0, used, 1);
+        ++kb;
+#pragma unroll 1
+        for (int i = i0; ok && i < it.nblk; i += kBy, ++used) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && issue_pv(i, used, h);
+            if (i + kBy < it.nblk) ok = ok && issue_qk(i + kBy, used + 1, h);
+          }
+          ++kb;
+          ++vb;
+        }
+      } else {
+        // Nothing of this item falls to the stream. (It leaves o_free alone: its next wait there comes after a P of its own,
+        // and so after the join of this item, and that after the phase before.)
+        if (lane == 0) mbar_arrive(&bars->q_empty);
+        if constexpr (PAIR) {
+#pragma unroll 1
+          for (int i = 0; ok && i < it.nblk; ++i) {
+#pragma unroll 1
+            for (int n = 0; ok && n < 4; ++n) {
+              ok = wait_w(&bars->unit_full[(kb & 1u) * 4 + n], (kb >> 1) & 1u);
+              if (ok && lane == 0) mbar_arrive(&bars->unit_empty[(kb & 1u) * 4 + n]);
+            }
+            ++kb;
+          }
+        }
+      }
+      blocks += it.nblk;
+      if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------ rows of V outside the hull
+    Places places;
+    bool ok = true;
+    for (int items = 0; ok; ++items) {
+      const Item it = next_item(items);
+      if (it.nblk == 0) break;
+#pragma unroll 1
+      for (int i = 0; ok && i < it.nblk; ++i) {
+        const int j0 = block_of(it, i) * kBlockN;
+        uint32_t place, use;
+        places.at(i, place, use);
+#pragma unroll 1
+        for (int h = 0; ok && h < 2; ++h) {
+          const int unit = place * 4 + 2 + h, j = j0 + h * kHalf;
+          ok = wait_w(&bars->unit_full[unit], use & 1u);
+          if (!ok) break;
+          if (!all_in(it.near, it.lo, it.hi, j, kHalf)) {
+            const uint32_t base = smem_u32(smem + LY::kUnitOff) + unit * LY::kUnit;
+#pragma unroll 1
+            for (int r = lane >> 3; r < kHalf; r += 4)  // eight lanes a row
+              if (!some_in(it.near, it.lo, it.hi, j + r, 1))
+#pragma unroll
+                for (int at = 0; at < LY::kAtoms; ++at) st_shared16(base + at * kHalfAtom + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            mbar_arrive(&bars->v_ok[place * 2 + h]);
+            mbar_arrive(&bars->unit_empty[unit]);
+          }
+        }
+      }
+      if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax and epilogue of one stream
+    const int st = (warp - 4) >> 2;
+    const int row = 32 * (warp & 3) + lane;  // TMEM lane = packed query row
+    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
+    constexpr int kBy = PAIR ? 1 : 2;
+    const int i0 = PAIR ? 0 : st;
+    uint32_t used = 0;  // blocks of this stream
+    bool ok = true;
+#pragma unroll 1
+    for (int items = 0; ok; ++items) {
+      const Item it = next_item(items);
+      if (it.nblk == 0) break;
+      const int rows = (PAIR && st ? it.rows1 : it.rows0) * s.g;  // packed rows of the tile
+      const int r0 = it.r0 + (PAIR && st ? nr : 0);
+      const bool live = 32 * (warp & 3) < rows;  // else the warp's rows are all padding
+      const bool valid = row < rows;
+      const int rl = s.by_g(row), r = r0 + rl;
+      int r_lo = it.lo, r_hi = it.hi;  // what this row sees, beside the keys below near
+      bool good = valid;
+      if (s.windowed && valid) {
+        const int64_t pos = raw_position(s.at, it.b, r);
+        const int p = inside(pos, s.L) ? static_cast<int>(pos) : 0;
+        r_lo = max(p - s.w.left, 0);
+        r_hi = min(p + s.w.right + 1, it.n);
+        // right, or not written: the row's keys are between those of the group's first and last row
+        good = inside(pos, s.L) && min(r_lo, it.n) >= it.lo && r_hi <= it.hi;
+        if (!good) {
+          report_error(s.dev_err, EC_DEVERR_BAD_IDX);
+          r_lo = r_hi = 0;
+        }
+      }
+      float m_used = -INFINITY, l_sum = 0.f;
+      if (!PAIR || rows > 0) {
+#pragma unroll 1
+        for (int i = i0; ok && i < it.nblk; i += kBy, ++used) {
+          int j = block_of(it, i) * kBlockN;
+          uint32_t s_addr = tmem + lane_off + st * 128;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h, s_addr += kHalf, j += kHalf) {
+            ok = wait_w(&bars->s_full[st][h], used & 1u);
+            if (!ok) break;
+            if (live) {
+              tc_fence_after();
+              uint32_t b0[32], b1[32];
+              EC_TMEM_LD32(s_addr, b0);
+              EC_TMEM_LD32(s_addr + 32, b1);
+              EC_TMEM_WAIT32(b0);
+              EC_TMEM_WAIT32(b1);
+              if (!__all_sync(0xffffffffu, !valid || all_in(it.near, r_lo, r_hi, j, kHalf))) {  // keys that the row does not see
+                auto below = [](int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; };
+                const uint64_t see = below(it.near - j) | (below(r_hi - j) & ~below(r_lo - j));
+                const uint32_t s0 = static_cast<uint32_t>(see), s1 = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  if (!((s0 >> e) & 1u)) b0[e] = __float_as_uint(-INFINITY);
+                  if (!((s1 >> e) & 1u)) b1[e] = __float_as_uint(-INFINITY);
+                }
+              }
+              // maximum (scale > 0 commutes with it), then p = 2^(s scale log2(e) - m)
+              float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                m4[e & 2] = max3(m4[e & 2], __uint_as_float(b0[e]), __uint_as_float(b0[e + 1]));
+                m4[(e & 2) + 1] = max3(m4[(e & 2) + 1], __uint_as_float(b1[e]), __uint_as_float(b1[e + 1]));
+              }
+              const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * s.scale_log2;
+              bool rescale = false;
+              float alpha = 1.f;
+              if (i == i0 && h == 0) {
+                m_used = mx;
+              } else if (mx > m_used + kRescaleLog2) {
+                alpha = ex2_approx(m_used - mx);
+                m_used = mx;
+                l_sum *= alpha;
+                rescale = true;
+              }
+              // without a finite score so far, nothing is subtracted and p = 0
+              const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+              const uint64_t scale2 = pack_f32x2(s.scale_log2, s.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
+              uint64_t sum2[2] = {0, 0};
+              // P over the buffer's first 32 columns, in bf16 as the products take it: each weight is off by 2^-8 of
+              // itself at most. Their sum is that of the fp32 weights.
+              auto weights = [&](const uint32_t (&x)[32], int c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  float p0, p1;
+                  unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
+                  p0 = ex2_approx(p0);
+                  p1 = ex2_approx(p1);
+                  sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
+                  pk[e >> 1] = pack_bf16x2(p0, p1);
+                }
+                EC_TMEM_ST16(s_addr + c, pk);
+              };
+              weights(b0, 0);
+              weights(b1, 16);
+              float sum_lo, sum_hi;
+              unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
+              l_sum += sum_lo + sum_hi;
+              if (__any_sync(0xffffffffu, rescale)) {
+                // the half before this one may still be under way into O
+                ok = wait_w(&bars->pv_done[st][h ^ 1], (h ? used : used - 1) & 1u);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  uint32_t o[32];
+                  EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+                  EC_TMEM_WAIT32(o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                  EC_TMEM_ST32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+                }
+              }
+              tmem_wait_st();
+              tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_full[st][h]);
+          }
+        }
+        if (ok && (PAIR || st < it.nblk)) ok = wait_w(&bars->pv_done[st][1], (used - 1) & 1u);
+      }
+      const bool complete = it.part < 0;
+      // slots of a CTA: [item goes on here, item begins here][tile]
+      const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (it.part > 0 ? 1 : 0)) * kTiles + (PAIR ? st : 0);
+      uint16_t* const orow = a.out + ((static_cast<int64_t>(it.b) * s.rows_max + r) * s.Hq + it.kvh * s.g + (row - rl * s.g)) * D;
+      // a slot is [D / 4][128] quads of columns, neighbouring rows side by side
+      float4* const prow = reinterpret_cast<float4*>(a.part_o) + slot * (kBlockM * (D / 4)) + row;
+      auto store = [&](const float (&y)[32], int col) {
+        if (complete && good) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(orow + col + 8 * e) =
+                make_uint4(pack_bf16x2(y[8 * e], y[8 * e + 1]), pack_bf16x2(y[8 * e + 2], y[8 * e + 3]),
+                           pack_bf16x2(y[8 * e + 4], y[8 * e + 5]), pack_bf16x2(y[8 * e + 6], y[8 * e + 7]));
+        } else if (!complete && valid) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            prow[(col / 4 + e) * kBlockM] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        }
+      };
+      if constexpr (PAIR) {
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+          const float f = complete ? (l_sum == 0.f ? 0.f : 1.f / l_sum) : 1.f;
+          if (!complete && valid) a.part_stat[slot * kBlockM + row] = make_float2(good ? m_used : kNotWritten(), l_sum);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+            EC_TMEM_WAIT32(o);
+            float y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = l_sum == 0.f ? 0.f : __uint_as_float(o[e]) * f;
+            store(y, c * 32);
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+      } else {
+        // join the two streams: each warpgroup takes half of the columns of both accumulators. Every warp is done with the
+        // item before, so its statistics may be overwritten
+        if (ok && items > 0) ok = wait_w(&bars->o_free, (items - 1) & 1);
+        stat[st * kBlockM + row] = make_float2(m_used, l_sum);
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&bars->join);
+        ok = ok && wait_w(&bars->join, items & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+          const float2 s0 = stat[row], s1 = stat[kBlockM + row];
+          const float M = fmaxf(s0.x, s1.x);
+          // a stream without weight (no block, or no finite score) contributes nothing
+          const bool has0 = s0.y != 0.f, has1 = it.nblk > 1 && s1.y != 0.f;
+          const float w0 = has0 && s0.x != -INFINITY ? ex2_approx(s0.x - M) : has0 ? 1.f : 0.f;
+          const float w1 = has1 && s1.x != -INFINITY ? ex2_approx(s1.x - M) : has1 ? 1.f : 0.f;
+          const float L = (has0 ? w0 * s0.y : 0.f) + (has1 ? w1 * s1.y : 0.f);
+          const float norm = complete ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+          const float f0 = w0 * norm, f1 = w1 * norm;
+          if (!complete && st == 0 && valid) a.part_stat[slot * kBlockM + row] = make_float2(good ? M : kNotWritten(), L);
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o0[32], o1[32];
+            EC_TMEM_LD32(tmem + lane_off + kTmemO + st * (D / 2) + c * 32, o0);
+            EC_TMEM_LD32(tmem + lane_off + kTmemO + 128 + st * (D / 2) + c * 32, o1);
+            EC_TMEM_WAIT32(o0);
+            EC_TMEM_WAIT32(o1);
+            float y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              y[e] = has0 ? __uint_as_float(o0[e]) * f0 : 0.f;
+              if (has1) y[e] = fmaf(__uint_as_float(o1[e]), f1, y[e]);
+            }
+            store(y, st * (D / 2) + c * 32);
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->o_free);
+      }
+      if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
+    }
+  }
+
+  // ---------------------------------------------------------------------- teardown
+  if (*abort_flag) {  // copies and products may still be under way: they take microseconds
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 200000u) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool PAIR>
+cudaError_t launch(const Args& a, int nr, int groups, int ctas, cudaStream_t s) {
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(tiles_kernel<D, PAIR>), Layout<D, PAIR>::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tiles_kernel<D, PAIR>, dim3(ctas), dim3(kThreads), Layout<D, PAIR>::kBytes, s, a, nr, groups);
+}
+
+}  // namespace
+
+cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, cudaStream_t s) {
+  const int tiles = (a.s.rows_max + nr - 1) / nr;
+  if (tiles == 1) return D == 64 ? launch<64, false>(a, nr, 1, ctas, s) : launch<128, false>(a, nr, 1, ctas, s);
+  const int groups = (tiles + 1) / 2;
+  return D == 64 ? launch<64, true>(a, nr, groups, ctas, s) : launch<128, true>(a, nr, groups, ctas, s);
+}
+
+}  // namespace paged
+}  // namespace ec

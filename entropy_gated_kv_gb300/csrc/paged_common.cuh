@@ -38,8 +38,8 @@ struct Args {
   Shape s;
   const uint16_t* q;
   uint16_t* out;
-  float* part_o;      // [slots][rows of a slot][D]
-  float2* part_stat;  // [slots][rows of a slot]: running maximum (base 2, scaled) and sum
+  float* part_o;      // [slots][32][D] (few rows), [slots][D / 4][128][4] (tiles)
+  float2* part_stat;  // [slots][rows of a slot]: running maximum (base 2, scaled; NaN: the row is not written) and sum
   Record* records;    // [CTAs]
 };
 
@@ -127,7 +127,15 @@ EC_DEV void st_shared16(uint32_t dst, uint4 v) {
 // attention_paged_rows.cu: at most kFewRows packed rows (positions times the heads of a KV head) a sequence.
 constexpr int kFewRows = 32;
 cudaError_t launch_few_rows(const Args& a, int D, int ctas, cudaStream_t s);
-constexpr int kFewSlots = 2;  // partial tiles that a CTA leaves at most, of kFewRows rows
+// attention_paged_tiles.cu: tiles of nr positions, nr times the heads of a KV head at most 128 packed rows.
+constexpr int kTileRows = 128;
+cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, cudaStream_t s);
+// A CTA leaves two cut items at most, one that goes on in it and one that begins there: slots
+// 2 tiles cta + tile and 2 tiles cta + tiles + tile, with one tile or two beside each other.
+EC_DEV int64_t part_slot(int first_cta, int i, int tiles, int tile) {
+  return static_cast<int64_t>(first_cta + i) * 2 * tiles + (i == 0 ? tiles : 0) + tile;
+}
+EC_DEV float kNotWritten() { return __int_as_float(0x7fffffff); }
 
 }  // namespace paged
 }  // namespace ec
