@@ -81,70 +81,61 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(const __gr
   dst[threadIdx.x] = pack_bf16x2(y.x * inv, y.y * inv);
 }
 
-// The same for tiles: a thread takes a row and four columns, four parts in flight. The CTAs share out the pieces of all
-// records, 32 rows by 16 columns each.
-constexpr int kTileMergeThreads = 128;
+// The same for tiles: a CTA takes a record and 32 rows of it, a thread a row and every eighth quad of columns, as many
+// parts in flight as make eight quads. Where a few items may go over many CTAs each (QUADS 1) a CTA takes eight quads only.
+constexpr int kTileMergeThreads = 256;
 
-template <int D>
-__global__ void __launch_bounds__(kTileMergeThreads) merge_tiles_kernel(const __grid_constant__ Args a, int tiles, int records) {
-  constexpr int kPieces = 4 * (D / 16);
-  __shared__ int list[2 * kMaxCtas];
-  __shared__ int count;
+template <int D, int QUADS>
+__global__ void __launch_bounds__(kTileMergeThreads) merge_tiles_kernel(const __grid_constant__ Args a, int tiles) {
+  constexpr int kWarps = kTileMergeThreads / 32, kBatch = 8 / QUADS;
   const Shape& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  if (warp == 0) {
-    int n = 0;
+  const Record rec = a.records[blockIdx.x];
+  const int row = blockIdx.y * 32 + lane, quad0 = blockIdx.z * kWarps * QUADS + warp;
+  if (rec.parts == 0 || row >= rec.rows || quad0 >= D / 4) return;
+  const int cta = blockIdx.x / tiles, tile = blockIdx.x - cta * tiles;
+  float m = -INFINITY, l = 0.f;
+  float4 o[QUADS] = {};
+  bool lost = false;
+  for (int i0 = 0; i0 < rec.parts; i0 += kBatch) {
+    float2 st[kBatch];
+    float4 y[kBatch][QUADS];
 #pragma unroll
-    for (int k = 0; k < 2 * kMaxCtas / 32; ++k) {
-      const int i = 32 * k + lane;
-      const uint32_t have = __ballot_sync(0xffffffffu, i < records && a.records[i].parts > 0);
-      if ((have >> lane) & 1u) list[n + __popc(have & ((1u << lane) - 1u))] = i;
-      n += __popc(have);
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = min(i0 + k, rec.parts - 1);
+      const int64_t slot = part_slot(cta, i, tiles, tile);
+      st[k] = __ldcg(a.part_stat + slot * kTileRows + row);
+#pragma unroll
+      for (int c = 0; c < QUADS; ++c)
+        y[k][c] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * (D / 4) + quad0 + c * kWarps) * kTileRows + row);
     }
-    if (lane == 0) count = n;
-  }
-  __syncthreads();
-  for (int piece = blockIdx.x; piece < count * kPieces; piece += gridDim.x) {
-    const int which = list[piece / kPieces], sub = piece % kPieces;
-    const Record rec = a.records[which];
-    const int row = (sub & 3) * 32 + lane, quad = (sub >> 2) * 4 + warp;
-    if (row >= rec.rows) continue;
-    const int cta = which / tiles, tile = which - cta * tiles;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool lost = false;
-    for (int i0 = 0; i0 < rec.parts; i0 += 4) {
-      float2 st[4];
-      float4 y[4];
+    float top = m;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        st[k] = make_float2(-INFINITY, 0.f);
-        y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i0 + k < rec.parts) {
-          const int64_t slot = part_slot(cta, i0 + k, tiles, tile);
-          st[k] = __ldcg(a.part_stat + slot * kTileRows + row);
-          y[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * (D / 4) + quad) * kTileRows + row);
-        }
-      }
-      const float top = fmaxf(fmaxf(fmaxf(st[0].x, st[1].x), fmaxf(st[2].x, st[3].x)), m);
-      const float f0 = m == -INFINITY ? 1.f : ex2_approx(m - top);
-      m = top;
-      l *= f0, o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+    for (int k = 0; k < kBatch; ++k) top = fmaxf(top, st[k].x);
+    const float f0 = m == -INFINITY ? 1.f : ex2_approx(m - top);
+    m = top;
+    l *= f0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        lost = lost || st[k].x != st[k].x;
-        const float f = st[k].x == -INFINITY ? 1.f : ex2_approx(st[k].x - top);  // no finite score: zeros, or NaN
-        l += f * st[k].y, o.x += f * y[k].x, o.y += f * y[k].y, o.z += f * y[k].z, o.w += f * y[k].w;
-      }
+    for (int c = 0; c < QUADS; ++c) o[c].x *= f0, o[c].y *= f0, o[c].z *= f0, o[c].w *= f0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + k >= rec.parts) break;
+      lost = lost || st[k].x != st[k].x;
+      const float f = st[k].x == -INFINITY ? 1.f : ex2_approx(st[k].x - top);  // no finite score: zeros, or NaN
+      l += f * st[k].y;
+#pragma unroll
+      for (int c = 0; c < QUADS; ++c) o[c].x += f * y[k][c].x, o[c].y += f * y[k][c].y, o[c].z += f * y[k][c].z, o[c].w += f * y[k][c].w;
     }
-    if (lost) continue;
-    const int xr = rec.row0 + row, r = s.by_g(xr);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint2* dst = reinterpret_cast<uint2*>(a.out + ((static_cast<int64_t>(rec.b) * s.rows_max + r) * s.Hq + rec.kvh * s.g + (xr - r * s.g)) * D);
-    dst[quad] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   }
+  if (lost) return;
+  const int xr = rec.row0 + row, r = s.by_g(xr);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint2* dst = reinterpret_cast<uint2*>(a.out + ((static_cast<int64_t>(rec.b) * s.rows_max + r) * s.Hq + rec.kvh * s.g + (xr - r * s.g)) * D);
+#pragma unroll
+  for (int c = 0; c < QUADS; ++c)
+    dst[quad0 + c * kWarps] = make_uint2(pack_bf16x2(o[c].x * inv, o[c].y * inv), pack_bf16x2(o[c].z * inv, o[c].w * inv));
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -257,9 +248,14 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
   } else {
     const int tiles = rows_max <= nr ? 1 : 2;
     e = launch_tiles(a, p.D, nr, ctas, s);
-    if (e == cudaSuccess)
-      e = launch_pdl(p.D == 64 ? merge_tiles_kernel<64> : merge_tiles_kernel<128>, dim3(2 * ctas), dim3(kTileMergeThreads), 0, s, a, tiles,
-                     ctas * tiles);
+    // eight items or fewer may each go over many CTAs: their parts one column quad a thread
+    const bool few_items = static_cast<int64_t>(p.B) * p.Hkv * ((rows_max + nr - 1) / nr) <= 8;
+    const int quads = p.D / 32;  // of a thread that takes every eighth one
+    const dim3 grid(ctas * tiles, kTileRows / 32, few_items ? quads : 1);
+    if (e == cudaSuccess && p.D == 64)
+      e = launch_pdl(few_items ? merge_tiles_kernel<64, 1> : merge_tiles_kernel<64, 2>, grid, dim3(kTileMergeThreads), 0, s, a, tiles);
+    else if (e == cudaSuccess)
+      e = launch_pdl(few_items ? merge_tiles_kernel<128, 1> : merge_tiles_kernel<128, 4>, grid, dim3(kTileMergeThreads), 0, s, a, tiles);
   }
   if (e == cudaSuccess) *status = EC_OK;
   return e;

@@ -32,6 +32,7 @@ constexpr int kBlockM = 128;
 constexpr int kBlockN = 128;
 constexpr int kHalf = 64;  // keys of a score buffer, of a unit in shared memory
 constexpr int kItems = 4;  // items handed out and not yet finished
+constexpr int kCutCost = 5;  // what the partial rows of cut items and their join cost, in blocks
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;  // stream t: scores of half h at columns [128 t + 64 h, + 64), O at [256 + 128 t, + D)
 constexpr uint32_t kDescHi = sdesc_hi(1024);
@@ -48,20 +49,17 @@ struct __align__(16) Item {
 };
 static_assert(sizeof(Item) == 64, "four 16-byte pieces");
 
-// A block's place in shared memory: in the pair form blocks alternate between the two, in the split form each stream has
-// its own, as a waiter that does not follow every use of a place could take one use for another.
-constexpr int NB = 2;
-
+template <int P>
 struct Bars {
   uint64_t q_full, q_empty;
-  uint64_t unit_full[NB * 4], unit_empty[NB * 4];  // a block's K halves, then its V halves
-  uint64_t v_ok[NB * 2];
+  uint64_t unit_full[P], unit_empty[P];  // halves of 64 keys of K or V
+  uint64_t v_ok[P];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][half]
   uint64_t join, o_free;
   uint64_t item_full[kItems], item_empty[kItems];
   uint32_t tmem_base;
   int abort;
-  int scan[kThreads / 32];
+  int scan[kThreads / 32], most[kThreads / 32];
   int begin[4], share;  // b, group, KV head, block of the CTA's first item
 };
 
@@ -70,11 +68,16 @@ struct Layout {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;
   static constexpr int kUnit = kAtoms * kHalfAtom;
+  // Rings of places for two halves each, K's and V's of the blocks in turn: one ring in the pair form; one for each
+  // stream in the split form, as a waiter that does not follow every use of a place could take one use for another.
+  static constexpr int kRings = PAIR ? 1 : 2;
+  static constexpr int kRing = PAIR ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);
+  static constexpr int kPlaces = 2 * kRing * kRings;
   static constexpr int kUnitOff = (PAIR ? 2 : 1) * kTileBytes;
-  static constexpr int kStatOff = kUnitOff + NB * 4 * kUnit;
-  static constexpr int kItemOff = kStatOff + 2 * kBlockM * 8;
+  static constexpr int kStatOff = kUnitOff + kPlaces * kUnit;
+  static constexpr int kItemOff = kStatOff + (PAIR ? 0 : 2 * kBlockM * 8);
   static constexpr int kBarOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
-  static constexpr int kBytes = kBarOff + static_cast<int>(sizeof(Bars));
+  static constexpr int kBytes = kBarOff + static_cast<int>(sizeof(Bars<kPlaces>));
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -152,18 +155,17 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   using LY = Layout<D, PAIR>;
   constexpr int kTiles = PAIR ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Bars* bars = reinterpret_cast<Bars*>(smem + LY::kBarOff);
+  auto* bars = reinterpret_cast<Bars<LY::kPlaces>*>(smem + LY::kBarOff);
   const Shape& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int step = nr * kTiles;  // positions of a group
 
   if (warp == 0) {  // the lanes share the barriers
-    if (lane < NB * 4) {
+    if (lane < LY::kPlaces) {
       mbar_init(&bars->unit_full[lane], 1);
-      // released by the issuers that read it, a V half by warp 3 too
-      mbar_init(&bars->unit_empty[lane], kTiles + ((lane & 3) >= 2 ? 1 : 0));
+      mbar_init(&bars->unit_empty[lane], kTiles + 1);  // released by the issuers that read it and by warp 3
+      mbar_init(&bars->v_ok[lane], 1);
     }
-    if (lane < NB * 2) mbar_init(&bars->v_ok[lane], 1);
     if (lane < 4) {
       mbar_init(&bars->s_full[lane >> 1][lane & 1], 1);
       mbar_init(&bars->p_full[lane >> 1][lane & 1], 4);
@@ -198,14 +200,16 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   // The line: each thread adds up the blocks of its (sequence, group) pairs, the CTA their sum, and the thread whose pairs
   // hold the first block of this CTA's share finds it.
   const int pairs = s.B * groups, per = (pairs + kThreads - 1) / kThreads, p0 = threadIdx.x * per;
-  int mine = 0;
+  int mine = 0, longest = 0;
 #pragma unroll 2
   for (int i = p0; i < min(p0 + per, pairs); ++i) {
-    const int b = i / groups;
-    mine += load_group(s, b, i - b * groups, step, blockIdx.x == 0).blocks * s.Hkv;
+    const int b = i / groups, blocks = load_group(s, b, i - b * groups, step, blockIdx.x == 0).blocks;
+    mine += blocks * s.Hkv;
+    longest = max(longest, blocks);
   }
   int incl = warp_inclusive(mine);
-  if (lane == 31) bars->scan[warp] = incl;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) bars->scan[warp] = incl, bars->most[warp] = longest;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -214,9 +218,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) incl += bars->scan[w];
     total += bars->scan[w];
+    longest = max(longest, bars->most[w]);
   }
   const int share = (total + gridDim.x - 1) / gridDim.x;
   const int begin = blockIdx.x * share;
+  // Whole items, each to the CTA whose share holds its first block, where that costs little more than the cuts' partial
+  // rows do.
+  const bool whole = (share + longest - 1) / max(longest, 1) * longest <= share + kCutCost;
   if (begin < total && begin >= incl - mine && begin < incl) {
     int off = begin - (incl - mine);
     for (int i = p0;; ++i) {
@@ -247,19 +255,15 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     if (!ok) it.nblk = 0;
     return it;
   };
-  // Place and use of the blocks of an item in order, for the roles that see all of them.
-  struct Places {
-    uint32_t blocks = 0, used[2] = {0, 0};
-    EC_DEV void at(int i, uint32_t& place, uint32_t& use) {
-      if constexpr (PAIR) {
-        place = blocks & 1u, use = blocks >> 1;
-        ++blocks;
-      } else {
-        place = i & 1u, use = used[place];
-        used[0] += place ^ 1u, used[1] += place;
-      }
+  // Place (of two halves) and use of K or V of a ring's next block.
+  struct Place {
+    uint32_t at, use;
+    EC_DEV void next() {
+      at += 2;
+      if (at >= LY::kRing) at -= LY::kRing, ++use;
     }
   };
+  auto ring_of = [](int i) { return PAIR ? 0 : i & 1; };  // of block i of an item
   auto block_of = [](const Item& it, int i) {
     const int v = it.v0 + i;
     return v < it.near_blocks ? v : v - it.near_blocks + it.first;
@@ -275,12 +279,25 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     int b = bars->begin[0], grp = bars->begin[1], kvh = bars->begin[2], u = bars->begin[3];
     Group g{};
     if (left > 0) g = load_group(s, b, grp, step, false);
-    Places places;
+    auto next_group = [&]() {
+      if (++kvh < s.Hkv) return;
+      kvh = 0;
+      do {
+        if (++grp == groups) grp = 0, ++b;
+        g = load_group(s, b, grp, step, false);
+      } while (g.blocks == 0);
+    };
+    if (whole && u > 0) {  // an item of the CTA before
+      left -= g.blocks - u;
+      u = 0;
+      if (left > 0) next_group();
+    }
+    Place k0{0, 0}, v0{1, 0}, k1{0, 0}, v1{1, 0};  // of the rings
     bool ok = true;
 #pragma unroll 1
     for (int count = 0;; ++count) {
       Item it;
-      it.nblk = ok && left > 0 ? min(g.blocks - u, left) : 0;
+      it.nblk = ok && left > 0 ? (whole ? g.blocks : min(g.blocks - u, left)) : 0;
       if (it.nblk > 0) {
         it.b = b, it.kvh = kvh, it.v0 = u;
         it.near_blocks = g.k.near, it.first = g.k.first;
@@ -323,12 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         const int page = next, j0 = block_of(it, i) * kBlockN;
         if (i + 1 < it.nblk) next = look(i + 1);
         const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-        uint32_t place, use;
-        places.at(i, place, use);
+        const int ring = ring_of(i);
 #pragma unroll 1
         for (int n = 0; ok && n < 4; ++n) {
-          const int h = n & 1, unit = place * 4 + n;
-          ok = wait_w(&bars->unit_empty[unit], (use & 1u) ^ 1u);
+          const Place pl = n < 2 ? (ring == 0 ? k0 : k1) : ring == 0 ? v0 : v1;
+          const int h = n & 1, unit = (ring * LY::kRing + pl.at) * 2 + h;
+          ok = wait_w(&bars->unit_empty[unit], (pl.use & 1u) ^ 1u);
           if (!ok) break;
           const uint32_t mask = (have >> (h * boxes)) & ((1u << boxes) - 1u);
           if (lane == 0) mbar_arrive_expect_tx(&bars->unit_full[unit], __popc(mask) * box * D * 2);
@@ -339,16 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             tma_load_5d(smem + LY::kUnitOff + unit * LY::kUnit + at * kHalfAtom + r * box * 128, n < 2 ? &a.tk : &a.tv,
                         &bars->unit_full[unit], 0, (j0 + h * kHalf + r * box) & ((1 << s.page_shift) - 1), at, kvh, pg);
         }
+        if (ring == 0) k0.next(), v0.next();
+        else k1.next(), v1.next();
       }
       left -= it.nblk;
       u = 0;
-      if (left > 0 && ++kvh == s.Hkv) {
-        kvh = 0;
-        do {
-          if (++grp == groups) grp = 0, ++b;
-          g = load_group(s, b, grp, step, false);
-        } while (g.blocks == 0);
-      }
+      if (left > 0) next_group();
     }
   } else if (warp <= 2) {
     // ------------------------------------------------------------------ issuer of one stream
@@ -361,19 +374,18 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const uint32_t s_col = tmem_u + st * 128, o_col = tmem_u + kTmemO + st * 128;
     constexpr int kBy = PAIR ? 1 : 2;  // a stream takes every kBy-th block
     uint32_t used = 0;    // blocks of this stream whose P V is under way or done
-    uint32_t blocks = 0;  // all blocks, in the pair form
+    Place k{0, 0}, v{1, 0};  // of the next scores, of the next P V
+    const uint32_t unit00 = PAIR ? 0 : st * LY::kRing * 2;
     bool ok = true;
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
       const bool live = PAIR ? (st == 0 || it.rows1 > 0) : static_cast<int>(st) < it.nblk;
       const int i0 = PAIR ? 0 : st;
-      uint32_t kb = blocks;  // the block whose scores are issued next, and the one whose P V is, in the pair form
-      uint32_t vb = blocks;
       auto issue_qk = [&](int i, uint32_t n, int h) {
-        const uint32_t unit = (PAIR ? kb & 1u : st) * 4 + h, use = PAIR ? kb >> 1 : n;
+        const uint32_t unit = unit00 + k.at * 2 + h;
         // K is here, and the buffer's last P has been read
-        if (!wait_w(&bars->unit_full[unit], use & 1u) || (n != 0 && !wait_w(&bars->pv_done[st][h], (n - 1) & 1u))) return false;
+        if (!wait_w(&bars->unit_full[unit], k.use & 1u) || (n != 0 && !wait_w(&bars->pv_done[st][h], (n - 1) & 1u))) return false;
         tc_fence_after();
         const uint32_t k_lo = sdesc_lo(unit0 + unit * LY::kUnit, 16);
         const uint32_t col = s_col + h * kHalf;
@@ -389,10 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         return true;
       };
       auto issue_pv = [&](int i, uint32_t n, int h) {
-        const uint32_t place = PAIR ? vb & 1u : st, use = PAIR ? vb >> 1 : n, unit = place * 4 + 2 + h;
-        if (!wait_w(&bars->unit_full[unit], use & 1u)) return false;
+        const uint32_t unit = unit00 + v.at * 2 + h;
+        if (!wait_w(&bars->unit_full[unit], v.use & 1u)) return false;
         const int j0 = block_of(it, i) * kBlockN + h * kHalf;
-        if (!all_in(it.near, it.lo, it.hi, j0, kHalf) && !wait_w(&bars->v_ok[place * 2 + h], use & 1u)) return false;
+        if (!all_in(it.near, it.lo, it.hi, j0, kHalf) && !wait_w(&bars->v_ok[unit], v.use & 1u)) return false;
         if (!wait_w(&bars->p_full[st][h], n & 1u)) return false;
         // the item's first product starts O anew: the warps of both streams have read it
         if (!PAIR && items > 0 && i == i0 && h == 0 && !wait_w(&bars->o_free, (items - 1) & 1)) return false;
@@ -413,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       ok = wait_w(&bars->q_full, items & 1);
       if (live) {
         ok = ok && issue_qk(i0, used, 0) && issue_qk(i0, used, 1);
-        ++kb;
+        k.next();
 #pragma unroll 1
         for (int i = i0; ok && i < it.nblk; i += kBy, ++used) {
 #pragma unroll
@@ -421,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             ok = ok && issue_pv(i, used, h);
             if (i + kBy < it.nblk) ok = ok && issue_qk(i + kBy, used + 1, h);
           }
-          ++kb;
-          ++vb;
+          if (i + kBy < it.nblk) k.next();
+          v.next();
         }
       } else {
         // Nothing of this item falls to the stream. (It leaves o_free alone: its next wait there comes after a P of its own,
@@ -433,19 +445,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
           for (int i = 0; ok && i < it.nblk; ++i) {
 #pragma unroll 1
             for (int n = 0; ok && n < 4; ++n) {
-              ok = wait_w(&bars->unit_full[(kb & 1u) * 4 + n], (kb >> 1) & 1u);
-              if (ok && lane == 0) mbar_arrive(&bars->unit_empty[(kb & 1u) * 4 + n]);
+              const Place pl = n < 2 ? k : v;
+              ok = wait_w(&bars->unit_full[pl.at * 2 + (n & 1)], pl.use & 1u);
+              if (ok && lane == 0) mbar_arrive(&bars->unit_empty[pl.at * 2 + (n & 1)]);
             }
-            ++kb;
+            k.next();
+            v.next();
           }
         }
       }
-      blocks += it.nblk;
       if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------------ rows of V outside the hull
-    Places places;
+    Place k0{0, 0}, v0{1, 0}, k1{0, 0}, v1{1, 0};  // of the rings
     bool ok = true;
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
@@ -453,14 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 #pragma unroll 1
       for (int i = 0; ok && i < it.nblk; ++i) {
         const int j0 = block_of(it, i) * kBlockN;
-        uint32_t place, use;
-        places.at(i, place, use);
+        const int ring = ring_of(i);
 #pragma unroll 1
-        for (int h = 0; ok && h < 2; ++h) {
-          const int unit = place * 4 + 2 + h, j = j0 + h * kHalf;
-          ok = wait_w(&bars->unit_full[unit], use & 1u);
+        for (int n = 0; ok && n < 4; ++n) {
+          const Place pl = n < 2 ? (ring == 0 ? k0 : k1) : ring == 0 ? v0 : v1;
+          const int unit = (ring * LY::kRing + pl.at) * 2 + (n & 1), j = j0 + (n & 1) * kHalf;
+          ok = wait_w(&bars->unit_full[unit], pl.use & 1u);
           if (!ok) break;
-          if (!all_in(it.near, it.lo, it.hi, j, kHalf)) {
+          if (n >= 2 && !all_in(it.near, it.lo, it.hi, j, kHalf)) {
             const uint32_t base = smem_u32(smem + LY::kUnitOff) + unit * LY::kUnit;
 #pragma unroll 1
             for (int r = lane >> 3; r < kHalf; r += 4)  // eight lanes a row
@@ -471,10 +484,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             __syncwarp();
           }
           if (lane == 0) {
-            mbar_arrive(&bars->v_ok[place * 2 + h]);
+            mbar_arrive(&bars->v_ok[unit]);
             mbar_arrive(&bars->unit_empty[unit]);
           }
         }
+        if (ring == 0) k0.next(), v0.next();
+        else k1.next(), v1.next();
       }
       if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);
     }

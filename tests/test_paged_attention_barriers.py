@@ -9,17 +9,18 @@ from tests.test_cached_attention_barriers import ITEMS, Bar, Broken, held
 
 
 class Cta:
-    """items: (blocks, whether the second tile has rows, which halves are cut by the hull) each."""
+    """items: (blocks, whether the second tile has rows, how many halves are cut by the hull) each. ring: places for two halves."""
 
-    def __init__(self, items, pair, seed, fixer_releases=True):
+    def __init__(self, items, pair, ring, seed, fixer_releases=True):
+        self.ring = ring
         self.items, self.pair, self.rng, self.fixer_releases = list(items) + [(0, False, None)], pair, random.Random(seed), fixer_releases
         two = lambda n: [[Bar(n) for _ in range(2)] for _ in range(2)]  # noqa: E731
         tiles = 2 if pair else 1
         self.item_full, self.item_empty = [Bar(1) for _ in range(ITEMS)], [Bar(5) for _ in range(ITEMS)]
         self.q_full, self.q_empty, self.join, self.o_free = Bar(1), Bar(2), Bar(2), Bar(2)
-        self.full = [[Bar(1) for _ in range(4)] for _ in range(2)]
-        self.empty = [[Bar(tiles + (fixer_releases and u >= 2)) for u in range(4)] for _ in range(2)]
-        self.v_ok = two(1)
+        rings = range(1 if pair else 2)
+        self.full, self.v_ok = ([[Bar(1) for _ in range(2 * ring)] for _ in rings] for _ in range(2))
+        self.empty = [[Bar(tiles + fixer_releases) for _ in range(2 * ring)] for _ in rings]
         self.s_full, self.p_full, self.pv_done = two(1), two(1), two(1)
         self.copies, self.products = [], [[], []]
         self.roles = {"producer": self.producer(), "fixer": self.fixer()}
@@ -27,75 +28,70 @@ class Cta:
             self.roles[f"issuer {st}"] = self.issuer(st)
             self.roles[f"softmax {st}"] = self.softmax(st)
 
-    def places(self):
-        """(place, use) of the blocks of an item in order."""
-        n, used = 0, [0, 0]
-        while True:
-            i = yield None
-            if self.pair:
-                at = n & 1, n >> 1
-                n += 1
-            else:
-                at = i & 1, used[i & 1]
-                used[i & 1] += 1
-            yield at
+    def units(self, c):
+        """(unit, use) of the halves K0, K1, V0, V1 of a ring's block c."""
+        return [(2 * ((2 * c + kv) % self.ring) + h, (2 * c + kv) // self.ring) for kv in range(2) for h in range(2)]
 
-    @staticmethod
-    def at(places, i):
-        next(places)
-        return places.send(i)
+    def blocks(self):
+        """Of each item: (index, its ring, its units) of the blocks in order."""
+        seen = [0, 0]
+        for nblk, _, _ in self.items:
+            line = []
+            for i in range(nblk):
+                r = 0 if self.pair else i & 1
+                line.append((i, r, self.units(seen[r])))
+                seen[r] += 1
+            yield line
 
     def producer(self):
-        places = self.places()
-        for n, (nblk, two, _) in enumerate(self.items):
+        for n, line in enumerate(self.blocks()):
             yield self.item_empty[n % ITEMS], n // ITEMS - 1
             self.item_full[n % ITEMS].arrive()
             yield None
-            if nblk == 0:
+            if not line:
                 return
             if n > 0:
                 yield self.q_empty, n - 1
             self.copies.append(self.q_full)
-            for i in range(nblk):
-                p, use = self.at(places, i)
-                for u in range(4):
-                    yield self.empty[p][u], use - 1
-                    self.copies.append(self.full[p][u])
+            for _, r, units in line:
+                for u, use in units:
+                    yield self.empty[r][u], use - 1
+                    self.copies.append(self.full[r][u])
                     yield None
 
     def fixer(self):
-        places = self.places()
-        for n, (nblk, two, _) in enumerate(self.items):
+        for n, line in enumerate(self.blocks()):
             yield self.item_full[n % ITEMS], n // ITEMS
-            if nblk == 0:
+            if not line:
                 return
-            for i in range(nblk):
-                p, use = self.at(places, i)
-                for h in range(2):
-                    yield self.full[p][2 + h], use
-                    self.v_ok[p][h].arrive()
+            for _, r, units in line:
+                for u, use in units:
+                    yield self.full[r][u], use
+                    self.v_ok[r][u].arrive()
                     if self.fixer_releases:
-                        self.empty[p][2 + h].arrive()
+                        self.empty[r][u].arrive()
                     yield None
             self.item_empty[n % ITEMS].arrive()
 
     def issuer(self, st):
-        used = blocks = 0
+        used = 0
         by = 1 if self.pair else 2
-        for n, (nblk, two, cut) in enumerate(self.items):
+        r = 0 if self.pair else st
+        for n, line in enumerate(self.blocks()):
+            _, two, cut = self.items[n]
             yield self.item_full[n % ITEMS], n // ITEMS
+            nblk = len(line)
             if nblk == 0:
                 return
             live = (st == 0 or two) if self.pair else st < nblk
             i0 = 0 if self.pair else st
-            kb = vb = blocks
 
-            def scores(i, c, h, kb):
-                p, use = (kb & 1, kb >> 1) if self.pair else (st, c)
-                yield self.full[p][h], use
+            def scores(i, c, h):
+                u, use = line[i][2][h]
+                yield self.full[r][u], use
                 if c:
                     yield self.pv_done[st][h], c - 1
-                self.products[st] += [self.s_full[st][h], self.empty[p][h]]
+                self.products[st] += [self.s_full[st][h], self.empty[r][u]]
                 if h == 1 and i + by >= nblk:
                     self.products[st].append(self.q_empty)
                 yield None
@@ -103,35 +99,30 @@ class Cta:
             yield self.q_full, n
             if live:
                 for h in range(2):
-                    yield from scores(i0, used, h, kb)
-                kb += 1
+                    yield from scores(i0, used, h)
                 for i in range(i0, nblk, by):
                     for h in range(2):
-                        p, use = (vb & 1, vb >> 1) if self.pair else (st, used)
-                        yield self.full[p][2 + h], use
+                        u, use = line[i][2][2 + h]
+                        yield self.full[r][u], use
                         if self.rng.random() < cut:
-                            yield self.v_ok[p][h], use
+                            yield self.v_ok[r][u], use
                         yield self.p_full[st][h], used
                         if not self.pair and n > 0 and i == i0 and h == 0:
                             yield self.o_free, n - 1
-                        self.products[st] += [self.pv_done[st][h], self.empty[p][2 + h]]
+                        self.products[st] += [self.pv_done[st][h], self.empty[r][u]]
                         yield None
                         if i + by < nblk:
-                            yield from scores(i + by, used + 1, h, kb)
-                    kb += 1
-                    vb += 1
+                            yield from scores(i + by, used + 1, h)
                     used += 1
             else:
                 self.q_empty.arrive()
                 yield None
                 if self.pair:
-                    for i in range(nblk):
-                        for u in range(4):
-                            yield self.full[kb & 1][u], kb >> 1
-                            self.empty[kb & 1][u].arrive()
+                    for _, _, units in line:
+                        for u, use in units:
+                            yield self.full[r][u], use
+                            self.empty[r][u].arrive()
                             yield None
-                        kb += 1
-            blocks += nblk
             self.item_empty[n % ITEMS].arrive()
             yield None
 
@@ -187,20 +178,20 @@ ROLES = ["producer", "fixer", "copies"] + [f"{r} {st}" for r in ("issuer", "soft
 LINES = [[1], [1, 1], [1] * 7, [3, 1], [2, 1, 1, 4, 1], [5, 1, 1, 1, 1, 1, 2, 3, 1], [2] * 6, [1, 7, 1, 2], [4, 4, 4]]
 
 
-@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("pair,ring", [(False, 3), (False, 6), (True, 5), (True, 8)])  # D = 128, 64
 @pytest.mark.parametrize("line", LINES, ids=str)
-def test_every_wait_ends_on_its_own_phase(line, pair):
+def test_every_wait_ends_on_its_own_phase(line, pair, ring):
     for seed in range(8):
         rng = random.Random(seed)
         items = [(n, rng.random() < 0.6, rng.choice([0.0, 0.5, 1.0])) for n in line]
         for role in [None, *ROLES]:
-            Cta(items, pair, seed).run(held(role, seed))
+            Cta(items, pair, ring, seed).run(held(role, seed))
 
 
 def test_places_freed_without_the_fixer_are_noticed():
-    # a V half that may be filled again before the fixer has passed: its arrival there, which an issuer waits for only where
+    # a half that may be filled again before the fixer has passed: its arrival, which an issuer waits for only where
     # keys are cut, may be late by a use
     with pytest.raises(Broken):
         for seed in range(8):
             for role in ROLES:
-                Cta([(6, False, 0.5), (4, False, 0.5)], False, seed, fixer_releases=False).run(held(role, seed))
+                Cta([(6, False, 0.5), (4, False, 0.5)], False, 3, seed, fixer_releases=False).run(held(role, seed))
