@@ -233,8 +233,8 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
   a.records = reinterpret_cast<Record*>(w + lay.records);
   const int ctas = std::min(sms, kMaxCtas);
   const bool few = few_rows(p, rows_max);
-  // a chunk of 16 keys, or a half block of 64 as far as a page holds it
-  const int box = few ? 16 : std::min(64, c.page_size), atoms = few || box == 64 ? p.D / 64 : 1;
+  // a chunk of 16 keys, or a block of 128 as far as a page holds it
+  const int box = few ? 16 : std::min(128, c.page_size), atoms = few || box == 128 ? p.D / 64 : 1;
   const int nr = tile_positions(p, rows_max);
   if (!encode_pool(enc, &a.tk, c.k, p, c, box, atoms) || !encode_pool(enc, &a.tv, c.v, p, c, box, atoms) ||
       (!few && !encode_queries(enc, &a.tq, q, p, rows_max, nr))) {

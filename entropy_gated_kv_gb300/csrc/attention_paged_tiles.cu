@@ -2,15 +2,23 @@
 // sequence's positions times the g query heads of a KV head) on the 5th-generation tensor cores.
 //
 //   out[x] = sum_j p_xj v_j / sum_j p_xj, p_xj = 2^(s_xj - m_x), s_xj = scale log2(e) <q_x, k_j>, m_x a running maximum
-// Two streams run through a CTA, each with its issuer, its softmax warps, two score buffers of 64 keys and an O
-// accumulator in tensor memory: while one half's softmax runs, the tensor cores do the other half's P V and the next
-// scores. Two forms:
+// Two streams run through a CTA, each with its issuer, its softmax warps, a score buffer of 128 keys and an O
+// accumulator in tensor memory: while one stream is in its softmax, the tensor cores do the other's P V and next scores.
+// The weights are handed over in two halves of 64 keys, so that P V of the first runs beside the exponentials of the
+// second. Two forms:
 //   - pair (a sequence may have more rows than a tile): a stream a tile, two tiles side by side on the same K/V, so that
 //     a byte brought to shared memory feeds 256 rows;
 //   - split (every sequence has one tile): the streams take the even and the odd key blocks of the tile and are
 //     joined at the item's end.
-// Blocks are 128 keys, brought in by TMA in halves of 64: one box of 64 rows, or of a smaller page, from the page
-// that the table names. The blocks of all items (sequence, group of tiles, KV head) stand in one line of
+// In the pair form the streams take turns at the tensor cores, P V and next scores in one piece: left to themselves they
+// fall into step, both in the softmax, then both at the tensor cores (3820 cycles a pair of blocks for 3300; 4 full steps
+// of 2048 rows, 28/4 heads, 210 us for 182). What a pair of blocks is bound by: a stream's own chain, softmax 1700
+// cycles (64 exponentials of a row take a lone warp 490, two warps of a scheduler 590 together), P V and scores 1000, and
+// some 600 between them, as a wait takes 120 to 200 cycles also when it is over. Tried beside that: score buffers
+// of 64 keys, two a stream (210 us: as many waits for half the product), one issuer for both streams (222 us), sixteen
+// softmax warps (204 us, with 104 registers each), all 128 scores in registers (180 us, but 3 to 5% slower in the split form).
+// Blocks are 128 keys, brought in by TMA: one box of 128 rows, or of a smaller page, from the page that the table
+// names. The blocks of all items (sequence, group of tiles, KV head) stand in one line of
 // which the CTAs, one an SM, take equal shares; an item cut between CTAs leaves fp32 partial rows, which a second
 // launch joins in a fixed order. A window leaves only the blocks that a group's rows see between them in the line.
 // Roles (12 warps):
@@ -30,15 +38,14 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kBlockM = 128;
 constexpr int kBlockN = 128;
-constexpr int kHalf = 64;  // keys of a score buffer, of a unit in shared memory
+constexpr int kHalf = 64;  // keys whose weights are handed over at once
 constexpr int kItems = 4;  // items handed out and not yet finished
 constexpr int kCutCost = 5;  // what the partial rows of cut items and their join cost, in blocks
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 256;  // stream t: scores of half h at columns [128 t + 64 h, + 64), O at [256 + 128 t, + D)
+constexpr uint32_t kTmemO = 256;  // stream t: scores at columns [128 t, + 128), O at [256 + 128 t, + D)
 constexpr uint32_t kDescHi = sdesc_hi(1024);
-constexpr int kAtomBytes = 128 * 128;   // 128 rows x 128 bytes (64 bf16): the query tile
-constexpr int kHalfAtom = kHalf * 128;  // 64 rows x 128 bytes: K and V
-__host__ __device__ constexpr uint32_t step_k(int kk, int atom) { return (kk >> 2) * (atom / 16) + (kk & 3) * 2; }
+constexpr int kAtomBytes = 128 * 128;  // 128 rows x 128 bytes (64 bf16)
+__host__ __device__ constexpr uint32_t step_k(int kk) { return (kk >> 2) * (kAtomBytes / 16) + (kk & 3) * 2; }
 constexpr uint32_t kStepPV = 16 * 128 / 16;
 
 // Work of a CTA on one (sequence, group of tiles, KV head): blocks v0 .. v0 + nblk - 1 of the group's; nblk 0: the end.
@@ -52,10 +59,10 @@ static_assert(sizeof(Item) == 64, "four 16-byte pieces");
 template <int P>
 struct Bars {
   uint64_t q_full, q_empty;
-  uint64_t unit_full[P], unit_empty[P];  // halves of 64 keys of K or V
+  uint64_t unit_full[P], unit_empty[P];  // K or V of a block
   uint64_t v_ok[P];
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [stream][half]
-  uint64_t join, o_free;
+  uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2];  // [stream][half]
+  uint64_t join, o_free, turn[2];
   uint64_t item_full[kItems], item_empty[kItems];
   uint32_t tmem_base;
   int abort;
@@ -67,14 +74,13 @@ template <int D, bool PAIR>
 struct Layout {
   static constexpr int kAtoms = D / 64;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;
-  static constexpr int kUnit = kAtoms * kHalfAtom;
-  // Rings of places for two halves each, K's and V's of the blocks in turn: one ring in the pair form; one for each
-  // stream in the split form, as a waiter that does not follow every use of a place could take one use for another.
+  // Rings of places, K's and V's of the blocks in turn: one ring in the pair form; one for each stream in the split
+  // form, as a waiter that does not follow every use of a place could take one use for another.
   static constexpr int kRings = PAIR ? 1 : 2;
-  static constexpr int kRing = PAIR ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);
-  static constexpr int kPlaces = 2 * kRing * kRings;
+  static constexpr int kRing = (PAIR ? 5 : 3) * (D == 128 ? 1 : 2);
+  static constexpr int kPlaces = kRing * kRings;
   static constexpr int kUnitOff = (PAIR ? 2 : 1) * kTileBytes;
-  static constexpr int kStatOff = kUnitOff + kPlaces * kUnit;
+  static constexpr int kStatOff = kUnitOff + kPlaces * kTileBytes;
   static constexpr int kItemOff = kStatOff + (PAIR ? 0 : 2 * kBlockM * 8);
   static constexpr int kBarOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
   static constexpr int kBytes = kBarOff + static_cast<int>(sizeof(Bars<kPlaces>));
@@ -129,6 +135,11 @@ EC_DEV float max3(float a, float b, float c) {
   return r;
 }
 
+// The rest of a wait that is not over at first sight.
+EC_DEV bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* dev_err) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, dev_err, kWaitLimitNs)) != 0;
+}
+
 // A group of tiles of a sequence: its positions (at most `step`), what they see, its blocks.
 struct Group {
   int rows, n, blocks;
@@ -166,10 +177,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       mbar_init(&bars->unit_empty[lane], kTiles + 1);  // released by the issuers that read it and by warp 3
       mbar_init(&bars->v_ok[lane], 1);
     }
-    if (lane < 4) {
-      mbar_init(&bars->s_full[lane >> 1][lane & 1], 1);
-      mbar_init(&bars->p_full[lane >> 1][lane & 1], 4);
-      mbar_init(&bars->pv_done[lane >> 1][lane & 1], 1);
+    if (lane < 4) mbar_init(&bars->p_full[lane >> 1][lane & 1], 4);
+    if (lane < 2) {
+      mbar_init(&bars->s_full[lane], 1);
+      mbar_init(&bars->pv_half[lane], 1);
+      mbar_init(&bars->pv_done[lane], 1);
+      mbar_init(&bars->turn[lane], 1);
     }
     if (lane < kItems) {
       mbar_init(&bars->item_full[lane], 1);
@@ -239,10 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   __syncthreads();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_wait_bounded(bar, parity, abort_flag, s.dev_err, kWaitLimitNs);
+  auto wait_w = [&](uint64_t* bar, uint32_t parity) {  // whole warp
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return wait_on(bar, parity, &bars->abort, s.dev_err);
   };
-  auto wait_w = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   // The n-th item of this CTA, once the producer has made it; nblk = 0 at the end and after a wait that gave up.
   Item* const items_s = reinterpret_cast<Item*>(smem + LY::kItemOff);
   auto next_item = [&](int n) {
@@ -255,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     if (!ok) it.nblk = 0;
     return it;
   };
-  // Place (of two halves) and use of K or V of a ring's next block.
+  // Place and use of K or V of a ring's next block.
   struct Place {
     uint32_t at, use;
     EC_DEV void next() {
@@ -271,9 +284,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 
   if (warp == 0) {
     // ------------------------------------------------------------------ items and loads
-    const int box = min(kHalf, 1 << s.page_shift);       // rows of a TMA box
-    const int boxes = kHalf / box;                       // boxes of a half's rows: 1, 2 or 4
-    const int atoms = box < kHalf ? LY::kAtoms : 1;      // boxes beside each other
+    const int box = min(kBlockN, 1 << s.page_shift);   // rows of a TMA box
+    const int boxes = kBlockN / box;                   // boxes of a block's rows: 1, 2, 4 or 8
+    const int atoms = box < kBlockN ? LY::kAtoms : 1;  // boxes beside each other
     if (lane < kTiles) a.records[blockIdx.x * kTiles + lane].parts = 0;
     int left = bars->begin[3] >= 0 && !*abort_flag ? min(share, total - begin) : 0;
     int b = bars->begin[0], grp = bars->begin[1], kvh = bars->begin[2], u = bars->begin[3];
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       // lane i: the page of the i-th box of a block's rows, one block ahead
       auto look = [&](int i) {
         const int j = block_of(it, i) * kBlockN + lane * box;
-        return lane < 2 * boxes && some_in(it.near, it.lo, it.hi, j, box) ? page_of(s, b, j) : -1;
+        return lane < boxes && some_in(it.near, it.lo, it.hi, j, box) ? page_of(s, b, j) : -1;
       };
       int next = look(0);
 #pragma unroll 1
@@ -341,20 +354,19 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         if (i + 1 < it.nblk) next = look(i + 1);
         const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
         const int ring = ring_of(i);
+        const int r = lane % boxes, at = lane / boxes;
+        const int pg = __shfl_sync(0xffffffffu, page, r);
 #pragma unroll 1
-        for (int n = 0; ok && n < 4; ++n) {
-          const Place pl = n < 2 ? (ring == 0 ? k0 : k1) : ring == 0 ? v0 : v1;
-          const int h = n & 1, unit = (ring * LY::kRing + pl.at) * 2 + h;
+        for (int n = 0; ok && n < 2; ++n) {
+          const Place pl = n == 0 ? (ring == 0 ? k0 : k1) : ring == 0 ? v0 : v1;
+          const int unit = ring * LY::kRing + pl.at;
           ok = wait_w(&bars->unit_empty[unit], (pl.use & 1u) ^ 1u);
           if (!ok) break;
-          const uint32_t mask = (have >> (h * boxes)) & ((1u << boxes) - 1u);
-          if (lane == 0) mbar_arrive_expect_tx(&bars->unit_full[unit], __popc(mask) * box * D * 2);
+          if (lane == 0) mbar_arrive_expect_tx(&bars->unit_full[unit], __popc(have) * box * D * 2);
           __syncwarp();
-          const int r = lane % boxes, at = lane / boxes;
-          const int pg = __shfl_sync(0xffffffffu, page, h * boxes + r);
-          if (at < atoms && ((mask >> r) & 1u))
-            tma_load_5d(smem + LY::kUnitOff + unit * LY::kUnit + at * kHalfAtom + r * box * 128, n < 2 ? &a.tk : &a.tv,
-                        &bars->unit_full[unit], 0, (j0 + h * kHalf + r * box) & ((1 << s.page_shift) - 1), at, kvh, pg);
+          if (at < atoms && pg >= 0)
+            tma_load_5d(smem + LY::kUnitOff + unit * LY::kTileBytes + at * kAtomBytes + r * box * 128, n == 0 ? &a.tk : &a.tv,
+                        &bars->unit_full[unit], 0, (j0 + r * box) & ((1 << s.page_shift) - 1), at, kvh, pg);
         }
         if (ring == 0) k0.next(), v0.next();
         else k1.next(), v1.next();
@@ -366,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   } else if (warp <= 2) {
     // ------------------------------------------------------------------ issuer of one stream
     // The whole warp waits, one thread issues: the products' descriptors live in uniform registers.
-    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kHalf, 0);
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBlockN, 0);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
     const uint32_t st = __shfl_sync(0xffffffffu, warp - 1, 0);
     const uint32_t q_lo = sdesc_lo(smem_u32(smem) + (PAIR ? st * LY::kTileBytes : 0), 16), unit0 = smem_u32(smem + LY::kUnitOff);
@@ -375,67 +387,84 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     constexpr int kBy = PAIR ? 1 : 2;  // a stream takes every kBy-th block
     uint32_t used = 0;    // blocks of this stream whose P V is under way or done
     Place k{0, 0}, v{1, 0};  // of the next scores, of the next P V
-    const uint32_t unit00 = PAIR ? 0 : st * LY::kRing * 2;
+    const uint32_t ring0 = PAIR ? 0 : st * LY::kRing;
+    // Turns of the pair form: a stream's P V and next scores go out in one piece, by turns with the other stream's.
+    uint32_t turns = 0;
+    auto my_turn = [&](bool both) {
+      if (!both) return true;
+      const uint32_t n = turns + st;  // stream 0's first turn waits for nothing
+      return n == 0 || wait_w(&bars->turn[st], (n - 1) & 1u);
+    };
     bool ok = true;
     for (int items = 0; ok; ++items) {
       const Item it = next_item(items);
       if (it.nblk == 0) break;
       const bool live = PAIR ? (st == 0 || it.rows1 > 0) : static_cast<int>(st) < it.nblk;
       const int i0 = PAIR ? 0 : st;
-      auto issue_qk = [&](int i, uint32_t n, int h) {
-        const uint32_t unit = unit00 + k.at * 2 + h;
-        // K is here, and the buffer's last P has been read
-        if (!wait_w(&bars->unit_full[unit], k.use & 1u) || (n != 0 && !wait_w(&bars->pv_done[st][h], (n - 1) & 1u))) return false;
-        tc_fence_after();
-        const uint32_t k_lo = sdesc_lo(unit0 + unit * LY::kUnit, 16);
-        const uint32_t col = s_col + h * kHalf;
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(col, q_lo + step_k(kk, kAtomBytes), k_lo + step_k(kk, kHalfAtom), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
-          umma_commit(&bars->s_full[st][h]);
-          umma_commit(&bars->unit_empty[unit]);
-          if (h == 1 && i + kBy >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last scores of the item
+      const bool both = PAIR && it.rows1 > 0;
+      // A step of the stream: P V of block i (none before the first), then the scores of the block after it (none behind the
+      // last). What can be waited for and worked out before the turn comes is.
+      auto turn = [&](int i) {
+        const bool weigh = i >= i0, more = i + kBy < it.nblk;
+        const uint32_t v_unit = ring0 + v.at, k_unit = ring0 + k.at;
+        const uint32_t v_lo = __shfl_sync(0xffffffffu, sdesc_lo(unit0 + v_unit * LY::kTileBytes, kAtomBytes), 0);
+        const uint32_t k_lo = __shfl_sync(0xffffffffu, sdesc_lo(unit0 + k_unit * LY::kTileBytes, 16), 0);
+        const uint32_t acc0 = __shfl_sync(0xffffffffu, i > i0 ? 1u : 0u, 0);
+        if (more && !wait_w(&bars->unit_full[k_unit], k.use & 1u)) return false;
+        if (weigh) {
+          if (!wait_w(&bars->unit_full[v_unit], v.use & 1u)) return false;
+          if (!all_in(it.near, it.lo, it.hi, block_of(it, i) * kBlockN, kBlockN) && !wait_w(&bars->v_ok[v_unit], v.use & 1u)) return false;
+          if (!wait_w(&bars->p_full[st][1], used & 1u)) return false;
+          // the item's first product starts O anew: the warps of both streams have read it
+          if (!PAIR && items > 0 && i == i0 && !wait_w(&bars->o_free, (items - 1) & 1)) return false;
         }
-        __syncwarp();
-        return true;
-      };
-      auto issue_pv = [&](int i, uint32_t n, int h) {
-        const uint32_t unit = unit00 + v.at * 2 + h;
-        if (!wait_w(&bars->unit_full[unit], v.use & 1u)) return false;
-        const int j0 = block_of(it, i) * kBlockN + h * kHalf;
-        if (!all_in(it.near, it.lo, it.hi, j0, kHalf) && !wait_w(&bars->v_ok[unit], v.use & 1u)) return false;
-        if (!wait_w(&bars->p_full[st][h], n & 1u)) return false;
-        // the item's first product starts O anew: the warps of both streams have read it
-        if (!PAIR && items > 0 && i == i0 && h == 0 && !wait_w(&bars->o_free, (items - 1) & 1)) return false;
+        if (!my_turn(both)) return false;
         tc_fence_after();
-        const uint32_t v_lo = sdesc_lo(unit0 + unit * LY::kUnit, kHalfAtom);
-        const uint32_t col = s_col + h * kHalf;
-        const uint32_t acc0 = h > 0 ? 1u : __shfl_sync(0xffffffffu, i > i0 ? 1u : 0u, 0);
-        if (elect_one()) {
+        if (weigh) {
 #pragma unroll
-          for (int kk = 0; kk < kHalf / 16; ++kk)
-            umma_ts(o_col, col + kk * 8, v_lo + kk * kStepPV, kDescHi, idesc_pv, kk > 0 ? 1u : acc0);
-          umma_commit(&bars->pv_done[st][h]);
-          umma_commit(&bars->unit_empty[unit]);
+          for (int h = 1; h >= 0; --h) {  // the half whose weights come first
+            if (h == 0) {
+              if (!wait_w(&bars->p_full[st][0], used & 1u)) return false;
+              tc_fence_after();
+            }
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kHalf / 16; ++kk)
+                umma_ts(o_col, s_col + h * 64 + kk * 8, v_lo + (h * 4 + kk) * kStepPV, kDescHi, idesc_pv, h == 0 || kk > 0 ? 1u : acc0);
+              umma_commit(h == 1 ? &bars->pv_half[st] : &bars->pv_done[st]);
+              if (h == 0) umma_commit(&bars->unit_empty[v_unit]);
+            }
+            __syncwarp();
+          }
+          v.next();
+          ++used;
         }
-        __syncwarp();
+        if (more) {
+          if (used != 0 && !wait_w(&bars->pv_done[st], (used - 1) & 1u)) return false;  // the buffer's last P has been read
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              umma_ss(s_col, q_lo + step_k(kk), k_lo + step_k(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
+              // the other stream's products may queue up behind these
+              if (kk == D / 16 - 1 && both) mbar_arrive(&bars->turn[st ^ 1]);
+            }
+            umma_commit(&bars->s_full[st]);
+            umma_commit(&bars->unit_empty[k_unit]);
+            if (i + 2 * kBy >= it.nblk) umma_commit(&bars->q_empty);  // the stream's last scores of the item
+          }
+          __syncwarp();
+          k.next();
+        } else if (both && lane == 0) {
+          mbar_arrive(&bars->turn[st ^ 1]);
+        }
+        turns += both;
         return true;
       };
       ok = wait_w(&bars->q_full, items & 1);
       if (live) {
-        ok = ok && issue_qk(i0, used, 0) && issue_qk(i0, used, 1);
-        k.next();
 #pragma unroll 1
-        for (int i = i0; ok && i < it.nblk; i += kBy, ++used) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ok = ok && issue_pv(i, used, h);
-            if (i + kBy < it.nblk) ok = ok && issue_qk(i + kBy, used + 1, h);
-          }
-          if (i + kBy < it.nblk) k.next();
-          v.next();
-        }
+        for (int i = i0 - kBy; ok && i < it.nblk; i += kBy) ok = turn(i);
       } else {
         // Nothing of this item falls to the stream. (It leaves o_free alone: its next wait there comes after a P of its own,
         // and so after the join of this item, and that after the phase before.)
@@ -444,10 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 #pragma unroll 1
           for (int i = 0; ok && i < it.nblk; ++i) {
 #pragma unroll 1
-            for (int n = 0; ok && n < 4; ++n) {
-              const Place pl = n < 2 ? k : v;
-              ok = wait_w(&bars->unit_full[pl.at * 2 + (n & 1)], pl.use & 1u);
-              if (ok && lane == 0) mbar_arrive(&bars->unit_empty[pl.at * 2 + (n & 1)]);
+            for (int n = 0; ok && n < 2; ++n) {
+              const Place pl = n == 0 ? k : v;
+              ok = wait_w(&bars->unit_full[pl.at], pl.use & 1u);
+              if (ok && lane == 0) mbar_arrive(&bars->unit_empty[pl.at]);
             }
             k.next();
             v.next();
@@ -468,18 +497,18 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         const int j0 = block_of(it, i) * kBlockN;
         const int ring = ring_of(i);
 #pragma unroll 1
-        for (int n = 0; ok && n < 4; ++n) {
-          const Place pl = n < 2 ? (ring == 0 ? k0 : k1) : ring == 0 ? v0 : v1;
-          const int unit = (ring * LY::kRing + pl.at) * 2 + (n & 1), j = j0 + (n & 1) * kHalf;
+        for (int n = 0; ok && n < 2; ++n) {
+          const Place pl = n == 0 ? (ring == 0 ? k0 : k1) : ring == 0 ? v0 : v1;
+          const int unit = ring * LY::kRing + pl.at;
           ok = wait_w(&bars->unit_full[unit], pl.use & 1u);
           if (!ok) break;
-          if (n >= 2 && !all_in(it.near, it.lo, it.hi, j, kHalf)) {
-            const uint32_t base = smem_u32(smem + LY::kUnitOff) + unit * LY::kUnit;
+          if (n == 1 && !all_in(it.near, it.lo, it.hi, j0, kBlockN)) {
+            const uint32_t base = smem_u32(smem + LY::kUnitOff) + unit * LY::kTileBytes;
 #pragma unroll 1
-            for (int r = lane >> 3; r < kHalf; r += 4)  // eight lanes a row
-              if (!some_in(it.near, it.lo, it.hi, j + r, 1))
+            for (int r = lane >> 3; r < kBlockN; r += 4)  // eight lanes a row
+              if (!some_in(it.near, it.lo, it.hi, j0 + r, 1))
 #pragma unroll
-                for (int at = 0; at < LY::kAtoms; ++at) st_shared16(base + at * kHalfAtom + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
+                for (int at = 0; at < LY::kAtoms; ++at) st_shared16(base + at * kAtomBytes + r * 128 + (lane & 7) * 16, make_uint4(0, 0, 0, 0));
             fence_proxy_async_smem();
             __syncwarp();
           }
@@ -530,94 +559,99 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       if (!PAIR || rows > 0) {
 #pragma unroll 1
         for (int i = i0; ok && i < it.nblk; i += kBy, ++used) {
-          int j = block_of(it, i) * kBlockN;
-          uint32_t s_addr = tmem + lane_off + st * 128;
+          const int j = block_of(it, i) * kBlockN;
+          const uint32_t s_addr = tmem + lane_off + st * 128;
+          ok = wait_w(&bars->s_full[st], used & 1u);
+          if (!ok) break;
+          if (live) {
+            tc_fence_after();
+            // Two halves of 64 keys, the second first. P goes over the scores of its half, in bf16 as the products take it: each
+            // weight is off by 2^-8 of itself at most. Their sum is that of the fp32 weights.
+            const bool plain = __all_sync(0xffffffffu, !valid || all_in(it.near, r_lo, r_hi, j, kBlockN));
+            const uint64_t scale2 = pack_f32x2(s.scale_log2, s.scale_log2);
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h, s_addr += kHalf, j += kHalf) {
-            ok = wait_w(&bars->s_full[st][h], used & 1u);
-            if (!ok) break;
-            if (live) {
-              tc_fence_after();
-              uint32_t b0[32], b1[32];
-              EC_TMEM_LD32(s_addr, b0);
-              EC_TMEM_LD32(s_addr + 32, b1);
-              EC_TMEM_WAIT32(b0);
-              EC_TMEM_WAIT32(b1);
-              if (!__all_sync(0xffffffffu, !valid || all_in(it.near, r_lo, r_hi, j, kHalf))) {  // keys that the row does not see
-                auto below = [](int x) { return x <= 0 ? 0ull : x >= 64 ? ~0ull : (1ull << x) - 1; };
-                const uint64_t see = below(it.near - j) | (below(r_hi - j) & ~below(r_lo - j));
-                const uint32_t s0 = static_cast<uint32_t>(see), s1 = static_cast<uint32_t>(see >> 32);
+            for (int h = 1; h >= 0; --h) {
+              uint32_t x[2][32];
+              EC_TMEM_LD32(s_addr + 64 * h, x[0]);
+              EC_TMEM_LD32(s_addr + 64 * h + 32, x[1]);
+              EC_TMEM_WAIT32(x[0]);
+              EC_TMEM_WAIT32(x[1]);
+              if (!plain) {  // keys that the row does not see
+                auto below = [](int y) { return y <= 0 ? 0u : y >= 32 ? ~0u : (1u << y) - 1u; };
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  if (!((s0 >> e) & 1u)) b0[e] = __float_as_uint(-INFINITY);
-                  if (!((s1 >> e) & 1u)) b1[e] = __float_as_uint(-INFINITY);
+                for (int c = 0; c < 2; ++c) {
+                  const int jc = j + 64 * h + 32 * c;
+                  const uint32_t see = below(it.near - jc) | (below(r_hi - jc) & ~below(r_lo - jc));
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (!((see >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
                 }
               }
               // maximum (scale > 0 commutes with it), then p = 2^(s scale log2(e) - m)
               float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                m4[e & 2] = max3(m4[e & 2], __uint_as_float(b0[e]), __uint_as_float(b0[e + 1]));
-                m4[(e & 2) + 1] = max3(m4[(e & 2) + 1], __uint_as_float(b1[e]), __uint_as_float(b1[e + 1]));
+                m4[e & 2] = max3(m4[e & 2], __uint_as_float(x[0][e]), __uint_as_float(x[0][e + 1]));
+                m4[(e & 2) + 1] = max3(m4[(e & 2) + 1], __uint_as_float(x[1][e]), __uint_as_float(x[1][e + 1]));
               }
               const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * s.scale_log2;
-              bool rescale = false;
-              float alpha = 1.f;
-              if (i == i0 && h == 0) {
+              if (i == i0 && h == 1) {
                 m_used = mx;
-              } else if (mx > m_used + kRescaleLog2) {
-                alpha = ex2_approx(m_used - mx);
-                m_used = mx;
-                l_sum *= alpha;
-                rescale = true;
+              } else {
+                const bool rescale = mx > m_used + kRescaleLog2;
+                if (__any_sync(0xffffffffu, rescale)) {
+                  // O is at rest at a block's first half, as its scores came after the last P V; at its second half
+                  // the first one's P V may be under way
+                  if (h == 0) ok = wait_w(&bars->pv_half[st], used & 1u);
+                  if (!ok) break;
+                  tc_fence_after();
+                  const float alpha = rescale ? ex2_approx(m_used - mx) : 1.f;
+                  if (rescale) m_used = mx;
+                  l_sum *= alpha;
+#pragma unroll 1
+                  for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+                    EC_TMEM_WAIT32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    EC_TMEM_ST32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+                  }
+                }
               }
               // without a finite score so far, nothing is subtracted and p = 0
               const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-              const uint64_t scale2 = pack_f32x2(s.scale_log2, s.scale_log2), neg_m2 = pack_f32x2(neg_m, neg_m);
+              const uint64_t neg_m2 = pack_f32x2(neg_m, neg_m);
               uint64_t sum2[2] = {0, 0};
-              // P over the buffer's first 32 columns, in bf16 as the products take it: each weight is off by 2^-8 of
-              // itself at most. Their sum is that of the fp32 weights.
-              auto weights = [&](const uint32_t (&x)[32], int c) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                   float p0, p1;
-                  unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, neg_m2), p0, p1);
+                  unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), scale2, neg_m2), p0, p1);
                   p0 = ex2_approx(p0);
                   p1 = ex2_approx(p1);
                   sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
                   pk[e >> 1] = pack_bf16x2(p0, p1);
                 }
-                EC_TMEM_ST16(s_addr + c, pk);
-              };
-              weights(b0, 0);
-              weights(b1, 16);
-              float sum_lo, sum_hi;
-              unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
-              l_sum += sum_lo + sum_hi;
-              if (__any_sync(0xffffffffu, rescale)) {
-                // the half before this one may still be under way into O
-                ok = wait_w(&bars->pv_done[st][h ^ 1], (h ? used : used - 1) & 1u);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                  uint32_t o[32];
-                  EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
-                  EC_TMEM_WAIT32(o);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                  EC_TMEM_ST32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
-                }
+                EC_TMEM_ST16(s_addr + 64 * h + 16 * c, pk);
               }
               tmem_wait_st();
               tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->p_full[st][h]);
+              float sum_lo, sum_hi;
+              unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
+              l_sum += sum_lo + sum_hi;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[st][h]);
+            if (!ok) break;
+          } else if (lane == 0) {
+            mbar_arrive(&bars->p_full[st][0]);
+            mbar_arrive(&bars->p_full[st][1]);
           }
         }
-        if (ok && (PAIR || st < it.nblk)) ok = wait_w(&bars->pv_done[st][1], (used - 1) & 1u);
+        if (ok && (PAIR || st < it.nblk)) ok = wait_w(&bars->pv_done[st], (used - 1) & 1u);
       }
       const bool complete = it.part < 0;
       // slots of a CTA: [item goes on here, item begins here][tile]
