@@ -242,8 +242,9 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
     return cudaErrorInvalidValue;
   }
   if (few) {
-    e = launch_few_rows(a, p.D, ctas, s);
-    if (e == cudaSuccess)
+    const int cluster = few_rows_cluster(p, rows_max, window, sms);
+    e = launch_few_rows(a, p.D, ctas, cluster, s);
+    if (e == cudaSuccess && cluster == 0)
       e = launch_pdl(p.D == 64 ? merge_rows_kernel<64> : merge_rows_kernel<128>, dim3(ctas, rows_max * sh.g), dim3(32 * kMergeWarps), 0, s, a);
   } else {
     const int tiles = rows_max <= nr ? 1 : 2;

@@ -148,10 +148,11 @@ struct Group {
 };
 EC_DEV Group load_group(const Shape& s, int b, int grp, int step, bool tell) {
   Group q;
+  const int r0 = grp * step;  // below rows_max
+  const int64_t first = s.windowed ? raw_position(s.at, b, r0) : 0;
   sizes_of(s, b, tell, q.rows, q.n);
-  const int r0 = grp * step;
   q.rows = min(step, q.rows - r0);
-  q.h = q.rows > 0 ? hull_of(s, b, r0, r0 + q.rows, q.n) : Hull{0, 0, 0};
+  q.h = q.rows > 0 ? hull_of(s, b, r0, r0 + q.rows, q.n, first) : Hull{0, 0, 0};
   q.k = blocks_of(q.h, 7);
   q.blocks = q.rows > 0 ? max(1, q.k.count) : 0;  // rows without a key are written too
   return q;

@@ -69,9 +69,10 @@ EC_DEV void sizes_of(const Shape& s, int b, bool tell, int& rows, int& keys) {
 struct Hull {
   int near, lo, hi;
 };
-EC_DEV Hull hull_of(const Shape& s, int b, int r0, int r1, int n) {
+// first: the position of row r0, which a caller may ask for before it knows the sizes.
+EC_DEV Hull hull_of(const Shape& s, int b, int r0, int r1, int n, int64_t first) {
   if (!s.windowed) return {0, 0, n};
-  int64_t p0 = raw_position(s.at, b, r0), p1 = raw_position(s.at, b, r1 - 1);
+  int64_t p0 = first, p1 = r1 - 1 == r0 ? first : raw_position(s.at, b, r1 - 1);
   while (!inside(p0, s.L) && r0 + 1 < r1) p0 = raw_position(s.at, b, ++r0);  // rows at bad positions are not written
   while (!inside(p1, s.L) && r0 + 1 < r1) p1 = raw_position(s.at, b, --r1 - 1);
   if (!inside(p0, s.L) || !inside(p1, s.L)) return {0, 0, 0};
@@ -126,7 +127,9 @@ EC_DEV void st_shared16(uint32_t dst, uint4 v) {
 
 // attention_paged_rows.cu: at most kFewRows packed rows (positions times the heads of a KV head) a sequence.
 constexpr int kFewRows = 32;
-cudaError_t launch_few_rows(const Args& a, int D, int ctas, cudaStream_t s);
+// cluster 0: shares of the line, partial rows where items are cut; else a cluster of so many CTAs for each item.
+cudaError_t launch_few_rows(const Args& a, int D, int ctas, int cluster, cudaStream_t s);
+int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, int sms);
 // attention_paged_tiles.cu: tiles of nr positions, nr times the heads of a KV head at most 128 packed rows.
 constexpr int kTileRows = 128;
 cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, cudaStream_t s);
