@@ -248,15 +248,19 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
       e = launch_pdl(p.D == 64 ? merge_rows_kernel<64> : merge_rows_kernel<128>, dim3(ctas, rows_max * sh.g), dim3(32 * kMergeWarps), 0, s, a);
   } else {
     const int tiles = rows_max <= nr ? 1 : 2;
-    e = launch_tiles(a, p.D, nr, ctas, s);
+    const int cluster = tiles_cluster(p, rows_max, nr, window, sms);
+    e = launch_tiles(a, p.D, nr, ctas, cluster, s);
     // eight items or fewer may each go over many CTAs: their parts one column quad a thread
     const bool few_items = static_cast<int64_t>(p.B) * p.Hkv * ((rows_max + nr - 1) / nr) <= 8;
     const int quads = p.D / 32;  // of a thread that takes every eighth one
     const dim3 grid(ctas * tiles, kTileRows / 32, few_items ? quads : 1);
-    if (e == cudaSuccess && p.D == 64)
+    if (cluster != 0) {
+      // joined on the chip
+    } else if (e == cudaSuccess && p.D == 64) {
       e = launch_pdl(few_items ? merge_tiles_kernel<64, 1> : merge_tiles_kernel<64, 2>, grid, dim3(kTileMergeThreads), 0, s, a, tiles);
-    else if (e == cudaSuccess)
+    } else if (e == cudaSuccess) {
       e = launch_pdl(few_items ? merge_tiles_kernel<128, 1> : merge_tiles_kernel<128, 4>, grid, dim3(kTileMergeThreads), 0, s, a, tiles);
+    }
   }
   if (e == cudaSuccess) *status = EC_OK;
   return e;

@@ -94,17 +94,6 @@ EC_DEV void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-EC_DEV float4 ld_dsmem16(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-EC_DEV float2 ld_dsmem8(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-
 // CLUSTER: an item a cluster; else shares of the line.
 template <int D, int MT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_constant__ Args a) {
@@ -475,24 +464,24 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
 #pragma unroll 1
       for (int i = rank * kThreads + threadIdx.x; i < packed * (D / 8); i += S * kThreads) {
         const int x = i / (D / 8), c = i % (D / 8) * 8;
-        float2 st[8];
+        float2 st[kMaxCluster];
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
+        for (int r = 0; r < kMaxCluster; ++r) {
           st[r] = r < S ? ld_dsmem8(dsmem_map(smem_u32(&misc.stat[x]), r)) : make_float2(-INFINITY, 0.f);
           top = fmaxf(top, st[r].x);
         }
         const bool lost = st[0].x != st[0].x;
         float4 y[2] = {};
-        float4 z[8][2];
+        float4 z[kMaxCluster][2];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)  // all on the way at once
+        for (int r = 0; r < kMaxCluster; ++r)  // all on the way at once
           if (r < S) {
             const uint32_t src = dsmem_map(smem_u32(join + x * LY::kPitch + c), r);
             z[r][0] = ld_dsmem16(src), z[r][1] = ld_dsmem16(src + 16);
           }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
+        for (int r = 0; r < kMaxCluster; ++r) {
           if (r >= S) break;
           const float4 z0 = z[r][0], z1 = z[r][1];
           const float f = st[r].x == -INFINITY ? 1.f : ex2_approx(st[r].x - top);  // no finite score: zeros, or NaN
@@ -542,9 +531,7 @@ cudaError_t launch(const Args& a, int ctas, int cluster, cudaStream_t s) {
 
 }  // namespace
 
-namespace {
-// Clusters of S CTAs that are resident at once (an SM of a cluster holds one CTA, and a GPU part's SMs need not be a
-// multiple of S: 15 clusters of 8 on 152 SMs).
+// An SM of a cluster holds one CTA, and a GPU part's SMs need not be a multiple of S: 15 clusters of 8 on 152 SMs.
 int resident_clusters(int S) {
   int n = 0;
   const cudaError_t e = cached_per_device(
@@ -568,12 +555,11 @@ int resident_clusters(int S) {
       &S);
   return e == cudaSuccess ? n : 0;
 }
-}  // namespace
 
 int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, int sms) {
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
   if (items > sms) return 0;
-  int S = 8;
+  int S = kMaxCluster;
   while (S > 1 && resident_clusters(S) < items) --S;
   int64_t keys = scope_hi(p);
   if (w != nullptr) keys = std::min<int64_t>(keys, static_cast<int64_t>(w->left) + w->right + w->sinks + rows_max + 2 * kChunk);

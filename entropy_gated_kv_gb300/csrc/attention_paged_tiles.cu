@@ -20,7 +20,9 @@
 // Blocks are 128 keys, brought in by TMA: one box of 128 rows, or of a smaller page, from the page that the table
 // names. The blocks of all items (sequence, group of tiles, KV head) stand in one line of
 // which the CTAs, one an SM, take equal shares; an item cut between CTAs leaves fp32 partial rows, which a second
-// launch joins in a fixed order. A window leaves only the blocks that a group's rows see between them in the line.
+// launch joins in a fixed order. Where items of the split form are few, each goes to a cluster of up to eight CTAs
+// instead, a CTA an equal part of its blocks, joined over distributed shared memory: one launch and no line.
+// A window leaves only the blocks that a group's rows see between them.
 // Roles (12 warps):
 //   warp 0      plan, items, TMA producer        warps 4..7    softmax and epilogue of stream 0
 //   warps 1, 2  issuers of the two streams       warps 8..11   of stream 1
@@ -80,6 +82,8 @@ struct Layout {
   static constexpr int kRing = (PAIR ? 5 : 3) * (D == 128 ? 1 : 2);
   static constexpr int kPlaces = kRing * kRings;
   static constexpr int kUnitOff = (PAIR ? 2 : 1) * kTileBytes;
+  static constexpr int kJoinPitch = D * 4 + 16;  // bytes of a row for a cluster's join, over the places: 8 rows fall to all banks
+  static_assert(PAIR || kPlaces * kTileBytes >= kBlockM * kJoinPitch, "join");
   static constexpr int kStatOff = kUnitOff + kPlaces * kTileBytes;
   static constexpr int kItemOff = kStatOff + (PAIR ? 0 : 2 * kBlockM * 8);
   static constexpr int kBarOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
@@ -162,7 +166,8 @@ EC_DEV Group load_group(const Shape& s, int b, int grp, int step, bool tell) {
 EC_DEV bool all_in(int near, int lo, int hi, int j0, int count) { return j0 + count <= near || (j0 >= lo && j0 + count <= hi); }
 EC_DEV bool some_in(int near, int lo, int hi, int j0, int count) { return j0 < near || (j0 < hi && j0 + count > lo); }
 
-template <int D, bool PAIR>
+// CLUSTER (split form): an item a cluster; else shares of the line.
+template <int D, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Args a, int nr, int groups) {
   using LY = Layout<D, PAIR>;
   constexpr int kTiles = PAIR ? 2 : 1;
@@ -211,46 +216,59 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   pdl_wait();  // everything above overlaps the previous kernel
   pdl_launch_dependents();
 
-  // The line: each thread adds up the blocks of its (sequence, group) pairs, the CTA their sum, and the thread whose pairs
-  // hold the first block of this CTA's share finds it.
-  const int pairs = s.B * groups, per = (pairs + kThreads - 1) / kThreads, p0 = threadIdx.x * per;
-  int mine = 0, longest = 0;
+  int share = 0, left = 0, place[4] = {0, 0, 0, 0};  // the CTA's first item: sequence, group, KV head, block; blocks from there on
+  bool whole = false;
+  if constexpr (CLUSTER) {
+    const int item = blockIdx.x / cluster_size();
+    place[0] = item / s.Hkv, place[2] = item % s.Hkv;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  } else {
+    // The line: each thread adds up the blocks of its (sequence, group) pairs, the CTA their sum, and the thread whose pairs
+    // hold the first block of this CTA's share finds it.
+    const int pairs = s.B * groups, per = (pairs + kThreads - 1) / kThreads, p0 = threadIdx.x * per;
+    int mine = 0, longest = 0;
 #pragma unroll 2
-  for (int i = p0; i < min(p0 + per, pairs); ++i) {
-    const int b = i / groups, blocks = load_group(s, b, i - b * groups, step, blockIdx.x == 0).blocks;
-    mine += blocks * s.Hkv;
-    longest = max(longest, blocks);
-  }
-  int incl = warp_inclusive(mine);
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 31) bars->scan[warp] = incl, bars->most[warp] = longest;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) incl += bars->scan[w];
-    total += bars->scan[w];
-    longest = max(longest, bars->most[w]);
-  }
-  const int share = (total + gridDim.x - 1) / gridDim.x;
-  const int begin = blockIdx.x * share;
-  // Whole items, each to the CTA whose share holds its first block, where that costs little more than the cuts' partial
-  // rows do.
-  const bool whole = (share + longest - 1) / max(longest, 1) * longest <= share + kCutCost;
-  if (begin < total && begin >= incl - mine && begin < incl) {
-    int off = begin - (incl - mine);
-    for (int i = p0;; ++i) {
-      const int b = i / groups, blocks = load_group(s, b, i - b * groups, step, false).blocks;
-      if (off < blocks * s.Hkv) {
-        bars->begin[0] = b, bars->begin[1] = i - b * groups, bars->begin[2] = off / blocks, bars->begin[3] = off % blocks;
-        break;
-      }
-      off -= blocks * s.Hkv;
+    for (int i = p0; i < min(p0 + per, pairs); ++i) {
+      const int b = i / groups, blocks = load_group(s, b, i - b * groups, step, blockIdx.x == 0).blocks;
+      mine += blocks * s.Hkv;
+      longest = max(longest, blocks);
     }
+    int incl = warp_inclusive(mine);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) bars->scan[warp] = incl, bars->most[warp] = longest;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) incl += bars->scan[w];
+      total += bars->scan[w];
+      longest = max(longest, bars->most[w]);
+    }
+    share = (total + gridDim.x - 1) / gridDim.x;
+    const int begin = blockIdx.x * share;
+    // Whole items, each to the CTA whose share holds its first block, where that costs little more than the cuts' partial
+    // rows do.
+    whole = (share + longest - 1) / max(longest, 1) * longest <= share + kCutCost;
+    if (begin < total && begin >= incl - mine && begin < incl) {
+      int off = begin - (incl - mine);
+      for (int i = p0;; ++i) {
+        const int b = i / groups, blocks = load_group(s, b, i - b * groups, step, false).blocks;
+        if (off < blocks * s.Hkv) {
+          bars->begin[0] = b, bars->begin[1] = i - b * groups, bars->begin[2] = off / blocks, bars->begin[3] = off % blocks;
+          break;
+        }
+        off -= blocks * s.Hkv;
+      }
+    }
+    __syncthreads();
+    left = bars->begin[3] >= 0 ? min(share, total - begin) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) place[i] = bars->begin[i];
   }
-  __syncthreads();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort;
   auto wait_w = [&](uint64_t* bar, uint32_t parity) {  // whole warp
@@ -289,10 +307,19 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const int boxes = kBlockN / box;                   // boxes of a block's rows: 1, 2, 4 or 8
     const int atoms = box < kBlockN ? LY::kAtoms : 1;  // boxes beside each other
     if (lane < kTiles) a.records[blockIdx.x * kTiles + lane].parts = 0;
-    int left = bars->begin[3] >= 0 && !*abort_flag ? min(share, total - begin) : 0;
-    int b = bars->begin[0], grp = bars->begin[1], kvh = bars->begin[2], u = bars->begin[3];
+    int b = place[0], grp = place[1], kvh = place[2], u = place[3];
     Group g{};
-    if (left > 0) g = load_group(s, b, grp, step, false);
+    if constexpr (CLUSTER) {
+      const int S = cluster_size(), rank = cluster_ctarank();
+      g = load_group(s, b, 0, step, rank == 0 && kvh == 0 && lane == 0);
+      u = g.blocks * rank / S;
+      left = g.blocks * (rank + 1) / S - u;
+      if (lane == 0) bars->begin[0] = g.rows, bars->begin[1] = left;
+    } else {
+      if (lane < kTiles) a.records[blockIdx.x * kTiles + lane].parts = 0;
+      if (left > 0) g = load_group(s, b, grp, step, false);
+    }
+    if (*abort_flag) left = 0;
     auto next_group = [&]() {
       if (++kvh < s.Hkv) return;
       kvh = 0;
@@ -326,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         mbar_arrive(&bars->item_full[count % kItems]);
       }
       if (it.nblk == 0) break;
-      if (it.part == 1 && lane < kTiles) {  // the item begins here and goes on in the next CTAs
+      if (!CLUSTER && it.part == 1 && lane < kTiles) {  // the item begins here and goes on in the next CTAs
         const int rest = g.blocks - it.nblk;
         Record r{};
         r.rows = (lane == 0 ? it.rows0 : it.rows1) * s.g;
@@ -374,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       }
       left -= it.nblk;
       u = 0;
+      if (CLUSTER) left = 0;
       if (left > 0) next_group();
     }
   } else if (warp <= 2) {
@@ -654,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         }
         if (ok && (PAIR || st < it.nblk)) ok = wait_w(&bars->pv_done[st], (used - 1) & 1u);
       }
-      const bool complete = it.part < 0;
+      const bool complete = !CLUSTER && it.part < 0;
       // slots of a CTA: [item goes on here, item begins here][tile]
       const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (it.part > 0 ? 1 : 0)) * kTiles + (PAIR ? st : 0);
       uint16_t* const orow = a.out + ((static_cast<int64_t>(it.b) * s.rows_max + r) * s.Hq + it.kvh * s.g + (row - rl * s.g)) * D;
@@ -667,6 +695,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             *reinterpret_cast<uint4*>(orow + col + 8 * e) =
                 make_uint4(pack_bf16x2(y[8 * e], y[8 * e + 1]), pack_bf16x2(y[8 * e + 2], y[8 * e + 3]),
                            pack_bf16x2(y[8 * e + 4], y[8 * e + 5]), pack_bf16x2(y[8 * e + 6], y[8 * e + 7]));
+        } else if (CLUSTER && !complete) {
+          const uint32_t dst = smem_u32(smem + LY::kUnitOff) + row * LY::kJoinPitch + col * 4;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            st_shared16(dst + 16 * e, make_uint4(__float_as_uint(y[4 * e]), __float_as_uint(y[4 * e + 1]), __float_as_uint(y[4 * e + 2]), __float_as_uint(y[4 * e + 3])));
         } else if (!complete && valid) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -712,7 +745,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
           const float L = (has0 ? w0 * s0.y : 0.f) + (has1 ? w1 * s1.y : 0.f);
           const float norm = complete ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
           const float f0 = w0 * norm, f1 = w1 * norm;
-          if (!complete && st == 0 && valid) a.part_stat[slot * kBlockM + row] = make_float2(good ? M : kNotWritten(), L);
+          if (!complete && st == 0 && valid) {
+            const float2 mine = make_float2(good ? M : kNotWritten(), L);
+            if constexpr (CLUSTER) reinterpret_cast<float2*>(smem)[row] = mine;  // the queries have been read
+            else a.part_stat[slot * kBlockM + row] = mine;
+          }
 #pragma unroll 1
           for (int c = 0; c < D / 64; ++c) {
             uint32_t o0[32], o1[32];
@@ -749,22 +786,85 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if constexpr (CLUSTER) {
+    // the cluster's CTAs share out the tile's rows and read all parts of theirs
+    const int S = cluster_size(), rank = cluster_ctarank(), packed = bars->begin[0] * s.g;
+    if (bars->begin[1] == 0 && threadIdx.x < kBlockM) reinterpret_cast<float2*>(smem)[threadIdx.x] = make_float2(-INFINITY, 0.f);
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    const int x0 = packed * rank / S, n = (packed * (rank + 1) / S - x0) * (D / 4);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int x = x0 + i / (D / 4), c = i % (D / 4) * 4;
+      float2 st[kMaxCluster];
+      float4 z[kMaxCluster];
+      float top = -INFINITY, sum = 0.f;
+      bool lost = false;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        st[r] = make_float2(-INFINITY, 0.f);
+        z[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < S) {
+          st[r] = ld_dsmem8(dsmem_map(smem_u32(smem) + x * 8, r));
+          z[r] = ld_dsmem16(dsmem_map(smem_u32(smem + LY::kUnitOff) + x * LY::kJoinPitch + c * 4, r));
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        top = fmaxf(top, st[r].x);
+        lost = lost || st[r].x != st[r].x;
+      }
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (st[r].y == 0.f) continue;  // no weight; of a CTA without a block its rows hold anything
+        const float f = st[r].x == -INFINITY ? 1.f : ex2_approx(st[r].x - top);
+        sum += f * st[r].y;
+        o.x += f * z[r].x, o.y += f * z[r].y, o.z += f * z[r].z, o.w += f * z[r].w;
+      }
+      if (lost) continue;
+      const int r = s.by_g(x);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint2* dst = reinterpret_cast<uint2*>(
+          a.out + ((static_cast<int64_t>(place[0]) * s.rows_max + r) * s.Hq + place[2] * s.g + (x - r * s.g)) * D + c);
+      *dst = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    }
+    cluster_arrive_release();  // no CTA leaves while another one reads its rows
+    cluster_wait_acquire();
+  }
 }
 
-template <int D, bool PAIR>
-cudaError_t launch(const Args& a, int nr, int groups, int ctas, cudaStream_t s) {
-  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(tiles_kernel<D, PAIR>), Layout<D, PAIR>::kBytes);
+template <int D, bool PAIR, bool CLUSTER>
+cudaError_t launch(const Args& a, int nr, int groups, int ctas, int cluster, cudaStream_t s) {
+  constexpr int kBytes = Layout<D, PAIR>::kBytes;
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(tiles_kernel<D, PAIR, CLUSTER>), kBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tiles_kernel<D, PAIR>, dim3(ctas), dim3(kThreads), Layout<D, PAIR>::kBytes, s, a, nr, groups);
+  if constexpr (CLUSTER)
+    return launch_pdl_cluster(tiles_kernel<D, PAIR, CLUSTER>, dim3(a.s.B * a.s.Hkv * cluster), dim3(kThreads), kBytes, cluster, s, a, nr, groups);
+  return launch_pdl(tiles_kernel<D, PAIR, CLUSTER>, dim3(ctas), dim3(kThreads), kBytes, s, a, nr, groups);
 }
 
 }  // namespace
 
-cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, cudaStream_t s) {
-  const int tiles = (a.s.rows_max + nr - 1) / nr;
-  if (tiles == 1) return D == 64 ? launch<64, false>(a, nr, 1, ctas, s) : launch<128, false>(a, nr, 1, ctas, s);
-  const int groups = (tiles + 1) / 2;
-  return D == 64 ? launch<64, true>(a, nr, groups, ctas, s) : launch<128, true>(a, nr, groups, ctas, s);
+int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, int sms) {
+  const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
+  if (rows_max > nr || items > sms) return 0;
+  int S = kMaxCluster;
+  while (S > 1 && resident_clusters(S) < items) --S;
+  int64_t keys = scope_hi(p);
+  if (w != nullptr) keys = std::min<int64_t>(keys, static_cast<int64_t>(w->left) + w->right + w->sinks + rows_max + 2 * kBlockN);
+  const int64_t blocks = (keys + kBlockN - 1) / kBlockN;
+  return (blocks + S - 1) / S <= (items * blocks + sms - 1) / sms + kCutCost ? S : 0;
+}
+
+cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, int cluster, cudaStream_t s) {
+  const int groups = ((a.s.rows_max + nr - 1) / nr + 1) / 2;
+  const bool pair = a.s.rows_max > nr;
+  if (D == 64)
+    return pair ? launch<64, true, false>(a, nr, groups, ctas, 0, s)
+                : cluster ? launch<64, false, true>(a, nr, 1, 0, cluster, s) : launch<64, false, false>(a, nr, 1, ctas, 0, s);
+  return pair ? launch<128, true, false>(a, nr, groups, ctas, 0, s)
+              : cluster ? launch<128, false, true>(a, nr, 1, 0, cluster, s) : launch<128, false, false>(a, nr, 1, ctas, 0, s);
 }
 
 }  // namespace paged

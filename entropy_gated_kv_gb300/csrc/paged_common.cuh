@@ -121,6 +121,16 @@ EC_DEV uint4 ld_shared16(uint32_t src) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
   return v;
 }
+EC_DEV float4 ld_dsmem16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+EC_DEV float2 ld_dsmem8(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
 EC_DEV void st_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -129,10 +139,13 @@ EC_DEV void st_shared16(uint32_t dst, uint4 v) {
 constexpr int kFewRows = 32;
 // cluster 0: shares of the line, partial rows where items are cut; else a cluster of so many CTAs for each item.
 cudaError_t launch_few_rows(const Args& a, int D, int ctas, int cluster, cudaStream_t s);
+constexpr int kMaxCluster = 8;
+int resident_clusters(int S);  // clusters of S CTAs, one an SM, that are on the device at once
 int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, int sms);
 // attention_paged_tiles.cu: tiles of nr positions, nr times the heads of a KV head at most 128 packed rows.
 constexpr int kTileRows = 128;
-cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, cudaStream_t s);
+cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, int cluster, cudaStream_t s);
+int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, int sms);
 // A CTA leaves two cut items at most, one that goes on in it and one that begins there: slots
 // 2 tiles cta + tile and 2 tiles cta + tiles + tile, with one tile or two beside each other.
 EC_DEV int64_t part_slot(int first_cta, int i, int tiles, int tile) {
