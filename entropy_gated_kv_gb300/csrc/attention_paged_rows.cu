@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
     prefetch_tmap(&a.tk);
     prefetch_tmap(&a.tv);
   }
+  prefetch_small(s, kThreads);
   pdl_wait();  // everything may come from the previous kernels in the stream
   pdl_launch_dependents();
 

@@ -10,7 +10,7 @@
 //     a byte brought to shared memory feeds 256 rows;
 //   - split (every sequence has one tile): the streams take the even and the odd key blocks of the tile and are
 //     joined at the item's end.
-// In the pair form the streams take turns at the tensor cores, P V and next scores in one piece: left to themselves they
+// The streams take turns at the tensor cores, P V and next scores in one piece: left to themselves they
 // fall into step, both in the softmax, then both at the tensor cores (3820 cycles a pair of blocks for 3300; 4 full steps
 // of 2048 rows, 28/4 heads, 210 us for 182). What a pair of blocks is bound by: a stream's own chain, softmax 1700
 // cycles (64 exponentials of a row take a lone warp 490, two warps of a scheduler 590 together), P V and scores 1000, and
@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  prefetch_small(s, kThreads);
   pdl_wait();  // everything above overlaps the previous kernel
   pdl_launch_dependents();
 
@@ -417,10 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     uint32_t used = 0;    // blocks of this stream whose P V is under way or done
     Place k{0, 0}, v{1, 0};  // of the next scores, of the next P V
     const uint32_t ring0 = PAIR ? 0 : st * LY::kRing;
-    // Turns of the pair form: a stream's P V and next scores go out in one piece, by turns with the other stream's.
+    // Turns: a stream's P V and next scores go out in one piece, by turns with the other stream's.
     uint32_t turns = 0;
-    auto my_turn = [&](bool both) {
-      if (!both) return true;
+    auto my_turn = [&](bool by_turns) {
+      if (!by_turns) return true;
       const uint32_t n = turns + st;  // stream 0's first turn waits for nothing
       return n == 0 || wait_w(&bars->turn[st], (n - 1) & 1u);
     };
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       if (it.nblk == 0) break;
       const bool live = PAIR ? (st == 0 || it.rows1 > 0) : static_cast<int>(st) < it.nblk;
       const int i0 = PAIR ? 0 : st;
-      const bool both = PAIR && it.rows1 > 0;
+      const bool by_turns = !PAIR || it.rows1 > 0;  // else stream 0 is alone
       // A step of the stream: P V of block i (none before the first), then the scores of the block after it (none behind the
       // last). What can be waited for and worked out before the turn comes is.
       auto turn = [&](int i) {
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
           // the item's first product starts O anew: the warps of both streams have read it
           if (!PAIR && items > 0 && i == i0 && !wait_w(&bars->o_free, (items - 1) & 1)) return false;
         }
-        if (!my_turn(both)) return false;
+        if (!my_turn(by_turns)) return false;
         tc_fence_after();
         if (weigh) {
 #pragma unroll
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             for (int kk = 0; kk < D / 16; ++kk) {
               umma_ss(s_col, q_lo + step_k(kk), k_lo + step_k(kk), kDescHi, idesc_qk, kk > 0 ? 1u : 0u);
               // the other stream's products may queue up behind these
-              if (kk == D / 16 - 1 && both) mbar_arrive(&bars->turn[st ^ 1]);
+              if (kk == D / 16 - 1 && by_turns) mbar_arrive(&bars->turn[st ^ 1]);
             }
             umma_commit(&bars->s_full[st]);
             umma_commit(&bars->unit_empty[k_unit]);
@@ -484,10 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
           }
           __syncwarp();
           k.next();
-        } else if (both && lane == 0) {
+        } else if (by_turns && lane == 0) {
           mbar_arrive(&bars->turn[st ^ 1]);
         }
-        turns += both;
+        turns += by_turns;
         return true;
       };
       ok = wait_w(&bars->q_full, items & 1);
@@ -510,6 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             k.next();
             v.next();
           }
+        }
+      }
+      if (!PAIR && st == 1) {  // as many turns as stream 0, whose blocks may be one more
+#pragma unroll 1
+        for (int e = live ? it.nblk & 1 : 2; ok && e > 0; --e, ++turns) {
+          ok = my_turn(true);
+          if (ok && lane == 0) mbar_arrive(&bars->turn[0]);
         }
       }
       if (lane == 0) mbar_arrive(&bars->item_empty[items % kItems]);

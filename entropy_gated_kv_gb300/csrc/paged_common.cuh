@@ -107,6 +107,22 @@ EC_DEV int page_of(const Shape& s, int b, int j) {
   return s.n_pages;
 }
 
+// Sizes, page numbers and first positions into L2, each line by one thread of the grid, before the wait for the kernel in
+// front: a prefetch into L2, where that kernel's writes go too, reads nothing stale. The chain of sizes, first
+// position, page number, keys has a DRAM access less at each step.
+EC_DEV void prefetch_lines(const void* p, int64_t bytes, int64_t line) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p) / 128 * 128 + line * 128;
+  if (at < reinterpret_cast<uintptr_t>(p) + bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(at) : "memory");
+}
+EC_DEV void prefetch_small(const Shape& s, int threads) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * threads + threadIdx.x;
+  prefetch_lines(s.R, s.B * 4ll, i);
+  if (s.kv_len != nullptr) prefetch_lines(s.kv_len, s.B * 4ll, i);
+  prefetch_lines(s.table, ((s.B - 1) * s.table_stride + ((s.L + (1 << s.page_shift) - 1) >> s.page_shift)) * 4, i);
+  if (s.windowed && s.at.idx != nullptr && i < s.B) prefetch_lines(s.at.idx + i * s.at.stride, 4, 0);
+  if (s.windowed && s.at.start != nullptr) prefetch_lines(s.at.start, s.B * 4ll, i);
+}
+
 EC_DEV int warp_inclusive(int x) {
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {

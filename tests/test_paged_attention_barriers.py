@@ -87,7 +87,7 @@ class Cta:
             live = (st == 0 or two) if self.pair else st < nblk
             i0 = 0 if self.pair else st
 
-            both = self.pair and two
+            by_turns = not self.pair or two
             yield self.q_full, n
             if live:
                 for i in range(i0 - by, nblk, by):
@@ -101,7 +101,7 @@ class Cta:
                         yield self.p_full[st][1], used
                         if not self.pair and n > 0 and i == i0:
                             yield self.o_free, n - 1
-                    if both and turns + st:
+                    if by_turns and turns + st:
                         yield self.turn[st], turns + st - 1
                     if i >= i0:
                         self.products[st].append(self.pv_half[st])
@@ -116,7 +116,7 @@ class Cta:
                         self.products[st] += [self.s_full[st], self.empty[r][line[i + by][2][0][0]]]
                         if i + 2 * by >= nblk:
                             self.products[st].append(self.q_empty)
-                    if both:
+                    if by_turns:
                         self.turn[st ^ 1].arrive()
                         turns += 1
                     yield None
@@ -129,6 +129,11 @@ class Cta:
                             yield self.full[r][u], use
                             self.empty[r][u].arrive()
                             yield None
+            if not self.pair and st == 1:
+                for _ in range(nblk % 2 if live else 2):
+                    yield self.turn[1], turns
+                    self.turn[0].arrive()
+                    turns += 1
             self.item_empty[n % ITEMS].arrive()
             yield None
 
