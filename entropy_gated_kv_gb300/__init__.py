@@ -544,11 +544,12 @@ def prefix_attention(p: Params, q, prefix, cache, R, out, kv_len=None, scale: fl
 class _Pages:
     """The checked C view (ec_paged_kv) of a paged cache."""
 
-    __slots__ = ("c", "ref", "index", "heads", "B", "positions", "at")
+    __slots__ = ("c", "ref", "index", "heads", "B", "positions", "at", "shape", "strides", "table_shape")
 
     def __init__(self, k, v, table):
         self.index = _cuda_index(k, "k")
-        self.at = self.key(k, v, table)
+        self.at, self.shape, self.table_shape = (k.data_ptr(), v.data_ptr(), table.data_ptr()), k.shape, table.shape
+        self.strides = (k.stride(), v.stride(), table.stride())
         if k.dim() != 4 or 0 in k.shape:
             raise ValueError(f"a pool is [n_pages, page_size, Hkv, D], got {list(k.shape)}")
         n, ps, H, D = k.shape
@@ -572,11 +573,11 @@ class _Pages:
         self.c = C.EcPagedKv(ps, n, stride, k.data_ptr(), v.data_ptr(), table.data_ptr(), row)
         self.ref = ctypes.byref(self.c)
 
-    @staticmethod
-    def key(k, v, t):
-        """What the view was made of: addresses alone do not tell a tensor that was changed in place."""
-        return (k.data_ptr(), v.data_ptr(), t.data_ptr(), k.shape, v.shape, t.shape, k.stride(), v.stride(), t.stride(), k.dtype, v.dtype,
-                t.dtype)
+    def holds(self, k, v, t) -> bool:
+        """Whether the view is still that of these tensors. Addresses alone do not tell: one that was resized,
+        restrided or given other data in place may lie where it lay."""
+        return (self.at == (k.data_ptr(), v.data_ptr(), t.data_ptr()) and k.shape == self.shape == v.shape and t.shape == self.table_shape
+                and self.strides == (k.stride(), v.stride(), t.stride()) and k.dtype is v.dtype is torch.bfloat16 and t.dtype is torch.int32)
 
 
 class PagedCache:
@@ -599,7 +600,7 @@ class PagedCache:
     def view(self) -> _Pages:
         """The checked C view; made and checked again when a tensor is not what it was."""
         c, k, v, t = self._c, self.k, self.v, self.table
-        if c is None or c.at != _Pages.key(k, v, t):
+        if c is None or not c.holds(k, v, t):
             c = _Pages(k, v, t)
             object.__setattr__(self, "_c", c)
         return c
@@ -621,16 +622,17 @@ def _pages_of(p: Params, cache: PagedCache) -> _Pages:
     return c
 
 
-def _row_view(t, name: str, heads: int, p: Params, rows: int, index: int):
-    """byref of the ec_rows of t, bf16 [B, rows, heads, D] with adjacent heads."""
-    if t.dtype is not torch.bfloat16 or t.shape != (p.B, rows, heads, p.D):
-        raise ValueError(f"{name} must be bf16 {[p.B, rows, heads, p.D]}, got {t.dtype} {list(t.shape)}")
+def _row_view(t, name: str, shape: tuple, index: int) -> tuple:
+    """The fields of the ec_rows of t, bf16 of that shape [B, rows, heads, D] with adjacent heads."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape:
+        raise ValueError(f"{name} must be bf16 {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}: EntropyCache kernels take CUDA tensors, all of one device")
+    B, rows, heads, D = shape
     sb, sr, sh, sd = t.stride()
-    if (sd != 1 and p.D > 1) or (sh != p.D and heads > 1):
+    if sd != 1 or (sh != D and heads > 1):
         raise ValueError(f"the heads of a row of {name} must be adjacent")
-    return ctypes.byref(C.EcRows(t.data_ptr(), sb if p.B > 1 else 0, sr if rows > 1 else heads * p.D))
+    return t.data_ptr(), (sb if B > 1 else 0), (sr if rows > 1 else heads * D)
 
 
 def _places(p: Params, idx, start, rows: int, index: int):
@@ -639,11 +641,13 @@ def _places(p: Params, idx, start, rows: int, index: int):
         return None, 0, _opt(start, "start", torch.int32, (p.B,), index)
     if start is not None:
         raise ValueError("idx and start exclude each other")
-    if idx.dtype is not torch.int32 or idx.dim() != 2 or idx.shape[0] != p.B or idx.shape[1] < rows or idx.get_device() != index:
-        raise ValueError(f"idx must be int32 [{p.B}, {rows} or more] on cuda:{index}, got {idx.dtype} {list(idx.shape)} on {idx.device}")
-    if idx.shape[1] > 1 and idx.stride(1) != 1:
+    n = idx.shape
+    if idx.dtype is not torch.int32 or len(n) != 2 or n[0] != p.B or n[1] < rows or idx.get_device() != index:
+        raise ValueError(f"idx must be int32 [{p.B}, {rows} or more] on cuda:{index}, got {idx.dtype} {list(n)} on {idx.device}")
+    s0, s1 = idx.stride()
+    if s1 != 1 and n[1] > 1:
         raise ValueError("a sequence's idx must be contiguous")
-    return idx.data_ptr(), (idx.stride(0) if p.B > 1 else idx.shape[1]), None
+    return idx.data_ptr(), (s0 if n[0] > 1 else n[1]), None
 
 
 def kv_append_paged(p: Params, cache: PagedCache, k_new, v_new, R, idx=None, start=None, rope=None, q_new=None, q_out=None,
@@ -655,28 +659,38 @@ def kv_append_paged(p: Params, cache: PagedCache, k_new, v_new, R, idx=None, sta
     [L, D / 2], None: rows are copied. Returns q_out, a new tensor of zeros by default. See
     ec_kv_append_paged."""
     c = _pages_of(p, cache)
-    i, rows = c.index, k_new.shape[1]
-    kr, vr = _row_view(k_new, "k_new", p.Hkv, p, rows, i), _row_view(v_new, "v_new", p.Hkv, p, rows, i)
-    if q_new is None and q_out is not None:
-        raise ValueError("q_out without q_new")
-    qr = None if q_new is None else _row_view(q_new, "q_new", p.Hq, p, rows, i)
-    rp = _checked(R, "R", torch.int32, (p.B,), i)
+    i, B, rows, D = c.index, p.B, k_new.shape[1], p.D
+    shape = (B, rows, p.Hkv, D)
+    kv = _row_view(k_new, "k_new", shape, i) + _row_view(v_new, "v_new", shape, i)
+    if q_new is None:
+        if q_out is not None:
+            raise ValueError("q_out without q_new")
+        x = C.EcRows3(*kv)
+        at = ctypes.addressof(x)
+        qr = op = None
+    else:
+        shape = (B, rows, p.Hq, D)
+        x = C.EcRows3(*kv, *_row_view(q_new, "q_new", shape, i))
+        at = ctypes.addressof(x)
+        qr, op = at + 48, None if q_out is None else _checked(q_out, "q_out", torch.bfloat16, shape, i)
+    rp = _checked(R, "R", torch.int32, (B,), i)
     ip, si, sp = _places(p, idx, start, rows, i)
     cs = sn = None
     if rope is not None:
-        cs, sn = (_checked(t, n, torch.float32, (p.L, p.D // 2), i) for t, n in zip(rope, ("cos", "sin")))
-    ep = _opt(dev_err, "dev_err", torch.int32, (1,), i)
-    op = None if q_out is None else _checked(q_out, "q_out", torch.bfloat16, (p.B, rows, p.Hq, p.D), i)
+        cs, sn = rope
+        shape = (p.L, D // 2)
+        cs, sn = _checked(cs, "cos", torch.float32, shape, i), _checked(sn, "sin", torch.float32, shape, i)
+    ep = None if dev_err is None else _checked(dev_err, "dev_err", torch.int32, (1,), i)
     f = lib().ec_kv_append_paged
     if stream is None and (op is not None or qr is None) and torch._C._cuda_getDevice() == i:
-        st = f(p.ref(), c.ref, rows, kr, vr, qr, op, cs, sn, ip, si, sp, rp, ep, torch._C._cuda_getCurrentRawStream(i))
+        st = f(p.ref(), c.ref, rows, at, at + 24, qr, op, cs, sn, ip, si, sp, rp, ep, torch._C._cuda_getCurrentRawStream(i))
     else:
         def call(s):
             nonlocal q_out
             if q_new is not None and q_out is None:
-                q_out = torch.zeros(p.B, rows, p.Hq, p.D, dtype=torch.bfloat16, device=q_new.device)
+                q_out = torch.zeros(B, rows, p.Hq, D, dtype=torch.bfloat16, device=q_new.device)
             o = None if q_out is None else q_out.data_ptr()
-            return f(p.ref(), c.ref, rows, kr, vr, qr, o, cs, sn, ip, si, sp, rp, ep, s)
+            return f(p.ref(), c.ref, rows, at, at + 24, qr, o, cs, sn, ip, si, sp, rp, ep, s)
 
         st = _launch(i, stream, call)
     C.check(st, "ec_kv_append_paged")
@@ -690,34 +704,37 @@ def paged_attention_workspace_size(p: Params, rows: int) -> int:
 
 def _attend_paged(p: Params, q, cache, R, out, places, window, kv_len, scale, ws, dev_err, stream):
     c = _pages_of(p, cache)
-    i = c.index
+    i, B = c.index, p.B
     if q.dim() != 4:
         raise ValueError(f"q must be [B, rows, Hq, D], got {list(q.shape)}")
     rows = q.shape[1]
-    shape = (p.B, rows, p.Hq, p.D)
+    shape = (B, rows, p.Hq, p.D)
     qp = _checked(q, "q", torch.bfloat16, shape, i)
     op = _checked(out, "out", torch.bfloat16, shape, i)
-    rp = _checked(R, "R", torch.int32, (p.B,), i)
-    lp = _opt(kv_len, "kv_len", torch.int32, (p.B,), i)
-    ep = _opt(dev_err, "dev_err", torch.int32, (1,), i)
+    shape = (B,)
+    rp = _checked(R, "R", torch.int32, shape, i)
+    lp = None if kv_len is None else _checked(kv_len, "kv_len", torch.int32, shape, i)
+    ep = None if dev_err is None else _checked(dev_err, "dev_err", torch.int32, (1,), i)
     if ws is not None and (ws.get_device() != i or not ws.is_contiguous()):
         raise ValueError(f"ws must be a contiguous tensor on {q.device}")
-    sc = (1.0 / math.sqrt(p.D)) if scale is None else float(scale)
+    sc = p.D**-0.5 if scale is None else float(scale)
     if window is None:
-        what, where = "ec_paged_attention", ()
+        what, f = "ec_paged_attention", lib().ec_paged_attention
+        a = (p.ref(), rows, qp, c.ref, rp, lp, sc, op)
     else:
-        what, where = "ec_paged_window_attention", _places(p, *places, rows, i)
-    f = getattr(lib(), what)
+        what, f = "ec_paged_window_attention", lib().ec_paged_window_attention
+        a = (p.ref(), rows, qp, c.ref, *_places(p, *places, rows, i), rp, lp, *window, sc, op)
+    if ws is not None and stream is None and torch._C._cuda_getDevice() == i:
+        st = f(*a, ws.data_ptr(), ws.nbytes, ep, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        def call(s):
+            w = ws
+            if w is None:
+                w = torch.empty(max(256, paged_attention_workspace_size(p, rows)), dtype=torch.uint8, device=q.device)
+            return f(*a, w.data_ptr(), w.nbytes, ep, s)
 
-    def call(s):
-        w = ws
-        if w is None:
-            w = torch.empty(max(256, paged_attention_workspace_size(p, rows)), dtype=torch.uint8, device=q.device)
-        if window is None:
-            return f(p.ref(), rows, qp, c.ref, rp, lp, sc, op, w.data_ptr(), w.nbytes, ep, s)
-        return f(p.ref(), rows, qp, c.ref, *where, rp, lp, *window, sc, op, w.data_ptr(), w.nbytes, ep, s)
-
-    C.check(_launch(i, stream, call), what)
+        st = _launch(i, stream, call)
+    C.check(st, what)
     return out
 
 

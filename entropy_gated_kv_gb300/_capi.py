@@ -74,6 +74,12 @@ class EcRows(ctypes.Structure):
     _fields_ = [("x", _p), ("batch_stride", _i64), ("row_stride", _i64)]
 
 
+class EcRows3(ctypes.Structure):
+    """Three ec_rows behind one another."""
+
+    _fields_ = [(f"{n}{i}", t) for i in range(3) for n, t in EcRows._fields_]
+
+
 # name -> (restype, argtypes)
 SIGNATURES: dict[str, tuple] = {
     "ec_status_string": (ctypes.c_char_p, [_i32]),
