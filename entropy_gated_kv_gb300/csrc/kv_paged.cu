@@ -4,7 +4,9 @@
 // of a pool and the rotation beside the write have no counterpart there. For row r < R[b] at position pos:
 //   K page row (b, pos) = rotate(k_new[b, r], pos), V page row = v_new[b, r], q_out[b, r] = rotate(q_new[b, r], pos)
 //   rotate: (x_i, x_{i + D/2}) -> (x_i c_i - x_{i + D/2} s_i, x_{i + D/2} c_i + x_i s_i), fp32, rounded once.
-// HBM-bound: every row is read and written once, 4 (Hq + 2 Hkv) D bytes, beside 4 D bytes of the angles' table.
+// HBM-bound: every row is read and written once, 4 (Hq + 2 Hkv) D bytes, beside 4 D bytes of the angles' table; a short
+// call by its chain of loads (sizes, rows and positions, page numbers and angles). Loading the rows beside the sizes took
+// 0.2 us off that, and registers that cost the long call 30.
 #include <algorithm>
 
 #include "ec_common.cuh"
@@ -15,8 +17,11 @@ namespace ec {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kInFlight = 3;  // 32-byte pieces that a thread loads before it stores any
+// Threads of a CTA, and 32-byte pieces that a thread loads before it stores any. 4 x 4096 rows of 32 heads: 123 us (6.6
+// TB/s) so, 139 with 256 x 3, 138 with 256 x 2, 122 with 128 x 3; 8 x 95 rows of 28/4 heads: 4.9 us, 5.8, 5.0, 5.3: smaller
+// CTAs mix loads and stores of more rows on an SM, larger ones start fewer for a short call.
+constexpr int kThreads = 192;
+constexpr int kInFlight = 2;
 
 struct AppendArgs {
   int32_t L, Hq, Hkv, rows_max, page_shift, n_pages, pieces, rows_per_cta;
