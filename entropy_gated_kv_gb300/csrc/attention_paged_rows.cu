@@ -1,4 +1,4 @@
-// attention_paged_rows.cu — attention over a paged K/V cache for few rows: single tokens and short blocks, at most 32
+// attention_paged_rows.cu — attention over a paged K/V cache for few rows: single tokens and short blocks, at most 16
 // packed rows (a sequence's positions times the g query heads of a KV head).
 //
 //   out[x] = sum_j p_xj v_j / sum_j p_xj, p_xj = 2^(s_xj - m_x), s_xj = scale log2(e) <q_x, k_j>, m_x a running maximum
@@ -38,15 +38,15 @@ struct Misc {
   int scan[kWarps];
   Place begin;
   int share, abort;
-  float2 stat[2 * 16];  // of the CTA's rows, for its cluster
+  float2 stat[kFewRows];  // of the CTA's rows, for its cluster
 };
 
-template <int D, int MT>
+template <int D>
 struct Layout {
   static constexpr int kKBytes = kChunk * D * 2;  // a K or V chunk: [D / 64][16][64], 128-byte swizzle
   static constexpr int kStage = 2 * kKBytes;
-  static constexpr int kStages = D == 64 ? 5 : MT == 1 ? 3 : 2;  // chunks in flight a warp
-  static constexpr int kRows = 16 * MT;
+  static constexpr int kStages = D == 64 ? 5 : 3;  // chunks in flight a warp
+  static constexpr int kRows = kFewRows;
   static constexpr int kPitch = D + 4;  // floats of a row in the join's buffers: two rows in 8 share a bank
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kJoinOff = kRing;
@@ -95,9 +95,9 @@ EC_DEV void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 }
 
 // CLUSTER: an item a cluster; else shares of the line.
-template <int D, int MT, bool CLUSTER>
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_constant__ Args a) {
-  using LY = Layout<D, MT>;
+  using LY = Layout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& misc = *reinterpret_cast<Misc*>(smem + LY::kMiscOff);
   const Shape& s = a.s;
@@ -132,40 +132,40 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
     at.left = (lim - base + kWarps - 1) / kWarps;
     __syncthreads();  // the barriers are up
   } else {
-  // The line: each thread adds up the units of its sequences, the CTA their sum, and the thread whose sequences hold the
-  // first unit of this CTA's share finds it.
-  const int per = (s.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
-  int mine = 0;
-  for (int b = b0; b < min(b0 + per, s.B); ++b) mine += load_seq(s, b, blockIdx.x == 0).units * s.Hkv;
-  int incl = warp_inclusive(mine);
-  if (lane == 31) misc.scan[warp] = incl;
-  __syncthreads();
-  int total = 0;
+    // The line: each thread adds up the units of its sequences, the CTA their sum, and the thread whose sequences hold the
+    // first unit of this CTA's share finds it.
+    const int per = (s.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
+    int mine = 0;
+    for (int b = b0; b < min(b0 + per, s.B); ++b) mine += load_seq(s, b, blockIdx.x == 0).units * s.Hkv;
+    int incl = warp_inclusive(mine);
+    if (lane == 31) misc.scan[warp] = incl;
+    __syncthreads();
+    int total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) incl += misc.scan[w];
-    total += misc.scan[w];
-  }
-  const int share = (total + gridDim.x - 1) / gridDim.x;
-  const int begin = blockIdx.x * share;
-  if (begin < total && begin >= incl - mine && begin < incl) {
-    int off = begin - (incl - mine);
-    for (int b = b0;; ++b) {
-      const int units = load_seq(s, b, false).units;
-      if (off < units * s.Hkv) {
-        misc.begin = {b, off / units, off % units, min(share, total - begin)};
-        break;
-      }
-      off -= units * s.Hkv;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) incl += misc.scan[w];
+      total += misc.scan[w];
     }
-  }
-  if (threadIdx.x == 0) misc.share = share;
-  __syncthreads();
-  if (threadIdx.x == 0) a.records[blockIdx.x].parts = 0;
-  at = misc.begin;
-  if (at.left == 0 || misc.abort) return;
-  cs = load_seq(s, at.b, false);
-  lim = cs.chunks;
+    const int share = (total + gridDim.x - 1) / gridDim.x;
+    const int begin = blockIdx.x * share;
+    if (begin < total && begin >= incl - mine && begin < incl) {
+      int off = begin - (incl - mine);
+      for (int b = b0;; ++b) {
+        const int units = load_seq(s, b, false).units;
+        if (off < units * s.Hkv) {
+          misc.begin = {b, off / units, off % units, min(share, total - begin)};
+          break;
+        }
+        off -= units * s.Hkv;
+      }
+    }
+    if (threadIdx.x == 0) misc.share = share;
+    __syncthreads();
+    if (threadIdx.x == 0) a.records[blockIdx.x].parts = 0;
+    at = misc.begin;
+    if (at.left == 0 || misc.abort) return;
+    cs = load_seq(s, at.b, false);
+    lim = cs.chunks;
   }
 
   // ---- loads: the warp's chunks in the line's order, kStages of them ahead
@@ -228,39 +228,35 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
     const int u1 = CLUSTER ? at.left : min(cs.units, at.u + at.left);
     const int packed = cs.rows * s.g;
     // the rows of this thread's fragments: their queries, and the keys that they see
-    uint32_t qf[MT][D / 16][4];
-    int r_lo[MT][2], r_hi[MT][2];
+    uint32_t qf[D / 16][4];
+    int r_lo[2], r_hi[2];
     bool even = true;  // this thread's rows see the same keys as the hull
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int e = 0; e < 2; ++e) {
+      const int x = gid + 8 * e;
+      const bool live = x < packed;
+      const int r = live ? s.by_g(x) : 0;
+      const uint16_t* src = a.q + ((static_cast<int64_t>(at.b) * s.rows_max + r) * s.Hq + at.kvh * s.g + (x - r * s.g)) * D + 2 * tid;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int x = 16 * t + gid + 8 * e;
-        const bool live = x < packed;
-        const int r = live ? s.by_g(x) : 0;
-        const uint16_t* src = a.q + ((static_cast<int64_t>(at.b) * s.rows_max + r) * s.Hq + at.kvh * s.g + (x - r * s.g)) * D + 2 * tid;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          qf[t][kk][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk)) : 0u;
-          qf[t][kk][e + 2] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8)) : 0u;
-        }
-        r_lo[t][e] = cs.h.lo, r_hi[t][e] = cs.h.hi;
-        if (s.windowed && live) {
-          const int64_t pos = raw_position(s.at, at.b, r);
-          const int p = inside(pos, s.L) ? static_cast<int>(pos) : 0;
-          r_lo[t][e] = max(p - s.w.left, 0);
-          r_hi[t][e] = min(p + s.w.right + 1, cs.n);
-          even = even && r_lo[t][e] <= cs.h.lo && r_hi[t][e] >= cs.h.hi;
-        }
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk)) : 0u;
+        qf[kk][e + 2] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8)) : 0u;
       }
+      r_lo[e] = cs.h.lo, r_hi[e] = cs.h.hi;
+      if (s.windowed && live) {
+        const int64_t pos = raw_position(s.at, at.b, r);
+        const int p = inside(pos, s.L) ? static_cast<int>(pos) : 0;
+        r_lo[e] = max(p - s.w.left, 0);
+        r_hi[e] = min(p + s.w.right + 1, cs.n);
+        even = even && r_lo[e] <= cs.h.lo && r_hi[e] >= cs.h.hi;
+      }
+    }
     even = __all_sync(0xffffffffu, even);
 
-    float o[MT][D / 8][4] = {};
-    float m[MT][2], l[MT][2];
+    float o[D / 8][4] = {};
+    float m[2], l[2];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m[t][e] = -INFINITY, l[t][e] = 0.f;
+    for (int e = 0; e < 2; ++e) m[e] = -INFINITY, l[e] = 0.f;
 
 #pragma unroll 1
     for (int u = at.u; u < u1; ++u) {
@@ -284,80 +280,69 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
         __syncwarp();
       }
       // scores of 16 keys: two fragments of 8
-      float sc[MT][2][4] = {};
+      float sc[2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t kf[4];
         ldsm4(kf, kb + (kk >> 2) * (kChunk * 128) + k_lane + ((((kk & 3) * 2 + k_c) ^ swz) << 4));
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          mma16816(sc[t][0], qf[t][kk], kf[0], kf[1]);
-          mma16816(sc[t][1], qf[t][kk], kf[2], kf[3]);
-        }
+        mma16816(sc[0], qf[kk], kf[0], kf[1]);
+        mma16816(sc[1], qf[kk], kf[2], kf[3]);
       }
       if (!(whole && even)) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int j = j0 + 8 * i + 2 * tid + (c & 1);
-              if (!(j < cs.h.near || (j >= r_lo[t][c >> 1] && j < r_hi[t][c >> 1]))) sc[t][i][c] = -INFINITY;
-            }
-      }
-      uint32_t pf[MT][4];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        float mx[2];
-        bool grow = false;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(fmaxf(sc[t][0][2 * e], sc[t][0][2 * e + 1]), fmaxf(sc[t][1][2 * e], sc[t][1][2 * e + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          mx[e] = x * s.scale_log2;
-          grow = grow || mx[e] > m[t][e] + kRescaleLog2;
-        }
-        if (__any_sync(0xffffffffu, grow)) {
-          float al[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool up = mx[e] > m[t][e] + kRescaleLog2;
-            al[e] = up ? ex2_approx(m[t][e] - mx[e]) : 1.f;
-            if (up) m[t][e] = mx[e];
-            l[t][e] *= al[e];
+          for (int c = 0; c < 4; ++c) {
+            const int j = j0 + 8 * i + 2 * tid + (c & 1);
+            if (!(j < cs.h.near || (j >= r_lo[c >> 1] && j < r_hi[c >> 1]))) sc[i][c] = -INFINITY;
           }
+      }
+      uint32_t pf[4];
+      float mx[2];
+      bool grow = false;
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[t][d][c] *= al[c >> 1];
-        }
-        float p[2][4];
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(fmaxf(sc[0][2 * e], sc[0][2 * e + 1]), fmaxf(sc[1][2 * e], sc[1][2 * e + 1]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        mx[e] = x * s.scale_log2;
+        grow = grow || mx[e] > m[e] + kRescaleLog2;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        float al[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float nm = m[t][e] == -INFINITY ? 0.f : -m[t][e];  // no key seen yet: every score is -infinity
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) p[i][2 * e + c] = ex2_approx(fmaf(sc[t][i][2 * e + c], s.scale_log2, nm));
-          l[t][e] += (p[0][2 * e] + p[0][2 * e + 1]) + (p[1][2 * e] + p[1][2 * e + 1]);
+          const bool up = mx[e] > m[e] + kRescaleLog2;
+          al[e] = up ? ex2_approx(m[e] - mx[e]) : 1.f;
+          if (up) m[e] = mx[e];
+          l[e] *= al[e];
         }
-        // the weights are rounded to bf16 for the product (2^-8 of each), the sum is of the unrounded ones
-        pf[t][0] = pack_bf16x2(p[0][0], p[0][1]);
-        pf[t][1] = pack_bf16x2(p[0][2], p[0][3]);
-        pf[t][2] = pack_bf16x2(p[1][0], p[1][1]);
-        pf[t][3] = pack_bf16x2(p[1][2], p[1][3]);
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[d][c] *= al[c >> 1];
       }
+      float p[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float nm = m[e] == -INFINITY ? 0.f : -m[e];  // no key seen yet: every score is -infinity
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) p[i][2 * e + c] = ex2_approx(fmaf(sc[i][2 * e + c], s.scale_log2, nm));
+        l[e] += (p[0][2 * e] + p[0][2 * e + 1]) + (p[1][2 * e] + p[1][2 * e + 1]);
+      }
+      // the weights are rounded to bf16 for the product (2^-8 of each), the sum is of the unrounded ones
+      pf[0] = pack_bf16x2(p[0][0], p[0][1]);
+      pf[1] = pack_bf16x2(p[0][2], p[0][3]);
+      pf[2] = pack_bf16x2(p[1][0], p[1][1]);
+      pf[3] = pack_bf16x2(p[1][2], p[1][3]);
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         uint32_t vf[4];
         ldsm4t(vf, vb + (d >> 2) * (kChunk * 128) + v_lane + ((((d & 3) * 2 + v_c) ^ swz) << 4));
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          mma16816(o[t][2 * d], pf[t], vf[0], vf[1]);
-          mma16816(o[t][2 * d + 1], pf[t], vf[2], vf[3]);
-        }
+        mma16816(o[2 * d], pf, vf[0], vf[1]);
+        mma16816(o[2 * d + 1], pf, vf[2], vf[3]);
       }
       ++used;
       __syncwarp();
@@ -368,34 +353,30 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
     float2* stat = reinterpret_cast<float2*>(smem + LY::kStatOff);
     float* join = reinterpret_cast<float*>(smem + LY::kJoinOff);
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 1);
-        l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 2);
-        if (tid == 0) stat[warp * LY::kRows + 16 * t + gid + 8 * e] = make_float2(m[t][e], l[t][e]);
-      }
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (tid == 0) stat[warp * LY::kRows + gid + 8 * e] = make_float2(m[e], l[e]);
+    }
     __syncthreads();
     // Buffers of four warps beside the ring; with no loads under way (an item a cluster) the other four's in the ring.
     auto buffer = [&](int w) { return w < kWarps / 2 ? join + w * LY::kRows * LY::kPitch : reinterpret_cast<float*>(smem) + (w - kWarps / 2) * LY::kRows * LY::kPitch; };
     auto put = [&](int w, bool add) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int e = 0; e < 2; ++e) {
+        const int x = gid + 8 * e;
+        float top = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int x = 16 * t + gid + 8 * e;
-          float top = -INFINITY;
+        for (int i = 0; i < kWarps; ++i) top = fmaxf(top, stat[i * LY::kRows + x].x);
+        const float f = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - top);
+        float2* row = reinterpret_cast<float2*>(buffer(w) + x * LY::kPitch) + tid;
 #pragma unroll
-          for (int i = 0; i < kWarps; ++i) top = fmaxf(top, stat[i * LY::kRows + x].x);
-          const float f = m[t][e] == -INFINITY ? 0.f : ex2_approx(m[t][e] - top);
-          float2* row = reinterpret_cast<float2*>(buffer(w) + x * LY::kPitch) + tid;
-#pragma unroll
-          for (int d = 0; d < D / 8; ++d) {
-            float2 y = make_float2(o[t][d][2 * e] * f, o[t][d][2 * e + 1] * f);
-            if (add) y.x += row[4 * d].x, y.y += row[4 * d].y;
-            row[4 * d] = y;
-          }
+        for (int d = 0; d < D / 8; ++d) {
+          float2 y = make_float2(o[d][2 * e] * f, o[d][2 * e + 1] * f);
+          if (add) y.x += row[4 * d].x, y.y += row[4 * d].y;
+          row[4 * d] = y;
         }
+      }
     };
     if constexpr (CLUSTER) {
       put(warp, false);
@@ -521,13 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
   }
 }
 
-template <int D, int MT>
+template <int D>
 cudaError_t launch(const Args& a, int ctas, int cluster, cudaStream_t s) {
-  const void* f = cluster ? reinterpret_cast<const void*>(few_rows_kernel<D, MT, true>) : reinterpret_cast<const void*>(few_rows_kernel<D, MT, false>);
-  const cudaError_t e = ensure_dyn_smem(f, Layout<D, MT>::kBytes);
+  const void* f = cluster ? reinterpret_cast<const void*>(few_rows_kernel<D, true>) : reinterpret_cast<const void*>(few_rows_kernel<D, false>);
+  const cudaError_t e = ensure_dyn_smem(f, Layout<D>::kBytes);
   if (e != cudaSuccess) return e;
-  if (cluster == 0) return launch_pdl(few_rows_kernel<D, MT, false>, dim3(ctas), dim3(kThreads), Layout<D, MT>::kBytes, s, a);
-  return launch_pdl_cluster(few_rows_kernel<D, MT, true>, dim3(a.s.B * a.s.Hkv * cluster), dim3(kThreads), Layout<D, MT>::kBytes, cluster, s, a);
+  if (cluster == 0) return launch_pdl(few_rows_kernel<D, false>, dim3(ctas), dim3(kThreads), Layout<D>::kBytes, s, a);
+  return launch_pdl_cluster(few_rows_kernel<D, true>, dim3(a.s.B * a.s.Hkv * cluster), dim3(kThreads), Layout<D>::kBytes, cluster, s, a);
 }
 
 }  // namespace
@@ -538,8 +519,8 @@ int resident_clusters(int S) {
   const cudaError_t e = cached_per_device(
       3100 + S, &n,
       [](int* out, void* ctx) -> cudaError_t {
-        const void* f = reinterpret_cast<const void*>(few_rows_kernel<128, 1, true>);
-        const cudaError_t r = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<128, 1>::kBytes);
+        const void* f = reinterpret_cast<const void*>(few_rows_kernel<128, true>);
+        const cudaError_t r = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<128>::kBytes);
         if (r != cudaSuccess) return r;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
@@ -548,7 +529,7 @@ int resident_clusters(int S) {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(attr[0].val.clusterDim.x);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Layout<128, 1>::kBytes;
+        cfg.dynamicSmemBytes = Layout<128>::kBytes;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         return cudaOccupancyMaxActiveClusters(out, f, &cfg);
@@ -569,9 +550,7 @@ int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, int 
 }
 
 cudaError_t launch_few_rows(const Args& a, int D, int ctas, int cluster, cudaStream_t s) {
-  const bool one = a.s.rows_max * a.s.g <= 16;
-  if (D == 64) return one ? launch<64, 1>(a, ctas, cluster, s) : launch<64, 2>(a, ctas, cluster, s);
-  return one ? launch<128, 1>(a, ctas, cluster, s) : launch<128, 2>(a, ctas, cluster, s);
+  return D == 64 ? launch<64>(a, ctas, cluster, s) : launch<128>(a, ctas, cluster, s);
 }
 
 }  // namespace paged

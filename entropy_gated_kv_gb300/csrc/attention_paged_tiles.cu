@@ -20,7 +20,7 @@
 // Blocks are 128 keys, brought in by TMA: one box of 128 rows, or of a smaller page, from the page that the table
 // names. The blocks of all items (sequence, group of tiles, KV head) stand in one line of
 // which the CTAs, one an SM, take equal shares; an item cut between CTAs leaves fp32 partial rows, which a second
-// launch joins in a fixed order. Where items of the split form are few, each goes to a cluster of up to eight CTAs
+// launch joins in a fixed order. Where items are few, each goes to a cluster of up to eight CTAs
 // instead, a CTA an equal part of its blocks, joined over distributed shared memory: one launch and no line.
 // A window leaves only the blocks that a group's rows see between them.
 // Roles (12 warps):
@@ -83,7 +83,7 @@ struct Layout {
   static constexpr int kPlaces = kRing * kRings;
   static constexpr int kUnitOff = (PAIR ? 2 : 1) * kTileBytes;
   static constexpr int kJoinPitch = D * 4 + 16;  // bytes of a row for a cluster's join, over the places: 8 rows fall to all banks
-  static_assert(PAIR || kPlaces * kTileBytes >= kBlockM * kJoinPitch, "join");
+  static_assert(kPlaces * kTileBytes >= (PAIR ? 2 : 1) * kBlockM * kJoinPitch, "join");
   static constexpr int kStatOff = kUnitOff + kPlaces * kTileBytes;
   static constexpr int kItemOff = kStatOff + (PAIR ? 0 : 2 * kBlockM * 8);
   static constexpr int kBarOff = kItemOff + kItems * static_cast<int>(sizeof(Item));
@@ -166,7 +166,7 @@ EC_DEV Group load_group(const Shape& s, int b, int grp, int step, bool tell) {
 EC_DEV bool all_in(int near, int lo, int hi, int j0, int count) { return j0 + count <= near || (j0 >= lo && j0 + count <= hi); }
 EC_DEV bool some_in(int near, int lo, int hi, int j0, int count) { return j0 < near || (j0 < hi && j0 + count > lo); }
 
-// CLUSTER (split form): an item a cluster; else shares of the line.
+// CLUSTER: an item a cluster; else shares of the line.
 template <int D, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Args a, int nr, int groups) {
   using LY = Layout<D, PAIR>;
@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   int share = 0, left = 0, place[4] = {0, 0, 0, 0};  // the CTA's first item: sequence, group, KV head, block; blocks from there on
   bool whole = false;
   if constexpr (CLUSTER) {
-    const int item = blockIdx.x / cluster_size();
-    place[0] = item / s.Hkv, place[2] = item % s.Hkv;
+    const int item = blockIdx.x / cluster_size(), pair = item / s.Hkv;
+    place[0] = pair / groups, place[1] = pair % groups, place[2] = item % s.Hkv;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -307,15 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const int box = min(kBlockN, 1 << s.page_shift);   // rows of a TMA box
     const int boxes = kBlockN / box;                   // boxes of a block's rows: 1, 2, 4 or 8
     const int atoms = box < kBlockN ? LY::kAtoms : 1;  // boxes beside each other
-    if (lane < kTiles) a.records[blockIdx.x * kTiles + lane].parts = 0;
     int b = place[0], grp = place[1], kvh = place[2], u = place[3];
     Group g{};
     if constexpr (CLUSTER) {
       const int S = cluster_size(), rank = cluster_ctarank();
-      g = load_group(s, b, 0, step, rank == 0 && kvh == 0 && lane == 0);
+      g = load_group(s, b, grp, step, rank == 0 && kvh == 0 && grp == 0 && lane == 0);
       u = g.blocks * rank / S;
       left = g.blocks * (rank + 1) / S - u;
-      if (lane == 0) bars->begin[0] = g.rows, bars->begin[1] = left;
+      if (lane == 0) bars->begin[0] = max(g.rows, 0), bars->begin[1] = left;
     } else {
       if (lane < kTiles) a.records[blockIdx.x * kTiles + lane].parts = 0;
       if (left > 0) g = load_group(s, b, grp, step, false);
@@ -704,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                 make_uint4(pack_bf16x2(y[8 * e], y[8 * e + 1]), pack_bf16x2(y[8 * e + 2], y[8 * e + 3]),
                            pack_bf16x2(y[8 * e + 4], y[8 * e + 5]), pack_bf16x2(y[8 * e + 6], y[8 * e + 7]));
         } else if (CLUSTER && !complete) {
-          const uint32_t dst = smem_u32(smem + LY::kUnitOff) + row * LY::kJoinPitch + col * 4;
+          const uint32_t dst = smem_u32(smem + LY::kUnitOff) + ((PAIR ? st * kBlockM : 0) + row) * LY::kJoinPitch + col * 4;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             st_shared16(dst + 16 * e, make_uint4(__float_as_uint(y[4 * e]), __float_as_uint(y[4 * e + 1]), __float_as_uint(y[4 * e + 2]), __float_as_uint(y[4 * e + 3])));
@@ -715,11 +714,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         }
       };
       if constexpr (PAIR) {
+        if constexpr (CLUSTER) {  // both streams are done with the places that the rows go to
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&bars->join);
+          ok = ok && wait_w(&bars->join, items & 1);
+        }
         if (!ok) break;
         tc_fence_after();
         if (live) {
           const float f = complete ? (l_sum == 0.f ? 0.f : 1.f / l_sum) : 1.f;
-          if (!complete && valid) a.part_stat[slot * kBlockM + row] = make_float2(good ? m_used : kNotWritten(), l_sum);
+          if (!complete && valid) {
+            const float2 mine = make_float2(good ? m_used : kNotWritten(), l_sum);
+            if constexpr (CLUSTER) reinterpret_cast<float2*>(smem + st * LY::kTileBytes)[row] = mine;  // the queries have been read
+            else a.part_stat[slot * kBlockM + row] = mine;
+          }
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -796,14 +804,17 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   }
   if constexpr (CLUSTER) {
     // the cluster's CTAs share out the tile's rows and read all parts of theirs
-    const int S = cluster_size(), rank = cluster_ctarank(), packed = bars->begin[0] * s.g;
-    if (bars->begin[1] == 0 && threadIdx.x < kBlockM) reinterpret_cast<float2*>(smem)[threadIdx.x] = make_float2(-INFINITY, 0.f);
+    const int S = cluster_size(), rank = cluster_ctarank(), rows = bars->begin[0];
+    const int rows0 = min(rows, nr) * s.g, packed = rows * s.g;  // of tile 0, of both
+    if (bars->begin[1] == 0)
+      for (int i = threadIdx.x; i < kTiles * kBlockM; i += kThreads)
+        reinterpret_cast<float2*>(smem + i / kBlockM * LY::kTileBytes)[i % kBlockM] = make_float2(-INFINITY, 0.f);
     cluster_arrive_release();
     cluster_wait_acquire();
     const int x0 = packed * rank / S, n = (packed * (rank + 1) / S - x0) * (D / 4);
 #pragma unroll 1
     for (int i = threadIdx.x; i < n; i += kThreads) {
-      const int x = x0 + i / (D / 4), c = i % (D / 4) * 4;
+      const int xx = x0 + i / (D / 4), c = i % (D / 4) * 4, t = PAIR && xx >= rows0, x = t ? xx - rows0 : xx;
       float2 st[kMaxCluster];
       float4 z[kMaxCluster];
       float top = -INFINITY, sum = 0.f;
@@ -813,8 +824,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         st[r] = make_float2(-INFINITY, 0.f);
         z[r] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < S) {
-          st[r] = ld_dsmem8(dsmem_map(smem_u32(smem) + x * 8, r));
-          z[r] = ld_dsmem16(dsmem_map(smem_u32(smem + LY::kUnitOff) + x * LY::kJoinPitch + c * 4, r));
+          st[r] = ld_dsmem8(dsmem_map(smem_u32(smem) + t * LY::kTileBytes + x * 8, r));
+          z[r] = ld_dsmem16(dsmem_map(smem_u32(smem + LY::kUnitOff) + (t * kBlockM + x) * LY::kJoinPitch + c * 4, r));
         }
       }
 #pragma unroll
@@ -831,10 +842,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         o.x += f * z[r].x, o.y += f * z[r].y, o.z += f * z[r].z, o.w += f * z[r].w;
       }
       if (lost) continue;
-      const int r = s.by_g(x);
+      const int rl = s.by_g(x), r = place[1] * step + t * nr + rl;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       uint2* dst = reinterpret_cast<uint2*>(
-          a.out + ((static_cast<int64_t>(place[0]) * s.rows_max + r) * s.Hq + place[2] * s.g + (x - r * s.g)) * D + c);
+          a.out + ((static_cast<int64_t>(place[0]) * s.rows_max + r) * s.Hq + place[2] * s.g + (x - rl * s.g)) * D + c);
       *dst = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
     cluster_arrive_release();  // no CTA leaves while another one reads its rows
@@ -848,31 +859,34 @@ cudaError_t launch(const Args& a, int nr, int groups, int ctas, int cluster, cud
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(tiles_kernel<D, PAIR, CLUSTER>), kBytes);
   if (e != cudaSuccess) return e;
   if constexpr (CLUSTER)
-    return launch_pdl_cluster(tiles_kernel<D, PAIR, CLUSTER>, dim3(a.s.B * a.s.Hkv * cluster), dim3(kThreads), kBytes, cluster, s, a, nr, groups);
+    return launch_pdl_cluster(tiles_kernel<D, PAIR, CLUSTER>, dim3(a.s.B * a.s.Hkv * groups * cluster), dim3(kThreads), kBytes, cluster, s, a, nr, groups);
   return launch_pdl(tiles_kernel<D, PAIR, CLUSTER>, dim3(ctas), dim3(kThreads), kBytes, s, a, nr, groups);
 }
 
 }  // namespace
 
 int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, int sms) {
-  const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
-  if (rows_max > nr || items > sms) return 0;
+  const bool pair = rows_max > nr;
+  const int64_t step = pair ? 2 * nr : nr, items = static_cast<int64_t>(p.B) * p.Hkv * ((rows_max + step - 1) / step);
+  if (items > sms) return 0;
   int S = kMaxCluster;
   while (S > 1 && resident_clusters(S) < items) --S;
   int64_t keys = scope_hi(p);
   if (w != nullptr) keys = std::min<int64_t>(keys, static_cast<int64_t>(w->left) + w->right + w->sinks + rows_max + 2 * kBlockN);
   const int64_t blocks = (keys + kBlockN - 1) / kBlockN;
-  return (blocks + S - 1) / S <= (items * blocks + sms - 1) / sms + kCutCost ? S : 0;
+  return S > 1 && (blocks + S - 1) / S <= (items * blocks + sms - 1) / sms + kCutCost ? S : 0;
+}
+
+template <int D>
+static cudaError_t launch_any(const Args& a, int nr, int ctas, int cluster, cudaStream_t s) {
+  const int groups = ((a.s.rows_max + nr - 1) / nr + 1) / 2;
+  if (a.s.rows_max > nr)
+    return cluster ? launch<D, true, true>(a, nr, groups, 0, cluster, s) : launch<D, true, false>(a, nr, groups, ctas, 0, s);
+  return cluster ? launch<D, false, true>(a, nr, 1, 0, cluster, s) : launch<D, false, false>(a, nr, 1, ctas, 0, s);
 }
 
 cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, int cluster, cudaStream_t s) {
-  const int groups = ((a.s.rows_max + nr - 1) / nr + 1) / 2;
-  const bool pair = a.s.rows_max > nr;
-  if (D == 64)
-    return pair ? launch<64, true, false>(a, nr, groups, ctas, 0, s)
-                : cluster ? launch<64, false, true>(a, nr, 1, 0, cluster, s) : launch<64, false, false>(a, nr, 1, ctas, 0, s);
-  return pair ? launch<128, true, false>(a, nr, groups, ctas, 0, s)
-              : cluster ? launch<128, false, true>(a, nr, 1, 0, cluster, s) : launch<128, false, false>(a, nr, 1, ctas, 0, s);
+  return D == 64 ? launch_any<64>(a, nr, ctas, cluster, s) : launch_any<128>(a, nr, ctas, cluster, s);
 }
 
 }  // namespace paged

@@ -38,7 +38,7 @@ struct Args {
   Shape s;
   const uint16_t* q;
   uint16_t* out;
-  float* part_o;      // [slots][32][D] (few rows), [slots][D / 4][128][4] (tiles)
+  float* part_o;      // [slots][16][D] (few rows), [slots][D / 4][128][4] (tiles)
   float2* part_stat;  // [slots][rows of a slot]: running maximum (base 2, scaled; NaN: the row is not written) and sum
   Record* records;    // [CTAs]
 };
@@ -151,8 +151,10 @@ EC_DEV void st_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// attention_paged_rows.cu: at most kFewRows packed rows (positions times the heads of a KV head) a sequence.
-constexpr int kFewRows = 32;
+// attention_paged_rows.cu: at most kFewRows packed rows (positions times the heads of a KV head) a sequence, the rows of
+// one mma.sync tile. (With two such tiles a warp the products bound it: 8 x 32 rows of 32 heads behind 2048 keys, ragged,
+// 66 us there and 48 as tiles of 128; 4 rows of 28/4 heads behind 2048 keys 12.0 and 8.8.)
+constexpr int kFewRows = 16;
 // cluster 0: shares of the line, partial rows where items are cut; else a cluster of so many CTAs for each item.
 cudaError_t launch_few_rows(const Args& a, int D, int ctas, int cluster, cudaStream_t s);
 constexpr int kMaxCluster = 8;

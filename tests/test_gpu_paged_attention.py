@@ -45,6 +45,11 @@ FULL = [
     (1, 130, 2, 2, 128, 512, [130], None),                          # pages larger than the sequence
     (6, 900, 7, 1, 128, 32, [95, 1, 40, 0, 128, 19], [900, 899, 33, 7, 640, 127]),
     (1, 9000, 2, 2, 128, 16, [200], [8999]),                        # few tiles, many blocks: cut items of two tiles
+    (2, 30000, 4, 2, 64, 16, [1, 2], [30000, 17]),                  # few rows, many chunks: cut items
+    (1, 20000, 1, 1, 64, 64, [100], [19999]),                       # one tile a sequence: cut items
+    (30, 300, 8, 8, 64, 32, [40 + b for b in range(30)], [(31 * b) % 301 for b in range(30)]),  # more items than SMs
+    (1, 700, 14, 2, 128, 16, [95], [613]),                          # pairs of tiles in clusters
+    (2, 100, 28, 4, 64, 16, [40, 3], [90, 100]),                    # a second tile without rows, CTAs without blocks
 ]
 
 
@@ -275,3 +280,84 @@ def test_far_pages(E, R):
     d["cache"] = E.PagedCache(k, v, far)
     c.call(E, d)
     c.check(d["out"])
+
+
+@pytest.mark.parametrize("g", [1, 12, 40])
+@pytest.mark.parametrize("R,seed", [(4, 0), (4, 1), (60, 2), (300, 3)])
+def test_positions_out_of_order(E, R, g, seed):
+    """A row is right, or not written and reported; none is wrong."""
+    rng = np.random.default_rng(seed)
+    pos = [rng.permutation(500)[:R], np.sort(rng.permutation(500)[:R])]
+    c = P.Case(2, 500, 2 * g, 2, 64, 16, [R, R], None, (30, 9, 5), "idx", pos=pos, seed=seed, fill=0.25)
+    d = c.inputs(E)
+    every = P.Pool(np.random.default_rng(1), 2, 500, 2, 64, 16, [500, 500])  # every position has a page
+    every.put(c.k, c.v)
+    d["cache"] = every.device(E)
+    c.call(E, d)
+    torch.cuda.synchronize()
+    lost = [(0, r) for r in range(R) if bool((d["out"][0, r] == P.SENTINEL).all())]
+    assert int(d["dev_err"].item()) == (E._capi.EC_DEVERR_BAD_IDX if lost else 0)
+    c.check(d["out"], lost=lost)
+
+
+def test_binding_checks_its_tensors(E):
+    c = P.Case(2, 300, 4, 2, 64, 16, [3, 3], None, (9, 9, 0), seed=1)
+    d = c.inputs(E)
+    p, q, cache, R, out = (d[n] for n in ("p", "q", "cache", "R", "out"))
+    w = dict(left=1, right=1, idx=d["idx"])
+    bad = [
+        lambda: E.paged_attention(p, q.float(), cache, R, out),
+        lambda: E.paged_attention(p, q[0], cache, R, out),
+        lambda: E.paged_attention(p, q.cpu(), cache, R, out),
+        lambda: E.paged_attention(p, q, cache, R, out[:, :2]),
+        lambda: E.paged_attention(p, q.transpose(0, 1), cache, R, out),
+        lambda: E.paged_attention(p, q, (cache.k, cache.v), R, out),
+        lambda: E.paged_attention(p, q, cache, R.long(), out),
+        lambda: E.paged_attention(p, q, cache, R[:1], out),
+        lambda: E.paged_attention(p, q, cache, R, out, kv_len=R.float()),
+        lambda: E.paged_attention(p, q, cache, R, out, ws=torch.empty(1 << 20, dtype=torch.uint8)),
+        lambda: E.paged_attention(p, q, cache, R, out, dev_err=R),
+        lambda: E.paged_window_attention(p, q, cache, R, out, 1, 1, idx=d["idx"], start=R),
+        lambda: E.paged_window_attention(p, q, cache, R, out, 1, 1, idx=d["idx"][:, :2]),
+        lambda: E.paged_window_attention(p, q, cache, R, out, 1, 1, idx=d["idx"].long()),
+        lambda: E.paged_window_attention(p, q, cache, R, out, 1, 1, idx=d["idx"].t().contiguous().t()),
+        lambda: E.paged_window_attention(p, q, cache, R, out, 1, 1, start=R.cpu()),
+        lambda: E.PagedCache(cache.k, cache.v[:1], cache.table),
+        lambda: E.PagedCache(cache.k, cache.v.float(), cache.table),
+        lambda: E.PagedCache(cache.k, cache.v, cache.table.long()),
+        lambda: E.PagedCache(cache.k, cache.v, cache.table[0]),
+        lambda: E.PagedCache(cache.k, cache.v, cache.table.t().contiguous().t()),
+        lambda: E.PagedCache(cache.k, cache.v, cache.table[:1].expand(2, -1)),
+        lambda: E.PagedCache(cache.k.transpose(1, 2), cache.v.transpose(1, 2), cache.table),
+        lambda: E.PagedCache(cache.k, torch.stack([cache.v, cache.v], 1)[:, 0], cache.table),
+        lambda: E.paged_attention(E.Params(B=2, L=400, Hq=4, Hkv=2, D=64, V=8, C_max=1, k=1), q, cache, R, out),  # the table is too short
+        lambda: E.paged_attention(E.Params(B=2, L=300, Hq=4, Hkv=4, D=64, V=8, C_max=1, k=1), q, cache, R, out),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was taken")
+    for f in (lambda: E.paged_attention(p, q, cache, R, q), lambda: E.paged_attention(p, q, cache, R, out, scale=0.0),
+              lambda: E.paged_window_attention(p, q, cache, R, out, -2, 1, idx=d["idx"]),
+              lambda: E.paged_window_attention(p, q, cache, R, out, sinks=-1, **w)):
+        with pytest.raises(E.EcError):
+            f()
+
+
+def test_cache_follows_its_tensors(E):
+    """A tensor exchanged or changed in place after the cache was made."""
+    c = P.Case(2, 300, 4, 2, 64, 16, [3, 40], [300, 123], None, None, seed=2)
+    d = c.run(E)
+    cache = d["cache"]
+    table = cache.table.clone()
+    swap = torch.where((table >= 0) & (table < c.pool.n_pages), c.pool.n_pages - 1 - table, table)
+    cache.k, cache.v, cache.table = cache.k.flip(0), cache.v.flip(0), swap
+    d["out"].fill_(P.SENTINEL)
+    c.call(E, d)
+    c.check(d["out"])
+    cache.table.resize_(1, cache.table.shape[1])
+    with pytest.raises(ValueError):
+        c.call(E, d)
+    cache.table = table.t().contiguous().t()
+    with pytest.raises(ValueError):
+        c.call(E, d)

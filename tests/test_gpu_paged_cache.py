@@ -301,3 +301,79 @@ def test_denoising_loop(E):
                     ref = O.attention(Q.f64(q[b, :n]), kk[b], vv[b], 1 / np.sqrt(D))
                     assert np.allclose(ref, want, rtol=1e-9, atol=1e-12)
         assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("R", [1, 40])
+def test_append_and_attention_in_one_graph(E, R):
+    """The refresh and the attention behind it, captured together and replayed: the second reads what the first has written."""
+    B, L, Hq, Hkv, D, page = 2, 300, 8, 2, 128, 16
+    a = Append(B, L, Hq, Hkv, D, page, [R, R], "idx", seed=R)
+    d = a.inputs(E)
+    for x in ("k", "v"):
+        getattr(d["cache"], x).normal_()
+    out = torch.full((B, R, Hq, D), P.SENTINEL, dtype=torch.bfloat16, device="cuda")
+    ws = E.workspace(E.paged_attention_workspace_size(d["p"], R))
+
+    def both():
+        a.call(E, d)
+        E.paged_window_attention(d["p"], d["q_out"], d["cache"], d["R"], out, 60, 60, 4, idx=d["idx"], ws=ws, dev_err=d["dev_err"])
+
+    both()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        both()
+    for seed in (1, 2):
+        for x in a.parts:
+            x.normal_(generator=torch.Generator(device="cuda").manual_seed(seed))
+        for x in ("k", "v"):
+            getattr(d["cache"], x).zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(d["dev_err"].item()) == 0
+        t = d["cache"].table.long()
+        k, v = (Q.f64(getattr(d["cache"], x)[t].flatten(1, 2)[:, :L]) for x in ("k", "v"))
+        for b in range(B):
+            assert (np.abs(v[b, a.pos[b]] - Q.f64(a.parts[2][b])) == 0).all()
+            want, tol = P.attention(Q.f64(d["q_out"][b]), k[b], v[b], D**-0.5, P.visible(a.pos[b], L, (60, 60, 4)))
+            assert (np.abs(Q.f64(out[b]) - want) <= tol).all()
+
+
+def test_append_binding_checks(E):
+    c = Append(2, 64, 4, 2, 64, 16, [5, 5], "idx", rows=6, seed=1)
+    d = c.inputs(E)
+    q, k, v = c.parts
+    p, cache, R, idx, rope = d["p"], d["cache"], d["R"], d["idx"], d["rope"]
+    bad = [
+        lambda: E.kv_append_paged(p, cache, k.float(), v, R),
+        lambda: E.kv_append_paged(p, cache, k, v[:, :5], R),
+        lambda: E.kv_append_paged(p, cache, k.cpu(), v, R),
+        lambda: E.kv_append_paged(p, cache, k.transpose(2, 3).contiguous().transpose(2, 3), v, R),
+        lambda: E.kv_append_paged(p, cache, k, v, R, q_out=d["q_out"]),
+        lambda: E.kv_append_paged(p, cache, k, v, R, q_new=q, q_out=d["q_out"][:, :5]),
+        lambda: E.kv_append_paged(p, cache, k, v, R, idx=idx, start=R),
+        lambda: E.kv_append_paged(p, cache, k, v, R, rope=(rope[0][:5], rope[1])),
+        lambda: E.kv_append_paged(p, cache, k, v, R, rope=(rope[0], rope[1].double())),
+        lambda: E.kv_append_paged(p, cache, k, v, R.long()),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was taken")
+    pool = cache.k.flatten()
+    for f in (lambda: E.kv_append_paged(p, cache, k, v, R, q_new=q, q_out=q),
+              lambda: E.kv_append_paged(p, cache, pool[: k.numel()].view_as(k), v, R)):
+        with pytest.raises(E.EcError):
+            f()
+
+
+def test_far_pages_are_written(E):
+    """Rows of pages past 2^31 elements of the pool."""
+    page, H, D = 1024, 2, 128
+    n = (1 << 31) // (page * H * D) + 9
+    k, v = (torch.empty(n, page, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.tensor([[n - 1]], dtype=torch.int32, device="cuda")
+    p = E.Params(B=1, L=page, Hq=H, Hkv=H, D=D, V=8, C_max=1, k=1)
+    x = torch.randn(1, 7, 2 * H, D, device="cuda").to(torch.bfloat16)
+    start = torch.tensor([100], dtype=torch.int32, device="cuda")
+    E.kv_append_paged(p, E.PagedCache(k, v, table), x[:, :, :H], x[:, :, H:], torch.tensor([7], dtype=torch.int32, device="cuda"), start=start)
+    assert torch.equal(k[n - 1, 100:107], x[0, :, :H]) and torch.equal(v[n - 1, 100:107], x[0, :, H:])

@@ -156,6 +156,10 @@ class Cta:
                     used += 1
                 if self.pair or st < nblk:
                     yield self.pv_done[st], used - 1
+            if self.pair and len(self.items) == 2:  # an item a cluster
+                self.join.arrive()
+                yield None
+                yield self.join, n
             if not self.pair:
                 if n > 0:
                     yield self.o_free, n - 1
