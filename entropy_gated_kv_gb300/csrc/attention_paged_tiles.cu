@@ -30,6 +30,7 @@
 // A waiter on an mbarrier sees a phase's parity only, so whoever waits on a barrier follows every one of its
 // phases or has seen by another way that the one before is complete.
 #include <algorithm>
+#include <type_traits>
 
 #include "paged_common.cuh"
 
@@ -605,82 +606,97 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             // weight is off by 2^-8 of itself at most. Their sum is that of the fp32 weights.
             const bool plain = __all_sync(0xffffffffu, !valid || all_in(it.near, r_lo, r_hi, j, kBlockN));
             const uint64_t scale2 = pack_f32x2(s.scale_log2, s.scale_log2);
+            // (twice, with the masks and without: what is in the way of the plain blocks costs them 4%)
+            auto halves = [&](auto masked) {
 #pragma unroll 1
-            for (int h = 1; h >= 0; --h) {
-              uint32_t x[2][32];
-              EC_TMEM_LD32(s_addr + 64 * h, x[0]);
-              EC_TMEM_LD32(s_addr + 64 * h + 32, x[1]);
-              EC_TMEM_WAIT32(x[0]);
-              EC_TMEM_WAIT32(x[1]);
-              if (!plain) {  // keys that the row does not see
-                auto below = [](int y) { return y <= 0 ? 0u : y >= 32 ? ~0u : (1u << y) - 1u; };
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const int jc = j + 64 * h + 32 * c;
-                  const uint32_t see = below(it.near - jc) | (below(r_hi - jc) & ~below(r_lo - jc));
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (!((see >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
+              for (int h = 1; h >= 0; --h) {
+                if (masked && !__any_sync(0xffffffffu, valid && some_in(it.near, r_lo, r_hi, j + 64 * h, kHalf))) {
+                  uint32_t none[16] = {};  // no row of the warp sees a key of the half
+                  EC_TMEM_ST16(s_addr + 64 * h, none);
+                  EC_TMEM_ST16(s_addr + 64 * h + 16, none);
+                  tmem_wait_st();
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&bars->p_full[st][h]);
+                  continue;
                 }
-              }
-              // maximum (scale > 0 commutes with it), then p = 2^(s scale log2(e) - m)
-              float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                uint32_t x[2][32];
+                EC_TMEM_LD32(s_addr + 64 * h, x[0]);
+                EC_TMEM_LD32(s_addr + 64 * h + 32, x[1]);
+                EC_TMEM_WAIT32(x[0]);
+                EC_TMEM_WAIT32(x[1]);
+                if (masked) {  // keys that the row does not see
+                  auto below = [](int y) { return y <= 0 ? 0u : y >= 32 ? ~0u : (1u << y) - 1u; };
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                m4[e & 2] = max3(m4[e & 2], __uint_as_float(x[0][e]), __uint_as_float(x[0][e + 1]));
-                m4[(e & 2) + 1] = max3(m4[(e & 2) + 1], __uint_as_float(x[1][e]), __uint_as_float(x[1][e + 1]));
-              }
-              const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * s.scale_log2;
-              if (i == i0 && h == 1) {
-                m_used = mx;
-              } else {
-                const bool rescale = mx > m_used + kRescaleLog2;
-                if (__any_sync(0xffffffffu, rescale)) {
-                  // O is at rest at a block's first half, as its scores came after the last P V; at its second half
-                  // the first one's P V may be under way
-                  if (h == 0) ok = wait_w(&bars->pv_half[st], used & 1u);
-                  if (!ok) break;
-                  tc_fence_after();
-                  const float alpha = rescale ? ex2_approx(m_used - mx) : 1.f;
-                  if (rescale) m_used = mx;
-                  l_sum *= alpha;
-#pragma unroll 1
-                  for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
-                    EC_TMEM_WAIT32(o);
+                  for (int c = 0; c < 2; ++c) {
+                    const int jc = j + 64 * h + 32 * c;
+                    const uint32_t see = below(it.near - jc) | (below(r_hi - jc) & ~below(r_lo - jc));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                    EC_TMEM_ST32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+                    for (int e = 0; e < 32; ++e)
+                      if (!((see >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
                   }
                 }
-              }
-              // without a finite score so far, nothing is subtracted and p = 0
-              const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-              const uint64_t neg_m2 = pack_f32x2(neg_m, neg_m);
-              uint64_t sum2[2] = {0, 0};
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t pk[16];
+                // maximum (scale > 0 commutes with it), then p = 2^(s scale log2(e) - m)
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                  float p0, p1;
-                  unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), scale2, neg_m2), p0, p1);
-                  p0 = ex2_approx(p0);
-                  p1 = ex2_approx(p1);
-                  sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
-                  pk[e >> 1] = pack_bf16x2(p0, p1);
+                  m4[e & 2] = max3(m4[e & 2], __uint_as_float(x[0][e]), __uint_as_float(x[0][e + 1]));
+                  m4[(e & 2) + 1] = max3(m4[(e & 2) + 1], __uint_as_float(x[1][e]), __uint_as_float(x[1][e + 1]));
                 }
-                EC_TMEM_ST16(s_addr + 64 * h + 16 * c, pk);
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * s.scale_log2;
+                if (i == i0 && h == 1) {
+                  m_used = mx;
+                } else {
+                  const bool rescale = mx > m_used + kRescaleLog2;
+                  if (__any_sync(0xffffffffu, rescale)) {
+                    // O is at rest at a block's first half, as its scores came after the last P V; at its second half
+                    // the first one's P V may be under way
+                    if (h == 0) ok = wait_w(&bars->pv_half[st], used & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float alpha = rescale ? ex2_approx(m_used - mx) : 1.f;
+                    if (rescale) m_used = mx;
+                    l_sum *= alpha;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                      uint32_t o[32];
+                      EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+                      EC_TMEM_WAIT32(o);
+#pragma unroll
+                      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                      EC_TMEM_ST32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
+                    }
+                  }
+                }
+                // without a finite score so far, nothing is subtracted and p = 0
+                const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+                const uint64_t neg_m2 = pack_f32x2(neg_m, neg_m);
+                uint64_t sum2[2] = {0, 0};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  uint32_t pk[16];
+#pragma unroll
+                  for (int e = 0; e < 32; e += 2) {
+                    float p0, p1;
+                    unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])), scale2, neg_m2), p0, p1);
+                    p0 = ex2_approx(p0);
+                    p1 = ex2_approx(p1);
+                    sum2[(e >> 1) & 1] = add_f32x2(sum2[(e >> 1) & 1], pack_f32x2(p0, p1));
+                    pk[e >> 1] = pack_bf16x2(p0, p1);
+                  }
+                  EC_TMEM_ST16(s_addr + 64 * h + 16 * c, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_full[st][h]);
+                float sum_lo, sum_hi;
+                unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
+                l_sum += sum_lo + sum_hi;
               }
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars->p_full[st][h]);
-              float sum_lo, sum_hi;
-              unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sum_lo, sum_hi);
-              l_sum += sum_lo + sum_hi;
-            }
+            };
+            if (plain) halves(std::false_type{});
+            else halves(std::true_type{});
             if (!ok) break;
           } else if (lane == 0) {
             mbar_arrive(&bars->p_full[st][0]);
