@@ -544,12 +544,14 @@ def prefix_attention(p: Params, q, prefix, cache, R, out, kv_len=None, scale: fl
 class _Pages:
     """The checked C view (ec_paged_kv) of a paged cache."""
 
-    __slots__ = ("c", "ref", "index", "heads", "B", "positions", "at", "shape", "strides", "table_shape")
+    __slots__ = ("c", "ref", "index", "heads", "B", "positions", "at")
 
     def __init__(self, k, v, table):
-        self.index = _cuda_index(k, "k")
-        self.at, self.shape, self.table_shape = (k.data_ptr(), v.data_ptr(), table.data_ptr()), k.shape, table.shape
-        self.strides = (k.stride(), v.stride(), table.stride())
+        self.index, self.at = _cuda_index(k, "k"), (k.data_ptr(), v.data_ptr(), table.data_ptr())
+        for t, name in ((k, "k"), (v, "v"), (table, "table")):
+            end = t.storage_offset() + 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+            if t.numel() > 0 and end * t.element_size() > t.untyped_storage().nbytes():
+                raise ValueError(f"the memory of {name} has become smaller than {name}")
         if k.dim() != 4 or 0 in k.shape:
             raise ValueError(f"a pool is [n_pages, page_size, Hkv, D], got {list(k.shape)}")
         n, ps, H, D = k.shape
@@ -573,36 +575,36 @@ class _Pages:
         self.c = C.EcPagedKv(ps, n, stride, k.data_ptr(), v.data_ptr(), table.data_ptr(), row)
         self.ref = ctypes.byref(self.c)
 
-    def holds(self, k, v, t) -> bool:
-        """Whether the view is still that of these tensors. Addresses alone do not tell: one that was resized,
-        restrided or given other data in place may lie where it lay."""
-        return (self.at == (k.data_ptr(), v.data_ptr(), t.data_ptr()) and k.shape == self.shape == v.shape and t.shape == self.table_shape
-                and self.strides == (k.stride(), v.stride(), t.stride()) and k.dtype is v.dtype is torch.bfloat16 and t.dtype is torch.int32)
-
 
 class PagedCache:
     """One layer's K/V cache in pages (ec_paged_kv): k, v bf16 [n_pages, page_size, Hkv, D] (contiguous
     pages; the two may be views of one pool), table int32 [B, pages of a sequence]. Position j of
     sequence b is row j % page_size of page table[b, j // page_size]; entries of positions that no call
-    touches may hold anything. A tensor may be exchanged for another one or changed in place; every
-    call checks what the cache holds then."""
+    touches may hold anything. The cache keeps views of its own: a tensor may be exchanged for another one (checked at
+    the next call), and one that is resized or restrided in place elsewhere is here what it was."""
 
-    __slots__ = ("k", "v", "table", "_c")
+    __slots__ = ("_k", "_v", "_table", "_c")
 
     def __init__(self, k, v, table):
-        self.k, self.v, self.table = k, v, table
+        self._k, self._v, self._table, self._c = k.detach(), v.detach(), table.detach(), None
         self.view()
 
-    def __setattr__(self, name, value):
-        object.__setattr__(self, "_c", None)
-        object.__setattr__(self, name, value)
+    def _exchange(name):
+        def put(self, t):
+            setattr(self, name, t.detach())
+            self._c = None
+
+        return property(lambda self: getattr(self, name).detach(), put)
+
+    k, v, table = _exchange("_k"), _exchange("_v"), _exchange("_table")
+    del _exchange
 
     def view(self) -> _Pages:
-        """The checked C view; made and checked again when a tensor is not what it was."""
-        c, k, v, t = self._c, self.k, self.v, self.table
-        if c is None or not c.holds(k, v, t):
-            c = _Pages(k, v, t)
-            object.__setattr__(self, "_c", c)
+        """The checked C view; made and checked again when a tensor was exchanged or its memory has moved."""
+        c, k, v, t = self._c, self._k, self._v, self._table
+        if c is None or c.at != (k.data_ptr(), v.data_ptr(), t.data_ptr()):
+            self._c = None
+            c = self._c = _Pages(k, v, t)
         return c
 
     @classmethod

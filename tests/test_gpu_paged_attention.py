@@ -355,9 +355,24 @@ def test_cache_follows_its_tensors(E):
     d["out"].fill_(P.SENTINEL)
     c.call(E, d)
     c.check(d["out"])
-    cache.table.resize_(1, cache.table.shape[1])
-    with pytest.raises(ValueError):
-        c.call(E, d)
-    cache.table = table.t().contiguous().t()
+    swap.resize_(1, swap.shape[1])  # the cache keeps the shape that it was given
+    cache.k.transpose_(0, 1)
+    d["out"].fill_(P.SENTINEL)
+    c.call(E, d)
+    c.check(d["out"])
+    for bad in (table.t().contiguous().t(), table[:1].contiguous()):
+        cache.table = bad
+        for _ in range(2):
+            with pytest.raises(ValueError):
+                c.call(E, d)
+    cache.table = swap.resize_(*table.shape)
+    k = cache.k
+    cache.k = moved = k.clone()
+    c.call(E, d)
+    for n in (moved.untyped_storage().nbytes() // 2, 0):
+        moved.untyped_storage().resize_(n)
+        with pytest.raises(ValueError):
+            c.call(E, d)
+    cache.k, cache.v = k, cache.v.float()
     with pytest.raises(ValueError):
         c.call(E, d)
