@@ -5,6 +5,7 @@
 // causal mask. Pages and windows have no counterpart there.
 //   out[b, r, h] = sum_j softmax_j(scale <q[b, r, h], k_j>) v_j over the keys j that row r sees, KV head h / g
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "paged_common.cuh"
@@ -180,6 +181,32 @@ bool encode_queries(EncodeTiledFn enc, CUtensorMap* m, const void* q, const ec_p
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The current device's; null on an error.
+const Device* device_info(cudaError_t* e) {
+  constexpr int kDevices = 64;
+  static Device info[kDevices];
+  static std::atomic<bool> ready[kDevices];
+  static std::mutex mutex;
+  int dev = 0;
+  *e = cudaGetDevice(&dev);
+  if (*e != cudaSuccess) return nullptr;
+  if (dev < 0 || dev >= kDevices) {
+    *e = cudaErrorNotSupported;
+    return nullptr;
+  }
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!ready[dev].load(std::memory_order_relaxed)) {
+      *e = current_device_sms(&info[dev].sms);
+      if (*e == cudaSuccess) *e = setup_few_rows(&info[dev]);
+      if (*e == cudaSuccess) *e = setup_tiles();
+      if (*e != cudaSuccess) return nullptr;
+      ready[dev].store(true, std::memory_order_release);
+    }
+  }
+  return &info[dev];
+}
+
 bool few_rows(const ec_params& p, int32_t rows_max) { return static_cast<int64_t>(rows_max) * (p.Hq / p.Hkv) <= kFewRows; }
 
 // Positions of a tile.
@@ -213,9 +240,9 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
   *status = EC_ERR_CUDA;
   const EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return cudaErrorNotSupported;
-  int sms = 0;
-  cudaError_t e = cached_per_device(3000, &sms, [](int* n, void*) { return current_device_sms(n); }, nullptr);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  const Device* const device = device_info(&e);
+  if (device == nullptr) return e;
   Args a;
   Shape& sh = a.s;
   sh.B = p.B, sh.L = p.L, sh.Hq = p.Hq, sh.Hkv = p.Hkv, sh.g = p.Hq / p.Hkv, sh.rows_max = rows_max;
@@ -231,7 +258,7 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
   a.part_o = reinterpret_cast<float*>(w);
   a.part_stat = reinterpret_cast<float2*>(w + lay.stat);
   a.records = reinterpret_cast<Record*>(w + lay.records);
-  const int ctas = std::min(sms, kMaxCtas);
+  const int ctas = std::min(device->sms, kMaxCtas);
   const bool few = few_rows(p, rows_max);
   // a chunk of 16 keys, or a block of 128 as far as a page holds it
   const int box = few ? 16 : std::min(128, c.page_size), atoms = few || box == 128 ? p.D / 64 : 1;
@@ -242,13 +269,13 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
     return cudaErrorInvalidValue;
   }
   if (few) {
-    const int cluster = few_rows_cluster(p, rows_max, window, sms);
+    const int cluster = few_rows_cluster(p, rows_max, window, *device);
     e = launch_few_rows(a, p.D, ctas, cluster, s);
     if (e == cudaSuccess && cluster == 0)
       e = launch_pdl(p.D == 64 ? merge_rows_kernel<64> : merge_rows_kernel<128>, dim3(ctas, rows_max * sh.g), dim3(32 * kMergeWarps), 0, s, a);
   } else {
     const int tiles = rows_max <= nr ? 1 : 2;
-    const int cluster = tiles_cluster(p, rows_max, nr, window, sms);
+    const int cluster = tiles_cluster(p, rows_max, nr, window, *device);
     e = launch_tiles(a, p.D, nr, ctas, cluster, s);
     // eight items or fewer may each go over many CTAs: their parts one column quad a thread
     const bool few_items = static_cast<int64_t>(p.B) * p.Hkv * ((rows_max + nr - 1) / nr) <= 8;

@@ -504,49 +504,45 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
 
 template <int D>
 cudaError_t launch(const Args& a, int ctas, int cluster, cudaStream_t s) {
-  const void* f = cluster ? reinterpret_cast<const void*>(few_rows_kernel<D, true>) : reinterpret_cast<const void*>(few_rows_kernel<D, false>);
-  const cudaError_t e = ensure_dyn_smem(f, Layout<D>::kBytes);
-  if (e != cudaSuccess) return e;
   if (cluster == 0) return launch_pdl(few_rows_kernel<D, false>, dim3(ctas), dim3(kThreads), Layout<D>::kBytes, s, a);
   return launch_pdl_cluster(few_rows_kernel<D, true>, dim3(a.s.B * a.s.Hkv * cluster), dim3(kThreads), Layout<D>::kBytes, cluster, s, a);
 }
 
 }  // namespace
 
-// An SM of a cluster holds one CTA, and a GPU part's SMs need not be a multiple of S: 15 clusters of 8 on 152 SMs.
-int resident_clusters(int S) {
-  int n = 0;
-  const cudaError_t e = cached_per_device(
-      3100 + S, &n,
-      [](int* out, void* ctx) -> cudaError_t {
-        const void* f = reinterpret_cast<const void*>(few_rows_kernel<128, true>);
-        const cudaError_t r = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<128>::kBytes);
-        if (r != cudaSuccess) return r;
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = static_cast<unsigned>(*static_cast<int*>(ctx));
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(attr[0].val.clusterDim.x);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Layout<128>::kBytes;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaOccupancyMaxActiveClusters(out, f, &cfg);
-      },
-      &S);
-  return e == cudaSuccess ? n : 0;
+cudaError_t setup_few_rows(Device* d) {
+  auto allow = [](const void* f, int bytes) { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); };
+  const void* f = reinterpret_cast<const void*>(few_rows_kernel<128, true>);
+  cudaError_t e = allow(f, Layout<128>::kBytes);
+  if (e == cudaSuccess) e = allow(reinterpret_cast<const void*>(few_rows_kernel<128, false>), Layout<128>::kBytes);
+  if (e == cudaSuccess) e = allow(reinterpret_cast<const void*>(few_rows_kernel<64, true>), Layout<64>::kBytes);
+  if (e == cudaSuccess) e = allow(reinterpret_cast<const void*>(few_rows_kernel<64, false>), Layout<64>::kBytes);
+  d->clusters[0] = 0;
+  d->clusters[1] = d->sms;
+  for (int S = 2; e == cudaSuccess && S <= kMaxCluster; ++S) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(S);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Layout<128>::kBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&d->clusters[S], f, &cfg);
+  }
+  return e;
 }
 
-int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, int sms) {
+int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, const Device& d) {
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
-  if (items > sms) return 0;
-  int S = kMaxCluster;
-  while (S > 1 && resident_clusters(S) < items) --S;
+  if (items > d.sms) return 0;
+  const int S = cluster_for(d, items);
   int64_t keys = scope_hi(p);
   if (w != nullptr) keys = std::min<int64_t>(keys, static_cast<int64_t>(w->left) + w->right + w->sinks + rows_max + 2 * kChunk);
   const int64_t units = (keys + kChunk * kWarps - 1) / (kChunk * kWarps);
-  return (units + S - 1) / S <= (items * units + sms - 1) / sms + kJoinUnits ? S : 0;
+  return (units + S - 1) / S <= (items * units + d.sms - 1) / d.sms + kJoinUnits ? S : 0;
 }
 
 cudaError_t launch_few_rows(const Args& a, int D, int ctas, int cluster, cudaStream_t s) {

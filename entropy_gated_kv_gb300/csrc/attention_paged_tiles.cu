@@ -872,8 +872,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 template <int D, bool PAIR, bool CLUSTER>
 cudaError_t launch(const Args& a, int nr, int groups, int ctas, int cluster, cudaStream_t s) {
   constexpr int kBytes = Layout<D, PAIR>::kBytes;
-  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(tiles_kernel<D, PAIR, CLUSTER>), kBytes);
-  if (e != cudaSuccess) return e;
   if constexpr (CLUSTER)
     return launch_pdl_cluster(tiles_kernel<D, PAIR, CLUSTER>, dim3(a.s.B * a.s.Hkv * groups * cluster), dim3(kThreads), kBytes, cluster, s, a, nr, groups);
   return launch_pdl(tiles_kernel<D, PAIR, CLUSTER>, dim3(ctas), dim3(kThreads), kBytes, s, a, nr, groups);
@@ -881,16 +879,31 @@ cudaError_t launch(const Args& a, int nr, int groups, int ctas, int cluster, cud
 
 }  // namespace
 
-int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, int sms) {
+cudaError_t setup_tiles() {
+  cudaError_t e = cudaSuccess;
+  auto allow = [&](const void* f, int bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  allow(reinterpret_cast<const void*>(tiles_kernel<64, false, false>), Layout<64, false>::kBytes);
+  allow(reinterpret_cast<const void*>(tiles_kernel<64, false, true>), Layout<64, false>::kBytes);
+  allow(reinterpret_cast<const void*>(tiles_kernel<64, true, false>), Layout<64, true>::kBytes);
+  allow(reinterpret_cast<const void*>(tiles_kernel<64, true, true>), Layout<64, true>::kBytes);
+  allow(reinterpret_cast<const void*>(tiles_kernel<128, false, false>), Layout<128, false>::kBytes);
+  allow(reinterpret_cast<const void*>(tiles_kernel<128, false, true>), Layout<128, false>::kBytes);
+  allow(reinterpret_cast<const void*>(tiles_kernel<128, true, false>), Layout<128, true>::kBytes);
+  allow(reinterpret_cast<const void*>(tiles_kernel<128, true, true>), Layout<128, true>::kBytes);
+  return e;
+}
+
+int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, const Device& d) {
   const bool pair = rows_max > nr;
   const int64_t step = pair ? 2 * nr : nr, items = static_cast<int64_t>(p.B) * p.Hkv * ((rows_max + step - 1) / step);
-  if (items > sms) return 0;
-  int S = kMaxCluster;
-  while (S > 1 && resident_clusters(S) < items) --S;
+  if (items > d.sms) return 0;
+  const int S = cluster_for(d, items);
   int64_t keys = scope_hi(p);
   if (w != nullptr) keys = std::min<int64_t>(keys, static_cast<int64_t>(w->left) + w->right + w->sinks + rows_max + 2 * kBlockN);
   const int64_t blocks = (keys + kBlockN - 1) / kBlockN;
-  return S > 1 && (blocks + S - 1) / S <= (items * blocks + sms - 1) / sms + kCutCost ? S : 0;
+  return S > 1 && (blocks + S - 1) / S <= (items * blocks + d.sms - 1) / d.sms + kCutCost ? S : 0;
 }
 
 template <int D>

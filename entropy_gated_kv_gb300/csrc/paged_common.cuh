@@ -158,12 +158,24 @@ constexpr int kFewRows = 16;
 // cluster 0: shares of the line, partial rows where items are cut; else a cluster of so many CTAs for each item.
 cudaError_t launch_few_rows(const Args& a, int D, int ctas, int cluster, cudaStream_t s);
 constexpr int kMaxCluster = 8;
-int resident_clusters(int S);  // clusters of S CTAs, one an SM, that are on the device at once
-int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, int sms);
+// What the launches ask of a device, found once: its SMs, and clusters of S CTAs, one an SM, that are on it at once (a part
+// of the GPU need not have a multiple of S SMs: 15 clusters of 8 on 152).
+struct Device {
+  int sms, clusters[kMaxCluster + 1];
+};
+cudaError_t setup_few_rows(Device* d);  // the kernels' shared memory, and d->clusters
+cudaError_t setup_tiles();
+// CTAs of a cluster that `items` clusters can have at once.
+inline int cluster_for(const Device& d, int64_t items) {
+  int S = kMaxCluster;
+  while (S > 1 && d.clusters[S] < items) --S;
+  return S;
+}
+int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, const Device& d);
 // attention_paged_tiles.cu: tiles of nr positions, nr times the heads of a KV head at most 128 packed rows.
 constexpr int kTileRows = 128;
 cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, int cluster, cudaStream_t s);
-int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, int sms);
+int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, const Device& d);
 // A CTA leaves two cut items at most, one that goes on in it and one that begins there: slots
 // 2 tiles cta + tile and 2 tiles cta + tiles + tile, with one tile or two beside each other.
 EC_DEV int64_t part_slot(int first_cta, int i, int tiles, int tile) {
