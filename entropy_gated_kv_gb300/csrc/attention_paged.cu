@@ -82,19 +82,22 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(const __gr
   dst[threadIdx.x] = pack_bf16x2(y.x * inv, y.y * inv);
 }
 
-// The same for tiles: a CTA takes a record and 32 rows of it, a thread a row and every eighth quad of columns, as many
-// parts in flight as make eight quads. Where a few items may go over many CTAs each (QUADS 1) a CTA takes eight quads only.
-constexpr int kTileMergeThreads = 256;
+// The same for tiles: a CTA takes a record and 64 rows of it, a thread a row and every eighth quad of columns, as many
+// parts in flight as make eight quads. Where a few items may go over many CTAs each (QUADS 1) a CTA takes eight quads only:
+// for all calls that took 7 us more on 8 x 95 rows of 28/4 heads, most of its CTAs without a record. (32 rows a CTA:
+// 94.4 us for 93.1 on 95 rows behind 32768 keys, 32 heads; 128 rows: 95.0.)
+constexpr int kTileMergeThreads = 512;
+constexpr int kTileMergeRows = 64;
 
 template <int D, int QUADS>
 __global__ void __launch_bounds__(kTileMergeThreads) merge_tiles_kernel(const __grid_constant__ Args a, int tiles) {
-  constexpr int kWarps = kTileMergeThreads / 32, kBatch = 8 / QUADS;
+  constexpr int kWarps = 8, kBatch = 8 / QUADS;  // of 32 rows
   const Shape& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
   const Record rec = a.records[blockIdx.x];
-  const int row = blockIdx.y * 32 + lane, quad0 = blockIdx.z * kWarps * QUADS + warp;
+  const int row = blockIdx.y * kTileMergeRows + warp / kWarps * 32 + lane, quad0 = blockIdx.z * kWarps * QUADS + warp % kWarps;
   if (rec.parts == 0 || row >= rec.rows || quad0 >= D / 4) return;
   const int cta = blockIdx.x / tiles, tile = blockIdx.x - cta * tiles;
   float m = -INFINITY, l = 0.f;
@@ -280,7 +283,7 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
     // eight items or fewer may each go over many CTAs: their parts one column quad a thread
     const bool few_items = static_cast<int64_t>(p.B) * p.Hkv * ((rows_max + nr - 1) / nr) <= 8;
     const int quads = p.D / 32;  // of a thread that takes every eighth one
-    const dim3 grid(ctas * tiles, kTileRows / 32, few_items ? quads : 1);
+    const dim3 grid(ctas * tiles, kTileRows / kTileMergeRows, few_items ? quads : 1);
     if (cluster != 0) {
       // joined on the chip
     } else if (e == cudaSuccess && p.D == 64) {
