@@ -12,7 +12,7 @@
 //     joined at the item's end.
 // The streams take turns at the tensor cores, P V and next scores in one piece: left to themselves they
 // fall into step, both in the softmax, then both at the tensor cores (3820 cycles a pair of blocks for 3300; 4 full steps
-// of 2048 rows, 28/4 heads, 210 us for 182). What a pair of blocks is bound by: a stream's own chain, softmax 1700
+// of 2048 rows, 28/4 heads, 210 us for the 178 of today). What a pair of blocks is bound by: a stream's own chain, softmax 1700
 // cycles (64 exponentials of a row take a lone warp 490, two warps of a scheduler 590 together), P V and scores 1000, and
 // some 600 between them, as a wait takes 120 to 200 cycles also when it is over. Tried beside that: score buffers
 // of 64 keys, two a stream (210 us: as many waits for half the product), one issuer for both streams (222 us), sixteen
@@ -43,7 +43,14 @@ constexpr int kBlockM = 128;
 constexpr int kBlockN = 128;
 constexpr int kHalf = 64;  // keys whose weights are handed over at once
 constexpr int kItems = 4;  // items handed out and not yet finished
-constexpr int kCutCost = 5;  // what the partial rows of cut items and their join cost, in blocks
+// A cluster for an item, or the line and a second launch that costs some six blocks. Line and clusters measured: 95 rows of 28/4 heads
+// behind 16384 keys 44 and 40 us, behind 24576 47 and 53; 512 rows behind 8192 61 and 67; 95 rows of 32 heads behind 32768 95 and 86; 18 rows
+// of 28/4 behind 16384 30 and 27, behind 32768 38 and 43. Pairs in clusters of one CTA are off: 1024 rows of 32 heads 25 and 33.
+constexpr int kJoinCost = 6;
+constexpr int kFullCtas = 85;  // of the split form, whose blocks take a CTA 0.8 us by itself: more share the HBM's rate
+// What the partial rows of cut items cost, in blocks, where the choice is whole items in the line: with 3, 8 x 95 rows of 28/4 heads behind
+// 2048 keys 40.0 us for 37.5; with 8, 2048 rows of 28/4 heads 67.5 for 59.7.
+constexpr int kCutCost = 5;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;  // stream t: scores at columns [128 t, + 128), O at [256 + 128 t, + D)
 constexpr uint32_t kDescHi = sdesc_hi(1024);
@@ -895,7 +902,7 @@ cudaError_t setup_tiles() {
   return e;
 }
 
-int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, const Device& d) {
+int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, bool ragged, const Device& d) {
   const bool pair = rows_max > nr;
   const int64_t step = pair ? 2 * nr : nr, items = static_cast<int64_t>(p.B) * p.Hkv * ((rows_max + step - 1) / step);
   if (items > d.sms) return 0;
@@ -903,7 +910,7 @@ int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w,
   int64_t keys = scope_hi(p);
   if (w != nullptr) keys = std::min<int64_t>(keys, static_cast<int64_t>(w->left) + w->right + w->sinks + rows_max + 2 * kBlockN);
   const int64_t blocks = (keys + kBlockN - 1) / kBlockN;
-  return S > 1 && (blocks + S - 1) / S <= (items * blocks + d.sms - 1) / d.sms + kCutCost ? S : 0;
+  return (S > 1 || !pair) && cluster_pays(d, items, S, blocks, pair ? d.sms : kFullCtas, kJoinCost, ragged) ? S : 0;
 }
 
 template <int D>

@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "ec_common.cuh"
 #include "ec_internal.h"
 
@@ -171,11 +173,19 @@ inline int cluster_for(const Device& d, int64_t items) {
   while (S > 1 && d.clusters[S] < items) --S;
   return S;
 }
-int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, const Device& d);
+// Whether each of `items` items of `steps` steps goes to a cluster of S CTAs and is joined there, or all stand in the line, at the cost
+// of a second launch and its join, `join` steps of a full GPU. `full` CTAs and more share the HBM's rate, fewer take their own.
+// Where only the device knows which sequences are long (`ragged`), one long one may be all that a cluster's call waits for: clusters only
+// where that is no more than the join costs again.
+inline bool cluster_pays(const Device& d, int64_t items, int S, int64_t steps, int64_t full, int64_t join, bool ragged) {
+  const int64_t each = (steps + S - 1) / S;
+  return ragged ? each * full <= 2 * join * d.sms : each * std::max(items * S, full) <= items * steps + join * d.sms;
+}
+int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, bool ragged, const Device& d);
 // attention_paged_tiles.cu: tiles of nr positions, nr times the heads of a KV head at most 128 packed rows.
 constexpr int kTileRows = 128;
 cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, int cluster, cudaStream_t s);
-int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, const Device& d);
+int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, bool ragged, const Device& d);
 // A CTA leaves two cut items at most, one that goes on in it and one that begins there: slots
 // 2 tiles cta + tile and 2 tiles cta + tiles + tile, with one tile or two beside each other.
 EC_DEV int64_t part_slot(int first_cta, int i, int tiles, int tile) {
