@@ -175,6 +175,26 @@ EC_DEV bool all_in(int near, int lo, int hi, int j0, int count) { return j0 + co
 EC_DEV bool some_in(int near, int lo, int hi, int j0, int count) { return j0 < near || (j0 < hi && j0 + count > lo); }
 
 // CLUSTER: an item a cluster; else shares of the line.
+// Four lanes beside each other hold a row each, in four pieces of 16 bytes; after it lane q of them holds piece q of the
+// four rows. A store of 16 bytes then goes to 64 together in each of 8 rows: to 32 rows of a lane each, the stores of an item's end
+// took some 6000 cycles.
+EC_DEV void turn_quads(uint32_t (&w)[4][4], int lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[i][e] : w[i | bit][e], bit);
+        if (up) w[i][e] = got;
+        else w[i | bit][e] = got;
+      }
+    }
+  }
+}
+
 template <int D, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Args a, int nr, int groups) {
   using LY = Layout<D, PAIR>;
@@ -655,7 +675,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
                   m_used = mx;
                 } else {
                   const bool rescale = mx > m_used + kRescaleLog2;
-                  if (__any_sync(0xffffffffu, rescale)) {
+                  // (a row without a weight so far has zeros in O: a window's first half block may be all masked)
+                  if (!__any_sync(0xffffffffu, rescale && (!masked || m_used != -INFINITY))) {
+                    if (rescale) m_used = mx;
+                  } else {
                     // O is at rest at a block's first half, as its scores came after the last P V; at its second half
                     // the first one's P V may be under way
                     if (h == 0) ok = wait_w(&bars->pv_half[st], used & 1u);
@@ -715,16 +738,23 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       const bool complete = !CLUSTER && it.part < 0;
       // slots of a CTA: [item goes on here, item begins here][tile]
       const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (it.part > 0 ? 1 : 0)) * kTiles + (PAIR ? st : 0);
-      uint16_t* const orow = a.out + ((static_cast<int64_t>(it.b) * s.rows_max + r) * s.Hq + it.kvh * s.g + (row - rl * s.g)) * D;
+      // out's rows of the four lanes that trade pieces of their rows; -1: not written
+      const int mine = good ? (it.b * s.rows_max + r) * s.Hq + it.kvh * s.g + (row - rl * s.g) : -1;
+      int orow[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) orow[i] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + i);
       // a slot is [D / 4][128] quads of columns, neighbouring rows side by side
       float4* const prow = reinterpret_cast<float4*>(a.part_o) + slot * (kBlockM * (D / 4)) + row;
       auto store = [&](const float (&y)[32], int col) {
-        if (complete && good) {
+        if (complete) {
+          uint32_t w[4][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(orow + col + 8 * e) =
-                make_uint4(pack_bf16x2(y[8 * e], y[8 * e + 1]), pack_bf16x2(y[8 * e + 2], y[8 * e + 3]),
-                           pack_bf16x2(y[8 * e + 4], y[8 * e + 5]), pack_bf16x2(y[8 * e + 6], y[8 * e + 7]));
+          for (int e = 0; e < 16; ++e) w[e >> 2][e & 3] = pack_bf16x2(y[2 * e], y[2 * e + 1]);
+          turn_quads(w, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (orow[i] >= 0)
+              *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(orow[i]) * D + col + 8 * (lane & 3)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
         } else if (CLUSTER && !complete) {
           const uint32_t dst = smem_u32(smem + LY::kUnitOff) + ((PAIR ? st * kBlockM : 0) + row) * LY::kJoinPitch + col * 4;
 #pragma unroll
