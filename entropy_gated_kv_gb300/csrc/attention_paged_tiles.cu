@@ -51,6 +51,10 @@ constexpr int kFullCtas = 85;  // of the split form, whose blocks take a CTA 0.8
 // What the partial rows of cut items cost, in blocks, where the choice is whole items in the line: with 3, 8 x 95 rows of 28/4 heads behind
 // 2048 keys 40.0 us for 37.5; with 8, 2048 rows of 28/4 heads 67.5 for 59.7.
 constexpr int kCutCost = 5;
+// An item takes a CTA two blocks' time beside its own, for the first scores, the last weights and O. In the line it counts so many units
+// more, in front of its blocks: 16384 rows in windows, where the first groups see half as many blocks as the others, 409 us without and 401 so,
+// 8 x 95 rows of 28/4 heads, ragged, 32.0 and 30.5; with three 31.8.
+constexpr int kItemCost = 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;  // stream t: scores at columns [128 t, + 128), O at [256 + 128 t, + D)
 constexpr uint32_t kDescHi = sdesc_hi(1024);
@@ -77,7 +81,7 @@ struct Bars {
   uint32_t tmem_base;
   int abort;
   int scan[kThreads / 32], most[kThreads / 32];
-  int begin[4], share;  // b, group, KV head, block of the CTA's first item
+  int begin[4], share;  // b, group, KV head, unit of the CTA's first item
 };
 
 template <int D, bool PAIR>
@@ -136,6 +140,11 @@ EC_DEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+EC_DEV uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 EC_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -169,6 +178,8 @@ EC_DEV Group load_group(const Shape& s, int b, int grp, int step, bool tell) {
   q.blocks = q.rows > 0 ? max(1, q.k.count) : 0;  // rows without a key are written too
   return q;
 }
+
+EC_DEV int units_of(const Group& g) { return g.blocks > 0 ? g.blocks + kItemCost : 0; }
 
 // Keys j0 .. j0 + count - 1 are all of the hull, or some of them.
 EC_DEV bool all_in(int near, int lo, int hi, int j0, int count) { return j0 + count <= near || (j0 >= lo && j0 + count <= hi); }
@@ -245,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   pdl_wait();  // everything above overlaps the previous kernel
   pdl_launch_dependents();
 
-  int share = 0, left = 0, place[4] = {0, 0, 0, 0};  // the CTA's first item: sequence, group, KV head, block; blocks from there on
+  int share = 0, left = 0, place[4] = {0, 0, 0, 0};  // the CTA's first item: sequence, group, KV head, unit; units from there on
   bool whole = false;
   if constexpr (CLUSTER) {
     const int item = blockIdx.x / cluster_size(), pair = item / s.Hkv;
@@ -260,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     int mine = 0, longest = 0;
 #pragma unroll 2
     for (int i = p0; i < min(p0 + per, pairs); ++i) {
-      const int b = i / groups, blocks = load_group(s, b, i - b * groups, step, blockIdx.x == 0).blocks;
-      mine += blocks * s.Hkv;
-      longest = max(longest, blocks);
+      const int b = i / groups, units = units_of(load_group(s, b, i - b * groups, step, blockIdx.x == 0));
+      mine += units * s.Hkv;
+      longest = max(longest, units);
     }
     int incl = warp_inclusive(mine);
     longest = __reduce_max_sync(0xffffffffu, longest);
@@ -285,12 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     if (begin < total && begin >= incl - mine && begin < incl) {
       int off = begin - (incl - mine);
       for (int i = p0;; ++i) {
-        const int b = i / groups, blocks = load_group(s, b, i - b * groups, step, false).blocks;
-        if (off < blocks * s.Hkv) {
-          bars->begin[0] = b, bars->begin[1] = i - b * groups, bars->begin[2] = off / blocks, bars->begin[3] = off % blocks;
+        const int b = i / groups, units = units_of(load_group(s, b, i - b * groups, step, false));
+        if (off < units * s.Hkv) {
+          bars->begin[0] = b, bars->begin[1] = i - b * groups, bars->begin[2] = off / units, bars->begin[3] = off % units;
           break;
         }
-        off -= blocks * s.Hkv;
+        off -= units * s.Hkv;
       }
     }
     __syncthreads();
@@ -335,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const int box = min(kBlockN, 1 << s.page_shift);   // rows of a TMA box
     const int boxes = kBlockN / box;                   // boxes of a block's rows: 1, 2, 4 or 8
     const int atoms = box < kBlockN ? LY::kAtoms : 1;  // boxes beside each other
+    constexpr int kLead = CLUSTER ? 0 : kItemCost;
     int b = place[0], grp = place[1], kvh = place[2], u = place[3];
     Group g{};
     if constexpr (CLUSTER) {
@@ -357,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       } while (g.blocks == 0);
     };
     if (whole && u > 0) {  // an item of the CTA before
-      left -= g.blocks - u;
+      left -= g.blocks + kLead - u;
       u = 0;
       if (left > 0) next_group();
     }
@@ -366,13 +378,15 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 #pragma unroll 1
     for (int count = 0;; ++count) {
       Item it;
-      it.nblk = ok && left > 0 ? (whole ? g.blocks : min(g.blocks - u, left)) : 0;
+      const int size = g.blocks + kLead, take = whole ? size : min(size - u, left);
+      it.v0 = max(u - kLead, 0);
+      it.nblk = ok && left > 0 ? max(u + take - kLead, 0) - it.v0 : 0;  // 0, too, where the share ends before the item's first block
       if (it.nblk > 0) {
-        it.b = b, it.kvh = kvh, it.v0 = u;
+        it.b = b, it.kvh = kvh;
         it.near_blocks = g.k.near, it.first = g.k.first;
         it.near = g.h.near, it.lo = g.h.lo, it.hi = g.h.hi, it.n = g.n;
         it.r0 = grp * step, it.rows0 = min(nr, g.rows), it.rows1 = g.rows - it.rows0;
-        it.part = it.nblk == g.blocks ? -1 : u == 0 ? 1 : 0;
+        it.part = it.nblk == g.blocks ? -1 : it.v0 == 0 ? 1 : 0;
       }
       ok = wait_w(&bars->item_empty[count % kItems], ((count / kItems) & 1) ^ 1);
       if (!ok) it.nblk = 0;
@@ -382,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       }
       if (it.nblk == 0) break;
       if (!CLUSTER && it.part == 1 && lane < kTiles) {  // the item begins here and goes on in the next CTAs
-        const int rest = g.blocks - it.nblk;
+        const int rest = size - u - take;
         Record r{};
         r.rows = (lane == 0 ? it.rows0 : it.rows1) * s.g;
         r.parts = r.rows > 0 ? 1 + (rest + share - 1) / share : 0;
@@ -427,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         if (ring == 0) k0.next(), v0.next();
         else k1.next(), v1.next();
       }
-      left -= it.nblk;
+      left -= take;
       u = 0;
       if (CLUSTER) left = 0;
       if (left > 0) next_group();
@@ -781,15 +795,26 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             if constexpr (CLUSTER) reinterpret_cast<float2*>(smem + st * LY::kTileBytes)[row] = mine;  // the queries have been read
             else a.part_stat[slot * kBlockM + row] = mine;
           }
+          const bool empty = __any_sync(0xffffffffu, l_sum == 0.f);  // a row without a key, whose O may hold 0 x infinity
+          const uint64_t f2 = pack_f32x2(f, f);
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o);
-            EC_TMEM_WAIT32(o);
-            float y[32];
+          for (int c = 0; c < D / 32; c += 2) {
+            uint32_t o[2][32];
+            EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32, o[0]);
+            EC_TMEM_LD32(tmem + lane_off + kTmemO + st * 128 + c * 32 + 32, o[1]);
+            EC_TMEM_WAIT32(o[0]);
+            EC_TMEM_WAIT32(o[1]);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = l_sum == 0.f ? 0.f : __uint_as_float(o[e]) * f;
-            store(y, c * 32);
+            for (int k = 0; k < 2; ++k) {
+              float y[32];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(o[k][e]), __uint_as_float(o[k][e + 1])), f2), y[e], y[e + 1]);
+              if (empty)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = l_sum == 0.f ? 0.f : y[e];
+              store(y, (c + k) * 32);
+            }
           }
           tc_fence_before();
         }
