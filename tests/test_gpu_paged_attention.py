@@ -87,6 +87,29 @@ def test_window_attention(E, B, L, Hq, Hkv, D, page, Rs, lens, window, at):
     P.Case(B, L, Hq, Hkv, D, page, Rs, lens, window, at, seed=L + B).run(E)
 
 
+# Clusters of one CTA, clusters with many blocks each, the same sizes with lengths that only the device knows.
+@pytest.mark.parametrize("lens", [None, "ragged"])
+@pytest.mark.parametrize("B,L,Hq,Hkv,D,R", [
+    (4, 300, 32, 32, 64, 20), (4, 1024, 32, 32, 64, 20), (4, 2300, 28, 28, 64, 20), (3, 500, 32, 32, 64, 1), (3, 1100, 32, 32, 128, 1),
+    (1, 9000, 32, 32, 64, 95), (1, 9000, 8, 8, 64, 300), (16, 1100, 28, 4, 64, 18)])
+def test_clusters(E, B, L, Hq, Hkv, D, R, lens):
+    lens = None if lens is None else [(L - 7 * b * b * b) % (L + 1) for b in range(B)]
+    P.Case(B, L, Hq, Hkv, D, 16 if R == 1 else 64, [R] * B, lens, at=None, kind="split", seed=L).run(E)
+
+
+# A line whose shares end anywhere: in the middle of an item, before its first block, at its end.
+@pytest.mark.parametrize("R", [1, 30, 130])
+@pytest.mark.parametrize("seed", range(8))
+def test_shares_of_the_line(E, R, seed):
+    rng = np.random.default_rng(seed)
+    B, L = int(rng.integers(20, 42)), int(rng.choice([100, 130, 400, 900, 1300]))
+    R = min(R, L)  # more rows than positions are refused
+    lens = [int(x) for x in rng.integers(0, L + 1, B) * (rng.random(B) < 0.9)]
+    rows = [int(x) for x in rng.integers(0, R + 1, B)]
+    rows[0] = R
+    P.Case(B, L, 8, 8, 64, 32, rows, lens, at=None, kind="split", seed=seed).run(E)
+
+
 @pytest.mark.parametrize("pos,window", [
     ([[0, 1, 298, 299]], (3, 3, 0)),           # rows far from each other: keys between them that no row sees
     ([[5, 5, 5, 200]], (40, 0, 9)),            # the same position more than once
