@@ -661,6 +661,8 @@ def kv_append_paged(p: Params, cache: PagedCache, k_new, v_new, R, idx=None, sta
     [L, D / 2], None: rows are copied. Returns q_out, a new tensor of zeros by default. See
     ec_kv_append_paged."""
     c = _pages_of(p, cache)
+    if k_new.dim() != 4:
+        raise ValueError(f"k_new must be [B, rows, Hkv, D], got {list(k_new.shape)}")
     i, B, rows, D = c.index, p.B, k_new.shape[1], p.D
     shape = (B, rows, p.Hkv, D)
     kv = _row_view(k_new, "k_new", shape, i) + _row_view(v_new, "v_new", shape, i)

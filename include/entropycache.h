@@ -451,7 +451,8 @@ ec_status ec_prefix_attention(const ec_params* p, const void* q, const ec_kv* pr
  *                row j % page_size of page table[b, j / page_size]. Entries of positions that no
  *                call touches may hold anything. Two sequences may read the same page.
  * A page number outside [0, n_pages) sets EC_DEVERR_BAD_PAGE; its rows are not written, and are read
- * as zeros. */
+ * as zeros. EC_ERR_UNSUPPORTED for another page_size, a page_stride of 2^36 or more, and pools that span more
+ * than 2^40 bytes. */
 typedef struct ec_paged_kv {
   int32_t page_size, n_pages;
   int64_t page_stride;
@@ -482,7 +483,7 @@ typedef struct ec_rows {
  * below its successor sets EC_DEVERR_BAD_IDX and its row is skipped. start int32 [B] on the device.
  * A position outside [0, L) sets EC_DEVERR_BAD_IDX, an R outside [0, rows_max] EC_DEVERR_BAD_R; the row,
  * the sequence is skipped (a row whose page is bad still writes q_out). Pages that the call writes belong to
- * one sequence and stand once in its table. 1 <= rows_max <= L; D 64 or 128. The caches and q_out must not
+ * one sequence and stand once in its table. 1 <= rows_max <= L; D 64 or 128; EC_ERR_UNSUPPORTED for Hq * D above 2^26. The caches and q_out must not
  * overlap each other or the other buffers (EC_ERR_INVALID_ARG). */
 ec_status ec_kv_append_paged(const ec_params* p, const ec_paged_kv* cache, int32_t rows_max, const ec_rows* k_new,
                              const ec_rows* v_new, const ec_rows* q_new, void* q_out, const float* rope_cos,
@@ -500,7 +501,9 @@ ec_status ec_kv_append_paged(const ec_params* p, const ec_paged_kv* cache, int32
  * NaN included, nor the table's entries there.
  * kv_len int32 [B] on the device, or NULL. A length outside [0, L] sets EC_DEVERR_BAD_LEN, an R outside
  * [0, rows_max] EC_DEVERR_BAD_R; the sequence is skipped. EC_ERR_UNSUPPORTED for B * rows_max * Hq of
- * 2^31 or more. scale must be above 0 and at most 2e38.
+ * 2^31 or more, and for B * Hkv * tiles * (L / 128 + 2) above 2^30 (tiles: of 128 query rows, rows_max * Hq / Hkv of
+ * them). A wait inside the kernel that does not end sets EC_DEVERR_TIMEOUT; out is not complete then. scale must
+ * be above 0 and at most 2e38.
  * ws: ec_paged_attention_workspace_size(p, rows_max) bytes, 16-byte aligned, no initial contents needed;
  * calls that share it must not overlap in time. It must not overlap the other buffers, nor out the inputs
  * (EC_ERR_INVALID_ARG). Products, sums and rounding as ec_partial_attention; no atomics: the same inputs

@@ -366,6 +366,15 @@ def test_append_binding_checks(E):
             f()
 
 
+def test_append_of_no_rows_array(E):
+    c = Append(2, 64, 4, 2, 64, 16, [5, 5], "idx", rows=6, seed=1)
+    d = c.inputs(E)
+    q, k, v = c.parts
+    for x in (k.flatten(), k[0], k[:, 0, 0, 0], k[None]):
+        with pytest.raises(ValueError):
+            E.kv_append_paged(d["p"], d["cache"], x, v, d["R"])
+
+
 def test_far_pages_are_written(E):
     """Rows of pages past 2^31 elements of the pool."""
     page, H, D = 1024, 2, 128
