@@ -11,12 +11,13 @@
 //   - split (every sequence has one tile): the streams take the even and the odd key blocks of the tile and are
 //     joined at the item's end.
 // The streams take turns at the tensor cores, P V and next scores in one piece: left to themselves they
-// fall into step, both in the softmax, then both at the tensor cores (3820 cycles a pair of blocks for 3300; 4 full steps
-// of 2048 rows, 28/4 heads, 210 us for the 178 of today). What a pair of blocks is bound by: a stream's own chain, softmax 1700
-// cycles (64 exponentials of a row take a lone warp 490, two warps of a scheduler 590 together), P V and scores 1000, and
-// some 600 between them, as a wait takes 120 to 200 cycles also when it is over. Tried beside that: score buffers
-// of 64 keys, two a stream (210 us: as many waits for half the product), one issuer for both streams (222 us), sixteen
-// softmax warps (204 us, with 104 registers each), all 128 scores in registers (180 us, but 3 to 5% slower in the split form).
+// fall into step, both in the softmax, then both at the tensor cores (4 full steps of 2048 rows, 28/4 heads, 210 us for 182).
+// 4 such steps take 172 us now, 1390 TFLOP/s, a pair of blocks 3010 cycles. What bounds them: a stream's own chain, softmax 1690
+// cycles (64 exponentials of a row take a lone warp 490, two warps of a scheduler 590 together), then 1330 until the next
+// scores are there, of which P V and scores are 1000, as a wait takes 120 to 200 cycles also when it is over; and an item's end
+// and begin, another 6000. Tried when they took 182: score buffers of 64 keys, two a stream (210 us: as many waits for half the product), one
+// issuer for both streams (222 us), sixteen softmax warps (204 us, with 104 registers each), all 128 scores in registers (180 us, but 3 to
+// 5% slower in the split form). An L2 prefetch of the next item's queries took 1.5 us off 172 and cost windows 3 of 398.
 // Blocks are 128 keys, brought in by TMA: one box of 128 rows, or of a smaller page, from the page that the table
 // names. The blocks of all items (sequence, group of tiles, KV head) stand in one line of
 // which the CTAs, one an SM, take equal shares; an item cut between CTAs leaves fp32 partial rows, which a second
@@ -187,8 +188,8 @@ EC_DEV bool some_in(int near, int lo, int hi, int j0, int count) { return j0 < n
 
 // CLUSTER: an item a cluster; else shares of the line.
 // Four lanes beside each other hold a row each, in four pieces of 16 bytes; after it lane q of them holds piece q of the
-// four rows. A store of 16 bytes then goes to 64 together in each of 8 rows: to 32 rows of a lane each, the stores of an item's end
-// took some 6000 cycles.
+// four rows. A store of 16 bytes then goes to 64 together in each of 8 rows. (A piece of a row of its own from each lane: 178 us for 172 on
+// 4 full steps of 2048 rows, 444 for 405 on 16384 rows in windows.)
 EC_DEV void turn_quads(uint32_t (&w)[4][4], int lane) {
 #pragma unroll
   for (int bit = 1; bit <= 2; bit <<= 1) {
