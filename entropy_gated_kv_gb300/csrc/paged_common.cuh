@@ -155,7 +155,7 @@ EC_DEV void st_shared16(uint32_t dst, uint4 v) {
 
 // attention_paged_rows.cu: at most kFewRows packed rows (positions times the heads of a KV head) a sequence, the rows of
 // one mma.sync tile. (With two such tiles a warp the products bound it: 8 x 32 rows of 32 heads behind 2048 keys, ragged,
-// 66 us there and 48 as tiles of 128; 4 rows of 28/4 heads behind 2048 keys 12.0 and 8.8.)
+// 66 us there and 46 as tiles of 128; 4 rows of 28/4 heads behind 2048 keys 12.0 and 8.8.)
 constexpr int kFewRows = 16;
 // cluster 0: shares of the line, partial rows where items are cut; else a cluster of so many CTAs for each item.
 cudaError_t launch_few_rows(const Args& a, int D, int ctas, int cluster, cudaStream_t s);
