@@ -110,6 +110,27 @@ def test_shares_of_the_line(E, R, seed):
     P.Case(B, L, 8, 8, 64, 32, rows, lens, at=None, kind="split", seed=seed).run(E)
 
 
+@pytest.mark.parametrize("R", [1, 60, 300])
+@pytest.mark.parametrize("seed", range(6))
+def test_shares_of_the_line_in_windows(E, R, seed):
+    rng = np.random.default_rng(100 + seed)
+    B, L = int(rng.integers(20, 42)), int(rng.choice([130, 700, 1500]))
+    R = min(R, L)
+    lens = [int(x) for x in rng.integers(1, L + 1, B)]
+    rows = [min(n, int(x)) for n, x in zip(lens, rng.integers(0, R + 1, B))]
+    window = (int(rng.choice([0, 50, 400])), int(rng.choice([0, 50, -1])), int(rng.choice([0, 3, 200])))
+    P.Case(B, L, 8, 8, 64, 32, rows, lens, window, at="idx" if seed % 2 else "start", rows=R, seed=seed).run(E)
+
+
+@pytest.mark.parametrize("R", [1, 20, 150])
+@pytest.mark.parametrize("window", [None, (-1, 0, 0)])
+def test_sequences_that_share_pages(E, R, window):
+    c = P.Case(3, 700, 8, 4, 64, 32, [R, R, 1], [700, 500, 130], window, at="start", kind="one", seed=R)
+    c.k[1:, :128], c.v[1:, :128] = c.k[0, :128], c.v[0, :128]  # a prefix of four pages
+    c.pool.table[1:, :4] = c.pool.table[0, :4]
+    c.run(E)
+
+
 @pytest.mark.parametrize("pos,window", [
     ([[0, 1, 298, 299]], (3, 3, 0)),           # rows far from each other: keys between them that no row sees
     ([[5, 5, 5, 200]], (40, 0, 9)),            # the same position more than once
