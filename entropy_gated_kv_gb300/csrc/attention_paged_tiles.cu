@@ -18,6 +18,8 @@
 // and begin, another 6000. Tried when they took 182: score buffers of 64 keys, two a stream (210 us: as many waits for half the product), one
 // issuer for both streams (222 us), sixteen softmax warps (204 us, with 104 registers each), all 128 scores in registers (180 us, but 3 to
 // 5% slower in the split form). An L2 prefetch of the next item's queries took 1.5 us off 172 and cost windows 3 of 398.
+// For the 172 also tried: the weights of the first half in two quarters (177: a wait more), waits that poll (182), every fourth
+// exponential by a polynomial of degree 3 (177: issue slots bind, not the exponentials' unit).
 // Blocks are 128 keys, brought in by TMA: one box of 128 rows, or of a smaller page, from the page that the table
 // names. The blocks of all items (sequence, group of tiles, KV head) stand in one line of
 // which the CTAs, one an SM, take equal shares; an item cut between CTAs leaves fp32 partial rows, which a second
