@@ -624,8 +624,8 @@ def _pages_of(p: Params, cache: PagedCache) -> _Pages:
     return c
 
 
-def _row_view(t, name: str, shape: tuple, index: int) -> tuple:
-    """The fields of the ec_rows of t, bf16 of that shape [B, rows, heads, D] with adjacent heads."""
+def _row_view(t, name: str, shape: tuple, index: int) -> bytes:
+    """The ec_rows of t, bf16 of that shape [B, rows, heads, D] with adjacent heads."""
     if t.dtype is not torch.bfloat16 or t.shape != shape:
         raise ValueError(f"{name} must be bf16 {list(shape)}, got {t.dtype} {list(t.shape)}")
     if t.get_device() != index:
@@ -634,7 +634,7 @@ def _row_view(t, name: str, shape: tuple, index: int) -> tuple:
     sb, sr, sh, sd = t.stride()
     if sd != 1 or (sh != D and heads > 1):
         raise ValueError(f"the heads of a row of {name} must be adjacent")
-    return t.data_ptr(), (sb if B > 1 else 0), (sr if rows > 1 else heads * D)
+    return C.ROWS.pack(t.data_ptr(), sb if B > 1 else 0, sr if rows > 1 else heads * D)
 
 
 def _places(p: Params, idx, start, rows: int, index: int):
@@ -665,18 +665,14 @@ def kv_append_paged(p: Params, cache: PagedCache, k_new, v_new, R, idx=None, sta
         raise ValueError(f"k_new must be [B, rows, Hkv, D], got {list(k_new.shape)}")
     i, B, rows, D = c.index, p.B, k_new.shape[1], p.D
     shape = (B, rows, p.Hkv, D)
-    kv = _row_view(k_new, "k_new", shape, i) + _row_view(v_new, "v_new", shape, i)
+    kr, vr = _row_view(k_new, "k_new", shape, i), _row_view(v_new, "v_new", shape, i)
     if q_new is None:
         if q_out is not None:
             raise ValueError("q_out without q_new")
-        x = C.EcRows3(*kv)
-        at = ctypes.addressof(x)
         qr = op = None
     else:
         shape = (B, rows, p.Hq, D)
-        x = C.EcRows3(*kv, *_row_view(q_new, "q_new", shape, i))
-        at = ctypes.addressof(x)
-        qr, op = at + 48, None if q_out is None else _checked(q_out, "q_out", torch.bfloat16, shape, i)
+        qr, op = _row_view(q_new, "q_new", shape, i), None if q_out is None else _checked(q_out, "q_out", torch.bfloat16, shape, i)
     rp = _checked(R, "R", torch.int32, (B,), i)
     ip, si, sp = _places(p, idx, start, rows, i)
     cs = sn = None
@@ -687,14 +683,14 @@ def kv_append_paged(p: Params, cache: PagedCache, k_new, v_new, R, idx=None, sta
     ep = None if dev_err is None else _checked(dev_err, "dev_err", torch.int32, (1,), i)
     f = lib().ec_kv_append_paged
     if stream is None and (op is not None or qr is None) and torch._C._cuda_getDevice() == i:
-        st = f(p.ref(), c.ref, rows, at, at + 24, qr, op, cs, sn, ip, si, sp, rp, ep, torch._C._cuda_getCurrentRawStream(i))
+        st = f(p.ref(), c.ref, rows, kr, vr, qr, op, cs, sn, ip, si, sp, rp, ep, torch._C._cuda_getCurrentRawStream(i))
     else:
         def call(s):
             nonlocal q_out
             if q_new is not None and q_out is None:
                 q_out = torch.zeros(B, rows, p.Hq, D, dtype=torch.bfloat16, device=q_new.device)
             o = None if q_out is None else q_out.data_ptr()
-            return f(p.ref(), c.ref, rows, at, at + 24, qr, o, cs, sn, ip, si, sp, rp, ep, s)
+            return f(p.ref(), c.ref, rows, kr, vr, qr, o, cs, sn, ip, si, sp, rp, ep, s)
 
         st = _launch(i, stream, call)
     C.check(st, "ec_kv_append_paged")

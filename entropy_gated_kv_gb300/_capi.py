@@ -5,6 +5,7 @@ Loading fails loudly when the in-tree library has not been built: there is no fa
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "libentropycache.so"
@@ -74,10 +75,8 @@ class EcRows(ctypes.Structure):
     _fields_ = [("x", _p), ("batch_stride", _i64), ("row_stride", _i64)]
 
 
-class EcRows3(ctypes.Structure):
-    """Three ec_rows behind one another."""
-
-    _fields_ = [(f"{n}{i}", t) for i in range(3) for n, t in EcRows._fields_]
+ROWS = struct.Struct("@Pqq")  # an ec_rows as bytes, which a call takes in a pointer's place: made faster than a Structure
+assert ROWS.size == ctypes.sizeof(EcRows)
 
 
 # name -> (restype, argtypes)
