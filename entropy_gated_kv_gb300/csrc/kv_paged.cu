@@ -24,8 +24,8 @@ constexpr int kThreads = 192;
 constexpr int kInFlight = 2;
 
 struct AppendArgs {
-  int32_t L, Hq, Hkv, rows_max, page_shift, n_pages, pieces, rows_per_cta;
-  FastDiv per_row;  // pieces of a row
+  int32_t L, Hq, Hkv, rows_max, page_shift, n_pages;
+  RowSplit split;
   int64_t page_stride, table_stride;
   ec_rows k, v, q;
   uint16_t *kp, *vp, *q_out;
@@ -40,7 +40,7 @@ struct AppendArgs {
 template <int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int T = D / 16;
-  const int b = blockIdx.y, r0 = blockIdx.x * a.rows_per_cta;
+  const int b = blockIdx.y, r0 = blockIdx.x * a.split.rows_per_cta;
   pdl_wait();  // the rows, idx and R may come from the previous kernels in the stream
   pdl_launch_dependents();
   const int Rb = __ldg(a.R + b);
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     if (r0 == 0 && threadIdx.x == 0) report_error(a.dev_err, EC_DEVERR_BAD_R);
     return;
   }
-  const int n = min(a.rows_per_cta, Rb - r0) * a.pieces;
+  const int n = a.split.count(r0, Rb);
   const int nq = a.q_out != nullptr ? a.Hq : 0;
   for (int base = threadIdx.x; base < n; base += kInFlight * kThreads) {
     uint4 lo[kInFlight], hi[kInFlight];
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     for (int i = 0; i < kInFlight; ++i) {
       const int u = base + i * kThreads;
       if (u < n) {
-        const int rl = a.per_row(u), w = u - rl * a.pieces, h = w / T, t = w % T, r = r0 + rl;
+        const int rl = a.split.per_row(u), w = u - rl * a.split.pieces, h = w / T, t = w % T, r = r0 + rl;
         const bool is_q = h < nq;
         const bool is_k = !is_q && h < nq + a.Hkv;
         const ec_rows& x = is_q ? a.q : is_k ? a.k : a.v;
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     for (int i = 0; i < kInFlight; ++i) {
       const int u = base + i * kThreads;
       if (u >= n) break;
-      const int rl = a.per_row(u), w = u - rl * a.pieces, h = w / T, t = w % T, r = r0 + rl;
+      const int rl = a.split.per_row(u), w = u - rl * a.split.pieces, h = w / T, t = w % T, r = r0 + rl;
       const int64_t raw = raw_position(a.at, b, r);
       const int pos = inside(raw, a.L) ? static_cast<int>(raw) : -1;
       // a position given twice would be written by two rows at once
@@ -128,13 +128,11 @@ cudaError_t launch_kv_append_paged(const ec_params& p, const ec_paged_kv& c, int
   a.L = p.L, a.Hq = p.Hq, a.Hkv = p.Hkv, a.rows_max = rows_max;
   while ((1 << a.page_shift) < c.page_size) ++a.page_shift;
   a.n_pages = c.n_pages, a.page_stride = c.page_stride, a.table_stride = c.table_stride;
-  a.pieces = ((q_out != nullptr ? p.Hq : 0) + 2 * p.Hkv) * (p.D / 16);
-  a.per_row.set(a.pieces);
-  a.rows_per_cta = std::min(rows_max, std::max(1, kInFlight * kThreads / a.pieces));
+  a.split.set(rows_max, ((q_out != nullptr ? p.Hq : 0) + 2 * p.Hkv) * (p.D / 16), kInFlight * kThreads);
   a.k = k, a.v = v, a.q = q;
   a.kp = static_cast<uint16_t*>(c.k), a.vp = static_cast<uint16_t*>(c.v), a.q_out = static_cast<uint16_t*>(q_out);
   a.cs = cs, a.sn = sn, a.table = c.table, a.R = R, a.at = at, a.dev_err = dev_err;
-  const dim3 grid((rows_max + a.rows_per_cta - 1) / a.rows_per_cta, p.B);
+  const dim3 grid((rows_max + a.split.rows_per_cta - 1) / a.split.rows_per_cta, p.B);
   return launch_pdl(p.D == 64 ? append_kernel<64> : append_kernel<128>, grid, dim3(kThreads), 0, s, a);
 }
 

@@ -45,6 +45,21 @@ struct Args {
   Record* records;    // [CTAs]
 };
 
+// How the append's rows fall to its CTAs: rows of `pieces` pieces each, as many to a CTA as make `at_once` pieces, one at
+// least.
+struct RowSplit {
+  int32_t pieces, rows_per_cta;
+  FastDiv per_row;
+  void set(int32_t rows_max, int32_t row_pieces, int32_t at_once) {
+    pieces = row_pieces;
+    rows_per_cta = std::min(rows_max, std::max(1, at_once / row_pieces));
+    per_row.set(row_pieces);
+  }
+  // Pieces of the CTA whose rows begin at r0, of `rows` in all; at most pieces or at_once. A CTA past the last row has none:
+  // rows - r0 times pieces would leave 32 bits there.
+  EC_DEV int count(int r0, int rows) const { return r0 < rows ? min(rows_per_cta, rows - r0) * pieces : 0; }
+};
+
 // Position of row r of sequence b; it may lie outside [0, L).
 EC_DEV int64_t raw_position(const RowPlaces& at, int b, int r) {
   if (at.idx != nullptr) return __ldg(at.idx + b * at.stride + r);

@@ -75,6 +75,7 @@ inline float __uint_as_float(unsigned v) {
   std::memcpy(&f, &v, 4);
   return f;
 }
+inline float __int_as_float(int v) { return __uint_as_float(static_cast<unsigned>(v)); }
 inline unsigned __vminu4(unsigned a, unsigned b) {
   unsigned r = 0;
   for (int i = 0; i < 32; i += 8) {

@@ -1,0 +1,36 @@
+"""GPU tests of the paged cache's operators at the ends of what they accept."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def E():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import entropy_gated_kv_gb300 as E
+
+    E.lib()
+    return E
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def test_few_rows_in_a_large_array(E):
+    """Two rows in an array whose rows' pieces, all in all, are more than 2^31: nothing past R is read or written."""
+    rows, Hkv, D, page = 65600, 2048, 128, 16  # 2^15 pieces a row
+    p = E.Params(B=1, L=rows, Hq=Hkv, Hkv=Hkv, D=D, V=8, C_max=1, k=1)
+    x = torch.empty(1, rows, Hkv, D, dtype=torch.bfloat16, device="cuda")  # 34 GB; keys and values are the same rows
+    x[0, :2].normal_()
+    table = torch.full((1, -(-rows // page)), -1, dtype=torch.int32, device="cuda")
+    table[0, 7] = 1
+    cache = E.PagedCache.empty(3, page, Hkv, D, table)
+    err = i32([0])
+    E.kv_append_paged(p, cache, x, x, i32([2]), start=i32([7 * page + 14]), dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0  # any other position has no page
+    for t in (cache.k, cache.v):
+        assert torch.equal(t[1, 14:], x[0, :2])
+        assert not t[0].any() and not t[2].any() and not t[1, :14].any()
