@@ -184,9 +184,10 @@ EC_DEV Group load_group(const Shape& s, int b, int grp, int step, bool tell) {
 
 EC_DEV int units_of(const Group& g) { return g.blocks > 0 ? g.blocks + kItemCost : 0; }
 
-// Keys j0 .. j0 + count - 1 are all of the hull, or some of them.
+// Keys j0 .. j0 + count - 1 are all of the hull, or some of them. (Rows past the last key have an empty one, lo = hi = n, that
+// may lie inside a box.)
 EC_DEV bool all_in(int near, int lo, int hi, int j0, int count) { return j0 + count <= near || (j0 >= lo && j0 + count <= hi); }
-EC_DEV bool some_in(int near, int lo, int hi, int j0, int count) { return j0 < near || (j0 < hi && j0 + count > lo); }
+EC_DEV bool some_in(int near, int lo, int hi, int j0, int count) { return j0 < near || max(j0, lo) < min(j0 + count, hi); }
 
 // CLUSTER: an item a cluster; else shares of the line.
 // Four lanes beside each other hold a row each, in four pieces of 16 bytes; after it lane q of them holds piece q of the
