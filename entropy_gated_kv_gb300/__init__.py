@@ -702,6 +702,9 @@ def paged_attention_workspace_size(p: Params, rows: int) -> int:
     return int(lib().ec_paged_attention_workspace_size(p.ref(), rows))
 
 
+_I32 = (-(1 << 31), (1 << 31) - 1)
+
+
 def _attend_paged(p: Params, q, cache, R, out, places, window, kv_len, scale, ws, dev_err, stream):
     c = _pages_of(p, cache)
     i, B = c.index, p.B
@@ -750,7 +753,10 @@ def paged_window_attention(p: Params, q, cache: PagedCache, R, out, left: int, r
                            kv_len=None, scale: float | None = None, ws: torch.Tensor | None = None, dev_err=None, stream=None):
     """paged_attention where the row at position pos (idx[b, r], or start[b] + r, or r) sees the keys pos - left ..
     pos + right (-1: no bound on that side) and the first `sinks` ones. See ec_paged_window_attention."""
-    return _attend_paged(p, q, cache, R, out, (idx, start), (int(left), int(right), int(sinks)), kv_len, scale, ws, dev_err, stream)
+    window = (int(left), int(right), int(sinks))
+    if min(window) < _I32[0] or max(window) > _I32[1]:  # ctypes would keep their low bits
+        window = tuple(max(_I32[0], min(x, _I32[1])) for x in window)  # past the last position, or refused
+    return _attend_paged(p, q, cache, R, out, (idx, start), window, kv_len, scale, ws, dev_err, stream)
 
 
 @dataclass
