@@ -544,10 +544,12 @@ def prefix_attention(p: Params, q, prefix, cache, R, out, kv_len=None, scale: fl
 class _Pages:
     """The checked C view (ec_paged_kv) of a paged cache."""
 
-    __slots__ = ("c", "ref", "index", "heads", "B", "positions", "at")
+    __slots__ = ("c", "ref", "index", "heads", "B", "positions", "at", "bytes", "_memory")
 
     def __init__(self, k, v, table):
         self.index, self.at = _cuda_index(k, "k"), (k.data_ptr(), v.data_ptr(), table.data_ptr())
+        self._memory = tuple(t.untyped_storage().nbytes for t in (k, v, table))
+        self.bytes = tuple(f() for f in self._memory)
         for t, name in ((k, "k"), (v, "v"), (table, "table")):
             end = t.storage_offset() + 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
             if t.numel() > 0 and end * t.element_size() > t.untyped_storage().nbytes():
@@ -575,6 +577,12 @@ class _Pages:
         self.c = C.EcPagedKv(ps, n, stride, k.data_ptr(), v.data_ptr(), table.data_ptr(), row)
         self.ref = ctypes.byref(self.c)
 
+    def holds(self, k, v, table) -> bool:
+        """Whether the tensors' memory is what it was. Addresses alone do not tell: memory that was given back and taken
+        anew, smaller, may lie where it lay."""
+        kb, vb, tb = self._memory
+        return self.at == (k.data_ptr(), v.data_ptr(), table.data_ptr()) and self.bytes == (kb(), vb(), tb())
+
 
 class PagedCache:
     """One layer's K/V cache in pages (ec_paged_kv): k, v bf16 [n_pages, page_size, Hkv, D] (contiguous
@@ -600,9 +608,9 @@ class PagedCache:
     del _exchange
 
     def view(self) -> _Pages:
-        """The checked C view; made and checked again when a tensor was exchanged or its memory has moved."""
+        """The checked C view; made and checked again when a tensor was exchanged or its memory is another one."""
         c, k, v, t = self._c, self._k, self._v, self._table
-        if c is None or c.at != (k.data_ptr(), v.data_ptr(), t.data_ptr()):
+        if c is None or not c.holds(k, v, t):
             self._c = None
             c = self._c = _Pages(k, v, t)
         return c

@@ -34,3 +34,19 @@ def test_few_rows_in_a_large_array(E):
     for t in (cache.k, cache.v):
         assert torch.equal(t[1, 14:], x[0, :2])
         assert not t[0].any() and not t[2].any() and not t[1, :14].any()
+
+
+def test_storage_that_shrank_where_it_lay(E):
+    """A cache whose memory was given back and taken anew, smaller, may find it at the same address."""
+    torch.cuda.empty_cache()
+    k = torch.zeros(256, 64, 8, 128, dtype=torch.bfloat16, device="cuda")  # 32 MiB
+    v, table = torch.zeros_like(k), torch.zeros(1, 8, dtype=torch.int32, device="cuda")
+    cache = E.PagedCache(k, v, table)
+    for t in (k, v):
+        full = t.untyped_storage().nbytes()
+        t.untyped_storage().resize_(0)
+        t.untyped_storage().resize_(full - full // 4)
+        with pytest.raises(ValueError, match="has become smaller"):
+            cache.view()
+        t.untyped_storage().resize_(full)
+    cache.view()
