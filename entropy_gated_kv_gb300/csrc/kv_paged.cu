@@ -73,9 +73,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       const int rl = a.split.per_row(u), w = u - rl * a.split.pieces, h = w / T, t = w % T, r = r0 + rl;
       const int64_t raw = raw_position(a.at, b, r);
       const int pos = inside(raw, a.L) ? static_cast<int>(raw) : -1;
-      // a position given twice would be written by two rows at once
-      const bool twice = a.at.idx != nullptr && r + 1 < Rb && pos >= __ldg(a.at.idx + b * a.at.stride + r + 1);
-      if (pos < 0 || twice) {
+      // Rows ascend: one that does not lie below its successor is bad, and is left out, as two neighbours at one position
+      // would both write it. Rows further apart at one position have such a row between them: the list is reported,
+      // but both write.
+      const bool falls = a.at.idx != nullptr && r + 1 < Rb && pos >= __ldg(a.at.idx + b * a.at.stride + r + 1);
+      if (pos < 0 || falls) {
         if (w == 0) report_error(a.dev_err, EC_DEVERR_BAD_IDX);
         continue;
       }

@@ -480,7 +480,9 @@ typedef struct ec_rows {
  * k_new, v_new: ec_rows of Hkv heads, q_new of Hq; q_out bf16 [B, rows_max, Hq, D], rows at and past R[b]
  * are not written. idx int32 on the device, strictly ascending per sequence, as ec_select_recompute
  * writes them (idx_stride >= rows_max: st->idx with idx_stride = L may be given); an idx that is not
- * below its successor sets EC_DEVERR_BAD_IDX and its row is skipped. start int32 [B] on the device.
+ * below its successor sets EC_DEVERR_BAD_IDX and its row is skipped (neighbours that repeat a position would
+ * both write it). Where a list descends and comes back, rows further apart may have one position: both write it,
+ * and what the list, which is reported as bad, leaves there is unspecified. start int32 [B] on the device.
  * A position outside [0, L) sets EC_DEVERR_BAD_IDX, an R outside [0, rows_max] EC_DEVERR_BAD_R; the row,
  * the sequence is skipped (a row whose page is bad still writes q_out). Pages that the call writes belong to
  * one sequence and stand once in its table. 1 <= rows_max <= L; D 64 or 128; EC_ERR_UNSUPPORTED for Hq * D above 2^26. The caches and q_out must not

@@ -50,3 +50,26 @@ def test_storage_that_shrank_where_it_lay(E):
             cache.view()
         t.untyped_storage().resize_(full)
     cache.view()
+
+
+@pytest.mark.parametrize("R", [4, 300])
+def test_a_position_that_comes_back(E, R):
+    """idx that fall and come back to a position are reported; the row above its successor is left out, the others are in their
+    places. (The two rows of the one position hold the same bits here: which of two different ones stays is not specified.)"""
+    L, H, D, page = 400, 2, 128, 16
+    p = E.Params(B=1, L=L, Hq=H, Hkv=H, D=D, V=8, C_max=1, k=1)
+    pos = list(range(R))
+    pos[1:3] = [9, 0]
+    pos[3:] = range(20, 20 + R - 3)
+    x = torch.randn(1, R, 2 * H, D, device="cuda").to(torch.bfloat16)
+    x[0, 2] = x[0, 0]
+    table = torch.randperm(L // page, device="cuda").to(torch.int32)[None]
+    cache, err = E.PagedCache.empty(L // page, page, H, D, table), i32([0])
+    E.kv_append_paged(p, cache, x[:, :, :H], x[:, :, H:], i32([R]), idx=i32([pos]), dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == E._capi.EC_DEVERR_BAD_IDX
+    want = torch.zeros(L, 2 * H, D, dtype=torch.bfloat16, device="cuda")
+    for r in [0, *range(3, R)]:
+        want[pos[r]] = x[0, r]
+    got = torch.cat([cache.k[table[0].long()].flatten(0, 1), cache.v[table[0].long()].flatten(0, 1)], 1)
+    assert torch.equal(got, want)
