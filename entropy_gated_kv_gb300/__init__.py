@@ -544,12 +544,12 @@ def prefix_attention(p: Params, q, prefix, cache, R, out, kv_len=None, scale: fl
 class _Pages:
     """The checked C view (ec_paged_kv) of a paged cache."""
 
-    __slots__ = ("c", "ref", "index", "heads", "B", "positions", "at", "bytes", "_memory")
+    __slots__ = ("c", "ref", "index", "heads", "B", "positions", "at", "bytes", "memory")
 
     def __init__(self, k, v, table):
         self.index, self.at = _cuda_index(k, "k"), (k.data_ptr(), v.data_ptr(), table.data_ptr())
-        self._memory = tuple(t.untyped_storage().nbytes for t in (k, v, table))
-        self.bytes = tuple(f() for f in self._memory)
+        self.memory = tuple(t.untyped_storage().nbytes for t in (k, v, table))
+        self.bytes = tuple(f() for f in self.memory)
         for t, name in ((k, "k"), (v, "v"), (table, "table")):
             end = t.storage_offset() + 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
             if t.numel() > 0 and end * t.element_size() > t.untyped_storage().nbytes():
@@ -577,12 +577,6 @@ class _Pages:
         self.c = C.EcPagedKv(ps, n, stride, k.data_ptr(), v.data_ptr(), table.data_ptr(), row)
         self.ref = ctypes.byref(self.c)
 
-    def holds(self, k, v, table) -> bool:
-        """Whether the tensors' memory is what it was. Addresses alone do not tell: memory that was given back and taken
-        anew, smaller, may lie where it lay."""
-        kb, vb, tb = self._memory
-        return self.at == (k.data_ptr(), v.data_ptr(), table.data_ptr()) and self.bytes == (kb(), vb(), tb())
-
 
 class PagedCache:
     """One layer's K/V cache in pages (ec_paged_kv): k, v bf16 [n_pages, page_size, Hkv, D] (contiguous
@@ -608,11 +602,15 @@ class PagedCache:
     del _exchange
 
     def view(self) -> _Pages:
-        """The checked C view; made and checked again when a tensor was exchanged or its memory is another one."""
+        """The checked C view; made and checked again when a tensor was exchanged or its memory is another one. Addresses alone
+        do not tell: memory that was given back and taken anew, smaller, may lie where it lay."""
         c, k, v, t = self._c, self._k, self._v, self._table
-        if c is None or not c.holds(k, v, t):
-            self._c = None
-            c = self._c = _Pages(k, v, t)
+        if c is not None and c.at == (k.data_ptr(), v.data_ptr(), t.data_ptr()):
+            kb, vb, tb = c.memory
+            if c.bytes == (kb(), vb(), tb()):
+                return c
+        self._c = None
+        c = self._c = _Pages(k, v, t)
         return c
 
     @classmethod
@@ -710,7 +708,7 @@ def paged_attention_workspace_size(p: Params, rows: int) -> int:
     return int(lib().ec_paged_attention_workspace_size(p.ref(), rows))
 
 
-_I32 = (-(1 << 31), (1 << 31) - 1)
+_LEAST, _MOST = -(1 << 31), (1 << 31) - 1  # of 32 bits
 
 
 def _attend_paged(p: Params, q, cache, R, out, places, window, kv_len, scale, ws, dev_err, stream):
@@ -761,9 +759,9 @@ def paged_window_attention(p: Params, q, cache: PagedCache, R, out, left: int, r
                            kv_len=None, scale: float | None = None, ws: torch.Tensor | None = None, dev_err=None, stream=None):
     """paged_attention where the row at position pos (idx[b, r], or start[b] + r, or r) sees the keys pos - left ..
     pos + right (-1: no bound on that side) and the first `sinks` ones. See ec_paged_window_attention."""
-    window = (int(left), int(right), int(sinks))
-    if min(window) < _I32[0] or max(window) > _I32[1]:  # ctypes would keep their low bits
-        window = tuple(max(_I32[0], min(x, _I32[1])) for x in window)  # past the last position, or refused
+    window = left, right, sinks = int(left), int(right), int(sinks)
+    if not (_LEAST <= left <= _MOST and _LEAST <= right <= _MOST and _LEAST <= sinks <= _MOST):  # ctypes would keep their low bits
+        window = tuple(max(_LEAST, min(x, _MOST)) for x in window)  # past the last position, or refused
     return _attend_paged(p, q, cache, R, out, (idx, start), window, kv_len, scale, ws, dev_err, stream)
 
 
