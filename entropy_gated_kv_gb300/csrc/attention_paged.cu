@@ -210,11 +210,6 @@ const Device* device_info(cudaError_t* e) {
   return &info[dev];
 }
 
-bool few_rows(const ec_params& p, int32_t rows_max) { return static_cast<int64_t>(rows_max) * (p.Hq / p.Hkv) <= kFewRows; }
-
-// Positions of a tile.
-int tile_positions(const ec_params& p, int32_t rows_max) { return std::min(kTileRows / (p.Hq / p.Hkv), rows_max); }
-
 struct WsLayout {
   size_t stat, records, total;
 };
@@ -271,15 +266,14 @@ cudaError_t launch_paged_attention(const ec_params& p, int32_t rows_max, const v
     *status = EC_ERR_INVALID_ARG;
     return cudaErrorInvalidValue;
   }
-  const bool ragged = p.B > 1 && kv_len != nullptr && window == nullptr;  // a window bounds what a long sequence reads
   if (few) {
-    const int cluster = few_rows_cluster(p, rows_max, window, ragged, *device);
+    const int cluster = few_rows_cluster(p, rows_max, window, at, kv_len != nullptr, *device);
     e = launch_few_rows(a, p.D, ctas, cluster, s);
     if (e == cudaSuccess && cluster == 0)
       e = launch_pdl(p.D == 64 ? merge_rows_kernel<64> : merge_rows_kernel<128>, dim3(ctas, rows_max * sh.g), dim3(32 * kMergeWarps), 0, s, a);
   } else {
     const int tiles = rows_max <= nr ? 1 : 2;
-    const int cluster = tiles_cluster(p, rows_max, nr, window, ragged, *device);
+    const int cluster = tiles_cluster(p, rows_max, nr, window, at, kv_len != nullptr, *device);
     e = launch_tiles(a, p.D, nr, ctas, cluster, s);
     // eight items or fewer may each go over many CTAs: their parts one column quad a thread
     const bool few_items = static_cast<int64_t>(p.B) * p.Hkv * ((rows_max + nr - 1) / nr) <= 8;

@@ -27,11 +27,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kChunk = 16;  // keys of a warp's step
 constexpr int kChunkShift = 4;
-// A unit takes a CTA 0.7 us by itself and 1.5 in a full GPU; a second launch and its join 1 to 4 us. Line and clusters measured: one token
-// of 28/4 heads behind 4096 keys 9.9 and 9.0 us, behind 8192 11.3 and 11.8, behind 16384 13.7 and 17.6; 3 tokens of 32 heads (clusters
-// of one CTA) behind 2048 24.2 and 20.7, behind 4096 39.3 and 37.1; 12 of 28/4 behind 8192 40.9 and 37.9.
-constexpr int kJoinUnits = 2;
-constexpr int kFullCtas = 72;
+static_assert(kChunk * kWarps == kStepKeys);
 
 // A CTA's place in the line: unit u of item (b, kvh), `left` units of the share from there on.
 struct Place {
@@ -537,16 +533,6 @@ cudaError_t setup_few_rows(Device* d) {
     e = cudaOccupancyMaxActiveClusters(&d->clusters[S], f, &cfg);
   }
   return e;
-}
-
-int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, bool ragged, const Device& d) {
-  const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
-  if (items > d.sms) return 0;
-  const int S = cluster_for(d, items);
-  int64_t keys = scope_hi(p);
-  if (w != nullptr) keys = std::min<int64_t>(keys, static_cast<int64_t>(w->left) + w->right + w->sinks + rows_max + 2 * kChunk);
-  const int64_t units = (keys + kChunk * kWarps - 1) / (kChunk * kWarps);
-  return cluster_pays(d, items, S, units, kFullCtas, kJoinUnits, ragged) ? S : 0;
 }
 
 cudaError_t launch_few_rows(const Args& a, int D, int ctas, int cluster, cudaStream_t s) {

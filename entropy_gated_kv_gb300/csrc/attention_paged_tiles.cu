@@ -42,15 +42,10 @@ namespace paged {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kBlockM = 128;
-constexpr int kBlockN = 128;
+constexpr int kBlockM = kTileRows;
+constexpr int kBlockN = kStepKeys;
 constexpr int kHalf = 64;  // keys whose weights are handed over at once
 constexpr int kItems = 4;  // items handed out and not yet finished
-// A cluster for an item, or the line and a second launch that costs some six blocks. Line and clusters measured: 95 rows of 28/4 heads
-// behind 16384 keys 44 and 40 us, behind 24576 47 and 53; 512 rows behind 8192 61 and 67; 95 rows of 32 heads behind 32768 95 and 86; 18 rows
-// of 28/4 behind 16384 30 and 27, behind 32768 38 and 43. Pairs in clusters of one CTA are off: 1024 rows of 32 heads 25 and 33.
-constexpr int kJoinCost = 6;
-constexpr int kFullCtas = 85;  // of the split form, whose blocks take a CTA 0.8 us by itself: more share the HBM's rate
 // What the partial rows of cut items cost, in blocks, where the choice is whole items in the line: with 3, 8 x 95 rows of 28/4 heads behind
 // 2048 keys 40.0 us for 37.5; with 8, 2048 rows of 28/4 heads 67.5 for 59.7.
 constexpr int kCutCost = 5;
@@ -959,17 +954,6 @@ cudaError_t setup_tiles() {
   allow(reinterpret_cast<const void*>(tiles_kernel<128, true, false>), Layout<128, true>::kBytes);
   allow(reinterpret_cast<const void*>(tiles_kernel<128, true, true>), Layout<128, true>::kBytes);
   return e;
-}
-
-int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, bool ragged, const Device& d) {
-  const bool pair = rows_max > nr;
-  const int64_t step = pair ? 2 * nr : nr, items = static_cast<int64_t>(p.B) * p.Hkv * ((rows_max + step - 1) / step);
-  if (items > d.sms) return 0;
-  const int S = cluster_for(d, items);
-  int64_t keys = scope_hi(p);
-  if (w != nullptr) keys = std::min<int64_t>(keys, static_cast<int64_t>(w->left) + w->right + w->sinks + rows_max + 2 * kBlockN);
-  const int64_t blocks = (keys + kBlockN - 1) / kBlockN;
-  return (S > 1 || !pair) && cluster_pays(d, items, S, blocks, pair ? d.sms : kFullCtas, kJoinCost, ragged) ? S : 0;
 }
 
 template <int D>

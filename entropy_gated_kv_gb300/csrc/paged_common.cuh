@@ -8,6 +8,7 @@
 
 #include "ec_common.cuh"
 #include "ec_internal.h"
+#include "paged_choice.h"
 
 namespace ec {
 namespace paged {
@@ -168,39 +169,11 @@ EC_DEV void st_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// attention_paged_rows.cu: at most kFewRows packed rows (positions times the heads of a KV head) a sequence, the rows of
-// one mma.sync tile. (With two such tiles a warp the products bound it: 8 x 32 rows of 32 heads behind 2048 keys, ragged,
-// 66 us there and 46 as tiles of 128; 4 rows of 28/4 heads behind 2048 keys 12.0 and 8.8.)
-constexpr int kFewRows = 16;
 // cluster 0: shares of the line, partial rows where items are cut; else a cluster of so many CTAs for each item.
 cudaError_t launch_few_rows(const Args& a, int D, int ctas, int cluster, cudaStream_t s);
-constexpr int kMaxCluster = 8;
-// What the launches ask of a device, found once: its SMs, and clusters of S CTAs, one an SM, that are on it at once (a part
-// of the GPU need not have a multiple of S SMs: 15 clusters of 8 on 152).
-struct Device {
-  int sms, clusters[kMaxCluster + 1];
-};
+cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, int cluster, cudaStream_t s);
 cudaError_t setup_few_rows(Device* d);  // the kernels' shared memory, and d->clusters
 cudaError_t setup_tiles();
-// CTAs of a cluster that `items` clusters can have at once.
-inline int cluster_for(const Device& d, int64_t items) {
-  int S = kMaxCluster;
-  while (S > 1 && d.clusters[S] < items) --S;
-  return S;
-}
-// Whether each of `items` items of `steps` steps goes to a cluster of S CTAs and is joined there, or all stand in the line, at the cost
-// of a second launch and its join, `join` steps of a full GPU. `full` CTAs and more share the HBM's rate, fewer take their own.
-// Where only the device knows which sequences are long (`ragged`), one long one may be all that a cluster's call waits for: clusters only
-// where that is no more than the join costs again.
-inline bool cluster_pays(const Device& d, int64_t items, int S, int64_t steps, int64_t full, int64_t join, bool ragged) {
-  const int64_t each = (steps + S - 1) / S;
-  return ragged ? each * full <= 2 * join * d.sms : each * std::max(items * S, full) <= items * steps + join * d.sms;
-}
-int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, bool ragged, const Device& d);
-// attention_paged_tiles.cu: tiles of nr positions, nr times the heads of a KV head at most 128 packed rows.
-constexpr int kTileRows = 128;
-cudaError_t launch_tiles(const Args& a, int D, int nr, int ctas, int cluster, cudaStream_t s);
-int tiles_cluster(const ec_params& p, int32_t rows_max, int nr, const Window* w, bool ragged, const Device& d);
 // A CTA leaves two cut items at most, one that goes on in it and one that begins there: slots
 // 2 tiles cta + tile and 2 tiles cta + tiles + tile, with one tile or two beside each other.
 EC_DEV int64_t part_slot(int first_cta, int i, int tiles, int tile) {
