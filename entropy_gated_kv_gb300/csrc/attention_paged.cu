@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(const __gr
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
       a.out + ((static_cast<int64_t>(rec.b) * s.rows_max + r) * s.Hq + rec.kvh * s.g + (xr - r * s.g)) * D);
-  dst[threadIdx.x] = pack_bf16x2(y.x * inv, y.y * inv);
+  dst[threadIdx.x] = sum == 0.f ? 0u : pack_bf16x2(y.x * inv, y.y * inv);  // every score -infinity: y may hold 0 x infinity
 }
 
 // The same for tiles: a CTA takes a record and 64 rows of it, a thread a row and every eighth quad of columns, as many

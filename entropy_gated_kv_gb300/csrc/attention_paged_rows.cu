@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
       z.y = pack_bf16x2(y[0].z * inv, y[0].w * inv);
       z.z = pack_bf16x2(y[1].x * inv, y[1].y * inv);
       z.w = pack_bf16x2(y[1].z * inv, y[1].w * inv);
+      if (sum == 0.f) z = make_uint4(0, 0, 0, 0);  // every score -infinity: y may hold 0 x infinity
       *reinterpret_cast<uint4*>(a.out + ((static_cast<int64_t>(at.b) * s.rows_max + r) * s.Hq + at.kvh * s.g + (x - r * s.g)) * D + c) = z;
     };
     const int slot = blockIdx.x * 2 + (at.u == 0 ? 1 : 0);

@@ -73,3 +73,24 @@ def test_a_position_that_comes_back(E, R):
         want[pos[r]] = x[0, r]
     got = torch.cat([cache.k[table[0].long()].flatten(0, 1), cache.v[table[0].long()].flatten(0, 1)], 1)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 1.0])
+@pytest.mark.parametrize("L,lengths", [(300, False), (300, True), (20000, False), (20000, True)])  # joined on the chip, by a second launch
+@pytest.mark.parametrize("R", [1, 20, 150])
+def test_rows_without_weight_are_zeros(E, R, L, lengths, value):
+    """Every score of the second sequence is -infinity: its rows are zeros, whatever the values are."""
+    B, H, D, page = 2, 2, 64, 64
+    p = E.Params(B=B, L=L, Hq=H, Hkv=H, D=D, V=8, C_max=1, k=1)
+    per = -(-L // page)
+    table = torch.arange(B * per, device="cuda").to(torch.int32).view(B, per)
+    cache = E.PagedCache.empty(B * per, page, H, D, table)
+    cache.v.fill_(1.0)
+    cache.k[per:], cache.v[per:] = -float("inf"), value
+    q, err = torch.ones(B, R, H, D, dtype=torch.bfloat16, device="cuda"), i32([0])
+    out = torch.full_like(q, -123.0)
+    E.paged_attention(p, q, cache, i32([R, R]), out, kv_len=i32([L, L]) if lengths else None, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert (out[0] == 1).all()
+    assert (out[1] == 0).all()
