@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(const __gr
 // The same for tiles: a CTA takes a record and 64 rows of it, a thread a row and every eighth quad of columns, as many
 // parts in flight as make eight quads. Where a few items may go over many CTAs each (QUADS 1) a CTA takes eight quads only:
 // for all calls that took 7 us more on 8 x 95 rows of 28/4 heads, most of its CTAs without a record. (32 rows a CTA:
-// 94.4 us for 93.1 on 95 rows behind 32768 keys, 32 heads; 128 rows: 95.0.)
+// 94.4 us for 93.1 on 95 rows behind 32768 keys, 32 heads, 128 rows 95.0, measured when that call stood in the line; clusters take it now.)
 constexpr int kTileMergeThreads = 512;
 constexpr int kTileMergeRows = 64;
 

@@ -12,7 +12,7 @@
 //     take equal shares of it: long and short sequences load the SMs alike. An item cut between CTAs leaves
 //     fp32 partial rows, which a second launch joins.
 //   - Where the items are few, each goes to a cluster of up to eight CTAs instead, a CTA an equal part of its chunks, joined
-//     over distributed shared memory: one launch and no line. (One token, 28/4 heads, 2047
+//     over distributed shared memory: one launch and no line; paged_choice.h has the rule. (One token, 28/4 heads, 2047
 //     keys: 8.9 us in shares of the line, 7.4 in clusters; 16 tokens with a window of 1024: 18.7 and 12.4.)
 //   - A window leaves the chunks of its keys and of the sinks, nothing else is read.
 #include <algorithm>

@@ -24,7 +24,7 @@
 // names. The blocks of all items (sequence, group of tiles, KV head) stand in one line of
 // which the CTAs, one an SM, take equal shares; an item cut between CTAs leaves fp32 partial rows, which a second
 // launch joins in a fixed order. Where items are few, each goes to a cluster of up to eight CTAs
-// instead, a CTA an equal part of its blocks, joined over distributed shared memory: one launch and no line.
+// instead, a CTA an equal part of its blocks, joined over distributed shared memory: one launch and no line (paged_choice.h).
 // A window leaves only the blocks that a group's rows see between them.
 // Roles (12 warps):
 //   warp 0      plan, items, TMA producer        warps 4..7    softmax and epilogue of stream 0
@@ -184,7 +184,6 @@ EC_DEV int units_of(const Group& g) { return g.blocks > 0 ? g.blocks + kItemCost
 EC_DEV bool all_in(int near, int lo, int hi, int j0, int count) { return j0 + count <= near || (j0 >= lo && j0 + count <= hi); }
 EC_DEV bool some_in(int near, int lo, int hi, int j0, int count) { return j0 < near || max(j0, lo) < min(j0 + count, hi); }
 
-// CLUSTER: an item a cluster; else shares of the line.
 // Four lanes beside each other hold a row each, in four pieces of 16 bytes; after it lane q of them holds piece q of the
 // four rows. A store of 16 bytes then goes to 64 together in each of 8 rows. (A piece of a row of its own from each lane: 178 us for 172 on
 // 4 full steps of 2048 rows, 444 for 405 on 16384 rows in windows.)
@@ -205,6 +204,7 @@ EC_DEV void turn_quads(uint32_t (&w)[4][4], int lane) {
   }
 }
 
+// CLUSTER: an item a cluster; else shares of the line.
 template <int D, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Args a, int nr, int groups) {
   using LY = Layout<D, PAIR>;
