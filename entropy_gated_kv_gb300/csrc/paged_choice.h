@@ -75,12 +75,13 @@ inline bool cluster_pays(const Device& d, int64_t items, int S, const Reach& r, 
 // all keys before them, line and clusters, every sequence long and one of them (in brackets a long item's own cost): 4 x 8192 keys
 // (5 steps) 21.7 and 17.2, 12.7 and 14.5; 16 x 8192 (15) 51.5 and 46.8, 17.4 and 29.2; 16 x 32768 (61) 170 and 169, 27 and 97; the last 16384 of
 // 32768: 92 and 87, 23 and 53; the last 8192: 52 and 47, 20 and 31. Two rows with 512 keys to either side, beside each other and all over
-// the sequence: 4 x 32768 (20) 11 and 8, 17 and 15; 16 x 16384 (30) 17 and 9, 42 and 49, one sequence's alone apart 19 and 38.
+// the sequence: 4 x 32768 (20) 11 and 8, 17 and 15; 16 x 16384 (30) 17 and 9, 42 and 49, one sequence's alone apart 19 and 38; 16 x 32768 (61)
+// 17 and 9, 82 and 87, one long sequence of 16 with its rows apart 26 and 77.
 inline int few_rows_cluster(const ec_params& p, int32_t rows_max, const Window* w, const RowPlaces& at, bool lengths, const Device& d) {
   const int64_t items = static_cast<int64_t>(p.B) * p.Hkv;
   if (items > d.sms) return 0;
   const int S = cluster_for(d, items);
-  const Cost cost{72, 2, w != nullptr ? 8 : 4, 22};
+  const Cost cost{72, 2, w != nullptr ? 8 : 4, 32};
   return cluster_pays(d, items, S, reach_of(p, rows_max, w, at, lengths, 1, 32), cost) ? S : 0;
 }
 // Tiles: a second launch costs some six blocks. Line and clusters measured: 95 rows of 28/4 heads

@@ -24,7 +24,7 @@ def test_windows_without_a_bound_are_ragged(program, B, L, rows, window, places)
     assert choice(program, B, L, 28, 4, rows, window, places)[1] == 0
 
 
-@pytest.mark.parametrize("B,L,rows", [(16, 16384, 2), (16, 16384, 4), (4, 32768, 32), (16, 4096, 32), (4, 8192, 95), (4, 32768, 95), (1, 32768, 32)])
+@pytest.mark.parametrize("B,L,rows", [(16, 32768, 2), (16, 16384, 4), (4, 32768, 32), (16, 4096, 32), (4, 8192, 95), (4, 32768, 95), (1, 32768, 32)])
 @pytest.mark.parametrize("lengths", [False, True])
 def test_rows_that_may_lie_apart(program, B, L, rows, lengths):  # noqa: F811
     """Positions only the device knows, a narrow window: the rows of one sequence may reach over all of it."""
@@ -44,6 +44,7 @@ def test_rows_that_may_lie_apart(program, B, L, rows, lengths):  # noqa: F811
     (16, 32768, 28, 4, 1, (8191, 0, 4), "idx", True, ("rows", 2)),         # or a quarter of it
     (8, 4096, 32, 32, 95, (256, 256, 64), "idx", True, ("tiles", 0)),
     (4, 32768, 28, 4, 2, (512, 512, 4), "idx", True, ("rows", 6)),          # apart or not, clusters are the faster
+    (16, 16384, 28, 4, 2, (512, 512, 4), "idx", True, ("rows", 2)),
     (4, 8192, 28, 4, 4, (512, 512, 4), "idx", True, ("tiles", 6)),
     (4, 32768, 28, 4, 4, (512, 512, 4), "idx", True, ("tiles", 6)),
     (1, 32768, 28, 4, 95, (512, 512, 4), "idx", True, ("tiles", 8)),
